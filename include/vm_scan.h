@@ -54,7 +54,8 @@ enum {
   VM_ERR_FLAG = 4,        /* a flag or pool_axis is not 0/1, or options has
                              unknown bits                                     */
   VM_ERR_ALIAS = 5,       /* the output overlaps an input                     */
-  VM_ERR_UNSUPPORTED = 6, /* dstate outside [1, 16], a non-finite scale, or
+  VM_ERR_UNSUPPORTED = 6, /* dstate outside [1, 16], a head size past its
+                             limit (see the call), a non-finite scale, or
                              sizes past the kernels' 32-bit offsets or grid
                              limits: 32 rows of seqlen + 16 steps, or one
                              batch row of B or C, must span < 2 GiB; the map
@@ -420,6 +421,195 @@ int vm_ss2d_scan_bwd(const vm_scan_dir *dirs, const void *u, const void *z,
                      const void *dout, float combine_scale, const vm_scan_grad *grads,
                      float *du, void *dz, int64_t batch, int64_t dim, int64_t height,
                      int64_t width, int64_t dstate, int dtype, int options, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Matrix-state mixers: the gated delta rule, the per-head norm and rotation of
+ * its queries and keys, and the clipping of gradients by their global norm.
+ * Token tensors of these calls are token-major, [batch, seqlen, heads, dim]: a
+ * head's values are contiguous, so one projection's output row can be passed
+ * as it is.  A token stride (elements from one token to the next; 0 = dense,
+ * heads * dim; otherwise >= heads * dim) lets q, k and v be slices of such a
+ * row; the stride from one batch row to the next is seqlen token strides.
+ * The dtype selects the storage of q, k, v, out and of their gradients;
+ * everything else is fp32.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Inputs of the gated delta rule.  Value heads hv are a multiple of key heads
+ * hk: value head h reads key head h / (hv / hk).
+ *   q, k     [batch, seqlen, hk, dk]   token stride q_stride, k_stride
+ *   v        [batch, seqlen, hv, dv]   token stride v_stride
+ *   g        [batch, seqlen, hv] fp32  log of the decay, g <= 0 (dense); values
+ *                                      below -120, -Inf among them, decay to 0
+ *   beta     [batch, seqlen, hv] fp32  write strength (dense)
+ *   h0       [n, hv, dk, dv] fp32      initial states; NULL = 0
+ *   offsets  [n + 1] int32             NULL: n = batch sequences of seqlen
+ *                                      tokens.  Else batch is 1 and sequence i
+ *                                      is tokens offsets[i] .. offsets[i+1]-1 of
+ *                                      the packed row: non-decreasing from 0 to
+ *                                      seqlen (a precondition; the kernels clamp
+ *                                      what they read to [0, seqlen], and with
+ *                                      other offsets the results are undefined
+ *                                      but no access leaves the tensors).  A
+ *                                      sequence may be empty.
+ */
+typedef struct vm_delta {
+  const void *q;
+  const void *k;
+  const void *v;
+  const float *g;
+  const float *beta;
+  const float *h0;
+  const int32_t *offsets;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+} vm_delta;
+
+/*
+ * The gated delta rule.  For every sequence and value head, from S_0 = h0:
+ *   S'_t = exp(g_t) S_{t-1}
+ *   S_t  = S'_t + beta_t k_t (v_t - S'_t^T k_t)^T
+ *   out_t = scale S_t^T q_t
+ * reverse = 1 visits the tokens of each sequence from its last to its first.
+ *   out    [batch, seqlen, hv, dv] (dtype), dense; tokens of no sequence are
+ *          not written
+ *   state  [n, hv, dk, dv] fp32: the last states; NULL = not kept.  An empty
+ *          sequence's is its h0.  May be h0 itself (the states then advance in
+ *          place), but must not overlap it otherwise.
+ *   n      number of sequences (batch without offsets)
+ * dk and dv in [1, 128] (VM_ERR_UNSUPPORTED beyond).  hv % hk != 0 is
+ * VM_ERR_SHAPE.  Sequences are computed in chunks of 64 steps, within which
+ * a NaN or Inf of one token reaches the outputs of earlier tokens too.
+ * Temporary memory per 64 tokens and value head: 34 KB.
+ */
+int vm_gated_delta_fwd(const vm_delta *p, void *out, float *state, float scale,
+                       int64_t batch, int64_t seqlen, int64_t n, int64_t hk,
+                       int64_t hv, int64_t dk, int64_t dv, int dtype,
+                       int reverse, void *stream);
+
+/* Gradients of the gated delta rule (dense; the caller's buffers). */
+typedef struct vm_delta_grad {
+  void *dq;      /* [batch, seqlen, hk, dk] (dtype), summed over the value heads of a key head */
+  void *dk;      /* [batch, seqlen, hk, dk] (dtype) */
+  void *dv;      /* [batch, seqlen, hv, dv] (dtype) */
+  float *dg;     /* [batch, seqlen, hv] */
+  float *dbeta;  /* [batch, seqlen, hv] */
+  float *dh0;    /* [n, hv, dk, dv] or NULL (not computed) */
+} vm_delta_grad;
+
+/*
+ * Backward pass of vm_gated_delta_fwd: the gradients of
+ * L = sum(dout * out) + sum(dstate * state) for the same arguments.
+ *   dout [batch, seqlen, hv, dv] (dtype), dense; dstate [n, hv, dk, dv] or
+ *   NULL (= 0).  Gradients of tokens of no sequence are not written.  A token
+ *   whose g is below -120 has dg as if it were -120 (0).
+ * Outputs must not overlap any input or each other.  Sums over value heads
+ * and over a chunk are formed in a fixed order (deterministic).
+ * Temporary memory per 64 tokens and value head, in bytes: 34 K and
+ * 8 dk dv + 512 dv.
+ */
+int vm_gated_delta_bwd(const vm_delta *p, const void *dout, const float *dstate,
+                       const vm_delta_grad *grad, float scale, int64_t batch,
+                       int64_t seqlen, int64_t n, int64_t hk, int64_t hv,
+                       int64_t dk, int64_t dv, int dtype, int reverse,
+                       void *stream);
+
+/*
+ * One token of the gated delta rule for every row of a batch, on states that
+ * are kept: q, k [batch, hk, dk], v, out [batch, hv, dv] (dtype), g, beta
+ * [batch, hv] fp32, all dense; state [n_slots, hv, dk, dv] fp32 is updated in
+ * place.  slots [batch] int32: the state of each row, NULL = row b uses state
+ * b (batch <= n_slots, else VM_ERR_SHAPE).  A row whose slot is outside
+ * [0, n_slots) is idle: its out is zero and it touches no state.  Two rows
+ * must not name the same slot (their updates would race).  No temporary
+ * memory, one launch: the call can be captured in a graph.
+ */
+int vm_gated_delta_step(const void *q, const void *k, const void *v,
+                        const float *g, const float *beta, float *state,
+                        const int32_t *slots, void *out, float scale,
+                        int64_t batch, int64_t n_slots, int64_t hk, int64_t hv,
+                        int64_t dk, int64_t dv, int dtype, void *stream);
+
+/*
+ * Per-head norm and rotation of queries and keys, options of `norm_options`
+ * (bitwise OR; other bits VM_ERR_FLAG):
+ *   VM_NORM_L2           divide by sqrt(sum x^2 + eps); without it by
+ *                        sqrt(mean x^2 + eps)
+ *   VM_ROPE_INTERLEAVED  rotate the pairs (2i, 2i+1); without it (i, i + rot/2)
+ */
+enum { VM_NORM_L2 = 1, VM_ROPE_INTERLEAVED = 2 };
+
+/*
+ *   q [batch, seqlen, hq, dim], k [batch, seqlen, hk, dim] (dtype; k may be
+ *   NULL with hk = 0), token strides as above.
+ *   wq, wk [dim] fp32: gains after the norm; NULL = 1.
+ *   cos, sin [table, rot / 2] fp32: the rotation's table; rot (even, in
+ *   [0, dim]) leading values of each head are turned; rot = 0: no rotation,
+ *   cos, sin, positions unused.
+ *   positions [batch, seqlen] int32: each token's row of the table; NULL =
+ *   0 .. seqlen - 1.  A token whose position is outside [0, table) is padding:
+ *   its outputs and gradients are zero and it adds nothing to dwq and dwk.
+ */
+typedef struct vm_head_norm {
+  const void *q;
+  const void *k;
+  const float *wq;
+  const float *wk;
+  const float *cos;
+  const float *sin;
+  const int32_t *positions;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t table;
+  int64_t rot;
+} vm_head_norm;
+
+/*
+ * q_out, k_out = rotate(gain * normalise(q)), and of k: dense, the shapes of
+ * q and k, both in one launch.  dim in [1, 512] (VM_ERR_UNSUPPORTED beyond).
+ */
+int vm_head_norm_rope(const vm_head_norm *p, void *q_out, void *k_out,
+                      int64_t batch, int64_t seqlen, int64_t hq, int64_t hk,
+                      int64_t dim, float eps, int norm_options, int dtype,
+                      void *stream);
+
+/*
+ * Its backward: from dq_out, dk_out (dense, dtype) the gradients dq, dk
+ * (dense, dtype) and dwq, dwk [dim] fp32 (NULL = not computed; only with the
+ * gain given, else VM_ERR_NULL).  Summed in a fixed order (deterministic).
+ * Temporary memory: up to 1024 partial sums of dwq and dwk.
+ */
+int vm_head_norm_rope_bwd(const vm_head_norm *p, const void *dq_out,
+                          const void *dk_out, void *dq, void *dk, float *dwq,
+                          float *dwk, int64_t batch, int64_t seqlen, int64_t hq,
+                          int64_t hk, int64_t dim, float eps, int norm_options,
+                          int dtype, void *stream);
+
+/* One gradient of vm_clip_grad_norm.  elems may be 0. */
+typedef struct vm_grad_tensor {
+  const void *in;
+  void *out;      /* NULL: only counted in the norm; may be in itself */
+  int64_t elems;
+  int64_t dtype;  /* VM_F32 or VM_BF16, of in and out */
+} vm_grad_tensor;
+
+/*
+ * The Euclidean norm over every element of `count` gradients, and each
+ * gradient scaled to at most that norm:
+ *   norm = sqrt(sum in^2),  out = in * min(1, max_norm / (norm + 1e-6))
+ * list is host memory, read before the call returns.  norm [1] fp32 (device)
+ * receives the norm (required).  Squares are summed in fp64, in a fixed order
+ * (deterministic); a NaN or Inf among the gradients follows the formula by
+ * IEEE rules.  max_norm < 0 or NaN is VM_ERR_UNSUPPORTED.  An out must not
+ * overlap its in except by being it, nor any other tensor of the list (the
+ * latter is not checked).  count in [0, 65536] (VM_ERR_UNSUPPORTED beyond).
+ * Temporary memory: up to 2048 partial sums (65536 for very long lists).
+ */
+int vm_clip_grad_norm(const vm_grad_tensor *list, int64_t count, float max_norm,
+                      float *norm, void *stream);
 
 #ifdef __cplusplus
 }

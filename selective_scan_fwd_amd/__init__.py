@@ -12,7 +12,9 @@ Names and argument order follow the C ABI:
   vm_atrous_scatter, vm_pool_scan_repeat, vm_ss2d_scan_fwd,
   vm_causal_conv1d_silu, vm_causal_conv1d_silu_bwd, vm_selective_scan_bwd,
   vm_bidir_scan_bwd, vm_pool_scan_repeat_bwd, vm_ss2d_scan_bwd,
-  vm_atrous_group_len.
+  vm_atrous_group_len; and the matrix-state mixers: vm_gated_delta_fwd,
+  vm_gated_delta_bwd, vm_gated_delta_step, vm_head_norm_rope,
+  vm_head_norm_rope_bwd, vm_clip_grad_norm.
 """
 from __future__ import annotations
 
@@ -27,6 +29,7 @@ LIB_PATH = os.path.join(_PKG, "libvmscan.so")
 
 VM_F32, VM_BF16 = 0, 1
 VM_DELTA_SOFTPLUS, VM_ZOH = 1, 2
+VM_NORM_L2, VM_ROPE_INTERLEAVED = 1, 2
 VM_OK = 0
 STATUS_NAMES = {0: "VM_OK", 1: "VM_ERR_NULL", 2: "VM_ERR_SHAPE", 3: "VM_ERR_DTYPE", 4: "VM_ERR_FLAG",
                 5: "VM_ERR_ALIAS", 6: "VM_ERR_UNSUPPORTED", 7: "VM_ERR_HIP", 8: "VM_ERR_ALLOC"}
@@ -36,7 +39,9 @@ EXPORTED = ("vm_status_string", "vm_version", "vm_selective_scan_fwd", "vm_bidir
             "vm_atrous_group_len", "vm_atrous_gather", "vm_atrous_scatter", "vm_pool_scan_repeat",
             "vm_ss2d_scan_fwd", "vm_causal_conv1d_silu", "vm_causal_conv1d_silu_bwd",
             "vm_selective_scan_bwd", "vm_bidir_scan_bwd", "vm_pool_scan_repeat_bwd",
-            "vm_ss2d_scan_bwd")
+            "vm_ss2d_scan_bwd",
+            "vm_gated_delta_fwd", "vm_gated_delta_bwd", "vm_gated_delta_step",
+            "vm_head_norm_rope", "vm_head_norm_rope_bwd", "vm_clip_grad_norm")
 
 
 class VmScanDir(ctypes.Structure):
@@ -51,6 +56,29 @@ class VmScanGrad(ctypes.Structure):
     """struct vm_scan_grad (one direction's gradient buffers)."""
     _fields_ = [(k, ctypes.c_void_p) for k in ("du", "ddelta", "dA", "dB", "dC", "dD", "ddelta_bias",
                                                 "dconv_w", "dconv_b")]
+
+
+class VmDelta(ctypes.Structure):
+    """struct vm_delta (inputs of the gated delta rule)."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("q", "k", "v", "g", "beta", "h0", "offsets")] + \
+               [(k, ctypes.c_int64) for k in ("q_stride", "k_stride", "v_stride")]
+
+
+class VmDeltaGrad(ctypes.Structure):
+    """struct vm_delta_grad (gradient buffers of the gated delta rule)."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("dq", "dk", "dv", "dg", "dbeta", "dh0")]
+
+
+class VmHeadNorm(ctypes.Structure):
+    """struct vm_head_norm (inputs of the per-head norm and rotation)."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("q", "k", "wq", "wk", "cos", "sin", "positions")] + \
+               [(k, ctypes.c_int64) for k in ("q_stride", "k_stride", "table", "rot")]
+
+
+class VmGradTensor(ctypes.Structure):
+    """struct vm_grad_tensor (one gradient of vm_clip_grad_norm)."""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("elems", ctypes.c_int64),
+                ("dtype", ctypes.c_int64)]
 
 
 class VmError(RuntimeError):
@@ -94,7 +122,17 @@ def load_library():
             lib.vm_bidir_scan_bwd.argtypes = [D, D, P, P, F, G, G, P, I64, I64, I64, I64, I, I, P]
             lib.vm_pool_scan_repeat_bwd.argtypes = [D, D, P, P, F, G, G, P, I64, I64, I64, I64, I64, I, I, I, P]
             lib.vm_ss2d_scan_bwd.argtypes = [D, P, P, P, F, G, P, P, I64, I64, I64, I64, I64, I, I, P]
-            for name in ("vm_selective_scan_fwd", "vm_bidir_scan_fwd", "vm_bidir_scan_fwd_noalloc",
+            X, Y = ctypes.POINTER(VmDelta), ctypes.POINTER(VmDeltaGrad)
+            N = ctypes.POINTER(VmHeadNorm)
+            lib.vm_gated_delta_fwd.argtypes = [X, P, P, F, I64, I64, I64, I64, I64, I64, I64, I, I, P]
+            lib.vm_gated_delta_bwd.argtypes = [X, P, P, Y, F, I64, I64, I64, I64, I64, I64, I64, I, I, P]
+            lib.vm_gated_delta_step.argtypes = [P, P, P, P, P, P, P, P, F, I64, I64, I64, I64, I64, I64, I, P]
+            lib.vm_head_norm_rope.argtypes = [N, P, P, I64, I64, I64, I64, I64, F, I, I, P]
+            lib.vm_head_norm_rope_bwd.argtypes = [N, P, P, P, P, P, P, I64, I64, I64, I64, I64, F, I, I, P]
+            lib.vm_clip_grad_norm.argtypes = [ctypes.POINTER(VmGradTensor), I64, F, P, P]
+            for name in ("vm_gated_delta_fwd", "vm_gated_delta_bwd", "vm_gated_delta_step", "vm_head_norm_rope",
+                         "vm_head_norm_rope_bwd", "vm_clip_grad_norm",
+                         "vm_selective_scan_fwd", "vm_bidir_scan_fwd", "vm_bidir_scan_fwd_noalloc",
                          "vm_atrous_gather",
                          "vm_atrous_scatter", "vm_pool_scan_repeat", "vm_ss2d_scan_fwd",
                          "vm_causal_conv1d_silu", "vm_causal_conv1d_silu_bwd", "vm_selective_scan_bwd",
@@ -549,8 +587,251 @@ def vm_ss2d_scan_bwd(u, dirs, dout, z=None, combine_scale=1.0, delta_softplus=Tr
     return du, grads, dz
 
 
+# ------------------------------------------------------- matrix-state mixers
+def _tokens(t, name, dtype, shape, device):
+    """q, k or v [batch, seqlen, heads, dim]: each token's heads contiguous,
+    tokens evenly spaced.  Returns the C ABI's token stride (0 = dense)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda" or t.device != device:
+        raise ValueError(f"{name} must be on a GPU device, {device} (got {t.device})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return 0
+    batch, L, heads, dim = shape
+    sb, st, sh, sd = t.stride()
+    step = st if L > 1 else sb                   # (one token a row: the batch stride is the token stride)
+    if (sd == 1 or dim == 1) and (sh == dim or heads == 1) and step >= heads * dim and \
+            (L == 1 or batch == 1 or sb == L * st):
+        return step
+    raise ValueError(f"{name} must be [batch, seqlen, heads, dim] with contiguous heads and evenly spaced "
+                     f"tokens (strides {t.stride()})")
+
+
+def _delta(q, k, v, g, beta, h0, offsets):
+    """Validate the gated delta rule's inputs; returns (VmDelta, sizes)."""
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{name} must be a [batch, seqlen, heads, dim] tensor")
+    batch, L, hk, dk = q.shape
+    hv, dv = v.shape[2:]
+    dev = q.device
+    sq = _tokens(q, "q", q.dtype, (batch, L, hk, dk), dev)
+    sk = _tokens(k, "k", q.dtype, (batch, L, hk, dk), dev)
+    sv = _tokens(v, "v", q.dtype, (batch, L, hv, dv), dev)
+    _dev(g, "g", torch.float32, (batch, L, hv), dev)
+    _dev(beta, "beta", torch.float32, (batch, L, hv), dev)
+    n = batch
+    if offsets is not None:
+        if batch != 1:
+            raise ValueError("packed sequences (offsets) take batch 1")
+        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+            raise ValueError("offsets must be an int32 tensor [sequences + 1]")
+        _dev(offsets, "offsets", torch.int32, None, dev)
+        n = offsets.shape[0] - 1
+    if h0 is not None:
+        _dev(h0, "h0", torch.float32, (n, hv, dk, dv), dev)
+    ptr = lambda t: t.data_ptr() if t is not None else None
+    s = VmDelta(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), ptr(h0), ptr(offsets),
+                sq, sk, sv)
+    return s, (batch, L, n, hk, hv, dk, dv)
+
+
+def vm_gated_delta_fwd(q, k, v, g, beta, scale=None, h0=None, want_state=False, reverse=False, offsets=None,
+                       out=None, state=None):
+    """Gated delta rule over whole sequences; returns (out, state).
+    q, k: [batch, L, hk, dk]; v: [batch, L, hv, dv] (hv a multiple of hk; fp32 or
+    bf16; slices of a common projection row are read in place); g (log decay,
+    <= 0), beta: [batch, L, hv] fp32; h0: [n, hv, dk, dv] fp32 or None;
+    scale: dk ** -0.5 by default.  offsets (int32 [n + 1], batch 1): sequence i
+    is tokens offsets[i] .. offsets[i + 1] - 1.  reverse=True visits each
+    sequence from its last token.  out is [batch, L, hv, dv]; state (the last
+    states, [n, hv, dk, dv] fp32) is None unless want_state or a state buffer
+    (which may be h0) is given."""
+    p, (batch, L, n, hk, hv, dk, dv) = _delta(q, k, v, g, beta, h0, offsets)
+    dev = q.device
+    out = torch.empty((batch, L, hv, dv), dtype=q.dtype, device=dev) if out is None else \
+        _dev(out, "out", q.dtype, (batch, L, hv, dv), dev)
+    if state is not None:
+        _dev(state, "state", torch.float32, (n, hv, dk, dv), dev)
+    elif want_state:
+        state = torch.empty((n, hv, dk, dv), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        st = load_library().vm_gated_delta_fwd(ctypes.byref(p), _ptr(out), _ptr(state),
+                                               float(dk ** -0.5 if scale is None else scale), batch, L, n, hk, hv, dk,
+                                               dv, _dtype_code(q), int(bool(reverse)), _stream(dev))
+    _check(st, "vm_gated_delta_fwd")
+    return out, state
+
+
+def vm_gated_delta_bwd(q, k, v, g, beta, dout, scale=None, h0=None, dstate=None, reverse=False, offsets=None):
+    """Gradients of sum(dout * out) + sum(dstate * state) of vm_gated_delta_fwd.
+    Returns a dict: q, k, v (dense, in their dtype), g, beta (fp32) and, when h0
+    is given, h0 (fp32)."""
+    p, (batch, L, n, hk, hv, dk, dv) = _delta(q, k, v, g, beta, h0, offsets)
+    dev = q.device
+    _dev(dout, "dout", q.dtype, (batch, L, hv, dv), dev)
+    if dstate is not None:
+        _dev(dstate, "dstate", torch.float32, (n, hv, dk, dv), dev)
+    make = lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=dev)
+    d = dict(q=make(q.dtype, batch, L, hk, dk), k=make(q.dtype, batch, L, hk, dk), v=make(q.dtype, batch, L, hv, dv),
+             g=make(torch.float32, batch, L, hv), beta=make(torch.float32, batch, L, hv))
+    if h0 is not None:
+        d["h0"] = make(torch.float32, n, hv, dk, dv)
+    grads = VmDeltaGrad(*(d[x].data_ptr() if x in d else None for x in ("q", "k", "v", "g", "beta", "h0")))
+    with torch.cuda.device(dev):
+        st = load_library().vm_gated_delta_bwd(ctypes.byref(p), _ptr(dout), _ptr(dstate), ctypes.byref(grads),
+                                               float(dk ** -0.5 if scale is None else scale), batch, L, n, hk, hv, dk,
+                                               dv, _dtype_code(q), int(bool(reverse)), _stream(dev))
+    _check(st, "vm_gated_delta_bwd")
+    return d
+
+
+def vm_gated_delta_step(q, k, v, g, beta, state, scale=None, slots=None, out=None):
+    """One token of the gated delta rule on kept states; returns out.
+    q, k: [batch, hk, dk]; v: [batch, hv, dv]; g, beta: [batch, hv] fp32; state
+    [n_slots, hv, dk, dv] fp32 is updated in place.  slots (int32 [batch]): each
+    row's state (distinct); a row with a slot outside [0, n_slots) is idle: zero
+    out, no state touched."""
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{name} must be a [batch, heads, dim] tensor")
+    batch, hk, dk = q.shape
+    hv, dv = v.shape[1:]
+    dev = q.device
+    _dev(q, "q", None, None, None)
+    _dev(k, "k", q.dtype, (batch, hk, dk), dev)
+    _dev(v, "v", q.dtype, (batch, hv, dv), dev)
+    _dev(g, "g", torch.float32, (batch, hv), dev)
+    _dev(beta, "beta", torch.float32, (batch, hv), dev)
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be a [n_slots, hv, dk, dv] tensor")
+    _dev(state, "state", torch.float32, (state.shape[0], hv, dk, dv), dev)
+    if slots is not None:
+        _dev(slots, "slots", torch.int32, (batch,), dev)
+    out = torch.empty((batch, hv, dv), dtype=q.dtype, device=dev) if out is None else \
+        _dev(out, "out", q.dtype, (batch, hv, dv), dev)
+    with torch.cuda.device(dev):
+        st = load_library().vm_gated_delta_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
+                                                _ptr(slots), _ptr(out), float(dk ** -0.5 if scale is None else scale),
+                                                batch, state.shape[0], hk, hv, dk, dv, _dtype_code(q), _stream(dev))
+    _check(st, "vm_gated_delta_step")
+    return out
+
+
+def _head_norm(q, k, wq, wk, cos, sin, positions):
+    for name, t in (("q", q), ("k", k)):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dim() != 4):
+            raise ValueError(f"{name} must be a [batch, seqlen, heads, dim] tensor")
+    batch, L, hq, dim = q.shape
+    hk = k.shape[2] if k is not None else 0
+    dev = q.device
+    sq = _tokens(q, "q", q.dtype, (batch, L, hq, dim), dev)
+    sk = _tokens(k, "k", q.dtype, (batch, L, hk, dim), dev) if k is not None else 0
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None:
+            _dev(w, name, torch.float32, (dim,), dev)
+    table = rot = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    if cos is not None:
+        if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
+            raise ValueError("cos must be a [table, rot / 2] tensor")
+        table, rot = cos.shape[0], 2 * cos.shape[1]
+        _dev(cos, "cos", torch.float32, cos.shape, dev)
+        _dev(sin, "sin", torch.float32, cos.shape, dev)
+        if positions is not None:
+            _dev(positions, "positions", torch.int32, (batch, L), dev)
+    ptr = lambda t: t.data_ptr() if t is not None else None
+    s = VmHeadNorm(q.data_ptr(), ptr(k), ptr(wq), ptr(wk), ptr(cos), ptr(sin),
+                   ptr(positions) if cos is not None else None, sq, sk, table, rot)
+    return s, (batch, L, hq, hk, dim)
+
+
+def _norm_options(l2, interleaved):
+    return (VM_NORM_L2 if l2 else 0) | (VM_ROPE_INTERLEAVED if interleaved else 0)
+
+
+def vm_head_norm_rope(q, k=None, wq=None, wk=None, cos=None, sin=None, positions=None, eps=1e-6, l2=False,
+                      interleaved=False, q_out=None, k_out=None):
+    """Queries and keys normalised per head, scaled by a gain and rotated by
+    position, in one launch; returns (q_out, k_out), dense.
+    q: [batch, L, hq, dim]; k: [batch, L, hk, dim] or None (fp32 or bf16; slices
+    of a common projection row are read in place); wq, wk: [dim] fp32 or None;
+    cos, sin: [table, rot / 2] fp32 or None (no rotation); positions: int32
+    [batch, L], None = 0 .. L - 1, outside the table = padding (zero output).
+    l2=True divides by sqrt(sum x^2 + eps) instead of sqrt(mean x^2 + eps);
+    interleaved=True pairs (2i, 2i + 1) instead of (i, i + rot / 2)."""
+    p, (batch, L, hq, hk, dim) = _head_norm(q, k, wq, wk, cos, sin, positions)
+    dev = q.device
+    q_out = torch.empty((batch, L, hq, dim), dtype=q.dtype, device=dev) if q_out is None else \
+        _dev(q_out, "q_out", q.dtype, (batch, L, hq, dim), dev)
+    if k is not None:
+        k_out = torch.empty((batch, L, hk, dim), dtype=q.dtype, device=dev) if k_out is None else \
+            _dev(k_out, "k_out", q.dtype, (batch, L, hk, dim), dev)
+    with torch.cuda.device(dev):
+        st = load_library().vm_head_norm_rope(ctypes.byref(p), _ptr(q_out), _ptr(k_out), batch, L, hq, hk, dim,
+                                              float(eps), _norm_options(l2, interleaved), _dtype_code(q), _stream(dev))
+    _check(st, "vm_head_norm_rope")
+    return q_out, k_out
+
+
+def vm_head_norm_rope_bwd(dq_out, dk_out, q, k=None, wq=None, wk=None, cos=None, sin=None, positions=None, eps=1e-6,
+                          l2=False, interleaved=False):
+    """Gradients of sum(dq_out * q_out) + sum(dk_out * k_out) of
+    vm_head_norm_rope: (dq, dk, dwq, dwk); dq, dk dense in their dtype, dwq and
+    dwk fp32 (None without the gain)."""
+    p, (batch, L, hq, hk, dim) = _head_norm(q, k, wq, wk, cos, sin, positions)
+    dev = q.device
+    _dev(dq_out, "dq_out", q.dtype, (batch, L, hq, dim), dev)
+    if (dk_out is None) != (k is None):
+        raise ValueError("dk_out comes with k")
+    if k is not None:
+        _dev(dk_out, "dk_out", q.dtype, (batch, L, hk, dim), dev)
+    dq = torch.empty((batch, L, hq, dim), dtype=q.dtype, device=dev)
+    dk = torch.empty((batch, L, hk, dim), dtype=q.dtype, device=dev) if k is not None else None
+    dwq = torch.empty((dim,), dtype=torch.float32, device=dev) if wq is not None else None
+    dwk = torch.empty((dim,), dtype=torch.float32, device=dev) if wk is not None and k is not None else None
+    with torch.cuda.device(dev):
+        st = load_library().vm_head_norm_rope_bwd(ctypes.byref(p), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk),
+                                                  _ptr(dwq), _ptr(dwk), batch, L, hq, hk, dim, float(eps),
+                                                  _norm_options(l2, interleaved), _dtype_code(q), _stream(dev))
+    _check(st, "vm_head_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+def vm_clip_grad_norm(grads, max_norm, out=None):
+    """Scale the gradients to at most the Euclidean norm max_norm over all of
+    them; returns the norm before (fp32 tensor of no dimensions, on the GPU).
+    grads: a list of fp32 and bf16 tensors on one GPU, scaled in place, or into
+    the tensors of the list `out` (the same shapes and dtypes)."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads must hold at least one tensor")
+    dev = grads[0].device
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError("out must hold one tensor for each gradient")
+    arr = (VmGradTensor * len(grads))()
+    for i, (x, y) in enumerate(zip(grads, outs)):
+        _dev(x, f"grads[{i}]", None, None, dev)
+        if y is not x:
+            _dev(y, f"out[{i}]", x.dtype, x.shape, dev)
+        arr[i] = VmGradTensor(x.data_ptr(), y.data_ptr(), x.numel(), _dtype_code(x))
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        st = load_library().vm_clip_grad_norm(arr, len(grads), float(max_norm), _ptr(norm), _stream(dev))
+    _check(st, "vm_clip_grad_norm")
+    return norm
+
+
 __all__ = ["vm_selective_scan_fwd", "vm_bidir_scan_fwd", "vm_bidir_scan_fwd_noalloc", "vm_atrous_gather", "vm_atrous_scatter",
            "vm_pool_scan_repeat", "vm_ss2d_scan_fwd", "vm_causal_conv1d_silu",
            "vm_causal_conv1d_silu_bwd", "vm_pool_scan_repeat_bwd", "vm_ss2d_scan_bwd",
            "vm_selective_scan_bwd", "vm_bidir_scan_bwd", "VmScanGrad", "vm_atrous_group_len", "vm_status_string", "vm_version",
-           "VmScanDir", "VmError", "load_library", "LIB_PATH", "EXPORTED"]
+           "VmScanDir", "VmError",
+           "vm_gated_delta_fwd", "vm_gated_delta_bwd", "vm_gated_delta_step", "vm_head_norm_rope",
+           "vm_head_norm_rope_bwd", "vm_clip_grad_norm", "VmDelta", "VmDeltaGrad", "VmHeadNorm", "VmGradTensor", "load_library", "LIB_PATH", "EXPORTED"]

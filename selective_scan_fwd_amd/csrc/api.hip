@@ -10,79 +10,15 @@
 #include <mutex>
 #include <vector>
 
+#include "api_util.h"
 #include "vm_internal.h"
 #include "vm_scan.h"
 
-namespace {
-
-constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
-constexpr int64_t kMaxElems = int64_t{1} << 40;
-// The map kernels (gather, scatter, pool, repeat, transpose, merge) run one
-// 256-thread workgroup per [H, W] plane on grid x: planes * 256 work-items
-// must stay below 2^32.
-constexpr int64_t kMaxPlanes = (int64_t{1} << 24) - 1;
-// The scan kernels run one to two 16-channel row blocks per workgroup of up
-// to 256 work-items on grid x; the same bound on the row-block count keeps
-// the work-item count below 2^32.
-bool row_blocks_ok(int64_t batch, int64_t dim) { return batch * ((dim + 15) / 16) <= kMaxPlanes; }
-
-struct Span {
-  uintptr_t lo = 0, hi = 0;  // [lo, hi)
-};
-Span span(const void *p, int64_t bytes) {
-  Span s;
-  if (p != nullptr) {
-    s.lo = reinterpret_cast<uintptr_t>(p);
-    s.hi = s.lo + static_cast<uintptr_t>(bytes);
-  }
-  return s;
-}
-bool overlaps(Span a, Span b) { return a.lo != 0 && b.lo != 0 && a.lo < b.hi && b.lo < a.hi; }
-
-bool dims_ok(std::initializer_list<int64_t> dims, int64_t *prod) {
-  int64_t p = 1;
-  for (int64_t d : dims) {
-    if (d <= 0 || d > kMaxDim) return false;
-    if (p > kMaxElems / d) return false;
-    p *= d;
-  }
-  *prod = p;
-  return true;
-}
-
-bool flag_ok(int f) { return f == 0 || f == 1; }
-bool options_ok(int o) { return (o & ~(VM_DELTA_SOFTPLUS | VM_ZOH)) == 0; }
-
-// Element extent of B or C: dense [batch, dstate, L], or token-major with
-// stride bcs (last element at ((batch*L - 1)*bcs + dstate - 1)).
-int64_t bc_extent(int64_t batch, int64_t dstate, int64_t L, int64_t bcs) {
-  return bcs > 0 ? (batch * L - 1) * bcs + dstate : batch * dstate * L;
-}
-
-// Checks of one scan direction.  u_elems / tok_elems: elements of u and of
-// delta; L: length of delta, B and C; dim, dstate: parameter shapes.
-int check_dir(const vm_scan_dir *p, int64_t u_elems, int64_t tok_elems, int64_t batch, int64_t L,
-              int64_t dim, int64_t dstate, int esize, Span out) {
-  if (p == nullptr || p->u == nullptr || p->delta == nullptr || p->A == nullptr ||
-      p->B == nullptr || p->C == nullptr || p->D == nullptr)
-    return VM_ERR_NULL;
-  int64_t unused = 0;
-  if (p->bc_stride < 0 || (p->bc_stride > 0 && p->bc_stride < dstate)) return VM_ERR_SHAPE;
-  if (p->bc_stride > 0 && !dims_ok({batch, L, p->bc_stride}, &unused)) return VM_ERR_SHAPE;
-  const int64_t bc = bc_extent(batch, dstate, L, p->bc_stride);
-  const Span ins[] = {span(p->u, u_elems * esize), span(p->delta, tok_elems * esize),
-                      span(p->A, dim * dstate * 4), span(p->B, bc * esize),
-                      span(p->C, bc * esize), span(p->D, dim * 4),
-                      span(p->delta_bias, dim * 4), span(p->conv_w, dim * 16),
-                      span(p->conv_b, dim * 4)};
-  for (const Span &s : ins)
-    if (overlaps(s, out)) return VM_ERR_ALIAS;
-  return VM_OK;
-}
+namespace vmk {
 
 // ---------------------------------------------------------------- workspace
-std::mutex g_pool_mu;
-std::map<int, hipMemPool_t> g_pools;
+static std::mutex g_pool_mu;
+static std::map<int, hipMemPool_t> g_pools;
 
 hipError_t pool_for_current_device(hipMemPool_t *out) {
   int dev = 0;
@@ -113,54 +49,56 @@ hipError_t pool_for_current_device(hipMemPool_t *out) {
   return hipSuccess;
 }
 
-// Temporary fp32 buffers that live on `stream` for the duration of one call.
-// Requests below kChunk bytes are carved, 256-byte aligned, from shared
-// chunks of kChunk bytes; larger ones get an allocation of their own.  Each
-// pool free costs the host about 5 to 30 microseconds, so a backward call's
-// dozen buffers freed one by one took longer on the host than its kernels
-// on the GPU.
-class Scratch {
- public:
-  explicit Scratch(hipStream_t s) : s_(s) {}
-  ~Scratch() {
-    for (void *p : ptrs_) (void)hipFreeAsync(p, s_);
-  }
-  void *bytes(int64_t n, int *status) {
-    if (*status != VM_OK) return nullptr;
-    const size_t need = (static_cast<size_t>(n) + 255) & ~static_cast<size_t>(255);
-    if (need >= kChunk) return alloc(need, status);
-    if (base_ == nullptr || used_ + need > kChunk) {
-      base_ = static_cast<char *>(alloc(kChunk, status));
-      used_ = 0;
-      if (base_ == nullptr) return nullptr;
-    }
-    void *p = base_ + used_;
-    used_ += need;
-    return p;
-  }
-  float *get(int64_t floats, int *status) { return static_cast<float *>(bytes(floats * 4, status)); }
+}  // namespace vmk
 
- private:
-  static constexpr size_t kChunk = size_t{64} << 20;
-  void *alloc(size_t n, int *status) {
-    hipMemPool_t pool;
-    void *p = nullptr;
-    if (pool_for_current_device(&pool) != hipSuccess ||
-        hipMallocFromPoolAsync(&p, n, pool, s_) != hipSuccess) {
-      (void)hipGetLastError();
-      *status = VM_ERR_ALLOC;
-      return nullptr;
-    }
-    ptrs_.push_back(p);
-    return p;
-  }
-  hipStream_t s_;
-  std::vector<void *> ptrs_;
-  char *base_ = nullptr;      // the current chunk, and the bytes of it handed out
-  size_t used_ = 0;
-};
+namespace {
 
-int hip_status(hipError_t e) { return e == hipSuccess ? VM_OK : VM_ERR_HIP; }
+using vmk::Scratch;
+using vmk::Span;
+using vmk::dims_ok;
+using vmk::hip_status;
+using vmk::kMaxDim;
+using vmk::overlaps;
+using vmk::span;
+
+// The map kernels (gather, scatter, pool, repeat, transpose, merge) run one
+// 256-thread workgroup per [H, W] plane on grid x: planes * 256 work-items
+// must stay below 2^32.
+constexpr int64_t kMaxPlanes = (int64_t{1} << 24) - 1;
+// The scan kernels run one to two 16-channel row blocks per workgroup of up
+// to 256 work-items on grid x; the same bound on the row-block count keeps
+// the work-item count below 2^32.
+bool row_blocks_ok(int64_t batch, int64_t dim) { return batch * ((dim + 15) / 16) <= kMaxPlanes; }
+
+bool flag_ok(int f) { return f == 0 || f == 1; }
+bool options_ok(int o) { return (o & ~(VM_DELTA_SOFTPLUS | VM_ZOH)) == 0; }
+
+// Element extent of B or C: dense [batch, dstate, L], or token-major with
+// stride bcs (last element at ((batch*L - 1)*bcs + dstate - 1)).
+int64_t bc_extent(int64_t batch, int64_t dstate, int64_t L, int64_t bcs) {
+  return bcs > 0 ? (batch * L - 1) * bcs + dstate : batch * dstate * L;
+}
+
+// Checks of one scan direction.  u_elems / tok_elems: elements of u and of
+// delta; L: length of delta, B and C; dim, dstate: parameter shapes.
+int check_dir(const vm_scan_dir *p, int64_t u_elems, int64_t tok_elems, int64_t batch, int64_t L,
+              int64_t dim, int64_t dstate, int esize, Span out) {
+  if (p == nullptr || p->u == nullptr || p->delta == nullptr || p->A == nullptr ||
+      p->B == nullptr || p->C == nullptr || p->D == nullptr)
+    return VM_ERR_NULL;
+  int64_t unused = 0;
+  if (p->bc_stride < 0 || (p->bc_stride > 0 && p->bc_stride < dstate)) return VM_ERR_SHAPE;
+  if (p->bc_stride > 0 && !dims_ok({batch, L, p->bc_stride}, &unused)) return VM_ERR_SHAPE;
+  const int64_t bc = bc_extent(batch, dstate, L, p->bc_stride);
+  const Span ins[] = {span(p->u, u_elems * esize), span(p->delta, tok_elems * esize),
+                      span(p->A, dim * dstate * 4), span(p->B, bc * esize),
+                      span(p->C, bc * esize), span(p->D, dim * 4),
+                      span(p->delta_bias, dim * 4), span(p->conv_w, dim * 16),
+                      span(p->conv_b, dim * 4)};
+  for (const Span &s : ins)
+    if (overlaps(s, out)) return VM_ERR_ALIAS;
+  return VM_OK;
+}
 
 // fp32 view of a token tensor: the tensor itself (fp32) or a widened copy.
 const float *as_f32(const void *src, int64_t n, bool bf16, Scratch &ws, hipStream_t s,
@@ -429,14 +367,14 @@ const char *vm_status_string(int status) {
     case VM_ERR_DTYPE: return "VM_ERR_DTYPE: unknown dtype";
     case VM_ERR_FLAG: return "VM_ERR_FLAG: a flag is not 0 or 1, or unknown option bits";
     case VM_ERR_ALIAS: return "VM_ERR_ALIAS: the output overlaps an input";
-    case VM_ERR_UNSUPPORTED: return "VM_ERR_UNSUPPORTED: dstate outside [1, 16], non-finite scale, or sizes past the kernels' 32-bit offsets or grid limits";
+    case VM_ERR_UNSUPPORTED: return "VM_ERR_UNSUPPORTED: dstate outside [1, 16], a head size past its limit, non-finite scale, or sizes past the kernels' 32-bit offsets or grid limits";
     case VM_ERR_HIP: return "VM_ERR_HIP: a HIP launch or runtime call failed";
     case VM_ERR_ALLOC: return "VM_ERR_ALLOC: temporary device memory unavailable";
     default: return "unknown status";
   }
 }
 
-int vm_version(void) { return 10000; }
+int vm_version(void) { return 10100; }
 
 int64_t vm_atrous_group_len(int64_t height, int64_t width) {
   if (height <= 0 || width <= 0 || height > kMaxDim || width > kMaxDim) return -VM_ERR_SHAPE;

@@ -1,0 +1,102 @@
+// Internal declarations of the matrix-state mixer kernels (gated delta rule,
+// per-head norm and rotation, gradient clipping).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "vm_scan.h"
+
+namespace vmk {
+
+// ------------------------------------------------------ norm and rotation
+struct NormArgs {
+  const void *x[2];       // q, k: [tokens][heads][dim], token stride xs (elements)
+  const float *w[2];      // gains or nullptr
+  void *y[2];             // forward: outputs (dense); backward: gradients of x
+  const void *dy[2];      // backward: gradients of the outputs (dense)
+  float *partial;         // backward: [blocks][2][dim] sums for dw, or nullptr
+  float *dw[2];
+  const float *cos, *sin;
+  const int32_t *pos;
+  int64_t xs[2];
+  int64_t tokens, seqlen, table;
+  int heads[2];
+  int dim, rot;
+  float eps, over;        // over: 1 / dim, or 1 for the Euclidean norm
+  int interleaved;
+  int splits;             // lane groups that share one token's heads
+};
+constexpr int kNormMaxBlocks = 1024;
+// Blocks of the launch (the number of partial sums of the backward pass).
+int norm_blocks(const NormArgs &a, bool bf16, bool back);
+hipError_t launch_norm(NormArgs a, bool bf16, bool back, hipStream_t s);
+
+// ------------------------------------------------------------- clipping
+constexpr int kClipTable = 120;        // tensors of one launch (kernel arguments)
+constexpr int64_t kClipChunk = 16384;  // elements of one block's piece
+constexpr int kClipPartials = 2048;
+struct ClipTable {
+  const void *in[kClipTable];
+  void *out[kClipTable];
+  int64_t elems[kClipTable];
+  uint32_t first[kClipTable + 1];      // first chunk of each tensor
+  uint8_t bf16[kClipTable];
+  int n;
+};
+hipError_t launch_clip_sums(const ClipTable &t, double *partial, int blocks, hipStream_t s);
+hipError_t launch_clip_scale(const ClipTable &t, const double *partial, int partials, float max_norm,
+                             float *norm, int blocks, hipStream_t s);
+hipError_t launch_clip_norm_only(const double *partial, int partials, float *norm, hipStream_t s);
+
+// ------------------------------------------------------ gated delta rule
+constexpr int kDeltaChunk = 64;
+struct DeltaArgs {
+  const void *q, *k, *v;
+  const float *g, *beta, *h0;
+  const int32_t *off;
+  int64_t qs, ks, vs;      // token strides (elements)
+  int64_t L;               // tokens of a batch row
+  int64_t slots;           // chunk slots over all sequences
+  int nseq, hk, hv, dk, dv;
+  int reverse;
+  float scale;
+  // per (slot, value head)
+  float *T;                // [64][64]: (I + A)^-1, lower triangular
+  float *P;                // [64][64]: scaled masked products of queries and keys
+  double *gam;             // [64]: running sums of the log decay
+  // forward
+  void *out;
+  float *state;
+  // backward
+  const void *dout;
+  const float *dstate;
+  float *S;                // per (slot, value head) [dk][dv]: state at the chunk's start
+  float *V;                // [64][dv]: the chunk's corrected values
+  float *dS;               // [dk][dv]: gradient of the state at the chunk's end
+  float *dR;               // [64][dv]
+  void *dq, *dkey, *dval;
+  float *dg, *dbeta, *dh0;
+};
+// Chunk slots of `n` sequences over L tokens in all (packed) or each.
+int64_t delta_slots(int64_t batch, int64_t L, int64_t n, bool packed);
+hipError_t launch_delta_prep(const DeltaArgs &a, bool bf16, bool need_p, hipStream_t s);
+// keep: store S and V for the backward pass instead of out and state.
+hipError_t launch_delta_scan(const DeltaArgs &a, bool bf16, bool keep, hipStream_t s);
+hipError_t launch_delta_scan_bwd(const DeltaArgs &a, bool bf16, hipStream_t s);
+hipError_t launch_delta_grad(const DeltaArgs &a, bool bf16, hipStream_t s);
+
+struct StepArgs {
+  const void *q, *k, *v;
+  const float *g, *beta;
+  float *state;
+  const int32_t *slots;
+  void *out;
+  float scale;
+  int64_t n_slots;
+  int batch, hk, hv, dk, dv;
+};
+hipError_t launch_delta_step(const StepArgs &a, bool bf16, hipStream_t s);
+
+}  // namespace vmk
