@@ -72,7 +72,12 @@ int check_delta(const vm_delta *p, float scale, int64_t batch, int64_t seqlen, i
     return VM_ERR_SHAPE;
   if (p->offsets != nullptr ? batch != 1 : n != batch) return VM_ERR_SHAPE;
   if (!std::isfinite(scale) || dk > 128 || dv > 128 || hv > kMaxHeads) return VM_ERR_UNSUPPORTED;
-  if (n > kMaxSlots || vmk::delta_slots(batch, seqlen, n, p->offsets != nullptr) > kMaxSlots) return VM_ERR_UNSUPPORTED;
+  // (the kernels reach the 64 tokens of a chunk with 31-bit byte offsets)
+  for (int64_t stride : {z->qs, z->ks, z->vs, hv * dv})
+    if (stride * 64 * 4 >= (int64_t{1} << 31)) return VM_ERR_UNSUPPORTED;
+  // (the scans put sequences, heads and up to 2 blocks of columns on x)
+  if (n * hv > kMaxSlots || vmk::delta_slots(batch, seqlen, n, p->offsets != nullptr) > kMaxSlots)
+    return VM_ERR_UNSUPPORTED;
   return VM_OK;
 }
 
@@ -101,13 +106,19 @@ vmk::DeltaArgs delta_args(const vm_delta *p, const DeltaSizes &z, float scale, i
   return a;
 }
 
-// The chunks' triangular inverses, masked products and running decays.
-int chunk_scratch(vmk::DeltaArgs &a, Scratch &ws) {
+// The chunks' triangular inverses, masked products and decays.
+int chunk_scratch(vmk::DeltaArgs &a, bool bf16, bool backward, Scratch &ws) {
   int st = VM_OK;
-  const int64_t per = a.slots * a.hv, c = vmk::kDeltaChunk;
-  a.T = ws.get(per * c * c, &st);
-  a.P = ws.get(per * c * c, &st);
-  a.gam = static_cast<double *>(ws.bytes(per * c * 8, &st));
+  const int64_t per = a.slots * a.hv, c = vmk::kDeltaChunk, tri = per * vmk::kTriTerm * 2;
+  const int terms_p = vmk::delta_terms_p(bf16);
+  a.T = static_cast<uint16_t *>(ws.bytes(tri * vmk::kTermsT, &st));
+  (backward ? a.PT : a.P) = static_cast<uint16_t *>(ws.bytes(tri * terms_p, &st));
+  a.eg = ws.get(per * c, &st);
+  a.ew = ws.get(per * c, &st);
+  if (backward) {
+    a.TT = static_cast<uint16_t *>(ws.bytes(tri * vmk::kTermsT, &st));
+    a.gam = static_cast<double *>(ws.bytes(per * c * 8, &st));
+  }
   return st;
 }
 
@@ -177,9 +188,9 @@ int vm_gated_delta_fwd(const vm_delta *p, void *out, float *state, float scale, 
   vmk::DeltaArgs a = delta_args(p, z, scale, batch, seqlen, n, hk, hv, dk, dv, reverse);
   a.out = out;
   a.state = state;
-  st = chunk_scratch(a, ws);
+  st = chunk_scratch(a, bf16, false, ws);
   if (st != VM_OK) return st;
-  st = hip_status(vmk::launch_delta_prep(a, bf16, true, s));
+  st = hip_status(vmk::launch_delta_prep(a, bf16, false, s));
   if (st != VM_OK) return st;
   return hip_status(vmk::launch_delta_scan(a, bf16, false, s));
 }
@@ -215,7 +226,7 @@ int vm_gated_delta_bwd(const vm_delta *p, const void *dout, const float *dstate,
   a.dg = grad->dg;
   a.dbeta = grad->dbeta;
   a.dh0 = grad->dh0;
-  st = chunk_scratch(a, ws);
+  st = chunk_scratch(a, bf16, true, ws);
   const int64_t per = a.slots * hv;
   a.S = ws.get(per * dk * dv, &st);
   a.dS = ws.get(per * dk * dv, &st);

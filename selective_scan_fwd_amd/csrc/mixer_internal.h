@@ -62,10 +62,15 @@ struct DeltaArgs {
   int nseq, hk, hv, dk, dv;
   int reverse;
   float scale;
-  // per (slot, value head)
-  float *T;                // [64][64]: (I + A)^-1, lower triangular
-  float *P;                // [64][64]: scaled masked products of queries and keys
-  double *gam;             // [64]: running sums of the log decay
+  // Per (slot, value head), written by the preparing kernel.  The matrices are
+  // stored as bf16 terms in the order in which a wave loads them as the left
+  // operand of a matrix instruction: [term][block of 16 x 32][lane][8], the 6
+  // blocks that are not zero.
+  uint16_t *T;             // (I + A)^-1, kTermsT terms
+  uint16_t *P;             // scaled masked products of queries and keys, terms_p
+  uint16_t *TT, *PT;       // their transposes (backward)
+  float *eg, *ew;          // [64]: exp(G), exp(G_C - G) of the running log decay G
+  double *gam;             // [64]: G (backward)
   // forward
   void *out;
   float *state;
@@ -79,9 +84,27 @@ struct DeltaArgs {
   void *dq, *dkey, *dval;
   float *dg, *dbeta, *dh0;
 };
+// Terms of bf16 that stand for an fp32 value (8 bits each, so three hold all
+// 24), and how many are kept of P, which enters the output only: with bf16
+// tokens the output is rounded to 8 bits and 16 suffice.
+constexpr int kTermsT = 3;
+inline int delta_terms_p(bool bf16) { return bf16 ? 2 : 3; }
+constexpr int kTriBlocks = 6;
+constexpr int64_t kTriTerm = kTriBlocks * 64 * 8;   // values of one term
+// Whether every row of q and k is whole 16-byte pieces, and those of v (the
+// backward scan: dout, of token stride os) whole 4-byte ones.
+inline bool delta_vec(const DeltaArgs &a, int64_t esize) {
+  return a.dk % 8 == 0 && (a.qs * esize) % 16 == 0 && (a.ks * esize) % 16 == 0 &&
+         (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && (reinterpret_cast<uintptr_t>(a.k) & 15) == 0;
+}
+inline bool delta_vec_values(const DeltaArgs &a, const void *v, int64_t stride, int64_t esize, int64_t bytes) {
+  return (a.dv * esize) % bytes == 0 && (stride * esize) % bytes == 0 &&
+         (reinterpret_cast<uintptr_t>(v) % bytes) == 0;
+}
 // Chunk slots of `n` sequences over L tokens in all (packed) or each.
 int64_t delta_slots(int64_t batch, int64_t L, int64_t n, bool packed);
-hipError_t launch_delta_prep(const DeltaArgs &a, bool bf16, bool need_p, hipStream_t s);
+// backward: TT, PT and gam instead of P.
+hipError_t launch_delta_prep(const DeltaArgs &a, bool bf16, bool backward, hipStream_t s);
 // keep: store S and V for the backward pass instead of out and state.
 hipError_t launch_delta_scan(const DeltaArgs &a, bool bf16, bool keep, hipStream_t s);
 hipError_t launch_delta_scan_bwd(const DeltaArgs &a, bool bf16, hipStream_t s);
