@@ -24,6 +24,11 @@ HIPCC_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
 
+# The gated delta rule's kernels hold their matrix accumulators in ordinary
+# registers: vector instructions work on them between the products, and with
+# the accumulation registers each such use was a move there and back.
+SOURCE_FLAGS = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for src in SOURCES if src.startswith("delta_")}
+
 
 def hipcc() -> str:
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
@@ -52,7 +57,7 @@ def build(verbose: bool = False) -> str:
         for src in SOURCES + PROBE_SOURCES:
             obj = os.path.join(tmpdir, src + ".o")
             objs[src] = obj
-            cmds.append([hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c",
+            cmds.append([hipcc(), *HIPCC_FLAGS, *SOURCE_FLAGS.get(src, []), "-I", INCLUDE, "-I", CSRC, "-c",
                          os.path.join(CSRC, src), "-o", obj])
         _run(cmds)
         links = []

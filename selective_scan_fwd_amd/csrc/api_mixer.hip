@@ -228,10 +228,11 @@ int vm_gated_delta_bwd(const vm_delta *p, const void *dout, const float *dstate,
   a.dh0 = grad->dh0;
   st = chunk_scratch(a, bf16, true, ws);
   const int64_t per = a.slots * hv;
-  a.S = ws.get(per * dk * dv, &st);
-  a.dS = ws.get(per * dk * dv, &st);
-  a.V = ws.get(per * vmk::kDeltaChunk * dv, &st);
-  a.dR = ws.get(per * vmk::kDeltaChunk * dv, &st);
+  a.dvp = static_cast<int>((dv + 15) / 16 * 16);
+  a.S = ws.get(per * dk * a.dvp, &st);
+  a.dS = ws.get(per * dk * a.dvp, &st);
+  a.V = ws.get(per * vmk::kDeltaChunk * a.dvp, &st);
+  a.dR = ws.get(per * vmk::kDeltaChunk * a.dvp, &st);
   if (st != VM_OK) return st;
   st = hip_status(vmk::launch_delta_prep(a, bf16, true, s));
   if (st == VM_OK) st = hip_status(vmk::launch_delta_scan(a, bf16, true, s));

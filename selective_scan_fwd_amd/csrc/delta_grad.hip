@@ -21,62 +21,142 @@ namespace vmk {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kSlice = 32;              // value columns of one pass
-constexpr int kPitchS = kSlice + 4;
+constexpr int kSlice = 32;              // value columns of one pass, one inner step of the products
+constexpr int kSlicePieces = kSlice / 8;
 
-template <int PITCH>
-__device__ __forceinline__ f32x4 tile_a(const float *m, int rt, int kt, int li, int lg) {
-  return load4(m + (16 * rt + li) * PITCH + 16 * kt + 4 * lg);
-}
-template <int PITCH>
-__device__ __forceinline__ f32x4 tile_at(const float *m, int rt, int kt, int li, int lg) {
-  const float *p = m + (16 * kt + 4 * lg) * PITCH + 16 * rt + li;
-  return f32x4{p[0], p[PITCH], p[2 * PITCH], p[3 * PITCH]};
+// Rows of a slice: 64 bytes a term; piece p of row r at place p ^ (r / 4).
+__device__ __forceinline__ int slice_at(int row, int piece) {
+  return row * kSlice + ((piece ^ ((row >> 2) & 3)) << 3);
 }
 
-// Four values of a row at column c of [..][d], zero past the row's end.
-template <typename T>
-__device__ __forceinline__ f32x4 load_row4(const T *row, int c, int d, bool vec) {
-  if (vec) return c < d ? load4(row + c) : f32x4{0, 0, 0, 0};
-  f32x4 v = {0, 0, 0, 0};
+// The first phase's operands, in terms.
+template <typename T, int DK>
+struct SliceLds {
+  static constexpr int kState = DK * kSlice, kRows = kC * kSlice;   // values of a term
+  __attribute__((aligned(16))) uint16_t s[3 * kState], d[3 * kState], v[3 * kRows], r[3 * kRows],
+      o[kInputTerms<T> * kRows];
+};
+// The second phase's: K, Q and two of the masked products as left operands.
+template <typename T, int DK>
+struct ProductLds {
+  static constexpr int kTerm = kC * DK;
+  __attribute__((aligned(16))) uint16_t k[kInputTerms<T> * kTerm], q[kInputTerms<T> * kTerm];
+  __attribute__((aligned(16))) uint16_t m[3 * kTriTerm], n[3 * kTriTerm];
+};
+
+__device__ __forceinline__ float dot4(f32x4 a, f32x4 b) {
+  return __builtin_fmaf(a[0], b[0], __builtin_fmaf(a[1], b[1], __builtin_fmaf(a[2], b[2], a[3] * b[3])));
+}
+__device__ __forceinline__ f32x4 as_f32(u32x4 x) { return __builtin_bit_cast(f32x4, x); }
+// The piece's values in fp32.
+__device__ __forceinline__ void widen(const Piece<float> &p, f32x4 &a, f32x4 &b) {
+  a = as_f32(p.x[0]);
+  b = as_f32(p.x[1]);
+}
+__device__ __forceinline__ void widen(const Piece<bf16_t> &p, f32x4 &a, f32x4 &b) {
+  a = f32x4{__uint_as_float(p.x[0] << 16), __uint_as_float(p.x[0] & 0xffff0000u), __uint_as_float(p.x[1] << 16),
+            __uint_as_float(p.x[1] & 0xffff0000u)};
+  b = f32x4{__uint_as_float(p.x[2] << 16), __uint_as_float(p.x[2] & 0xffff0000u), __uint_as_float(p.x[3] << 16),
+            __uint_as_float(p.x[3] & 0xffff0000u)};
+}
+template <int TERMS, int TERM>
+__device__ __forceinline__ void put_terms(uint16_t *m, int row, int piece, f32x4 a, f32x4 b) {
+  const Terms<TERMS> t = split<TERMS>(a, b);
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (c + e < d) v[e] = to_f32(row[c + e]);
-  return v;
+  for (int i = 0; i < TERMS; ++i) *reinterpret_cast<bf16x8 *>(m + i * TERM + slice_at(row, piece)) = t.t[i];
+}
+
+// c += a b over the terms whose places add up to less than three.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 product(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4 c) {
+#pragma unroll
+  for (int t = 0; t < NA; ++t)
+#pragma unroll
+    for (int u = 0; u < NB; ++u)
+      if (t + u < 3) c = mfma32(a[t], b[u], c);
+  return c;
+}
+template <int N, int TERM>
+__device__ __forceinline__ void read_slice(const uint16_t *m, int row, int lg, bf16x8 (&x)[N]) {
+#pragma unroll
+  for (int t = 0; t < N; ++t) x[t] = read8(m + t * TERM + slice_at(row, lg));
+}
+// Columns 16 ct .. of four rows at `row`, transposed (natural column order).
+template <int DK>
+__device__ __forceinline__ s16x4 read_tile(const uint16_t *m, int row, int ct, int li) {
+  const int c = li % 4;
+  const uint16_t *p = m + swizzled<DK>(row + li / 4, 2 * ct + c / 2) + 4 * (c % 2);
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) s16x4 *)const_cast<uint16_t *>(p));
+}
+template <int N, int DK>
+__device__ __forceinline__ f32x4 tile_values(const uint16_t *m, int row, int ct, int li) {
+  f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+  for (int t = N - 1; t >= 0; --t) {
+    const s16x4 y = read_tile<DK>(m + t * kC * DK, row, ct, li);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] += to_f32(static_cast<bf16_t>(y[r]));
+  }
+  return x;
+}
+// Columns 16 ct .. of K or Q as a right operand over rows 32 ks ..
+template <int N, int DK>
+__device__ __forceinline__ void read_right(const uint16_t *m, int ks, int ct, int li, int lg, bf16x8 (&x)[N]) {
+#pragma unroll
+  for (int t = 0; t < N; ++t)
+    x[t] = join(read_tile<DK>(m + t * kC * DK, 32 * ks + 4 * lg, ct, li),
+                read_tile<DK>(m + t * kC * DK, 32 * ks + 16 + 4 * lg, ct, li));
+}
+
+// Tiles (c, pt0) and (c, pt1) of rows of `a` by rows of `b`, c <= pt (UP: c >= pt).
+template <int NA, int NB, int TERM, bool UP>
+__device__ __forceinline__ void masked_tiles(const uint16_t *a, const uint16_t *b, int pt0, int pt1, int li, int lg,
+                                             f32x4 (&p0)[2], f32x4 (&p1)[4]) {
+  bf16x8 b0[NB], b1[NB];
+  read_slice<NB, TERM>(b, 16 * pt0 + li, lg, b0);
+  read_slice<NB, TERM>(b, 16 * pt1 + li, lg, b1);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    bf16x8 x[NA];
+    read_slice<NA, TERM>(a, 16 * c + li, lg, x);
+    if (UP ? c >= 2 && c >= pt0 : c < 2 && c <= pt0) p0[c % 2] = product(x, b0, p0[c % 2]);
+    if (UP ? c >= pt1 : c <= pt1) p1[c] = product(x, b1, p1[c]);
+  }
 }
 
 // One workgroup per (chunk slot, key head), the value heads of the key head in
-// turn: dq and dk are summed over them in registers.  Wave w owns rows
-// 16 (w % 4) .. and half w / 4 of the columns.
-template <typename T, int DK>
+// turn: dq and dk are summed over them in registers.
+//
+// Products with S and dS: wave w owns rows 16 (w % 4) .. and half w / 4 of the
+// columns.  Of the four masked products (M, N and their transposes, each as
+// the left operand that the second phase needs) two waves compute one, five
+// 16 x 16 tiles a wave: the rows (lanes) of tiles 0 and 3, or of 1 and 2.
+template <typename T, int DK, bool VEC>
 __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
-  constexpr int kPitch = DK + 4, kNt = DK / 32;
-  __shared__ float sk[kC * kPitch];
-  __shared__ float sq[kC * kPitch];
-  __shared__ float slice[(2 * DK + 3 * kC) * kPitchS];
+  constexpr int kNt = DK / 32, kNi = kInputTerms<T>;
+  typedef SliceLds<T, DK> Slice;
+  typedef ProductLds<T, DK> Product;
+  constexpr int kBuffers = 2 * sizeof(Slice) <= 156 * 1024 ? 2 : 1;
+  constexpr size_t kBytes = kBuffers * sizeof(Slice) > sizeof(Product) ? kBuffers * sizeof(Slice) : sizeof(Product);
+  __shared__ __attribute__((aligned(16))) char raw[kBytes];
   __shared__ double sg[kC];
-  __shared__ float seg[kC], sw[kC], sbeta[kC], srv[kC], swk[8], sdot[8];
-  __shared__ float sgam[2][kC], sbet[2][kC];
-  float *sS = slice, *sD = sS + DK * kPitchS, *sO = sD + DK * kPitchS, *sV = sO + kC * kPitchS,
-        *sR = sV + kC * kPitchS;
-  static_assert((2 * DK + 3 * kC) * kPitchS >= 2 * kC * kPitchC, "the masked products reuse the slices");
-  float *sm = slice, *sn = slice + kC * kPitchC;
+  __shared__ __attribute__((aligned(16))) float seg[kC], sw[kC], sbeta[kC], srv[kC];
+  __shared__ float swk[8], sdot[8], sgam[2][kC], sbet[2][kC];
+  Slice *slices = reinterpret_cast<Slice *>(raw);
+  Product &pr = *reinterpret_cast<Product *>(raw);
   const int64_t slot = blockIdx.x;
   const Seq q = sequence(A, sequence_of(A, slot));
   const int64_t c0 = (slot - q.slot0) * kC;
   if (c0 >= q.len || c0 < 0) return;
-  const int n = q.len - c0 < kC ? static_cast<int>(q.len - c0) : kC;
+  const Window win = window(A, q, c0);
+  const int n = win.n;
   const int kh = blockIdx.y, group = A.hv / A.hk;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, li = lane % 16,
             lg = lane / 16;
   const int rt = wave % 4, half = wave / 4;
-  const int64_t t0 = token_of(A, q, c0, 0), dt = A.reverse ? -1 : 1;
-  stage_rows<DK, kPitch, kThreads>(sk, static_cast<const T *>(A.k) + t0 * A.ks + static_cast<int64_t>(kh) * A.dk,
-                                   dt * A.ks, n, A.dk, can_vec4(A.k, A.ks, A.dk, sizeof(T)));
-  stage_rows<DK, kPitch, kThreads>(sq, static_cast<const T *>(A.q) + t0 * A.qs + static_cast<int64_t>(kh) * A.dk,
-                                   dt * A.qs, n, A.dk, can_vec4(A.q, A.qs, A.dk, sizeof(T)));
-  const bool vec_s = (A.dv & 3) == 0;
-  const bool vec_o = can_vec4(A.dout, A.dv, A.dv, sizeof(T)), vec_v = can_vec4(A.v, A.vs, A.dv, sizeof(T));
+  // masked products: of pt0 at most two tiles are not zero, c % 2 in p0
+  const int pm = wave / 2, pta = wave % 2, pt0 = pm % 2 == 0 ? pta : 3 - pta, pt1 = 3 - pt0;
   const f32x4 zero = {0, 0, 0, 0};
   f32x4 dq[kNt], dk[kNt];
 #pragma unroll
@@ -87,115 +167,212 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
     __syncthreads();
     if (threadIdx.x < kC) {
       const int i = threadIdx.x;
-      const double gi = A.gam[at * kC + i], gl = A.gam[at * kC + kC - 1];
-      sg[i] = gi;
-      seg[i] = hw_exp2(static_cast<float>(gi) * kLog2e);
-      sw[i] = hw_exp2(static_cast<float>(gl - gi) * kLog2e);
+      sg[i] = A.gam[at * kC + i];
+      seg[i] = A.eg[at * kC + i];
+      sw[i] = A.ew[at * kC + i];
       sbeta[i] = i < n ? A.beta[token_of(A, q, c0, i) * A.hv + h] : 0.0f;
     }
-    f32x4 aq[kNt], ak[kNt], ax[kNt], pm[2], pn[2];
+    f32x4 aq[kNt], ak[kNt], ax[kNt], p0[2], p1[4];
 #pragma unroll
     for (int c = 0; c < kNt; ++c) aq[c] = ak[c] = ax[c] = zero;
-    pm[0] = pm[1] = pn[0] = pn[1] = zero;
-    float dot = 0, rv = 0;
-    const float *gS = A.S + at * A.dk * A.dv, *gD = A.dS + at * A.dk * A.dv;
-    const float *gV = A.V + at * kC * A.dv, *gR = A.dR + at * kC * A.dv;
-    for (int v0 = 0; v0 < A.dv; v0 += kSlice) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < DK * (kSlice / 4); i += kThreads) {
-        const int row = i / (kSlice / 4), c = (i % (kSlice / 4)) * 4;
-        f32x4 x = zero, y = zero;
-        if (row < A.dk) {
-          x = load_row4(gS + static_cast<int64_t>(row) * A.dv, v0 + c, A.dv, vec_s);
-          y = load_row4(gD + static_cast<int64_t>(row) * A.dv, v0 + c, A.dv, vec_s);
-        }
-        dot += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
-        *reinterpret_cast<f32x4 *>(sS + row * kPitchS + c) = x;
-        *reinterpret_cast<f32x4 *>(sD + row * kPitchS + c) = y;
-      }
-      {
-        static_assert(kC * (kSlice / 4) == kThreads, "one piece of a row to a thread");
-        const int row = threadIdx.x / (kSlice / 4), c = (threadIdx.x % (kSlice / 4)) * 4;
-        f32x4 o = zero, x = zero, r = zero, v = zero;
-        if (row < n) {
-          const int64_t t = t0 + dt * row;
-          o = load_row4(static_cast<const T *>(A.dout) + (t * A.hv + h) * A.dv, v0 + c, A.dv, vec_o);
-          v = load_row4(static_cast<const T *>(A.v) + t * A.vs + static_cast<int64_t>(h) * A.dv, v0 + c, A.dv, vec_v);
-          x = load_row4(gV + static_cast<int64_t>(row) * A.dv, v0 + c, A.dv, vec_s);
-          r = load_row4(gR + static_cast<int64_t>(row) * A.dv, v0 + c, A.dv, vec_s);
-        }
-        rv += r[0] * v[0] + r[1] * v[1] + r[2] * v[2] + r[3] * v[3];
-        *reinterpret_cast<f32x4 *>(sO + row * kPitchS + c) = o;
-        *reinterpret_cast<f32x4 *>(sV + row * kPitchS + c) = x;
-        *reinterpret_cast<f32x4 *>(sR + row * kPitchS + c) = r;
-      }
-      __syncthreads();
 #pragma unroll
-      for (int kt = 0; kt < kSlice / 16; ++kt) {
-        const f32x4 o = tile_a<kPitchS>(sO, rt, kt, li, lg), v = tile_a<kPitchS>(sV, rt, kt, li, lg),
-                    r = tile_a<kPitchS>(sR, rt, kt, li, lg);
+    for (int c = 0; c < 4; ++c) p0[c / 2] = p1[c] = zero;
+    float dot = 0, rv = 0;
+    const Rsrc gS = buffer(A.S + at * A.dk * A.dvp, A.dk * A.dvp * 4), gD = buffer(A.dS + at * A.dk * A.dvp, A.dk * A.dvp * 4);
+    const Rsrc gV = buffer(A.V + at * kC * A.dvp), gR = buffer(A.dR + at * kC * A.dvp);
+    const int64_t os = static_cast<int64_t>(A.hv) * A.dv;
+    const Rsrc gO = buffer(static_cast<const T *>(A.dout) + win.low * os + static_cast<int64_t>(h) * A.dv);
+    const Rsrc gv = buffer(static_cast<const T *>(A.v) + win.low * A.vs + static_cast<int64_t>(h) * A.dv);
+    // a thread's piece of S and dS, and of dR and v (first half) or V and dout
+    const int srow = threadIdx.x / kSlicePieces, piece = threadIdx.x % kSlicePieces, row = srow % kC;
+    static_assert(kC * kSlicePieces == 4 * 64, "the first half is waves 0 to 3");
+    const bool first = wave < 4;
+    Piece<float> ls, ld, lx;
+    Piece<T> ly;
+    auto load = [&](int v0) {
+      const int c = v0 + 8 * piece;
+      const uint32_t ok = c < A.dvp ? (srow * A.dvp + c) * 4 : kNowhere;
+      if (DK * kSlicePieces >= kThreads || srow < DK) {
+        ls = load_piece<true>(gS, ok, c, A.dvp, 0.0f);
+        ld = load_piece<true>(gD, ok, c, A.dvp, 0.0f);
+      }
+      const uint32_t rk = c < A.dvp ? (row * A.dvp + c) * 4 : kNowhere;
+      lx = load_piece<true>(first ? gR : gV, rk, c, A.dvp, 0.0f);
+      const uint32_t tk = row < n && c < A.dv ? win.at(A, row, (first ? A.vs : os) * sizeof(T)) + c * sizeof(T) : kNowhere;
+      ly = load_piece<VEC>(first ? gv : gO, tk, c, A.dv, T());
+    };
+    auto store = [&](Slice &l) {
+      f32x4 a, b, x, y;
+      if (DK * kSlicePieces >= kThreads || srow < DK) {
+        widen(ls, a, b);
+        widen(ld, x, y);
+        dot += dot4(a, x) + dot4(b, y);
+        put_terms<3, Slice::kState>(l.s, srow, piece, a, b);
+        put_terms<3, Slice::kState>(l.d, srow, piece, x, y);
+      }
+      widen(lx, a, b);
+      widen(ly, x, y);
+      put_terms<3, Slice::kRows>(first ? l.r : l.v, row, piece, a, b);
+      if (first)
+        rv += dot4(a, x) + dot4(b, y);
+      else
+        put_terms<kNi, Slice::kRows>(l.o, row, piece, x, y);
+    };
+    load(0);
+    store(slices[0]);
+    __syncthreads();
+    int buf = 0;
+    for (int v0 = 0; v0 < A.dv; v0 += kSlice) {
+      const Slice &l = slices[buf];
+      const bool more = v0 + kSlice < A.dv;
+      if (more) load(v0 + kSlice);
+      {
+        bf16x8 o[kNi], v[3], r[3];
+        read_slice<kNi, Slice::kRows>(l.o, 16 * rt + li, lg, o);
+        read_slice<3, Slice::kRows>(l.v, 16 * rt + li, lg, v);
+        read_slice<3, Slice::kRows>(l.r, 16 * rt + li, lg, r);
 #pragma unroll
         for (int c = 0; c < kNt; ++c) {
-          const f32x4 bs = tile_a<kPitchS>(sS, half * kNt + c, kt, li, lg),
-                      bd = tile_a<kPitchS>(sD, half * kNt + c, kt, li, lg);
-          aq[c] = mfma16(o, bs, aq[c]);
-          ax[c] = mfma16(r, bs, ax[c]);
-          ak[c] = mfma16(v, bd, ak[c]);
+          bf16x8 b[3];
+          read_slice<3, Slice::kState>(l.s, 16 * (half * kNt + c) + li, lg, b);
+          aq[c] = product(o, b, aq[c]);
+          ax[c] = product(r, b, ax[c]);
+          read_slice<3, Slice::kState>(l.d, 16 * (half * kNt + c) + li, lg, b);
+          ak[c] = product(v, b, ak[c]);
         }
+      }
+      // masked products: rows (inner indices of the next phase) of tile c,
+      // columns (lanes) of tiles pt0 and pt1
+      if (pm == 0) {                       // M: V_j by dout_i, j <= i
+        masked_tiles<3, kNi, Slice::kRows, false>(l.v, l.o, pt0, pt1, li, lg, p0, p1);
+      } else if (pm == 1) {                // its transpose: dout_i by V_j, i >= j
+        masked_tiles<kNi, 3, Slice::kRows, true>(l.o, l.v, pt0, pt1, li, lg, p0, p1);
+      } else if (pm == 2) {                // N: V_j by dR_i
+        masked_tiles<3, 3, Slice::kRows, false>(l.v, l.r, pt0, pt1, li, lg, p0, p1);
+      } else {                             // its transpose
+        masked_tiles<3, 3, Slice::kRows, true>(l.r, l.v, pt0, pt1, li, lg, p0, p1);
+      }
+      if (kBuffers == 1) __syncthreads();
+      buf = kBuffers == 2 ? buf ^ 1 : 0;
+      if (more) store(slices[buf]);
+      __syncthreads();
+    }
+    // second phase: K and Q, the sums that the loading threads hold
+    {
+      const Rsrc rk = buffer(static_cast<const T *>(A.k) + win.low * A.ks + static_cast<int64_t>(kh) * A.dk);
+      const Rsrc rq = buffer(static_cast<const T *>(A.q) + win.low * A.qs + static_cast<int64_t>(kh) * A.dk);
+      constexpr int kPieces = DK / 8;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (2 * half + c > rt) continue;
-          const f32x4 b = tile_a<kPitchS>(sV, 2 * half + c, kt, li, lg);
-          pm[c] = mfma16(o, b, pm[c]);
-          pn[c] = mfma16(r, b, pn[c]);
-        }
+      for (int x = 0; x < kC * kPieces / kThreads; ++x) {
+        const int i = threadIdx.x + x * kThreads, r = i / kPieces, p = i % kPieces;
+        const bool in = r < n && 8 * p < A.dk;
+        const Piece<T> a = load_piece<VEC>(rk, in ? win.at(A, r, A.ks * sizeof(T)) + 8 * p * sizeof(T) : kNowhere, 8 * p, A.dk, T());
+        const Piece<T> b = load_piece<VEC>(rq, in ? win.at(A, r, A.qs * sizeof(T)) + 8 * p * sizeof(T) : kNowhere, 8 * p, A.dk, T());
+        store_piece<DK>(pr.k, Product::kTerm, r, p, a);
+        store_piece<DK>(pr.q, Product::kTerm, r, p, b);
       }
     }
-    __syncthreads();
-    // masked products, and the sums that the staging threads hold
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * rt + 4 * lg + r, j = 16 * (2 * half + c) + li;
-        const float d = i >= j ? hw_exp2(static_cast<float>(sg[i] - sg[j]) * kLog2e) : 0.0f;
-        sm[i * kPitchC + j] = i >= j ? A.scale * d * pm[c][r] : 0.0f;
-        sn[i * kPitchC + j] = i > j ? -d * pn[c][r] : 0.0f;
-      }
-#pragma unroll
-    for (int o = 1; o < kSlice / 4; o *= 2) rv += __shfl_xor(rv, o);
-    if (threadIdx.x % (kSlice / 4) == 0) srv[threadIdx.x / (kSlice / 4)] = rv;
+    for (int o = 1; o < kSlicePieces; o *= 2) rv += __shfl_xor(rv, o);
+    if (first && piece == 0) srv[row] = rv;
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) dot += __shfl_xor(dot, o);
     if (lane == 0) sdot[wave] = dot;
+    // the masked products' factors, and their way to LDS as left operands
+    auto put_masked = [&](uint16_t *dst, bool transposed, bool is_n) {
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const int ct = side == 0 ? pt0 : pt1, a = 16 * ct + li;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          if (side == 0 ? ks != (transposed ? 1 : 0) : (transposed ? ct >= 2 && ks == 0 : ct < 2 && ks == 1)) continue;
+          f32x4 x[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            x[u] = side == 0 ? p0[u] : p1[2 * ks + u];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int b = 16 * (2 * ks + u) + 4 * lg + r, i = transposed ? b : a, j = transposed ? a : b;
+              const bool in = is_n ? i > j : i >= j;
+              const float d = hw_exp2(static_cast<float>(sg[i] - sg[j]) * kLog2e);
+              const float f = is_n ? (transposed ? -sbeta[i] : -1.0f) : A.scale;
+              x[u][r] = in ? x[u][r] * d * f : 0.0f;
+            }
+          }
+          const Terms<3> t = split<3>(x[0], x[1]);
+          const int block = transposed ? tri_block_t(ct, ks) : tri_block(ct, ks);
+#pragma unroll
+          for (int y = 0; y < 3; ++y) *reinterpret_cast<bf16x8 *>(dst + y * kTriTerm + (block * 64 + lane) * 8) = t.t[y];
+        }
+      }
+    };
+    if (pm == 0) put_masked(pr.m, false, false);
+    if (pm == 2) put_masked(pr.n, false, true);
     __syncthreads();
     const f32x4 eg = load4(seg + 16 * rt + 4 * lg), w = load4(sw + 16 * rt + 4 * lg),
                 be = load4(sbeta + 16 * rt + 4 * lg);
     f32x4 sum_g = zero, sum_b = zero, sum_w = zero;     // over this wave's columns
+    f32x4 y[kNt];
 #pragma unroll
     for (int c = 0; c < kNt; ++c) {
-      const int ct = half * kNt + c;
-      f32x4 xq = aq[c] * eg * A.scale, z1 = ak[c] * w, y = zero;
-      const f32x4 kr = tile_at<kPitch>(sk, ct, rt, li, lg), qr = tile_at<kPitch>(sq, ct, rt, li, lg);
-      sum_w += z1 * kr;
+      aq[c] = aq[c] * eg * A.scale;
+      y[c] = zero;
+    }
 #pragma unroll
-      for (int kt = 0; kt < 4; ++kt) {
-        const f32x4 bk = tile_at<kPitch>(sk, ct, kt, li, lg);
-        if (kt <= rt) {
-          xq = mfma16(tile_a<kPitchC>(sm, rt, kt, li, lg), bk, xq);
-          y = mfma16(tile_a<kPitchC>(sn, rt, kt, li, lg), bk, y);
-        }
-        if (kt >= rt) {
-          const f32x4 bq = tile_at<kPitch>(sq, ct, kt, li, lg);
-          z1 = mfma16(tile_at<kPitchC>(sm, rt, kt, li, lg), bq, z1);
-          z1 = mfma16(tile_at<kPitchC>(sn, rt, kt, li, lg) * load4(sbeta + 16 * kt + 4 * lg), bk, z1);
-        }
+    for (int ks = 0; ks < 2; ++ks) {
+      if (rt < 2 && ks == 1) continue;
+      bf16x8 m[3], nn[3];
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        m[t] = read8(pr.m + t * kTriTerm + (tri_block(rt, ks) * 64 + lane) * 8);
+        nn[t] = read8(pr.n + t * kTriTerm + (tri_block(rt, ks) * 64 + lane) * 8);
       }
-      const f32x4 x = ax[c] * eg, z2 = (y - x) * be;
-      sum_b += kr * (y - x);
-      sum_g += qr * xq + kr * (z2 - z1);
-      dq[c] += xq;
-      dk[c] += z1 + z2;
+#pragma unroll
+      for (int c = 0; c < kNt; ++c) {
+        bf16x8 b[kNi];
+        read_right<kNi, DK>(pr.k, ks, half * kNt + c, li, lg, b);
+        aq[c] = product(m, b, aq[c]);
+        y[c] = product(nn, b, y[c]);
+      }
+    }
+    __syncthreads();
+    if (pm == 1) put_masked(pr.m, true, false);
+    if (pm == 3) put_masked(pr.n, true, true);
+#pragma unroll
+    for (int c = 0; c < kNt; ++c) {
+      const f32x4 kr = tile_values<kNi, DK>(pr.k, 16 * rt + 4 * lg, half * kNt + c, li);
+      const f32x4 qr = tile_values<kNi, DK>(pr.q, 16 * rt + 4 * lg, half * kNt + c, li);
+      ak[c] *= w;
+      sum_w += ak[c] * kr;
+      y[c] -= ax[c] * eg;
+      sum_b += kr * y[c];
+      sum_g += qr * aq[c] + kr * y[c] * be;
+      dq[c] += aq[c];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      if (rt >= 2 && ks == 0) continue;
+      bf16x8 m[3], nn[3];
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        m[t] = read8(pr.m + t * kTriTerm + (tri_block_t(rt, ks) * 64 + lane) * 8);
+        nn[t] = read8(pr.n + t * kTriTerm + (tri_block_t(rt, ks) * 64 + lane) * 8);
+      }
+#pragma unroll
+      for (int c = 0; c < kNt; ++c) {
+        bf16x8 b[kNi];
+        read_right<kNi, DK>(pr.q, ks, half * kNt + c, li, lg, b);
+        ak[c] = product(m, b, ak[c]);
+        read_right<kNi, DK>(pr.k, ks, half * kNt + c, li, lg, b);
+        ak[c] = product(nn, b, ak[c]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kNt; ++c) {
+      const f32x4 kr = tile_values<kNi, DK>(pr.k, 16 * rt + 4 * lg, half * kNt + c, li);
+      sum_g -= kr * ak[c];
+      dk[c] += ak[c] + y[c] * be;
     }
 #pragma unroll
     for (int o = 1; o < 16; o *= 2)
@@ -226,8 +403,8 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
       float x = sgam[0][lane] + sgam[1][lane];
       if (lane == 63) x += seg[kC - 1] * ss + sk_all;
       for (int o = 1; o < 64; o *= 2) {
-        const float y = __shfl_down(x, o);
-        if (lane + o < 64) x += y;
+        const float z = __shfl_down(x, o);
+        if (lane + o < 64) x += z;
       }
       if (lane < n) {
         const int64_t i = token_of(A, q, c0, lane) * A.hv + h;
@@ -236,23 +413,37 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
       }
     }
   }
+  const int64_t os = static_cast<int64_t>(A.hk) * A.dk;
+  const Rsrc oq = buffer(static_cast<T *>(A.dq) + win.low * os + static_cast<int64_t>(kh) * A.dk);
+  const Rsrc ok = buffer(static_cast<T *>(A.dkey) + win.low * os + static_cast<int64_t>(kh) * A.dk);
 #pragma unroll
-  for (int c = 0; c < kNt; ++c)
+  for (int r = 0; r < 4; ++r) {
+    const int i = 16 * rt + 4 * lg + r;
+    const uint32_t at = i < n ? win.at(A, i, os * sizeof(T)) : kNowhere;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = 16 * rt + 4 * lg + r, col = 16 * (half * kNt + c) + li;
-      if (i < n && col < A.dk) {
-        const int64_t o = ((t0 + dt * i) * A.hk + kh) * A.dk + col;
-        static_cast<T *>(A.dq)[o] = from_f32<T>(dq[c][r]);
-        static_cast<T *>(A.dkey)[o] = from_f32<T>(dk[c][r]);
+    for (int c = 0; c < kNt; ++c) {
+      const int col = 16 * (half * kNt + c) + li;
+      const uint32_t o = col < A.dk ? at + col * sizeof(T) : kNowhere;
+      if constexpr (kNi == 1) {
+        const uint32_t y = pack2(dq[c][r], dk[c][r]);
+        bstore(oq, o, static_cast<bf16_t>(y));
+        bstore(ok, o, static_cast<bf16_t>(y >> 16));
+      } else {
+        bstore(oq, o, dq[c][r]);
+        bstore(ok, o, dk[c][r]);
       }
     }
+  }
 }
 
 template <typename T, int DK>
 hipError_t launch(const DeltaArgs &a, hipStream_t s) {
   const dim3 grid(static_cast<uint32_t>(a.slots), a.hk);
-  hipLaunchKernelGGL((delta_grad_kernel<T, DK>), grid, dim3(kThreads), 0, s, a);
+  if (delta_vec(a, sizeof(T)) && delta_vec_values(a, a.v, a.vs, sizeof(T), 16) && a.dv % 8 == 0 &&
+      delta_vec_values(a, a.dout, static_cast<int64_t>(a.hv) * a.dv, sizeof(T), 16))
+    hipLaunchKernelGGL((delta_grad_kernel<T, DK, true>), grid, dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((delta_grad_kernel<T, DK, false>), grid, dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 

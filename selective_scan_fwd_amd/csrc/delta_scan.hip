@@ -21,9 +21,6 @@ namespace {
 //
 // Rows of the state are held so that K's rows are read in whole pieces: row
 // 4 lg + r of tile 2 ks + p is state row 32 ks + 8 lg + 4 p + r.
-#ifndef VMK_OCC
-#define VMK_OCC 1
-#endif
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kCols = 16 * kWaves;         // state columns of a workgroup
@@ -251,26 +248,40 @@ __device__ __forceinline__ void rows_times(const uint16_t *m, const Terms<NB> (&
   }
 }
 
-// x[d] += columns (state rows of tile d) of m times b, over the 64 rows of m.
-template <int DK, int NA, int NB>
-__device__ __forceinline__ void columns_times(const uint16_t *m, const Terms<NB> (&b)[2], int li, int lg,
-                                              f32x4 (&x)[DK / 16]) {
+// The columns (state rows) of one term of m as left operands, over the 64 rows of
+// m.  Where the next chunk is on its way to LDS they are read before it is sent
+// for: the compiler lets no transposing read pass a load to LDS without waiting
+// for that load.
+template <int DK>
+struct Columns {
+  bf16x8 a[2][DK / 16];
+  __device__ __forceinline__ void read(const uint16_t *m, int li, int lg) {
 #pragma unroll
-  for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-    for (int t = 0; t < NA; ++t) {
-      bf16x8 a[DK / 16];
+    for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
       for (int d = 0; d < DK / 16; ++d)
-        a[d] = join(read_columns<DK>(m + t * kC * DK, 32 * kt + 4 * lg, d / 2, d & 1, li),
-                    read_columns<DK>(m + t * kC * DK, 32 * kt + 16 + 4 * lg, d / 2, d & 1, li));
+        a[kt][d] = join(read_columns<DK>(m, 32 * kt + 4 * lg, d / 2, d & 1, li),
+                        read_columns<DK>(m, 32 * kt + 16 + 4 * lg, d / 2, d & 1, li));
+  }
+};
+
+// x[d] += columns (state rows of tile d) of m times b.  first: m's first term.
+template <int DK, int NA, int NB>
+__device__ __forceinline__ void columns_times(const Columns<DK> &first, const uint16_t *m, const Terms<NB> (&b)[2], int li,
+                                              int lg, f32x4 (&x)[DK / 16]) {
+#pragma unroll
+  for (int t = 0; t < NA; ++t) {
+    Columns<DK> c = first;
+    if (t > 0) c.read(m + t * kC * DK, li, lg);
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
       for (int u = 0; u < NB; ++u) {
         if (t + u >= (NA > NB ? NA : NB)) continue;
 #pragma unroll
-        for (int d = 0; d < DK / 16; ++d) x[d] = mfma32(a[d], b[kt].t[u], x[d]);
+        for (int d = 0; d < DK / 16; ++d) x[d] = mfma32(c.a[kt][d], b[kt].t[u], x[d]);
       }
-    }
+  }
 }
 
 // x[rt] += row tiles of a triangular operand (TR: of its transpose) times b.
@@ -314,17 +325,17 @@ __device__ __forceinline__ Place place(const DeltaArgs &A, int colblocks) {
   return p;
 }
 
-// One chunk's D tiles [DK][16] of fp32 at [dk][dv] memory, and [64][16] at
-// [64][dv] or at token rows; columns that are not the head's go nowhere.
+// D tiles [DK][16] at [dk][cols] memory, and [64][16] at [64][dvp]; columns past
+// them go nowhere.
 template <int DK>
-__device__ __forceinline__ void store_state(const DeltaArgs &A, float *base, const f32x4 (&S)[DK / 16], int lg, int col) {
+__device__ __forceinline__ void store_state(const DeltaArgs &A, float *base, int cols, const f32x4 (&S)[DK / 16], int lg, int col) {
   // (rows past dk lie past the resource's end)
-  const Rsrc r = buffer(base, A.dk * A.dv * 4);
-  const uint32_t first = col < A.dv ? (8 * lg * A.dv + col) * 4 : kNowhere;
+  const Rsrc r = buffer(base, A.dk * cols * 4);
+  const uint32_t first = col < cols ? (8 * lg * cols + col) * 4 : kNowhere;
 #pragma unroll
   for (int d = 0; d < DK / 16; ++d)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) bstore(r, first + (state_row(d, 0, e) * A.dv) * 4, S[d][e]);
+    for (int e = 0; e < 4; ++e) bstore(r, first + state_row(d, 0, e) * cols * 4, S[d][e]);
 }
 template <int DK>
 __device__ __forceinline__ void load_state(const DeltaArgs &A, const float *base, f32x4 (&S)[DK / 16], int lg, int col) {
@@ -339,17 +350,17 @@ __device__ __forceinline__ void load_state(const DeltaArgs &A, const float *base
 }
 __device__ __forceinline__ void store_rows(const DeltaArgs &A, float *base, const f32x4 (&x)[4], int lg, int col) {
   const Rsrc r = buffer(base);
-  const uint32_t first = col < A.dv ? (4 * lg * A.dv + col) * 4 : kNowhere;
+  const uint32_t first = col < A.dvp ? (4 * lg * A.dvp + col) * 4 : kNowhere;
 #pragma unroll
   for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) bstore(r, first + (16 * rt + e) * A.dv * 4, x[rt][e]);
+    for (int e = 0; e < 4; ++e) bstore(r, first + (16 * rt + e) * A.dvp * 4, x[rt][e]);
 }
 template <typename T> constexpr bool kDirect = sizeof(T) == 2;
 
 // Forward.  KEEP: S and V are stored for the backward pass, out and state not.
 template <typename T, int DK, bool KEEP, bool VEC>
-__global__ __launch_bounds__(kThreads, VMK_OCC) void delta_scan_kernel(DeltaArgs A, int colblocks) {
+__global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs A, int colblocks) {
   constexpr int kNi = kInputTerms<T>, kNs = 3;
   constexpr int kTermsP = KEEP ? 0 : kNi == 1 ? 2 : 3;
   constexpr int kNo = kNi == 1 ? 2 : 3;               // terms of S and V on their way to out only
@@ -382,12 +393,14 @@ __global__ __launch_bounds__(kThreads, VMK_OCC) void delta_scan_kernel(DeltaArgs
     const Lds &l = lds[buf];
     f32x4 v[4];
     next.values(l, v);
+    Columns<DK> kc;
+    if (kDma) kc.read(l.k, li, lg);
     const bool more = c0 + kC < q.len;
     if (more) next.load(A, q, c0 + kC, A.T, A.P, lds[kBuffers == 2 ? buf ^ 1 : 0]);
     Terms<kNs> st[DK / 32];
 #pragma unroll
     for (int ks = 0; ks < DK / 32; ++ks) st[ks] = split<kNs>(S[2 * ks], S[2 * ks + 1]);
-    if (KEEP) store_state<DK>(A, A.S + at * A.dk * A.dv, S, lg, col);
+    if (KEEP) store_state<DK>(A, A.S + at * A.dk * A.dvp, A.dvp, S, lg, col);
     f32x4 x[4];
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) x[rt] = f32x4{0, 0, 0, 0};
@@ -421,7 +434,8 @@ __global__ __launch_bounds__(kThreads, VMK_OCC) void delta_scan_kernel(DeltaArgs
     const float last = l.eg[kC - 1];
 #pragma unroll
     for (int d = 0; d < DK / 16; ++d) S[d] *= last;
-    columns_times<DK, kNi, kNs>(l.k, r3, li, lg, S);
+    if (!kDma) kc.read(l.k, li, lg);
+    columns_times<DK, kNi, kNs>(kc, l.k, r3, li, lg, S);
     if constexpr (!KEEP) {
       Terms<kNo> vo[2];
       split_rows<kNo>(V, vo);
@@ -436,15 +450,15 @@ __global__ __launch_bounds__(kThreads, VMK_OCC) void delta_scan_kernel(DeltaArgs
       rows.plan(A, w, static_cast<int64_t>(A.hv) * A.dv * sizeof(T), sizeof(T), lg, col);
       store_tokens(static_cast<T *>(A.out) + (w.low * A.hv + h) * A.dv, rows, o);
     } else {
-      store_rows(A, A.V + at * kC * A.dv, V, lg, col);
+      store_rows(A, A.V + at * kC * A.dvp, V, lg, col);
     }
     __syncthreads();
   }
-  if (!KEEP && A.state != nullptr) store_state<DK>(A, A.state + state_at, S, lg, col);
+  if (!KEEP && A.state != nullptr) store_state<DK>(A, A.state + state_at, A.dv, S, lg, col);
 }
 
 template <typename T, int DK, bool VEC>
-__global__ __launch_bounds__(kThreads, VMK_OCC) void delta_scan_bwd_kernel(DeltaArgs A, int colblocks) {
+__global__ __launch_bounds__(kThreads) void delta_scan_bwd_kernel(DeltaArgs A, int colblocks) {
   constexpr int kNi = kInputTerms<T>, kNs = 3;
   constexpr int kTermsP = kNi == 1 ? 2 : 3;
   constexpr bool kDma = VEC && kDirect<T>;
@@ -478,8 +492,13 @@ __global__ __launch_bounds__(kThreads, VMK_OCC) void delta_scan_bwd_kernel(Delta
     const Lds &l = lds[buf];
     f32x4 o[4];
     next.values(l, o);
+    Columns<DK> kc, qc;
+    if (kDma) {
+      kc.read(l.k, li, lg);
+      qc.read(l.q, li, lg);
+    }
     if (c0 > 0) next.load(A, q, c0 - kC, A.TT, A.PT, lds[kBuffers == 2 ? buf ^ 1 : 0]);
-    store_state<DK>(A, A.dS + at * A.dk * A.dv, D, lg, col);
+    store_state<DK>(A, A.dS + at * A.dk * A.dvp, A.dvp, D, lg, col);
     f32x4 V[4], R[4];
     {
       Terms<kNs> st[DK / 32];
@@ -513,18 +532,20 @@ __global__ __launch_bounds__(kThreads, VMK_OCC) void delta_scan_bwd_kernel(Delta
 #pragma unroll
     for (int d = 0; d < DK / 16; ++d) D[d] *= last;
     split_rows<kNs>(x, t3);
-    columns_times<DK, kNi, kNs>(l.k, t3, li, lg, D);
+    if (!kDma) kc.read(l.k, li, lg);
+    columns_times<DK, kNi, kNs>(kc, l.k, t3, li, lg, D);
     split_rows<kNs>(o, t3);
-    columns_times<DK, kNi, kNs>(l.q, t3, li, lg, D);
+    if (!kDma) qc.read(l.q, li, lg);
+    columns_times<DK, kNi, kNs>(qc, l.q, t3, li, lg, D);
     if (kBuffers == 1) __syncthreads();
     buf = kBuffers == 2 ? buf ^ 1 : 0;
     if (c0 > 0) next.store(lds[buf]);
-    store_rows(A, A.dR + at * kC * A.dv, R, lg, col);
+    store_rows(A, A.dR + at * kC * A.dvp, R, lg, col);
     rows.plan(A, w, row * sizeof(T), sizeof(T), lg, col);
     store_tokens(static_cast<T *>(A.dval) + (w.low * A.hv + h) * A.dv, rows, dv);
     __syncthreads();
   }
-  if (A.dh0 != nullptr) store_state<DK>(A, A.dh0 + state_at, D, lg, col);
+  if (A.dh0 != nullptr) store_state<DK>(A, A.dh0 + state_at, A.dv, D, lg, col);
 }
 
 int column_blocks(const DeltaArgs &a) { return (a.dv + 16 * kWaves - 1) / (16 * kWaves); }

@@ -77,10 +77,12 @@ struct DeltaArgs {
   // backward
   const void *dout;
   const float *dstate;
-  float *S;                // per (slot, value head) [dk][dv]: state at the chunk's start
-  float *V;                // [64][dv]: the chunk's corrected values
-  float *dS;               // [dk][dv]: gradient of the state at the chunk's end
-  float *dR;               // [64][dv]
+  // per (slot, value head), rows of dvp = dv rounded up to 16 values, zero past dv
+  int dvp;
+  float *S;                // [dk][dvp]: state at the chunk's start
+  float *V;                // [64][dvp]: the chunk's corrected values
+  float *dS;               // [dk][dvp]: gradient of the state at the chunk's end
+  float *dR;               // [64][dvp]
   void *dq, *dkey, *dval;
   float *dg, *dbeta, *dh0;
 };
