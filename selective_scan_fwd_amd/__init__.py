@@ -18,7 +18,9 @@ Names and argument order follow the C ABI:
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import itertools
 import os
 import threading
 
@@ -588,56 +590,75 @@ def vm_ss2d_scan_bwd(u, dirs, dout, z=None, combine_scale=1.0, delta_softplus=Tr
 
 
 # ------------------------------------------------------- matrix-state mixers
-def _tokens(t, name, dtype, shape, device):
+def _arg(t, name, dtype, shape, index):
+    """Address of a contiguous tensor (None = NULL).  index: the GPU's number.
+    The one quick test covers the good case; _dev says what is wrong."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0
+            and t.is_contiguous()):
+        _dev(t, name, dtype, shape, torch.device("cuda", index) if index >= 0 else None)
+    return t.data_ptr()
+
+
+def _launch(name, index, *args):
+    """Call an entry point on the current stream of GPU `index`."""
+    if index == torch.cuda.current_device():
+        st = getattr(load_library(), name)(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            st = getattr(load_library(), name)(*args, torch.cuda.current_stream().cuda_stream)
+    if st != VM_OK:
+        _check(st, name)
+
+
+def _tokens(t, name, dtype, shape, index):
     """q, k or v [batch, seqlen, heads, dim]: each token's heads contiguous,
-    tokens evenly spaced.  Returns the C ABI's token stride (0 = dense)."""
+    tokens evenly spaced.  Returns the address and the C ABI's token stride
+    (0 = dense)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda" or t.device != device:
-        raise ValueError(f"{name} must be on a GPU device, {device} (got {t.device})")
-    if t.dtype != dtype:
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be on a GPU device{', cuda:%d' % index if index >= 0 else ''} (got {t.device})")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.is_contiguous():
-        return 0
+        return t.data_ptr(), 0
     batch, L, heads, dim = shape
     sb, st, sh, sd = t.stride()
     step = st if L > 1 else sb                   # (one token a row: the batch stride is the token stride)
     if (sd == 1 or dim == 1) and (sh == dim or heads == 1) and step >= heads * dim and \
             (L == 1 or batch == 1 or sb == L * st):
-        return step
+        return t.data_ptr(), step
     raise ValueError(f"{name} must be [batch, seqlen, heads, dim] with contiguous heads and evenly spaced "
                      f"tokens (strides {t.stride()})")
 
 
 def _delta(q, k, v, g, beta, h0, offsets):
-    """Validate the gated delta rule's inputs; returns (VmDelta, sizes)."""
+    """Validate the gated delta rule's inputs; returns (VmDelta, GPU, sizes)."""
     for name, t in (("q", q), ("k", k), ("v", v)):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError(f"{name} must be a [batch, seqlen, heads, dim] tensor")
     batch, L, hk, dk = q.shape
     hv, dv = v.shape[2:]
-    dev = q.device
-    sq = _tokens(q, "q", q.dtype, (batch, L, hk, dk), dev)
-    sk = _tokens(k, "k", q.dtype, (batch, L, hk, dk), dev)
-    sv = _tokens(v, "v", q.dtype, (batch, L, hv, dv), dev)
-    _dev(g, "g", torch.float32, (batch, L, hv), dev)
-    _dev(beta, "beta", torch.float32, (batch, L, hv), dev)
-    n = batch
+    index, dtype = q.get_device(), q.dtype
+    pq, sq = _tokens(q, "q", dtype, (batch, L, hk, dk), index)
+    pk, sk = _tokens(k, "k", dtype, (batch, L, hk, dk), index)
+    pv, sv = _tokens(v, "v", dtype, (batch, L, hv, dv), index)
+    pg = _arg(g, "g", torch.float32, (batch, L, hv), index)
+    pb = _arg(beta, "beta", torch.float32, (batch, L, hv), index)
+    n, po = batch, None
     if offsets is not None:
         if batch != 1:
             raise ValueError("packed sequences (offsets) take batch 1")
         if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
             raise ValueError("offsets must be an int32 tensor [sequences + 1]")
-        _dev(offsets, "offsets", torch.int32, None, dev)
         n = offsets.shape[0] - 1
-    if h0 is not None:
-        _dev(h0, "h0", torch.float32, (n, hv, dk, dv), dev)
-    ptr = lambda t: t.data_ptr() if t is not None else None
-    s = VmDelta(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), ptr(h0), ptr(offsets),
-                sq, sk, sv)
-    return s, (batch, L, n, hk, hv, dk, dv)
+        po = _arg(offsets, "offsets", torch.int32, (n + 1,), index)
+    ph = _arg(h0, "h0", torch.float32, (n, hv, dk, dv), index)
+    return VmDelta(pq, pk, pv, pg, pb, ph, po, sq, sk, sv), index, (batch, L, n, hk, hv, dk, dv)
 
 
 def vm_gated_delta_fwd(q, k, v, g, beta, scale=None, h0=None, want_state=False, reverse=False, offsets=None,
@@ -651,19 +672,14 @@ def vm_gated_delta_fwd(q, k, v, g, beta, scale=None, h0=None, want_state=False, 
     sequence from its last token.  out is [batch, L, hv, dv]; state (the last
     states, [n, hv, dk, dv] fp32) is None unless want_state or a state buffer
     (which may be h0) is given."""
-    p, (batch, L, n, hk, hv, dk, dv) = _delta(q, k, v, g, beta, h0, offsets)
-    dev = q.device
-    out = torch.empty((batch, L, hv, dv), dtype=q.dtype, device=dev) if out is None else \
-        _dev(out, "out", q.dtype, (batch, L, hv, dv), dev)
-    if state is not None:
-        _dev(state, "state", torch.float32, (n, hv, dk, dv), dev)
-    elif want_state:
-        state = torch.empty((n, hv, dk, dv), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        st = load_library().vm_gated_delta_fwd(ctypes.byref(p), _ptr(out), _ptr(state),
-                                               float(dk ** -0.5 if scale is None else scale), batch, L, n, hk, hv, dk,
-                                               dv, _dtype_code(q), int(bool(reverse)), _stream(dev))
-    _check(st, "vm_gated_delta_fwd")
+    p, index, (batch, L, n, hk, hv, dk, dv) = _delta(q, k, v, g, beta, h0, offsets)
+    if out is None:
+        out = torch.empty((batch, L, hv, dv), dtype=q.dtype, device=q.device)
+    if state is None and want_state:
+        state = torch.empty((n, hv, dk, dv), dtype=torch.float32, device=q.device)
+    _launch("vm_gated_delta_fwd", index, p, _arg(out, "out", q.dtype, (batch, L, hv, dv), index),
+            _arg(state, "state", torch.float32, (n, hv, dk, dv), index), dk ** -0.5 if scale is None else scale, batch, L,
+            n, hk, hv, dk, dv, _dtype_code(q), int(bool(reverse)))
     return out, state
 
 
@@ -671,22 +687,17 @@ def vm_gated_delta_bwd(q, k, v, g, beta, dout, scale=None, h0=None, dstate=None,
     """Gradients of sum(dout * out) + sum(dstate * state) of vm_gated_delta_fwd.
     Returns a dict: q, k, v (dense, in their dtype), g, beta (fp32) and, when h0
     is given, h0 (fp32)."""
-    p, (batch, L, n, hk, hv, dk, dv) = _delta(q, k, v, g, beta, h0, offsets)
-    dev = q.device
-    _dev(dout, "dout", q.dtype, (batch, L, hv, dv), dev)
-    if dstate is not None:
-        _dev(dstate, "dstate", torch.float32, (n, hv, dk, dv), dev)
-    make = lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=dev)
+    p, index, (batch, L, n, hk, hv, dk, dv) = _delta(q, k, v, g, beta, h0, offsets)
+    po = _arg(dout, "dout", q.dtype, (batch, L, hv, dv), index)
+    ps = _arg(dstate, "dstate", torch.float32, (n, hv, dk, dv), index)
+    make = lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=q.device)
     d = dict(q=make(q.dtype, batch, L, hk, dk), k=make(q.dtype, batch, L, hk, dk), v=make(q.dtype, batch, L, hv, dv),
              g=make(torch.float32, batch, L, hv), beta=make(torch.float32, batch, L, hv))
     if h0 is not None:
         d["h0"] = make(torch.float32, n, hv, dk, dv)
     grads = VmDeltaGrad(*(d[x].data_ptr() if x in d else None for x in ("q", "k", "v", "g", "beta", "h0")))
-    with torch.cuda.device(dev):
-        st = load_library().vm_gated_delta_bwd(ctypes.byref(p), _ptr(dout), _ptr(dstate), ctypes.byref(grads),
-                                               float(dk ** -0.5 if scale is None else scale), batch, L, n, hk, hv, dk,
-                                               dv, _dtype_code(q), int(bool(reverse)), _stream(dev))
-    _check(st, "vm_gated_delta_bwd")
+    _launch("vm_gated_delta_bwd", index, p, po, ps, grads, dk ** -0.5 if scale is None else scale, batch, L, n, hk, hv,
+            dk, dv, _dtype_code(q), int(bool(reverse)))
     return d
 
 
@@ -701,24 +712,18 @@ def vm_gated_delta_step(q, k, v, g, beta, state, scale=None, slots=None, out=Non
             raise ValueError(f"{name} must be a [batch, heads, dim] tensor")
     batch, hk, dk = q.shape
     hv, dv = v.shape[1:]
-    dev = q.device
-    _dev(q, "q", None, None, None)
-    _dev(k, "k", q.dtype, (batch, hk, dk), dev)
-    _dev(v, "v", q.dtype, (batch, hv, dv), dev)
-    _dev(g, "g", torch.float32, (batch, hv), dev)
-    _dev(beta, "beta", torch.float32, (batch, hv), dev)
+    index, dtype = q.get_device(), q.dtype
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be a [n_slots, hv, dk, dv] tensor")
-    _dev(state, "state", torch.float32, (state.shape[0], hv, dk, dv), dev)
-    if slots is not None:
-        _dev(slots, "slots", torch.int32, (batch,), dev)
-    out = torch.empty((batch, hv, dv), dtype=q.dtype, device=dev) if out is None else \
-        _dev(out, "out", q.dtype, (batch, hv, dv), dev)
-    with torch.cuda.device(dev):
-        st = load_library().vm_gated_delta_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
-                                                _ptr(slots), _ptr(out), float(dk ** -0.5 if scale is None else scale),
-                                                batch, state.shape[0], hk, hv, dk, dv, _dtype_code(q), _stream(dev))
-    _check(st, "vm_gated_delta_step")
+    n = state.shape[0]
+    if out is None:
+        out = torch.empty((batch, hv, dv), dtype=dtype, device=q.device)
+    _launch("vm_gated_delta_step", index, _arg(q, "q", dtype, (batch, hk, dk), index),
+            _arg(k, "k", dtype, (batch, hk, dk), index), _arg(v, "v", dtype, (batch, hv, dv), index),
+            _arg(g, "g", torch.float32, (batch, hv), index), _arg(beta, "beta", torch.float32, (batch, hv), index),
+            _arg(state, "state", torch.float32, (n, hv, dk, dv), index),
+            _arg(slots, "slots", torch.int32, (batch,), index), _arg(out, "out", dtype, (batch, hv, dv), index),
+            dk ** -0.5 if scale is None else scale, batch, n, hk, hv, dk, dv, _dtype_code(q))
     return out
 
 
@@ -728,27 +733,23 @@ def _head_norm(q, k, wq, wk, cos, sin, positions):
             raise ValueError(f"{name} must be a [batch, seqlen, heads, dim] tensor")
     batch, L, hq, dim = q.shape
     hk = k.shape[2] if k is not None else 0
-    dev = q.device
-    sq = _tokens(q, "q", q.dtype, (batch, L, hq, dim), dev)
-    sk = _tokens(k, "k", q.dtype, (batch, L, hk, dim), dev) if k is not None else 0
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w is not None:
-            _dev(w, name, torch.float32, (dim,), dev)
+    index, dtype = q.get_device(), q.dtype
+    pq, sq = _tokens(q, "q", dtype, (batch, L, hq, dim), index)
+    pk, sk = _tokens(k, "k", dtype, (batch, L, hk, dim), index) if k is not None else (None, 0)
     table = rot = 0
+    pc = ps = pp = None
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
     if cos is not None:
         if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
             raise ValueError("cos must be a [table, rot / 2] tensor")
-        table, rot = cos.shape[0], 2 * cos.shape[1]
-        _dev(cos, "cos", torch.float32, cos.shape, dev)
-        _dev(sin, "sin", torch.float32, cos.shape, dev)
-        if positions is not None:
-            _dev(positions, "positions", torch.int32, (batch, L), dev)
-    ptr = lambda t: t.data_ptr() if t is not None else None
-    s = VmHeadNorm(q.data_ptr(), ptr(k), ptr(wq), ptr(wk), ptr(cos), ptr(sin),
-                   ptr(positions) if cos is not None else None, sq, sk, table, rot)
-    return s, (batch, L, hq, hk, dim)
+        shape = cos.shape
+        table, rot = shape[0], 2 * shape[1]
+        pc, ps = _arg(cos, "cos", torch.float32, shape, index), _arg(sin, "sin", torch.float32, shape, index)
+        pp = _arg(positions, "positions", torch.int32, (batch, L), index)
+    s = VmHeadNorm(pq, pk, _arg(wq, "wq", torch.float32, (dim,), index), _arg(wk, "wk", torch.float32, (dim,), index),
+                   pc, ps, pp, sq, sk, table, rot)
+    return s, index, (batch, L, hq, hk, dim)
 
 
 def _norm_options(l2, interleaved):
@@ -765,17 +766,16 @@ def vm_head_norm_rope(q, k=None, wq=None, wk=None, cos=None, sin=None, positions
     [batch, L], None = 0 .. L - 1, outside the table = padding (zero output).
     l2=True divides by sqrt(sum x^2 + eps) instead of sqrt(mean x^2 + eps);
     interleaved=True pairs (2i, 2i + 1) instead of (i, i + rot / 2)."""
-    p, (batch, L, hq, hk, dim) = _head_norm(q, k, wq, wk, cos, sin, positions)
-    dev = q.device
-    q_out = torch.empty((batch, L, hq, dim), dtype=q.dtype, device=dev) if q_out is None else \
-        _dev(q_out, "q_out", q.dtype, (batch, L, hq, dim), dev)
-    if k is not None:
-        k_out = torch.empty((batch, L, hk, dim), dtype=q.dtype, device=dev) if k_out is None else \
-            _dev(k_out, "k_out", q.dtype, (batch, L, hk, dim), dev)
-    with torch.cuda.device(dev):
-        st = load_library().vm_head_norm_rope(ctypes.byref(p), _ptr(q_out), _ptr(k_out), batch, L, hq, hk, dim,
-                                              float(eps), _norm_options(l2, interleaved), _dtype_code(q), _stream(dev))
-    _check(st, "vm_head_norm_rope")
+    p, index, (batch, L, hq, hk, dim) = _head_norm(q, k, wq, wk, cos, sin, positions)
+    if q_out is None:
+        q_out = torch.empty((batch, L, hq, dim), dtype=q.dtype, device=q.device)
+    if k is None:
+        k_out = None
+    elif k_out is None:
+        k_out = torch.empty((batch, L, hk, dim), dtype=q.dtype, device=q.device)
+    _launch("vm_head_norm_rope", index, p, _arg(q_out, "q_out", q.dtype, (batch, L, hq, dim), index),
+            _arg(k_out, "k_out", q.dtype, (batch, L, hk, dim), index), batch, L, hq, hk, dim, eps,
+            _norm_options(l2, interleaved), _dtype_code(q))
     return q_out, k_out
 
 
@@ -784,48 +784,67 @@ def vm_head_norm_rope_bwd(dq_out, dk_out, q, k=None, wq=None, wk=None, cos=None,
     """Gradients of sum(dq_out * q_out) + sum(dk_out * k_out) of
     vm_head_norm_rope: (dq, dk, dwq, dwk); dq, dk dense in their dtype, dwq and
     dwk fp32 (None without the gain)."""
-    p, (batch, L, hq, hk, dim) = _head_norm(q, k, wq, wk, cos, sin, positions)
-    dev = q.device
-    _dev(dq_out, "dq_out", q.dtype, (batch, L, hq, dim), dev)
+    p, index, (batch, L, hq, hk, dim) = _head_norm(q, k, wq, wk, cos, sin, positions)
     if (dk_out is None) != (k is None):
         raise ValueError("dk_out comes with k")
-    if k is not None:
-        _dev(dk_out, "dk_out", q.dtype, (batch, L, hk, dim), dev)
-    dq = torch.empty((batch, L, hq, dim), dtype=q.dtype, device=dev)
-    dk = torch.empty((batch, L, hk, dim), dtype=q.dtype, device=dev) if k is not None else None
-    dwq = torch.empty((dim,), dtype=torch.float32, device=dev) if wq is not None else None
-    dwk = torch.empty((dim,), dtype=torch.float32, device=dev) if wk is not None and k is not None else None
-    with torch.cuda.device(dev):
-        st = load_library().vm_head_norm_rope_bwd(ctypes.byref(p), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk),
-                                                  _ptr(dwq), _ptr(dwk), batch, L, hq, hk, dim, float(eps),
-                                                  _norm_options(l2, interleaved), _dtype_code(q), _stream(dev))
-    _check(st, "vm_head_norm_rope_bwd")
+    pq = _arg(dq_out, "dq_out", q.dtype, (batch, L, hq, dim), index)
+    pk = _arg(dk_out, "dk_out", q.dtype, (batch, L, hk, dim), index)
+    make = lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=q.device)
+    dq = make(q.dtype, batch, L, hq, dim)
+    dk = make(q.dtype, batch, L, hk, dim) if k is not None else None
+    dwq = make(torch.float32, dim) if wq is not None else None
+    dwk = make(torch.float32, dim) if wk is not None and k is not None else None
+    ptr = lambda t: t.data_ptr() if t is not None else None
+    _launch("vm_head_norm_rope_bwd", index, p, pq, pk, ptr(dq), ptr(dk), ptr(dwq), ptr(dwk), batch, L, hq, hk, dim, eps,
+            _norm_options(l2, interleaved), _dtype_code(q))
     return dq, dk, dwq, dwk
 
 
 def vm_clip_grad_norm(grads, max_norm, out=None):
     """Scale the gradients to at most the Euclidean norm max_norm over all of
     them; returns the norm before (fp32 tensor of no dimensions, on the GPU).
-    grads: a list of fp32 and bf16 tensors on one GPU, scaled in place, or into
-    the tensors of the list `out` (the same shapes and dtypes)."""
+    grads: a list of contiguous fp32 and bf16 tensors on one GPU, scaled in
+    place, or into the tensors of the list `out` (of the same dtypes and as many
+    elements)."""
     grads = list(grads)
     if not grads:
         raise ValueError("grads must hold at least one tensor")
-    dev = grads[0].device
     outs = grads if out is None else list(out)
     if len(outs) != len(grads):
         raise ValueError("out must hold one tensor for each gradient")
-    arr = (VmGradTensor * len(grads))()
-    for i, (x, y) in enumerate(zip(grads, outs)):
-        _dev(x, f"grads[{i}]", None, None, dev)
-        if y is not x:
-            _dev(y, f"out[{i}]", x.dtype, x.shape, dev)
-        arr[i] = VmGradTensor(x.data_ptr(), y.data_ptr(), x.numel(), _dtype_code(x))
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        st = load_library().vm_clip_grad_norm(arr, len(grads), float(max_norm), _ptr(norm), _stream(dev))
-    _check(st, "vm_clip_grad_norm")
+    # a model has hundreds of gradients: every test is one pass of a C function
+    # over the list, and only where one fails is the tensor looked for
+    T = torch.Tensor
+    try:
+        index = T.get_device(grads[0])
+        sizes, types = list(map(T.numel, grads)), [x.dtype for x in grads]
+        codes = [_GRAD_CODES[x] for x in types]
+        good = index >= 0 and set(map(T.get_device, grads)) == {index} and all(map(T.is_contiguous, grads))
+        ins = list(map(T.data_ptr, grads))
+        if outs is grads:
+            to = ins
+        else:
+            good = good and set(map(T.get_device, outs)) == {index} and all(map(T.is_contiguous, outs)) and \
+                list(map(T.numel, outs)) == sizes and [x.dtype for x in outs] == types
+            to = list(map(T.data_ptr, outs))
+    except (TypeError, KeyError):
+        good = False
+    if not good:
+        dev = getattr(grads[0], "device", None)
+        for i, (x, y) in enumerate(zip(grads, outs)):
+            _dev(x, f"grads[{i}]", None, None, dev)
+            _dtype_code(x)
+            _dev(y, f"out[{i}]", x.dtype, None, dev)
+            if x.numel() != y.numel():
+                raise ValueError(f"out[{i}] has {y.numel()} elements, expected {x.numel()}")
+    table = array.array("q", itertools.chain.from_iterable(zip(ins, to, sizes, codes)))
+    norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+    _launch("vm_clip_grad_norm", index, ctypes.cast(table.buffer_info()[0], ctypes.POINTER(VmGradTensor)), len(grads),
+            max_norm, norm.data_ptr())
     return norm
+
+
+_GRAD_CODES = {torch.float32: VM_F32, torch.bfloat16: VM_BF16}
 
 
 __all__ = ["vm_selective_scan_fwd", "vm_bidir_scan_fwd", "vm_bidir_scan_fwd_noalloc", "vm_atrous_gather", "vm_atrous_scatter",

@@ -106,20 +106,42 @@ vmk::DeltaArgs delta_args(const vm_delta *p, const DeltaSizes &z, float scale, i
   return a;
 }
 
+// Temporary memory of one call as one allocation: the parts are laid out first
+// (each pool allocation and free costs the host some 10 us).
+class Parts {
+ public:
+  template <typename P>
+  void add(P **to, int64_t bytes) {
+    to_[n_] = reinterpret_cast<void **>(to);
+    at_[n_++] = total_;
+    total_ += (bytes + 255) & ~int64_t{255};
+  }
+  int get(Scratch &ws) {
+    int st = VM_OK;
+    char *base = static_cast<char *>(ws.bytes(total_, &st));
+    if (st == VM_OK)
+      for (int i = 0; i < n_; ++i) *to_[i] = base + at_[i];
+    return st;
+  }
+
+ private:
+  void **to_[12];
+  int64_t at_[12], total_ = 0;
+  int n_ = 0;
+};
+
 // The chunks' triangular inverses, masked products and decays.
-int chunk_scratch(vmk::DeltaArgs &a, bool bf16, bool backward, Scratch &ws) {
-  int st = VM_OK;
+void chunk_parts(vmk::DeltaArgs &a, bool bf16, bool backward, Parts &parts) {
   const int64_t per = a.slots * a.hv, c = vmk::kDeltaChunk, tri = per * vmk::kTriTerm * 2;
   const int terms_p = vmk::delta_terms_p(bf16);
-  a.T = static_cast<uint16_t *>(ws.bytes(tri * vmk::kTermsT, &st));
-  (backward ? a.PT : a.P) = static_cast<uint16_t *>(ws.bytes(tri * terms_p, &st));
-  a.eg = ws.get(per * c, &st);
-  a.ew = ws.get(per * c, &st);
+  parts.add(&a.T, tri * vmk::kTermsT);
+  parts.add(backward ? &a.PT : &a.P, tri * terms_p);
+  parts.add(&a.eg, per * c * 4);
+  parts.add(&a.ew, per * c * 4);
   if (backward) {
-    a.TT = static_cast<uint16_t *>(ws.bytes(tri * vmk::kTermsT, &st));
-    a.gam = static_cast<double *>(ws.bytes(per * c * 8, &st));
+    parts.add(&a.TT, tri * vmk::kTermsT);
+    parts.add(&a.gam, per * c * 8);
   }
-  return st;
 }
 
 int check_norm(const vm_head_norm *p, int64_t batch, int64_t seqlen, int64_t hq, int64_t hk, int64_t dim, float eps,
@@ -188,7 +210,9 @@ int vm_gated_delta_fwd(const vm_delta *p, void *out, float *state, float scale, 
   vmk::DeltaArgs a = delta_args(p, z, scale, batch, seqlen, n, hk, hv, dk, dv, reverse);
   a.out = out;
   a.state = state;
-  st = chunk_scratch(a, bf16, false, ws);
+  Parts parts;
+  chunk_parts(a, bf16, false, parts);
+  st = parts.get(ws);
   if (st != VM_OK) return st;
   st = hip_status(vmk::launch_delta_prep(a, bf16, false, s));
   if (st != VM_OK) return st;
@@ -226,13 +250,15 @@ int vm_gated_delta_bwd(const vm_delta *p, const void *dout, const float *dstate,
   a.dg = grad->dg;
   a.dbeta = grad->dbeta;
   a.dh0 = grad->dh0;
-  st = chunk_scratch(a, bf16, true, ws);
+  Parts parts;
+  chunk_parts(a, bf16, true, parts);
   const int64_t per = a.slots * hv;
   a.dvp = static_cast<int>((dv + 15) / 16 * 16);
-  a.S = ws.get(per * dk * a.dvp, &st);
-  a.dS = ws.get(per * dk * a.dvp, &st);
-  a.V = ws.get(per * vmk::kDeltaChunk * a.dvp, &st);
-  a.dR = ws.get(per * vmk::kDeltaChunk * a.dvp, &st);
+  parts.add(&a.S, per * dk * a.dvp * 4);
+  parts.add(&a.dS, per * dk * a.dvp * 4);
+  parts.add(&a.V, per * vmk::kDeltaChunk * a.dvp * 4);
+  parts.add(&a.dR, per * vmk::kDeltaChunk * a.dvp * 4);
+  st = parts.get(ws);
   if (st != VM_OK) return st;
   st = hip_status(vmk::launch_delta_prep(a, bf16, true, s));
   if (st == VM_OK) st = hip_status(vmk::launch_delta_scan(a, bf16, true, s));

@@ -37,8 +37,8 @@ template <> __device__ __forceinline__ f32x4 load4<bf16_t>(const bf16_t *p) {
 }
 __device__ __forceinline__ void store4(float *p, f32x4 v) { *reinterpret_cast<f32x4 *>(p) = v; }
 __device__ __forceinline__ void store4(bf16_t *p, f32x4 v) {
-  *reinterpret_cast<u16x4 *>(p) =
-      u16x4{from_f32<bf16_t>(v[0]), from_f32<bf16_t>(v[1]), from_f32<bf16_t>(v[2]), from_f32<bf16_t>(v[3])};
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<bf16x4 *>(p) = __builtin_convertvector(v, bf16x4);   // (to nearest even)
 }
 
 // Where a lane's two pieces of 4 values lie in the head, and which angles turn
@@ -158,25 +158,31 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs A) {
       live = p >= 0 && p < A.table;
       if (live) {
         const int64_t row = p * (A.rot >> 1);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (pl.angle[e] >= 0) {
-            co[e] = A.cos[row + pl.angle[e]];
-            si[e] = A.sin[row + pl.angle[e]];
+        if (VEC) {                         // (rot is a multiple of 8, the tables 16-byte aligned)
+          if (pl.angle[0] >= 0) {
+            co = load4(A.cos + row + pl.angle[0]);
+            si = load4(A.sin + row + pl.angle[0]);
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (pl.angle[e] >= 0) {
+              co[e] = A.cos[row + pl.angle[e]];
+              si[e] = A.sin[row + pl.angle[e]];
+            }
+        }
       }
     }
     for (int h = first; h < heads; h += A.splits) {
-      const int m = h >= A.heads[0];
-      const int hh = m ? h - A.heads[0] : h;
-      const T *x = static_cast<const T *>(A.x[m]) + t * A.xs[m] + static_cast<int64_t>(hh) * A.dim;
+      const int m = h >= A.heads[0], hh = m ? h - A.heads[0] : h;
       T *y = static_cast<T *>(A.y[m]) + (t * A.heads[m] + hh) * A.dim;
       if (!live) {
         store_head<VEC>(y, pl, inter_piece, f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0});
         continue;
       }
-      f32x4 a, b;
-      load_head<VEC>(x, pl, inter_piece, a, b);
+      f32x4 a, b, p, q;
+      load_head<VEC>(static_cast<const T *>(A.x[m]) + t * A.xs[m] + static_cast<int64_t>(hh) * A.dim, pl, inter_piece, a, b);
+      if (BACK) load_head<VEC>(static_cast<const T *>(A.dy[m]) + (t * A.heads[m] + hh) * A.dim, pl, inter_piece, p, q);
       const float squares = group_sum<LPR>(dot4(a, a) + dot4(b, b));
       const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(squares, A.over, A.eps));
       const f32x4 na = a * r, nb = b * r;
@@ -185,8 +191,6 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs A) {
         const f32x4 ua = na * wa, ub = nb * wb;
         store_head<VEC>(y, pl, inter_piece, ua * co - ub * si, ub * co + ua * si);
       } else {
-        f32x4 p, q;
-        load_head<VEC>(static_cast<const T *>(A.dy[m]) + (t * A.heads[m] + hh) * A.dim, pl, inter_piece, p, q);
         const f32x4 da = p * co + q * si, db = q * co - p * si;
         if (m) {
           dw[1][0] += da * na;
@@ -275,10 +279,13 @@ hipError_t launch_dim(const NormArgs &a, int blocks, bool back, hipStream_t s) {
   }
 }
 
-// Groups that share one token: one where the tokens alone give the card enough
-// groups, else up to a group per head.
+// Groups that share one token: one where the tokens alone give the card 16
+// workgroups a compute unit, else up to a group per head.  (4097 tokens of 4
+// rows, 24 heads of 128 in bf16: 53 us; with 2, 4 or 8 workgroups 54 to 55, with
+// 32 55, and fp32 gradients 60 instead of 46.  Several heads in flight in a lane
+// were no faster: 54 to 72 us.)
 int head_splits(const NormArgs &a) {
-  const int64_t want = 256 * 8 * (kThreads / lanes_per_head(a.dim));
+  const int64_t want = 256 * 16 * (kThreads / lanes_per_head(a.dim));
   const int heads = a.heads[0] + a.heads[1];
   int64_t s = (want + a.tokens - 1) / a.tokens;
   return static_cast<int>(s < 1 ? 1 : s > heads ? heads : s);
@@ -299,7 +306,7 @@ hipError_t launch_norm(NormArgs a, bool bf16, bool back, hipStream_t s) {
   const int blocks = norm_blocks(a, bf16, back);
   // whole pieces of 4 values, 4 values aligned
   const int64_t piece = bf16 ? 8 : 16;
-  bool vec = a.dim % 8 == 0 && a.rot % 8 == 0;
+  bool vec = a.dim % 8 == 0 && a.rot % 8 == 0 && aligned(a.cos, 16) && aligned(a.sin, 16);
   for (int m = 0; m < 2; ++m)
     vec = vec && (a.heads[m] == 0 || (aligned(a.x[m], piece) && aligned(a.y[m], piece) && a.xs[m] % 4 == 0 &&
                                       (!back || aligned(a.dy[m], piece))));
