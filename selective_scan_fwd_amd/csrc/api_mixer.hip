@@ -134,12 +134,11 @@ class Parts {
 void chunk_parts(vmk::DeltaArgs &a, bool bf16, bool backward, Parts &parts) {
   const int64_t per = a.slots * a.hv, c = vmk::kDeltaChunk, tri = per * vmk::kTriTerm * 2;
   const int terms_p = vmk::delta_terms_p(bf16);
-  parts.add(&a.T, tri * vmk::kTermsT);
-  parts.add(backward ? &a.PT : &a.P, tri * terms_p);
+  parts.add(&a.T, tri * (vmk::kTermsT + (backward ? 0 : terms_p)));
   parts.add(&a.eg, per * c * 4);
   parts.add(&a.ew, per * c * 4);
   if (backward) {
-    parts.add(&a.TT, tri * vmk::kTermsT);
+    parts.add(&a.TT, tri * (vmk::kTermsT + terms_p));
     parts.add(&a.gam, per * c * 8);
   }
 }

@@ -155,7 +155,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A) {
       }
     }
     {
-      uint16_t *dst = (BACK ? A.PT : A.P) + at * kTermsP * kTriTerm;
+      uint16_t *dst = (BACK ? A.TT : A.T) + (at * (kTermsT + kTermsP) + kTermsT) * kTriTerm;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         if (BACK ? (wave >= 2 && ks == 0) : (wave < 2 && ks == 1)) continue;
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A) {
       for (int r = 0; r < 4; ++r) st[(16 * a + 4 * lg + r) * kPitchC + 16 * wave + li] = t[a][r];
     }
     if (BACK) {                            // the transpose from the registers
-      uint16_t *dst = A.TT + at * kTermsT * kTriTerm;
+      uint16_t *dst = A.TT + at * (kTermsT + kTermsP) * kTriTerm;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         if (wave >= 2 && ks == 0) continue;
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A) {
       }
     }
     __syncthreads();
-    uint16_t *dst = A.T + at * kTermsT * kTriTerm;
+    uint16_t *dst = A.T + at * (kTermsT + (BACK ? 0 : kTermsP)) * kTriTerm;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       if (wave < 2 && ks == 1) continue;

@@ -14,27 +14,35 @@
 namespace vmk {
 namespace {
 
-// A wave owns 16 columns of the state: every product of the chunk stays within
-// those columns, so a wave's chain of products passes from registers to
+// A pair of waves owns 16 columns of the state: every product of the chunk stays
+// within those columns, so the chain of products passes from registers to
 // registers (a result tile is, split into terms, the next product's right
-// operand) and waves share only the chunk's left operands in LDS.
+// operand) and workgroup-wide only the chunk's left operands are shared.  Wave
+// p of the pair holds half p of the state's rows and of the chunk's steps: it
+// forms half of the sum of K S over the state's rows, for all steps, and the
+// halves meet through LDS, as do the parts of the triangular products and the
+// corrected values.  The chain of a chunk is what bounds a long sequence; a wave
+// issues about one instruction in five cycles however idle the rest of its SIMD
+// is, so halving the instructions of the chain is worth three exchanges.
 //
 // Rows of the state are held so that K's rows are read in whole pieces: row
 // 4 lg + r of tile 2 ks + p is state row 32 ks + 8 lg + 4 p + r.
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kCols = 16 * kWaves;         // state columns of a workgroup
-
 __device__ __forceinline__ int state_row(int d, int lg, int r) { return 32 * (d / 2) + 8 * lg + 4 * (d & 1) + r; }
 
+// NP pairs of waves, 16 NP columns, to a workgroup.
+template <int NP>
+struct Shape {
+  static constexpr int kWaves = 2 * NP, kThreads = 64 * kWaves, kCols = 16 * NP;
+};
+
 // A chunk's operands in LDS: K and Q in terms, the triangles' blocks, decays.
-template <typename T, int DK, int TRI, bool WITH_Q>
+template <typename T, int DK, int TRI, bool WITH_Q, int NP>
 struct ChunkLds {
   static constexpr int kTerm = kC * DK;
   __attribute__((aligned(16))) uint16_t k[kInputTerms<T> * kTerm];
   __attribute__((aligned(16))) uint16_t q[WITH_Q ? kInputTerms<T> * kTerm : 8];
   __attribute__((aligned(16))) uint16_t tri[TRI * kTriTerm];
-  __attribute__((aligned(16))) uint16_t v[sizeof(T) == 2 ? kC * kCols : 8];   // (the workgroup's columns)
+  __attribute__((aligned(16))) uint16_t v[sizeof(T) == 2 ? kC * Shape<NP>::kCols : 8];   // (the workgroup's columns)
   __attribute__((aligned(16))) float eg[kC], ew[kC], beta[kC];
 };
 
@@ -44,18 +52,22 @@ struct ChunkLds {
 // `v` stands for v or dout: token rows of dv values, of which a workgroup takes
 // kCols columns.  Byte offsets from a chunk's lowest token are the same for all
 // whole chunks and kept in registers.
-template <typename T, int DK, int TRI, int TERMS1, bool WITH_Q, bool VEC, bool DIRECT>
+template <typename T, int DK, int TRI, bool WITH_Q, bool VEC, bool DIRECT, int NP>
 struct ChunkLoad {
-  typedef ChunkLds<T, DK, TRI, WITH_Q> Lds;
+  typedef ChunkLds<T, DK, TRI, WITH_Q, NP> Lds;
+  static constexpr int kWaves = Shape<NP>::kWaves, kThreads = Shape<NP>::kThreads, kCols = Shape<NP>::kCols;
   static constexpr int kPieces = DK / 8, kPer = kC * kPieces / kThreads;
+  // v to LDS: rows of an instruction with 16 or 4 bytes a lane, and instructions of a wave
+  static constexpr int kRows16 = 512 / kCols, kRows4 = 128 / kCols;
+  static constexpr int kV16 = kC / kRows16 / kWaves, kV4 = kC / kRows4 / kWaves;
   static constexpr int kTri = (TRI * kTriBlocks + kWaves - 1) / kWaves;
   Piece<T> k[DIRECT ? 1 : kPer], q[!DIRECT && WITH_Q ? kPer : 1];
   u32x4 tri[DIRECT ? 1 : kTri];
   float eg, ew, beta;
   T v[DIRECT ? 1 : 4][4];
-  uint32_t ok[kPer], oq[WITH_Q ? kPer : 1], ov[DIRECT ? 8 : 16], ob;
+  uint32_t ok[kPer], oq[WITH_Q ? kPer : 1], ov[DIRECT ? kV4 : 16], ob;
   int n = -1;                               // steps that the offsets are for
-  int wave, lane, li, lg, col0, kh, h;
+  int wave, lane, li, lg, col0, kh, h;      // (wave 2 i + p: pair i, half p)
   bool v16;                                 // DIRECT: v in pieces of 16 bytes, else of 4
   const T *vbase;
   int64_t vstride;
@@ -87,64 +99,41 @@ struct ChunkLoad {
     ob = lane < n ? w.at(A, lane, A.hv * 4) : kNowhere;
     if constexpr (DIRECT) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // 16 bytes: 8 rows of 8 pieces an instruction, 2 of them; 4 bytes: 2 rows of 32
-        const int row = v16 ? (i * kWaves + wave) * 8 + lane / 8 : (i * kWaves + wave) * 2 + lane / 32;
-        const int c = col0 + (v16 ? 8 * (lane % 8) : 2 * (lane % 32));
+      for (int i = 0; i < kV4; ++i) {
+        const int per16 = kCols / 8, per4 = kCols / 2;
+        const int row = v16 ? (i * kWaves + wave) * kRows16 + lane / per16 : (i * kWaves + wave) * kRows4 + lane / per4;
+        const int c = col0 + (v16 ? 8 * (lane % per16) : 2 * (lane % per4));
         ov[i] = row < n && c < A.dv ? w.at(A, row, vstride * sizeof(T)) + c * sizeof(T) : kNowhere;
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int row = 16 * (i / 4) + 4 * lg + i % 4, c = col0 + 16 * wave + li;
+        const int row = 16 * (i / 4) + 4 * lg + i % 4, c = col0 + 16 * (wave / 2) + li;
         ov[i] = row < n && c < A.dv ? w.at(A, row, vstride * sizeof(T)) + c * sizeof(T) : kNowhere;
       }
     }
   }
 
-  // m1 (TERMS1 of the TRI terms) and m2: the triangular operands.
-  __device__ __forceinline__ void load(const DeltaArgs &A, const Seq &s, int64_t c0, const uint16_t *m1,
-                                       const uint16_t *m2, Lds &l) {
+  // In three parts, so that the loads' issue spreads over the chunk before.
+  // tri: the triangular operands, TRI terms of each (slot, head).
+  __device__ __forceinline__ void load_v_k(const DeltaArgs &A, const Seq &s, int64_t c0, Lds &l) {
     const Window w = window(A, s, c0);
     if (w.n != n) plan(A, w);
     const int64_t at = (s.slot0 + c0 / kC) * A.hv + h;
     const Rsrc rk = buffer(static_cast<const T *>(A.k) + w.low * A.ks + static_cast<int64_t>(kh) * A.dk);
-    const Rsrc rq = buffer(static_cast<const T *>(A.q) + w.low * A.qs + static_cast<int64_t>(kh) * A.dk);
-    const Rsrc r1 = buffer(m1 + at * TERMS1 * kTriTerm), r2 = buffer(m2 + at * (TRI - TERMS1) * kTriTerm);
     const Rsrc reg = buffer(A.eg + at * kC), rew = buffer(A.ew + at * kC), rbeta = buffer(A.beta + w.low * A.hv + h);
     const Rsrc rv = buffer(vbase + w.low * vstride);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if constexpr (DIRECT) {
-        to_lds16(rk, l.k + (i * kWaves + wave) * 512, ok[i]);
-        if (WITH_Q) to_lds16(rq, l.q + (i * kWaves + wave) * 512, oq[i]);
-      } else {
-        const int c = 8 * (((i * kWaves + wave) * 64 + lane) % kPieces);
-        k[i] = load_piece<VEC>(rk, ok[i], c, A.dk, T());
-        if (WITH_Q) q[i] = load_piece<VEC>(rq, oq[i], c, A.dk, T());
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kTri; ++i) {
-      const int b = wave + i * kWaves, t1 = TERMS1 * kTriBlocks;
-      const uint32_t off = (b < t1 ? b : b - t1) * 1024 + lane * 16;
-      if constexpr (DIRECT) {
-        if (b < TRI * kTriBlocks) to_lds16(b < t1 ? r1 : r2, l.tri + b * 512, off);
-      } else {
-        tri[i] = bload16(b < t1 ? r1 : r2, b < TRI * kTriBlocks ? off : kNowhere);
-      }
-    }
     if constexpr (DIRECT) {
+      if (v16) {
+#pragma unroll
+        for (int i = 0; i < kV16; ++i) to_lds16(rv, l.v + (i * kWaves + wave) * 512, ov[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kV4; ++i) to_lds4(rv, l.v + (i * kWaves + wave) * 128, ov[i]);
+      }
       if (wave == 0) to_lds4(reg, l.eg, lane * 4);
       if (wave == 1) to_lds4(rew, l.ew, lane * 4);
       if (wave == 2) to_lds4(rbeta, l.beta, ob);
-      if (v16) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) to_lds16(rv, l.v + (i * kWaves + wave) * 512, ov[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) to_lds4(rv, l.v + (i * kWaves + wave) * 128, ov[i]);
-      }
     } else {
       eg = bload<float>(reg, lane * 4);
       ew = bload<float>(rew, lane * 4);
@@ -152,6 +141,43 @@ struct ChunkLoad {
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i / 4][i % 4] = bload<T>(rv, ov[i]);
     }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if constexpr (DIRECT)
+        to_lds16(rk, l.k + (i * kWaves + wave) * 512, ok[i]);
+      else
+        k[i] = load_piece<VEC>(rk, ok[i], 8 * (((i * kWaves + wave) * 64 + lane) % kPieces), A.dk, T());
+    }
+  }
+  __device__ __forceinline__ void load_q(const DeltaArgs &A, const Seq &s, int64_t c0, Lds &l) {
+    const Window w = window(A, s, c0);
+    const Rsrc rq = buffer(static_cast<const T *>(A.q) + w.low * A.qs + static_cast<int64_t>(kh) * A.dk);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if constexpr (DIRECT)
+        to_lds16(rq, l.q + (i * kWaves + wave) * 512, oq[i]);
+      else
+        q[i] = load_piece<VEC>(rq, oq[i], 8 * (((i * kWaves + wave) * 64 + lane) % kPieces), A.dk, T());
+    }
+  }
+  __device__ __forceinline__ void load_tri(const DeltaArgs &A, const Seq &s, int64_t c0, const uint16_t *m, Lds &l) {
+    const Rsrc r = buffer(m + ((s.slot0 + c0 / kC) * A.hv + h) * (TRI * kTriTerm), TRI * kTriTerm * 2);
+#pragma unroll
+    for (int i = 0; i < kTri; ++i) {
+      // (waves with no block left read zeros past the resource's end)
+      const int b = wave + i * kWaves;
+      if constexpr (DIRECT) {
+        if ((i + 1) * kWaves <= TRI * kTriBlocks || b < TRI * kTriBlocks)
+          to_lds16(r, l.tri + b * 512, (i * kWaves * 64 + threadIdx.x) * 16);
+      } else {
+        tri[i] = bload16(r, (i * kWaves * 64 + threadIdx.x) * 16);
+      }
+    }
+  }
+  __device__ __forceinline__ void load(const DeltaArgs &A, const Seq &s, int64_t c0, const uint16_t *m, Lds &l) {
+    load_v_k(A, s, c0, l);
+    if (WITH_Q) load_q(A, s, c0, l);
+    load_tri(A, s, c0, m, l);
   }
 
   __device__ __forceinline__ void store(Lds &l) const {
@@ -177,137 +203,209 @@ struct ChunkLoad {
     }
   }
 
-  // The wave's 64 x 16 of v, as D tiles.  From registers they are taken as soon
-  // as they have come, from LDS with the chunk.
-  __device__ __forceinline__ void values(const Lds &l, f32x4 (&x)[4]) const {
+  // Step tile rt of the pair's 16 columns of v, as a D tile.  From registers it is
+  // taken as soon as it has come, from LDS with the chunk.
+  __device__ __forceinline__ f32x4 values(const Lds &l, int rt) const {
+    f32x4 x;
+    if constexpr (DIRECT) {
+      const uint16_t *p = l.v + (16 * rt + 4 * lg + li / 4) * kCols + 16 * (wave / 2) + 4 * (li % 4);
+      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) s16x4 *)const_cast<uint16_t *>(p));
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) {
-      if constexpr (DIRECT) {
-        const uint16_t *p = l.v + (16 * rt + 4 * lg + li / 4) * kCols + 16 * wave + 4 * (li % 4);
-        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s16x4 *)const_cast<uint16_t *>(p));
+      for (int r = 0; r < 4; ++r) x[r] = to_f32(static_cast<bf16_t>(y[r]));
+    } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[rt][r] = to_f32(static_cast<bf16_t>(y[r]));
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[rt][r] = to_f32(v[rt][r]);
-      }
+      for (int r = 0; r < 4; ++r) x[r] = to_f32(rt == 0 ? v[0][r] : rt == 1 ? v[1][r] : rt == 2 ? v[2][r] : v[3][r]);
     }
+    return x;
   }
 };
 
-// Byte offsets of a wave's D tiles in token rows of `stride` values.
+// Byte offsets of a wave's two D tiles (its half's steps) in token rows of
+// `stride` values.
 struct RowOffsets {
-  uint32_t at[16];
+  uint32_t at[8];
   int n = -1;
-  __device__ __forceinline__ void plan(const DeltaArgs &A, const Window &w, int64_t stride_bytes, int esize, int lg,
-                                       int col) {
+  __device__ __forceinline__ void plan(const DeltaArgs &A, const Window &w, int64_t stride_bytes, int esize, int p,
+                                       int lg, int col) {
     if (w.n == n) return;
     n = w.n;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int row = 16 * (i / 4) + 4 * lg + i % 4;
+    for (int i = 0; i < 8; ++i) {
+      const int row = 32 * p + 16 * (i / 4) + 4 * lg + i % 4;
       at[i] = row < n && col < A.dv ? w.at(A, row, stride_bytes) + col * esize : kNowhere;
     }
   }
 };
-__device__ __forceinline__ void store_tokens(bf16_t *base, const RowOffsets &o, const f32x4 (&x)[4]) {
+__device__ __forceinline__ void store_tokens(bf16_t *base, const RowOffsets &o, const f32x4 (&x)[2]) {
   const Rsrc r = buffer(base);
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) {
+  for (int i = 0; i < 8; i += 2) {
     const uint32_t y = pack2(x[i / 4][i % 4], x[i / 4][i % 4 + 1]);
     bstore(r, o.at[i], static_cast<bf16_t>(y));
     bstore(r, o.at[i + 1], static_cast<bf16_t>(y >> 16));
   }
 }
-__device__ __forceinline__ void store_tokens(float *base, const RowOffsets &o, const f32x4 (&x)[4]) {
+__device__ __forceinline__ void store_tokens(float *base, const RowOffsets &o, const f32x4 (&x)[2]) {
   const Rsrc r = buffer(base);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) bstore(r, o.at[i], x[i / 4][i % 4]);
+  for (int i = 0; i < 8; ++i) bstore(r, o.at[i], x[i / 4][i % 4]);
 }
 
-// x[rt] += rows (tiles rt) of m times b, over all columns of m (whole rows).
-template <int DK, int NA, int NB>
-__device__ __forceinline__ void rows_times(const uint16_t *m, const Terms<NB> (&b)[DK / 32], int li, int lg,
-                                           f32x4 (&x)[4]) {
+// Left operands in registers.  Where K and Q are single terms they are read
+// ahead of the products that use them, before the exchange that those wait for.
+//
+// Rows of m, all four tiles, the columns of half p; x[rt] += their product with b.
+template <int DK, int NA>
+struct RowTiles {
+  bf16x8 a[DK / 64][4][NA];
+  __device__ __forceinline__ void read(const uint16_t *m, int p, int li, int lg) {
 #pragma unroll
-  for (int ks = 0; ks < DK / 32; ++ks) {
-    bf16x8 a[4][NA];
+    for (int ks = 0; ks < DK / 64; ++ks)
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt)
+      for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-      for (int t = 0; t < NA; ++t) a[rt][t] = read8(m + t * kC * DK + swizzled<DK>(16 * rt + li, 4 * ks + lg));
+        for (int t = 0; t < NA; ++t)
+          a[ks][rt][t] = read8(m + t * kC * DK + swizzled<DK>(16 * rt + li, 4 * (p * (DK / 64) + ks) + lg));
+  }
+  template <int NB>
+  __device__ __forceinline__ void times(const Terms<NB> (&b)[DK / 64], f32x4 (&x)[4]) const {
+#pragma unroll
+    for (int ks = 0; ks < DK / 64; ++ks)
+#pragma unroll
+      for (int t = 0; t < NA; ++t)
+#pragma unroll
+        for (int u = 0; u < NB; ++u) {
+          if (t + u >= (NA > NB ? NA : NB)) continue;
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) x[rt] = mfma32(a[ks][rt][t], b[ks].t[u], x[rt]);
+        }
+  }
+};
+
+// Columns (the state rows of half p) of m, one term, over its 64 rows.
+template <int DK>
+struct ColumnTiles {
+  bf16x8 a[2][DK / 32];
+  __device__ __forceinline__ void read(const uint16_t *m, int p, int li, int lg) {
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+      for (int d = 0; d < DK / 32; ++d)
+        a[kt][d] = join(read_columns<DK>(m, 32 * kt + 4 * lg, p * (DK / 64) + d / 2, d & 1, li),
+                        read_columns<DK>(m, 32 * kt + 16 + 4 * lg, p * (DK / 64) + d / 2, d & 1, li));
+  }
+  // The same while loads to LDS are under way: the compiler lets no transposing
+  // read of its own pass those without waiting for them.  (Rows 16 apart lie at
+  // the same place of their row, see swizzled().)
+  __device__ __forceinline__ void read_past_loads(const uint16_t *m, int p, int li, int lg) {
+#pragma unroll
+    for (int b = 0; b < DK / 64; ++b) {
+      const uint16_t *at = m + swizzled<DK>(4 * lg + li / 4, 4 * (p * (DK / 64) + b) + li % 4);
+      const uint32_t addr = static_cast<uint32_t>(
+          reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const uint16_t *)at));
+      s16x4 x[8];
+      constexpr int kStep = 16 * DK * 2;
+      asm volatile(
+          "ds_read_b64_tr_b16 %0, %8 offset:%9\n\t"
+          "ds_read_b64_tr_b16 %1, %8 offset:%10\n\t"
+          "ds_read_b64_tr_b16 %2, %8 offset:%11\n\t"
+          "ds_read_b64_tr_b16 %3, %8 offset:%12\n\t"
+          "ds_read_b64_tr_b16 %4, %8 offset:%13\n\t"
+          "ds_read_b64_tr_b16 %5, %8 offset:%14\n\t"
+          "ds_read_b64_tr_b16 %6, %8 offset:%15\n\t"
+          "ds_read_b64_tr_b16 %7, %8 offset:%16\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]), "=&v"(x[6]), "=&v"(x[7])
+          : "v"(addr), "n"(0), "n"(kStep), "n"(2 * kStep), "n"(3 * kStep), "n"(8), "n"(kStep + 8), "n"(2 * kStep + 8),
+            "n"(3 * kStep + 8)
+          : "memory");
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) a[kt][2 * b + half] = join(x[4 * half + 2 * kt], x[4 * half + 2 * kt + 1]);
+    }
+  }
+  // The first of NA terms of m; the others are read as they are used.
+  template <int NA, int NB>
+  __device__ __forceinline__ void times(const uint16_t *m, const Terms<NB> (&b)[2], int p, int li, int lg,
+                                        f32x4 (&x)[DK / 32]) const {
+#pragma unroll
+    for (int t = 0; t < NA; ++t) {
+      ColumnTiles c = *this;
+      if (t > 0) c.read(m + t * kC * DK, p, li, lg);
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int u = 0; u < NB; ++u) {
+          if (t + u >= (NA > NB ? NA : NB)) continue;
+#pragma unroll
+          for (int d = 0; d < DK / 32; ++d) x[d] = mfma32(c.a[kt][d], b[kt].t[u], x[d]);
+        }
+    }
+  }
+};
+
+// Two blocks of a triangular operand; x[i] += block i times y.
+template <int NA>
+struct Blocks {
+  bf16x8 a[2][NA];
+  __device__ __forceinline__ void read(const uint16_t *m, int b0, int b1, int lane) {
+#pragma unroll
+    for (int t = 0; t < NA; ++t) {
+      a[0][t] = read8(m + t * kTriTerm + (b0 * 64 + lane) * 8);
+      a[1][t] = read8(m + t * kTriTerm + (b1 * 64 + lane) * 8);
+    }
+  }
+  template <int NB>
+  __device__ __forceinline__ void times(const Terms<NB> &y, f32x4 (&x)[2]) const {
 #pragma unroll
     for (int t = 0; t < NA; ++t)
 #pragma unroll
       for (int u = 0; u < NB; ++u) {
         if (t + u >= (NA > NB ? NA : NB)) continue;
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) x[rt] = mfma32(a[rt][t], b[ks].t[u], x[rt]);
+        x[0] = mfma32(a[0][t], y.t[u], x[0]);
+        x[1] = mfma32(a[1][t], y.t[u], x[1]);
       }
-  }
-}
-
-// The columns (state rows) of one term of m as left operands, over the 64 rows of
-// m.  Where the next chunk is on its way to LDS they are read before it is sent
-// for: the compiler lets no transposing read pass a load to LDS without waiting
-// for that load.
-template <int DK>
-struct Columns {
-  bf16x8 a[2][DK / 16];
-  __device__ __forceinline__ void read(const uint16_t *m, int li, int lg) {
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-      for (int d = 0; d < DK / 16; ++d)
-        a[kt][d] = join(read_columns<DK>(m, 32 * kt + 4 * lg, d / 2, d & 1, li),
-                        read_columns<DK>(m, 32 * kt + 16 + 4 * lg, d / 2, d & 1, li));
   }
 };
 
-// x[d] += columns (state rows of tile d) of m times b.  first: m's first term.
-template <int DK, int NA, int NB>
-__device__ __forceinline__ void columns_times(const Columns<DK> &first, const uint16_t *m, const Terms<NB> (&b)[2], int li,
-                                              int lg, f32x4 (&x)[DK / 16]) {
-#pragma unroll
-  for (int t = 0; t < NA; ++t) {
-    Columns<DK> c = first;
-    if (t > 0) c.read(m + t * kC * DK, li, lg);
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-      for (int u = 0; u < NB; ++u) {
-        if (t + u >= (NA > NB ? NA : NB)) continue;
-#pragma unroll
-        for (int d = 0; d < DK / 16; ++d) x[d] = mfma32(c.a[kt][d], b[kt].t[u], x[d]);
-      }
-  }
+// A wave's registers through LDS: [item][lane] of 16 bytes.
+__device__ __forceinline__ void put(char *x, int item, int lane, f32x4 v) {
+  *reinterpret_cast<f32x4 *>(x + item * 1024 + lane * 16) = v;
 }
-
-// x[rt] += row tiles of a triangular operand (TR: of its transpose) times b.
-template <int NA, int NB, bool TR>
-__device__ __forceinline__ void triangle_times(const uint16_t *m, const Terms<NB> (&b)[2], int lane, f32x4 (&x)[4]) {
-  constexpr int kMost = NA > NB ? NA : NB;
+__device__ __forceinline__ f32x4 take(const char *x, int item, int lane) {
+  return *reinterpret_cast<const f32x4 *>(x + item * 1024 + lane * 16);
+}
+template <int N>
+__device__ __forceinline__ void put(char *x, int item, int lane, const Terms<N> &t) {
 #pragma unroll
-  for (int t = 0; t < NA; ++t)
+  for (int i = 0; i < N; ++i) *reinterpret_cast<bf16x8 *>(x + (item + i) * 1024 + lane * 16) = t.t[i];
+}
+template <int N>
+__device__ __forceinline__ Terms<N> take_terms(const char *x, int item, int lane) {
+  Terms<N> t;
 #pragma unroll
-    for (int u = 0; u < NB; ++u) {
-      if (t + u >= kMost) continue;
+  for (int i = 0; i < N; ++i) t.t[i] = *reinterpret_cast<const bf16x8 *>(x + (item + i) * 1024 + lane * 16);
+  return t;
+}
+// The two tiles of half p, and of the other half (with constant indices: arrays
+// indexed by p would live in memory).
+__device__ __forceinline__ void halves(const f32x4 (&x)[4], int p, f32x4 (&mine)[2], f32x4 (&other)[2]) {
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          if (TR ? (rt >= 2 && ks == 0) : (rt < 2 && ks == 1)) continue;
-          const int block = TR ? tri_block_t(rt, ks) : tri_block(rt, ks);
-          x[rt] = mfma32(read8(m + t * kTriTerm + (block * 64 + lane) * 8), b[ks].t[u], x[rt]);
-        }
+    for (int e = 0; e < 4; ++e) {
+      mine[i][e] = p == 0 ? x[i][e] : x[2 + i][e];
+      other[i][e] = p == 0 ? x[2 + i][e] : x[i][e];
     }
 }
-
-template <int N>
-__device__ __forceinline__ void split_rows(const f32x4 (&x)[4], Terms<N> (&t)[2]) {
-  t[0] = split<N>(x[0], x[1]);
-  t[1] = split<N>(x[2], x[3]);
+// All waves' writes to LDS are visible after it; loads and stores of global
+// memory (and loads to LDS) stay under way.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 // Workgroups of one sequence and head (which share K, Q and the triangles) are
@@ -325,254 +423,390 @@ __device__ __forceinline__ Place place(const DeltaArgs &A, int colblocks) {
   return p;
 }
 
-// D tiles [DK][16] at [dk][cols] memory, and [64][16] at [64][dvp]; columns past
-// them go nowhere.
+// Half p's D tiles of a state at [dk][cols] memory, and of [64][16] at [64][dvp];
+// columns past them go nowhere, rows past dk lie past the resource's end.
 template <int DK>
-__device__ __forceinline__ void store_state(const DeltaArgs &A, float *base, int cols, const f32x4 (&S)[DK / 16], int lg, int col) {
-  // (rows past dk lie past the resource's end)
+__device__ __forceinline__ void store_state(const DeltaArgs &A, float *base, int cols, const f32x4 (&S)[DK / 32], int p,
+                                            int lg, int col) {
   const Rsrc r = buffer(base, A.dk * cols * 4);
-  const uint32_t first = col < cols ? (8 * lg * cols + col) * 4 : kNowhere;
+  const uint32_t first = col < cols ? ((p * (DK / 2) + 8 * lg) * cols + col) * 4 : kNowhere;
 #pragma unroll
-  for (int d = 0; d < DK / 16; ++d)
+  for (int d = 0; d < DK / 32; ++d)
 #pragma unroll
     for (int e = 0; e < 4; ++e) bstore(r, first + state_row(d, 0, e) * cols * 4, S[d][e]);
 }
 template <int DK>
-__device__ __forceinline__ void load_state(const DeltaArgs &A, const float *base, f32x4 (&S)[DK / 16], int lg, int col) {
-  const Rsrc r = buffer(base);
+__device__ __forceinline__ void load_state(const DeltaArgs &A, const float *base, f32x4 (&S)[DK / 32], int p, int lg,
+                                           int col) {
+  const Rsrc r = buffer(base, base != nullptr ? A.dk * A.dv * 4 : 0);
+  const uint32_t first = col < A.dv ? ((p * (DK / 2) + 8 * lg) * A.dv + col) * 4 : kNowhere;
 #pragma unroll
-  for (int d = 0; d < DK / 16; ++d)
+  for (int d = 0; d < DK / 32; ++d)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int row = state_row(d, lg, e);
-      S[d][e] = bload<float>(r, base != nullptr && row < A.dk && col < A.dv ? (row * A.dv + col) * 4 : kNowhere);
-    }
+    for (int e = 0; e < 4; ++e) S[d][e] = bload<float>(r, first + state_row(d, 0, e) * A.dv * 4);
 }
-__device__ __forceinline__ void store_rows(const DeltaArgs &A, float *base, const f32x4 (&x)[4], int lg, int col) {
+__device__ __forceinline__ void store_rows(const DeltaArgs &A, float *base, const f32x4 (&x)[2], int p, int lg, int col) {
   const Rsrc r = buffer(base);
-  const uint32_t first = col < A.dvp ? (4 * lg * A.dvp + col) * 4 : kNowhere;
+  const uint32_t first = col < A.dvp ? ((32 * p + 4 * lg) * A.dvp + col) * 4 : kNowhere;
 #pragma unroll
-  for (int rt = 0; rt < 4; ++rt)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) bstore(r, first + (16 * rt + e) * A.dvp * 4, x[rt][e]);
+    for (int e = 0; e < 4; ++e) bstore(r, first + (16 * i + e) * A.dvp * 4, x[i][e]);
 }
-template <typename T> constexpr bool kDirect = sizeof(T) == 2;
+
+// Whether whole pieces go to LDS directly.
+template <typename T, bool VEC> constexpr bool kDirect = VEC && sizeof(T) == 2;
+// Exchanged items (1 KB) of a pair: two regions, the first reused.
+constexpr int kItemsA = 10, kItemsB = 2, kItems = kItemsA + kItemsB;
 
 // Forward.  KEEP: S and V are stored for the backward pass, out and state not.
-template <typename T, int DK, bool KEEP, bool VEC>
-__global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs A, int colblocks) {
-  constexpr int kNi = kInputTerms<T>, kNs = 3;
+template <typename T, int DK, bool KEEP, bool VEC, int NP>
+__global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_kernel(DeltaArgs A, int colblocks) {
+  constexpr int kNi = kInputTerms<T>, kNs = 3, kHalf = DK / 64;
   constexpr int kTermsP = KEEP ? 0 : kNi == 1 ? 2 : 3;
   constexpr int kNo = kNi == 1 ? 2 : 3;               // terms of S and V on their way to out only
-  constexpr bool kDma = VEC && kDirect<T>;
-  typedef ChunkLoad<T, DK, kTermsT + kTermsP, kTermsT, !KEEP, VEC, kDma> Load;
+  constexpr bool kDma = kDirect<T, VEC>, kAhead = kNi == 1;
+  typedef ChunkLoad<T, DK, kTermsT + kTermsP, !KEEP, VEC, kDma, NP> Load;
   typedef typename Load::Lds Lds;
   constexpr int kBuffers = kDma ? 2 : 1;
-  __shared__ Lds lds[kBuffers];
+  __shared__ struct {
+    Lds lds[kBuffers];
+    __attribute__((aligned(16))) char xch[NP][kItems * 1024];
+  } sh;
   const Place pl = place(A, colblocks);
-  const int s = pl.s, h = pl.h, kh = h / (A.hv / A.hk);
+  const int s = pl.s, h = pl.h;
   const Seq q = sequence(A, s);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, li = lane % 16,
-            lg = lane / 16;
-  const int col = (pl.cb * kWaves + wave) * 16 + li;
-  const int64_t state_at = (static_cast<int64_t>(s) * A.hv + h) * A.dk * A.dv;
-  f32x4 S[DK / 16];
-  load_state<DK>(A, A.h0 != nullptr ? A.h0 + state_at : nullptr, S, lg, col);
   Load next;
   next.init(A, h, pl.cb, static_cast<const T *>(A.v), A.vs);
+  const int lane = next.lane, li = next.li, lg = next.lg, p = next.wave % 2;
+  char *xa = sh.xch[next.wave / 2], *xb = xa + kItemsA * 1024;
+  const int col = next.col0 + 16 * (next.wave / 2) + li;
+  const int64_t state_at = (static_cast<int64_t>(s) * A.hv + h) * A.dk * A.dv;
+  const f32x4 zero = {0, 0, 0, 0};
+  f32x4 S[DK / 32];
+  load_state<DK>(A, A.h0 != nullptr ? A.h0 + state_at : nullptr, S, p, lg, col);
   RowOffsets rows;
   if (q.len > 0) {
-    next.load(A, q, 0, A.T, A.P, lds[0]);
-    next.store(lds[0]);
+    next.load(A, q, 0, A.T, sh.lds[0]);
+    next.store(sh.lds[0]);
   }
   __syncthreads();
   int buf = 0;
   for (int64_t c0 = 0; c0 < q.len; c0 += kC) {
     const Window w = window(A, q, c0);
     const int64_t at = (q.slot0 + c0 / kC) * A.hv + h;
-    const Lds &l = lds[buf];
-    f32x4 v[4];
-    next.values(l, v);
-    Columns<DK> kc;
-    if (kDma) kc.read(l.k, li, lg);
+    const Lds &l = sh.lds[buf];
+    Lds &ln = sh.lds[kBuffers == 2 ? buf ^ 1 : 0];
     const bool more = c0 + kC < q.len;
-    if (more) next.load(A, q, c0 + kC, A.T, A.P, lds[kBuffers == 2 ? buf ^ 1 : 0]);
-    Terms<kNs> st[DK / 32];
-#pragma unroll
-    for (int ks = 0; ks < DK / 32; ++ks) st[ks] = split<kNs>(S[2 * ks], S[2 * ks + 1]);
-    if (KEEP) store_state<DK>(A, A.S + at * A.dk * A.dvp, A.dvp, S, lg, col);
-    f32x4 x[4];
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) x[rt] = f32x4{0, 0, 0, 0};
-    rows_times<DK, kNi, kNs>(l.k, st, li, lg, x);
-    f32x4 o[4];
-    if (!KEEP) {
-      Terms<kNo> so[DK / 32];
-#pragma unroll
-      for (int ks = 0; ks < DK / 32; ++ks)
-#pragma unroll
-        for (int t = 0; t < kNo; ++t) so[ks].t[t] = st[ks].t[t];
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) o[rt] = f32x4{0, 0, 0, 0};
-      rows_times<DK, kNi, kNo>(l.q, so, li, lg, o);
+    const f32x4 v[2] = {next.values(l, 2 * p), next.values(l, 2 * p + 1)};
+    RowTiles<DK, kNi> kr, qr;
+    if (kAhead) {
+      kr.read(l.k, p, li, lg);
+      if (!KEEP) qr.read(l.q, p, li, lg);
+      __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) {
-      const f32x4 eg = load4(l.eg + 16 * rt + 4 * lg), b = load4(l.beta + 16 * rt + 4 * lg);
-      x[rt] = b * (v[rt] - eg * x[rt]);
-      if (!KEEP) o[rt] = o[rt] * eg * A.scale;
-    }
-    Terms<kNs> r3[2];
-    split_rows<kNs>(x, r3);
-    f32x4 V[4];
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) V[rt] = f32x4{0, 0, 0, 0};
-    triangle_times<kTermsT, kNs, false>(l.tri, r3, lane, V);
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) x[rt] = V[rt] * load4(l.ew + 16 * rt + 4 * lg);
-    split_rows<kNs>(x, r3);
+    const f32x4 eg[2] = {load4(l.eg + 32 * p + 4 * lg), load4(l.eg + 32 * p + 16 + 4 * lg)};
+    const f32x4 be[2] = {load4(l.beta + 32 * p + 4 * lg), load4(l.beta + 32 * p + 16 + 4 * lg)};
+    const f32x4 ew[2] = {load4(l.ew + 32 * p + 4 * lg), load4(l.ew + 32 * p + 16 + 4 * lg)};
     const float last = l.eg[kC - 1];
+    if (more) next.load_v_k(A, q, c0 + kC, ln);
+    if (KEEP) store_state<DK>(A, A.S + at * A.dk * A.dvp, A.dvp, S, p, lg, col);
+    // K S and Q S over this half's state rows
+    f32x4 xm[2], om[2];
+    Blocks<kTermsT> ta, tb;
+    {
+      f32x4 x[4] = {zero, zero, zero, zero}, other[2];
+      Terms<kNs> st[kHalf];
 #pragma unroll
-    for (int d = 0; d < DK / 16; ++d) S[d] *= last;
-    if (!kDma) kc.read(l.k, li, lg);
-    columns_times<DK, kNi, kNs>(kc, l.k, r3, li, lg, S);
-    if constexpr (!KEEP) {
-      Terms<kNo> vo[2];
-      split_rows<kNo>(V, vo);
-      triangle_times<kTermsP, kNo, false>(l.tri + kTermsT * kTriTerm, vo, lane, o);
+      for (int ks = 0; ks < kHalf; ++ks) st[ks] = split<kNs>(S[2 * ks], S[2 * ks + 1]);
+      if (!kAhead) kr.read(l.k, p, li, lg);
+      kr.times(st, x);
+      if (kAhead) {
+        ta.read(l.tri, tri_block(2 * p, p), tri_block(2 * p + 1, p), lane);
+        tb.read(l.tri, tri_block(2, 0), tri_block(3, 0), lane);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (!KEEP && more) next.load_q(A, q, c0 + kC, ln);
+      halves(x, p, xm, other);
+      put(xa, 2 * p, lane, other[0]);
+      put(xa, 2 * p + 1, lane, other[1]);
+      if (!KEEP) {
+        Terms<kNo> so[kHalf];
+#pragma unroll
+        for (int ks = 0; ks < kHalf; ++ks)
+#pragma unroll
+          for (int t = 0; t < kNo; ++t) so[ks].t[t] = st[ks].t[t];
+        f32x4 o4[4] = {zero, zero, zero, zero};
+        if (!kAhead) qr.read(l.q, p, li, lg);
+        qr.times(so, o4);
+        halves(o4, p, om, other);
+        put(xa, 4 + 2 * p, lane, other[0]);
+        put(xa, 5 + 2 * p, lane, other[1]);
+      }
     }
-    if (kBuffers == 1) __syncthreads();
+    lds_barrier();
+    // this half's steps: R, and V = T R (of the second half's the first half's part)
+    f32x4 r[2], o[2], V[2] = {zero, zero};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      r[i] = be[i] * (v[i] - eg[i] * (xm[i] + take(xa, 2 - 2 * p + i, lane)));
+      if (!KEEP) o[i] = (om[i] + take(xa, 6 - 2 * p + i, lane)) * (eg[i] * A.scale);
+    }
+    if (more) next.load_tri(A, q, c0 + kC, A.T, ln);
+    const Terms<kNs> rt = split<kNs>(r[0], r[1]);
+    if (!kAhead) {
+      ta.read(l.tri, tri_block(2 * p, p), tri_block(2 * p + 1, p), lane);
+      tb.read(l.tri, tri_block(2, 0), tri_block(3, 0), lane);
+    }
+    if (p == 0) {
+      f32x4 y[2] = {zero, zero};
+      tb.times(rt, y);
+      put(xb, 0, lane, y[0]);
+      put(xb, 1, lane, y[1]);
+    }
+    ta.times(rt, V);
+    constexpr int kTp = KEEP ? 1 : kTermsP;
+    Blocks<kTp> pa, pb;
+    if (!KEEP && kAhead) {
+      pa.read(l.tri + kTermsT * kTriTerm, tri_block(2 * p, p), tri_block(2 * p + 1, p), lane);
+      pb.read(l.tri + kTermsT * kTriTerm, tri_block(2, 0), tri_block(3, 0), lane);
+    }
+    lds_barrier();
+    if (p == 1) {
+      V[0] += take(xb, 0, lane);
+      V[1] += take(xb, 1, lane);
+    }
+    Terms<kNs> vw[2];
+    const Terms<kNs> mine = split<kNs>(V[0] * ew[0], V[1] * ew[1]);
+    put(xa, 3 * p, lane, mine);
+    Terms<kNo> vo;
+    if (!KEEP) {
+      vo = split<kNo>(V[0], V[1]);
+      if (p == 0) put(xa, 6, lane, vo);
+    }
+#pragma unroll
+    for (int d = 0; d < DK / 32; ++d) S[d] *= last;
+    ColumnTiles<DK> kc;
+    if (kDma)
+      kc.read_past_loads(l.k, p, li, lg);
+    else
+      kc.read(l.k, p, li, lg);
+    lds_barrier();
+    if (p == 0) {
+      vw[0] = mine;
+      vw[1] = take_terms<kNs>(xa, 3, lane);
+    } else {
+      vw[0] = take_terms<kNs>(xa, 0, lane);
+      vw[1] = mine;
+    }
+    kc.template times<kNi>(l.k, vw, p, li, lg, S);
+    if constexpr (!KEEP) {
+      if (!kAhead) {
+        pa.read(l.tri + kTermsT * kTriTerm, tri_block(2 * p, p), tri_block(2 * p + 1, p), lane);
+        pb.read(l.tri + kTermsT * kTriTerm, tri_block(2, 0), tri_block(3, 0), lane);
+      }
+      pa.times(vo, o);
+      if (p == 1) pb.times(take_terms<kNo>(xa, 6, lane), o);
+    }
+    if (kBuffers == 1) lds_barrier();
     buf = kBuffers == 2 ? buf ^ 1 : 0;
-    if (more) next.store(lds[buf]);
+    if (more) next.store(ln);
     // (stores come after the wait for the next chunk's loads, which would
     // otherwise wait for them too)
     if constexpr (!KEEP) {
-      rows.plan(A, w, static_cast<int64_t>(A.hv) * A.dv * sizeof(T), sizeof(T), lg, col);
+      rows.plan(A, w, static_cast<int64_t>(A.hv) * A.dv * sizeof(T), sizeof(T), p, lg, col);
       store_tokens(static_cast<T *>(A.out) + (w.low * A.hv + h) * A.dv, rows, o);
     } else {
-      store_rows(A, A.V + at * kC * A.dvp, V, lg, col);
+      store_rows(A, A.V + at * kC * A.dvp, V, p, lg, col);
     }
-    __syncthreads();
+    lds_barrier();
   }
-  if (!KEEP && A.state != nullptr) store_state<DK>(A, A.state + state_at, A.dv, S, lg, col);
+  if (!KEEP && A.state != nullptr) store_state<DK>(A, A.state + state_at, A.dv, S, p, lg, col);
 }
 
-template <typename T, int DK, bool VEC>
-__global__ __launch_bounds__(kThreads) void delta_scan_bwd_kernel(DeltaArgs A, int colblocks) {
-  constexpr int kNi = kInputTerms<T>, kNs = 3;
+template <typename T, int DK, bool VEC, int NP>
+__global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(DeltaArgs A, int colblocks) {
+  constexpr int kNi = kInputTerms<T>, kNs = 3, kHalf = DK / 64;
   constexpr int kTermsP = kNi == 1 ? 2 : 3;
-  constexpr bool kDma = VEC && kDirect<T>;
-  typedef ChunkLoad<T, DK, kTermsT + kTermsP, kTermsT, true, VEC, kDma> Load;
+  constexpr bool kDma = kDirect<T, VEC>, kAhead = kNi == 1;
+  typedef ChunkLoad<T, DK, kTermsT + kTermsP, true, VEC, kDma, NP> Load;
   typedef typename Load::Lds Lds;
   constexpr int kBuffers = kDma ? 2 : 1;
-  __shared__ Lds lds[kBuffers];
+  __shared__ struct {
+    Lds lds[kBuffers];
+    __attribute__((aligned(16))) char xch[NP][kItems * 1024];
+  } sh;
   const Place pl = place(A, colblocks);
-  const int s = pl.s, h = pl.h, kh = h / (A.hv / A.hk);
+  const int s = pl.s, h = pl.h;
   const Seq q = sequence(A, s);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, li = lane % 16,
-            lg = lane / 16;
-  const int col = (pl.cb * kWaves + wave) * 16 + li;
-  const int64_t state_at = (static_cast<int64_t>(s) * A.hv + h) * A.dk * A.dv;
   const int64_t row = static_cast<int64_t>(A.hv) * A.dv;      // token stride of dout and dv
-  f32x4 D[DK / 16];
-  load_state<DK>(A, A.dstate != nullptr ? A.dstate + state_at : nullptr, D, lg, col);
   Load next;
   next.init(A, h, pl.cb, static_cast<const T *>(A.dout), row);
+  const int lane = next.lane, li = next.li, lg = next.lg, p = next.wave % 2;
+  char *xa = sh.xch[next.wave / 2], *xb = xa + kItemsA * 1024;
+  const int col = next.col0 + 16 * (next.wave / 2) + li;
+  const int64_t state_at = (static_cast<int64_t>(s) * A.hv + h) * A.dk * A.dv;
+  const f32x4 zero = {0, 0, 0, 0};
+  f32x4 D[DK / 32];
+  load_state<DK>(A, A.dstate != nullptr ? A.dstate + state_at : nullptr, D, p, lg, col);
   RowOffsets rows;
   const int64_t first = (static_cast<int64_t>(q.len + kC - 1) / kC - 1) * kC;
   if (q.len > 0) {
-    next.load(A, q, first, A.TT, A.PT, lds[0]);
-    next.store(lds[0]);
+    next.load(A, q, first, A.TT, sh.lds[0]);
+    next.store(sh.lds[0]);
   }
   __syncthreads();
   int buf = 0;
   for (int64_t c0 = first; c0 >= 0; c0 -= kC) {
     const Window w = window(A, q, c0);
     const int64_t at = (q.slot0 + c0 / kC) * A.hv + h;
-    const Lds &l = lds[buf];
+    const Lds &l = sh.lds[buf];
+    Lds &ln = sh.lds[kBuffers == 2 ? buf ^ 1 : 0];
+    const bool more = c0 > 0;
+    // all of dout for P^T dout, this half's for Q^T dout
     f32x4 o[4];
-    next.values(l, o);
-    Columns<DK> kc, qc;
-    if (kDma) {
-      kc.read(l.k, li, lg);
-      qc.read(l.q, li, lg);
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) o[rt] = next.values(l, rt);
+    RowTiles<DK, kNi> kr;
+    const uint16_t *tp = l.tri + kTermsT * kTriTerm;
+    Blocks<kTermsP> pa, pb;                 // P^T: this half's rows by the second half's steps, and the first's
+    if (kAhead) {
+      kr.read(l.k, p, li, lg);
+      pa.read(tp, tri_block_t(2 * p, 1), tri_block_t(2 * p + 1, 1), lane);
+      pb.read(tp, tri_block_t(0, 0), tri_block_t(1, 0), lane);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (c0 > 0) next.load(A, q, c0 - kC, A.TT, A.PT, lds[kBuffers == 2 ? buf ^ 1 : 0]);
-    store_state<DK>(A, A.dS + at * A.dk * A.dvp, A.dvp, D, lg, col);
-    f32x4 V[4], R[4];
-    {
-      Terms<kNs> st[DK / 32];
-#pragma unroll
-      for (int ks = 0; ks < DK / 32; ++ks) st[ks] = split<kNs>(D[2 * ks], D[2 * ks + 1]);
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) V[rt] = f32x4{0, 0, 0, 0};
-      rows_times<DK, kNi, kNs>(l.k, st, li, lg, V);
-    }
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) V[rt] = V[rt] * load4(l.ew + 16 * rt + 4 * lg);
-    {
-      Terms<kNi> ot[2];
-      split_rows<kNi>(o, ot);
-      triangle_times<kTermsP, kNi, true>(l.tri + kTermsT * kTriTerm, ot, lane, V);
-    }
-    Terms<kNs> t3[2];
-    split_rows<kNs>(V, t3);
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) R[rt] = f32x4{0, 0, 0, 0};
-    triangle_times<kTermsT, kNs, true>(l.tri, t3, lane, R);
+    const f32x4 eg[2] = {load4(l.eg + 32 * p + 4 * lg), load4(l.eg + 32 * p + 16 + 4 * lg)};
+    const f32x4 be[2] = {load4(l.beta + 32 * p + 4 * lg), load4(l.beta + 32 * p + 16 + 4 * lg)};
+    const f32x4 ew[2] = {load4(l.ew + 32 * p + 4 * lg), load4(l.ew + 32 * p + 16 + 4 * lg)};
     const float last = l.eg[kC - 1];
-    f32x4 dv[4], x[4];
+    if (more) next.load_v_k(A, q, c0 - kC, ln);
+    store_state<DK>(A, A.dS + at * A.dk * A.dvp, A.dvp, D, p, lg, col);
+    f32x4 xm[2], of[2];
+    Blocks<kTermsT> ta, tb;
+    {
+      f32x4 x[4] = {zero, zero, zero, zero}, other[2];
+      Terms<kNs> st[kHalf];
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) {
-      const f32x4 eg = load4(l.eg + 16 * rt + 4 * lg);
-      dv[rt] = R[rt] * load4(l.beta + 16 * rt + 4 * lg);
-      x[rt] = f32x4{0, 0, 0, 0} - dv[rt] * eg;
-      o[rt] = o[rt] * eg * A.scale;
+      for (int ks = 0; ks < kHalf; ++ks) st[ks] = split<kNs>(D[2 * ks], D[2 * ks + 1]);
+      if (!kAhead) kr.read(l.k, p, li, lg);
+      kr.times(st, x);
+      if (kAhead) {
+        ta.read(l.tri, tri_block_t(2 * p, p), tri_block_t(2 * p + 1, p), lane);
+        tb.read(l.tri, tri_block_t(0, 1), tri_block_t(1, 1), lane);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (more) next.load_q(A, q, c0 - kC, ln);
+      halves(x, p, xm, other);
+      put(xa, 2 * p, lane, other[0]);
+      put(xa, 2 * p + 1, lane, other[1]);
+      halves(o, p, of, other);
     }
+    const Terms<kNs> od = split<kNs>(of[0] * (eg[0] * A.scale), of[1] * (eg[1] * A.scale));
+    put(xa, 4 + 3 * p, lane, od);
+    lds_barrier();
+    f32x4 V[2];
 #pragma unroll
-    for (int d = 0; d < DK / 16; ++d) D[d] *= last;
-    split_rows<kNs>(x, t3);
-    if (!kDma) kc.read(l.k, li, lg);
-    columns_times<DK, kNi, kNs>(kc, l.k, t3, li, lg, D);
-    split_rows<kNs>(o, t3);
-    if (!kDma) qc.read(l.q, li, lg);
-    columns_times<DK, kNi, kNs>(qc, l.q, t3, li, lg, D);
-    if (kBuffers == 1) __syncthreads();
+    for (int i = 0; i < 2; ++i) V[i] = (xm[i] + take(xa, 2 - 2 * p + i, lane)) * ew[i];
+    Terms<kNs> ow[2];
+    if (p == 0) {
+      ow[0] = od;
+      ow[1] = take_terms<kNs>(xa, 7, lane);
+    } else {
+      ow[0] = take_terms<kNs>(xa, 4, lane);
+      ow[1] = od;
+    }
+    if (more) next.load_tri(A, q, c0 - kC, A.TT, ln);
+    if (!kAhead) {
+      pa.read(tp, tri_block_t(2 * p, 1), tri_block_t(2 * p + 1, 1), lane);
+      pb.read(tp, tri_block_t(0, 0), tri_block_t(1, 0), lane);
+    }
+    pa.times(split<kNi>(o[2], o[3]), V);
+    if (p == 0) pb.times(split<kNi>(o[0], o[1]), V);
+    const Terms<kNs> vt = split<kNs>(V[0], V[1]);
+    f32x4 R[2] = {zero, zero};
+    if (!kAhead) {
+      ta.read(l.tri, tri_block_t(2 * p, p), tri_block_t(2 * p + 1, p), lane);
+      tb.read(l.tri, tri_block_t(0, 1), tri_block_t(1, 1), lane);
+    }
+    if (p == 1) {
+      f32x4 y[2] = {zero, zero};
+      tb.times(vt, y);
+      put(xb, 0, lane, y[0]);
+      put(xb, 1, lane, y[1]);
+    }
+    ta.times(vt, R);
+    ColumnTiles<DK> qc, kc;
+    if (kDma)
+      qc.read_past_loads(l.q, p, li, lg);
+    else
+      qc.read(l.q, p, li, lg);
+    lds_barrier();
+    if (p == 0) {
+      R[0] += take(xb, 0, lane);
+      R[1] += take(xb, 1, lane);
+    }
+    const f32x4 dv[2] = {R[0] * be[0], R[1] * be[1]};
+    Terms<kNs> xw[2];
+    const Terms<kNs> mine = split<kNs>(zero - dv[0] * eg[0], zero - dv[1] * eg[1]);
+    put(xa, 3 * p, lane, mine);
+#pragma unroll
+    for (int d = 0; d < DK / 32; ++d) D[d] *= last;
+    qc.template times<kNi>(l.q, ow, p, li, lg, D);
+    if (kDma)
+      kc.read_past_loads(l.k, p, li, lg);
+    else
+      kc.read(l.k, p, li, lg);
+    lds_barrier();
+    if (p == 0) {
+      xw[0] = mine;
+      xw[1] = take_terms<kNs>(xa, 3, lane);
+    } else {
+      xw[0] = take_terms<kNs>(xa, 0, lane);
+      xw[1] = mine;
+    }
+    kc.template times<kNi>(l.k, xw, p, li, lg, D);
+    if (kBuffers == 1) lds_barrier();
     buf = kBuffers == 2 ? buf ^ 1 : 0;
-    if (c0 > 0) next.store(lds[buf]);
-    store_rows(A, A.dR + at * kC * A.dvp, R, lg, col);
-    rows.plan(A, w, row * sizeof(T), sizeof(T), lg, col);
+    if (more) next.store(ln);
+    store_rows(A, A.dR + at * kC * A.dvp, R, p, lg, col);
+    rows.plan(A, w, row * sizeof(T), sizeof(T), p, lg, col);
     store_tokens(static_cast<T *>(A.dval) + (w.low * A.hv + h) * A.dv, rows, dv);
-    __syncthreads();
+    lds_barrier();
   }
-  if (A.dh0 != nullptr) store_state<DK>(A, A.dh0 + state_at, A.dv, D, lg, col);
+  if (A.dh0 != nullptr) store_state<DK>(A, A.dh0 + state_at, A.dv, D, p, lg, col);
 }
 
-int column_blocks(const DeltaArgs &a) { return (a.dv + 16 * kWaves - 1) / (16 * kWaves); }
+// Pairs of a workgroup: two where rows of 128 fill LDS (fp32 in terms, or two
+// buffers of bf16).
+template <int DK> constexpr int kPairs = DK == 128 ? 2 : 4;
 
 template <typename T, int DK, bool VEC>
 hipError_t launch_fwd(const DeltaArgs &a, bool keep, hipStream_t s) {
-  const int cb = column_blocks(a);
-  const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(a.nseq) * a.hv * cb));
+  constexpr int NP = kPairs<DK>;
+  const int cb = (a.dv + 16 * NP - 1) / (16 * NP);
+  const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(a.nseq) * a.hv * cb)), block(Shape<NP>::kThreads);
   if (keep)
-    hipLaunchKernelGGL((delta_scan_kernel<T, DK, true, VEC>), grid, dim3(kThreads), 0, s, a, cb);
+    hipLaunchKernelGGL((delta_scan_kernel<T, DK, true, VEC, NP>), grid, block, 0, s, a, cb);
   else
-    hipLaunchKernelGGL((delta_scan_kernel<T, DK, false, VEC>), grid, dim3(kThreads), 0, s, a, cb);
+    hipLaunchKernelGGL((delta_scan_kernel<T, DK, false, VEC, NP>), grid, block, 0, s, a, cb);
   return hipGetLastError();
 }
 template <typename T, int DK>
 hipError_t launch_fwd(const DeltaArgs &a, bool keep, hipStream_t s) {
   return delta_vec(a, sizeof(T)) && delta_vec_values(a, a.v, a.vs, sizeof(T), 4)
-             ? launch_fwd<T, DK, true>(a, keep, s) : launch_fwd<T, DK, false>(a, keep, s);
+             ? launch_fwd<T, DK, true>(a, keep, s)
+             : launch_fwd<T, DK, false>(a, keep, s);
 }
 template <typename T, int DK>
 hipError_t launch_bwd(const DeltaArgs &a, hipStream_t s) {
-  const int cb = column_blocks(a);
-  const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(a.nseq) * a.hv * cb));
+  constexpr int NP = kPairs<DK>;
+  const int cb = (a.dv + 16 * NP - 1) / (16 * NP);
+  const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(a.nseq) * a.hv * cb)), block(Shape<NP>::kThreads);
   if (delta_vec(a, sizeof(T)) && delta_vec_values(a, a.dout, static_cast<int64_t>(a.hv) * a.dv, sizeof(T), 4))
-    hipLaunchKernelGGL((delta_scan_bwd_kernel<T, DK, true>), grid, dim3(kThreads), 0, s, a, cb);
+    hipLaunchKernelGGL((delta_scan_bwd_kernel<T, DK, true, NP>), grid, block, 0, s, a, cb);
   else
-    hipLaunchKernelGGL((delta_scan_bwd_kernel<T, DK, false>), grid, dim3(kThreads), 0, s, a, cb);
+    hipLaunchKernelGGL((delta_scan_bwd_kernel<T, DK, false, NP>), grid, block, 0, s, a, cb);
   return hipGetLastError();
 }
 

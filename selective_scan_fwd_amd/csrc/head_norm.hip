@@ -173,6 +173,16 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs A) {
         }
       }
     }
+    // the next head is on its way while one is worked on (4097 tokens of 4 rows: 67 -> 63 us)
+    f32x4 next_a, next_b, next_p, next_q;
+    auto fetch = [&](int h) {
+      const int m = h >= A.heads[0], hh = m ? h - A.heads[0] : h;
+      load_head<VEC>(static_cast<const T *>(A.x[m]) + t * A.xs[m] + static_cast<int64_t>(hh) * A.dim, pl, inter_piece,
+                     next_a, next_b);
+      if (BACK)
+        load_head<VEC>(static_cast<const T *>(A.dy[m]) + (t * A.heads[m] + hh) * A.dim, pl, inter_piece, next_p, next_q);
+    };
+    if (live && first < heads) fetch(first);
     for (int h = first; h < heads; h += A.splits) {
       const int m = h >= A.heads[0], hh = m ? h - A.heads[0] : h;
       T *y = static_cast<T *>(A.y[m]) + (t * A.heads[m] + hh) * A.dim;
@@ -180,9 +190,8 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs A) {
         store_head<VEC>(y, pl, inter_piece, f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0});
         continue;
       }
-      f32x4 a, b, p, q;
-      load_head<VEC>(static_cast<const T *>(A.x[m]) + t * A.xs[m] + static_cast<int64_t>(hh) * A.dim, pl, inter_piece, a, b);
-      if (BACK) load_head<VEC>(static_cast<const T *>(A.dy[m]) + (t * A.heads[m] + hh) * A.dim, pl, inter_piece, p, q);
+      const f32x4 a = next_a, b = next_b, p = next_p, q = next_q;
+      if (h + A.splits < heads) fetch(h + A.splits);
       const float squares = group_sum<LPR>(dot4(a, a) + dot4(b, b));
       const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(squares, A.over, A.eps));
       const f32x4 na = a * r, nb = b * r;
@@ -281,9 +290,8 @@ hipError_t launch_dim(const NormArgs &a, int blocks, bool back, hipStream_t s) {
 
 // Groups that share one token: one where the tokens alone give the card 16
 // workgroups a compute unit, else up to a group per head.  (4097 tokens of 4
-// rows, 24 heads of 128 in bf16: 53 us; with 2, 4 or 8 workgroups 54 to 55, with
-// 32 55, and fp32 gradients 60 instead of 46.  Several heads in flight in a lane
-// were no faster: 54 to 72 us.)
+// rows, 24 heads of 128 in bf16, inputs not in the caches: 63 us, with 4
+// workgroups 71, with 64 75.)
 int head_splits(const NormArgs &a) {
   const int64_t want = 256 * 16 * (kThreads / lanes_per_head(a.dim));
   const int heads = a.heads[0] + a.heads[1];

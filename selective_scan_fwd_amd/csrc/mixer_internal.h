@@ -66,9 +66,10 @@ struct DeltaArgs {
   // stored as bf16 terms in the order in which a wave loads them as the left
   // operand of a matrix instruction: [term][block of 16 x 32][lane][8], the 6
   // blocks that are not zero.
-  uint16_t *T;             // (I + A)^-1, kTermsT terms
-  uint16_t *P;             // scaled masked products of queries and keys, terms_p
-  uint16_t *TT, *PT;       // their transposes (backward)
+  // T = (I + A)^-1 has kTermsT terms, the scaled masked products P of queries
+  // and keys terms_p.
+  uint16_t *T;             // forward: T, then P; backward: T
+  uint16_t *TT;            // backward: the transposes of T, then of P
   float *eg, *ew;          // [64]: exp(G), exp(G_C - G) of the running log decay G
   double *gam;             // [64]: G (backward)
   // forward
