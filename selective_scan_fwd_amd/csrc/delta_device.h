@@ -206,6 +206,15 @@ __device__ __forceinline__ void store_piece(uint16_t *m, int term, int row, int 
 }
 template <typename T> constexpr int kInputTerms = sizeof(T) == 2 ? 1 : 3;
 
+// A value that is the same for the whole wave, where the compiler cannot tell:
+// buffer resources made from it would be taken apart lane by lane.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(x));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(x >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 struct Seq {
   int64_t base;   // first token
   int64_t slot0;  // first chunk slot
@@ -213,7 +222,7 @@ struct Seq {
 };
 
 __device__ __forceinline__ int64_t packed_offset(const DeltaArgs &A, int s) {
-  const int64_t o = A.off[s];
+  const int64_t o = uniform(A.off[s]);
   return o < 0 ? 0 : o > A.L ? A.L : o;
 }
 __device__ __forceinline__ Seq sequence(const DeltaArgs &A, int s) {
@@ -228,11 +237,15 @@ __device__ __forceinline__ Seq sequence(const DeltaArgs &A, int s) {
     q.len = end > q.base ? static_cast<int>(end - q.base) : 0;
     q.slot0 = q.base / kC + s;
   }
+  q.base = uniform(q.base);
+  q.slot0 = uniform(q.slot0);
+  q.len = uniform(q.len);
   return q;
 }
 // The sequence of a chunk slot: the last one whose first slot is <= slot.
 __device__ __forceinline__ int sequence_of(const DeltaArgs &A, int64_t slot) {
-  if (A.off == nullptr) return static_cast<int>(slot / ((A.L + kC - 1) / kC));
+  if (A.off == nullptr)                  // (fewer than 2^23 slots)
+    return static_cast<int>(static_cast<uint32_t>(slot) / static_cast<uint32_t>((A.L + kC - 1) / kC));
   int lo = 0, hi = A.nseq - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;

@@ -36,12 +36,14 @@ struct SliceLds {
   __attribute__((aligned(16))) uint16_t s[3 * kState], d[3 * kState], v[3 * kRows], r[3 * kRows],
       o[kInputTerms<T> * kRows];
 };
-// The second phase's: K, Q and two of the masked products as left operands.
+// The second phase's: K and Q, and the masked products as left operands.
 template <typename T, int DK>
-struct ProductLds {
+struct KeyLds {
   static constexpr int kTerm = kC * DK;
-  __attribute__((aligned(16))) uint16_t k[kInputTerms<T> * kTerm], q[kInputTerms<T> * kTerm];
-  __attribute__((aligned(16))) uint16_t m[3 * kTriTerm], n[3 * kTriTerm];
+  __attribute__((aligned(16))) uint16_t m[kInputTerms<T> * kTerm];
+};
+struct MaskedLds {
+  __attribute__((aligned(16))) uint16_t m[4][3 * kTriTerm];   // M, its transpose, N, its transpose
 };
 
 __device__ __forceinline__ float dot4(f32x4 a, f32x4 b) {
@@ -136,15 +138,24 @@ template <typename T, int DK, bool VEC>
 __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
   constexpr int kNt = DK / 32, kNi = kInputTerms<T>;
   typedef SliceLds<T, DK> Slice;
-  typedef ProductLds<T, DK> Product;
-  constexpr int kBuffers = 2 * sizeof(Slice) <= 156 * 1024 ? 2 : 1;
-  constexpr size_t kBytes = kBuffers * sizeof(Slice) > sizeof(Product) ? kBuffers * sizeof(Slice) : sizeof(Product);
+  typedef KeyLds<T, DK> Key;
+  // The masked products take the slices' place.  K and Q have their own where
+  // there is room, and are loaded once; else (fp32 rows of 128) they are loaded
+  // for every head, one after the other into one place.
+  constexpr size_t kMost = 157 * 1024, kPhase1 = sizeof(Slice) > sizeof(MaskedLds) ? sizeof(Slice) : sizeof(MaskedLds);
+  constexpr bool kOwnKeys = kPhase1 + 2 * sizeof(Key) <= kMost;
+  constexpr int kBuffers = 2 * sizeof(Slice) + (kOwnKeys ? 2 * sizeof(Key) : 0) <= kMost ? 2 : 1;
+  constexpr size_t kShared1 = kBuffers * sizeof(Slice) > kPhase1 ? kBuffers * sizeof(Slice) : kPhase1;
+  constexpr size_t kShared2 = sizeof(MaskedLds) + sizeof(Key);
+  constexpr size_t kBytes = kOwnKeys ? kShared1 + 2 * sizeof(Key) : kShared1 > kShared2 ? kShared1 : kShared2;
   __shared__ __attribute__((aligned(16))) char raw[kBytes];
   __shared__ double sg[kC];
   __shared__ __attribute__((aligned(16))) float seg[kC], sw[kC], sbeta[kC], srv[kC];
-  __shared__ float swk[8], sdot[8], sgam[2][kC], sbet[2][kC];
+  __shared__ float swk[8], sdot[8], sgam[2][kC], sbet[2][kC], sgate[kC];
   Slice *slices = reinterpret_cast<Slice *>(raw);
-  Product &pr = *reinterpret_cast<Product *>(raw);
+  MaskedLds &pr = *reinterpret_cast<MaskedLds *>(raw);
+  Key *keys = reinterpret_cast<Key *>(raw + (kOwnKeys ? kShared1 : sizeof(MaskedLds)));
+  uint16_t *key_k = keys[0].m, *key_q = keys[kOwnKeys ? 1 : 0].m;
   const int64_t slot = blockIdx.x;
   const Seq q = sequence(A, sequence_of(A, slot));
   const int64_t c0 = (slot - q.slot0) * kC;
@@ -158,52 +169,88 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
   // masked products: of pt0 at most two tiles are not zero, c % 2 in p0
   const int pm = wave / 2, pta = wave % 2, pt0 = pm % 2 == 0 ? pta : 3 - pta, pt1 = 3 - pt0;
   const f32x4 zero = {0, 0, 0, 0};
+  // a thread's piece of S and dS, and of dR and v (first half) or V and dout
+  const int srow = threadIdx.x / kSlicePieces, piece = threadIdx.x % kSlicePieces, row = srow % kC;
+  static_assert(kC * kSlicePieces == 4 * 64, "the first half is waves 0 to 3");
+  const bool first = wave < 4;
+  const int64_t os = static_cast<int64_t>(A.hv) * A.dv;
+  const uint32_t at_v = row < n ? win.at(A, row, (first ? A.vs : os) * sizeof(T)) : kNowhere;
+  Piece<float> ls, ld, lx;
+  Piece<T> ly;
+  auto load = [&](int h, int v0) {
+    const int64_t at = slot * A.hv + h;
+    const int c = v0 + 8 * piece;
+    if (wave < DK / 16) {                  // (16 rows of a state to a wave)
+      const uint32_t o = c < A.dvp ? (srow * A.dvp + c) * 4 : kNowhere;
+      ls = load_piece<true>(buffer(A.S + at * A.dk * A.dvp, A.dk * A.dvp * 4), o, c, A.dvp, 0.0f);
+      ld = load_piece<true>(buffer(A.dS + at * A.dk * A.dvp, A.dk * A.dvp * 4), o, c, A.dvp, 0.0f);
+    }
+    lx = load_piece<true>(buffer((first ? A.dR : A.V) + at * kC * A.dvp), c < A.dvp ? (row * A.dvp + c) * 4 : kNowhere, c,
+                          A.dvp, 0.0f);
+    const T *t = first ? static_cast<const T *>(A.v) + win.low * A.vs : static_cast<const T *>(A.dout) + win.low * os;
+    ly = load_piece<VEC>(buffer(t + static_cast<int64_t>(h) * A.dv), c < A.dv ? at_v + c * sizeof(T) : kNowhere, c, A.dv, T());
+  };
+  double gate_g = 0;
+  float gate_eg = 0, gate_ew = 0, gate_b = 0, gate_in = 0;
+  auto load_gates = [&](int h) {           // (wave 7, which has least to do)
+    if (wave == 7) {
+      const int64_t at = (slot * A.hv + h) * kC + lane;
+      gate_g = A.gam[at];
+      gate_eg = A.eg[at];
+      gate_ew = A.ew[at];
+      if (lane < n) {
+        const int64_t i = token_of(A, q, c0, lane) * A.hv + h;
+        gate_b = A.beta[i];
+        gate_in = A.g[i];
+      }
+    }
+  };
+  constexpr int kPieces = DK / 8, kPer = kC * kPieces / kThreads;
+  auto load_keys = [&](const void *base, int64_t stride, uint16_t *dst) {
+    const Rsrc r = buffer(static_cast<const T *>(base) + win.low * stride + static_cast<int64_t>(kh) * A.dk);
+    Piece<T> x[kPer];
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) {
+      const int i = threadIdx.x + y * kThreads, row = i / kPieces, p = i % kPieces;
+      const uint32_t o = row < n && 8 * p < A.dk ? win.at(A, row, stride * sizeof(T)) + 8 * p * sizeof(T) : kNowhere;
+      x[y] = load_piece<VEC>(r, o, 8 * p, A.dk, T());
+    }
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) {
+      const int i = threadIdx.x + y * kThreads;
+      store_piece<DK>(dst, Key::kTerm, i / kPieces, i % kPieces, x[y]);
+    }
+  };
+  // everything that the first head needs is on its way at once
+  load_gates(kh * group);
+  load(kh * group, 0);
+  if (kOwnKeys) {
+    load_keys(A.k, A.ks, key_k);
+    load_keys(A.q, A.qs, key_q);
+  }
   f32x4 dq[kNt], dk[kNt];
 #pragma unroll
   for (int c = 0; c < kNt; ++c) dq[c] = dk[c] = zero;
   for (int e = 0; e < group; ++e) {
     const int h = kh * group + e;
-    const int64_t at = slot * A.hv + h;
     __syncthreads();
-    if (threadIdx.x < kC) {
-      const int i = threadIdx.x;
-      sg[i] = A.gam[at * kC + i];
-      seg[i] = A.eg[at * kC + i];
-      sw[i] = A.ew[at * kC + i];
-      sbeta[i] = i < n ? A.beta[token_of(A, q, c0, i) * A.hv + h] : 0.0f;
+    if (wave == 7) {
+      sg[lane] = gate_g;
+      seg[lane] = gate_eg;
+      sw[lane] = gate_ew;
+      sbeta[lane] = gate_b;
+      sgate[lane] = gate_in;
     }
+    const int lane0 = lane;
     f32x4 aq[kNt], ak[kNt], ax[kNt], p0[2], p1[4];
 #pragma unroll
     for (int c = 0; c < kNt; ++c) aq[c] = ak[c] = ax[c] = zero;
 #pragma unroll
     for (int c = 0; c < 4; ++c) p0[c / 2] = p1[c] = zero;
     float dot = 0, rv = 0;
-    const Rsrc gS = buffer(A.S + at * A.dk * A.dvp, A.dk * A.dvp * 4), gD = buffer(A.dS + at * A.dk * A.dvp, A.dk * A.dvp * 4);
-    const Rsrc gV = buffer(A.V + at * kC * A.dvp), gR = buffer(A.dR + at * kC * A.dvp);
-    const int64_t os = static_cast<int64_t>(A.hv) * A.dv;
-    const Rsrc gO = buffer(static_cast<const T *>(A.dout) + win.low * os + static_cast<int64_t>(h) * A.dv);
-    const Rsrc gv = buffer(static_cast<const T *>(A.v) + win.low * A.vs + static_cast<int64_t>(h) * A.dv);
-    // a thread's piece of S and dS, and of dR and v (first half) or V and dout
-    const int srow = threadIdx.x / kSlicePieces, piece = threadIdx.x % kSlicePieces, row = srow % kC;
-    static_assert(kC * kSlicePieces == 4 * 64, "the first half is waves 0 to 3");
-    const bool first = wave < 4;
-    Piece<float> ls, ld, lx;
-    Piece<T> ly;
-    auto load = [&](int v0) {
-      const int c = v0 + 8 * piece;
-      const uint32_t ok = c < A.dvp ? (srow * A.dvp + c) * 4 : kNowhere;
-      if (DK * kSlicePieces >= kThreads || srow < DK) {
-        ls = load_piece<true>(gS, ok, c, A.dvp, 0.0f);
-        ld = load_piece<true>(gD, ok, c, A.dvp, 0.0f);
-      }
-      const uint32_t rk = c < A.dvp ? (row * A.dvp + c) * 4 : kNowhere;
-      lx = load_piece<true>(first ? gR : gV, rk, c, A.dvp, 0.0f);
-      const uint32_t tk = row < n && c < A.dv ? win.at(A, row, (first ? A.vs : os) * sizeof(T)) + c * sizeof(T) : kNowhere;
-      ly = load_piece<VEC>(first ? gv : gO, tk, c, A.dv, T());
-    };
     auto store = [&](Slice &l) {
       f32x4 a, b, x, y;
-      if (DK * kSlicePieces >= kThreads || srow < DK) {
+      if (wave < DK / 16) {                  // (16 rows of a state to a wave)
         widen(ls, a, b);
         widen(ld, x, y);
         dot += dot4(a, x) + dot4(b, y);
@@ -218,14 +265,17 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
       else
         put_terms<kNi, Slice::kRows>(l.o, row, piece, x, y);
     };
-    load(0);
     store(slices[0]);
     __syncthreads();
     int buf = 0;
     for (int v0 = 0; v0 < A.dv; v0 += kSlice) {
       const Slice &l = slices[buf];
+      // (so that the addresses of this phase are not held through the second)
+      int lane1 = lane0;
+      asm volatile("" : "+v"(lane1));
+      const int li = lane1 % 16, lg = lane1 / 16;
       const bool more = v0 + kSlice < A.dv;
-      if (more) load(v0 + kSlice);
+      if (more) load(h, v0 + kSlice);
       {
         bf16x8 o[kNi], v[3], r[3];
         read_slice<kNi, Slice::kRows>(l.o, 16 * rt + li, lg, o);
@@ -257,21 +307,14 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
       if (more) store(slices[buf]);
       __syncthreads();
     }
-    // second phase: K and Q, the sums that the loading threads hold
+    // (lane indices of its own: the second phase's many LDS addresses are then
+    // formed there, instead of being held in registers through the first)
+    int lane2 = lane;
+    asm volatile("" : "+v"(lane2));
     {
-      const Rsrc rk = buffer(static_cast<const T *>(A.k) + win.low * A.ks + static_cast<int64_t>(kh) * A.dk);
-      const Rsrc rq = buffer(static_cast<const T *>(A.q) + win.low * A.qs + static_cast<int64_t>(kh) * A.dk);
-      constexpr int kPieces = DK / 8;
-#pragma unroll
-      for (int x = 0; x < kC * kPieces / kThreads; ++x) {
-        const int i = threadIdx.x + x * kThreads, r = i / kPieces, p = i % kPieces;
-        const bool in = r < n && 8 * p < A.dk;
-        const Piece<T> a = load_piece<VEC>(rk, in ? win.at(A, r, A.ks * sizeof(T)) + 8 * p * sizeof(T) : kNowhere, 8 * p, A.dk, T());
-        const Piece<T> b = load_piece<VEC>(rq, in ? win.at(A, r, A.qs * sizeof(T)) + 8 * p * sizeof(T) : kNowhere, 8 * p, A.dk, T());
-        store_piece<DK>(pr.k, Product::kTerm, r, p, a);
-        store_piece<DK>(pr.q, Product::kTerm, r, p, b);
-      }
-    }
+    const int lane = lane2, li = lane2 % 16, lg = lane2 / 16;
+    // second phase, with the sums that the loading threads hold
+    if (!kOwnKeys) load_keys(A.k, A.ks, key_k);
 #pragma unroll
     for (int o = 1; o < kSlicePieces; o *= 2) rv += __shfl_xor(rv, o);
     if (first && piece == 0) srv[row] = rv;
@@ -279,7 +322,7 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
     for (int o = 1; o < 64; o *= 2) dot += __shfl_xor(dot, o);
     if (lane == 0) sdot[wave] = dot;
     // the masked products' factors, and their way to LDS as left operands
-    auto put_masked = [&](uint16_t *dst, bool transposed, bool is_n) {
+    auto put_masked = [&](uint16_t *dst, const bool transposed, const bool is_n) {
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
         const int ct = side == 0 ? pt0 : pt1, a = 16 * ct + li;
@@ -306,8 +349,7 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
         }
       }
     };
-    if (pm == 0) put_masked(pr.m, false, false);
-    if (pm == 2) put_masked(pr.n, false, true);
+    put_masked(pr.m[pm], pm % 2 == 1, pm >= 2);
     __syncthreads();
     const f32x4 eg = load4(seg + 16 * rt + 4 * lg), w = load4(sw + 16 * rt + 4 * lg),
                 be = load4(sbeta + 16 * rt + 4 * lg);
@@ -318,61 +360,77 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
       aq[c] = aq[c] * eg * A.scale;
       y[c] = zero;
     }
+    // with K: M K, N K, (beta N)^T K
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       if (rt < 2 && ks == 1) continue;
       bf16x8 m[3], nn[3];
 #pragma unroll
       for (int t = 0; t < 3; ++t) {
-        m[t] = read8(pr.m + t * kTriTerm + (tri_block(rt, ks) * 64 + lane) * 8);
-        nn[t] = read8(pr.n + t * kTriTerm + (tri_block(rt, ks) * 64 + lane) * 8);
+        m[t] = read8(pr.m[0] + t * kTriTerm + (tri_block(rt, ks) * 64 + lane) * 8);
+        nn[t] = read8(pr.m[2] + t * kTriTerm + (tri_block(rt, ks) * 64 + lane) * 8);
       }
 #pragma unroll
       for (int c = 0; c < kNt; ++c) {
         bf16x8 b[kNi];
-        read_right<kNi, DK>(pr.k, ks, half * kNt + c, li, lg, b);
+        read_right<kNi, DK>(key_k, ks, half * kNt + c, li, lg, b);
         aq[c] = product(m, b, aq[c]);
         y[c] = product(nn, b, y[c]);
       }
     }
-    __syncthreads();
-    if (pm == 1) put_masked(pr.m, true, false);
-    if (pm == 3) put_masked(pr.n, true, true);
+    f32x4 kr[kNt];
 #pragma unroll
     for (int c = 0; c < kNt; ++c) {
-      const f32x4 kr = tile_values<kNi, DK>(pr.k, 16 * rt + 4 * lg, half * kNt + c, li);
-      const f32x4 qr = tile_values<kNi, DK>(pr.q, 16 * rt + 4 * lg, half * kNt + c, li);
+      kr[c] = tile_values<kNi, DK>(key_k, 16 * rt + 4 * lg, half * kNt + c, li);
       ak[c] *= w;
-      sum_w += ak[c] * kr;
+      sum_w += ak[c] * kr[c];
       y[c] -= ax[c] * eg;
-      sum_b += kr * y[c];
-      sum_g += qr * aq[c] + kr * y[c] * be;
+      sum_b += kr[c] * y[c];
+      sum_g += kr[c] * y[c] * be;
+      dk[c] += y[c] * be;
       dq[c] += aq[c];
     }
-    __syncthreads();
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       if (rt >= 2 && ks == 0) continue;
-      bf16x8 m[3], nn[3];
+      bf16x8 nn[3];
 #pragma unroll
-      for (int t = 0; t < 3; ++t) {
-        m[t] = read8(pr.m + t * kTriTerm + (tri_block_t(rt, ks) * 64 + lane) * 8);
-        nn[t] = read8(pr.n + t * kTriTerm + (tri_block_t(rt, ks) * 64 + lane) * 8);
-      }
+      for (int t = 0; t < 3; ++t) nn[t] = read8(pr.m[3] + t * kTriTerm + (tri_block_t(rt, ks) * 64 + lane) * 8);
 #pragma unroll
       for (int c = 0; c < kNt; ++c) {
         bf16x8 b[kNi];
-        read_right<kNi, DK>(pr.q, ks, half * kNt + c, li, lg, b);
-        ak[c] = product(m, b, ak[c]);
-        read_right<kNi, DK>(pr.k, ks, half * kNt + c, li, lg, b);
+        read_right<kNi, DK>(key_k, ks, half * kNt + c, li, lg, b);
         ak[c] = product(nn, b, ak[c]);
+      }
+    }
+    // with Q: M^T Q
+    if (!kOwnKeys) {
+      __syncthreads();
+      load_keys(A.q, A.qs, key_q);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      if (rt >= 2 && ks == 0) continue;
+      bf16x8 m[3];
+#pragma unroll
+      for (int t = 0; t < 3; ++t) m[t] = read8(pr.m[1] + t * kTriTerm + (tri_block_t(rt, ks) * 64 + lane) * 8);
+#pragma unroll
+      for (int c = 0; c < kNt; ++c) {
+        bf16x8 b[kNi];
+        read_right<kNi, DK>(key_q, ks, half * kNt + c, li, lg, b);
+        ak[c] = product(m, b, ak[c]);
       }
     }
 #pragma unroll
     for (int c = 0; c < kNt; ++c) {
-      const f32x4 kr = tile_values<kNi, DK>(pr.k, 16 * rt + 4 * lg, half * kNt + c, li);
-      sum_g -= kr * ak[c];
-      dk[c] += ak[c] + y[c] * be;
+      const f32x4 qr = tile_values<kNi, DK>(key_q, 16 * rt + 4 * lg, half * kNt + c, li);
+      sum_g += qr * aq[c] - kr[c] * ak[c];
+      dk[c] += ak[c];
+    }
+    if (e + 1 < group) {
+      load_gates(h + 1);
+      load(h + 1, 0);
     }
 #pragma unroll
     for (int o = 1; o < 16; o *= 2)
@@ -408,18 +466,19 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
       }
       if (lane < n) {
         const int64_t i = token_of(A, q, c0, lane) * A.hv + h;
-        A.dg[i] = A.g[i] < kMinLogDecay ? 0.0f : x;
+        A.dg[i] = sgate[lane] < kMinLogDecay ? 0.0f : x;
         A.dbeta[i] = srv[lane] + sbet[0][lane] + sbet[1][lane];
       }
     }
+    }
   }
-  const int64_t os = static_cast<int64_t>(A.hk) * A.dk;
-  const Rsrc oq = buffer(static_cast<T *>(A.dq) + win.low * os + static_cast<int64_t>(kh) * A.dk);
-  const Rsrc ok = buffer(static_cast<T *>(A.dkey) + win.low * os + static_cast<int64_t>(kh) * A.dk);
+  const int64_t ks = static_cast<int64_t>(A.hk) * A.dk;
+  const Rsrc oq = buffer(static_cast<T *>(A.dq) + win.low * ks + static_cast<int64_t>(kh) * A.dk);
+  const Rsrc ok = buffer(static_cast<T *>(A.dkey) + win.low * ks + static_cast<int64_t>(kh) * A.dk);
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int i = 16 * rt + 4 * lg + r;
-    const uint32_t at = i < n ? win.at(A, i, os * sizeof(T)) : kNowhere;
+    const uint32_t at = i < n ? win.at(A, i, ks * sizeof(T)) : kNowhere;
 #pragma unroll
     for (int c = 0; c < kNt; ++c) {
       const int col = 16 * (half * kNt + c) + li;

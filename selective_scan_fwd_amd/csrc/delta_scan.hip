@@ -489,6 +489,7 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_kernel(DeltaAr
   if (q.len > 0) {
     next.load(A, q, 0, A.T, sh.lds[0]);
     next.store(sh.lds[0]);
+    if (KEEP) store_state<DK>(A, A.S + (q.slot0 * A.hv + h) * A.dk * A.dvp, A.dvp, S, p, lg, col);
   }
   __syncthreads();
   int buf = 0;
@@ -510,7 +511,6 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_kernel(DeltaAr
     const f32x4 ew[2] = {load4(l.ew + 32 * p + 4 * lg), load4(l.ew + 32 * p + 16 + 4 * lg)};
     const float last = l.eg[kC - 1];
     if (more) next.load_v_k(A, q, c0 + kC, ln);
-    if (KEEP) store_state<DK>(A, A.S + at * A.dk * A.dvp, A.dvp, S, p, lg, col);
     // K S and Q S over this half's state rows
     f32x4 xm[2], om[2];
     Blocks<kTermsT> ta, tb;
@@ -618,6 +618,7 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_kernel(DeltaAr
       store_tokens(static_cast<T *>(A.out) + (w.low * A.hv + h) * A.dv, rows, o);
     } else {
       store_rows(A, A.V + at * kC * A.dvp, V, p, lg, col);
+      if (more) store_state<DK>(A, A.S + (at + A.hv) * A.dk * A.dvp, A.dvp, S, p, lg, col);
     }
     lds_barrier();
   }
@@ -654,6 +655,7 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(Del
   if (q.len > 0) {
     next.load(A, q, first, A.TT, sh.lds[0]);
     next.store(sh.lds[0]);
+    store_state<DK>(A, A.dS + ((q.slot0 + first / kC) * A.hv + h) * A.dk * A.dvp, A.dvp, D, p, lg, col);
   }
   __syncthreads();
   int buf = 0;
@@ -681,7 +683,6 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(Del
     const f32x4 ew[2] = {load4(l.ew + 32 * p + 4 * lg), load4(l.ew + 32 * p + 16 + 4 * lg)};
     const float last = l.eg[kC - 1];
     if (more) next.load_v_k(A, q, c0 - kC, ln);
-    store_state<DK>(A, A.dS + at * A.dk * A.dvp, A.dvp, D, p, lg, col);
     f32x4 xm[2], of[2];
     Blocks<kTermsT> ta, tb;
     {
@@ -770,6 +771,7 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(Del
     buf = kBuffers == 2 ? buf ^ 1 : 0;
     if (more) next.store(ln);
     store_rows(A, A.dR + at * kC * A.dvp, R, p, lg, col);
+    if (more) store_state<DK>(A, A.dS + (at - A.hv) * A.dk * A.dvp, A.dvp, D, p, lg, col);
     rows.plan(A, w, row * sizeof(T), sizeof(T), p, lg, col);
     store_tokens(static_cast<T *>(A.dval) + (w.low * A.hv + h) * A.dv, rows, dv);
     lds_barrier();
