@@ -204,6 +204,16 @@ __device__ __forceinline__ void store_piece(uint16_t *m, int term, int row, int 
 #pragma unroll
   for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x8 *>(m + i * term + swizzled<COLS>(row, piece)) = t.t[i];
 }
+// The piece's terms.
+__device__ __forceinline__ void piece_terms(const Piece<bf16_t> &p, bf16x8 (&t)[1]) {
+  t[0] = __builtin_bit_cast(bf16x8, p.x);
+}
+__device__ __forceinline__ void piece_terms(const Piece<float> &p, bf16x8 (&t)[3]) {
+  const Terms<3> x = split<3>(__builtin_bit_cast(f32x4, p.x[0]), __builtin_bit_cast(f32x4, p.x[1]));
+  t[0] = x.t[0];
+  t[1] = x.t[1];
+  t[2] = x.t[2];
+}
 template <typename T> constexpr int kInputTerms = sizeof(T) == 2 ? 1 : 3;
 
 // A value that is the same for the whole wave, where the compiler cannot tell:
@@ -278,32 +288,6 @@ __device__ __forceinline__ f32x4 load4(const float *p) { return *reinterpret_cas
 __device__ __forceinline__ f32x4 load4(const bf16_t *p) {
   const u16x4 r = *reinterpret_cast<const u16x4 *>(p);
   return f32x4{to_f32(r[0]), to_f32(r[1]), to_f32(r[2]), to_f32(r[3])};
-}
-
-// Rows 0 .. n-1 (tokens t0, t0 + dt, ...) of src[token][d] into dst[64][PITCH],
-// zero elsewhere up to column COLS.  vec: d, the stride and the pointer are
-// multiples of 4 values.
-template <int COLS, int PITCH, int THREADS, typename T>
-__device__ __forceinline__ void stage_rows(float *dst, const T *src, int64_t stride, int n, int d, bool vec) {
-  for (int i = threadIdx.x; i < kC * (COLS / 4); i += THREADS) {
-    const int row = i / (COLS / 4), c = (i % (COLS / 4)) * 4;
-    f32x4 v = {0, 0, 0, 0};
-    if (row < n && c < d) {
-      const T *p = src + row * stride + c;
-      if (vec) {
-        v = load4(p);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (c + e < d) v[e] = to_f32(p[e]);
-      }
-    }
-    *reinterpret_cast<f32x4 *>(dst + row * PITCH + c) = v;
-  }
-}
-
-__device__ __forceinline__ bool can_vec4(const void *p, int64_t stride, int d, int esize) {
-  return (d & 3) == 0 && (stride & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & (4 * esize - 1)) == 0;
 }
 
 }  // namespace vmk

@@ -21,45 +21,90 @@ constexpr int kThreads = 256;
 // Wave w computes columns 16w .. of the transposed products (rows j, columns i):
 // a lane then holds, for one i, the 8 values of j that a 16 x 32 block of P asks
 // of it as a left operand, so P goes to memory from the registers.
+//
+// Bound by the latency of its chain (loads, products, substitution, blocks), so
+// LDS is kept small for as many workgroups a compute unit as the registers
+// allow: forward, a wave's queries go straight to its registers, and T takes
+// the place of A.
 template <typename T, int DK, bool BACK, bool VEC>
-__global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A) {
+__global__ __launch_bounds__(kThreads, 4) void delta_prep_kernel(DeltaArgs A) {
   constexpr int kNi = kInputTerms<T>, kTerm = kC * DK, kPieces = DK / 8;
   constexpr int kTermsP = kNi == 1 ? 2 : 3;
-  constexpr int kRows = 2 * kNi * kTerm;                    // bf16 values of K and Q
-  constexpr int kUnion = kRows * 2 > kC * kPitchC * 4 ? kRows * 2 : kC * kPitchC * 4;
-  __shared__ __attribute__((aligned(16))) char raw[kUnion];  // K and Q, later T
-  __shared__ __attribute__((aligned(16))) float sa[kC * kPitchC];
-  __shared__ __attribute__((aligned(16))) float sd[4][16 * 20];  // inverses of the diagonal blocks
-  __shared__ double sg[kC];
-  __shared__ float sbeta[kC];
-  uint16_t *sk = reinterpret_cast<uint16_t *>(raw), *sq = sk + kNi * kTerm;
-  float *st = reinterpret_cast<float *>(raw);
+  __shared__ __attribute__((aligned(16))) uint16_t sk[kNi * kTerm];
+  __shared__ __attribute__((aligned(16))) uint16_t sq[BACK ? kNi * kTerm : 8];
+  __shared__ __attribute__((aligned(16))) float sa[kC * kPitchC];  // A, later T
+  // inverses of the diagonal blocks, once the products are done
+  float(*sd)[16 * 20] = reinterpret_cast<float(*)[16 * 20]>(sk);
+  static_assert(sizeof(sk) >= 4 * 16 * 20 * sizeof(float), "");
+  __shared__ double sg[4][kC];                                     // of up to four heads
+  __shared__ float sbeta[4][kC];
   const int64_t slot = blockIdx.x;
   const Seq q = sequence(A, sequence_of(A, slot));
   const int64_t c0 = (slot - q.slot0) * kC;
   if (c0 >= q.len || c0 < 0) return;
-  const int n = q.len - c0 < kC ? static_cast<int>(q.len - c0) : kC;
-  const int kh = blockIdx.y;
+  const Window w = window(A, q, c0);
+  const int n = w.n;
+  const int kh = blockIdx.y, group = A.hv / A.hk;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, li = lane % 16,
             lg = lane / 16;
+  // gates of heads wave, wave + 4, ..: running sums, and what the scans take of them
+  float gv = 0, bv = 0;
+  auto load_gates = [&](int e) {
+    gv = bv = 0;
+    if (e < group && lane < n) {
+      const int64_t i = token_of(A, q, c0, lane) * A.hv + kh * group + e;
+      gv = A.g[i];
+      bv = A.beta[i];
+    }
+  };
+  auto sum_gates = [&](int e) {
+    if (e >= group) return;
+    const int64_t at = (slot * A.hv + kh * group + e) * kC + lane;
+    double x = gv < kMinLogDecay ? kMinLogDecay : gv;
+    for (int o = 1; o < 64; o *= 2) {
+      const double y = __shfl_up(x, o);
+      if (lane >= o) x += y;
+    }
+    sg[wave][lane] = x;
+    sbeta[wave][lane] = bv;
+    A.eg[at] = hw_exp2(static_cast<float>(x) * kLog2e);
+    A.ew[at] = hw_exp2(static_cast<float>(__shfl(x, 63) - x) * kLog2e);
+    if (BACK) A.gam[at] = x;
+  };
+  bf16x8 fq[BACK ? 1 : DK / 32][kNi];      // forward: this wave's queries as right operands
   {
-    const Window w = window(A, q, c0);
-    const Rsrc k = buffer(static_cast<const T *>(A.k) + w.low * A.ks + static_cast<int64_t>(kh) * A.dk);
-    const Rsrc qq = buffer(static_cast<const T *>(A.q) + w.low * A.qs + static_cast<int64_t>(kh) * A.dk);
-    Piece<T> pk[kC * kPieces / kThreads], pq[kC * kPieces / kThreads];
+    load_gates(wave);
+    const Rsrc rk = buffer(static_cast<const T *>(A.k) + w.low * A.ks + static_cast<int64_t>(kh) * A.dk);
+    const Rsrc rq = buffer(static_cast<const T *>(A.q) + w.low * A.qs + static_cast<int64_t>(kh) * A.dk);
+    constexpr int kPer = kC * kPieces / kThreads;
+    Piece<T> pk[kPer], pq[BACK ? kPer : DK / 32];
 #pragma unroll
-    for (int x = 0; x < kC * kPieces / kThreads; ++x) {
+    for (int x = 0; x < kPer; ++x) {
       const int i = threadIdx.x + x * kThreads, row = i / kPieces, p = i % kPieces;
       const bool in = row < n && 8 * p < A.dk;
-      pk[x] = load_piece<VEC>(k, in ? w.at(A, row, A.ks * sizeof(T)) + 8 * p * sizeof(T) : kNowhere, 8 * p, A.dk, T());
-      pq[x] = load_piece<VEC>(qq, in ? w.at(A, row, A.qs * sizeof(T)) + 8 * p * sizeof(T) : kNowhere, 8 * p, A.dk, T());
+      pk[x] = load_piece<VEC>(rk, in ? w.at(A, row, A.ks * sizeof(T)) + 8 * p * sizeof(T) : kNowhere, 8 * p, A.dk, T());
+      if (BACK)
+        pq[x] = load_piece<VEC>(rq, in ? w.at(A, row, A.qs * sizeof(T)) + 8 * p * sizeof(T) : kNowhere, 8 * p, A.dk, T());
+    }
+    if (!BACK) {
+      const int row = 16 * wave + li;
+      const uint32_t at = w.at(A, row, A.qs * sizeof(T));
+#pragma unroll
+      for (int ks = 0; ks < DK / 32; ++ks) {
+        const int c = 32 * ks + 8 * lg;
+        pq[ks] = load_piece<VEC>(rq, row < n && c < A.dk ? at + c * sizeof(T) : kNowhere, c, A.dk, T());
+      }
     }
 #pragma unroll
-    for (int x = 0; x < kC * kPieces / kThreads; ++x) {
+    for (int x = 0; x < kPer; ++x) {
       const int i = threadIdx.x + x * kThreads, row = i / kPieces, p = i % kPieces;
       store_piece<DK>(sk, kTerm, row, p, pk[x]);
-      store_piece<DK>(sq, kTerm, row, p, pq[x]);
+      if (BACK) store_piece<DK>(sq, kTerm, row, p, pq[x]);
     }
+    if (!BACK)
+#pragma unroll
+      for (int ks = 0; ks < DK / 32; ++ks) piece_terms(pq[ks], fq[ks]);
+    sum_gates(wave);
   }
   __syncthreads();
   // kk[c]: k_j.k_i, rows j of tile c, columns i of tile wave (c <= wave);
@@ -71,25 +116,21 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A) {
 #pragma unroll
   for (int ks = 0; ks < DK / 32; ++ks) {
     const int piece = 4 * ks + lg;
-    bf16x8 bk[kNi], bq[kNi];
+    bf16x8 bk[kNi];
 #pragma unroll
-    for (int t = 0; t < kNi; ++t) {
-      bk[t] = read8(sk + t * kTerm + swizzled<DK>(16 * wave + li, piece));
-      bq[t] = read8(sq + t * kTerm + swizzled<DK>(16 * wave + li, piece));
-    }
+    for (int t = 0; t < kNi; ++t) bk[t] = read8(sk + t * kTerm + swizzled<DK>(16 * wave + li, piece));
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      bf16x8 ak[kNi];
-#pragma unroll
-      for (int t = 0; t < kNi; ++t) ak[t] = read8(sk + t * kTerm + swizzled<DK>(16 * c + li, piece));
       if (c <= wave) {
 #pragma unroll
-        for (int t = 0; t < kNi; ++t)
+        for (int t = 0; t < kNi; ++t) {
+          const bf16x8 ak = read8(sk + t * kTerm + swizzled<DK>(16 * c + li, piece));
 #pragma unroll
           for (int u = 0; t + u < kNi; ++u) {
-            kk[c] = mfma32(ak[t], bk[u], kk[c]);
-            if (!BACK) qk[c] = mfma32(ak[t], bq[u], qk[c]);
+            kk[c] = mfma32(ak, bk[u], kk[c]);
+            if (!BACK) qk[c] = mfma32(ak, fq[BACK ? 0 : ks][u], qk[c]);
           }
+        }
       }
       if (BACK && c >= wave) {
 #pragma unroll
@@ -101,36 +142,22 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A) {
       }
     }
   }
-  const int group = A.hv / A.hk;
   for (int e = 0; e < group; ++e) {
-    const int h = kh * group + e;
+    const int h = kh * group + e, s4 = e % 4;
     const int64_t at = slot * A.hv + h;
-    __syncthreads();                       // the previous use of sa, sg and of raw
-    if (wave == 0) {
-      double x = 0;
-      float b = 0;
-      if (lane < n) {
-        const int64_t i = token_of(A, q, c0, lane) * A.hv + h;
-        const float gv = A.g[i];
-        x = gv < kMinLogDecay ? kMinLogDecay : gv;
-        b = A.beta[i];
+    if (e > 0) {
+      __syncthreads();                     // the previous head's use of sa and sd
+      if (s4 == 0) {
+        load_gates(e + wave);
+        sum_gates(e + wave);
+        __syncthreads();
       }
-      for (int o = 1; o < 64; o *= 2) {
-        const double y = __shfl_up(x, o);
-        if (lane >= o) x += y;
-      }
-      sg[lane] = x;
-      sbeta[lane] = b;
-      A.eg[at * kC + lane] = hw_exp2(static_cast<float>(x) * kLog2e);
-      A.ew[at * kC + lane] = hw_exp2(static_cast<float>(__shfl(x, 63) - x) * kLog2e);
-      if (BACK) A.gam[at * kC + lane] = x;
     }
-    __syncthreads();
     f32x4 pt[4];
     {
       const int i = 16 * wave + li;        // (backward P: this is j)
-      const double gi = sg[i];
-      const float bi = sbeta[i];
+      const double gi = sg[s4][i];
+      const float bi = sbeta[s4][i];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         pt[c] = f32x4{0, 0, 0, 0};
@@ -139,7 +166,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int j = 16 * c + 4 * lg + r;
-            const double diff = gi - sg[j];
+            const double diff = gi - sg[s4][j];
             if (c <= wave) {
               const float d = hw_exp2(static_cast<float>(diff) * kLog2e);
               a[r] = j < i ? bi * d * kk[c][r] : 0.0f;
@@ -201,8 +228,6 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A) {
         const f32x4 zero = {0, 0, 0, 0};
         t[a] = zero - mfma16(load4(&sd[a][li * 20 + 4 * lg]), acc, zero);
       }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) st[(16 * a + 4 * lg + r) * kPitchC + 16 * wave + li] = t[a][r];
     }
     if (BACK) {                            // the transpose from the registers
       uint16_t *dst = A.TT + at * (kTermsT + kTermsP) * kTriTerm;
@@ -215,12 +240,18 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A) {
           *reinterpret_cast<bf16x8 *>(dst + y * kTriTerm + (tri_block_t(wave, ks) * 64 + lane) * 8) = x.t[y];
       }
     }
+    __syncthreads();                       // every wave has read A
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+      if (a >= wave)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sa[(16 * a + 4 * lg + r) * kPitchC + 16 * wave + li] = t[a][r];
     __syncthreads();
     uint16_t *dst = A.T + at * (kTermsT + (BACK ? 0 : kTermsP)) * kTriTerm;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       if (wave < 2 && ks == 1) continue;
-      const float *row = st + (16 * wave + li) * kPitchC + 32 * ks + 4 * lg;
+      const float *row = sa + (16 * wave + li) * kPitchC + 32 * ks + 4 * lg;
       const f32x4 zero = {0, 0, 0, 0};
       const f32x4 lo = load4(row), hi = 2 * ks + 1 <= wave ? load4(row + 16) : zero;
       const Terms<kTermsT> x = split<kTermsT>(lo, hi);
