@@ -433,6 +433,12 @@ int vm_ss2d_scan_bwd(const vm_scan_dir *dirs, const void *u, const void *z,
  * row; the stride from one batch row to the next is seqlen token strides.
  * The dtype selects the storage of q, k, v, out and of their gradients;
  * everything else is fp32.
+ * Calls that need temporary device memory take a workspace: device memory of
+ * at least the bytes that the call's _workspace function returns, 256-byte
+ * aligned, free for the call's work on its stream until that work is done.
+ * workspace = NULL: the memory comes from the library's stream-ordered pool.
+ * With a workspace a call makes no allocation and can be captured in a graph.
+ * A workspace that is too small or not aligned is VM_ERR_ALLOC.
  * ---------------------------------------------------------------------------
  */
 
@@ -483,12 +489,23 @@ typedef struct vm_delta {
  * dk and dv in [1, 128] (VM_ERR_UNSUPPORTED beyond).  hv % hk != 0 is
  * VM_ERR_SHAPE.  Sequences are computed in chunks of 64 steps, within which
  * a NaN or Inf of one token reaches the outputs of earlier tokens too.
- * Temporary memory per 64 tokens and value head: 34 KB.
  */
 int vm_gated_delta_fwd(const vm_delta *p, void *out, float *state, float scale,
                        int64_t batch, int64_t seqlen, int64_t n, int64_t hk,
                        int64_t hv, int64_t dk, int64_t dv, int dtype,
-                       int reverse, void *stream);
+                       int reverse, void *workspace, int64_t workspace_bytes,
+                       void *stream);
+
+/*
+ * Workspace of vm_gated_delta_fwd (backward = 0) or vm_gated_delta_bwd
+ * (backward = 1), with packed = 1 for sequences given by offsets.  About 31 KB
+ * per 64 tokens and value head, backward 50 KB + 8 dk dv + 512 dv bytes.
+ * Returns -VM_ERR_SHAPE or -VM_ERR_UNSUPPORTED for sizes that no call takes,
+ * as the other _workspace functions do.  Pure host function.
+ */
+int64_t vm_gated_delta_workspace(int64_t batch, int64_t seqlen, int64_t n,
+                                 int64_t hv, int64_t dk, int64_t dv, int dtype,
+                                 int packed, int backward);
 
 /* Gradients of the gated delta rule (dense; the caller's buffers). */
 typedef struct vm_delta_grad {
@@ -508,13 +525,12 @@ typedef struct vm_delta_grad {
  *   whose g is below -120 has dg as if it were -120 (0).
  * Outputs must not overlap any input or each other.  Sums over value heads
  * and over a chunk are formed in a fixed order (deterministic).
- * Temporary memory per 64 tokens and value head, in bytes: 34 K and
- * 8 dk dv + 512 dv.
  */
 int vm_gated_delta_bwd(const vm_delta *p, const void *dout, const float *dstate,
                        const vm_delta_grad *grad, float scale, int64_t batch,
                        int64_t seqlen, int64_t n, int64_t hk, int64_t hv,
                        int64_t dk, int64_t dv, int dtype, int reverse,
+                       void *workspace, int64_t workspace_bytes,
                        void *stream);
 
 /*
@@ -580,13 +596,17 @@ int vm_head_norm_rope(const vm_head_norm *p, void *q_out, void *k_out,
  * Its backward: from dq_out, dk_out (dense, dtype) the gradients dq, dk
  * (dense, dtype) and dwq, dwk [dim] fp32 (NULL = not computed; only with the
  * gain given, else VM_ERR_NULL).  Summed in a fixed order (deterministic).
- * Temporary memory: up to 1024 partial sums of dwq and dwk.
+ * A workspace is needed only for dwq or dwk.
  */
 int vm_head_norm_rope_bwd(const vm_head_norm *p, const void *dq_out,
                           const void *dk_out, void *dq, void *dk, float *dwq,
                           float *dwk, int64_t batch, int64_t seqlen, int64_t hq,
                           int64_t hk, int64_t dim, float eps, int norm_options,
-                          int dtype, void *stream);
+                          int dtype, void *workspace,
+                          int64_t workspace_bytes, void *stream);
+
+/* Workspace of vm_head_norm_rope_bwd.  Pure host function. */
+int64_t vm_head_norm_rope_workspace(int64_t dim);
 
 /* One gradient of vm_clip_grad_norm.  elems may be 0. */
 typedef struct vm_grad_tensor {
@@ -606,10 +626,13 @@ typedef struct vm_grad_tensor {
  * IEEE rules.  max_norm < 0 or NaN is VM_ERR_UNSUPPORTED.  An out must not
  * overlap its in except by being it, nor any other tensor of the list (the
  * latter is not checked).  count in [0, 65536] (VM_ERR_UNSUPPORTED beyond).
- * Temporary memory: up to 2048 partial sums (65536 for very long lists).
  */
 int vm_clip_grad_norm(const vm_grad_tensor *list, int64_t count, float max_norm,
-                      float *norm, void *stream);
+                      float *norm, void *workspace, int64_t workspace_bytes,
+                      void *stream);
+
+/* Workspace of vm_clip_grad_norm.  Pure host function. */
+int64_t vm_clip_grad_workspace(int64_t count);
 
 #ifdef __cplusplus
 }

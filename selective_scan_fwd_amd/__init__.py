@@ -20,7 +20,6 @@ from __future__ import annotations
 
 import array
 import ctypes
-import itertools
 import os
 import threading
 
@@ -43,7 +42,8 @@ EXPORTED = ("vm_status_string", "vm_version", "vm_selective_scan_fwd", "vm_bidir
             "vm_selective_scan_bwd", "vm_bidir_scan_bwd", "vm_pool_scan_repeat_bwd",
             "vm_ss2d_scan_bwd",
             "vm_gated_delta_fwd", "vm_gated_delta_bwd", "vm_gated_delta_step",
-            "vm_head_norm_rope", "vm_head_norm_rope_bwd", "vm_clip_grad_norm")
+            "vm_head_norm_rope", "vm_head_norm_rope_bwd", "vm_clip_grad_norm",
+            "vm_gated_delta_workspace", "vm_head_norm_rope_workspace", "vm_clip_grad_workspace")
 
 
 class VmScanDir(ctypes.Structure):
@@ -126,12 +126,17 @@ def load_library():
             lib.vm_ss2d_scan_bwd.argtypes = [D, P, P, P, F, G, P, P, I64, I64, I64, I64, I64, I, I, P]
             X, Y = ctypes.POINTER(VmDelta), ctypes.POINTER(VmDeltaGrad)
             N = ctypes.POINTER(VmHeadNorm)
-            lib.vm_gated_delta_fwd.argtypes = [X, P, P, F, I64, I64, I64, I64, I64, I64, I64, I, I, P]
-            lib.vm_gated_delta_bwd.argtypes = [X, P, P, Y, F, I64, I64, I64, I64, I64, I64, I64, I, I, P]
+            lib.vm_gated_delta_fwd.argtypes = [X, P, P, F, I64, I64, I64, I64, I64, I64, I64, I, I, P, I64, P]
+            lib.vm_gated_delta_bwd.argtypes = [X, P, P, Y, F, I64, I64, I64, I64, I64, I64, I64, I, I, P, I64, P]
             lib.vm_gated_delta_step.argtypes = [P, P, P, P, P, P, P, P, F, I64, I64, I64, I64, I64, I64, I, P]
             lib.vm_head_norm_rope.argtypes = [N, P, P, I64, I64, I64, I64, I64, F, I, I, P]
-            lib.vm_head_norm_rope_bwd.argtypes = [N, P, P, P, P, P, P, I64, I64, I64, I64, I64, F, I, I, P]
-            lib.vm_clip_grad_norm.argtypes = [ctypes.POINTER(VmGradTensor), I64, F, P, P]
+            lib.vm_head_norm_rope_bwd.argtypes = [N, P, P, P, P, P, P, I64, I64, I64, I64, I64, F, I, I, P, I64, P]
+            lib.vm_clip_grad_norm.argtypes = [ctypes.POINTER(VmGradTensor), I64, F, P, P, I64, P]
+            lib.vm_gated_delta_workspace.argtypes = [I64, I64, I64, I64, I64, I64, I, I, I]
+            lib.vm_head_norm_rope_workspace.argtypes = [I64]
+            lib.vm_clip_grad_workspace.argtypes = [I64]
+            for name in ("vm_gated_delta_workspace", "vm_head_norm_rope_workspace", "vm_clip_grad_workspace"):
+                getattr(lib, name).restype = I64
             for name in ("vm_gated_delta_fwd", "vm_gated_delta_bwd", "vm_gated_delta_step", "vm_head_norm_rope",
                          "vm_head_norm_rope_bwd", "vm_clip_grad_norm",
                          "vm_selective_scan_fwd", "vm_bidir_scan_fwd", "vm_bidir_scan_fwd_noalloc",
@@ -601,15 +606,32 @@ def _arg(t, name, dtype, shape, index):
     return t.data_ptr()
 
 
+def _current_stream(index):
+    """The raw handle of torch's current stream (a Stream object costs 3 us)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _launch(name, index, *args):
     """Call an entry point on the current stream of GPU `index`."""
+    call = getattr(load_library(), name)
     if index == torch.cuda.current_device():
-        st = getattr(load_library(), name)(*args, torch.cuda.current_stream().cuda_stream)
+        st = call(*args, _current_stream(index))
     else:
         with torch.cuda.device(index):
-            st = getattr(load_library(), name)(*args, torch.cuda.current_stream().cuda_stream)
+            st = call(*args, _current_stream(index))
     if st != VM_OK:
         _check(st, name)
+
+
+def _workspace(nbytes, device):
+    """Temporary memory of one call from torch's allocator, which hands it on in
+    stream order.  Returns the tensor (to be kept until the call returns), its
+    address and size."""
+    if nbytes <= 0:                              # sizes that the call itself refuses
+        return None, None, 0
+    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), nbytes
 
 
 def _tokens(t, name, dtype, shape, index):
@@ -677,9 +699,11 @@ def vm_gated_delta_fwd(q, k, v, g, beta, scale=None, h0=None, want_state=False, 
         out = torch.empty((batch, L, hv, dv), dtype=q.dtype, device=q.device)
     if state is None and want_state:
         state = torch.empty((n, hv, dk, dv), dtype=torch.float32, device=q.device)
+    ws, wp, wn = _workspace(load_library().vm_gated_delta_workspace(batch, L, n, hv, dk, dv, _dtype_code(q),
+                                                                    offsets is not None, 0), q.device)
     _launch("vm_gated_delta_fwd", index, p, _arg(out, "out", q.dtype, (batch, L, hv, dv), index),
             _arg(state, "state", torch.float32, (n, hv, dk, dv), index), dk ** -0.5 if scale is None else scale, batch, L,
-            n, hk, hv, dk, dv, _dtype_code(q), int(bool(reverse)))
+            n, hk, hv, dk, dv, _dtype_code(q), int(bool(reverse)), wp, wn)
     return out, state
 
 
@@ -696,8 +720,10 @@ def vm_gated_delta_bwd(q, k, v, g, beta, dout, scale=None, h0=None, dstate=None,
     if h0 is not None:
         d["h0"] = make(torch.float32, n, hv, dk, dv)
     grads = VmDeltaGrad(*(d[x].data_ptr() if x in d else None for x in ("q", "k", "v", "g", "beta", "h0")))
+    ws, wp, wn = _workspace(load_library().vm_gated_delta_workspace(batch, L, n, hv, dk, dv, _dtype_code(q),
+                                                                    offsets is not None, 1), q.device)
     _launch("vm_gated_delta_bwd", index, p, po, ps, grads, dk ** -0.5 if scale is None else scale, batch, L, n, hk, hv,
-            dk, dv, _dtype_code(q), int(bool(reverse)))
+            dk, dv, _dtype_code(q), int(bool(reverse)), wp, wn)
     return d
 
 
@@ -795,8 +821,10 @@ def vm_head_norm_rope_bwd(dq_out, dk_out, q, k=None, wq=None, wk=None, cos=None,
     dwq = make(torch.float32, dim) if wq is not None else None
     dwk = make(torch.float32, dim) if wk is not None and k is not None else None
     ptr = lambda t: t.data_ptr() if t is not None else None
+    ws, wp, wn = _workspace(load_library().vm_head_norm_rope_workspace(dim) if dwq is not None or dwk is not None else 0,
+                            q.device)
     _launch("vm_head_norm_rope_bwd", index, p, pq, pk, ptr(dq), ptr(dk), ptr(dwq), ptr(dwk), batch, L, hq, hk, dim, eps,
-            _norm_options(l2, interleaved), _dtype_code(q))
+            _norm_options(l2, interleaved), _dtype_code(q), wp, wn)
     return dq, dk, dwq, dwk
 
 
@@ -837,10 +865,14 @@ def vm_clip_grad_norm(grads, max_norm, out=None):
             _dev(y, f"out[{i}]", x.dtype, None, dev)
             if x.numel() != y.numel():
                 raise ValueError(f"out[{i}] has {y.numel()} elements, expected {x.numel()}")
-    table = array.array("q", itertools.chain.from_iterable(zip(ins, to, sizes, codes)))
-    norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+    table = array.array("q", bytes(32 * len(grads)))
+    for i, column in enumerate((ins, to, sizes, codes)):       # VmGradTensor: four fields of 8 bytes
+        table[i::4] = array.array("q", column)
+    dev = grads[0].device
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    ws, wp, wn = _workspace(load_library().vm_clip_grad_workspace(len(grads)), dev)
     _launch("vm_clip_grad_norm", index, ctypes.cast(table.buffer_info()[0], ctypes.POINTER(VmGradTensor)), len(grads),
-            max_norm, norm.data_ptr())
+            max_norm, norm.data_ptr(), wp, wn)
     return norm
 
 

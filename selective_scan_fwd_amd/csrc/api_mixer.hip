@@ -24,6 +24,7 @@ using vmk::span;
 // (work-items below 2^32) and heads on y.
 constexpr int64_t kMaxSlots = (int64_t{1} << 23) - 1;
 constexpr int64_t kMaxHeads = 65535;
+constexpr int64_t kMaxDeltaDim = 128, kMaxNormDim = 512, kMaxGrads = 65536;
 
 // Extent in elements of [batch, seqlen, heads, dim] with a token stride
 // (0 = dense); false if the stride is short or the extent overflows.
@@ -71,7 +72,7 @@ int check_delta(const vm_delta *p, float scale, int64_t batch, int64_t seqlen, i
       !dims_ok({n, hv, dk, dv}, &z->states))
     return VM_ERR_SHAPE;
   if (p->offsets != nullptr ? batch != 1 : n != batch) return VM_ERR_SHAPE;
-  if (!std::isfinite(scale) || dk > 128 || dv > 128 || hv > kMaxHeads) return VM_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || dk > kMaxDeltaDim || dv > kMaxDeltaDim || hv > kMaxHeads) return VM_ERR_UNSUPPORTED;
   // (the kernels reach the 64 tokens of a chunk with 31-bit byte offsets)
   for (int64_t stride : {z->qs, z->ks, z->vs, hv * dv})
     if (stride * 64 * 4 >= (int64_t{1} << 31)) return VM_ERR_UNSUPPORTED;
@@ -106,19 +107,26 @@ vmk::DeltaArgs delta_args(const vm_delta *p, const DeltaSizes &z, float scale, i
   return a;
 }
 
-// Temporary memory of one call as one allocation: the parts are laid out first
-// (each pool allocation and free costs the host some 10 us).
+// Temporary memory of one call in one piece: the parts are laid out first, then
+// taken from the caller's workspace or from the pool (where each allocation and
+// free costs the host some 10 us).
 class Parts {
  public:
+  static constexpr int64_t whole(int64_t bytes) { return (bytes + 255) & ~int64_t{255}; }
   template <typename P>
   void add(P **to, int64_t bytes) {
     to_[n_] = reinterpret_cast<void **>(to);
     at_[n_++] = total_;
-    total_ += (bytes + 255) & ~int64_t{255};
+    total_ += whole(bytes);
   }
-  int get(Scratch &ws) {
+  int64_t total() const { return total_; }
+  int get(void *workspace, int64_t bytes, Scratch &ws) {
     int st = VM_OK;
-    char *base = static_cast<char *>(ws.bytes(total_, &st));
+    char *base = static_cast<char *>(workspace);
+    if (base == nullptr)
+      base = static_cast<char *>(ws.bytes(total_, &st));
+    else if (bytes < total_ || (reinterpret_cast<uintptr_t>(base) & 255) != 0)
+      st = VM_ERR_ALLOC;
     if (st == VM_OK)
       for (int i = 0; i < n_; ++i) *to_[i] = base + at_[i];
     return st;
@@ -130,8 +138,9 @@ class Parts {
   int n_ = 0;
 };
 
-// The chunks' triangular inverses, masked products and decays.
-void chunk_parts(vmk::DeltaArgs &a, bool bf16, bool backward, Parts &parts) {
+// The chunks' triangular inverses, masked products and decays, and for the
+// backward pass what its kernels hand on.
+void delta_parts(vmk::DeltaArgs &a, bool bf16, bool backward, Parts &parts) {
   const int64_t per = a.slots * a.hv, c = vmk::kDeltaChunk, tri = per * vmk::kTriTerm * 2;
   const int terms_p = vmk::delta_terms_p(bf16);
   parts.add(&a.T, tri * (vmk::kTermsT + (backward ? 0 : terms_p)));
@@ -140,6 +149,11 @@ void chunk_parts(vmk::DeltaArgs &a, bool bf16, bool backward, Parts &parts) {
   if (backward) {
     parts.add(&a.TT, tri * (vmk::kTermsT + terms_p));
     parts.add(&a.gam, per * c * 8);
+    a.dvp = (a.dv + 15) / 16 * 16;
+    parts.add(&a.S, per * a.dk * a.dvp * 4);
+    parts.add(&a.dS, per * a.dk * a.dvp * 4);
+    parts.add(&a.V, per * c * a.dvp * 4);
+    parts.add(&a.dR, per * c * a.dvp * 4);
   }
 }
 
@@ -161,7 +175,7 @@ int check_norm(const vm_head_norm *p, int64_t batch, int64_t seqlen, int64_t hq,
     if (p->cos == nullptr || p->sin == nullptr) return VM_ERR_NULL;
     if (!dims_ok({p->table, p->rot}, &unused)) return VM_ERR_SHAPE;
   }
-  if (dim > 512 || hq > kMaxHeads || hk > kMaxHeads || !(eps >= 0.0f) || !std::isfinite(eps)) return VM_ERR_UNSUPPORTED;
+  if (dim > kMaxNormDim || hq > kMaxHeads || hk > kMaxHeads || !(eps >= 0.0f) || !std::isfinite(eps)) return VM_ERR_UNSUPPORTED;
   elems[0] = tokens * hq * dim;
   elems[1] = tokens * hk * dim;
   a->x[0] = p->q;
@@ -184,13 +198,50 @@ int check_norm(const vm_head_norm *p, int64_t batch, int64_t seqlen, int64_t hq,
   return VM_OK;
 }
 
+// Partial sums of one launch over up to kClipTable of `count` gradients: all
+// launches together at most kClipPartials, at least one each.
+int64_t clip_launches(int64_t count) { return (count + vmk::kClipTable - 1) / vmk::kClipTable; }
+int64_t clip_partials(int64_t count) {
+  const int64_t launches = clip_launches(count);
+  return launches > 0 && vmk::kClipPartials / launches > 1 ? vmk::kClipPartials / launches : 1;
+}
+
 }  // namespace
 
 extern "C" {
 
+int64_t vm_gated_delta_workspace(int64_t batch, int64_t seqlen, int64_t n, int64_t hv, int64_t dk, int64_t dv,
+                                 int dtype, int packed, int backward) {
+  int64_t unused = 0;
+  if (!dims_ok({batch, seqlen, hv, dk}, &unused) || !dims_ok({batch, seqlen, hv, dv}, &unused) ||
+      !dims_ok({n, hv, dk, dv}, &unused))
+    return -VM_ERR_SHAPE;
+  if (dk > kMaxDeltaDim || dv > kMaxDeltaDim) return -VM_ERR_UNSUPPORTED;
+  vmk::DeltaArgs a = {};
+  a.slots = vmk::delta_slots(batch, seqlen, n, packed != 0);
+  a.hv = static_cast<int>(hv);
+  a.dk = static_cast<int>(dk);
+  a.dv = static_cast<int>(dv);
+  Parts parts;
+  delta_parts(a, dtype == VM_BF16, backward != 0, parts);
+  return parts.total();
+}
+
+int64_t vm_head_norm_rope_workspace(int64_t dim) {
+  if (dim <= 0) return -VM_ERR_SHAPE;
+  if (dim > kMaxNormDim) return -VM_ERR_UNSUPPORTED;
+  return Parts::whole(vmk::kNormMaxBlocks * 2 * dim * 4);
+}
+
+int64_t vm_clip_grad_workspace(int64_t count) {
+  if (count < 0) return -VM_ERR_SHAPE;
+  if (count > kMaxGrads) return -VM_ERR_UNSUPPORTED;
+  return Parts::whole((clip_launches(count) * clip_partials(count) + 1) * 8);
+}
+
 int vm_gated_delta_fwd(const vm_delta *p, void *out, float *state, float scale, int64_t batch, int64_t seqlen,
                        int64_t n, int64_t hk, int64_t hv, int64_t dk, int64_t dv, int dtype, int reverse,
-                       void *stream) {
+                       void *workspace, int64_t workspace_bytes, void *stream) {
   DeltaSizes z = {};
   int st = check_delta(p, scale, batch, seqlen, n, hk, hv, dk, dv, dtype, reverse, &z);
   if (st != VM_OK) return st;
@@ -210,8 +261,8 @@ int vm_gated_delta_fwd(const vm_delta *p, void *out, float *state, float scale, 
   a.out = out;
   a.state = state;
   Parts parts;
-  chunk_parts(a, bf16, false, parts);
-  st = parts.get(ws);
+  delta_parts(a, bf16, false, parts);
+  st = parts.get(workspace, workspace_bytes, ws);
   if (st != VM_OK) return st;
   st = hip_status(vmk::launch_delta_prep(a, bf16, false, s));
   if (st != VM_OK) return st;
@@ -220,7 +271,7 @@ int vm_gated_delta_fwd(const vm_delta *p, void *out, float *state, float scale, 
 
 int vm_gated_delta_bwd(const vm_delta *p, const void *dout, const float *dstate, const vm_delta_grad *grad, float scale,
                        int64_t batch, int64_t seqlen, int64_t n, int64_t hk, int64_t hv, int64_t dk, int64_t dv,
-                       int dtype, int reverse, void *stream) {
+                       int dtype, int reverse, void *workspace, int64_t workspace_bytes, void *stream) {
   DeltaSizes z = {};
   int st = check_delta(p, scale, batch, seqlen, n, hk, hv, dk, dv, dtype, reverse, &z);
   if (st != VM_OK) return st;
@@ -250,14 +301,8 @@ int vm_gated_delta_bwd(const vm_delta *p, const void *dout, const float *dstate,
   a.dbeta = grad->dbeta;
   a.dh0 = grad->dh0;
   Parts parts;
-  chunk_parts(a, bf16, true, parts);
-  const int64_t per = a.slots * hv;
-  a.dvp = static_cast<int>((dv + 15) / 16 * 16);
-  parts.add(&a.S, per * dk * a.dvp * 4);
-  parts.add(&a.dS, per * dk * a.dvp * 4);
-  parts.add(&a.V, per * vmk::kDeltaChunk * a.dvp * 4);
-  parts.add(&a.dR, per * vmk::kDeltaChunk * a.dvp * 4);
-  st = parts.get(ws);
+  delta_parts(a, bf16, true, parts);
+  st = parts.get(workspace, workspace_bytes, ws);
   if (st != VM_OK) return st;
   st = hip_status(vmk::launch_delta_prep(a, bf16, true, s));
   if (st == VM_OK) st = hip_status(vmk::launch_delta_scan(a, bf16, true, s));
@@ -278,7 +323,7 @@ int vm_gated_delta_step(const void *q, const void *k, const void *v, const float
       !dims_ok({batch, hv}, &gates) || !dims_ok({n_slots, hv, dk, dv}, &states))
     return VM_ERR_SHAPE;
   if (slots == nullptr && batch > n_slots) return VM_ERR_SHAPE;
-  if (!std::isfinite(scale) || dk > 128 || dv > 128 || gates * 4 >= (int64_t{1} << 26)) return VM_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || dk > kMaxDeltaDim || dv > kMaxDeltaDim || gates * 4 >= (int64_t{1} << 26)) return VM_ERR_UNSUPPORTED;
   const int es = dtype == VM_BF16 ? 2 : 4;
   const Span ins[] = {span(q, keys * es), span(k, keys * es), span(v, values * es), span(g, gates * 4),
                       span(beta, gates * 4), span(slots, batch * 4)};
@@ -323,7 +368,7 @@ int vm_head_norm_rope(const vm_head_norm *p, void *q_out, void *k_out, int64_t b
 
 int vm_head_norm_rope_bwd(const vm_head_norm *p, const void *dq_out, const void *dk_out, void *dq, void *dk, float *dwq,
                           float *dwk, int64_t batch, int64_t seqlen, int64_t hq, int64_t hk, int64_t dim, float eps,
-                          int norm_options, int dtype, void *stream) {
+                          int norm_options, int dtype, void *workspace, int64_t workspace_bytes, void *stream) {
   vmk::NormArgs a = {};
   int64_t ext[2] = {0, 0}, elems[2] = {0, 0};
   int st = check_norm(p, batch, seqlen, hq, hk, dim, eps, norm_options, dtype, &a, ext, elems);
@@ -347,15 +392,20 @@ int vm_head_norm_rope_bwd(const vm_head_norm *p, const void *dq_out, const void 
   a.dw[1] = dwk;
   hipStream_t s = static_cast<hipStream_t>(stream);
   Scratch ws(s);
-  if (dwq != nullptr || dwk != nullptr) a.partial = ws.get(static_cast<int64_t>(vmk::kNormMaxBlocks) * 2 * dim, &st);
-  if (st != VM_OK) return st;
+  if (dwq != nullptr || dwk != nullptr) {
+    Parts parts;
+    parts.add(&a.partial, vm_head_norm_rope_workspace(dim));
+    st = parts.get(workspace, workspace_bytes, ws);
+    if (st != VM_OK) return st;
+  }
   return hip_status(vmk::launch_norm(a, bf16, true, s));
 }
 
-int vm_clip_grad_norm(const vm_grad_tensor *list, int64_t count, float max_norm, float *norm, void *stream) {
+int vm_clip_grad_norm(const vm_grad_tensor *list, int64_t count, float max_norm, float *norm, void *workspace,
+                      int64_t workspace_bytes, void *stream) {
   if (norm == nullptr || (list == nullptr && count > 0)) return VM_ERR_NULL;
   if (count < 0) return VM_ERR_SHAPE;
-  if (count > 65536 || !(max_norm >= 0.0f)) return VM_ERR_UNSUPPORTED;
+  if (count > kMaxGrads || !(max_norm >= 0.0f)) return VM_ERR_UNSUPPORTED;
   const Span sn = span(norm, 4);
   bool scaled = false;
   int64_t chunks = 0;
@@ -374,11 +424,11 @@ int vm_clip_grad_norm(const vm_grad_tensor *list, int64_t count, float max_norm,
   hipStream_t s = static_cast<hipStream_t>(stream);
   Scratch ws(s);
   int st = VM_OK;
-  const int64_t launches = (count + vmk::kClipTable - 1) / vmk::kClipTable;
-  // partial sums of one launch: all launches together at most kClipPartials,
-  // at least one each
-  const int64_t most = launches > 0 && vmk::kClipPartials / launches > 1 ? vmk::kClipPartials / launches : 1;
-  double *partial = static_cast<double *>(ws.bytes((launches * most + 1) * 8, &st));
+  const int64_t most = clip_partials(count);
+  double *partial = nullptr;
+  Parts parts;
+  parts.add(&partial, vm_clip_grad_workspace(count));
+  st = parts.get(workspace, workspace_bytes, ws);
   if (st != VM_OK) return st;
   int used = 0;
   for (int pass = 0; pass < (scaled ? 2 : 1); ++pass)

@@ -408,19 +408,43 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// The sequence at place r of the packed ones in order of falling length (the
+// lengths need not make sense: any values have an order).
+__device__ __forceinline__ int by_length(const DeltaArgs &A, int r) {
+  const int lane = threadIdx.x & 63, n = A.nseq;
+  const int len = lane < n ? A.off[lane + 1] - A.off[lane] : 0;
+  int before = 0;
+  for (int j = 0; j < n; ++j) {
+    const int other = __builtin_amdgcn_readlane(len, j);
+    before += other > len || (other == len && j < lane) ? 1 : 0;
+  }
+  return __builtin_ctzll(__ballot(lane < n && before == r));
+}
+
 // Workgroups of one sequence and head (which share K, Q and the triangles) are
-// neighbours on one XCD.
+// neighbours on one XCD.  Sequences of one length: each XCD takes a run of them
+// (with their heads, which share K and Q too).  Packed sequences: the heads go
+// round the XCDs, and up to 64 sequences are taken in order of falling length,
+// so that no XCD and no compute unit is left with the long ones at the end.
 struct Place {
   int s, h, cb;
 };
-__device__ __forceinline__ Place place(const DeltaArgs &A, int colblocks) {
-  const int id = xcd_remap(blockIdx.x, gridDim.x);
-  Place p;
-  p.cb = id % colblocks;
-  const int sh = id / colblocks;
-  p.h = sh % A.hv;
-  p.s = sh / A.hv;
-  return p;
+__device__ __forceinline__ bool place(const DeltaArgs &A, int colblocks, Place *p) {
+  int sh;
+  if (A.off == nullptr) {
+    const int id = xcd_remap(blockIdx.x, gridDim.x);
+    p->cb = id % colblocks;
+    sh = id / colblocks;
+  } else {
+    const int k = blockIdx.x / kXcd;
+    p->cb = k % colblocks;
+    sh = k / colblocks * kXcd + blockIdx.x % kXcd;
+    if (sh >= A.nseq * A.hv) return false;      // (the grid is whole rounds of the XCDs)
+  }
+  p->h = sh % A.hv;
+  p->s = sh / A.hv;
+  if (A.off != nullptr && A.nseq > 1 && A.nseq <= 64) p->s = by_length(A, p->s);
+  return true;
 }
 
 // Half p's D tiles of a state at [dk][cols] memory, and of [64][16] at [64][dvp];
@@ -473,7 +497,8 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_kernel(DeltaAr
     Lds lds[kBuffers];
     __attribute__((aligned(16))) char xch[NP][kItems * 1024];
   } sh;
-  const Place pl = place(A, colblocks);
+  Place pl;
+  if (!place(A, colblocks, &pl)) return;
   const int s = pl.s, h = pl.h;
   const Seq q = sequence(A, s);
   Load next;
@@ -637,7 +662,8 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(Del
     Lds lds[kBuffers];
     __attribute__((aligned(16))) char xch[NP][kItems * 1024];
   } sh;
-  const Place pl = place(A, colblocks);
+  Place pl;
+  if (!place(A, colblocks, &pl)) return;
   const int s = pl.s, h = pl.h;
   const Seq q = sequence(A, s);
   const int64_t row = static_cast<int64_t>(A.hv) * A.dv;      // token stride of dout and dv
@@ -783,11 +809,18 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(Del
 // buffers of bf16).
 template <int DK> constexpr int kPairs = DK == 128 ? 2 : 4;
 
+// Workgroups of a scan with cb column blocks, as place() takes them apart.
+dim3 scan_grid(const DeltaArgs &a, int cb) {
+  int64_t heads = static_cast<int64_t>(a.nseq) * a.hv;
+  if (a.off != nullptr) heads = (heads + kXcd - 1) / kXcd * kXcd;
+  return dim3(static_cast<uint32_t>(heads * cb));
+}
+
 template <typename T, int DK, bool VEC>
 hipError_t launch_fwd(const DeltaArgs &a, bool keep, hipStream_t s) {
   constexpr int NP = kPairs<DK>;
   const int cb = (a.dv + 16 * NP - 1) / (16 * NP);
-  const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(a.nseq) * a.hv * cb)), block(Shape<NP>::kThreads);
+  const dim3 grid = scan_grid(a, cb), block(Shape<NP>::kThreads);
   if (keep)
     hipLaunchKernelGGL((delta_scan_kernel<T, DK, true, VEC, NP>), grid, block, 0, s, a, cb);
   else
@@ -804,7 +837,7 @@ template <typename T, int DK>
 hipError_t launch_bwd(const DeltaArgs &a, hipStream_t s) {
   constexpr int NP = kPairs<DK>;
   const int cb = (a.dv + 16 * NP - 1) / (16 * NP);
-  const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(a.nseq) * a.hv * cb)), block(Shape<NP>::kThreads);
+  const dim3 grid = scan_grid(a, cb), block(Shape<NP>::kThreads);
   if (delta_vec(a, sizeof(T)) && delta_vec_values(a, a.dout, static_cast<int64_t>(a.hv) * a.dv, sizeof(T), 4))
     hipLaunchKernelGGL((delta_scan_bwd_kernel<T, DK, true, NP>), grid, block, 0, s, a, cb);
   else

@@ -25,31 +25,31 @@ __global__ __launch_bounds__(64) void delta_step_kernel(StepArgs A) {
   const int64_t bh = blockIdx.x / colblocks;
   const int b = static_cast<int>(bh / A.hv), h = static_cast<int>(bh % A.hv), kh = h / (A.hv / A.hk);
   const int col = cb * kCols + (lane % 8) * 4;
-  const int64_t slot = A.slots != nullptr ? A.slots[b] : b;
-  T *out = static_cast<T *>(A.out) + bh * A.dv;
-  if (slot < 0 || slot >= A.n_slots) {
+  const int64_t slot = uniform(A.slots != nullptr ? A.slots[b] : b);
+  const Rsrc out = buffer(static_cast<T *>(A.out) + bh * A.dv, A.dv * sizeof(T));
+  const auto store_out = [&](f32x4 y) {
     if (rg == 0)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (col + e < A.dv) out[col + e] = from_f32<T>(0.0f);
+      for (int e = 0; e < 4; ++e) bstore(out, (col + e) * sizeof(T), from_f32<T>(y[e]));
+  };
+  if (slot < 0 || slot >= A.n_slots) {
+    store_out(f32x4{0, 0, 0, 0});
     return;
   }
-  float *S = A.state + (slot * A.hv + h) * A.dk * A.dv;
+  // rows past dk lie past the resource's end, columns past dv go nowhere
+  const Rsrc S = buffer(A.state + (slot * A.hv + h) * A.dk * A.dv, A.dk * A.dv * 4);
+  uint32_t at[4];                           // of row rg, this lane's columns
+#pragma unroll
+  for (int e = 0; e < 4; ++e) at[e] = col + e < A.dv ? (rg * A.dv + col + e) * 4 : kNowhere;
+  const uint32_t step = 8 * A.dv * 4;
   f32x4 x[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int row = rg + 8 * i;
-    x[i] = f32x4{0, 0, 0, 0};
-    if (row < A.dk) {
-      const float *p = S + static_cast<int64_t>(row) * A.dv + col;
-      if (VEC) {
-        if (col < A.dv) x[i] = load4(p);
-      } else {
+    if (VEC)
+      x[i] = __builtin_bit_cast(f32x4, bload16(S, at[0] + i * step));
+    else
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col + e < A.dv) x[i][e] = p[e];
-      }
-    }
+      for (int e = 0; e < 4; ++e) x[i][e] = bload<float>(S, at[e] + i * step);
   }
   const int64_t key = (static_cast<int64_t>(b) * A.hk + kh) * A.dk;
   for (int i = lane; i < DK; i += 64) {
@@ -57,10 +57,10 @@ __global__ __launch_bounds__(64) void delta_step_kernel(StepArgs A) {
     sq[i] = i < A.dk ? to_f32(static_cast<const T *>(A.q)[key + i]) : 0.0f;
   }
   const float a = hw_exp2(A.g[bh] * kLog2e), beta = A.beta[bh];
-  f32x4 v = {0, 0, 0, 0};
+  const Rsrc values = buffer(static_cast<const T *>(A.v) + bh * A.dv, A.dv * sizeof(T));
+  f32x4 v;
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (col + e < A.dv) v[e] = to_f32(static_cast<const T *>(A.v)[bh * A.dv + col + e]);
+  for (int e = 0; e < 4; ++e) v[e] = to_f32(bload<T>(values, (col + e) * sizeof(T)));
   __syncthreads();
   f32x4 pk = {0, 0, 0, 0}, pq = {0, 0, 0, 0};
   float qk = 0;
@@ -84,25 +84,14 @@ __global__ __launch_bounds__(64) void delta_step_kernel(StepArgs A) {
   const f32x4 err = (v - pk) * beta;
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int row = rg + 8 * i;
-    if (row < A.dk) {
-      const f32x4 y = x[i] + err * sk[row];
-      float *p = S + static_cast<int64_t>(row) * A.dv + col;
-      if (VEC) {
-        if (col < A.dv) *reinterpret_cast<f32x4 *>(p) = y;
-      } else {
+    const f32x4 y = x[i] + err * sk[rg + 8 * i];
+    if (VEC)
+      bstore16(S, at[0] + i * step, __builtin_bit_cast(u32x4, y));
+    else
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col + e < A.dv) p[e] = y[e];
-      }
-    }
+      for (int e = 0; e < 4; ++e) bstore(S, at[e] + i * step, y[e]);
   }
-  if (rg == 0) {
-    const f32x4 y = (pq + err * qk) * A.scale;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (col + e < A.dv) out[col + e] = from_f32<T>(y[e]);
-  }
+  store_out((pq + err * qk) * A.scale);
 }
 
 template <typename T, int DK>

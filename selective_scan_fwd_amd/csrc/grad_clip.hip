@@ -17,6 +17,7 @@ namespace vmk {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAhead = 8;    // loads of 16 bytes that a thread has in flight
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -53,8 +54,8 @@ __device__ __forceinline__ double chunk_squares(const T *x, int n) {
   int done = 0;
   if (aligned16(x)) {
     const int vecs = n / kVec;
-    for (int i = threadIdx.x; i < vecs; i += kThreads) {
-      const u32x4 raw = reinterpret_cast<const u32x4 *>(x)[i];
+    const u32x4 *from = reinterpret_cast<const u32x4 *>(x);
+    const auto add = [&](u32x4 raw) {
       const T *e = reinterpret_cast<const T *>(&raw);
 #pragma unroll
       for (int j = 0; j < kVec; j += 2) {
@@ -62,7 +63,16 @@ __device__ __forceinline__ double chunk_squares(const T *x, int n) {
         a = __builtin_fma(p, p, a);
         b = __builtin_fma(q, q, b);
       }
+    };
+    int i = threadIdx.x;
+    for (; i + (kAhead - 1) * kThreads < vecs; i += kAhead * kThreads) {
+      u32x4 raw[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) raw[j] = from[i + j * kThreads];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) add(raw[j]);
     }
+    for (; i < vecs; i += kThreads) add(from[i]);
     done = vecs * kVec;
   }
   for (int i = done + threadIdx.x; i < n; i += kThreads) {
@@ -78,13 +88,23 @@ __device__ __forceinline__ void chunk_scale(const T *x, T *y, int n, float f) {
   int done = 0;
   if (aligned16(x) && aligned16(y)) {
     const int vecs = n / kVec;
-    for (int i = threadIdx.x; i < vecs; i += kThreads) {
-      u32x4 raw = reinterpret_cast<const u32x4 *>(x)[i];
+    const u32x4 *from = reinterpret_cast<const u32x4 *>(x);
+    u32x4 *to = reinterpret_cast<u32x4 *>(y);
+    const auto scaled = [f](u32x4 raw) {
       T *e = reinterpret_cast<T *>(&raw);
 #pragma unroll
       for (int j = 0; j < kVec; ++j) e[j] = from_f32<T>(to_f32(e[j]) * f);
-      reinterpret_cast<u32x4 *>(y)[i] = raw;
+      return raw;
+    };
+    int i = threadIdx.x;
+    for (; i + (kAhead - 1) * kThreads < vecs; i += kAhead * kThreads) {
+      u32x4 raw[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) raw[j] = from[i + j * kThreads];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) to[i + j * kThreads] = scaled(raw[j]);
     }
+    for (; i < vecs; i += kThreads) to[i] = scaled(from[i]);
     done = vecs * kVec;
   }
   for (int i = done + threadIdx.x; i < n; i += kThreads) y[i] = from_f32<T>(to_f32(x[i]) * f);
@@ -126,7 +146,8 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, const
   float f = max_norm / (total + 1e-6f);
   f = f > 1.0f ? 1.0f : f;              // (NaN stays NaN)
   const uint32_t chunks = t.first[t.n];
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+  for (uint32_t b = blockIdx.x; b < chunks; b += gridDim.x) {
+    const uint32_t c = chunks - 1 - b;  // what the sums read last is nearest still
     const int i = tensor_of(t, c);
     if (t.out[i] == nullptr || (f == 1.0f && t.out[i] == t.in[i])) continue;
     const int64_t at = static_cast<int64_t>(c - t.first[i]) * kClipChunk;

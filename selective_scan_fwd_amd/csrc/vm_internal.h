@@ -62,11 +62,11 @@ __device__ __forceinline__ float silu_f(float z) {
   return z * hw_rcp(1.0f + hw_exp2(-z * kLog2e));
 }
 
+constexpr int kXcd = 8;
 // Workgroups are dispatched round-robin over the 8 XCDs of an MI355X.  Give
 // each XCD a contiguous range of logical blocks, so that neighbouring row
 // blocks of one batch row (which share B and C) meet in the same L2.
 __device__ __forceinline__ int xcd_remap(int bid, int nblocks) {
-  constexpr int kXcd = 8;
   int q = nblocks / kXcd, r = nblocks % kXcd;
   int x = bid % kXcd, k = bid / kXcd;
   return x * q + (x < r ? x : r) + k;

@@ -33,17 +33,17 @@ def _delta(h0=None, offsets=None, strides=(0, 0, 0), **null):
     return p
 
 
-def _fwd(lib, p=None, out=_at(9), state=None, scale=1.0, dtype=0, reverse=0, **more):
+def _fwd(lib, p=None, out=_at(9), state=None, scale=1.0, dtype=0, reverse=0, ws=(None, 0), **more):
     s = {**OK_SHAPE, **more}
     return lib.vm_gated_delta_fwd(ctypes.byref(p if p is not None else _delta()), out, state, scale, s["batch"], s["L"],
-                                  s["n"], s["hk"], s["hv"], s["dk"], s["dv"], dtype, reverse, None)
+                                  s["n"], s["hk"], s["hv"], s["dk"], s["dv"], dtype, reverse, *ws, None)
 
 
-def _bwd(lib, p=None, dout=_at(10), dstate=None, g=None, scale=1.0, dtype=0, reverse=0, **more):
+def _bwd(lib, p=None, dout=_at(10), dstate=None, g=None, scale=1.0, dtype=0, reverse=0, ws=(None, 0), **more):
     s = {**OK_SHAPE, **more}
     g = vm.VmDeltaGrad(*(_at(11 + i) for i in range(6))) if g is None else g
     return lib.vm_gated_delta_bwd(ctypes.byref(p if p is not None else _delta()), dout, dstate, ctypes.byref(g), scale,
-                                  s["batch"], s["L"], s["n"], s["hk"], s["hv"], s["dk"], s["dv"], dtype, reverse, None)
+                                  s["batch"], s["L"], s["n"], s["hk"], s["hv"], s["dk"], s["dv"], dtype, reverse, *ws, None)
 
 
 @pytest.mark.parametrize("call", [_fwd, _bwd])
@@ -121,14 +121,15 @@ def _step_at(name):
     return _at(["q", "k", "v", "g", "beta", "state", "slots", "out"].index(name))
 
 
-def _norm(lib, back=False, batch=2, L=3, hq=4, hk=2, dim=8, eps=1e-6, options=0, dtype=0, rot=4, table=9, stride=0, **ptr):
+def _norm(lib, back=False, batch=2, L=3, hq=4, hk=2, dim=8, eps=1e-6, options=0, dtype=0, rot=4, table=9, stride=0,
+          ws=(None, 0), **ptr):
     p = dict(q=_at(0), k=_at(1), wq=_at(2), wk=_at(3), cos=_at(4), sin=_at(5), positions=_at(6), qo=_at(7), ko=_at(8),
              dq=_at(9), dk=_at(10), dwq=_at(11), dwk=_at(12))
     p.update(ptr)
     h = vm.VmHeadNorm(p["q"], p["k"], p["wq"], p["wk"], p["cos"], p["sin"], p["positions"], stride, 0, table, rot)
     tail = (batch, L, hq, hk, dim, eps, options, dtype, None)
     if back:
-        return lib.vm_head_norm_rope_bwd(ctypes.byref(h), p["qo"], p["ko"], p["dq"], p["dk"], p["dwq"], p["dwk"], *tail)
+        return lib.vm_head_norm_rope_bwd(ctypes.byref(h), p["qo"], p["ko"], p["dq"], p["dk"], p["dwq"], p["dwk"], *tail[:-1], *ws, None)
     return lib.vm_head_norm_rope(ctypes.byref(h), p["qo"], p["ko"], *tail)
 
 
@@ -160,13 +161,13 @@ def test_head_norm_refusals(lib, back):
 
 
 def test_clip_refusals(lib):
-    def call(tensors, most=1.0, norm=_at(9), count=None):
+    def call(tensors, most=1.0, norm=_at(9), count=None, ws=(None, 0)):
         arr = (vm.VmGradTensor * max(1, len(tensors)))(*(vm.VmGradTensor(*t) for t in tensors))
-        return lib.vm_clip_grad_norm(arr, len(tensors) if count is None else count, most, norm, None)
+        return lib.vm_clip_grad_norm(arr, len(tensors) if count is None else count, most, norm, *ws, None)
 
     good = (_at(0), _at(1), 10, 0)
     assert call([good], norm=None) == 1
-    assert lib.vm_clip_grad_norm(None, 1, 1.0, _at(9), None) == 1
+    assert lib.vm_clip_grad_norm(None, 1, 1.0, _at(9), None, 0, None) == 1
     assert call([(None, _at(1), 10, 0)]) == 1
     assert call([good], count=-1) == 2
     assert call([(_at(0), _at(1), -1, 0)]) == 2
@@ -176,6 +177,25 @@ def test_clip_refusals(lib):
     assert call([(_at(0), _at(0) + 8, 10, 0)]) == 5                 # partly on its own input
     assert call([good], norm=_at(1) + 4) == 5
     assert call([good], norm=_at(0)) == 5
+
+
+def test_workspaces(lib):
+    """Sizes from the _workspace functions; a workspace that is too small or not
+    aligned is refused before anything is launched."""
+    size = lib.vm_gated_delta_workspace(2, 5, 2, 4, 8, 6, 0, 0, 0)
+    back = lib.vm_gated_delta_workspace(2, 5, 2, 4, 8, 6, 0, 0, 1)
+    assert 0 < size < back
+    assert lib.vm_gated_delta_workspace(1, 128, 3, 4, 8, 6, 0, 1, 0) > lib.vm_gated_delta_workspace(1, 128, 1, 4, 8, 6, 0, 0, 0)
+    assert lib.vm_gated_delta_workspace(2, 0, 2, 4, 8, 6, 0, 0, 0) == -2
+    assert _fwd(lib, ws=(_at(40), size - 1)) == 8 and _fwd(lib, ws=(_at(40) + 16, size + 64)) == 8
+    assert _bwd(lib, ws=(_at(40), back - 1)) == 8 and _bwd(lib, ws=(_at(40) + 128, back + 128)) == 8
+    size = lib.vm_head_norm_rope_workspace(8)
+    assert size > 0
+    assert _norm(lib, True, ws=(_at(40), size - 1)) == 8
+    size = lib.vm_clip_grad_workspace(300)
+    assert size >= lib.vm_clip_grad_workspace(0) > 0
+    arr = (vm.VmGradTensor * 1)(vm.VmGradTensor(_at(0), _at(1), 10, 0))
+    assert lib.vm_clip_grad_norm(arr, 1, 1.0, _at(9), _at(40), 7, None) == 8
 
 
 def test_binding_refuses_tensors_off_the_gpu():

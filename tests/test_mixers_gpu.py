@@ -278,6 +278,39 @@ def test_step_replays_in_a_graph():
         assert torch.equal(out, want) and torch.equal(state, eager)
 
 
+def test_delta_forward_replays_in_a_graph():
+    # the binding's workspace comes from torch's allocator, so a capture allocates nothing of its own
+    _case("delta forward in a graph")
+    x, _ = delta_inputs(19, 2, 130, 2, 4, 64, 64, BF16)
+    vm.vm_gated_delta_fwd(**x, want_state=True)
+    torch.cuda.synchronize()
+    out, state = torch.empty_like(x["v"]), torch.empty(2, 4, 64, 64, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        vm.vm_gated_delta_fwd(**x, out=out, state=state)
+    for k in range(4):
+        x["v"].mul_(0.5)
+        want, last = vm.vm_gated_delta_fwd(**x, want_state=True)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(state, last)
+
+
+def test_calls_without_a_workspace_use_the_pool():
+    _case("delta from the pool")
+    import ctypes
+    x, g = delta_inputs(20, 1, 100, 1, 2, 32, 32, F32)
+    want, _ = vm.vm_gated_delta_fwd(**x, scale=0.5)
+    out = torch.empty_like(want)
+    p = vm.VmDelta(*(x[m].data_ptr() for m in ("q", "k", "v", "g", "beta")), None, None, 0, 0, 0)
+    s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    for _ in range(3):
+        out.zero_()
+        assert vm.load_library().vm_gated_delta_fwd(ctypes.byref(p), ctypes.c_void_p(out.data_ptr()), None, 0.5, 1, 100, 1,
+                                                    1, 2, 32, 32, vm.VM_F32, 0, None, 0, s) == 0
+        assert torch.equal(out, want)
+
+
 # ---------------------------------------------------- norm with rotation
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("b,l,hq,hk,dim,rot", [(1, 1, 1, 1, 1, 0), (2, 7, 3, 1, 64, 64), (3, 5, 4, 2, 128, 32),
@@ -387,7 +420,7 @@ def test_clip_norm_only_through_the_c_abi():
     arr = (vm.VmGradTensor * 1)(vm.VmGradTensor(x.data_ptr(), None, x.numel(), vm.VM_F32))
     lib = vm.load_library()
     s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    assert lib.vm_clip_grad_norm(arr, 1, 1.0, ctypes.c_void_p(norm.data_ptr()), s) == 0
+    assert lib.vm_clip_grad_norm(arr, 1, 1.0, ctypes.c_void_p(norm.data_ptr()), None, 0, s) == 0
     assert abs(float(norm) / float(x.double().norm()) - 1) < 1e-6
-    assert lib.vm_clip_grad_norm(None, 0, 1.0, ctypes.c_void_p(norm.data_ptr()), s) == 0
+    assert lib.vm_clip_grad_norm(None, 0, 1.0, ctypes.c_void_p(norm.data_ptr()), None, 0, s) == 0
     assert float(norm) == 0.0
