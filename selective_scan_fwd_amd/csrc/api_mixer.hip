@@ -142,7 +142,7 @@ class Parts {
 // backward pass what its kernels hand on.
 void delta_parts(vmk::DeltaArgs &a, bool bf16, bool backward, Parts &parts) {
   const int64_t per = a.slots * a.hv, c = vmk::kDeltaChunk, tri = per * vmk::kTriTerm * 2;
-  const int terms_p = vmk::delta_terms_p(bf16);
+  const int terms_p = vmk::delta_terms_p(bf16, backward);
   parts.add(&a.T, tri * (vmk::kTermsT + (backward ? 0 : terms_p)));
   parts.add(&a.eg, per * c * 4);
   parts.add(&a.ew, per * c * 4);

@@ -29,7 +29,7 @@ constexpr int kThreads = 256;
 template <typename T, int DK, bool BACK, bool VEC>
 __global__ __launch_bounds__(kThreads, 4) void delta_prep_kernel(DeltaArgs A) {
   constexpr int kNi = kInputTerms<T>, kTerm = kC * DK, kPieces = DK / 8;
-  constexpr int kTermsP = kNi == 1 ? 2 : 3;
+  constexpr int kTermsP = delta_terms_p(kNi == 1, BACK);
   __shared__ __attribute__((aligned(16))) uint16_t sk[kNi * kTerm];
   __shared__ __attribute__((aligned(16))) uint16_t sq[BACK ? kNi * kTerm : 8];
   __shared__ __attribute__((aligned(16))) float sa[kC * kPitchC];  // A, later T

@@ -480,14 +480,15 @@ __device__ __forceinline__ void store_rows(const DeltaArgs &A, float *base, cons
 
 // Whether whole pieces go to LDS directly.
 template <typename T, bool VEC> constexpr bool kDirect = VEC && sizeof(T) == 2;
-// Exchanged items (1 KB) of a pair: two regions, the first reused.
-constexpr int kItemsA = 10, kItemsB = 2, kItems = kItemsA + kItemsB;
+// Exchanged items (1 KB) of a pair: forward two regions, the first reused;
+// backward one, reused twice.
+constexpr int kItemsA = 10, kItemsB = 2, kItems = kItemsA + kItemsB, kItemsBwd = 6;
 
 // Forward.  KEEP: S and V are stored for the backward pass, out and state not.
 template <typename T, int DK, bool KEEP, bool VEC, int NP>
 __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_kernel(DeltaArgs A, int colblocks) {
   constexpr int kNi = kInputTerms<T>, kNs = 3, kHalf = DK / 64;
-  constexpr int kTermsP = KEEP ? 0 : kNi == 1 ? 2 : 3;
+  constexpr int kTermsP = KEEP ? 0 : delta_terms_p(kNi == 1, false);
   constexpr int kNo = kNi == 1 ? 2 : 3;               // terms of S and V on their way to out only
   constexpr bool kDma = kDirect<T, VEC>, kAhead = kNi == 1;
   typedef ChunkLoad<T, DK, kTermsT + kTermsP, !KEEP, VEC, kDma, NP> Load;
@@ -653,14 +654,14 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_kernel(DeltaAr
 template <typename T, int DK, bool VEC, int NP>
 __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(DeltaArgs A, int colblocks) {
   constexpr int kNi = kInputTerms<T>, kNs = 3, kHalf = DK / 64;
-  constexpr int kTermsP = kNi == 1 ? 2 : 3;
+  constexpr int kTermsP = delta_terms_p(kNi == 1, true);
   constexpr bool kDma = kDirect<T, VEC>, kAhead = kNi == 1;
   typedef ChunkLoad<T, DK, kTermsT + kTermsP, true, VEC, kDma, NP> Load;
   typedef typename Load::Lds Lds;
   constexpr int kBuffers = kDma ? 2 : 1;
   __shared__ struct {
     Lds lds[kBuffers];
-    __attribute__((aligned(16))) char xch[NP][kItems * 1024];
+    __attribute__((aligned(16))) char xch[NP][kItemsBwd * 1024];
   } sh;
   Place pl;
   if (!place(A, colblocks, &pl)) return;
@@ -670,7 +671,7 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(Del
   Load next;
   next.init(A, h, pl.cb, static_cast<const T *>(A.dout), row);
   const int lane = next.lane, li = next.li, lg = next.lg, p = next.wave % 2;
-  char *xa = sh.xch[next.wave / 2], *xb = xa + kItemsA * 1024;
+  char *xa = sh.xch[next.wave / 2];
   const int col = next.col0 + 16 * (next.wave / 2) + li;
   const int64_t state_at = (static_cast<int64_t>(s) * A.hv + h) * A.dk * A.dv;
   const f32x4 zero = {0, 0, 0, 0};
@@ -691,7 +692,7 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(Del
     const Lds &l = sh.lds[buf];
     Lds &ln = sh.lds[kBuffers == 2 ? buf ^ 1 : 0];
     const bool more = c0 > 0;
-    // all of dout for P^T dout, this half's for Q^T dout
+    // all of dout for P^T dout and Q^T dout
     f32x4 o[4];
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) o[rt] = next.values(l, rt);
@@ -700,8 +701,6 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(Del
     Blocks<kTermsP> pa, pb;                 // P^T: this half's rows by the second half's steps, and the first's
     if (kAhead) {
       kr.read(l.k, p, li, lg);
-      pa.read(tp, tri_block_t(2 * p, 1), tri_block_t(2 * p + 1, 1), lane);
-      pb.read(tp, tri_block_t(0, 0), tri_block_t(1, 0), lane);
       __builtin_amdgcn_sched_barrier(0);
     }
     const f32x4 eg[2] = {load4(l.eg + 32 * p + 4 * lg), load4(l.eg + 32 * p + 16 + 4 * lg)};
@@ -709,7 +708,7 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(Del
     const f32x4 ew[2] = {load4(l.ew + 32 * p + 4 * lg), load4(l.ew + 32 * p + 16 + 4 * lg)};
     const float last = l.eg[kC - 1];
     if (more) next.load_v_k(A, q, c0 - kC, ln);
-    f32x4 xm[2], of[2];
+    f32x4 xm[2];
     Blocks<kTermsT> ta, tb;
     {
       f32x4 x[4] = {zero, zero, zero, zero}, other[2];
@@ -720,29 +719,20 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(Del
       kr.times(st, x);
       if (kAhead) {
         ta.read(l.tri, tri_block_t(2 * p, p), tri_block_t(2 * p + 1, p), lane);
-        tb.read(l.tri, tri_block_t(0, 1), tri_block_t(1, 1), lane);
+        if (p == 1) tb.read(l.tri, tri_block_t(0, 1), tri_block_t(1, 1), lane);
+        pa.read(tp, tri_block_t(2 * p, 1), tri_block_t(2 * p + 1, 1), lane);
+        if (p == 0) pb.read(tp, tri_block_t(0, 0), tri_block_t(1, 0), lane);
         __builtin_amdgcn_sched_barrier(0);
       }
       if (more) next.load_q(A, q, c0 - kC, ln);
       halves(x, p, xm, other);
       put(xa, 2 * p, lane, other[0]);
       put(xa, 2 * p + 1, lane, other[1]);
-      halves(o, p, of, other);
     }
-    const Terms<kNs> od = split<kNs>(of[0] * (eg[0] * A.scale), of[1] * (eg[1] * A.scale));
-    put(xa, 4 + 3 * p, lane, od);
     lds_barrier();
     f32x4 V[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) V[i] = (xm[i] + take(xa, 2 - 2 * p + i, lane)) * ew[i];
-    Terms<kNs> ow[2];
-    if (p == 0) {
-      ow[0] = od;
-      ow[1] = take_terms<kNs>(xa, 7, lane);
-    } else {
-      ow[0] = take_terms<kNs>(xa, 4, lane);
-      ow[1] = od;
-    }
     if (more) next.load_tri(A, q, c0 - kC, A.TT, ln);
     if (!kAhead) {
       pa.read(tp, tri_block_t(2 * p, 1), tri_block_t(2 * p + 1, 1), lane);
@@ -759,8 +749,8 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(Del
     if (p == 1) {
       f32x4 y[2] = {zero, zero};
       tb.times(vt, y);
-      put(xb, 0, lane, y[0]);
-      put(xb, 1, lane, y[1]);
+      put(xa, 0, lane, y[0]);             // (where this wave alone has read)
+      put(xa, 1, lane, y[1]);
     }
     ta.times(vt, R);
     ColumnTiles<DK> qc, kc;
@@ -770,8 +760,8 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(Del
       qc.read(l.q, p, li, lg);
     lds_barrier();
     if (p == 0) {
-      R[0] += take(xb, 0, lane);
-      R[1] += take(xb, 1, lane);
+      R[0] += take(xa, 0, lane);
+      R[1] += take(xa, 1, lane);
     }
     const f32x4 dv[2] = {R[0] * be[0], R[1] * be[1]};
     Terms<kNs> xw[2];
@@ -779,6 +769,11 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(Del
     put(xa, 3 * p, lane, mine);
 #pragma unroll
     for (int d = 0; d < DK / 32; ++d) D[d] *= last;
+    Terms<kNs> ow[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      ow[i] = split<kNs>(o[2 * i] * (load4(l.eg + 32 * i + 4 * lg) * A.scale),
+                         o[2 * i + 1] * (load4(l.eg + 32 * i + 16 + 4 * lg) * A.scale));
     qc.template times<kNi>(l.q, ow, p, li, lg, D);
     if (kDma)
       kc.read_past_loads(l.k, p, li, lg);

@@ -5,9 +5,14 @@
 // Two passes over the gradients, bound by memory: the first sums squares, the
 // second scales.  A pass handles up to 120 tensors in one launch: the table of
 // pointers and sizes travels in the kernel's arguments (3.6 KB), so nothing is
-// copied to the device first.  Tensors are cut into chunks of 16384 elements
-// and a block takes every grid-th chunk, so small and large tensors load the
-// card alike.
+// copied to the device first.  Tensors are cut into chunks of 2048 elements and
+// a block takes runs of up to 8 of them, as many runs as all others, so small
+// and large tensors load the card alike and no block is left with a last round
+// of its own (207 MB of bf16: sums 55 us; with chunks of 16384 dealt out one by
+// one 85 us).  The second pass goes back from the last run, which is nearest
+// still, to the first: 97 us, forwards 105 us.  Its loads and stores are past
+// their last use here and marked so; without that the next pass over other
+// memory waits for the written lines to leave the cache (sums 85 us).
 #include <hip/hip_runtime.h>
 
 #include "mixer_internal.h"
@@ -16,8 +21,8 @@
 namespace vmk {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kAhead = 8;    // loads of 16 bytes that a thread has in flight
+constexpr int kThreads = 512;
+constexpr int kAhead = 4;    // loads of 16 bytes that a thread has in flight
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -48,12 +53,12 @@ __device__ __forceinline__ bool aligned16(const void *p) {
 // Squares are exact in fp64 and their sums carry 53 bits, so no gradient
 // overflows the norm and the order of the sums costs nothing in fp32.
 template <typename T>
-__device__ __forceinline__ double chunk_squares(const T *x, int n) {
+__device__ __forceinline__ double run_squares(const T *x, int64_t n) {
   constexpr int kVec = 16 / sizeof(T);
   double a = 0, b = 0;
-  int done = 0;
+  int64_t done = 0;
   if (aligned16(x)) {
-    const int vecs = n / kVec;
+    const int64_t vecs = n / kVec;
     const u32x4 *from = reinterpret_cast<const u32x4 *>(x);
     const auto add = [&](u32x4 raw) {
       const T *e = reinterpret_cast<const T *>(&raw);
@@ -64,7 +69,7 @@ __device__ __forceinline__ double chunk_squares(const T *x, int n) {
         b = __builtin_fma(q, q, b);
       }
     };
-    int i = threadIdx.x;
+    int64_t i = threadIdx.x;
     for (; i + (kAhead - 1) * kThreads < vecs; i += kAhead * kThreads) {
       u32x4 raw[kAhead];
 #pragma unroll
@@ -75,7 +80,7 @@ __device__ __forceinline__ double chunk_squares(const T *x, int n) {
     for (; i < vecs; i += kThreads) add(from[i]);
     done = vecs * kVec;
   }
-  for (int i = done + threadIdx.x; i < n; i += kThreads) {
+  for (int64_t i = done + threadIdx.x; i < n; i += kThreads) {
     const double p = to_f32(x[i]);
     a = __builtin_fma(p, p, a);
   }
@@ -83,48 +88,68 @@ __device__ __forceinline__ double chunk_squares(const T *x, int n) {
 }
 
 template <typename T>
-__device__ __forceinline__ void chunk_scale(const T *x, T *y, int n, float f) {
+__device__ __forceinline__ void run_scale(const T *x, T *y, int64_t n, float f) {
   constexpr int kVec = 16 / sizeof(T);
-  int done = 0;
+  int64_t done = 0;
   if (aligned16(x) && aligned16(y)) {
-    const int vecs = n / kVec;
-    const u32x4 *from = reinterpret_cast<const u32x4 *>(x);
-    u32x4 *to = reinterpret_cast<u32x4 *>(y);
+    const int64_t vecs = n / kVec;
+    const u32x4 *from = reinterpret_cast<const u32x4 *>(x) + (vecs - 1);
+    u32x4 *to = reinterpret_cast<u32x4 *>(y) + (vecs - 1);
     const auto scaled = [f](u32x4 raw) {
       T *e = reinterpret_cast<T *>(&raw);
 #pragma unroll
       for (int j = 0; j < kVec; ++j) e[j] = from_f32<T>(to_f32(e[j]) * f);
       return raw;
     };
-    int i = threadIdx.x;
+    int64_t i = threadIdx.x;
     for (; i + (kAhead - 1) * kThreads < vecs; i += kAhead * kThreads) {
       u32x4 raw[kAhead];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) raw[j] = from[i + j * kThreads];
+      for (int j = 0; j < kAhead; ++j) raw[j] = __builtin_nontemporal_load(from - (i + j * kThreads));
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) to[i + j * kThreads] = scaled(raw[j]);
+      for (int j = 0; j < kAhead; ++j) __builtin_nontemporal_store(scaled(raw[j]), to - (i + j * kThreads));
     }
-    for (; i < vecs; i += kThreads) to[i] = scaled(from[i]);
+    for (; i < vecs; i += kThreads) __builtin_nontemporal_store(scaled(from[-i]), to - i);
     done = vecs * kVec;
   }
-  for (int i = done + threadIdx.x; i < n; i += kThreads) y[i] = from_f32<T>(to_f32(x[i]) * f);
+  for (int64_t i = done + threadIdx.x; i < n; i += kThreads) y[i] = from_f32<T>(to_f32(x[i]) * f);
 }
 
-__device__ __forceinline__ int chunk_len(int64_t elems, int64_t at) {
-  const int64_t left = elems - at;
-  return static_cast<int>(left < kClipChunk ? left : kClipChunk);
+// The elements [at, at + n) of tensor i that chunks [from, to) of its own hold.
+struct Run {
+  int64_t at, n;
+};
+__device__ __forceinline__ Run run_of(const ClipTable &t, int i, uint32_t from, uint32_t to) {
+  const int64_t at = static_cast<int64_t>(from - t.first[i]) * kClipChunk;
+  const int64_t end = static_cast<int64_t>(to - t.first[i]) * kClipChunk;
+  return Run{at, (end < t.elems[i] ? end : t.elems[i]) - at};
+}
+// Block b takes runs b, b + grid, ... of `len` chunks.
+struct Runs {
+  uint32_t chunks, len, rounds;
+};
+__device__ __forceinline__ Runs runs_of(const ClipTable &t) {
+  Runs r;
+  r.chunks = t.first[t.n];
+  r.rounds = (r.chunks + gridDim.x * kClipRun - 1) / (gridDim.x * kClipRun);
+  r.len = (r.chunks + gridDim.x * r.rounds - 1) / (gridDim.x * r.rounds);
+  return r;
 }
 
 __global__ __launch_bounds__(kThreads) void clip_sums_kernel(ClipTable t, double *partial) {
   __shared__ double red[kThreads / 64];
-  const uint32_t chunks = t.first[t.n];
+  const Runs all = runs_of(t);
   double sum = 0;
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int i = tensor_of(t, c);
-    const int64_t at = static_cast<int64_t>(c - t.first[i]) * kClipChunk;
-    const int n = chunk_len(t.elems[i], at);
-    sum += t.bf16[i] ? chunk_squares(static_cast<const bf16_t *>(t.in[i]) + at, n)
-                     : chunk_squares(static_cast<const float *>(t.in[i]) + at, n);
+  for (uint32_t y = 0; y < all.rounds; ++y) {
+    uint32_t c = (y * gridDim.x + blockIdx.x) * all.len;
+    const uint32_t end = c + all.len < all.chunks ? c + all.len : all.chunks;
+    for (int i = c < end ? tensor_of(t, c) : 0; c < end; ++i) {
+      const uint32_t to = t.first[i + 1] < end ? t.first[i + 1] : end;
+      const Run r = run_of(t, i, c, to);
+      sum += t.bf16[i] ? run_squares(static_cast<const bf16_t *>(t.in[i]) + r.at, r.n)
+                       : run_squares(static_cast<const float *>(t.in[i]) + r.at, r.n);
+      c = to;
+    }
   }
   sum = block_sum(sum, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
@@ -145,17 +170,20 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, const
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
   float f = max_norm / (total + 1e-6f);
   f = f > 1.0f ? 1.0f : f;              // (NaN stays NaN)
-  const uint32_t chunks = t.first[t.n];
-  for (uint32_t b = blockIdx.x; b < chunks; b += gridDim.x) {
-    const uint32_t c = chunks - 1 - b;  // what the sums read last is nearest still
-    const int i = tensor_of(t, c);
-    if (t.out[i] == nullptr || (f == 1.0f && t.out[i] == t.in[i])) continue;
-    const int64_t at = static_cast<int64_t>(c - t.first[i]) * kClipChunk;
-    const int n = chunk_len(t.elems[i], at);
-    if (t.bf16[i])
-      chunk_scale(static_cast<const bf16_t *>(t.in[i]) + at, static_cast<bf16_t *>(t.out[i]) + at, n, f);
-    else
-      chunk_scale(static_cast<const float *>(t.in[i]) + at, static_cast<float *>(t.out[i]) + at, n, f);
+  const Runs all = runs_of(t);
+  for (uint32_t y = all.rounds; y-- > 0;) {
+    const uint32_t begin = (y * gridDim.x + blockIdx.x) * all.len;
+    uint32_t c = begin + all.len < all.chunks ? begin + all.len : all.chunks;
+    for (int i = begin < c ? tensor_of(t, c - 1) : 0; begin < c; --i) {
+      const uint32_t from = t.first[i] > begin ? t.first[i] : begin;
+      const Run r = run_of(t, i, from, c);
+      c = from;
+      if (t.out[i] == nullptr || (f == 1.0f && t.out[i] == t.in[i])) continue;
+      if (t.bf16[i])
+        run_scale(static_cast<const bf16_t *>(t.in[i]) + r.at, static_cast<bf16_t *>(t.out[i]) + r.at, r.n, f);
+      else
+        run_scale(static_cast<const float *>(t.in[i]) + r.at, static_cast<float *>(t.out[i]) + r.at, r.n, f);
+    }
   }
 }
 

@@ -35,8 +35,9 @@ hipError_t launch_norm(NormArgs a, bool bf16, bool back, hipStream_t s);
 
 // ------------------------------------------------------------- clipping
 constexpr int kClipTable = 120;        // tensors of one launch (kernel arguments)
-constexpr int64_t kClipChunk = 16384;  // elements of one block's piece
-constexpr int kClipPartials = 2048;
+constexpr int64_t kClipChunk = 2048;   // elements
+constexpr uint32_t kClipRun = 8;       // chunks of a block at a time, at most
+constexpr int kClipPartials = 1024;   // blocks: four of 512 threads fill a compute unit
 struct ClipTable {
   const void *in[kClipTable];
   void *out[kClipTable];
@@ -88,10 +89,12 @@ struct DeltaArgs {
   float *dg, *dbeta, *dh0;
 };
 // Terms of bf16 that stand for an fp32 value (8 bits each, so three hold all
-// 24), and how many are kept of P, which enters the output only: with bf16
-// tokens the output is rounded to 8 bits and 16 suffice.
+// 24), and how many are kept of P: all, but forward, where it enters the output
+// only, 16 bits suffice with bf16 tokens, whose output is rounded to 8.  (The
+// gradients of g and beta are fp32 for all tokens: with 16 bits of P they are
+// 2.6e-6 off, with 24 bits 3e-7.)
 constexpr int kTermsT = 3;
-inline int delta_terms_p(bool bf16) { return bf16 ? 2 : 3; }
+inline constexpr int delta_terms_p(bool bf16, bool backward) { return bf16 && !backward ? 2 : 3; }
 constexpr int kTriBlocks = 6;
 constexpr int64_t kTriTerm = kTriBlocks * 64 * 8;   // values of one term
 // Whether every row of q and k is whole 16-byte pieces, and those of v (the
