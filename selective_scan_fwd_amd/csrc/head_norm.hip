@@ -27,12 +27,18 @@ constexpr int kThreads = 256;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 
-template <typename T> __device__ __forceinline__ f32x4 load4(const T *p);
-template <> __device__ __forceinline__ f32x4 load4<float>(const float *p) {
-  return *reinterpret_cast<const f32x4 *>(p);
+// LAST: what is loaded is not used again soon.
+template <bool LAST, typename V>
+__device__ __forceinline__ V load_as(const V *p) {
+  return LAST ? __builtin_nontemporal_load(p) : *p;
 }
-template <> __device__ __forceinline__ f32x4 load4<bf16_t>(const bf16_t *p) {
-  const u16x4 r = *reinterpret_cast<const u16x4 *>(p);
+template <bool LAST = false>
+__device__ __forceinline__ f32x4 load4(const float *p) {
+  return load_as<LAST>(reinterpret_cast<const f32x4 *>(p));
+}
+template <bool LAST = false>
+__device__ __forceinline__ f32x4 load4(const bf16_t *p) {
+  const u16x4 r = load_as<LAST>(reinterpret_cast<const u16x4 *>(p));
   return f32x4{to_f32(r[0]), to_f32(r[1]), to_f32(r[2]), to_f32(r[3])};
 }
 __device__ __forceinline__ void store4(float *p, f32x4 v) { *reinterpret_cast<f32x4 *>(p) = v; }
@@ -65,18 +71,18 @@ __device__ __forceinline__ void place_pair(int p, int dim, int rot, bool inter, 
   }
 }
 
-template <bool VEC, typename T>
+template <bool VEC, bool LAST, typename T>
 __device__ __forceinline__ void load_head(const T *x, const Place &pl, bool inter_piece, f32x4 &a, f32x4 &b) {
   if (VEC) {
     if (pl.at[0][0] < 0) {
       a = b = f32x4{0, 0, 0, 0};
     } else if (inter_piece) {
-      const f32x4 u = load4(x + pl.at[0][0]), v = load4(x + pl.at[0][0] + 4);
+      const f32x4 u = load4<LAST>(x + pl.at[0][0]), v = load4<LAST>(x + pl.at[0][0] + 4);
       a = f32x4{u[0], u[2], v[0], v[2]};
       b = f32x4{u[1], u[3], v[1], v[3]};
     } else {
-      a = load4(x + pl.at[0][0]);
-      b = load4(x + pl.at[1][0]);
+      a = load4<LAST>(x + pl.at[0][0]);
+      b = load4<LAST>(x + pl.at[1][0]);
     }
   } else {
 #pragma unroll
@@ -151,6 +157,18 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs A) {
        it += static_cast<int64_t>(gridDim.x) * kGroups) {
     const int64_t t = A.splits == 1 ? it : it / A.splits;
     const int first = A.splits == 1 ? 0 : static_cast<int>(it - t * A.splits);
+    // The next head is on its way while one is worked on (4097 tokens of 4 rows:
+    // 67 -> 63 us; two ahead gain nothing and cost the gradients 30 us), past its
+    // last use forward (60 us; the gradients, with twice the loads, lose 3 us).
+    f32x4 next_a, next_b, next_p, next_q;
+    auto fetch = [&](int h) {
+      const int m = h >= A.heads[0], hh = m ? h - A.heads[0] : h;
+      load_head<VEC, !BACK>(static_cast<const T *>(A.x[m]) + t * A.xs[m] + static_cast<int64_t>(hh) * A.dim, pl, inter_piece,
+                     next_a, next_b);
+      if (BACK)
+        load_head<VEC, !BACK>(static_cast<const T *>(A.dy[m]) + (t * A.heads[m] + hh) * A.dim, pl, inter_piece, next_p, next_q);
+    };
+    if (first < heads) fetch(first);
     f32x4 co = {1, 1, 1, 1}, si = {0, 0, 0, 0};
     bool live = true;
     if (A.rot > 0) {
@@ -173,16 +191,6 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs A) {
         }
       }
     }
-    // the next head is on its way while one is worked on (4097 tokens of 4 rows: 67 -> 63 us)
-    f32x4 next_a, next_b, next_p, next_q;
-    auto fetch = [&](int h) {
-      const int m = h >= A.heads[0], hh = m ? h - A.heads[0] : h;
-      load_head<VEC>(static_cast<const T *>(A.x[m]) + t * A.xs[m] + static_cast<int64_t>(hh) * A.dim, pl, inter_piece,
-                     next_a, next_b);
-      if (BACK)
-        load_head<VEC>(static_cast<const T *>(A.dy[m]) + (t * A.heads[m] + hh) * A.dim, pl, inter_piece, next_p, next_q);
-    };
-    if (live && first < heads) fetch(first);
     for (int h = first; h < heads; h += A.splits) {
       const int m = h >= A.heads[0], hh = m ? h - A.heads[0] : h;
       T *y = static_cast<T *>(A.y[m]) + (t * A.heads[m] + hh) * A.dim;
@@ -290,7 +298,7 @@ hipError_t launch_dim(const NormArgs &a, int blocks, bool back, hipStream_t s) {
 
 // Groups that share one token: one where the tokens alone give the card 16
 // workgroups a compute unit, else up to a group per head.  (4097 tokens of 4
-// rows, 24 heads of 128 in bf16, inputs not in the caches: 63 us, with 4
+// rows, 24 heads of 128 in bf16, inputs not in the caches: 60 us, with 4
 // workgroups 71, with 64 75.)
 int head_splits(const NormArgs &a) {
   const int64_t want = 256 * 16 * (kThreads / lanes_per_head(a.dim));
