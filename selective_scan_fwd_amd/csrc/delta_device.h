@@ -133,6 +133,10 @@ template <> __device__ __forceinline__ bf16_t bload<bf16_t>(Rsrc r, uint32_t off
 __device__ __forceinline__ void bstore(Rsrc r, uint32_t off, float v) {
   __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, static_cast<int>(off), 0, 0);
 }
+// Of what no kernel reads before the caches have passed on to other lines.
+__device__ __forceinline__ void bstore_far(Rsrc r, uint32_t off, float v) {
+  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, static_cast<int>(off), 0, /*nontemporal*/ 2);
+}
 __device__ __forceinline__ void bstore(Rsrc r, uint32_t off, bf16_t v) {
   __builtin_amdgcn_raw_buffer_store_b16(v, r, static_cast<int>(off), 0, 0);
 }
