@@ -486,8 +486,9 @@ typedef struct vm_delta {
  *          sequence's is its h0.  May be h0 itself (the states then advance in
  *          place), but must not overlap it otherwise.
  *   n      number of sequences (batch without offsets)
- * dk and dv in [1, 128] (VM_ERR_UNSUPPORTED beyond).  hv % hk != 0 is
- * VM_ERR_SHAPE.  Sequences are computed in chunks of 64 steps, within which
+ * dk and dv in [1, 128], n hv up to 2^21 - 8, up to 2^23 - 1 chunks of 64 steps
+ * over all sequences, and token strides (hv dv among them) below 2^23 elements:
+ * VM_ERR_UNSUPPORTED beyond.  hv % hk != 0 is VM_ERR_SHAPE.  Sequences are computed in chunks of 64 steps, within which
  * a NaN or Inf of one token reaches the outputs of earlier tokens too.
  */
 int vm_gated_delta_fwd(const vm_delta *p, void *out, float *state, float scale,

@@ -23,6 +23,9 @@ using vmk::span;
 // Grids put chunk slots and sequences on x with up to 512 work-items each
 // (work-items below 2^32) and heads on y.
 constexpr int64_t kMaxSlots = (int64_t{1} << 23) - 1;
+// Scans put sequences, heads (whole rounds of 8) and up to 4 blocks of columns
+// on x, and the backward pass two scans.
+constexpr int64_t kMaxScans = (int64_t{1} << 21) - 8;
 constexpr int64_t kMaxHeads = 65535;
 constexpr int64_t kMaxDeltaDim = 128, kMaxNormDim = 512, kMaxGrads = 65536;
 
@@ -76,8 +79,7 @@ int check_delta(const vm_delta *p, float scale, int64_t batch, int64_t seqlen, i
   // (the kernels reach the 64 tokens of a chunk with 31-bit byte offsets)
   for (int64_t stride : {z->qs, z->ks, z->vs, hv * dv})
     if (stride * 64 * 4 >= (int64_t{1} << 31)) return VM_ERR_UNSUPPORTED;
-  // (the scans put sequences, heads and up to 2 blocks of columns on x)
-  if (n * hv > kMaxSlots || vmk::delta_slots(batch, seqlen, n, p->offsets != nullptr) > kMaxSlots)
+  if (n * hv > kMaxScans || vmk::delta_slots(batch, seqlen, n, p->offsets != nullptr) > kMaxSlots)
     return VM_ERR_UNSUPPORTED;
   return VM_OK;
 }
@@ -306,7 +308,6 @@ int vm_gated_delta_bwd(const vm_delta *p, const void *dout, const float *dstate,
   if (st != VM_OK) return st;
   st = hip_status(vmk::launch_delta_prep(a, bf16, true, s));
   if (st == VM_OK) st = hip_status(vmk::launch_delta_scan(a, bf16, true, s));
-  if (st == VM_OK) st = hip_status(vmk::launch_delta_scan_bwd(a, bf16, s));
   if (st == VM_OK) st = hip_status(vmk::launch_delta_grad(a, bf16, s));
   return st;
 }

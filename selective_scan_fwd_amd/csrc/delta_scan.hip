@@ -429,16 +429,16 @@ __device__ __forceinline__ int by_length(const DeltaArgs &A, int r) {
 struct Place {
   int s, h, cb;
 };
-__device__ __forceinline__ bool place(const DeltaArgs &A, int colblocks, Place *p) {
+__device__ __forceinline__ bool place(const DeltaArgs &A, int colblocks, int block, int blocks, Place *p) {
   int sh;
   if (A.off == nullptr) {
-    const int id = xcd_remap(blockIdx.x, gridDim.x);
+    const int id = xcd_remap(block, blocks);
     p->cb = id % colblocks;
     sh = id / colblocks;
   } else {
-    const int k = blockIdx.x / kXcd;
+    const int k = block / kXcd;
     p->cb = k % colblocks;
-    sh = k / colblocks * kXcd + blockIdx.x % kXcd;
+    sh = k / colblocks * kXcd + block % kXcd;
     if (sh >= A.nseq * A.hv) return false;      // (the grid is whole rounds of the XCDs)
   }
   p->h = sh % A.hv;
@@ -486,22 +486,43 @@ template <typename T, bool VEC> constexpr bool kDirect = VEC && sizeof(T) == 2;
 // backward one, reused twice.
 constexpr int kItemsA = 10, kItemsB = 2, kItems = kItemsA + kItemsB, kItemsBwd = 6;
 
-// Forward.  KEEP: S and V are stored for the backward pass, out and state not.
+// Where token rows of T are whole pieces (VEC), two chunks' operands.
 template <typename T, int DK, bool KEEP, bool VEC, int NP>
-__global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_kernel(DeltaArgs A, int colblocks) {
-  constexpr int kNi = kInputTerms<T>, kNs = 3, kHalf = DK / 64;
-  constexpr int kTermsP = KEEP ? 0 : delta_terms_p(kNi == 1, false);
-  constexpr int kNo = kNi == 1 ? 2 : 3;               // terms of S and V on their way to out only
-  constexpr bool kDma = kDirect<T, VEC>, kAhead = kNi == 1;
+struct Forward {
+  static constexpr int kNi = kInputTerms<T>, kTermsP = KEEP ? 0 : delta_terms_p(kNi == 1, false);
+  static constexpr bool kDma = kDirect<T, VEC>;
   typedef ChunkLoad<T, DK, kTermsT + kTermsP, !KEEP, VEC, kDma, NP> Load;
-  typedef typename Load::Lds Lds;
-  constexpr int kBuffers = kDma ? 2 : 1;
-  __shared__ struct {
-    Lds lds[kBuffers];
+  static constexpr int kBuffers = kDma ? 2 : 1;
+  struct Shared {
+    typename Load::Lds lds[kBuffers];
     __attribute__((aligned(16))) char xch[NP][kItems * 1024];
-  } sh;
+  };
+};
+template <typename T, int DK, bool VEC, int NP>
+struct Backward {
+  static constexpr int kNi = kInputTerms<T>, kTermsP = delta_terms_p(kNi == 1, true);
+  static constexpr bool kDma = kDirect<T, VEC>;
+  typedef ChunkLoad<T, DK, kTermsT + kTermsP, true, VEC, kDma, NP> Load;
+  static constexpr int kBuffers = kDma ? 2 : 1;
+  struct Shared {
+    typename Load::Lds lds[kBuffers];
+    __attribute__((aligned(16))) char xch[NP][kItemsBwd * 1024];
+  };
+};
+
+// Forward.  KEEP: S and V are stored for the backward pass, out and state not.
+// `block` of `blocks` workgroups.
+template <typename T, int DK, bool KEEP, bool VEC, int NP>
+__device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, int block, int blocks,
+                                             typename Forward<T, DK, KEEP, VEC, NP>::Shared &sh) {
+  typedef Forward<T, DK, KEEP, VEC, NP> F;
+  typedef typename F::Load Load;
+  typedef typename Load::Lds Lds;
+  constexpr int kNi = F::kNi, kNs = 3, kHalf = DK / 64, kTermsP = F::kTermsP, kBuffers = F::kBuffers;
+  constexpr int kNo = kNi == 1 ? 2 : 3;               // terms of S and V on their way to out only
+  constexpr bool kDma = F::kDma, kAhead = kNi == 1;
   Place pl;
-  if (!place(A, colblocks, &pl)) return;
+  if (!place(A, colblocks, block, blocks, &pl)) return;
   const int s = pl.s, h = pl.h;
   const Seq q = sequence(A, s);
   Load next;
@@ -653,20 +674,17 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_kernel(DeltaAr
   if (!KEEP && A.state != nullptr) store_state<DK>(A, A.state + state_at, A.dv, S, p, lg, col);
 }
 
+// Backward: the gradient of the state, from the last chunk to the first.
 template <typename T, int DK, bool VEC, int NP>
-__global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(DeltaArgs A, int colblocks) {
-  constexpr int kNi = kInputTerms<T>, kNs = 3, kHalf = DK / 64;
-  constexpr int kTermsP = delta_terms_p(kNi == 1, true);
-  constexpr bool kDma = kDirect<T, VEC>, kAhead = kNi == 1;
-  typedef ChunkLoad<T, DK, kTermsT + kTermsP, true, VEC, kDma, NP> Load;
+__device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks, int block, int blocks,
+                                              typename Backward<T, DK, VEC, NP>::Shared &sh) {
+  typedef Backward<T, DK, VEC, NP> B;
+  typedef typename B::Load Load;
   typedef typename Load::Lds Lds;
-  constexpr int kBuffers = kDma ? 2 : 1;
-  __shared__ struct {
-    Lds lds[kBuffers];
-    __attribute__((aligned(16))) char xch[NP][kItemsBwd * 1024];
-  } sh;
+  constexpr int kNi = B::kNi, kNs = 3, kHalf = DK / 64, kTermsP = B::kTermsP, kBuffers = B::kBuffers;
+  constexpr bool kDma = B::kDma, kAhead = kNi == 1;
   Place pl;
-  if (!place(A, colblocks, &pl)) return;
+  if (!place(A, colblocks, block, blocks, &pl)) return;
   const int s = pl.s, h = pl.h;
   const Seq q = sequence(A, s);
   const int64_t row = static_cast<int64_t>(A.hv) * A.dv;      // token stride of dout and dv
@@ -802,56 +820,61 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_bwd_kernel(Del
   if (A.dh0 != nullptr) store_state<DK>(A, A.dh0 + state_at, A.dv, D, p, lg, col);
 }
 
+template <typename T, int DK, bool VEC, int NP>
+__global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_kernel(DeltaArgs A, int colblocks) {
+  __shared__ typename Forward<T, DK, false, VEC, NP>::Shared sh;
+  scan_forward<T, DK, false, VEC, NP>(A, colblocks, blockIdx.x, gridDim.x, sh);
+}
+
+// The backward scan needs nothing of the forward one, so one launch runs both:
+// half of the workgroups each, the longer backward ones first.
+template <typename T, int DK, bool VEC, int NP>
+__global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scans_kernel(DeltaArgs A, int colblocks) {
+  __shared__ union {
+    typename Forward<T, DK, true, VEC, NP>::Shared f;
+    typename Backward<T, DK, VEC, NP>::Shared b;
+  } sh;
+  const int blocks = gridDim.x / 2;
+  if (blockIdx.x < blocks)
+    scan_backward<T, DK, VEC, NP>(A, colblocks, blockIdx.x, blocks, sh.b);
+  else
+    scan_forward<T, DK, true, VEC, NP>(A, colblocks, blockIdx.x - blocks, blocks, sh.f);
+}
+
 // Pairs of a workgroup: two where rows of 128 fill LDS (fp32 in terms, or two
 // buffers of bf16).
 template <int DK> constexpr int kPairs = DK == 128 ? 2 : 4;
 
 // Workgroups of a scan with cb column blocks, as place() takes them apart.
-dim3 scan_grid(const DeltaArgs &a, int cb) {
+uint32_t scan_blocks(const DeltaArgs &a, int cb) {
   int64_t heads = static_cast<int64_t>(a.nseq) * a.hv;
   if (a.off != nullptr) heads = (heads + kXcd - 1) / kXcd * kXcd;
-  return dim3(static_cast<uint32_t>(heads * cb));
+  return static_cast<uint32_t>(heads * cb);
 }
 
 template <typename T, int DK, bool VEC>
-hipError_t launch_fwd(const DeltaArgs &a, bool keep, hipStream_t s) {
+hipError_t launch(const DeltaArgs &a, bool back, hipStream_t s) {
   constexpr int NP = kPairs<DK>;
   const int cb = (a.dv + 16 * NP - 1) / (16 * NP);
-  const dim3 grid = scan_grid(a, cb), block(Shape<NP>::kThreads);
-  if (keep)
-    hipLaunchKernelGGL((delta_scan_kernel<T, DK, true, VEC, NP>), grid, block, 0, s, a, cb);
+  const dim3 block(Shape<NP>::kThreads);
+  if (back)
+    hipLaunchKernelGGL((delta_scans_kernel<T, DK, VEC, NP>), dim3(2 * scan_blocks(a, cb)), block, 0, s, a, cb);
   else
-    hipLaunchKernelGGL((delta_scan_kernel<T, DK, false, VEC, NP>), grid, block, 0, s, a, cb);
+    hipLaunchKernelGGL((delta_scan_kernel<T, DK, VEC, NP>), dim3(scan_blocks(a, cb)), block, 0, s, a, cb);
   return hipGetLastError();
 }
 template <typename T, int DK>
-hipError_t launch_fwd(const DeltaArgs &a, bool keep, hipStream_t s) {
-  return delta_vec(a, sizeof(T)) && delta_vec_values(a, a.v, a.vs, sizeof(T), 4)
-             ? launch_fwd<T, DK, true>(a, keep, s)
-             : launch_fwd<T, DK, false>(a, keep, s);
-}
-template <typename T, int DK>
-hipError_t launch_bwd(const DeltaArgs &a, hipStream_t s) {
-  constexpr int NP = kPairs<DK>;
-  const int cb = (a.dv + 16 * NP - 1) / (16 * NP);
-  const dim3 grid = scan_grid(a, cb), block(Shape<NP>::kThreads);
-  if (delta_vec(a, sizeof(T)) && delta_vec_values(a, a.dout, static_cast<int64_t>(a.hv) * a.dv, sizeof(T), 4))
-    hipLaunchKernelGGL((delta_scan_bwd_kernel<T, DK, true, NP>), grid, block, 0, s, a, cb);
-  else
-    hipLaunchKernelGGL((delta_scan_bwd_kernel<T, DK, false, NP>), grid, block, 0, s, a, cb);
-  return hipGetLastError();
+hipError_t launch(const DeltaArgs &a, bool back, hipStream_t s) {
+  const bool vec = delta_vec(a, sizeof(T)) && delta_vec_values(a, a.v, a.vs, sizeof(T), 4) &&
+                   (!back || delta_vec_values(a, a.dout, static_cast<int64_t>(a.hv) * a.dv, sizeof(T), 4));
+  return vec ? launch<T, DK, true>(a, back, s) : launch<T, DK, false>(a, back, s);
 }
 
 }  // namespace
 
-hipError_t launch_delta_scan(const DeltaArgs &a, bool bf16, bool keep, hipStream_t s) {
-  if (a.dk <= 64) return bf16 ? launch_fwd<bf16_t, 64>(a, keep, s) : launch_fwd<float, 64>(a, keep, s);
-  return bf16 ? launch_fwd<bf16_t, 128>(a, keep, s) : launch_fwd<float, 128>(a, keep, s);
-}
-
-hipError_t launch_delta_scan_bwd(const DeltaArgs &a, bool bf16, hipStream_t s) {
-  if (a.dk <= 64) return bf16 ? launch_bwd<bf16_t, 64>(a, s) : launch_bwd<float, 64>(a, s);
-  return bf16 ? launch_bwd<bf16_t, 128>(a, s) : launch_bwd<float, 128>(a, s);
+hipError_t launch_delta_scan(const DeltaArgs &a, bool bf16, bool back, hipStream_t s) {
+  if (a.dk <= 64) return bf16 ? launch<bf16_t, 64>(a, back, s) : launch<float, 64>(a, back, s);
+  return bf16 ? launch<bf16_t, 128>(a, back, s) : launch<float, 128>(a, back, s);
 }
 
 }  // namespace vmk

@@ -111,9 +111,8 @@ inline bool delta_vec_values(const DeltaArgs &a, const void *v, int64_t stride, 
 int64_t delta_slots(int64_t batch, int64_t L, int64_t n, bool packed);
 // backward: TT, PT and gam instead of P.
 hipError_t launch_delta_prep(const DeltaArgs &a, bool bf16, bool backward, hipStream_t s);
-// keep: store S and V for the backward pass instead of out and state.
-hipError_t launch_delta_scan(const DeltaArgs &a, bool bf16, bool keep, hipStream_t s);
-hipError_t launch_delta_scan_bwd(const DeltaArgs &a, bool bf16, hipStream_t s);
+// Forward: out and state; back: S and V, and dS, dR, dv and dh0.
+hipError_t launch_delta_scan(const DeltaArgs &a, bool bf16, bool back, hipStream_t s);
 hipError_t launch_delta_grad(const DeltaArgs &a, bool bf16, hipStream_t s);
 
 struct StepArgs {
