@@ -743,7 +743,7 @@ def vm_gated_delta_step(q, k, v, g, beta, state, scale=None, slots=None, out=Non
         raise ValueError("state must be a [n_slots, hv, dk, dv] tensor")
     n = state.shape[0]
     if out is None:
-        out = torch.empty((batch, hv, dv), dtype=dtype, device=q.device)
+        out = torch.empty_like(v)                # (v is dense, which the call checks)
     _launch("vm_gated_delta_step", index, _arg(q, "q", dtype, (batch, hk, dk), index),
             _arg(k, "k", dtype, (batch, hk, dk), index), _arg(v, "v", dtype, (batch, hv, dv), index),
             _arg(g, "g", torch.float32, (batch, hv), index), _arg(beta, "beta", torch.float32, (batch, hv), index),
@@ -846,7 +846,8 @@ def vm_clip_grad_norm(grads, max_norm, out=None):
     try:
         index = T.get_device(grads[0])
         sizes, types = list(map(T.numel, grads)), [x.dtype for x in grads]
-        codes = [_GRAD_CODES[x] for x in types]
+        codes = [_GRAD_CODES[types[0]]] * len(types) if types.count(types[0]) == len(types) else \
+            [_GRAD_CODES[x] for x in types]
         good = index >= 0 and set(map(T.get_device, grads)) == {index} and all(map(T.is_contiguous, grads))
         ins = list(map(T.data_ptr, grads))
         if outs is grads:
@@ -866,8 +867,9 @@ def vm_clip_grad_norm(grads, max_norm, out=None):
             if x.numel() != y.numel():
                 raise ValueError(f"out[{i}] has {y.numel()} elements, expected {x.numel()}")
     table = array.array("q", bytes(32 * len(grads)))
-    for i, column in enumerate((ins, to, sizes, codes)):       # VmGradTensor: four fields of 8 bytes
-        table[i::4] = array.array("q", column)
+    table[0::4] = first = array.array("q", ins)                # VmGradTensor: four fields of 8 bytes
+    table[1::4] = first if to is ins else array.array("q", to)
+    table[2::4], table[3::4] = array.array("q", sizes), array.array("q", codes)
     dev = grads[0].device
     norm = torch.empty((), dtype=torch.float32, device=dev)
     ws, wp, wn = _workspace(load_library().vm_clip_grad_workspace(len(grads)), dev)
