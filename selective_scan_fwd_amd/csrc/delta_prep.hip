@@ -25,7 +25,9 @@ constexpr int kThreads = 256;
 // Bound by the latency of its chain (loads, products, substitution, blocks), so
 // LDS is kept small for as many workgroups a compute unit as the registers
 // allow: forward, a wave's queries go straight to its registers, and T takes
-// the place of A.
+// the place of A.  4 x 4097 tokens, 8 and 16 heads of 128, bf16: 49 us (62 with
+// queries and T in LDS of their own) for 34 MB read and 124 MB written; 128 x 197
+// tokens, 6 heads of 64, fp32: 46 us.
 template <typename T, int DK, bool BACK, bool VEC>
 __global__ __launch_bounds__(kThreads, 4) void delta_prep_kernel(DeltaArgs A) {
   constexpr int kNi = kInputTerms<T>, kTerm = kC * DK, kPieces = DK / 8;

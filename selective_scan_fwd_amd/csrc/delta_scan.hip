@@ -23,7 +23,11 @@ namespace {
 // halves meet through LDS, as do the parts of the triangular products and the
 // corrected values.  The chain of a chunk is what bounds a long sequence; a wave
 // issues about one instruction in five cycles however idle the rest of its SIMD
-// is, so halving the instructions of the chain is worth three exchanges.
+// is, so halving the instructions of the chain is worth three exchanges: 4 x 4097
+// tokens, 16 value heads of 128, bf16, 65 chunks: 211 us (3.2 us a chunk), 281
+// with one wave to 16 columns.  Without its loads it would take 159.  (128 x 197
+// tokens, 6 heads of 64, fp32: 88 us; 40 packed sequences of up to 1500 tokens, 8
+// value heads of 100: 77 us, in the order given and in runs over the XCDs 84.)
 //
 // Rows of the state are held so that K's rows are read in whole pieces: row
 // 4 lg + r of tile 2 ks + p is state row 32 ks + 8 lg + 4 p + r.
@@ -827,7 +831,9 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_kernel(DeltaAr
 }
 
 // The backward scan needs nothing of the forward one, so one launch runs both:
-// half of the workgroups each, the longer backward ones first.
+// half of the workgroups each, the longer backward ones first.  (2 x 4097 tokens,
+// 16 value heads of 128, bf16: 290 us, one after the other 154 and 232; 64 x 197,
+// 6 heads of 64, fp32: 95, 44 and 62.)
 template <typename T, int DK, bool VEC, int NP>
 __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scans_kernel(DeltaArgs A, int colblocks) {
   __shared__ union {

@@ -6,6 +6,8 @@
 // wave takes 32 columns of one head: 8 lanes hold 4 columns each of 8 groups of
 // rows, all loads are issued before the first use, and the one reduction over
 // the row groups carries both products, since out follows from S' alone.
+// 128 sequences of 32 heads, 128 x 128 (480 MB): 102 us, 4.7 TB/s, where a copy
+// of 4 GB runs at 4.9.  One sequence of 16 heads: 4.5 us, in a call of 10.
 #include <hip/hip_runtime.h>
 
 #include "delta_device.h"
