@@ -8,7 +8,7 @@
 // copied to the device first.  Tensors are cut into chunks of 2048 elements and
 // a block takes runs of up to 8 of them, as many runs as all others, so small
 // and large tensors load the card alike and no block is left with a last round
-// of its own (207 MB of bf16: sums 55 us; with chunks of 16384 dealt out one by
+// of its own (310 MB of bf16: sums 55 us; with chunks of 16384 dealt out one by
 // one 85 us).  The second pass goes back from the last run, which is nearest
 // still, to the first: 97 us, forwards 105 us.  Its loads and stores are past
 // their last use here and marked so; without that the next pass over other
