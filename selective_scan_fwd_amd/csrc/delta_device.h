@@ -115,6 +115,20 @@ __device__ __forceinline__ bf16x8 read8(const uint16_t *p) { return *reinterpret
 __device__ __forceinline__ constexpr int tri_block(int rt, int ks) { return rt < 2 ? rt : 2 * rt - 2 + ks; }
 __device__ __forceinline__ constexpr int tri_block_t(int rt, int ks) { return rt < 2 ? 2 * rt + ks : rt + 2; }
 
+// Eight values of a triangular operand on their way to the scans (see DeltaArgs).
+template <typename T, int TERMS>
+__device__ __forceinline__ void put_block(uint16_t *m, int block, int lane, f32x4 a, f32x4 b) {
+  if constexpr (sizeof(T) == 2) {
+    const Terms<TERMS> t = split<TERMS>(a, b);
+#pragma unroll
+    for (int x = 0; x < TERMS; ++x) *reinterpret_cast<bf16x8 *>(m + x * kTriTerm + (block * 64 + lane) * 8) = t.t[x];
+  } else {
+    f32x4 *p = reinterpret_cast<f32x4 *>(m) + (block * 64 + lane) * 2;
+    p[0] = a;
+    p[1] = b;
+  }
+}
+
 // Global memory through buffer resources: 32-bit byte offsets from a base, and
 // an offset of kNowhere reads zero and writes nothing, so rows past a chunk's
 // end and columns past a head's need no branch.

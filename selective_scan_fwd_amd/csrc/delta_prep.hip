@@ -32,6 +32,7 @@ template <typename T, int DK, bool BACK, bool VEC>
 __global__ __launch_bounds__(kThreads, 4) void delta_prep_kernel(DeltaArgs A) {
   constexpr int kNi = kInputTerms<T>, kTerm = kC * DK, kPieces = DK / 8;
   constexpr int kTermsP = delta_terms_p(kNi == 1, BACK);
+  constexpr int kUnitsT = tri_units_t(kNi == 1), kUnits = kUnitsT + tri_units_p(kNi == 1, BACK);
   __shared__ __attribute__((aligned(16))) uint16_t sk[kNi * kTerm];
   __shared__ __attribute__((aligned(16))) uint16_t sq[BACK ? kNi * kTerm : 8];
   __shared__ __attribute__((aligned(16))) float sa[kC * kPitchC];  // A, later T
@@ -184,15 +185,11 @@ __global__ __launch_bounds__(kThreads, 4) void delta_prep_kernel(DeltaArgs A) {
       }
     }
     {
-      uint16_t *dst = (BACK ? A.TT : A.T) + (at * (kTermsT + kTermsP) + kTermsT) * kTriTerm;
+      uint16_t *dst = (BACK ? A.TT : A.T) + (at * kUnits + kUnitsT) * kTriTerm;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         if (BACK ? (wave >= 2 && ks == 0) : (wave < 2 && ks == 1)) continue;
-        const Terms<kTermsP> t = split<kTermsP>(pt[2 * ks], pt[2 * ks + 1]);
-        const int block = BACK ? tri_block_t(wave, ks) : tri_block(wave, ks);
-#pragma unroll
-        for (int x = 0; x < kTermsP; ++x)
-          *reinterpret_cast<bf16x8 *>(dst + x * kTriTerm + (block * 64 + lane) * 8) = t.t[x];
+        put_block<T, kTermsP>(dst, BACK ? tri_block_t(wave, ks) : tri_block(wave, ks), lane, pt[2 * ks], pt[2 * ks + 1]);
       }
     }
     __syncthreads();
@@ -232,14 +229,11 @@ __global__ __launch_bounds__(kThreads, 4) void delta_prep_kernel(DeltaArgs A) {
       }
     }
     if (BACK) {                            // the transpose from the registers
-      uint16_t *dst = A.TT + at * (kTermsT + kTermsP) * kTriTerm;
+      uint16_t *dst = A.TT + at * kUnits * kTriTerm;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         if (wave >= 2 && ks == 0) continue;
-        const Terms<kTermsT> x = split<kTermsT>(t[2 * ks], t[2 * ks + 1]);
-#pragma unroll
-        for (int y = 0; y < kTermsT; ++y)
-          *reinterpret_cast<bf16x8 *>(dst + y * kTriTerm + (tri_block_t(wave, ks) * 64 + lane) * 8) = x.t[y];
+        put_block<T, kTermsT>(dst, tri_block_t(wave, ks), lane, t[2 * ks], t[2 * ks + 1]);
       }
     }
     __syncthreads();                       // every wave has read A
@@ -249,17 +243,14 @@ __global__ __launch_bounds__(kThreads, 4) void delta_prep_kernel(DeltaArgs A) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) sa[(16 * a + 4 * lg + r) * kPitchC + 16 * wave + li] = t[a][r];
     __syncthreads();
-    uint16_t *dst = A.T + at * (kTermsT + (BACK ? 0 : kTermsP)) * kTriTerm;
+    uint16_t *dst = A.T + at * (BACK ? kUnitsT : kUnits) * kTriTerm;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       if (wave < 2 && ks == 1) continue;
       const float *row = sa + (16 * wave + li) * kPitchC + 32 * ks + 4 * lg;
       const f32x4 zero = {0, 0, 0, 0};
       const f32x4 lo = load4(row), hi = 2 * ks + 1 <= wave ? load4(row + 16) : zero;
-      const Terms<kTermsT> x = split<kTermsT>(lo, hi);
-#pragma unroll
-      for (int y = 0; y < kTermsT; ++y)
-        *reinterpret_cast<bf16x8 *>(dst + y * kTriTerm + (tri_block(wave, ks) * 64 + lane) * 8) = x.t[y];
+      put_block<T, kTermsT>(dst, tri_block(wave, ks), lane, lo, hi);
     }
   }
 }

@@ -64,9 +64,12 @@ struct ChunkLoad {
   // v to LDS: rows of an instruction with 16 or 4 bytes a lane, and instructions of a wave
   static constexpr int kRows16 = 512 / kCols, kRows4 = 128 / kCols;
   static constexpr int kV16 = kC / kRows16 / kWaves, kV4 = kC / kRows4 / kWaves;
-  static constexpr int kTri = (TRI * kTriBlocks + kWaves - 1) / kWaves;
+  // triangular operands in memory: blocks of whole terms, or of fp32 matrices
+  static constexpr bool kWhole = sizeof(T) == 4;
+  static constexpr int kBlocks = (kWhole ? TRI / 3 : TRI) * kTriBlocks, kBlockBytes = kWhole ? 2048 : 1024;
+  static constexpr int kTri = (kBlocks + kWaves - 1) / kWaves;
   Piece<T> k[DIRECT ? 1 : kPer], q[!DIRECT && WITH_Q ? kPer : 1];
-  u32x4 tri[DIRECT ? 1 : kTri];
+  u32x4 tri[DIRECT ? 1 : kTri][kWhole ? 2 : 1];
   float eg, ew, beta;
   T v[DIRECT ? 1 : 4][4];
   uint32_t ok[kPer], oq[WITH_Q ? kPer : 1], ov[DIRECT ? kV4 : 16], ob;
@@ -119,7 +122,7 @@ struct ChunkLoad {
   }
 
   // In three parts, so that the loads' issue spreads over the chunk before.
-  // tri: the triangular operands, TRI terms of each (slot, head).
+  // tri: the triangular operands of each (slot, head).
   __device__ __forceinline__ void load_v_k(const DeltaArgs &A, const Seq &s, int64_t c0, Lds &l) {
     const Window w = window(A, s, c0);
     if (w.n != n) plan(A, w);
@@ -165,16 +168,18 @@ struct ChunkLoad {
     }
   }
   __device__ __forceinline__ void load_tri(const DeltaArgs &A, const Seq &s, int64_t c0, const uint16_t *m, Lds &l) {
-    const Rsrc r = buffer(m + ((s.slot0 + c0 / kC) * A.hv + h) * (TRI * kTriTerm), TRI * kTriTerm * 2);
+    const Rsrc r = buffer(m + ((s.slot0 + c0 / kC) * A.hv + h) * (kBlocks * kBlockBytes / 2), kBlocks * kBlockBytes);
 #pragma unroll
     for (int i = 0; i < kTri; ++i) {
       // (waves with no block left read zeros past the resource's end)
       const int b = wave + i * kWaves;
       if constexpr (DIRECT) {
-        if ((i + 1) * kWaves <= TRI * kTriBlocks || b < TRI * kTriBlocks)
+        if ((i + 1) * kWaves <= kBlocks || b < kBlocks)
           to_lds16(r, l.tri + b * 512, (i * kWaves * 64 + threadIdx.x) * 16);
       } else {
-        tri[i] = bload16(r, (i * kWaves * 64 + threadIdx.x) * 16);
+#pragma unroll
+        for (int j = 0; j < (kWhole ? 2 : 1); ++j)
+          tri[i][j] = bload16(r, (i * kWaves * 64 + threadIdx.x) * (kBlockBytes / 64) + 16 * j);
       }
     }
   }
@@ -197,7 +202,15 @@ struct ChunkLoad {
 #pragma unroll
       for (int i = 0; i < kTri; ++i) {
         const int b = wave + i * kWaves;
-        if (b < TRI * kTriBlocks) *reinterpret_cast<u32x4 *>(l.tri + b * 512 + lane * 8) = tri[i];
+        if (b >= kBlocks) continue;
+        if constexpr (kWhole) {
+          const Terms<3> t = split<3>(__builtin_bit_cast(f32x4, tri[i][0]), __builtin_bit_cast(f32x4, tri[i][1]));
+          uint16_t *to = l.tri + (b / kTriBlocks * 3 * kTriBlocks + b % kTriBlocks) * 512 + lane * 8;
+#pragma unroll
+          for (int x = 0; x < 3; ++x) *reinterpret_cast<bf16x8 *>(to + x * kTriTerm) = t.t[x];
+        } else {
+          *reinterpret_cast<u32x4 *>(l.tri + b * 512 + lane * 8) = tri[i][0];
+        }
       }
       if (wave == 0) {
         l.eg[lane] = eg;

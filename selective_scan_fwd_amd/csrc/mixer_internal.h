@@ -63,12 +63,12 @@ struct DeltaArgs {
   int nseq, hk, hv, dk, dv;
   int reverse;
   float scale;
-  // Per (slot, value head), written by the preparing kernel.  The matrices are
-  // stored as bf16 terms in the order in which a wave loads them as the left
-  // operand of a matrix instruction: [term][block of 16 x 32][lane][8], the 6
-  // blocks that are not zero.
-  // T = (I + A)^-1 has kTermsT terms, the scaled masked products P of queries
-  // and keys terms_p.
+  // Per (slot, value head), written by the preparing kernel: T = (I + A)^-1 and
+  // the scaled masked products P of queries and keys, in the order in which a
+  // wave loads them as the left operand of a matrix instruction, [block of
+  // 16 x 32][lane][8], the 6 blocks that are not zero.  For bf16 tokens in bf16
+  // terms, which go to LDS as they are; for fp32 tokens in fp32, which passes
+  // through registers on its way there and is split into three terms then.
   uint16_t *T;             // forward: T, then P; backward: T
   uint16_t *TT;            // backward: the transposes of T, then of P
   float *eg, *ew;          // [64]: exp(G), exp(G_C - G) of the running log decay G
@@ -95,6 +95,9 @@ struct DeltaArgs {
 // 2.6e-6 off, with 24 bits 3e-7.)
 constexpr int kTermsT = 3;
 inline constexpr int delta_terms_p(bool bf16, bool backward) { return bf16 && !backward ? 2 : 3; }
+// What a matrix takes in memory, in units of one term.
+inline constexpr int tri_units_t(bool bf16) { return bf16 ? kTermsT : 2; }
+inline constexpr int tri_units_p(bool bf16, bool backward) { return bf16 ? delta_terms_p(true, backward) : 2; }
 constexpr int kTriBlocks = 6;
 constexpr int64_t kTriTerm = kTriBlocks * 64 * 8;   // values of one term
 // Whether every row of q and k is whole 16-byte pieces, and those of v (the
