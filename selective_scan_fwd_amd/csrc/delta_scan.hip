@@ -80,7 +80,7 @@ struct ChunkLoad {
   int64_t vstride;
 
   __device__ __forceinline__ void init(const DeltaArgs &A, int h_, int cb, const T *vb, int64_t vs) {
-    wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64) % kWaves;
     lane = threadIdx.x % 64;
     li = lane % 16;
     lg = lane / 16;
@@ -175,11 +175,11 @@ struct ChunkLoad {
       const int b = wave + i * kWaves;
       if constexpr (DIRECT) {
         if ((i + 1) * kWaves <= kBlocks || b < kBlocks)
-          to_lds16(r, l.tri + b * 512, (i * kWaves * 64 + threadIdx.x) * 16);
+          to_lds16(r, l.tri + b * 512, (b * 64 + lane) * 16);
       } else {
 #pragma unroll
         for (int j = 0; j < (kWhole ? 2 : 1); ++j)
-          tri[i][j] = bload16(r, (i * kWaves * 64 + threadIdx.x) * (kBlockBytes / 64) + 16 * j);
+          tri[i][j] = bload16(r, (b * 64 + lane) * (kBlockBytes / 64) + 16 * j);
       }
     }
   }
@@ -499,6 +499,28 @@ __device__ __forceinline__ void store_rows(const DeltaArgs &A, float *base, cons
 
 // Whether whole pieces go to LDS directly.
 template <typename T, bool VEC> constexpr bool kDirect = VEC && sizeof(T) == 2;
+// Whether as many waves again do nothing but load, a chunk ahead: where the
+// others leave half of the registers (one wave a SIMD) and nothing passes
+// through registers on its way.
+template <typename T, bool VEC, int NP> constexpr bool kLoaders = kDirect<T, VEC> && NP == 2;
+template <typename T, bool VEC, int NP>
+constexpr int kBlock = Shape<NP>::kThreads * (kLoaders<T, VEC, NP> ? 2 : 1);
+// The loading waves' part of a scan from chunk c0 on, chunks `step` apart: as many
+// barriers a chunk as the others have.
+template <typename Load, typename Lds>
+__device__ __forceinline__ void load_chunks(Load &next, const DeltaArgs &A, const Seq &q, const uint16_t *m, int64_t c0,
+                                            int64_t step, Lds (&lds)[2]) {
+  int buf = 0;
+  for (; c0 >= 0 && c0 < q.len; c0 += step) {
+    buf ^= 1;
+    const bool more = c0 + step >= 0 && c0 + step < q.len;
+    if (more) next.load(A, q, c0 + step, m, lds[buf]);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) lds_barrier();
+    if (more) next.store(lds[buf]);
+    lds_barrier();
+  }
+}
 // Exchanged items (1 KB) of a pair: forward two regions, the first reused;
 // backward one, reused twice.
 constexpr int kItemsA = 10, kItemsB = 2, kItems = kItemsA + kItemsB, kItemsBwd = 6;
@@ -537,7 +559,7 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
   typedef typename Load::Lds Lds;
   constexpr int kNi = F::kNi, kNs = 3, kHalf = DK / 64, kTermsP = F::kTermsP, kBuffers = F::kBuffers;
   constexpr int kNo = kNi == 1 ? 2 : 3;               // terms of S and V on their way to out only
-  constexpr bool kDma = F::kDma, kAhead = kNi == 1;
+  constexpr bool kDma = F::kDma, kAhead = kNi == 1, kSelf = !kLoaders<T, VEC, NP>;   // (kSelf: waves load for themselves)
   Place pl;
   if (!place(A, colblocks, block, blocks, &pl)) return;
   const int s = pl.s, h = pl.h;
@@ -549,12 +571,24 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
   const int col = next.col0 + 16 * (next.wave / 2) + li;
   const int64_t state_at = (static_cast<int64_t>(s) * A.hv + h) * A.dk * A.dv;
   const f32x4 zero = {0, 0, 0, 0};
+  if constexpr (!kSelf)
+    if (uniform(static_cast<int>(threadIdx.x / 64)) >= Shape<NP>::kWaves) {
+      if (q.len > 0) {
+        next.load(A, q, 0, A.T, sh.lds[0]);
+        next.store(sh.lds[0]);
+      }
+      __syncthreads();
+      load_chunks(next, A, q, A.T, 0, kC, sh.lds);
+      return;
+    }
   f32x4 S[DK / 32];
   load_state<DK>(A, A.h0 != nullptr ? A.h0 + state_at : nullptr, S, p, lg, col);
   RowOffsets rows;
   if (q.len > 0) {
-    next.load(A, q, 0, A.T, sh.lds[0]);
-    next.store(sh.lds[0]);
+    if (kSelf) {
+      next.load(A, q, 0, A.T, sh.lds[0]);
+      next.store(sh.lds[0]);
+    }
     if (KEEP) store_state<DK>(A, A.S + (q.slot0 * A.hv + h) * A.dk * A.dvp, A.dvp, S, p, lg, col);
   }
   __syncthreads();
@@ -576,7 +610,7 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
     const f32x4 be[2] = {load4(l.beta + 32 * p + 4 * lg), load4(l.beta + 32 * p + 16 + 4 * lg)};
     const f32x4 ew[2] = {load4(l.ew + 32 * p + 4 * lg), load4(l.ew + 32 * p + 16 + 4 * lg)};
     const float last = l.eg[kC - 1];
-    if (more) next.load_v_k(A, q, c0 + kC, ln);
+    if (kSelf && more) next.load_v_k(A, q, c0 + kC, ln);
     // K S and Q S over this half's state rows
     f32x4 xm[2], om[2];
     Blocks<kTermsT> ta, tb;
@@ -592,7 +626,7 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
         tb.read(l.tri, tri_block(2, 0), tri_block(3, 0), lane);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (!KEEP && more) next.load_q(A, q, c0 + kC, ln);
+      if (kSelf && !KEEP && more) next.load_q(A, q, c0 + kC, ln);
       halves(x, p, xm, other);
       put(xa, 2 * p, lane, other[0]);
       put(xa, 2 * p + 1, lane, other[1]);
@@ -618,7 +652,7 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
       r[i] = be[i] * (v[i] - eg[i] * (xm[i] + take(xa, 2 - 2 * p + i, lane)));
       if (!KEEP) o[i] = (om[i] + take(xa, 6 - 2 * p + i, lane)) * (eg[i] * A.scale);
     }
-    if (more) next.load_tri(A, q, c0 + kC, A.T, ln);
+    if (kSelf && more) next.load_tri(A, q, c0 + kC, A.T, ln);
     const Terms<kNs> rt = split<kNs>(r[0], r[1]);
     if (!kAhead) {
       ta.read(l.tri, tri_block(2 * p, p), tri_block(2 * p + 1, p), lane);
@@ -676,7 +710,7 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
     }
     if (kBuffers == 1) lds_barrier();
     buf = kBuffers == 2 ? buf ^ 1 : 0;
-    if (more) next.store(ln);
+    if (kSelf && more) next.store(ln);
     // (stores come after the wait for the next chunk's loads, which would
     // otherwise wait for them too)
     if constexpr (!KEEP) {
@@ -699,7 +733,7 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
   typedef typename B::Load Load;
   typedef typename Load::Lds Lds;
   constexpr int kNi = B::kNi, kNs = 3, kHalf = DK / 64, kTermsP = B::kTermsP, kBuffers = B::kBuffers;
-  constexpr bool kDma = B::kDma, kAhead = kNi == 1;
+  constexpr bool kDma = B::kDma, kAhead = kNi == 1, kSelf = !kLoaders<T, VEC, NP>;
   Place pl;
   if (!place(A, colblocks, block, blocks, &pl)) return;
   const int s = pl.s, h = pl.h;
@@ -712,13 +746,25 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
   const int col = next.col0 + 16 * (next.wave / 2) + li;
   const int64_t state_at = (static_cast<int64_t>(s) * A.hv + h) * A.dk * A.dv;
   const f32x4 zero = {0, 0, 0, 0};
+  const int64_t first = (static_cast<int64_t>(q.len + kC - 1) / kC - 1) * kC;
+  if constexpr (!kSelf)
+    if (uniform(static_cast<int>(threadIdx.x / 64)) >= Shape<NP>::kWaves) {
+      if (q.len > 0) {
+        next.load(A, q, first, A.TT, sh.lds[0]);
+        next.store(sh.lds[0]);
+      }
+      __syncthreads();
+      load_chunks(next, A, q, A.TT, first, -kC, sh.lds);
+      return;
+    }
   f32x4 D[DK / 32];
   load_state<DK>(A, A.dstate != nullptr ? A.dstate + state_at : nullptr, D, p, lg, col);
   RowOffsets rows;
-  const int64_t first = (static_cast<int64_t>(q.len + kC - 1) / kC - 1) * kC;
   if (q.len > 0) {
-    next.load(A, q, first, A.TT, sh.lds[0]);
-    next.store(sh.lds[0]);
+    if (kSelf) {
+      next.load(A, q, first, A.TT, sh.lds[0]);
+      next.store(sh.lds[0]);
+    }
     store_state<DK>(A, A.dS + ((q.slot0 + first / kC) * A.hv + h) * A.dk * A.dvp, A.dvp, D, p, lg, col);
   }
   __syncthreads();
@@ -744,7 +790,7 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
     const f32x4 be[2] = {load4(l.beta + 32 * p + 4 * lg), load4(l.beta + 32 * p + 16 + 4 * lg)};
     const f32x4 ew[2] = {load4(l.ew + 32 * p + 4 * lg), load4(l.ew + 32 * p + 16 + 4 * lg)};
     const float last = l.eg[kC - 1];
-    if (more) next.load_v_k(A, q, c0 - kC, ln);
+    if (kSelf && more) next.load_v_k(A, q, c0 - kC, ln);
     f32x4 xm[2];
     Blocks<kTermsT> ta, tb;
     {
@@ -761,7 +807,7 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
         if (p == 0) pb.read(tp, tri_block_t(0, 0), tri_block_t(1, 0), lane);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (more) next.load_q(A, q, c0 - kC, ln);
+      if (kSelf && more) next.load_q(A, q, c0 - kC, ln);
       halves(x, p, xm, other);
       put(xa, 2 * p, lane, other[0]);
       put(xa, 2 * p + 1, lane, other[1]);
@@ -770,7 +816,7 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
     f32x4 V[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) V[i] = (xm[i] + take(xa, 2 - 2 * p + i, lane)) * ew[i];
-    if (more) next.load_tri(A, q, c0 - kC, A.TT, ln);
+    if (kSelf && more) next.load_tri(A, q, c0 - kC, A.TT, ln);
     if (!kAhead) {
       pa.read(tp, tri_block_t(2 * p, 1), tri_block_t(2 * p + 1, 1), lane);
       pb.read(tp, tri_block_t(0, 0), tri_block_t(1, 0), lane);
@@ -827,7 +873,7 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
     kc.template times<kNi>(l.k, xw, p, li, lg, D);
     if (kBuffers == 1) lds_barrier();
     buf = kBuffers == 2 ? buf ^ 1 : 0;
-    if (more) next.store(ln);
+    if (kSelf && more) next.store(ln);
     store_rows(A, A.dR + at * kC * A.dvp, R, p, lg, col);
     if (more) store_state<DK>(A, A.dS + (at - A.hv) * A.dk * A.dvp, A.dvp, D, p, lg, col);
     rows.plan(A, w, row * sizeof(T), sizeof(T), p, lg, col);
@@ -838,7 +884,7 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
 }
 
 template <typename T, int DK, bool VEC, int NP>
-__global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_kernel(DeltaArgs A, int colblocks) {
+__global__ __launch_bounds__((kBlock<T, VEC, NP>)) void delta_scan_kernel(DeltaArgs A, int colblocks) {
   __shared__ typename Forward<T, DK, false, VEC, NP>::Shared sh;
   scan_forward<T, DK, false, VEC, NP>(A, colblocks, blockIdx.x, gridDim.x, sh);
 }
@@ -848,7 +894,7 @@ __global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scan_kernel(DeltaAr
 // 16 value heads of 128, bf16: 290 us, one after the other 154 and 232; 64 x 197,
 // 6 heads of 64, fp32: 95, 44 and 62.)
 template <typename T, int DK, bool VEC, int NP>
-__global__ __launch_bounds__(Shape<NP>::kThreads) void delta_scans_kernel(DeltaArgs A, int colblocks) {
+__global__ __launch_bounds__((kBlock<T, VEC, NP>)) void delta_scans_kernel(DeltaArgs A, int colblocks) {
   __shared__ union {
     typename Forward<T, DK, true, VEC, NP>::Shared f;
     typename Backward<T, DK, VEC, NP>::Shared b;
@@ -875,7 +921,7 @@ template <typename T, int DK, bool VEC>
 hipError_t launch(const DeltaArgs &a, bool back, hipStream_t s) {
   constexpr int NP = kPairs<DK>;
   const int cb = (a.dv + 16 * NP - 1) / (16 * NP);
-  const dim3 block(Shape<NP>::kThreads);
+  const dim3 block(kBlock<T, VEC, NP>);
   if (back)
     hipLaunchKernelGGL((delta_scans_kernel<T, DK, VEC, NP>), dim3(2 * scan_blocks(a, cb)), block, 0, s, a, cb);
   else
