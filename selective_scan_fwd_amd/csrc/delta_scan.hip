@@ -671,6 +671,8 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
       pa.read(l.tri + kTermsT * kTriTerm, tri_block(2 * p, p), tri_block(2 * p + 1, p), lane);
       pb.read(l.tri + kTermsT * kTriTerm, tri_block(2, 0), tri_block(3, 0), lane);
     }
+    ColumnTiles<DK> kc;
+    if (!kSelf) kc.read(l.k, p, li, lg);
     lds_barrier();
     if (p == 1) {
       V[0] += take(xb, 0, lane);
@@ -686,10 +688,9 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
     }
 #pragma unroll
     for (int d = 0; d < DK / 32; ++d) S[d] *= last;
-    ColumnTiles<DK> kc;
-    if (kDma)
+    if (kDma && kSelf)
       kc.read_past_loads(l.k, p, li, lg);
-    else
+    else if (kSelf)
       kc.read(l.k, p, li, lg);
     lds_barrier();
     if (p == 0) {
@@ -837,7 +838,7 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
     }
     ta.times(vt, R);
     ColumnTiles<DK> qc, kc;
-    if (kDma)
+    if (kDma && kSelf)
       qc.read_past_loads(l.q, p, li, lg);
     else
       qc.read(l.q, p, li, lg);
@@ -858,7 +859,7 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
       ow[i] = split<kNs>(o[2 * i] * (load4(l.eg + 32 * i + 4 * lg) * A.scale),
                          o[2 * i + 1] * (load4(l.eg + 32 * i + 16 + 4 * lg) * A.scale));
     qc.template times<kNi>(l.q, ow, p, li, lg, D);
-    if (kDma)
+    if (kDma && kSelf)
       kc.read_past_loads(l.k, p, li, lg);
     else
       kc.read(l.k, p, li, lg);
