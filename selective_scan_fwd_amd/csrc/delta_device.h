@@ -170,8 +170,13 @@ __device__ __forceinline__ void to_lds4(Rsrc r, void *lds, uint32_t off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 4,
                                            static_cast<int>(off), 0, 0, 0);
 }
-// Waits for this wave's loads to LDS; other waves' follow with the barrier.
-__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+// Waits until no more than the last LEFT of this wave's loads (to LDS) are under
+// way; other waves' follow with the barrier.
+template <int LEFT = 0>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(LEFT < 64, "six bits, the upper two apart");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (LEFT & 15) | (LEFT >> 4) << 14);
+}
 
 // Eight values of a token row, as they are in memory.
 template <typename T> struct Piece;

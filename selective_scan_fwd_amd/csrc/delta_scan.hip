@@ -78,6 +78,7 @@ struct ChunkLoad {
   bool v16;                                 // DIRECT: v in pieces of 16 bytes, else of 4
   const T *vbase;
   int64_t vstride;
+  int64_t low, at;                          // of the chunk aimed at: lowest token, (slot, head)
 
   __device__ __forceinline__ void init(const DeltaArgs &A, int h_, int cb, const T *vb, int64_t vs) {
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64) % kWaves;
@@ -121,15 +122,15 @@ struct ChunkLoad {
     }
   }
 
-  // In three parts, so that the loads' issue spreads over the chunk before.
-  // tri: the triangular operands of each (slot, head).
-  __device__ __forceinline__ void load_v_k(const DeltaArgs &A, const Seq &s, int64_t c0, Lds &l) {
+  // Takes aim at chunk c0, whose parts are then loaded one by one.
+  __device__ __forceinline__ void aim(const DeltaArgs &A, const Seq &s, int64_t c0) {
     const Window w = window(A, s, c0);
     if (w.n != n) plan(A, w);
-    const int64_t at = (s.slot0 + c0 / kC) * A.hv + h;
-    const Rsrc rk = buffer(static_cast<const T *>(A.k) + w.low * A.ks + static_cast<int64_t>(kh) * A.dk);
-    const Rsrc reg = buffer(A.eg + at * kC), rew = buffer(A.ew + at * kC), rbeta = buffer(A.beta + w.low * A.hv + h);
-    const Rsrc rv = buffer(vbase + w.low * vstride);
+    low = w.low;
+    at = (s.slot0 + c0 / kC) * A.hv + h;
+  }
+  __device__ __forceinline__ void load_v(Lds &l) {
+    const Rsrc rv = buffer(vbase + low * vstride);
     if constexpr (DIRECT) {
       if (v16) {
 #pragma unroll
@@ -138,6 +139,14 @@ struct ChunkLoad {
 #pragma unroll
         for (int i = 0; i < kV4; ++i) to_lds4(rv, l.v + (i * kWaves + wave) * 128, ov[i]);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i / 4][i % 4] = bload<T>(rv, ov[i]);
+    }
+  }
+  __device__ __forceinline__ void load_gates(const DeltaArgs &A, Lds &l) {
+    const Rsrc reg = buffer(A.eg + at * kC), rew = buffer(A.ew + at * kC), rbeta = buffer(A.beta + low * A.hv + h);
+    if constexpr (DIRECT) {
       if (wave == 0) to_lds4(reg, l.eg, lane * 4);
       if (wave == 1) to_lds4(rew, l.ew, lane * 4);
       if (wave == 2) to_lds4(rbeta, l.beta, ob);
@@ -145,9 +154,10 @@ struct ChunkLoad {
       eg = bload<float>(reg, lane * 4);
       ew = bload<float>(rew, lane * 4);
       beta = bload<float>(rbeta, ob);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i / 4][i % 4] = bload<T>(rv, ov[i]);
     }
+  }
+  __device__ __forceinline__ void load_k(const DeltaArgs &A, Lds &l) {
+    const Rsrc rk = buffer(static_cast<const T *>(A.k) + low * A.ks + static_cast<int64_t>(kh) * A.dk);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       if constexpr (DIRECT)
@@ -156,21 +166,24 @@ struct ChunkLoad {
         k[i] = load_piece<VEC>(rk, ok[i], 8 * (((i * kWaves + wave) * 64 + lane) % kPieces), A.dk, T());
     }
   }
-  __device__ __forceinline__ void load_q(const DeltaArgs &A, const Seq &s, int64_t c0, Lds &l) {
-    const Window w = window(A, s, c0);
-    const Rsrc rq = buffer(static_cast<const T *>(A.q) + w.low * A.qs + static_cast<int64_t>(kh) * A.dk);
+  __device__ __forceinline__ void load_q(const DeltaArgs &A, Lds &l) {
+    if constexpr (WITH_Q) {
+      const Rsrc rq = buffer(static_cast<const T *>(A.q) + low * A.qs + static_cast<int64_t>(kh) * A.dk);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if constexpr (DIRECT)
-        to_lds16(rq, l.q + (i * kWaves + wave) * 512, oq[i]);
-      else
-        q[i] = load_piece<VEC>(rq, oq[i], 8 * (((i * kWaves + wave) * 64 + lane) % kPieces), A.dk, T());
+      for (int i = 0; i < kPer; ++i) {
+        if constexpr (DIRECT)
+          to_lds16(rq, l.q + (i * kWaves + wave) * 512, oq[i]);
+        else
+          q[i] = load_piece<VEC>(rq, oq[i], 8 * (((i * kWaves + wave) * 64 + lane) % kPieces), A.dk, T());
+      }
     }
   }
-  __device__ __forceinline__ void load_tri(const DeltaArgs &A, const Seq &s, int64_t c0, const uint16_t *m, Lds &l) {
-    const Rsrc r = buffer(m + ((s.slot0 + c0 / kC) * A.hv + h) * (kBlocks * kBlockBytes / 2), kBlocks * kBlockBytes);
+  // the triangular operands of the chunk and head
+  __device__ __forceinline__ void load_tri(const uint16_t *m, Lds &l, int from = 0, int to = kTri) {
+    const Rsrc r = buffer(m + at * (kBlocks * kBlockBytes / 2), kBlocks * kBlockBytes);
 #pragma unroll
     for (int i = 0; i < kTri; ++i) {
+      if (i < from || i >= to) continue;
       // (waves with no block left read zeros past the resource's end)
       const int b = wave + i * kWaves;
       if constexpr (DIRECT) {
@@ -184,10 +197,15 @@ struct ChunkLoad {
     }
   }
   __device__ __forceinline__ void load(const DeltaArgs &A, const Seq &s, int64_t c0, const uint16_t *m, Lds &l) {
-    load_v_k(A, s, c0, l);
-    if (WITH_Q) load_q(A, s, c0, l);
-    load_tri(A, s, c0, m, l);
+    aim(A, s, c0);
+    load_v(l);
+    load_gates(A, l);
+    load_k(A, l);
+    load_q(A, l);
+    load_tri(m, l);
   }
+  // Loads that every wave issues for a chunk, at least (DIRECT).
+  static constexpr int kLeast = kV16 + kPer * (WITH_Q ? 2 : 1) + kBlocks / kWaves;
 
   __device__ __forceinline__ void store(Lds &l) const {
     if constexpr (DIRECT) {
@@ -506,19 +524,62 @@ template <typename T, bool VEC, int NP> constexpr bool kLoaders = kDirect<T, VEC
 template <typename T, bool VEC, int NP>
 constexpr int kBlock = Shape<NP>::kThreads * (kLoaders<T, VEC, NP> ? 2 : 1);
 // The loading waves' part of a scan from chunk c0 on, chunks `step` apart: as many
-// barriers a chunk as the others have.
-template <typename Load, typename Lds>
+// barriers a chunk as the others have.  A buffer's parts are loaded again, for
+// the chunk after next, once the others have them in registers, some between
+// any two barriers (issuing loads takes its time too, and the others wait at the
+// barriers): BACK, the triangles and dout after the first barrier, Q after the
+// second, K and the gates after the third; forward v, Q and the gates after the
+// first, K and the triangles after the second.  Loads return in order: what the
+// next chunk needs has come when no more are out than were issued since.
+template <bool BACK, typename Load, typename Lds>
 __device__ __forceinline__ void load_chunks(Load &next, const DeltaArgs &A, const Seq &q, const uint16_t *m, int64_t c0,
                                             int64_t step, Lds (&lds)[2]) {
+  constexpr int kTri = Load::kTri;
+  const auto in = [&](int64_t c) { return c >= 0 && c < q.len; };
+  if (in(c0)) next.load(A, q, c0, m, lds[0]);
+  if (in(c0 + step)) next.load(A, q, c0 + step, m, lds[1]);
+  wait_loads();
+  __syncthreads();
   int buf = 0;
-  for (; c0 >= 0 && c0 < q.len; c0 += step) {
-    buf ^= 1;
-    const bool more = c0 + step >= 0 && c0 + step < q.len;
-    if (more) next.load(A, q, c0 + step, m, lds[buf]);
-#pragma unroll
-    for (int i = 0; i < 3; ++i) lds_barrier();
-    if (more) next.store(lds[buf]);
+  for (; in(c0); c0 += step) {
+    const bool more = in(c0 + 2 * step);
+    Lds &l = lds[buf];
+    if (more) next.aim(A, q, c0 + 2 * step);
     lds_barrier();
+    if (more) {
+      next.load_v(l);
+      if (BACK) {
+        next.load_tri(m, l, 0, kTri / 2);
+      } else {
+        next.load_gates(A, l);
+        next.load_q(A, l);
+      }
+    }
+    lds_barrier();
+    if (more) {
+      if (BACK) {
+        next.load_q(A, l);
+        next.load_tri(m, l, kTri / 2, kTri / 2 + 2);
+      } else {
+        next.load_k(A, l);
+        next.load_tri(m, l, 0, 2);
+      }
+    }
+    lds_barrier();
+    if (more) {
+      if (BACK) {
+        next.load_tri(m, l, kTri / 2 + 2, kTri);
+        next.load_k(A, l);
+        next.load_gates(A, l);
+      } else {
+        next.load_tri(m, l, 2, kTri);
+      }
+      wait_loads<Load::kLeast>();
+    } else {
+      wait_loads();
+    }
+    lds_barrier();
+    buf ^= 1;
   }
 }
 // Exchanged items (1 KB) of a pair: forward two regions, the first reused;
@@ -573,12 +634,7 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
   const f32x4 zero = {0, 0, 0, 0};
   if constexpr (!kSelf)
     if (uniform(static_cast<int>(threadIdx.x / 64)) >= Shape<NP>::kWaves) {
-      if (q.len > 0) {
-        next.load(A, q, 0, A.T, sh.lds[0]);
-        next.store(sh.lds[0]);
-      }
-      __syncthreads();
-      load_chunks(next, A, q, A.T, 0, kC, sh.lds);
+      load_chunks<false>(next, A, q, A.T, 0, kC, sh.lds);
       return;
     }
   f32x4 S[DK / 32];
@@ -610,7 +666,12 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
     const f32x4 be[2] = {load4(l.beta + 32 * p + 4 * lg), load4(l.beta + 32 * p + 16 + 4 * lg)};
     const f32x4 ew[2] = {load4(l.ew + 32 * p + 4 * lg), load4(l.ew + 32 * p + 16 + 4 * lg)};
     const float last = l.eg[kC - 1];
-    if (kSelf && more) next.load_v_k(A, q, c0 + kC, ln);
+    if (kSelf && more) {                    // (the loads' issue spreads over the chunk)
+      next.aim(A, q, c0 + kC);
+      next.load_v(ln);
+      next.load_gates(A, ln);
+      next.load_k(A, ln);
+    }
     // K S and Q S over this half's state rows
     f32x4 xm[2], om[2];
     Blocks<kTermsT> ta, tb;
@@ -626,7 +687,7 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
         tb.read(l.tri, tri_block(2, 0), tri_block(3, 0), lane);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (kSelf && !KEEP && more) next.load_q(A, q, c0 + kC, ln);
+      if (kSelf && !KEEP && more) next.load_q(A, ln);
       halves(x, p, xm, other);
       put(xa, 2 * p, lane, other[0]);
       put(xa, 2 * p + 1, lane, other[1]);
@@ -652,7 +713,7 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
       r[i] = be[i] * (v[i] - eg[i] * (xm[i] + take(xa, 2 - 2 * p + i, lane)));
       if (!KEEP) o[i] = (om[i] + take(xa, 6 - 2 * p + i, lane)) * (eg[i] * A.scale);
     }
-    if (kSelf && more) next.load_tri(A, q, c0 + kC, A.T, ln);
+    if (kSelf && more) next.load_tri(A.T, ln);
     const Terms<kNs> rt = split<kNs>(r[0], r[1]);
     if (!kAhead) {
       ta.read(l.tri, tri_block(2 * p, p), tri_block(2 * p + 1, p), lane);
@@ -750,12 +811,7 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
   const int64_t first = (static_cast<int64_t>(q.len + kC - 1) / kC - 1) * kC;
   if constexpr (!kSelf)
     if (uniform(static_cast<int>(threadIdx.x / 64)) >= Shape<NP>::kWaves) {
-      if (q.len > 0) {
-        next.load(A, q, first, A.TT, sh.lds[0]);
-        next.store(sh.lds[0]);
-      }
-      __syncthreads();
-      load_chunks(next, A, q, A.TT, first, -kC, sh.lds);
+      load_chunks<true>(next, A, q, A.TT, first, -kC, sh.lds);
       return;
     }
   f32x4 D[DK / 32];
@@ -791,7 +847,12 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
     const f32x4 be[2] = {load4(l.beta + 32 * p + 4 * lg), load4(l.beta + 32 * p + 16 + 4 * lg)};
     const f32x4 ew[2] = {load4(l.ew + 32 * p + 4 * lg), load4(l.ew + 32 * p + 16 + 4 * lg)};
     const float last = l.eg[kC - 1];
-    if (kSelf && more) next.load_v_k(A, q, c0 - kC, ln);
+    if (kSelf && more) {
+      next.aim(A, q, c0 - kC);
+      next.load_v(ln);
+      next.load_gates(A, ln);
+      next.load_k(A, ln);
+    }
     f32x4 xm[2];
     Blocks<kTermsT> ta, tb;
     {
@@ -808,7 +869,7 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
         if (p == 0) pb.read(tp, tri_block_t(0, 0), tri_block_t(1, 0), lane);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (kSelf && more) next.load_q(A, q, c0 - kC, ln);
+      if (kSelf && more) next.load_q(A, ln);
       halves(x, p, xm, other);
       put(xa, 2 * p, lane, other[0]);
       put(xa, 2 * p + 1, lane, other[1]);
@@ -817,7 +878,7 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
     f32x4 V[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) V[i] = (xm[i] + take(xa, 2 - 2 * p + i, lane)) * ew[i];
-    if (kSelf && more) next.load_tri(A, q, c0 - kC, A.TT, ln);
+    if (kSelf && more) next.load_tri(A.TT, ln);
     if (!kAhead) {
       pa.read(tp, tri_block_t(2 * p, 1), tri_block_t(2 * p + 1, 1), lane);
       pb.read(tp, tri_block_t(0, 0), tri_block_t(1, 0), lane);
