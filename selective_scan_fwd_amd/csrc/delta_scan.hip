@@ -24,10 +24,12 @@ namespace {
 // corrected values.  The chain of a chunk is what bounds a long sequence; a wave
 // issues about one instruction in five cycles however idle the rest of its SIMD
 // is, so halving the instructions of the chain is worth three exchanges: 4 x 4097
-// tokens, 16 value heads of 128, bf16, 65 chunks: 211 us (3.2 us a chunk), 281
-// with one wave to 16 columns.  Without its loads it would take 159.  (128 x 197
-// tokens, 6 heads of 64, fp32: 88 us; 40 packed sequences of up to 1500 tokens, 8
-// value heads of 100: 77 us, in the order given and in runs over the XCDs 84.)
+// tokens, 16 value heads of 128, bf16, 65 chunks: 211 us where one wave to 16
+// columns took 281, and 183 (2.8 us a chunk) with waves of their own for the
+// loads, see load_chunks(); with nothing loaded after the first chunk it would
+// take 163.  (128 x 197 tokens, 6 heads of 64, fp32: 88 us; 40 packed sequences
+// of up to 1500 tokens, 8 value heads of 100: 77 us, in the order given and in
+// runs over the XCDs 84.)
 //
 // Rows of the state are held so that K's rows are read in whole pieces: row
 // 4 lg + r of tile 2 ks + p is state row 32 ks + 8 lg + 4 p + r.
@@ -204,8 +206,8 @@ struct ChunkLoad {
     load_q(A, l);
     load_tri(m, l);
   }
-  // Loads that every wave issues for a chunk, at least (DIRECT).
-  static constexpr int kLeast = kV16 + kPer * (WITH_Q ? 2 : 1) + kBlocks / kWaves;
+  // Loads that every wave issues for a chunk besides the triangles', at least (DIRECT).
+  static constexpr int kLeast = kV16 + kPer * (WITH_Q ? 2 : 1);
 
   __device__ __forceinline__ void store(Lds &l) const {
     if constexpr (DIRECT) {
@@ -517,9 +519,9 @@ __device__ __forceinline__ void store_rows(const DeltaArgs &A, float *base, cons
 
 // Whether whole pieces go to LDS directly.
 template <typename T, bool VEC> constexpr bool kDirect = VEC && sizeof(T) == 2;
-// Whether as many waves again do nothing but load, a chunk ahead: where the
-// others leave half of the registers (one wave a SIMD) and nothing passes
-// through registers on its way.
+// Whether as many waves again do nothing but load: where the others leave half
+// of the registers (one wave a SIMD) and nothing has to pass through registers
+// on its way (which it might: 250 us instead of 183).
 template <typename T, bool VEC, int NP> constexpr bool kLoaders = kDirect<T, VEC> && NP == 2;
 template <typename T, bool VEC, int NP>
 constexpr int kBlock = Shape<NP>::kThreads * (kLoaders<T, VEC, NP> ? 2 : 1);
@@ -529,27 +531,31 @@ constexpr int kBlock = Shape<NP>::kThreads * (kLoaders<T, VEC, NP> ? 2 : 1);
 // any two barriers (issuing loads takes its time too, and the others wait at the
 // barriers): BACK, the triangles and dout after the first barrier, Q after the
 // second, K and the gates after the third; forward v, Q and the gates after the
-// first, K and the triangles after the second.  Loads return in order: what the
-// next chunk needs has come when no more are out than were issued since.
+// first, K and the triangles after the second; what is left of the triangles
+// (blocks from kEnd on) at the start of the next chunk.  Loads return in order:
+// what the next chunk needs has come when no more are out than were issued since.
 template <bool BACK, typename Load, typename Lds>
 __device__ __forceinline__ void load_chunks(Load &next, const DeltaArgs &A, const Seq &q, const uint16_t *m, int64_t c0,
                                             int64_t step, Lds (&lds)[2]) {
-  constexpr int kTri = Load::kTri;
+  constexpr int kTri = Load::kTri, kEnd = BACK ? 4 : (kTri + 1) / 2;
+  static_assert(kEnd <= Load::kBlocks / Load::kWaves, "every wave issues the triangles' first kEnd loads");
   const auto in = [&](int64_t c) { return c >= 0 && c < q.len; };
   if (in(c0)) next.load(A, q, c0, m, lds[0]);
   if (in(c0 + step)) next.load(A, q, c0 + step, m, lds[1]);
   wait_loads();
   __syncthreads();
   int buf = 0;
+  bool rest = false;                       // of the next chunk's triangles, aimed at still
   for (; in(c0); c0 += step) {
     const bool more = in(c0 + 2 * step);
     Lds &l = lds[buf];
+    if (rest) next.load_tri(m, lds[buf ^ 1], kEnd, kTri);
     if (more) next.aim(A, q, c0 + 2 * step);
     lds_barrier();
     if (more) {
       next.load_v(l);
       if (BACK) {
-        next.load_tri(m, l, 0, kTri / 2);
+        next.load_tri(m, l, 0, 3);
       } else {
         next.load_gates(A, l);
         next.load_q(A, l);
@@ -559,25 +565,25 @@ __device__ __forceinline__ void load_chunks(Load &next, const DeltaArgs &A, cons
     if (more) {
       if (BACK) {
         next.load_q(A, l);
-        next.load_tri(m, l, kTri / 2, kTri / 2 + 2);
+        next.load_tri(m, l, 3, kEnd);
       } else {
         next.load_k(A, l);
-        next.load_tri(m, l, 0, 2);
+        next.load_tri(m, l, 0, 1);
       }
     }
     lds_barrier();
     if (more) {
       if (BACK) {
-        next.load_tri(m, l, kTri / 2 + 2, kTri);
         next.load_k(A, l);
         next.load_gates(A, l);
       } else {
-        next.load_tri(m, l, 2, kTri);
+        next.load_tri(m, l, 1, kEnd);
       }
-      wait_loads<Load::kLeast>();
+      wait_loads<Load::kLeast + kEnd>();
     } else {
       wait_loads();
     }
+    rest = more;
     lds_barrier();
     buf ^= 1;
   }
@@ -953,8 +959,8 @@ __global__ __launch_bounds__((kBlock<T, VEC, NP>)) void delta_scan_kernel(DeltaA
 
 // The backward scan needs nothing of the forward one, so one launch runs both:
 // half of the workgroups each, the longer backward ones first.  (2 x 4097 tokens,
-// 16 value heads of 128, bf16: 290 us, one after the other 154 and 232; 64 x 197,
-// 6 heads of 64, fp32: 95, 44 and 62.)
+// 16 value heads of 128, bf16: 290 us, one after the other 154 and 232, and 228
+// with loading waves; 64 x 197, 6 heads of 64, fp32: 95, 44 and 62.)
 template <typename T, int DK, bool VEC, int NP>
 __global__ __launch_bounds__((kBlock<T, VEC, NP>)) void delta_scans_kernel(DeltaArgs A, int colblocks) {
   __shared__ union {
