@@ -9,7 +9,6 @@
 namespace vmk {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kC = kDeltaChunk;
 // Row pitch in floats of a [64][64] tile in LDS: 4 past a multiple of 64 banks,
@@ -221,7 +220,7 @@ __device__ __forceinline__ Piece<float> load_piece(Rsrc r, uint32_t at, int c, i
 }
 // Into rows of bf16 terms, `term` values apart.
 template <int COLS>
-__device__ __forceinline__ void store_piece(uint16_t *m, int term, int row, int piece, const Piece<bf16_t> &p) {
+__device__ __forceinline__ void store_piece(uint16_t *m, int /*term*/, int row, int piece, const Piece<bf16_t> &p) {
   *reinterpret_cast<u32x4 *>(m + swizzled<COLS>(row, piece)) = p.x;
 }
 template <int COLS>
@@ -311,9 +310,5 @@ __device__ __forceinline__ Window window(const DeltaArgs &A, const Seq &q, int64
 }
 
 __device__ __forceinline__ f32x4 load4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
-__device__ __forceinline__ f32x4 load4(const bf16_t *p) {
-  const u16x4 r = *reinterpret_cast<const u16x4 *>(p);
-  return f32x4{to_f32(r[0]), to_f32(r[1]), to_f32(r[2]), to_f32(r[3])};
-}
 
 }  // namespace vmk

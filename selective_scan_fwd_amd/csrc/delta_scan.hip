@@ -449,7 +449,7 @@ __device__ __forceinline__ void lds_barrier() {
 // lengths need not make sense: any values have an order).
 __device__ __forceinline__ int by_length(const DeltaArgs &A, int r) {
   const int lane = threadIdx.x & 63, n = A.nseq;
-  const int len = lane < n ? A.off[lane + 1] - A.off[lane] : 0;
+  const int len = lane < n ? static_cast<int>(static_cast<uint32_t>(A.off[lane + 1]) - static_cast<uint32_t>(A.off[lane])) : 0;
   int before = 0;
   for (int j = 0; j < n; ++j) {
     const int other = __builtin_amdgcn_readlane(len, j);
@@ -967,11 +967,11 @@ __global__ __launch_bounds__((kBlock<T, VEC, NP>)) void delta_scans_kernel(Delta
     typename Forward<T, DK, true, VEC, NP>::Shared f;
     typename Backward<T, DK, VEC, NP>::Shared b;
   } sh;
-  const int blocks = gridDim.x / 2;
-  if (blockIdx.x < blocks)
-    scan_backward<T, DK, VEC, NP>(A, colblocks, blockIdx.x, blocks, sh.b);
+  const int blocks = gridDim.x / 2, block = blockIdx.x;
+  if (block < blocks)
+    scan_backward<T, DK, VEC, NP>(A, colblocks, block, blocks, sh.b);
   else
-    scan_forward<T, DK, true, VEC, NP>(A, colblocks, blockIdx.x - blocks, blocks, sh.f);
+    scan_forward<T, DK, true, VEC, NP>(A, colblocks, block - blocks, blocks, sh.f);
 }
 
 // Pairs of a workgroup: two where rows of 128 fill LDS (fp32 in terms, or two

@@ -311,7 +311,7 @@ int head_splits(const NormArgs &a) {
 
 }  // namespace
 
-int norm_blocks(const NormArgs &a, bool bf16, bool back) {
+int norm_blocks(const NormArgs &a, bool back) {
   const int groups = kThreads / lanes_per_head(a.dim);
   const int64_t items = a.tokens * head_splits(a);
   const int64_t blocks = (items + groups - 1) / groups;
@@ -321,7 +321,7 @@ int norm_blocks(const NormArgs &a, bool bf16, bool back) {
 
 hipError_t launch_norm(NormArgs a, bool bf16, bool back, hipStream_t s) {
   a.splits = head_splits(a);
-  const int blocks = norm_blocks(a, bf16, back);
+  const int blocks = norm_blocks(a, back);
   // whole pieces of 4 values, 4 values aligned
   const int64_t piece = bf16 ? 8 : 16;
   bool vec = a.dim % 8 == 0 && a.rot % 8 == 0 && aligned(a.cos, 16) && aligned(a.sin, 16);

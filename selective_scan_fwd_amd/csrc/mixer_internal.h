@@ -30,7 +30,7 @@ struct NormArgs {
 };
 constexpr int kNormMaxBlocks = 1024;
 // Blocks of the launch (the number of partial sums of the backward pass).
-int norm_blocks(const NormArgs &a, bool bf16, bool back);
+int norm_blocks(const NormArgs &a, bool back);
 hipError_t launch_norm(NormArgs a, bool bf16, bool back, hipStream_t s);
 
 // ------------------------------------------------------------- clipping

@@ -150,6 +150,48 @@ def test_delta_packed_sequences(lens, reverse, dtype):
         close(d[m], rd[m], "d" + m)
 
 
+# rows of up to 128 in bf16 are loaded by waves of their own, two chunks ahead: one to
+# seven chunks, whole and ragged ends, values in pieces of 16 and of 4 bytes
+@pytest.mark.parametrize("size", [(1, 449, 1, 2, 128, 128), (2, 321, 2, 2, 96, 36), (1, 128, 1, 1, 72, 8), (3, 192, 1, 1, 128, 62)])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_delta_wide_keys_over_many_chunks(size, reverse):
+    _case(f"delta wide keys {size} reverse {reverse}")
+    b, l, hk, hv, dk, dv = size
+    x, g = delta_inputs(41, *size, BF16, decay=0.05)
+    rn = lambda *s: torch.randn(s, generator=g, device=DEV)
+    h0, dstate, dout = rn(b, hv, dk, dv), rn(b, hv, dk, dv), rn(b, l, hv, dv).to(BF16)
+    ref_in = {m: host(t) for m, t in x.items()}
+    out, state = vm.vm_gated_delta_fwd(**x, scale=0.3, h0=h0, want_state=True, reverse=reverse)
+    ro, rs, _ = mixers.delta(**ref_in, scale=0.3, h0=host(h0), reverse=reverse)
+    close(out, ro, "out")
+    close(state, rs, "state")
+    d = vm.vm_gated_delta_bwd(**x, dout=dout, scale=0.3, h0=h0, dstate=dstate, reverse=reverse)
+    rd = mixers.delta_grad(**ref_in, scale=0.3, dout=host(dout), h0=host(h0), dstate=host(dstate), reverse=reverse)
+    for m in ("q", "k", "v", "g", "beta", "h0"):
+        close(d[m], rd[m], "d" + m)
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+def test_delta_wide_keys_packed(reverse):
+    _case(f"delta wide keys packed reverse {reverse}")
+    lens, hk, hv, dk, dv = [0, 1, 64, 0, 65, 3, 200, 130, 128, 0], 1, 3, 104, 40
+    x, g = delta_inputs(42, 1, sum(lens), hk, hv, dk, dv, BF16, decay=0.1)
+    off = np.concatenate([[0], np.cumsum(lens)])
+    offsets = torch.tensor(off, dtype=torch.int32, device=DEV)
+    rn = lambda *s: torch.randn(s, generator=g, device=DEV)
+    h0, dstate, dout = rn(len(lens), hv, dk, dv), rn(len(lens), hv, dk, dv), rn(*x["v"].shape).to(BF16)
+    ref_in = {m: host(t) for m, t in x.items()}
+    out, state = vm.vm_gated_delta_fwd(**x, scale=0.5, h0=h0, want_state=True, reverse=reverse, offsets=offsets)
+    ro, rs, _ = mixers.delta(**ref_in, scale=0.5, h0=host(h0), reverse=reverse, offsets=off)
+    close(out, ro, "out")
+    close(state, rs, "state")
+    d = vm.vm_gated_delta_bwd(**x, dout=dout, scale=0.5, h0=h0, dstate=dstate, reverse=reverse, offsets=offsets)
+    rd = mixers.delta_grad(**ref_in, scale=0.5, dout=host(dout), h0=host(h0), dstate=host(dstate), reverse=reverse,
+                           offsets=off)
+    for m in ("q", "k", "v", "g", "beta", "h0"):
+        close(d[m], rd[m], "d" + m)
+
+
 def test_delta_offsets_outside_the_row_stay_inside():
     # offsets past the tokens are clamped: the first sequence still holds, the rest is empty
     _case("delta clamped offsets")
