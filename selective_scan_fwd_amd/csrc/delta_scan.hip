@@ -151,7 +151,7 @@ struct ChunkLoad {
     if constexpr (DIRECT) {
       if (wave == 0) to_lds4(reg, l.eg, lane * 4);
       if (wave == 1) to_lds4(rew, l.ew, lane * 4);
-      if (wave == 2) to_lds4(rbeta, l.beta, ob);
+      if (wave == 2 % kWaves) to_lds4(rbeta, l.beta, ob);
     } else {
       eg = bload<float>(reg, lane * 4);
       ew = bload<float>(rew, lane * 4);
@@ -522,7 +522,7 @@ template <typename T, bool VEC> constexpr bool kDirect = VEC && sizeof(T) == 2;
 // Whether as many waves again do nothing but load: where the others leave half
 // of the registers (one wave a SIMD) and nothing has to pass through registers
 // on its way (which it might: 250 us instead of 183).
-template <typename T, bool VEC, int NP> constexpr bool kLoaders = kDirect<T, VEC> && NP == 2;
+template <typename T, bool VEC, int NP> constexpr bool kLoaders = kDirect<T, VEC> && NP <= 2;
 template <typename T, bool VEC, int NP>
 constexpr int kBlock = Shape<NP>::kThreads * (kLoaders<T, VEC, NP> ? 2 : 1);
 // The loading waves' part of a scan from chunk c0 on, chunks `step` apart: as many
@@ -974,10 +974,6 @@ __global__ __launch_bounds__((kBlock<T, VEC, NP>)) void delta_scans_kernel(Delta
     scan_forward<T, DK, true, VEC, NP>(A, colblocks, block - blocks, blocks, sh.f);
 }
 
-// Pairs of a workgroup: two where rows of 128 fill LDS (fp32 in terms, or two
-// buffers of bf16).
-template <int DK> constexpr int kPairs = DK == 128 ? 2 : 4;
-
 // Workgroups of a scan with cb column blocks, as place() takes them apart.
 uint32_t scan_blocks(const DeltaArgs &a, int cb) {
   int64_t heads = static_cast<int64_t>(a.nseq) * a.hv;
@@ -985,9 +981,8 @@ uint32_t scan_blocks(const DeltaArgs &a, int cb) {
   return static_cast<uint32_t>(heads * cb);
 }
 
-template <typename T, int DK, bool VEC>
+template <typename T, int DK, bool VEC, int NP>
 hipError_t launch(const DeltaArgs &a, bool back, hipStream_t s) {
-  constexpr int NP = kPairs<DK>;
   const int cb = (a.dv + 16 * NP - 1) / (16 * NP);
   const dim3 block(kBlock<T, VEC, NP>);
   if (back)
@@ -995,6 +990,26 @@ hipError_t launch(const DeltaArgs &a, bool back, hipStream_t s) {
   else
     hipLaunchKernelGGL((delta_scan_kernel<T, DK, VEC, NP>), dim3(scan_blocks(a, cb)), block, 0, s, a, cb);
   return hipGetLastError();
+}
+// As few pairs of waves to a workgroup as give no more workgroups than the card
+// has compute units: each wave then has a SIMD of its own, and fewer wait for
+// each other.  With more workgroups, as many pairs as LDS and registers hold
+// share what is loaded: four, of rows of 128 two.  (4096 tokens, bf16, forward:
+// 8 heads of 64 117 us a call with one pair, 133 with two, 208 with four; 128 heads of
+// 64 223 with two, 276 with four; 256 heads 425 and 372; 16 heads of 128 144 with
+// one, 167 with two; 64 heads of 128 317 and 229.  fp32, whose loads the pairs
+// do themselves: 8 heads of 64 294 with two, 329 with four, 256 heads 796 and
+// 555; 16 heads of 128 469 with one, 421 with two.)
+template <typename T, int DK, bool VEC>
+hipError_t launch(const DeltaArgs &a, bool back, hipStream_t s) {
+  const auto fits = [&](int pairs) {
+    return scan_blocks(a, (a.dv + 16 * pairs - 1) / (16 * pairs)) * (back ? 2 : 1) <= 256;
+  };
+  if constexpr (kLoaders<T, VEC, 1>)
+    if (fits(1)) return launch<T, DK, VEC, 1>(a, back, s);
+  if constexpr (DK == 64)
+    if (!fits(2)) return launch<T, DK, VEC, 4>(a, back, s);
+  return launch<T, DK, VEC, 2>(a, back, s);
 }
 template <typename T, int DK>
 hipError_t launch(const DeltaArgs &a, bool back, hipStream_t s) {

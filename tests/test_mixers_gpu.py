@@ -171,6 +171,26 @@ def test_delta_wide_keys_over_many_chunks(size, reverse):
         close(d[m], rd[m], "d" + m)
 
 
+# the number of workgroups decides how many pairs of waves each has: with more heads
+# than the card has compute units four (wide keys: two), with a quarter of them two
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("size", [(90, 70, 1, 3, 48, 40), (90, 66, 3, 3, 50, 17), (70, 67, 2, 4, 72, 20),
+                                  (20, 130, 2, 4, 64, 72), (25, 65, 4, 4, 104, 36)])
+def test_delta_many_heads(size, dtype):
+    _case(f"delta many heads {size} {dtype}")
+    x, g = delta_inputs(43, *size, dtype, decay=0.2)
+    dout = torch.randn(x["v"].shape, generator=g, device=DEV).to(dtype)
+    ref_in = {m: host(t) for m, t in x.items()}
+    out, state = vm.vm_gated_delta_fwd(**x, scale=0.5, want_state=True)
+    ro, rs, _ = mixers.delta(**ref_in, scale=0.5)
+    close(out, ro, "out")
+    close(state, rs, "state")
+    d = vm.vm_gated_delta_bwd(**x, dout=dout, scale=0.5)
+    rd = mixers.delta_grad(**ref_in, scale=0.5, dout=host(dout))
+    for m in ("q", "k", "v", "g", "beta"):
+        close(d[m], rd[m], "d" + m)
+
+
 @pytest.mark.parametrize("reverse", [False, True])
 def test_delta_wide_keys_packed(reverse):
     _case(f"delta wide keys packed reverse {reverse}")
