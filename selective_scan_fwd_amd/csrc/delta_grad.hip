@@ -11,6 +11,9 @@
 //   dbeta = rowsum(dR v) - e^G k.X + k.Y
 //   dG = q.dq + k.(Z2 - Z1);  the chunk's last G also e^{G_C} <S, dS> + sum k.(w V dS^T)
 //   dg_t = sum of dG over the steps >= t of the chunk
+//        = <S, dS before the chunk> - sum of dG over the steps < t
+// (the second form where S is 0, so that the first token of a sequence without a
+// state has a gradient of 0 and not what rounding leaves of the sum)
 // (every decay factor of a product of i and j counts once for i and once
 // against j, so the sums over its terms are dot products of what is there).
 #include <hip/hip_runtime.h>
@@ -161,6 +164,7 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
   __shared__ double sg[kC];
   __shared__ __attribute__((aligned(16))) float seg[kC], sw[kC], sbeta[kC], srv[kC];
   __shared__ float swk[8], sdot[8], sgam[2][kC], sbet[2][kC], sgate[kC];
+  __shared__ bool sstate[8];
   Slice *slices = reinterpret_cast<Slice *>(raw);
   MaskedLds &pr = *reinterpret_cast<MaskedLds *>(raw);
   Key *keys = reinterpret_cast<Key *>(raw + (kOwnKeys ? kShared1 : sizeof(MaskedLds)));
@@ -257,12 +261,15 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) p0[c / 2] = p1[c] = zero;
     float dot = 0, rv = 0;
+    uint32_t bits = 0;                       // of the state, to see whether it is 0
     auto store = [&](Slice &l) {
       f32x4 a, b, x, y;
       if (wave < DK / 16) {                  // (16 rows of a state to a wave)
         widen(ls, a, b);
         widen(ld, x, y);
         dot += dot4(a, x) + dot4(b, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bits |= ls.x[0][i] | ls.x[1][i];
         put_terms<3, Slice::kState>(l.s, srow, piece, a, b);
         put_terms<3, Slice::kState>(l.d, srow, piece, x, y);
       }
@@ -328,7 +335,11 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
     if (first && piece == 0) srv[row] = rv;
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) dot += __shfl_xor(dot, o);
-    if (lane == 0) sdot[wave] = dot;
+    const bool state = __any((bits << 1) != 0);
+    if (lane == 0) {
+      sdot[wave] = dot;
+      sstate[wave] = state;
+    }
     // the masked products' factors, and their way to LDS as left operands
     auto put_masked = [&](uint16_t *dst, const bool transposed, const bool is_n) {
 #pragma unroll
@@ -468,9 +479,21 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(DeltaArgs A) {
       }
       float x = sgam[0][lane] + sgam[1][lane];
       if (lane == 63) x += seg[kC - 1] * ss + sk_all;
-      for (int o = 1; o < 64; o *= 2) {
-        const float z = __shfl_down(x, o);
-        if (lane + o < 64) x += z;
+      bool any = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) any = any || sstate[i];
+      if (any) {
+        for (int o = 1; o < 64; o *= 2) {
+          const float z = __shfl_down(x, o);
+          if (lane + o < 64) x += z;
+        }
+      } else {
+        for (int o = 1; o < 64; o *= 2) {
+          const float z = __shfl_up(x, o);
+          if (lane >= o) x += z;
+        }
+        x = __shfl_up(x, 1);
+        x = lane == 0 ? 0.0f : -x;
       }
       if (lane < n) {
         const int64_t i = token_of(A, q, c0, lane) * A.hv + h;

@@ -212,6 +212,25 @@ def test_delta_wide_keys_packed(reverse):
         close(d[m], rd[m], "d" + m)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_gate_gradient_of_a_first_token_is_zero(dtype, reverse):
+    # nothing decays before the first token: its gate's gradient is 0, not a rounding of it
+    _case(f"gate gradient of first tokens {dtype} reverse {reverse}")
+    for l, zero_state in ((1, False), (1, True), (64, False), (130, True)):
+        x, g = delta_inputs(44, 3, l, 2, 4, 64, 48, dtype)
+        dout = torch.randn(x["v"].shape, generator=g, device=DEV).to(dtype)
+        h0 = torch.zeros(3, 4, 64, 48, device=DEV) if zero_state else None
+        d = vm.vm_gated_delta_bwd(**x, dout=dout, h0=h0, reverse=reverse)
+        assert (d["g"][:, l - 1 if reverse else 0] == 0).all()
+        rd = mixers.delta_grad(**{m: host(t) for m, t in x.items()}, scale=64 ** -0.5, dout=host(dout), reverse=reverse)
+        close(d["g"], rd["g"], "dg")
+    x, g = delta_inputs(45, 1, 9, 1, 2, 32, 16, dtype)
+    offsets = torch.tensor([0, 1, 1, 4, 9], dtype=torch.int32, device=DEV)
+    d = vm.vm_gated_delta_bwd(**x, dout=torch.ones_like(x["v"]), offsets=offsets, reverse=reverse)
+    assert (d["g"][0, [0, 3, 8] if reverse else [0, 1, 4]] == 0).all()
+
+
 def test_delta_offsets_outside_the_row_stay_inside():
     # offsets past the tokens are clamped: the first sequence still holds, the rest is empty
     _case("delta clamped offsets")
