@@ -16,7 +16,7 @@
 // the head crosses lanes.  A group keeps one token's angles in registers and
 // walks over the token's heads, queries first, then keys.  4 x 4097 tokens, 24
 // heads of 128, bf16 (206 MB): 59 us; backward, 128 x 197 tokens, 12 heads of 64,
-// fp32 (233 MB): 58 us and 7 for the gains' sums.
+// fp32 (233 MB): 58 us and 6 for the gains' sums.
 #include <hip/hip_runtime.h>
 
 #include "mixer_internal.h"
@@ -264,7 +264,15 @@ __global__ __launch_bounds__(kThreads) void norm_dw_kernel(NormArgs A, int block
   const int m = i >= A.dim;
   if (A.dw[m] == nullptr) return;
   float s = 0;
-  for (int b = threadIdx.x % 64; b < blocks; b += 64) s += A.partial[static_cast<int64_t>(b) * 2 * A.dim + i];
+  constexpr int kAhead = 8;                 // loads under way
+  for (int b = threadIdx.x % 64; b < blocks; b += 64 * kAhead) {
+    float x[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      x[j] = b + 64 * j < blocks ? A.partial[static_cast<int64_t>(b + 64 * j) * 2 * A.dim + i] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) s += x[j];
+  }
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
   if (threadIdx.x % 64 == 0) A.dw[m][i - m * A.dim] = s;
 }
