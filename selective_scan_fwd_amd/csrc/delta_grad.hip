@@ -140,7 +140,8 @@ __device__ __forceinline__ void masked_tiles(const uint16_t *a, const uint16_t *
 // the second phase) do not overlap with another's.  Measured and not better:
 // slices loaded two ahead (293 us, spills), states from memory to the registers
 // of the one wave that needs them (270 to 300), 16 waves (290), the next head's
-// loads before the second phase (no change).
+// loads before the second phase (no change), staying for another chunk with its
+// first loads issued (fp32 109, bf16 310: spills).
 //
 // Products with S and dS: wave w owns rows 16 (w % 4) .. and half w / 4 of the
 // columns.  Of the four masked products (M, N and their transposes, each as
