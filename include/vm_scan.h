@@ -499,7 +499,7 @@ int vm_gated_delta_fwd(const vm_delta *p, void *out, float *state, float scale,
 
 /*
  * Workspace of vm_gated_delta_fwd (backward = 0) or vm_gated_delta_bwd
- * (backward = 1), with packed = 1 for sequences given by offsets.  About 31 KB
+ * (backward = 1), with packed = 1 for sequences given by offsets.  About 37 KB
  * (fp32: 25 KB) per 64 tokens and value head, backward 55 KB (37 KB) + 8 dk dv +
  * 512 dv bytes.
  * Returns -VM_ERR_SHAPE or -VM_ERR_UNSUPPORTED for sizes that no call takes,

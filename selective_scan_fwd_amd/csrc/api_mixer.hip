@@ -144,12 +144,12 @@ class Parts {
 // backward pass what its kernels hand on.
 void delta_parts(vmk::DeltaArgs &a, bool bf16, bool backward, Parts &parts) {
   const int64_t per = a.slots * a.hv, c = vmk::kDeltaChunk, tri = per * vmk::kTriTerm * 2;
-  const int units_t = vmk::tri_units_t(bf16), units_p = vmk::tri_units_p(bf16, backward);
-  parts.add(&a.T, tri * (units_t + (backward ? 0 : units_p)));
+  const int units = vmk::tri_units(bf16);
+  parts.add(&a.T, tri * units * (backward ? 1 : 2));
   parts.add(&a.eg, per * c * 4);
   parts.add(&a.ew, per * c * 4);
   if (backward) {
-    parts.add(&a.TT, tri * (units_t + units_p));
+    parts.add(&a.TT, tri * units * 2);
     parts.add(&a.gam, per * c * 8);
     a.dvp = (a.dv + 15) / 16 * 16;
     parts.add(&a.S, per * a.dk * a.dvp * 4);

@@ -25,14 +25,13 @@ constexpr int kThreads = 256;
 // Bound by the latency of its chain (loads, products, substitution, blocks), so
 // LDS is kept small for as many workgroups a compute unit as the registers
 // allow: forward, a wave's queries go straight to its registers, and T takes
-// the place of A.  4 x 4097 tokens, 8 and 16 heads of 128, bf16: 49 us (62 with
-// queries and T in LDS of their own) for 34 MB read and 124 MB written; 128 x 197
-// tokens, 6 heads of 64, fp32: 46 us.
+// the place of A.  4 x 4097 tokens, 8 and 16 heads of 128, bf16: 52 us for 34 MB
+// read and 155 MB written (49 with a term less of P, and then 62 with queries and T
+// in LDS of their own); 128 x 197 tokens, 6 heads of 64, fp32: 44 us.
 template <typename T, int DK, bool BACK, bool VEC>
 __global__ __launch_bounds__(kThreads, 4) void delta_prep_kernel(DeltaArgs A) {
   constexpr int kNi = kInputTerms<T>, kTerm = kC * DK, kPieces = DK / 8;
-  constexpr int kTermsP = delta_terms_p(kNi == 1, BACK);
-  constexpr int kUnitsT = tri_units_t(kNi == 1), kUnits = kUnitsT + tri_units_p(kNi == 1, BACK);
+  constexpr int kUnitsT = tri_units(kNi == 1), kUnits = 2 * kUnitsT;
   __shared__ __attribute__((aligned(16))) uint16_t sk[kNi * kTerm];
   __shared__ __attribute__((aligned(16))) uint16_t sq[BACK ? kNi * kTerm : 8];
   __shared__ __attribute__((aligned(16))) float sa[kC * kPitchC];  // A, later T
@@ -189,7 +188,7 @@ __global__ __launch_bounds__(kThreads, 4) void delta_prep_kernel(DeltaArgs A) {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         if (BACK ? (wave >= 2 && ks == 0) : (wave < 2 && ks == 1)) continue;
-        put_block<T, kTermsP>(dst, BACK ? tri_block_t(wave, ks) : tri_block(wave, ks), lane, pt[2 * ks], pt[2 * ks + 1]);
+        put_block<T, kTerms>(dst, BACK ? tri_block_t(wave, ks) : tri_block(wave, ks), lane, pt[2 * ks], pt[2 * ks + 1]);
       }
     }
     __syncthreads();
@@ -233,7 +232,7 @@ __global__ __launch_bounds__(kThreads, 4) void delta_prep_kernel(DeltaArgs A) {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         if (wave >= 2 && ks == 0) continue;
-        put_block<T, kTermsT>(dst, tri_block_t(wave, ks), lane, t[2 * ks], t[2 * ks + 1]);
+        put_block<T, kTerms>(dst, tri_block_t(wave, ks), lane, t[2 * ks], t[2 * ks + 1]);
       }
     }
     __syncthreads();                       // every wave has read A
@@ -250,7 +249,7 @@ __global__ __launch_bounds__(kThreads, 4) void delta_prep_kernel(DeltaArgs A) {
       const float *row = sa + (16 * wave + li) * kPitchC + 32 * ks + 4 * lg;
       const f32x4 zero = {0, 0, 0, 0};
       const f32x4 lo = load4(row), hi = 2 * ks + 1 <= wave ? load4(row + 16) : zero;
-      put_block<T, kTermsT>(dst, tri_block(wave, ks), lane, lo, hi);
+      put_block<T, kTerms>(dst, tri_block(wave, ks), lane, lo, hi);
     }
   }
 }

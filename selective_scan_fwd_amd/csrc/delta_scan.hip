@@ -24,12 +24,13 @@ namespace {
 // corrected values.  The chain of a chunk is what bounds a long sequence; a wave
 // issues about one instruction in five cycles however idle the rest of its SIMD
 // is, so halving the instructions of the chain is worth three exchanges: 4 x 4097
-// tokens, 16 value heads of 128, bf16, 65 chunks: 211 us where one wave to 16
-// columns took 281, and 183 (2.8 us a chunk) with waves of their own for the
-// loads, see load_chunks(); with nothing loaded after the first chunk it would
-// take 163.  (128 x 197 tokens, 6 heads of 64, fp32: 88 us; 40 packed sequences
-// of up to 1500 tokens, 8 value heads of 100: 77 us, in the order given and in
-// runs over the XCDs 84.)
+// tokens, 16 value heads of 128, bf16, 65 chunks, took 211 us where one wave to 16
+// columns took 281, and 183 with waves of their own for the loads, see
+// load_chunks(); with nothing loaded after the first chunk 163.  Those were with
+// two terms of what enters the output only; with all three it takes 202 (3.1 us a
+// chunk).  (128 x 197 tokens, 6 heads of 64, fp32: 83 us; 40 packed sequences of
+// up to 1500 tokens, 8 value heads of 100: 86 us, of two terms 77, and 84 in the
+// order given and in runs over the XCDs.)
 //
 // Rows of the state are held so that K's rows are read in whole pieces: row
 // 4 lg + r of tile 2 ks + p is state row 32 ks + 8 lg + 4 p + r.
@@ -42,13 +43,12 @@ struct Shape {
 };
 
 // A chunk's operands in LDS: K and Q in terms, the triangles' blocks, decays.
-template <typename T, int DK, int TRI, bool WITH_Q, int NP>
+template <typename T, int DK, int TRI, bool WITH_Q>
 struct ChunkLds {
   static constexpr int kTerm = kC * DK;
   __attribute__((aligned(16))) uint16_t k[kInputTerms<T> * kTerm];
   __attribute__((aligned(16))) uint16_t q[WITH_Q ? kInputTerms<T> * kTerm : 8];
   __attribute__((aligned(16))) uint16_t tri[TRI * kTriTerm];
-  __attribute__((aligned(16))) uint16_t v[sizeof(T) == 2 ? kC * Shape<NP>::kCols : 8];   // (the workgroup's columns)
   __attribute__((aligned(16))) float eg[kC], ew[kC], beta[kC];
 };
 
@@ -60,12 +60,13 @@ struct ChunkLds {
 // whole chunks and kept in registers.
 template <typename T, int DK, int TRI, bool WITH_Q, bool VEC, bool DIRECT, int NP>
 struct ChunkLoad {
-  typedef ChunkLds<T, DK, TRI, WITH_Q, NP> Lds;
+  typedef ChunkLds<T, DK, TRI, WITH_Q> Lds;
   static constexpr int kWaves = Shape<NP>::kWaves, kThreads = Shape<NP>::kThreads, kCols = Shape<NP>::kCols;
   static constexpr int kPieces = DK / 8, kPer = kC * kPieces / kThreads;
   // v to LDS: rows of an instruction with 16 or 4 bytes a lane, and instructions of a wave
   static constexpr int kRows16 = 512 / kCols, kRows4 = 128 / kCols;
   static constexpr int kV16 = kC / kRows16 / kWaves, kV4 = kC / kRows4 / kWaves;
+  static constexpr int kValues = DIRECT ? kC * kCols : 8;   // (the workgroup's columns)
   // triangular operands in memory: blocks of whole terms, or of fp32 matrices
   static constexpr bool kWhole = sizeof(T) == 4;
   static constexpr int kBlocks = (kWhole ? TRI / 3 : TRI) * kTriBlocks, kBlockBytes = kWhole ? 2048 : 1024;
@@ -131,15 +132,15 @@ struct ChunkLoad {
     low = w.low;
     at = (s.slot0 + c0 / kC) * A.hv + h;
   }
-  __device__ __forceinline__ void load_v(Lds &l) {
+  __device__ __forceinline__ void load_v(uint16_t *lv) {
     const Rsrc rv = buffer(vbase + low * vstride);
     if constexpr (DIRECT) {
       if (v16) {
 #pragma unroll
-        for (int i = 0; i < kV16; ++i) to_lds16(rv, l.v + (i * kWaves + wave) * 512, ov[i]);
+        for (int i = 0; i < kV16; ++i) to_lds16(rv, lv + (i * kWaves + wave) * 512, ov[i]);
       } else {
 #pragma unroll
-        for (int i = 0; i < kV4; ++i) to_lds4(rv, l.v + (i * kWaves + wave) * 128, ov[i]);
+        for (int i = 0; i < kV4; ++i) to_lds4(rv, lv + (i * kWaves + wave) * 128, ov[i]);
       }
     } else {
 #pragma unroll
@@ -198,16 +199,16 @@ struct ChunkLoad {
       }
     }
   }
+  // All but v.
   __device__ __forceinline__ void load(const DeltaArgs &A, const Seq &s, int64_t c0, const uint16_t *m, Lds &l) {
     aim(A, s, c0);
-    load_v(l);
     load_gates(A, l);
     load_k(A, l);
     load_q(A, l);
     load_tri(m, l);
   }
-  // Loads that every wave issues for a chunk besides the triangles', at least (DIRECT).
-  static constexpr int kLeast = kV16 + kPer * (WITH_Q ? 2 : 1);
+  // Loads that every wave issues for a chunk's K and Q (DIRECT).
+  static constexpr int kLeast = kPer * (WITH_Q ? 2 : 1);
 
   __device__ __forceinline__ void store(Lds &l) const {
     if constexpr (DIRECT) {
@@ -242,10 +243,10 @@ struct ChunkLoad {
 
   // Step tile rt of the pair's 16 columns of v, as a D tile.  From registers it is
   // taken as soon as it has come, from LDS with the chunk.
-  __device__ __forceinline__ f32x4 values(const Lds &l, int rt) const {
+  __device__ __forceinline__ f32x4 values(const uint16_t *lv, int rt) const {
     f32x4 x;
     if constexpr (DIRECT) {
-      const uint16_t *p = l.v + (16 * rt + 4 * lg + li / 4) * kCols + 16 * (wave / 2) + 4 * (li % 4);
+      const uint16_t *p = lv + (16 * rt + 4 * lg + li / 4) * kCols + 16 * (wave / 2) + 4 * (li % 4);
       const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
           (__attribute__((address_space(3))) s16x4 *)const_cast<uint16_t *>(p));
 #pragma unroll
@@ -521,7 +522,7 @@ __device__ __forceinline__ void store_rows(const DeltaArgs &A, float *base, cons
 template <typename T, bool VEC> constexpr bool kDirect = VEC && sizeof(T) == 2;
 // Whether as many waves again do nothing but load: where the others leave half
 // of the registers (one wave a SIMD) and nothing has to pass through registers
-// on its way (which it might: 250 us instead of 183).
+// on its way (which it might: 250 us instead of 183, of two terms).
 template <typename T, bool VEC, int NP> constexpr bool kLoaders = kDirect<T, VEC> && NP <= 2;
 template <typename T, bool VEC, int NP>
 constexpr int kBlock = Shape<NP>::kThreads * (kLoaders<T, VEC, NP> ? 2 : 1);
@@ -529,18 +530,23 @@ constexpr int kBlock = Shape<NP>::kThreads * (kLoaders<T, VEC, NP> ? 2 : 1);
 // barriers a chunk as the others have.  A buffer's parts are loaded again, for
 // the chunk after next, once the others have them in registers, some between
 // any two barriers (issuing loads takes its time too, and the others wait at the
-// barriers): BACK, the triangles and dout after the first barrier, Q after the
-// second, K and the gates after the third; forward v, Q and the gates after the
-// first, K and the triangles after the second; what is left of the triangles
-// (blocks from kEnd on) at the start of the next chunk.  Loads return in order:
+// barriers): BACK, the triangles after the first barrier, Q after the second, K
+// and the gates after the third; forward Q and the gates after the first, K and
+// the triangles after the second; what is left of the triangles (blocks from kEnd
+// on) at the start of the next chunk.  v (BACK: dout) has one buffer, which is
+// read at a chunk's start and loaded again, for the next chunk, after the first
+// barrier (a second one would not fit beside the triangles of keys of 128).  Loads return in order:
 // what the next chunk needs has come when no more are out than were issued since.
 template <bool BACK, typename Load, typename Lds>
 __device__ __forceinline__ void load_chunks(Load &next, const DeltaArgs &A, const Seq &q, const uint16_t *m, int64_t c0,
-                                            int64_t step, Lds (&lds)[2]) {
+                                            int64_t step, Lds (&lds)[2], uint16_t *v) {
   constexpr int kTri = Load::kTri, kEnd = BACK ? 4 : (kTri + 1) / 2;
   static_assert(kEnd <= Load::kBlocks / Load::kWaves, "every wave issues the triangles' first kEnd loads");
   const auto in = [&](int64_t c) { return c >= 0 && c < q.len; };
-  if (in(c0)) next.load(A, q, c0, m, lds[0]);
+  if (in(c0)) {
+    next.load(A, q, c0, m, lds[0]);
+    next.load_v(v);
+  }
   if (in(c0 + step)) next.load(A, q, c0 + step, m, lds[1]);
   wait_loads();
   __syncthreads();
@@ -550,10 +556,10 @@ __device__ __forceinline__ void load_chunks(Load &next, const DeltaArgs &A, cons
     const bool more = in(c0 + 2 * step);
     Lds &l = lds[buf];
     if (rest) next.load_tri(m, lds[buf ^ 1], kEnd, kTri);
-    if (more) next.aim(A, q, c0 + 2 * step);
     lds_barrier();
+    if (in(c0 + step)) next.load_v(v);     // (aimed at it still)
     if (more) {
-      next.load_v(l);
+      next.aim(A, q, c0 + 2 * step);
       if (BACK) {
         next.load_tri(m, l, 0, 3);
       } else {
@@ -588,30 +594,35 @@ __device__ __forceinline__ void load_chunks(Load &next, const DeltaArgs &A, cons
     buf ^= 1;
   }
 }
-// Exchanged items (1 KB) of a pair: forward two regions, the first reused;
-// backward one, reused twice.
-constexpr int kItemsA = 10, kItemsB = 2, kItems = kItemsA + kItemsB, kItemsBwd = 6;
+// Exchanged items (1 KB) of a pair, reused from one exchange to the next; without
+// outputs six.
+constexpr int kItems = 9, kItemsBwd = 6;
+// Buffers of v: where the waves load for themselves, they do so for the next chunk
+// while others may still read this one's.
+template <typename T, bool VEC, int NP> constexpr int kBuffersV = kDirect<T, VEC> && !kLoaders<T, VEC, NP> ? 2 : 1;
 
 // Where token rows of T are whole pieces (VEC), two chunks' operands.
 template <typename T, int DK, bool KEEP, bool VEC, int NP>
 struct Forward {
-  static constexpr int kNi = kInputTerms<T>, kTermsP = KEEP ? 0 : delta_terms_p(kNi == 1, false);
+  static constexpr int kNi = kInputTerms<T>;
   static constexpr bool kDma = kDirect<T, VEC>;
-  typedef ChunkLoad<T, DK, kTermsT + kTermsP, !KEEP, VEC, kDma, NP> Load;
+  typedef ChunkLoad<T, DK, KEEP ? kTerms : 2 * kTerms, !KEEP, VEC, kDma, NP> Load;
   static constexpr int kBuffers = kDma ? 2 : 1;
   struct Shared {
     typename Load::Lds lds[kBuffers];
-    __attribute__((aligned(16))) char xch[NP][kItems * 1024];
+    __attribute__((aligned(16))) uint16_t v[kBuffersV<T, VEC, NP>][Load::kValues];
+    __attribute__((aligned(16))) char xch[NP][(KEEP ? kItemsBwd : kItems) * 1024];
   };
 };
 template <typename T, int DK, bool VEC, int NP>
 struct Backward {
-  static constexpr int kNi = kInputTerms<T>, kTermsP = delta_terms_p(kNi == 1, true);
+  static constexpr int kNi = kInputTerms<T>;
   static constexpr bool kDma = kDirect<T, VEC>;
-  typedef ChunkLoad<T, DK, kTermsT + kTermsP, true, VEC, kDma, NP> Load;
+  typedef ChunkLoad<T, DK, 2 * kTerms, true, VEC, kDma, NP> Load;
   static constexpr int kBuffers = kDma ? 2 : 1;
   struct Shared {
     typename Load::Lds lds[kBuffers];
+    __attribute__((aligned(16))) uint16_t v[kBuffersV<T, VEC, NP>][Load::kValues];
     __attribute__((aligned(16))) char xch[NP][kItemsBwd * 1024];
   };
 };
@@ -624,8 +635,7 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
   typedef Forward<T, DK, KEEP, VEC, NP> F;
   typedef typename F::Load Load;
   typedef typename Load::Lds Lds;
-  constexpr int kNi = F::kNi, kNs = 3, kHalf = DK / 64, kTermsP = F::kTermsP, kBuffers = F::kBuffers;
-  constexpr int kNo = kNi == 1 ? 2 : 3;               // terms of S and V on their way to out only
+  constexpr int kNi = F::kNi, kNs = kTerms, kHalf = DK / 64, kBuffers = F::kBuffers;
   constexpr bool kDma = F::kDma, kAhead = kNi == 1, kSelf = !kLoaders<T, VEC, NP>;   // (kSelf: waves load for themselves)
   Place pl;
   if (!place(A, colblocks, block, blocks, &pl)) return;
@@ -634,13 +644,13 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
   Load next;
   next.init(A, h, pl.cb, static_cast<const T *>(A.v), A.vs);
   const int lane = next.lane, li = next.li, lg = next.lg, p = next.wave % 2;
-  char *xa = sh.xch[next.wave / 2], *xb = xa + kItemsA * 1024;
+  char *xa = sh.xch[next.wave / 2];
   const int col = next.col0 + 16 * (next.wave / 2) + li;
   const int64_t state_at = (static_cast<int64_t>(s) * A.hv + h) * A.dk * A.dv;
   const f32x4 zero = {0, 0, 0, 0};
   if constexpr (!kSelf)
     if (uniform(static_cast<int>(threadIdx.x / 64)) >= Shape<NP>::kWaves) {
-      load_chunks<false>(next, A, q, A.T, 0, kC, sh.lds);
+      load_chunks<false>(next, A, q, A.T, 0, kC, sh.lds, sh.v[0]);
       return;
     }
   f32x4 S[DK / 32];
@@ -649,6 +659,7 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
   if (q.len > 0) {
     if (kSelf) {
       next.load(A, q, 0, A.T, sh.lds[0]);
+      next.load_v(sh.v[0]);
       next.store(sh.lds[0]);
     }
     if (KEEP) store_state<DK>(A, A.S + (q.slot0 * A.hv + h) * A.dk * A.dvp, A.dvp, S, p, lg, col);
@@ -661,7 +672,8 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
     const Lds &l = sh.lds[buf];
     Lds &ln = sh.lds[kBuffers == 2 ? buf ^ 1 : 0];
     const bool more = c0 + kC < q.len;
-    const f32x4 v[2] = {next.values(l, 2 * p), next.values(l, 2 * p + 1)};
+    constexpr int kBv = kBuffersV<T, VEC, NP>;
+    const f32x4 v[2] = {next.values(sh.v[buf % kBv], 2 * p), next.values(sh.v[buf % kBv], 2 * p + 1)};
     RowTiles<DK, kNi> kr, qr;
     if (kAhead) {
       kr.read(l.k, p, li, lg);
@@ -674,13 +686,13 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
     const float last = l.eg[kC - 1];
     if (kSelf && more) {                    // (the loads' issue spreads over the chunk)
       next.aim(A, q, c0 + kC);
-      next.load_v(ln);
+      next.load_v(sh.v[(buf + 1) % kBv]);
       next.load_gates(A, ln);
       next.load_k(A, ln);
     }
     // K S and Q S over this half's state rows
     f32x4 xm[2], om[2];
-    Blocks<kTermsT> ta, tb;
+    Blocks<kNs> ta, tb;
     {
       f32x4 x[4] = {zero, zero, zero, zero}, other[2];
       Terms<kNs> st[kHalf];
@@ -695,20 +707,15 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
       }
       if (kSelf && !KEEP && more) next.load_q(A, ln);
       halves(x, p, xm, other);
-      put(xa, 2 * p, lane, other[0]);
-      put(xa, 2 * p + 1, lane, other[1]);
+      put(xa, 2 - 2 * p, lane, other[0]);  // (items in the order of the halves that take them)
+      put(xa, 3 - 2 * p, lane, other[1]);
       if (!KEEP) {
-        Terms<kNo> so[kHalf];
-#pragma unroll
-        for (int ks = 0; ks < kHalf; ++ks)
-#pragma unroll
-          for (int t = 0; t < kNo; ++t) so[ks].t[t] = st[ks].t[t];
         f32x4 o4[4] = {zero, zero, zero, zero};
         if (!kAhead) qr.read(l.q, p, li, lg);
-        qr.times(so, o4);
+        qr.times(st, o4);
         halves(o4, p, om, other);
-        put(xa, 4 + 2 * p, lane, other[0]);
-        put(xa, 5 + 2 * p, lane, other[1]);
+        put(xa, 6 - 2 * p, lane, other[0]);
+        put(xa, 7 - 2 * p, lane, other[1]);
       }
     }
     lds_barrier();
@@ -716,8 +723,8 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
     f32x4 r[2], o[2], V[2] = {zero, zero};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      r[i] = be[i] * (v[i] - eg[i] * (xm[i] + take(xa, 2 - 2 * p + i, lane)));
-      if (!KEEP) o[i] = (om[i] + take(xa, 6 - 2 * p + i, lane)) * (eg[i] * A.scale);
+      r[i] = be[i] * (v[i] - eg[i] * (xm[i] + take(xa, 2 * p + i, lane)));
+      if (!KEEP) o[i] = (om[i] + take(xa, 4 + 2 * p + i, lane)) * (eg[i] * A.scale);
     }
     if (kSelf && more) next.load_tri(A.T, ln);
     const Terms<kNs> rt = split<kNs>(r[0], r[1]);
@@ -728,29 +735,29 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
     if (p == 0) {
       f32x4 y[2] = {zero, zero};
       tb.times(rt, y);
-      put(xb, 0, lane, y[0]);
-      put(xb, 1, lane, y[1]);
+      put(xa, 0, lane, y[0]);              // (where this wave alone has read)
+      put(xa, 1, lane, y[1]);
     }
     ta.times(rt, V);
-    constexpr int kTp = KEEP ? 1 : kTermsP;
-    Blocks<kTp> pa, pb;
+    const uint16_t *tp = l.tri + kTerms * kTriTerm;
+    Blocks<kNs> pa, pb;
     if (!KEEP && kAhead) {
-      pa.read(l.tri + kTermsT * kTriTerm, tri_block(2 * p, p), tri_block(2 * p + 1, p), lane);
-      pb.read(l.tri + kTermsT * kTriTerm, tri_block(2, 0), tri_block(3, 0), lane);
+      pa.read(tp, tri_block(2 * p, p), tri_block(2 * p + 1, p), lane);
+      pb.read(tp, tri_block(2, 0), tri_block(3, 0), lane);
     }
     ColumnTiles<DK> kc;
     if (!kSelf) kc.read(l.k, p, li, lg);
     lds_barrier();
     if (p == 1) {
-      V[0] += take(xb, 0, lane);
-      V[1] += take(xb, 1, lane);
+      V[0] += take(xa, 0, lane);
+      V[1] += take(xa, 1, lane);
     }
     Terms<kNs> vw[2];
     const Terms<kNs> mine = split<kNs>(V[0] * ew[0], V[1] * ew[1]);
-    put(xa, 3 * p, lane, mine);
-    Terms<kNo> vo;
+    put(xa, 3 - 3 * p, lane, mine);        // (the second half's where it alone has just read)
+    Terms<kNs> vo;
     if (!KEEP) {
-      vo = split<kNo>(V[0], V[1]);
+      vo = split<kNs>(V[0], V[1]);
       if (p == 0) put(xa, 6, lane, vo);
     }
 #pragma unroll
@@ -762,19 +769,19 @@ __device__ __forceinline__ void scan_forward(const DeltaArgs &A, int colblocks, 
     lds_barrier();
     if (p == 0) {
       vw[0] = mine;
-      vw[1] = take_terms<kNs>(xa, 3, lane);
+      vw[1] = take_terms<kNs>(xa, 0, lane);
     } else {
-      vw[0] = take_terms<kNs>(xa, 0, lane);
+      vw[0] = take_terms<kNs>(xa, 3, lane);
       vw[1] = mine;
     }
     kc.template times<kNi>(l.k, vw, p, li, lg, S);
     if constexpr (!KEEP) {
       if (!kAhead) {
-        pa.read(l.tri + kTermsT * kTriTerm, tri_block(2 * p, p), tri_block(2 * p + 1, p), lane);
-        pb.read(l.tri + kTermsT * kTriTerm, tri_block(2, 0), tri_block(3, 0), lane);
+        pa.read(tp, tri_block(2 * p, p), tri_block(2 * p + 1, p), lane);
+        pb.read(tp, tri_block(2, 0), tri_block(3, 0), lane);
       }
       pa.times(vo, o);
-      if (p == 1) pb.times(take_terms<kNo>(xa, 6, lane), o);
+      if (p == 1) pb.times(take_terms<kNs>(xa, 6, lane), o);
     }
     if (kBuffers == 1) lds_barrier();
     buf = kBuffers == 2 ? buf ^ 1 : 0;
@@ -800,7 +807,7 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
   typedef Backward<T, DK, VEC, NP> B;
   typedef typename B::Load Load;
   typedef typename Load::Lds Lds;
-  constexpr int kNi = B::kNi, kNs = 3, kHalf = DK / 64, kTermsP = B::kTermsP, kBuffers = B::kBuffers;
+  constexpr int kNi = B::kNi, kNs = kTerms, kHalf = DK / 64, kBuffers = B::kBuffers;
   constexpr bool kDma = B::kDma, kAhead = kNi == 1, kSelf = !kLoaders<T, VEC, NP>;
   Place pl;
   if (!place(A, colblocks, block, blocks, &pl)) return;
@@ -817,7 +824,7 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
   const int64_t first = (static_cast<int64_t>(q.len + kC - 1) / kC - 1) * kC;
   if constexpr (!kSelf)
     if (uniform(static_cast<int>(threadIdx.x / 64)) >= Shape<NP>::kWaves) {
-      load_chunks<true>(next, A, q, A.TT, first, -kC, sh.lds);
+      load_chunks<true>(next, A, q, A.TT, first, -kC, sh.lds, sh.v[0]);
       return;
     }
   f32x4 D[DK / 32];
@@ -826,6 +833,7 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
   if (q.len > 0) {
     if (kSelf) {
       next.load(A, q, first, A.TT, sh.lds[0]);
+      next.load_v(sh.v[0]);
       next.store(sh.lds[0]);
     }
     store_state<DK>(A, A.dS + ((q.slot0 + first / kC) * A.hv + h) * A.dk * A.dvp, A.dvp, D, p, lg, col);
@@ -839,12 +847,13 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
     Lds &ln = sh.lds[kBuffers == 2 ? buf ^ 1 : 0];
     const bool more = c0 > 0;
     // all of dout for P^T dout and Q^T dout
+    constexpr int kBv = kBuffersV<T, VEC, NP>;
     f32x4 o[4];
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) o[rt] = next.values(l, rt);
+    for (int rt = 0; rt < 4; ++rt) o[rt] = next.values(sh.v[buf % kBv], rt);
     RowTiles<DK, kNi> kr;
-    const uint16_t *tp = l.tri + kTermsT * kTriTerm;
-    Blocks<kTermsP> pa, pb;                 // P^T: this half's rows by the second half's steps, and the first's
+    const uint16_t *tp = l.tri + kTerms * kTriTerm;
+    Blocks<kNs> pa, pb;                     // P^T: this half's rows by the second half's steps, and the first's
     if (kAhead) {
       kr.read(l.k, p, li, lg);
       __builtin_amdgcn_sched_barrier(0);
@@ -855,12 +864,12 @@ __device__ __forceinline__ void scan_backward(const DeltaArgs &A, int colblocks,
     const float last = l.eg[kC - 1];
     if (kSelf && more) {
       next.aim(A, q, c0 - kC);
-      next.load_v(ln);
+      next.load_v(sh.v[(buf + 1) % kBv]);
       next.load_gates(A, ln);
       next.load_k(A, ln);
     }
     f32x4 xm[2];
-    Blocks<kTermsT> ta, tb;
+    Blocks<kNs> ta, tb;
     {
       f32x4 x[4] = {zero, zero, zero, zero}, other[2];
       Terms<kNs> st[kHalf];
@@ -994,12 +1003,16 @@ hipError_t launch(const DeltaArgs &a, bool back, hipStream_t s) {
 // As few pairs of waves to a workgroup as give no more workgroups than the card
 // has compute units: each wave then has a SIMD of its own, and fewer wait for
 // each other.  With more workgroups, as many pairs as LDS and registers hold
-// share what is loaded: four, of rows of 128 two.  (4096 tokens, bf16, forward:
-// 8 heads of 64 117 us a call with one pair, 133 with two, 208 with four; 128 heads of
-// 64 223 with two, 276 with four; 256 heads 425 and 372; 16 heads of 128 144 with
-// one, 167 with two; 64 heads of 128 317 and 229.  fp32, whose loads the pairs
-// do themselves: 8 heads of 64 294 with two, 329 with four, 256 heads 796 and
-// 555; 16 heads of 128 469 with one, 421 with two.)
+// share what is loaded: four, of rows of 128 two.  Calls over 4096 tokens, us,
+// with one, two and four pairs, the rule's choice marked:
+//   heads            8            32            64           80           256
+//   of 64, bf16      132* 152 236 144* 161 247  170* 187 274 294 206* 288 675 511 466*
+//     backward       169* 184 264 292* 308 387  594 529* 592 749 659 682* 2341 2073 2008*
+//   of 64, fp32      - 272* 311   - 310* 362    - 334* 392   - 353* 429   - 797 636*
+//   of 128, bf16     157* 185 -   164* 193 -    343 226* -   498 400* -   (128: 674 441* -)
+//     backward       223* 251 -   512 446* -    1098 920* -  1379 1188* - (128: 2153 1772* -)
+// Just past the number of compute units a second, nearly empty round begins: 64
+// heads of 128 are 256 workgroups of two pairs, 80 heads 320 (226 and 400 us).
 template <typename T, int DK, bool VEC>
 hipError_t launch(const DeltaArgs &a, bool back, hipStream_t s) {
   const auto fits = [&](int pairs) {

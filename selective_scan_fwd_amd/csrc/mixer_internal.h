@@ -88,16 +88,14 @@ struct DeltaArgs {
   void *dq, *dkey, *dval;
   float *dg, *dbeta, *dh0;
 };
-// Terms of bf16 that stand for an fp32 value (8 bits each, so three hold all
-// 24), and how many are kept of P: all, but forward, where it enters the output
-// only, 16 bits suffice with bf16 tokens, whose output is rounded to 8.  (The
-// gradients of g and beta are fp32 for all tokens: with 16 bits of P they are
-// 2.6e-6 off, with 24 bits 3e-7.)
-constexpr int kTermsT = 3;
-inline constexpr int delta_terms_p(bool bf16, bool backward) { return bf16 && !backward ? 2 : 3; }
-// What a matrix takes in memory, in units of one term.
-inline constexpr int tri_units_t(bool bf16) { return bf16 ? kTermsT : 2; }
-inline constexpr int tri_units_p(bool bf16, bool backward) { return bf16 ? delta_terms_p(true, backward) : 2; }
+// Terms of bf16 that stand for an fp32 value: 8 bits each, so three hold all 24.
+// All are kept of every operand, those that enter a bf16 output only among them:
+// with two, the parts of an output that cancel (a large state read back and the
+// chunk's own values) leave an error past the output's rounding (first states of
+// 2000 times the values: 4e-2), and 3e-3 of the outputs round to another side.
+constexpr int kTerms = 3;
+// What a triangular matrix takes in memory, in units of one term.
+inline constexpr int tri_units(bool bf16) { return bf16 ? kTerms : 2; }
 constexpr int kTriBlocks = 6;
 constexpr int64_t kTriTerm = kTriBlocks * 64 * 8;   // values of one term
 // Whether every row of q and k is whole 16-byte pieces, and those of v (the
