@@ -486,10 +486,11 @@ typedef struct vm_delta {
  *          sequence's is its h0.  May be h0 itself (the states then advance in
  *          place), but must not overlap it otherwise.
  *   n      number of sequences (batch without offsets)
- * dk and dv in [1, 128], n hv up to 2^21 - 8, up to 2^23 - 1 chunks of 64 steps
- * over all sequences, and token strides (hv dv among them) below 2^23 elements:
- * VM_ERR_UNSUPPORTED beyond.  hv % hk != 0 is VM_ERR_SHAPE.  Sequences are computed in chunks of 64 steps, within which
- * a NaN or Inf of one token reaches the outputs of earlier tokens too.
+ * dk and dv in [1, 128], hv up to 65535, n hv up to 2^21 - 8, up to 2^23 - 1
+ * chunks of 64 steps over all sequences, and token strides (hv dv among them)
+ * below 2^23 elements: VM_ERR_UNSUPPORTED beyond.  hv % hk != 0 is VM_ERR_SHAPE.
+ * Sequences are computed in chunks of 64 steps, within which a NaN or Inf of one
+ * token reaches the outputs of earlier tokens too.
  */
 int vm_gated_delta_fwd(const vm_delta *p, void *out, float *state, float scale,
                        int64_t batch, int64_t seqlen, int64_t n, int64_t hk,
@@ -502,8 +503,9 @@ int vm_gated_delta_fwd(const vm_delta *p, void *out, float *state, float scale,
  * (backward = 1), with packed = 1 for sequences given by offsets.  About 37 KB
  * (fp32: 25 KB) per 64 tokens and value head, backward 55 KB (37 KB) + 8 dk dv +
  * 512 dv bytes.
- * Returns -VM_ERR_SHAPE or -VM_ERR_UNSUPPORTED for sizes that no call takes,
- * as the other _workspace functions do.  Pure host function.
+ * Returns -VM_ERR_SHAPE or -VM_ERR_UNSUPPORTED for sizes that no call (on rows of
+ * whole 16-byte pieces, where the sizes allow them) takes, as the other
+ * _workspace functions do.  Pure host function.
  */
 int64_t vm_gated_delta_workspace(int64_t batch, int64_t seqlen, int64_t n,
                                  int64_t hv, int64_t dk, int64_t dv, int dtype,
@@ -527,6 +529,9 @@ typedef struct vm_delta_grad {
  *   whose g is below -120 has dg as if it were -120 (0).
  * Outputs must not overlap any input or each other.  Sums over value heads
  * and over a chunk are formed in a fixed order (deterministic).
+ * Sizes as forward; with bf16 rows of whole pieces (dk a multiple of 8, dv even)
+ * and dk > 64 also n hv ceil(dv / 32) below 2^22 (n hv in whole eights with
+ * offsets): VM_ERR_UNSUPPORTED beyond.
  */
 int vm_gated_delta_bwd(const vm_delta *p, const void *dout, const float *dstate,
                        const vm_delta_grad *grad, float scale, int64_t batch,

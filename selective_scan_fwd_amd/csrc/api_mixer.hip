@@ -23,9 +23,11 @@ using vmk::span;
 // Grids put chunk slots and sequences on x with up to 512 work-items each
 // (work-items below 2^32) and heads on y.
 constexpr int64_t kMaxSlots = (int64_t{1} << 23) - 1;
-// Scans put sequences, heads (whole rounds of 8) and up to 4 blocks of columns
-// on x, and the backward pass two scans.
+// Scans put sequences, heads (whole rounds of 8) and blocks of columns on x, and
+// the backward pass two scans: how many work-items that makes goes by the variant,
+// see sizes_fit().
 constexpr int64_t kMaxScans = (int64_t{1} << 21) - 8;
+constexpr int64_t kMaxItems = (int64_t{1} << 32) - 1;
 constexpr int64_t kMaxHeads = 65535;
 constexpr int64_t kMaxDeltaDim = 128, kMaxNormDim = 512, kMaxGrads = 65536;
 
@@ -75,13 +77,17 @@ int check_delta(const vm_delta *p, float scale, int64_t batch, int64_t seqlen, i
       !dims_ok({n, hv, dk, dv}, &z->states))
     return VM_ERR_SHAPE;
   if (p->offsets != nullptr ? batch != 1 : n != batch) return VM_ERR_SHAPE;
-  if (!std::isfinite(scale) || dk > kMaxDeltaDim || dv > kMaxDeltaDim || hv > kMaxHeads) return VM_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || dk > kMaxDeltaDim || dv > kMaxDeltaDim) return VM_ERR_UNSUPPORTED;
   // (the kernels reach the 64 tokens of a chunk with 31-bit byte offsets)
   for (int64_t stride : {z->qs, z->ks, z->vs, hv * dv})
     if (stride * 64 * 4 >= (int64_t{1} << 31)) return VM_ERR_UNSUPPORTED;
-  if (n * hv > kMaxScans || vmk::delta_slots(batch, seqlen, n, p->offsets != nullptr) > kMaxSlots)
-    return VM_ERR_UNSUPPORTED;
   return VM_OK;
+}
+
+// Whether every launch of a call holds its grid.
+bool sizes_fit(const vmk::DeltaArgs &a, int64_t n, bool bf16, bool backward) {
+  return a.hv <= kMaxHeads && n * a.hv <= kMaxScans && a.slots <= kMaxSlots &&
+         vmk::delta_scan_items(a, bf16, backward) <= kMaxItems;
 }
 
 vmk::DeltaArgs delta_args(const vm_delta *p, const DeltaSizes &z, float scale, int64_t batch, int64_t seqlen,
@@ -218,12 +224,17 @@ int64_t vm_gated_delta_workspace(int64_t batch, int64_t seqlen, int64_t n, int64
   if (!dims_ok({batch, seqlen, hv, dk}, &unused) || !dims_ok({batch, seqlen, hv, dv}, &unused) ||
       !dims_ok({n, hv, dk, dv}, &unused))
     return -VM_ERR_SHAPE;
+  if (packed != 0 ? batch != 1 : n != batch) return -VM_ERR_SHAPE;
   if (dk > kMaxDeltaDim || dv > kMaxDeltaDim) return -VM_ERR_UNSUPPORTED;
+  static const int32_t some = 0;
   vmk::DeltaArgs a = {};
+  a.off = packed != 0 ? &some : nullptr;
   a.slots = vmk::delta_slots(batch, seqlen, n, packed != 0);
+  a.nseq = static_cast<int>(n);
   a.hv = static_cast<int>(hv);
   a.dk = static_cast<int>(dk);
   a.dv = static_cast<int>(dv);
+  if (!sizes_fit(a, n, dtype == VM_BF16, backward != 0)) return -VM_ERR_UNSUPPORTED;
   Parts parts;
   delta_parts(a, dtype == VM_BF16, backward != 0, parts);
   return parts.total();
@@ -250,6 +261,10 @@ int vm_gated_delta_fwd(const vm_delta *p, void *out, float *state, float scale, 
   if (out == nullptr) return VM_ERR_NULL;
   const bool bf16 = dtype == VM_BF16;
   const int es = bf16 ? 2 : 4;
+  vmk::DeltaArgs a = delta_args(p, z, scale, batch, seqlen, n, hk, hv, dk, dv, reverse);
+  a.out = out;
+  a.state = state;
+  if (!sizes_fit(a, n, bf16, false)) return VM_ERR_UNSUPPORTED;
   const Span ins[] = {span(p->q, z.q_ext * es), span(p->k, z.k_ext * es), span(p->v, z.v_ext * es),
                       span(p->g, z.gates * 4), span(p->beta, z.gates * 4),
                       state == p->h0 ? Span{} : span(p->h0, z.states * 4),
@@ -259,9 +274,6 @@ int vm_gated_delta_fwd(const vm_delta *p, void *out, float *state, float scale, 
 
   hipStream_t s = static_cast<hipStream_t>(stream);
   Scratch ws(s);
-  vmk::DeltaArgs a = delta_args(p, z, scale, batch, seqlen, n, hk, hv, dk, dv, reverse);
-  a.out = out;
-  a.state = state;
   Parts parts;
   delta_parts(a, bf16, false, parts);
   st = parts.get(workspace, workspace_bytes, ws);
@@ -282,6 +294,16 @@ int vm_gated_delta_bwd(const vm_delta *p, const void *dout, const float *dstate,
     return VM_ERR_NULL;
   const bool bf16 = dtype == VM_BF16;
   const int es = bf16 ? 2 : 4;
+  vmk::DeltaArgs a = delta_args(p, z, scale, batch, seqlen, n, hk, hv, dk, dv, reverse);
+  a.dout = dout;
+  a.dstate = dstate;
+  a.dq = grad->dq;
+  a.dkey = grad->dk;
+  a.dval = grad->dv;
+  a.dg = grad->dg;
+  a.dbeta = grad->dbeta;
+  a.dh0 = grad->dh0;
+  if (!sizes_fit(a, n, bf16, true)) return VM_ERR_UNSUPPORTED;
   const int64_t keys = batch * seqlen * hk * dk;
   const Span ins[] = {span(p->q, z.q_ext * es), span(p->k, z.k_ext * es), span(p->v, z.v_ext * es),
                       span(p->g, z.gates * 4), span(p->beta, z.gates * 4), span(p->h0, z.states * 4),
@@ -293,15 +315,6 @@ int vm_gated_delta_bwd(const vm_delta *p, const void *dout, const float *dstate,
 
   hipStream_t s = static_cast<hipStream_t>(stream);
   Scratch ws(s);
-  vmk::DeltaArgs a = delta_args(p, z, scale, batch, seqlen, n, hk, hv, dk, dv, reverse);
-  a.dout = dout;
-  a.dstate = dstate;
-  a.dq = grad->dq;
-  a.dkey = grad->dk;
-  a.dval = grad->dv;
-  a.dg = grad->dg;
-  a.dbeta = grad->dbeta;
-  a.dh0 = grad->dh0;
   Parts parts;
   delta_parts(a, bf16, true, parts);
   st = parts.get(workspace, workspace_bytes, ws);

@@ -984,22 +984,27 @@ __global__ __launch_bounds__((kBlock<T, VEC, NP>)) void delta_scans_kernel(Delta
 }
 
 // Workgroups of a scan with cb column blocks, as place() takes them apart.
-uint32_t scan_blocks(const DeltaArgs &a, int cb) {
+int64_t scan_blocks(const DeltaArgs &a, int cb) {
   int64_t heads = static_cast<int64_t>(a.nseq) * a.hv;
   if (a.off != nullptr) heads = (heads + kXcd - 1) / kXcd * kXcd;
-  return static_cast<uint32_t>(heads * cb);
+  return heads * cb;
 }
 
+// One variant of the kernels and its launch.
 template <typename T, int DK, bool VEC, int NP>
-hipError_t launch(const DeltaArgs &a, bool back, hipStream_t s) {
-  const int cb = (a.dv + 16 * NP - 1) / (16 * NP);
-  const dim3 block(kBlock<T, VEC, NP>);
-  if (back)
-    hipLaunchKernelGGL((delta_scans_kernel<T, DK, VEC, NP>), dim3(2 * scan_blocks(a, cb)), block, 0, s, a, cb);
-  else
-    hipLaunchKernelGGL((delta_scan_kernel<T, DK, VEC, NP>), dim3(scan_blocks(a, cb)), block, 0, s, a, cb);
-  return hipGetLastError();
-}
+struct Scan {
+  static int columns(const DeltaArgs &a) { return (a.dv + 16 * NP - 1) / (16 * NP); }
+  static int64_t blocks(const DeltaArgs &a, bool back) { return scan_blocks(a, columns(a)) * (back ? 2 : 1); }
+  static int64_t items(const DeltaArgs &a, bool back) { return blocks(a, back) * kBlock<T, VEC, NP>; }
+  static hipError_t launch(const DeltaArgs &a, bool back, hipStream_t s) {
+    const dim3 grid(static_cast<uint32_t>(blocks(a, back))), block(kBlock<T, VEC, NP>);
+    if (back)
+      hipLaunchKernelGGL((delta_scans_kernel<T, DK, VEC, NP>), grid, block, 0, s, a, columns(a));
+    else
+      hipLaunchKernelGGL((delta_scan_kernel<T, DK, VEC, NP>), grid, block, 0, s, a, columns(a));
+    return hipGetLastError();
+  }
+};
 // As few pairs of waves to a workgroup as give no more workgroups than the card
 // has compute units: each wave then has a SIMD of its own, and fewer wait for
 // each other.  With more workgroups, as many pairs as LDS and registers hold
@@ -1013,29 +1018,34 @@ hipError_t launch(const DeltaArgs &a, bool back, hipStream_t s) {
 //     backward       223* 251 -   512 446* -    1098 920* -  1379 1188* - (128: 2153 1772* -)
 // Just past the number of compute units a second, nearly empty round begins: 64
 // heads of 128 are 256 workgroups of two pairs, 80 heads 320 (226 and 400 us).
-template <typename T, int DK, bool VEC>
-hipError_t launch(const DeltaArgs &a, bool back, hipStream_t s) {
-  const auto fits = [&](int pairs) {
-    return scan_blocks(a, (a.dv + 16 * pairs - 1) / (16 * pairs)) * (back ? 2 : 1) <= 256;
-  };
+template <typename T, int DK, bool VEC, typename F>
+auto with_scan(const DeltaArgs &a, bool back, F f) {
   if constexpr (kLoaders<T, VEC, 1>)
-    if (fits(1)) return launch<T, DK, VEC, 1>(a, back, s);
+    if (Scan<T, DK, VEC, 1>::blocks(a, back) <= 256) return f(Scan<T, DK, VEC, 1>());
   if constexpr (DK == 64)
-    if (!fits(2)) return launch<T, DK, VEC, 4>(a, back, s);
-  return launch<T, DK, VEC, 2>(a, back, s);
+    if (Scan<T, DK, VEC, 2>::blocks(a, back) > 256) return f(Scan<T, DK, VEC, 4>());
+  return f(Scan<T, DK, VEC, 2>());
 }
-template <typename T, int DK>
-hipError_t launch(const DeltaArgs &a, bool back, hipStream_t s) {
+template <typename T, int DK, typename F>
+auto with_scan(const DeltaArgs &a, bool back, F f) {
   const bool vec = delta_vec(a, sizeof(T)) && delta_vec_values(a, a.v, a.vs, sizeof(T), 4) &&
                    (!back || delta_vec_values(a, a.dout, static_cast<int64_t>(a.hv) * a.dv, sizeof(T), 4));
-  return vec ? launch<T, DK, true>(a, back, s) : launch<T, DK, false>(a, back, s);
+  return vec ? with_scan<T, DK, true>(a, back, f) : with_scan<T, DK, false>(a, back, f);
+}
+template <typename F>
+auto with_scan(const DeltaArgs &a, bool bf16, bool back, F f) {
+  if (a.dk <= 64) return bf16 ? with_scan<bf16_t, 64>(a, back, f) : with_scan<float, 64>(a, back, f);
+  return bf16 ? with_scan<bf16_t, 128>(a, back, f) : with_scan<float, 128>(a, back, f);
 }
 
 }  // namespace
 
 hipError_t launch_delta_scan(const DeltaArgs &a, bool bf16, bool back, hipStream_t s) {
-  if (a.dk <= 64) return bf16 ? launch<bf16_t, 64>(a, back, s) : launch<float, 64>(a, back, s);
-  return bf16 ? launch<bf16_t, 128>(a, back, s) : launch<float, 128>(a, back, s);
+  return with_scan(a, bf16, back, [&](auto scan) { return scan.launch(a, back, s); });
+}
+
+int64_t delta_scan_items(const DeltaArgs &a, bool bf16, bool back) {
+  return with_scan(a, bf16, back, [&](auto scan) { return scan.items(a, back); });
 }
 
 }  // namespace vmk

@@ -114,6 +114,8 @@ int64_t delta_slots(int64_t batch, int64_t L, int64_t n, bool packed);
 hipError_t launch_delta_prep(const DeltaArgs &a, bool bf16, bool backward, hipStream_t s);
 // Forward: out and state; back: S and V, and dS, dR, dv and dh0.
 hipError_t launch_delta_scan(const DeltaArgs &a, bool bf16, bool back, hipStream_t s);
+// Work-items of that launch.
+int64_t delta_scan_items(const DeltaArgs &a, bool bf16, bool back);
 hipError_t launch_delta_grad(const DeltaArgs &a, bool bf16, hipStream_t s);
 
 struct StepArgs {
