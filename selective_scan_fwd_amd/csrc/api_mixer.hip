@@ -206,14 +206,6 @@ int check_norm(const vm_head_norm *p, int64_t batch, int64_t seqlen, int64_t hq,
   return VM_OK;
 }
 
-// Partial sums of one launch over up to kClipTable of `count` gradients: all
-// launches together at most kClipPartials, at least one each.
-int64_t clip_launches(int64_t count) { return (count + vmk::kClipTable - 1) / vmk::kClipTable; }
-int64_t clip_partials(int64_t count) {
-  const int64_t launches = clip_launches(count);
-  return launches > 0 && vmk::kClipPartials / launches > 1 ? vmk::kClipPartials / launches : 1;
-}
-
 }  // namespace
 
 extern "C" {
@@ -249,7 +241,7 @@ int64_t vm_head_norm_rope_workspace(int64_t dim) {
 int64_t vm_clip_grad_workspace(int64_t count) {
   if (count < 0) return -VM_ERR_SHAPE;
   if (count > kMaxGrads) return -VM_ERR_UNSUPPORTED;
-  return Parts::whole((clip_launches(count) * clip_partials(count) + 1) * 8);
+  return Parts::whole(vmk::kClipPartials * 8);
 }
 
 int vm_gated_delta_fwd(const vm_delta *p, void *out, float *state, float scale, int64_t batch, int64_t seqlen,
@@ -438,7 +430,6 @@ int vm_clip_grad_norm(const vm_grad_tensor *list, int64_t count, float max_norm,
   hipStream_t s = static_cast<hipStream_t>(stream);
   Scratch ws(s);
   int st = VM_OK;
-  const int64_t most = clip_partials(count);
   double *partial = nullptr;
   Parts parts;
   parts.add(&partial, vm_clip_grad_workspace(count));
@@ -462,12 +453,11 @@ int vm_clip_grad_norm(const vm_grad_tensor *list, int64_t count, float max_norm,
       }
       t.first[t.n] = at;
       if (t.n == 0) continue;
+      const int blocks = static_cast<int>(at < vmk::kClipPartials ? at : vmk::kClipPartials);
       if (pass == 0) {
-        const int blocks = static_cast<int>(at < most ? at : most);
-        st = hip_status(vmk::launch_clip_sums(t, partial + used, blocks, s));
-        used += blocks;
+        st = hip_status(vmk::launch_clip_sums(t, partial, used, blocks, s));
+        used = blocks > used ? blocks : used;
       } else {
-        const int blocks = static_cast<int>(at < vmk::kClipPartials ? at : vmk::kClipPartials);
         st = hip_status(vmk::launch_clip_scale(t, partial, used, max_norm, norm, blocks, s));
       }
       if (st != VM_OK) return st;

@@ -37,7 +37,7 @@ hipError_t launch_norm(NormArgs a, bool bf16, bool back, hipStream_t s);
 constexpr int kClipTable = 120;        // tensors of one launch (kernel arguments)
 constexpr int64_t kClipChunk = 2048;   // elements
 constexpr uint32_t kClipRun = 8;       // chunks of a block at a time, at most
-constexpr int kClipPartials = 1024;   // blocks: four of 512 threads fill a compute unit
+constexpr int kClipPartials = 1024;   // blocks of a launch, at most: four of 512 threads fill a compute unit
 struct ClipTable {
   const void *in[kClipTable];
   void *out[kClipTable];
@@ -46,7 +46,8 @@ struct ClipTable {
   uint8_t bf16[kClipTable];
   int n;
 };
-hipError_t launch_clip_sums(const ClipTable &t, double *partial, int blocks, hipStream_t s);
+// Adds to the first `have` partial sums, writes the rest of its blocks'.
+hipError_t launch_clip_sums(const ClipTable &t, double *partial, int have, int blocks, hipStream_t s);
 hipError_t launch_clip_scale(const ClipTable &t, const double *partial, int partials, float max_norm,
                              float *norm, int blocks, hipStream_t s);
 hipError_t launch_clip_norm_only(const double *partial, int partials, float *norm, hipStream_t s);
