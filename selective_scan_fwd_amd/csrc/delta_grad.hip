@@ -133,7 +133,7 @@ __device__ __forceinline__ void masked_tiles(const uint16_t *a, const uint16_t *
 // One workgroup per (chunk slot, key head), the value heads of the key head in
 // turn: dq and dk are summed over them in registers.
 //
-// 2 x 4097 tokens, 8 and 16 heads of 128, bf16: 245 us for 480 MB, mostly states
+// 2 x 4097 tokens, 8 and 16 heads of 128, bf16: 250 us for 480 MB, mostly states
 // (matrix instructions busy 17 % of it, the vector ones 27 %, LDS 26 %); 64 x 197
 // tokens, 6 heads of 64, fp32: 115 us.  One workgroup fills a compute unit's LDS
 // and registers, so its phases (a slice's loads, their splitting, the products,

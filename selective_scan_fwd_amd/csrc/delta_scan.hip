@@ -27,7 +27,7 @@ namespace {
 // tokens, 16 value heads of 128, bf16, 65 chunks, took 211 us where one wave to 16
 // columns took 281, and 183 with waves of their own for the loads, see
 // load_chunks(); with nothing loaded after the first chunk 163.  Those were with
-// two terms of what enters the output only; with all three it takes 202 (3.1 us a
+// two terms of what enters the output only; with all three it takes 203 (3.1 us a
 // chunk).  (128 x 197 tokens, 6 heads of 64, fp32: 83 us; 40 packed sequences of
 // up to 1500 tokens, 8 value heads of 100: 86 us, of two terms 77, and 84 in the
 // order given and in runs over the XCDs.)
@@ -535,8 +535,9 @@ constexpr int kBlock = Shape<NP>::kThreads * (kLoaders<T, VEC, NP> ? 2 : 1);
 // the triangles after the second; what is left of the triangles (blocks from kEnd
 // on) at the start of the next chunk.  v (BACK: dout) has one buffer, which is
 // read at a chunk's start and loaded again, for the next chunk, after the first
-// barrier (a second one would not fit beside the triangles of keys of 128).  Loads return in order:
-// what the next chunk needs has come when no more are out than were issued since.
+// barrier (a second one would not fit beside the triangles of keys of 128).  Loads
+// return in order: what the next chunk needs has come when no more are out than
+// were issued since.
 template <bool BACK, typename Load, typename Lds>
 __device__ __forceinline__ void load_chunks(Load &next, const DeltaArgs &A, const Seq &q, const uint16_t *m, int64_t c0,
                                             int64_t step, Lds (&lds)[2], uint16_t *v) {
@@ -968,8 +969,8 @@ __global__ __launch_bounds__((kBlock<T, VEC, NP>)) void delta_scan_kernel(DeltaA
 
 // The backward scan needs nothing of the forward one, so one launch runs both:
 // half of the workgroups each, the longer backward ones first.  (2 x 4097 tokens,
-// 16 value heads of 128, bf16: 290 us, one after the other 154 and 232, and 228
-// with loading waves; 64 x 197, 6 heads of 64, fp32: 95, 44 and 62.)
+// 16 value heads of 128, bf16: 290 us, one after the other 154 and 232, and 224 to
+// 234 with loading waves; 64 x 197, 6 heads of 64, fp32: 96, 44 and 62.)
 template <typename T, int DK, bool VEC, int NP>
 __global__ __launch_bounds__((kBlock<T, VEC, NP>)) void delta_scans_kernel(DeltaArgs A, int colblocks) {
   __shared__ union {

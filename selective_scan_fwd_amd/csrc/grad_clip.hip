@@ -11,11 +11,12 @@
 // of its own (310 MB of bf16: sums 55 us; with chunks of 16384 dealt out one by
 // one 85 us).  Longer lists take a launch for every 120, each over the whole card,
 // block b adding to partial sum b, so there are no more of them than of one
-// launch's (6000 tensors of 4 MB: sums 1.3 ms, with partial sums of its own for each
-// launch, 20 blocks of them, 20.8).  The second pass goes back from the last run, which is nearest
-// still, to the first: 97 us, forwards 105 us.  Its loads and stores are past
-// their last use here and marked so; without that the next pass over other
-// memory waits for the written lines to leave the cache (sums 85 us).
+// launch's (6000 tensors of 4 MB: sums 1.3 ms; with the partial sums divided
+// over the launches, 20 blocks each, 20.8).  The second pass goes back from the
+// last run, which is nearest still, to the first: 97 us, forwards 105 us.  Its
+// loads and stores are past their last use here and marked so; without that the
+// next pass over other memory waits for the written lines to leave the cache
+// (sums 85 us).
 #include <hip/hip_runtime.h>
 
 #include "mixer_internal.h"

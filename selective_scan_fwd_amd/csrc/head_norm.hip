@@ -6,8 +6,10 @@
 //          dx_i = r (e_i - n_i c sum(e n))
 //               = r^3 (eps e_i + c (e_i (sum x^2 - x_i^2) - x_i (sum(e x) - e_i x_i)))
 // The second form of dx is computed: a value's own terms leave both sums before
-// the difference is taken, so a head of one value (or one that dominates) keeps
-// its eps term, which the first form loses to cancellation.
+// the difference is taken, so a head whose other values are 0 (a head of one value
+// always) keeps its eps term, which the first form loses to cancellation.  Beside
+// other values they leave the sums to within a rounding of the sums, 2^-24 of x^2
+// for a value that dominates: there both forms are alike.
 //
 // Bound by memory: x is read once and y written once (back: x and dy read, dx
 // written).  A head is held by a group of lanes, 8 values to a lane as two
@@ -126,8 +128,10 @@ __device__ __forceinline__ float dot4(f32x4 a, f32x4 b) {
   return __builtin_fmaf(a[0], b[0], __builtin_fmaf(a[1], b[1], __builtin_fmaf(a[2], b[2], a[3] * b[3])));
 }
 
-// One value of dx (see above).  The squares and products here round as the
-// sums' own terms did, so that they leave the sums exactly.
+// One value of dx (see above).  The squares and products are rounded by
+// themselves: that is what a sum is in which all other terms are 0, and such a sum
+// they leave exactly.  (A sum of more terms took some of them unrounded, and was
+// rounded on the way.)
 __device__ __forceinline__ float own_term(float e, float x, float squares, float along, float over, float eps, float r) {
 #pragma clang fp contract(off)
   const float rest = e * (squares - x * x) - x * (along - e * x);
