@@ -641,6 +641,291 @@ int vm_clip_grad_norm(const vm_grad_tensor *list, int64_t count, float max_norm,
 /* Workspace of vm_clip_grad_norm.  Pure host function. */
 int64_t vm_clip_grad_workspace(int64_t count);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Prompts and single tokens: the selective scan and its short convolution over
+ * rows of tokens, as a language model's block has them, and the norms around a
+ * block.  Token tensors are token-major, [batch, seqlen, dim], with a token stride
+ * (elements; 0 = dense, otherwise >= the row's values) that lets them be slices of
+ * one projection's row; the stride from one batch row to the next is seqlen token
+ * strides.  Strides and workspaces are as in the section above.  The dtype selects
+ * the storage of token tensors, of their gradients and of kept windows; parameters,
+ * states and their gradients are fp32.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * The sequences of a call; NULL: every batch row is one, and states are numbered
+ * as they are.
+ *   offsets  [n + 1] int32  NULL: n = batch sequences of seqlen tokens.  Else batch
+ *                           is 1 and sequence i is tokens offsets[i] ..
+ *                           offsets[i+1]-1 of the packed row: non-decreasing from 0
+ *                           to at most seqlen (a precondition; the kernels clamp what
+ *                           they read to [0, seqlen], and with other offsets the
+ *                           results are undefined but no access leaves the tensors).
+ *                           A sequence may be empty; its state stays its first.
+ *                           Tokens behind the last sequence are not written.
+ *   slots    [n] int32      where in h0 and state (both of n_slots states) each
+ *                           sequence's state lies; NULL: sequence i has state i, of n.
+ *                           A sequence whose slot is outside [0, n_slots) starts from
+ *                           zero and its state is not kept.  Two sequences must not
+ *                           name the same slot.
+ *   fresh    [n] int32      nonzero: the sequence starts from zero though h0 is given;
+ *                           NULL: none does
+ * The backward calls take offsets only (slots or fresh: VM_ERR_FLAG).
+ */
+typedef struct vm_sequences {
+  const int32_t *offsets;
+  const int32_t *slots;
+  const int32_t *fresh;
+  int64_t n;
+  int64_t n_slots;
+} vm_sequences;
+
+/*
+ * Depthwise causal convolution over rows of tokens, with SiLU (silu = 1) or
+ * without: with x before a sequence's first token from its kept window,
+ *   v_t = bias + sum_k w_k x_{t-width+1+k},   out_t = SiLU(v_t) or v_t
+ *   x [batch, seqlen, dim] (dtype), token stride x_stride; w [dim, width], bias
+ *   [dim] (NULL = 0) fp32; out dense.
+ *   h0, state [n or n_slots, width - 1, dim] (dtype): the inputs before the first
+ *   token and the last ones, oldest first; NULL = 0 / not kept.  state may be h0
+ *   itself, but must not overlap it otherwise.
+ * width in [2, 4], dim up to 2^22 (VM_ERR_UNSUPPORTED).  One launch, no temporary
+ * memory.
+ */
+int vm_prompt_conv(const vm_sequences *q, const void *x, int64_t x_stride,
+                   const float *w, const float *bias, const void *h0,
+                   void *state, void *out, int64_t batch, int64_t seqlen,
+                   int64_t dim, int64_t width, int silu, int dtype,
+                   void *stream);
+
+/* Gradients of vm_prompt_conv (dense; the caller's buffers). */
+typedef struct vm_conv_grad {
+  void *dx;      /* [batch, seqlen, dim] (dtype) */
+  float *dw;     /* [dim, width] */
+  float *dbias;  /* [dim] or NULL (not computed) */
+  void *dh0;     /* [n, width - 1, dim] (dtype) or NULL */
+} vm_conv_grad;
+
+/*
+ * Backward pass of vm_prompt_conv: the gradients of
+ * L = sum(dout * out) + sum(dstate * state) for the same arguments.
+ *   dout [batch, seqlen, dim] (dtype), dense; dstate [n, width - 1, dim] (dtype) or
+ *   NULL (= 0).  Gradients of tokens of no sequence are not written.  Sums are
+ *   formed in a fixed order (deterministic).
+ */
+int vm_prompt_conv_bwd(const vm_sequences *q, const void *x, int64_t x_stride,
+                       const float *w, const float *bias, const void *h0,
+                       const void *dout, const void *dstate,
+                       const vm_conv_grad *grad, int64_t batch, int64_t seqlen,
+                       int64_t dim, int64_t width, int silu, int dtype,
+                       void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace of vm_prompt_conv_bwd (packed = 1 with offsets).  Pure host function. */
+int64_t vm_prompt_conv_workspace(int64_t batch, int64_t seqlen, int64_t n,
+                                 int64_t dim, int64_t width, int dtype,
+                                 int packed);
+
+/*
+ * One token of that convolution for every row of a batch, on kept windows:
+ * x [batch, dim] (dtype), row stride x_stride; state [n_slots, width - 1, dim]
+ * (dtype) is advanced in place; out [batch, dim], dense.  slots [batch] int32: the
+ * window of each row, NULL = row b uses window b (batch <= n_slots, else
+ * VM_ERR_SHAPE).  A row whose slot is outside [0, n_slots) is idle: its out is zero
+ * and it touches no window.  Two rows must not name the same slot.  One launch, no
+ * temporary memory.
+ */
+int vm_token_conv(const void *x, int64_t x_stride, const float *w,
+                  const float *bias, void *state, const int32_t *slots,
+                  void *out, int64_t batch, int64_t n_slots, int64_t dim,
+                  int64_t width, int silu, int dtype, void *stream);
+
+/*
+ * Inputs of the selective scan over rows of tokens (vm_scan_dir's, token-major):
+ *   u, delta, z  [batch, seqlen, dim]     z NULL: no gate
+ *   B, C         [batch, seqlen, dstate]
+ *   A [dim, dstate], D [dim] (NULL = 0), delta_bias [dim] (NULL = 0)  fp32
+ * and the token strides of the five token tensors.
+ */
+typedef struct vm_scan_rows {
+  const void *u;
+  const void *delta;
+  const float *A;
+  const void *B;
+  const void *C;
+  const float *D;
+  const float *delta_bias;
+  const void *z;
+  int64_t u_stride;
+  int64_t delta_stride;
+  int64_t B_stride;
+  int64_t C_stride;
+  int64_t z_stride;
+} vm_scan_rows;
+
+/*
+ * The selective scan over rows of tokens, from given states.  For every sequence
+ * and channel, with the recurrence of vm_selective_scan_fwd:
+ *   h_t = exp(dt_t A) h_{t-1} + dt_t B_t u_t,  y_t = C_t h_t + D u_t,
+ *   out_t = y_t SiLU(z_t)  (z != NULL),  y_t otherwise
+ *   h0, state [n or n_slots, dim, dstate] fp32: first and last states; NULL = 0 /
+ *   not kept.  state may be h0 itself, but must not overlap it otherwise.
+ *   out [batch, seqlen, dim] (dtype), dense.  options: VM_DELTA_SOFTPLUS or 0 (the
+ *   write is dt; VM_ZOH is VM_ERR_FLAG).
+ * dstate in [1, 16], dim up to 2^22, token strides below 2^23 elements
+ * (VM_ERR_UNSUPPORTED).  Long sequences of few channels are walked in chunks at
+ * once, whose states need a workspace (vm_prompt_scan_workspace; 0 bytes where
+ * there is one chunk to a sequence).
+ */
+int vm_prompt_scan(const vm_scan_rows *p, const vm_sequences *q,
+                   const float *h0, float *state, void *out, int64_t batch,
+                   int64_t seqlen, int64_t dim, int64_t dstate, int dtype,
+                   int options, void *workspace, int64_t workspace_bytes,
+                   void *stream);
+
+/*
+ * Workspace of vm_prompt_scan (backward = 0) or vm_prompt_scan_bwd (backward = 1),
+ * with packed = 1 for sequences given by offsets.  The backward pass takes about 4
+ * bytes per token and channel.  Pure host function.
+ */
+int64_t vm_prompt_scan_workspace(int64_t batch, int64_t seqlen, int64_t n,
+                                 int64_t dim, int64_t dstate, int packed,
+                                 int backward);
+
+/* Gradients of the selective scan over rows (dense; the caller's buffers). */
+typedef struct vm_rows_grad {
+  void *du;           /* [batch, seqlen, dim] (dtype) */
+  void *ddelta;       /* [batch, seqlen, dim] (dtype) */
+  float *dA;          /* [dim, dstate] */
+  void *dB;           /* [batch, seqlen, dstate] (dtype) */
+  void *dC;           /* [batch, seqlen, dstate] (dtype) */
+  float *dD;          /* [dim] or NULL (not computed) */
+  float *ddelta_bias; /* [dim] or NULL */
+  void *dz;           /* [batch, seqlen, dim] (dtype): required exactly with z */
+  float *dh0;         /* [n, dim, dstate] or NULL */
+} vm_rows_grad;
+
+/*
+ * Backward pass of vm_prompt_scan: the gradients of
+ * L = sum(dout * out) + sum(dstate * state) for the same arguments.
+ *   dout [batch, seqlen, dim] (dtype), dense; dstate [n, dim, N] or NULL (= 0).
+ * Gradients of tokens of no sequence are not written.  Outputs must not overlap any
+ * input or each other.  Sums over channels, rows and chunks are formed in a fixed
+ * order (deterministic).
+ */
+int vm_prompt_scan_bwd(const vm_scan_rows *p, const vm_sequences *q,
+                       const float *h0, const void *dout, const float *dstate,
+                       const vm_rows_grad *grad, int64_t batch, int64_t seqlen,
+                       int64_t dim, int64_t N, int dtype, int options,
+                       void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * One token of the selective scan for every row of a batch, on states that are
+ * kept: the rows of p with seqlen 1; state [n_slots, dim, dstate] fp32 is updated
+ * in place; out [batch, dim] (dtype), dense; slots as for vm_token_conv.  One
+ * launch, no temporary memory.
+ */
+int vm_token_scan(const vm_scan_rows *p, float *state, const int32_t *slots,
+                  void *out, int64_t batch, int64_t n_slots, int64_t dim,
+                  int64_t dstate, int dtype, int options, void *stream);
+
+/*
+ * Options of the norms around a block (others VM_ERR_FLAG):
+ *   VM_NORM_CENTER      before: take the mean off first
+ *   VM_NORM_GATE_FIRST  after: the norm of x SiLU(z), not SiLU(z) times that of x
+ */
+enum { VM_NORM_CENTER = 4, VM_NORM_GATE_FIRST = 8 };
+
+/*
+ * What a norm around a block is taken of.
+ *   x       [rows, dim] (dtype), row stride x_stride (0 = dense)
+ *   w       [w_dim] fp32 gains, NULL = 1; w_dim = dim (or 0), or, after a block,
+ *           group: the same gains for every group
+ *   b       [dim] fp32, NULL = 0; before a block only (else VM_ERR_FLAG)
+ *   scale   [dim] fp32: residual scale of each channel, NULL = 1; factor: of all
+ *   z       [rows, dim] (dtype), row stride z_stride: the gate after a block, NULL =
+ *           none; NULL before one
+ *   group   channels that are normed together, a divisor of dim; 0 = dim (before a
+ *           block only dim)
+ */
+typedef struct vm_block_norm {
+  const void *x;
+  const float *w;
+  const float *b;
+  const float *scale;
+  const void *z;
+  int64_t x_stride;
+  int64_t z_stride;
+  int64_t w_dim;
+  int64_t group;
+  float eps;
+  float factor;
+  int32_t options;
+} vm_block_norm;
+
+/*
+ * The norm before a block, of the residual with the last block's output added:
+ *   r = residual + factor scale x,   y = (r - mean) / sqrt(mean (r - mean)^2 + eps)
+ *   w + b    (mean = 0 without VM_NORM_CENTER; of r in fp32, before it is rounded)
+ *   residual, r [rows, dim] (rdtype: dtype, or VM_F32 beside bf16 rows; else
+ *   VM_ERR_DTYPE), dense; residual NULL = 0, r NULL = not kept, r may be residual
+ *   itself; y [rows, dim] (dtype), dense.
+ * dim up to 16384, rows below 2^31 (VM_ERR_UNSUPPORTED).  One launch.
+ */
+int vm_norm_before(const vm_block_norm *p, const void *residual, void *y,
+                   void *r, int64_t rows, int64_t dim, int dtype, int rdtype,
+                   void *stream);
+
+/* Gradients of the norms around a block; NULL = not computed. */
+typedef struct vm_norm_grad {
+  void *dx;         /* [rows, dim] (dtype); after a block required */
+  void *dresidual;  /* [rows, dim] (rdtype); before a block only */
+  void *dz;         /* [rows, dim] (dtype): after a block, required exactly with z */
+  float *dw;        /* [w_dim] */
+  float *db;        /* [dim]; before a block only */
+  float *dscale;    /* [dim] */
+} vm_norm_grad;
+
+/*
+ * Backward pass of vm_norm_before at the residual r that it gave: from dy (dtype)
+ * and dr (rdtype; what else arrives at r, NULL = 0), both dense,
+ *   dresidual = dr + the norm's gradient,  dx = factor scale dresidual
+ * and dw, db, dscale (only where w, b, scale are given, else VM_ERR_NULL; dscale
+ * needs x, which is not read otherwise and may be NULL).  At least one of dx and
+ * dresidual is given.  Summed in a fixed order (deterministic); a workspace is
+ * needed only for dw, db or dscale.
+ */
+int vm_norm_before_bwd(const vm_block_norm *p, const void *r, const void *dy,
+                       const void *dr, const vm_norm_grad *grad, int64_t rows,
+                       int64_t dim, int dtype, int rdtype, void *workspace,
+                       int64_t workspace_bytes, void *stream);
+
+/*
+ * The norm after a block, by groups of channels, gated and added to the residual:
+ *   y = n(x) w SiLU(z)  or (VM_NORM_GATE_FIRST)  n(x SiLU(z)) w,
+ *   n(v) = v / sqrt(mean v^2 + eps) over a group;  out = residual + factor scale y
+ *   residual, out [rows, dim] (rdtype), dense; residual NULL = 0; out may be
+ *   residual itself.
+ * group up to 16384, dim up to 2^22, rows below 2^31 (VM_ERR_UNSUPPORTED).  One
+ * launch.
+ */
+int vm_norm_after(const vm_block_norm *p, const void *residual, void *out,
+                  int64_t rows, int64_t dim, int dtype, int rdtype,
+                  void *stream);
+
+/*
+ * Its backward: from dout [rows, dim] (rdtype), dense, the gradients dx, dz, dw and
+ * dscale (the residual's is dout itself).  Deterministic; a workspace as above.
+ */
+int vm_norm_after_bwd(const vm_block_norm *p, const void *dout,
+                      const vm_norm_grad *grad, int64_t rows, int64_t dim,
+                      int dtype, int rdtype, void *workspace,
+                      int64_t workspace_bytes, void *stream);
+
+/* Workspace of the norms' backward passes (group 0 = dim).  Pure host function. */
+int64_t vm_block_norm_workspace(int64_t rows, int64_t dim, int64_t group);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,9 +12,12 @@ Names and argument order follow the C ABI:
   vm_atrous_scatter, vm_pool_scan_repeat, vm_ss2d_scan_fwd,
   vm_causal_conv1d_silu, vm_causal_conv1d_silu_bwd, vm_selective_scan_bwd,
   vm_bidir_scan_bwd, vm_pool_scan_repeat_bwd, vm_ss2d_scan_bwd,
-  vm_atrous_group_len; and the matrix-state mixers: vm_gated_delta_fwd,
+  vm_atrous_group_len; the matrix-state mixers: vm_gated_delta_fwd,
   vm_gated_delta_bwd, vm_gated_delta_step, vm_head_norm_rope,
-  vm_head_norm_rope_bwd, vm_clip_grad_norm.
+  vm_head_norm_rope_bwd, vm_clip_grad_norm; and the scan over prompts and single
+  tokens with the norms around a block: vm_prompt_conv, vm_prompt_conv_bwd,
+  vm_token_conv, vm_prompt_scan, vm_prompt_scan_bwd, vm_token_scan,
+  vm_norm_before, vm_norm_before_bwd, vm_norm_after, vm_norm_after_bwd.
 """
 from __future__ import annotations
 
@@ -31,6 +34,7 @@ LIB_PATH = os.path.join(_PKG, "libvmscan.so")
 VM_F32, VM_BF16 = 0, 1
 VM_DELTA_SOFTPLUS, VM_ZOH = 1, 2
 VM_NORM_L2, VM_ROPE_INTERLEAVED = 1, 2
+VM_NORM_CENTER, VM_NORM_GATE_FIRST = 4, 8
 VM_OK = 0
 STATUS_NAMES = {0: "VM_OK", 1: "VM_ERR_NULL", 2: "VM_ERR_SHAPE", 3: "VM_ERR_DTYPE", 4: "VM_ERR_FLAG",
                 5: "VM_ERR_ALIAS", 6: "VM_ERR_UNSUPPORTED", 7: "VM_ERR_HIP", 8: "VM_ERR_ALLOC"}
@@ -43,7 +47,10 @@ EXPORTED = ("vm_status_string", "vm_version", "vm_selective_scan_fwd", "vm_bidir
             "vm_ss2d_scan_bwd",
             "vm_gated_delta_fwd", "vm_gated_delta_bwd", "vm_gated_delta_step",
             "vm_head_norm_rope", "vm_head_norm_rope_bwd", "vm_clip_grad_norm",
-            "vm_gated_delta_workspace", "vm_head_norm_rope_workspace", "vm_clip_grad_workspace")
+            "vm_gated_delta_workspace", "vm_head_norm_rope_workspace", "vm_clip_grad_workspace",
+            "vm_prompt_conv", "vm_prompt_conv_bwd", "vm_token_conv", "vm_prompt_scan", "vm_prompt_scan_bwd",
+            "vm_token_scan", "vm_norm_before", "vm_norm_before_bwd", "vm_norm_after", "vm_norm_after_bwd",
+            "vm_prompt_conv_workspace", "vm_prompt_scan_workspace", "vm_block_norm_workspace")
 
 
 class VmScanDir(ctypes.Structure):
@@ -81,6 +88,40 @@ class VmGradTensor(ctypes.Structure):
     """struct vm_grad_tensor (one gradient of vm_clip_grad_norm)."""
     _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("elems", ctypes.c_int64),
                 ("dtype", ctypes.c_int64)]
+
+
+class VmSequences(ctypes.Structure):
+    """struct vm_sequences (the sequences of a call over rows of tokens)."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("offsets", "slots", "fresh")] + \
+               [(k, ctypes.c_int64) for k in ("n", "n_slots")]
+
+
+class VmConvGrad(ctypes.Structure):
+    """struct vm_conv_grad (gradient buffers of the convolution over rows)."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("dx", "dw", "dbias", "dh0")]
+
+
+class VmScanRows(ctypes.Structure):
+    """struct vm_scan_rows (inputs of the selective scan over rows)."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("u", "delta", "A", "B", "C", "D", "delta_bias", "z")] + \
+               [(k, ctypes.c_int64) for k in ("u_stride", "delta_stride", "B_stride", "C_stride", "z_stride")]
+
+
+class VmRowsGrad(ctypes.Structure):
+    """struct vm_rows_grad (gradient buffers of the selective scan over rows)."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("du", "ddelta", "dA", "dB", "dC", "dD", "ddelta_bias", "dz", "dh0")]
+
+
+class VmBlockNorm(ctypes.Structure):
+    """struct vm_block_norm (inputs of the norms around a block)."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("x", "w", "b", "scale", "z")] + \
+               [(k, ctypes.c_int64) for k in ("x_stride", "z_stride", "w_dim", "group")] + \
+               [("eps", ctypes.c_float), ("factor", ctypes.c_float), ("options", ctypes.c_int32)]
+
+
+class VmNormGrad(ctypes.Structure):
+    """struct vm_norm_grad (gradient buffers of the norms around a block)."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("dx", "dresidual", "dz", "dw", "db", "dscale")]
 
 
 class VmError(RuntimeError):
@@ -135,10 +176,29 @@ def load_library():
             lib.vm_gated_delta_workspace.argtypes = [I64, I64, I64, I64, I64, I64, I, I, I]
             lib.vm_head_norm_rope_workspace.argtypes = [I64]
             lib.vm_clip_grad_workspace.argtypes = [I64]
-            for name in ("vm_gated_delta_workspace", "vm_head_norm_rope_workspace", "vm_clip_grad_workspace"):
+            Q, R, B = ctypes.POINTER(VmSequences), ctypes.POINTER(VmScanRows), ctypes.POINTER(VmBlockNorm)
+            K = ctypes.POINTER(VmNormGrad)
+            lib.vm_prompt_conv.argtypes = [Q, P, I64, P, P, P, P, P, I64, I64, I64, I64, I, I, P]
+            lib.vm_prompt_conv_bwd.argtypes = [Q, P, I64, P, P, P, P, P, ctypes.POINTER(VmConvGrad), I64, I64, I64, I64, I, I,
+                                               P, I64, P]
+            lib.vm_token_conv.argtypes = [P, I64, P, P, P, P, P, I64, I64, I64, I64, I, I, P]
+            lib.vm_prompt_scan.argtypes = [R, Q, P, P, P, I64, I64, I64, I64, I, I, P, I64, P]
+            lib.vm_prompt_scan_bwd.argtypes = [R, Q, P, P, P, ctypes.POINTER(VmRowsGrad), I64, I64, I64, I64, I, I, P, I64, P]
+            lib.vm_token_scan.argtypes = [R, P, P, P, I64, I64, I64, I64, I, I, P]
+            lib.vm_norm_before.argtypes = [B, P, P, P, I64, I64, I, I, P]
+            lib.vm_norm_before_bwd.argtypes = [B, P, P, P, K, I64, I64, I, I, P, I64, P]
+            lib.vm_norm_after.argtypes = [B, P, P, I64, I64, I, I, P]
+            lib.vm_norm_after_bwd.argtypes = [B, P, K, I64, I64, I, I, P, I64, P]
+            lib.vm_prompt_conv_workspace.argtypes = [I64, I64, I64, I64, I64, I, I]
+            lib.vm_prompt_scan_workspace.argtypes = [I64, I64, I64, I64, I64, I, I]
+            lib.vm_block_norm_workspace.argtypes = [I64, I64, I64]
+            for name in ("vm_gated_delta_workspace", "vm_head_norm_rope_workspace", "vm_clip_grad_workspace",
+                         "vm_prompt_conv_workspace", "vm_prompt_scan_workspace", "vm_block_norm_workspace"):
                 getattr(lib, name).restype = I64
             for name in ("vm_gated_delta_fwd", "vm_gated_delta_bwd", "vm_gated_delta_step", "vm_head_norm_rope",
                          "vm_head_norm_rope_bwd", "vm_clip_grad_norm",
+                         "vm_prompt_conv", "vm_prompt_conv_bwd", "vm_token_conv", "vm_prompt_scan", "vm_prompt_scan_bwd",
+                         "vm_token_scan", "vm_norm_before", "vm_norm_before_bwd", "vm_norm_after", "vm_norm_after_bwd",
                          "vm_selective_scan_fwd", "vm_bidir_scan_fwd", "vm_bidir_scan_fwd_noalloc",
                          "vm_atrous_gather",
                          "vm_atrous_scatter", "vm_pool_scan_repeat", "vm_ss2d_scan_fwd",
@@ -881,10 +941,374 @@ def vm_clip_grad_norm(grads, max_norm, out=None):
 _GRAD_CODES = {torch.float32: VM_F32, torch.bfloat16: VM_BF16}
 
 
+# ------------------------------------------- prompts, single tokens and norms
+def _row_tensor(t, name, dtype, shape, index):
+    """A tensor [..., dim] whose rows are contiguous and evenly spaced.  Returns
+    the address and the C ABI's row stride (0 = dense)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be on a GPU device{', cuda:%d' % index if index >= 0 else ''} (got {t.device})")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    strides = t.stride()
+    step, rows = 0, 1                            # of one row, and rows so far, from the last axis to the first
+    good = strides[-1] == 1 or shape[-1] == 1
+    for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+        if size == 1:
+            continue
+        if rows == 1:
+            step = stride
+        elif stride != step * rows:
+            good = False
+        rows *= size
+    if good and (rows == 1 or step >= shape[-1]):
+        return t.data_ptr(), step if rows > 1 else 0
+    raise ValueError(f"{name} must have contiguous rows, evenly spaced (shape {tuple(shape)}, strides {strides})")
+
+
+def _float_arg(t, name, shape, index):
+    return None if t is None else _arg(t, name, torch.float32, shape, index)
+
+
+def _sequences(batch, offsets, slots, fresh, h0, state, index):
+    """Returns (VmSequences or None, sequences, kept states)."""
+    n, po = batch, None
+    if offsets is not None:
+        if batch != 1:
+            raise ValueError("packed sequences (offsets) take batch 1")
+        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+            raise ValueError("offsets must be an int32 tensor [sequences + 1]")
+        n = offsets.shape[0] - 1
+        po = _arg(offsets, "offsets", torch.int32, (n + 1,), index)
+    kept = n
+    if slots is not None:
+        some = h0 if h0 is not None else state
+        if some is None or some.dim() < 1:
+            raise ValueError("slots come with h0 or state [n_slots, ...]")
+        kept = some.shape[0]
+    elif po is None and fresh is None:
+        return None, n, kept
+    return VmSequences(po, _arg(slots, "slots", torch.int32, (n,), index), _arg(fresh, "fresh", torch.int32, (n,), index), n,
+                       kept), n, kept
+
+
+def _three(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a [batch, seqlen, channels] tensor")
+    return t
+
+
+def _conv_weights(w, dim):
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[0] != dim:
+        raise ValueError("w must be a [dim, width] tensor")
+    return w.shape[1]
+
+
+def vm_prompt_conv(x, w, bias=None, silu=True, h0=None, state=None, want_state=False, offsets=None, slots=None, fresh=None,
+                   out=None):
+    """Depthwise causal convolution over rows of tokens, with SiLU; returns
+    (out, state).  x: [batch, L, dim] (fp32 or bf16; a slice of a projection's row
+    is read in place); w: [dim, width] fp32, width 2 to 4; bias: [dim] fp32 or None.
+    h0: the inputs before each sequence's first token, [n, width - 1, dim] of x's
+    dtype, None = 0.  state (the last inputs, may be h0 itself) is None unless
+    want_state or a buffer is given.  offsets (int32 [n + 1], batch 1): sequence i is
+    tokens offsets[i] .. offsets[i + 1] - 1.  slots (int32 [n]): h0 and state are
+    pools [n_slots, ...] and each sequence's lies there (outside: starts from 0, not
+    kept; no two alike).  fresh (int32 [n]): nonzero = starts from 0."""
+    batch, L, dim = _three(x, "x").shape
+    width = _conv_weights(w, dim)
+    index, dtype = x.get_device(), x.dtype
+    px, xs = _row_tensor(x, "x", dtype, (batch, L, dim), index)
+    seq, n, kept = _sequences(batch, offsets, slots, fresh, h0, state, index)
+    shape = (kept, width - 1, dim)
+    if out is None:
+        out = torch.empty((batch, L, dim), dtype=dtype, device=x.device)
+    if state is None and want_state:
+        if slots is not None:
+            raise ValueError("with slots, state is a pool of the caller's")
+        state = torch.empty(shape, dtype=dtype, device=x.device)
+    _launch("vm_prompt_conv", index, seq, px, xs, _float_arg(w, "w", (dim, width), index),
+            _float_arg(bias, "bias", (dim,), index), _arg(h0, "h0", dtype, shape, index),
+            _arg(state, "state", dtype, shape, index), _arg(out, "out", dtype, (batch, L, dim), index), batch, L, dim, width,
+            int(bool(silu)), _dtype_code(x))
+    return out, state
+
+
+def vm_prompt_conv_bwd(x, w, dout, bias=None, silu=True, h0=None, dstate=None, offsets=None):
+    """Gradients of sum(dout * out) + sum(dstate * state) of vm_prompt_conv.
+    Returns a dict: x (dense, in its dtype), w, bias (fp32, with bias) and, when h0
+    is given, h0."""
+    batch, L, dim = _three(x, "x").shape
+    width = _conv_weights(w, dim)
+    index, dtype = x.get_device(), x.dtype
+    px, xs = _row_tensor(x, "x", dtype, (batch, L, dim), index)
+    seq, n, _ = _sequences(batch, offsets, None, None, h0, None, index)
+    shape = (n, width - 1, dim)
+    make = lambda kind, *size: torch.empty(size, dtype=kind, device=x.device)
+    d = dict(x=make(dtype, batch, L, dim), w=make(torch.float32, dim, width))
+    if bias is not None:
+        d["bias"] = make(torch.float32, dim)
+    if h0 is not None:
+        d["h0"] = make(dtype, *shape)
+    grads = VmConvGrad(*(d[k].data_ptr() if k in d else None for k in ("x", "w", "bias", "h0")))
+    ws, wp, wn = _workspace(load_library().vm_prompt_conv_workspace(batch, L, n, dim, width, _dtype_code(x),
+                                                                    offsets is not None), x.device)
+    _launch("vm_prompt_conv_bwd", index, seq, px, xs, _float_arg(w, "w", (dim, width), index),
+            _float_arg(bias, "bias", (dim,), index), _arg(h0, "h0", dtype, shape, index),
+            _arg(dout, "dout", dtype, (batch, L, dim), index), _arg(dstate, "dstate", dtype, shape, index), grads, batch, L,
+            dim, width, int(bool(silu)), _dtype_code(x), wp, wn)
+    return d
+
+
+def vm_token_conv(x, w, state, bias=None, silu=True, slots=None, out=None):
+    """One token of that convolution on kept windows; returns out [batch, dim].
+    x: [batch, dim] (a slice of a projection's row is read in place); state
+    [n_slots, width - 1, dim] of x's dtype is advanced in place.  slots (int32
+    [batch]): each row's window (distinct); a row with a slot outside [0, n_slots)
+    is idle: zero out, no window touched."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a [batch, dim] tensor")
+    batch, dim = x.shape
+    width = _conv_weights(w, dim)
+    index, dtype = x.get_device(), x.dtype
+    px, xs = _row_tensor(x, "x", dtype, (batch, dim), index)
+    if not isinstance(state, torch.Tensor) or state.dim() != 3:
+        raise ValueError("state must be a [n_slots, width - 1, dim] tensor")
+    n = state.shape[0]
+    if out is None:
+        out = torch.empty((batch, dim), dtype=dtype, device=x.device)
+    _launch("vm_token_conv", index, px, xs, _float_arg(w, "w", (dim, width), index), _float_arg(bias, "bias", (dim,), index),
+            _arg(state, "state", dtype, (n, width - 1, dim), index), _arg(slots, "slots", torch.int32, (batch,), index),
+            _arg(out, "out", dtype, (batch, dim), index), batch, n, dim, width, int(bool(silu)), _dtype_code(x))
+    return out
+
+
+def _scan_rows(u, delta, A, B, C, D, delta_bias, z):
+    """Validate the inputs of a scan over rows [..., dim]; returns (VmScanRows, GPU, dim, N)."""
+    if not isinstance(u, torch.Tensor):
+        raise TypeError("u must be a torch.Tensor")
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be a [dim, N] tensor")
+    lead, dim, N = tuple(u.shape[:-1]), u.shape[-1], A.shape[1]
+    index, dtype = u.get_device(), u.dtype
+    pu, su = _row_tensor(u, "u", dtype, (*lead, dim), index)
+    pd, sd = _row_tensor(delta, "delta", dtype, (*lead, dim), index)
+    pb, sb = _row_tensor(B, "B", dtype, (*lead, N), index)
+    pc, sc = _row_tensor(C, "C", dtype, (*lead, N), index)
+    pz, sz = _row_tensor(z, "z", dtype, (*lead, dim), index) if z is not None else (None, 0)
+    return VmScanRows(pu, pd, _float_arg(A, "A", (dim, N), index), pb, pc, _float_arg(D, "D", (dim,), index),
+                      _float_arg(delta_bias, "delta_bias", (dim,), index), pz, su, sd, sb, sc, sz), index, dim, N
+
+
+def vm_prompt_scan(u, delta, A, B, C, D=None, delta_bias=None, z=None, delta_softplus=True, h0=None, state=None,
+                   want_state=False, offsets=None, slots=None, fresh=None, out=None):
+    """Selective scan over rows of tokens; returns (out, state).  u, delta, z:
+    [batch, L, dim]; B, C: [batch, L, N] (fp32 or bf16; slices of a projection's row
+    are read in place); A: [dim, N], D, delta_bias: [dim] fp32.  h0, state: [n, dim,
+    N] fp32; state (the last states, may be h0 itself) is None unless want_state or a
+    buffer is given.  offsets, slots and fresh as in vm_prompt_conv.  out is dense."""
+    batch, L, dim = _three(u, "u").shape
+    p, index, dim, N = _scan_rows(u, delta, A, B, C, D, delta_bias, z)
+    seq, n, kept = _sequences(batch, offsets, slots, fresh, h0, state, index)
+    if out is None:
+        out = torch.empty((batch, L, dim), dtype=u.dtype, device=u.device)
+    if state is None and want_state:
+        if slots is not None:
+            raise ValueError("with slots, state is a pool of the caller's")
+        state = torch.empty((n, dim, N), dtype=torch.float32, device=u.device)
+    ws, wp, wn = _workspace(load_library().vm_prompt_scan_workspace(batch, L, n, dim, N, offsets is not None, 0), u.device)
+    _launch("vm_prompt_scan", index, p, seq, _float_arg(h0, "h0", (kept, dim, N), index),
+            _float_arg(state, "state", (kept, dim, N), index), _arg(out, "out", u.dtype, (batch, L, dim), index), batch, L,
+            dim, N, _dtype_code(u), _options(delta_softplus, False), wp, wn)
+    return out, state
+
+
+def vm_prompt_scan_bwd(u, delta, A, B, C, dout, D=None, delta_bias=None, z=None, delta_softplus=True, h0=None, dstate=None,
+                       offsets=None):
+    """Gradients of sum(dout * out) + sum(dstate * state) of vm_prompt_scan.
+    Returns a dict: u, delta, B, C and (with z) z, dense in their dtype; A and, where
+    given, D, delta_bias, h0 in fp32."""
+    batch, L, dim = _three(u, "u").shape
+    p, index, dim, N = _scan_rows(u, delta, A, B, C, D, delta_bias, z)
+    seq, n, _ = _sequences(batch, offsets, None, None, h0, None, index)
+    make = lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=u.device)
+    dt, f32 = u.dtype, torch.float32
+    d = dict(u=make(dt, batch, L, dim), delta=make(dt, batch, L, dim), A=make(f32, dim, N), B=make(dt, batch, L, N),
+             C=make(dt, batch, L, N))
+    if D is not None:
+        d["D"] = make(f32, dim)
+    if delta_bias is not None:
+        d["delta_bias"] = make(f32, dim)
+    if z is not None:
+        d["z"] = make(dt, batch, L, dim)
+    if h0 is not None:
+        d["h0"] = make(f32, n, dim, N)
+    grads = VmRowsGrad(*(d[k].data_ptr() if k in d else None
+                         for k in ("u", "delta", "A", "B", "C", "D", "delta_bias", "z", "h0")))
+    ws, wp, wn = _workspace(load_library().vm_prompt_scan_workspace(batch, L, n, dim, N, offsets is not None, 1), u.device)
+    _launch("vm_prompt_scan_bwd", index, p, seq, _float_arg(h0, "h0", (n, dim, N), index),
+            _arg(dout, "dout", dt, (batch, L, dim), index), _float_arg(dstate, "dstate", (n, dim, N), index), grads, batch, L,
+            dim, N, _dtype_code(u), _options(delta_softplus, False), wp, wn)
+    return d
+
+
+def vm_token_scan(u, delta, A, B, C, state, D=None, delta_bias=None, z=None, delta_softplus=True, slots=None, out=None):
+    """One token of the selective scan on kept states; returns out [batch, dim].
+    u, delta, z: [batch, dim]; B, C: [batch, N]; state [n_slots, dim, N] fp32 is
+    updated in place.  slots as in vm_token_conv."""
+    if not isinstance(u, torch.Tensor) or u.dim() != 2:
+        raise ValueError("u must be a [batch, dim] tensor")
+    p, index, dim, N = _scan_rows(u, delta, A, B, C, D, delta_bias, z)
+    batch = u.shape[0]
+    if not isinstance(state, torch.Tensor) or state.dim() != 3:
+        raise ValueError("state must be a [n_slots, dim, N] tensor")
+    n = state.shape[0]
+    if out is None:
+        out = torch.empty((batch, dim), dtype=u.dtype, device=u.device)
+    _launch("vm_token_scan", index, p, _float_arg(state, "state", (n, dim, N), index),
+            _arg(slots, "slots", torch.int32, (batch,), index), _arg(out, "out", u.dtype, (batch, dim), index), batch, n, dim,
+            N, _dtype_code(u), _options(delta_softplus, False))
+    return out
+
+
+def _lead(t, name):
+    """Rows and channels of a tensor [..., dim]."""
+    if not isinstance(t, torch.Tensor) or t.dim() < 1:
+        raise ValueError(f"{name} must be a [..., dim] tensor")
+    return t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1]
+
+
+def _residual_type(t, x_dtype):
+    return x_dtype if t is None else t.dtype
+
+
+def vm_norm_before(x, w=None, b=None, residual=None, scale=None, factor=1.0, center=False, eps=1e-5, want_residual=True,
+                   y=None, r=None):
+    """The norm before a block: r = residual + factor * scale * x, y = norm(r) * w +
+    b; returns (y, r).  x: [..., dim] (fp32 or bf16; rows may be slices); residual:
+    the same shape, of x's dtype or fp32, or None; w, b, scale: [dim] fp32 or None.
+    The norm divides by the root mean square (center=True: after taking the mean
+    off).  r (of residual's dtype; may be residual itself) is None unless
+    want_residual or a buffer is given."""
+    rows, dim = _lead(x, "x")
+    index, dtype = x.get_device(), x.dtype
+    px, xs = _row_tensor(x, "x", dtype, tuple(x.shape), index)
+    rtype = _residual_type(residual, _residual_type(r, dtype))
+    if y is None:
+        y = torch.empty(x.shape, dtype=dtype, device=x.device)
+    if r is None and want_residual:
+        r = torch.empty(x.shape, dtype=rtype, device=x.device)
+    vec = lambda t, name: _float_arg(t, name, (dim,), index)
+    p = VmBlockNorm(px, vec(w, "w"), vec(b, "b"), vec(scale, "scale"), None, xs, 0, 0, 0, eps, factor,
+                    VM_NORM_CENTER if center else 0)
+    _launch("vm_norm_before", index, p, _arg(residual, "residual", rtype, x.shape, index), _arg(y, "y", dtype, x.shape, index),
+            _arg(r, "r", rtype, x.shape, index), rows, dim, _dtype_code(x), _GRAD_CODES.get(rtype, -1))
+    return y, r
+
+
+def vm_norm_before_bwd(dy, r, w=None, b=None, dr=None, x=None, scale=None, factor=1.0, center=False, eps=1e-5):
+    """Gradients of sum(dy * y) + sum(dr * r) of vm_norm_before at the residual r
+    that it returned.  Returns a dict: residual (r's dtype), x (dy's dtype; the same
+    tensor where the two are equal) and, where given, w, b, scale (fp32; scale needs
+    x)."""
+    rows, dim = _lead(dy, "dy")
+    index, dtype, shape = dy.get_device(), dy.dtype, dy.shape
+    if not isinstance(r, torch.Tensor):
+        raise TypeError("r must be a torch.Tensor")
+    if scale is not None and x is None:
+        raise ValueError("the gradient of scale needs x")
+    rtype = r.dtype
+    px, xs = _row_tensor(x, "x", dtype, tuple(shape), index) if scale is not None else (None, 0)
+    make = lambda kind, size: torch.empty(size, dtype=kind, device=dy.device)
+    d = dict(residual=make(rtype, shape))
+    same = scale is None and factor == 1.0 and rtype is dtype
+    d["x"] = d["residual"] if same else make(dtype, shape)
+    for name, t in (("w", w), ("b", b), ("scale", scale)):
+        if t is not None:
+            d[name] = make(torch.float32, (dim,))
+    ptr = lambda name: d[name].data_ptr() if name in d else None
+    grads = VmNormGrad(None if same else ptr("x"), ptr("residual"), None, ptr("w"), ptr("b"), ptr("scale"))
+    vec = lambda t, name: _float_arg(t, name, (dim,), index)
+    p = VmBlockNorm(px, vec(w, "w"), vec(b, "b"), vec(scale, "scale"), None, xs, 0, 0, 0, eps, factor,
+                    VM_NORM_CENTER if center else 0)
+    some = w is not None or b is not None or scale is not None
+    ws, wp, wn = _workspace(load_library().vm_block_norm_workspace(rows, dim, 0) if some else 0, dy.device)
+    _launch("vm_norm_before_bwd", index, p, _arg(r, "r", rtype, shape, index), _arg(dy, "dy", dtype, shape, index),
+            _arg(dr, "dr", rtype, shape, index), grads, rows, dim, _dtype_code(dy), _GRAD_CODES.get(rtype, -1), wp, wn)
+    return d
+
+
+def _norm_after(x, w, z, group, scale, factor, gate_first, eps):
+    rows, dim = _lead(x, "x")
+    index, dtype = x.get_device(), x.dtype
+    group = dim if group is None else int(group)
+    if group < 1 or dim % group:
+        raise ValueError(f"group {group} does not divide {dim} channels")
+    px, xs = _row_tensor(x, "x", dtype, tuple(x.shape), index)
+    pz, zs = _row_tensor(z, "z", dtype, tuple(x.shape), index) if z is not None else (None, 0)
+    gains = dim
+    if w is not None:
+        if not isinstance(w, torch.Tensor) or w.dim() != 1 or w.shape[0] not in (dim, group):
+            raise ValueError(f"w must hold {dim} or {group} gains")
+        gains = w.shape[0]
+    if gate_first and z is None:
+        raise ValueError("gate_first needs z")
+    p = VmBlockNorm(px, _float_arg(w, "w", (gains,), index), None, _float_arg(scale, "scale", (dim,), index), pz, xs, zs,
+                    gains, group, eps, factor, VM_NORM_GATE_FIRST if gate_first else 0)
+    return p, index, rows, dim, group, gains
+
+
+def vm_norm_after(x, w=None, z=None, group=None, residual=None, scale=None, factor=1.0, gate_first=False, eps=1e-5, out=None):
+    """The norm of a block's output, gated and added to the residual; returns
+    residual + factor * scale * y, y = norm(x) * w * SiLU(z), or, gate_first, norm(x *
+    SiLU(z)) * w.  x, z: [..., dim] (fp32 or bf16; rows may be slices); group:
+    channels normed together (None = all); w: [dim] or [group] fp32; scale: [dim]
+    fp32; residual: the shape of x, of its dtype or fp32, or None.  out has
+    residual's dtype and may be residual itself."""
+    p, index, rows, dim, _, _ = _norm_after(x, w, z, group, scale, factor, gate_first, eps)
+    rtype = _residual_type(residual, _residual_type(out, x.dtype))
+    if out is None:
+        out = torch.empty(x.shape, dtype=rtype, device=x.device)
+    _launch("vm_norm_after", index, p, _arg(residual, "residual", rtype, x.shape, index), _arg(out, "out", rtype, x.shape, index),
+            rows, dim, _dtype_code(x), _GRAD_CODES.get(rtype, -1))
+    return out
+
+
+def vm_norm_after_bwd(dout, x, w=None, z=None, group=None, scale=None, factor=1.0, gate_first=False, eps=1e-5):
+    """Gradients of sum(dout * out) of vm_norm_after (the residual's is dout itself).
+    Returns a dict: x, z (dense, x's dtype) and, where given, w, scale (fp32)."""
+    p, index, rows, dim, group, gains = _norm_after(x, w, z, group, scale, factor, gate_first, eps)
+    if not isinstance(dout, torch.Tensor):
+        raise TypeError("dout must be a torch.Tensor")
+    make = lambda kind, size: torch.empty(size, dtype=kind, device=x.device)
+    d = dict(x=make(x.dtype, x.shape))
+    if z is not None:
+        d["z"] = make(x.dtype, x.shape)
+    if w is not None:
+        d["w"] = make(torch.float32, (gains,))
+    if scale is not None:
+        d["scale"] = make(torch.float32, (dim,))
+    ptr = lambda name: d[name].data_ptr() if name in d else None
+    grads = VmNormGrad(ptr("x"), None, ptr("z"), ptr("w"), None, ptr("scale"))
+    some = w is not None or scale is not None
+    ws, wp, wn = _workspace(load_library().vm_block_norm_workspace(rows, dim, group) if some else 0, x.device)
+    _launch("vm_norm_after_bwd", index, p, _arg(dout, "dout", dout.dtype, x.shape, index), grads, rows, dim, _dtype_code(x),
+            _GRAD_CODES.get(dout.dtype, -1), wp, wn)
+    return d
+
+
 __all__ = ["vm_selective_scan_fwd", "vm_bidir_scan_fwd", "vm_bidir_scan_fwd_noalloc", "vm_atrous_gather", "vm_atrous_scatter",
            "vm_pool_scan_repeat", "vm_ss2d_scan_fwd", "vm_causal_conv1d_silu",
            "vm_causal_conv1d_silu_bwd", "vm_pool_scan_repeat_bwd", "vm_ss2d_scan_bwd",
            "vm_selective_scan_bwd", "vm_bidir_scan_bwd", "VmScanGrad", "vm_atrous_group_len", "vm_status_string", "vm_version",
            "VmScanDir", "VmError",
            "vm_gated_delta_fwd", "vm_gated_delta_bwd", "vm_gated_delta_step", "vm_head_norm_rope",
-           "vm_head_norm_rope_bwd", "vm_clip_grad_norm", "VmDelta", "VmDeltaGrad", "VmHeadNorm", "VmGradTensor", "load_library", "LIB_PATH", "EXPORTED"]
+           "vm_head_norm_rope_bwd", "vm_clip_grad_norm", "VmDelta", "VmDeltaGrad", "VmHeadNorm", "VmGradTensor",
+           "vm_prompt_conv", "vm_prompt_conv_bwd", "vm_token_conv", "vm_prompt_scan", "vm_prompt_scan_bwd", "vm_token_scan",
+           "vm_norm_before", "vm_norm_before_bwd", "vm_norm_after", "vm_norm_after_bwd", "VmSequences", "VmConvGrad",
+           "VmScanRows", "VmRowsGrad", "VmBlockNorm", "VmNormGrad", "load_library", "LIB_PATH", "EXPORTED"]

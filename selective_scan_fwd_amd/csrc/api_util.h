@@ -89,6 +89,59 @@ class Scratch {
   size_t used_ = 0;
 };
 
+// Extent in elements of [batch, seqlen, heads, dim] with a token stride
+// (0 = dense); false if the stride is short or the extent overflows.
+inline bool token_extent(int64_t batch, int64_t seqlen, int64_t heads, int64_t dim, int64_t *stride, int64_t *extent) {
+  int64_t unused = 0;
+  if (!dims_ok({batch, seqlen, heads, dim}, &unused)) return false;
+  if (*stride == 0) *stride = heads * dim;
+  if (*stride < heads * dim || !dims_ok({batch, seqlen, *stride}, &unused)) return false;
+  *extent = (batch * seqlen - 1) * *stride + heads * dim;
+  return true;
+}
+
+template <int N, int M>
+bool any_overlap(const Span (&outs)[N], const Span (&ins)[M]) {
+  for (int i = 0; i < N; ++i) {
+    for (int j = 0; j < M; ++j)
+      if (overlaps(outs[i], ins[j])) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i], outs[j])) return true;
+  }
+  return false;
+}
+
+// Temporary memory of one call in one piece: the parts are laid out first, then
+// taken from the caller's workspace or from the pool (where each allocation and
+// free costs the host some 10 us).
+class Parts {
+ public:
+  static constexpr int64_t whole(int64_t bytes) { return (bytes + 255) & ~int64_t{255}; }
+  template <typename P>
+  void add(P **to, int64_t bytes) {
+    to_[n_] = reinterpret_cast<void **>(to);
+    at_[n_++] = total_;
+    total_ += whole(bytes);
+  }
+  int64_t total() const { return total_; }
+  int get(void *workspace, int64_t bytes, Scratch &ws) {
+    int st = VM_OK;
+    char *base = static_cast<char *>(workspace);
+    if (base == nullptr)
+      base = static_cast<char *>(ws.bytes(total_, &st));
+    else if (bytes < total_ || (reinterpret_cast<uintptr_t>(base) & 255) != 0)
+      st = VM_ERR_ALLOC;
+    if (st == VM_OK)
+      for (int i = 0; i < n_; ++i) *to_[i] = base + at_[i];
+    return st;
+  }
+
+ private:
+  void **to_[12];
+  int64_t at_[12], total_ = 0;
+  int n_ = 0;
+};
+
 inline int hip_status(hipError_t e) { return e == hipSuccess ? VM_OK : VM_ERR_HIP; }
 
 }  // namespace vmk

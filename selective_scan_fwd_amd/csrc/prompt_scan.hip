@@ -1,0 +1,186 @@
+// The selective scan over rows of tokens, as a language model's prompts come:
+//   dt = softplus(delta + bias);  h_t = exp(dt A) h_{t-1} + dt B_t u_t;
+//   y_t = C_t h_t + D u_t;  out_t = y_t SiLU(z_t)
+// dense or packed, from given or zero states, the last states kept.
+//
+// A wave walks over the tokens of 16 channels, 4 states to a lane (the layout at
+// the top of prompt_device.h).  A state update is three vector instructions
+// (dt A, 2^x, times h): the rank-one term and the read-out run on the matrix
+// units.  A sequence is cut in chunks where there are too few channels to fill the
+// card.  Then one launch walks every chunk but a sequence's last from a zero state
+// (its first, whose state is known, in full) and notes its end state and the sum of
+// its steps T; a second one forms each later chunk's first state from the chunks
+// before it, h <- exp(A T) h + end, and walks it in full.
+#include <hip/hip_runtime.h>
+
+#include "prompt_device.h"
+
+namespace vmk {
+namespace {
+
+constexpr int kGroups = 4;            // groups of 4 tokens to a tile
+constexpr int kTile = 4 * kGroups;
+
+// One tile's values as they were loaded.
+struct Raw {
+  float u[kGroups], d[kGroups], z[kGroups], b[kGroups], c[kGroups];
+};
+
+template <typename T, bool FULL, bool GATE>
+__device__ __forceinline__ void load_tile(const PromptScanArgs &a, const Lane &l, int64_t token, int left, int c0, Raw &r) {
+  const int m = left < kTile ? left : kTile;
+  const Rsrc ru = rows<T>(a.u, a.us, token, c0, m, l.cw), rd = rows<T>(a.delta, a.ds, token, c0, m, l.cw),
+             rb = rows<T>(a.B, a.bs, token, 0, m, a.n);
+  const uint32_t su = 4 * a.us * sizeof(T), sd = 4 * a.ds * sizeof(T), sb = 4 * a.bs * sizeof(T);
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    r.u[g] = bload<T>(ru, l.u + g * su);
+    r.d[g] = bload<T>(rd, l.d + g * sd);
+    r.b[g] = bload<T>(rb, l.b + g * sb);
+  }
+  if (FULL) {
+    const Rsrc rc = rows<T>(a.C, a.cs, token, 0, m, a.n);
+    const uint32_t sc = 4 * a.cs * sizeof(T);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) r.c[g] = bload<T>(rc, l.c + g * sc);
+    if (GATE) {
+      const Rsrc rz = rows<T>(a.z, a.zs, token, c0, m, l.cw);
+      const uint32_t sz = 4 * a.zs * sizeof(T);
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) r.z[g] = bload<T>(rz, l.z + g * sz);
+    }
+  }
+}
+
+template <int S, bool FULL>
+__device__ __forceinline__ void token(const float (&A2)[4], float dt, float b, float du, float c, f32x4 &h, float &y) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] *= hw_exp2(dt * A2[i]);
+  h = rank1<S>(b, du, h);
+  if (FULL) y = read_out<S>(c, h);
+}
+
+// Walks a chunk from state h; returns the sum of this lane's steps.
+template <typename T, bool FULL, bool GATE>
+__device__ __forceinline__ float walk(const PromptScanArgs &a, const Lane &l, const Piece &p, int c0, const float (&A2)[4],
+                                      float bias, float D, f32x4 &h) {
+  float steps = 0.0f;
+  Raw next;
+  load_tile<T, FULL, GATE>(a, l, p.t0, p.len, c0, next);
+  for (int at = 0; at < p.len; at += kTile) {
+    const Raw r = next;
+    load_tile<T, FULL, GATE>(a, l, p.t0 + at + kTile, p.len - at - kTile, c0, next);
+    const int m = p.len - at < kTile ? p.len - at : kTile;
+    const Rsrc ro = rows<T>(a.out, a.dim, p.t0 + at, c0, FULL ? m : 0, l.cw);
+    const uint32_t so = 4 * a.dim * sizeof(T);
+    const uint32_t oo = l.live ? (l.q * static_cast<uint32_t>(a.dim) + l.ch) * sizeof(T) : kOob;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      if (4 * g >= m) break;
+      // steps past the end are 0: they leave the state as it is
+      const float x = r.d[g] + bias;
+      const float dt = 4 * g + l.q < m ? (a.softplus ? softplus_f(x) : x) : 0.0f;
+      const float du = dt * r.u[g];
+      steps += dt;
+      float dts[4], y[4];
+      hand_out(dt, dts);
+      token<0, FULL>(A2, dts[0], r.b[g], du, r.c[g], h, y[0]);
+      token<1, FULL>(A2, dts[1], r.b[g], du, r.c[g], h, y[1]);
+      token<2, FULL>(A2, dts[2], r.b[g], du, r.c[g], h, y[2]);
+      token<3, FULL>(A2, dts[3], r.b[g], du, r.c[g], h, y[3]);
+      if (FULL) {
+        float o = __builtin_fmaf(D, r.u[g], gather(y));
+        if (GATE) o *= silu_f(r.z[g]);
+        bstore<T>(ro, oo + g * so, o);
+      }
+    }
+  }
+  return steps;
+}
+
+template <typename T, bool GATE, bool SECOND>
+__global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScanArgs a) {
+  const int lane = threadIdx.x % 64;
+  const int blocks = (a.dim + 15) / 16, waves = blockDim.x / 64;
+  const int wide = (blocks + waves - 1) / waves;
+  const int64_t slot = blockIdx.x / wide;
+  const int blk = uniform(static_cast<int>(blockIdx.x % wide) * waves + threadIdx.x / 64);
+  if (blk >= blocks) return;
+  const Piece p = piece_of(a.q, slot);
+  if (p.len < 0 || (SECOND ? p.c == 0 : p.c > 0 && p.c == p.count - 1)) return;
+  const int c0 = blk * 16;
+  const Lane l = lane_of<T>(a, c0, lane);
+  float A2[4];
+  const Rsrc rA = make_rsrc(a.A + static_cast<int64_t>(c0) * a.n, l.cw * a.n * 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A2[i] = rate2(bload<float>(rA, l.state[i]));
+  const float D = channel_value(a.D, c0, l), bias = channel_value(a.bias, c0, l);
+
+  const int64_t kept = kept_at(a.q, p.seq);
+  const int64_t block = slot * blocks + blk;
+  f32x4 h = {0, 0, 0, 0};
+  if (!SECOND) {
+    if (p.c == 0 && a.h0 != nullptr && kept >= 0 && starts_kept(a.q, p.seq)) {
+      const Rsrc rh = make_rsrc(a.h0 + (kept * a.dim + c0) * a.n, l.cw * a.n * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = bload<float>(rh, l.state[i]);
+    }
+  } else {
+    for (int64_t j = block - static_cast<int64_t>(p.c) * blocks; j < block; j += blocks) {
+      const f32x4 e = *reinterpret_cast<const f32x4 *>(a.ends + j * 256 + lane * 4);
+      const float t = a.steps[j * 16 + l.ch];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = __builtin_fmaf(hw_exp2(A2[i] * t), h[i], e[i]);
+    }
+  }
+  float steps;
+  if (SECOND || p.c == 0)
+    steps = walk<T, true, GATE>(a, l, p, c0, A2, bias, D, h);
+  else
+    steps = walk<T, false, false>(a, l, p, c0, A2, bias, D, h);
+  if (p.c == p.count - 1) {
+    if (a.state != nullptr && kept >= 0) {
+      const Rsrc rh = make_rsrc(a.state + (kept * a.dim + c0) * a.n, l.cw * a.n * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bstore<float>(rh, l.state[i], h[i]);
+    }
+  } else {
+    float s[4] = {steps, steps, steps, steps};
+    steps = gather(s);
+    *reinterpret_cast<f32x4 *>(a.ends + block * 256 + lane * 4) = h;
+    if (l.q == 0) a.steps[block * 16 + l.ch] = steps;
+  }
+}
+
+template <typename T, bool GATE>
+hipError_t launch_scan(const PromptScanArgs &a, hipStream_t s) {
+  const int blocks = (a.dim + 15) / 16, waves = blocks < kScanWaves ? blocks : kScanWaves;
+  const dim3 grid(static_cast<uint32_t>(a.q.slots * ((blocks + waves - 1) / waves)));
+  prompt_scan_kernel<T, GATE, false><<<grid, 64 * waves, 0, s>>>(a);
+  if (a.ends != nullptr) prompt_scan_kernel<T, GATE, true><<<grid, 64 * waves, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t seq_slots(int64_t nseq, int64_t L, int64_t chunk, bool packed) {
+  return packed ? L / chunk + nseq : nseq * ((L + chunk - 1) / chunk);
+}
+
+int64_t scan_chunk_tokens(int64_t tokens, int64_t nseq, int64_t L, int dim, bool packed, bool back) {
+  (void)back;
+  // waves that fill the card
+  const int64_t want = 2048 / scan_blocks(dim) + 1;
+  if (!packed && nseq >= want) return L;
+  int64_t chunk = packed ? (tokens + want - 1) / want : (L + (want + nseq - 1) / nseq - 1) / ((want + nseq - 1) / nseq);
+  chunk = (chunk + 15) / 16 * 16;
+  if (chunk < 64) chunk = 64;
+  return chunk < L ? chunk : L;
+}
+
+hipError_t launch_prompt_scan(const PromptScanArgs &a, bool bf16, hipStream_t s) {
+  if (bf16) return a.z != nullptr ? launch_scan<bf16_t, true>(a, s) : launch_scan<bf16_t, false>(a, s);
+  return a.z != nullptr ? launch_scan<float, true>(a, s) : launch_scan<float, false>(a, s);
+}
+
+}  // namespace vmk
