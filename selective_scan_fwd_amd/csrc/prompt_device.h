@@ -68,34 +68,83 @@ __device__ __forceinline__ bool starts_kept(const SeqArgs &q, int seq) {
 
 // ------------------------------------------------------ the scan's lane layout
 // A wave holds 16 channels with 4 states in each lane: lane l has channel l % 16
-// and states 4 q .. 4 q + 3, q = l / 16.  Tokens go by in groups of 4, and what is
-// one value per token and channel (dt, dt u, y, ...) lies with token q in lane
-// (channel, q).  Such a layout is that of a 4 x 4 x 1 matrix instruction's 16
-// products: rows are the states (or the group's tokens), columns 4 of the
-// channels, and the instruction's broadcasts hand the 4 tokens out:
-//   update    h[i] += B_t[4 q + i] (dt u)[channel]    B in `by state`
-//   read-out  sum_i C_t[4 q + i] h[i]                 C in `by token`
-// by state: lane (q, s, i) holds token s, state 4 q + i; by token: lane (q, i, s)
-// the same.  So neither the outer product nor the read-out's sum over a lane's
-// states costs vector instructions, and both are exact fp32 products and sums.
+// and states 4 q .. 4 q + 3, q = l / 16, so each row of 16 lanes wants the same four
+// values of B and C.  Tokens go by in groups of 4.  What is one value per token and
+// channel (dt, dt u, y, ...) lies with token q in lane (channel, q); a group's B and
+// C with token s, state 4 q + i in lane 4 s + i of row q, from where a vector
+// instruction's operand takes it to the whole row at once (DPP row_newbcast).
+// (Matrix instructions that form the outer product and the sum over a lane's states
+// are no help: a 4 x 4 x 1 product takes the SIMD 10 cycles, beside an exponential
+// 15, and no vector instruction goes on meanwhile; four multiplications take 11 to 17.)
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// h += b_s x_s of token S of the group.
-template <int S>
-__device__ __forceinline__ f32x4 rank1(float b, float x, f32x4 h) {
-  return __builtin_amdgcn_mfma_f32_4x4x1f32(b, x, h, 2, S, 4 + S);
+// y = sum_i c[4 S + i] h[i], to be settled (see there; s_nop: c may have been written
+// by the instruction before).
+template <int S> __device__ __forceinline__ float read_out(float c, const f32x4 &h);
+#define VM_READ_OUT(S, A, B, C, D)                                                    \
+  template <>                                                                         \
+  __device__ __forceinline__ float read_out<S>(float c, const f32x4 &h) {             \
+    float y;                                                                          \
+    asm("s_nop 1\n"                                                                   \
+        "v_mul_f32_dpp %0, %1, %2 row_newbcast:" #A " row_mask:0xf bank_mask:0xf\n"   \
+        "v_fmac_f32_dpp %0, %1, %3 row_newbcast:" #B " row_mask:0xf bank_mask:0xf\n"  \
+        "v_fmac_f32_dpp %0, %1, %4 row_newbcast:" #C " row_mask:0xf bank_mask:0xf\n"  \
+        "v_fmac_f32_dpp %0, %1, %5 row_newbcast:" #D " row_mask:0xf bank_mask:0xf\n"  \
+        : "=&v"(y)                                                                    \
+        : "v"(c), "v"(h[0]), "v"(h[1]), "v"(h[2]), "v"(h[3]));                        \
+    return y;                                                                         \
+  }
+VM_READ_OUT(0, 0, 1, 2, 3) VM_READ_OUT(1, 4, 5, 6, 7) VM_READ_OUT(2, 8, 9, 10, 11) VM_READ_OUT(3, 12, 13, 14, 15)
+#undef VM_READ_OUT
+// Two states after everything before: what assembly text wrote may be read through DPP
+// or a lane swap (whose waits the compiler counts for its own instructions only).
+__device__ __forceinline__ void settle(float (&y)[4]) {
+  asm("s_nop 1" : "+v"(y[0]), "+v"(y[1]), "+v"(y[2]), "+v"(y[3]));
 }
-// Row S of the products is token S's sum over this lane's states; the others
-// (another token's C with this token's states) are not used.
-template <int S>
-__device__ __forceinline__ float read_out(float c, f32x4 h) {
-  f32x4 y = {0, 0, 0, 0};
-  y = __builtin_amdgcn_mfma_f32_4x4x1f32(c, h[0], y, 2, 0, 0);
-  y = __builtin_amdgcn_mfma_f32_4x4x1f32(c, h[1], y, 2, 1, 0);
-  y = __builtin_amdgcn_mfma_f32_4x4x1f32(c, h[2], y, 2, 2, 0);
-  y = __builtin_amdgcn_mfma_f32_4x4x1f32(c, h[3], y, 2, 3, 0);
-  return y[S];
-}
+
+// One token's update and read-out:  e[i] = 2^e[i],  h[i] = e[i] h[i] + b[4 S + i] x,
+// y = sum_i c[4 S + i] h[i]  (y to be settled).  In one piece, for the waits that the
+// compiler does not count inside: an exponential's result may be read one state later,
+// and what the last instruction before wrote (b or c) through DPP two states later.
+#define VM_UPDATE_TEXT(A, B, C, D)                                             \
+  "v_exp_f32 %[e0], %[e0]\n"                                                   \
+  "v_exp_f32 %[e1], %[e1]\n"                                                   \
+  "v_exp_f32 %[e2], %[e2]\n"                                                   \
+  "v_exp_f32 %[e3], %[e3]\n"                                                   \
+  "v_mul_f32 %[h0], %[h0], %[e0]\n"                                            \
+  "v_mul_f32 %[h1], %[h1], %[e1]\n"                                            \
+  "v_mul_f32 %[h2], %[h2], %[e2]\n"                                            \
+  "v_mul_f32 %[h3], %[h3], %[e3]\n"                                            \
+  "v_fmac_f32_dpp %[h0], %[b], %[x] row_newbcast:" #A " row_mask:0xf bank_mask:0xf\n" \
+  "v_fmac_f32_dpp %[h1], %[b], %[x] row_newbcast:" #B " row_mask:0xf bank_mask:0xf\n" \
+  "v_fmac_f32_dpp %[h2], %[b], %[x] row_newbcast:" #C " row_mask:0xf bank_mask:0xf\n" \
+  "v_fmac_f32_dpp %[h3], %[b], %[x] row_newbcast:" #D " row_mask:0xf bank_mask:0xf\n"
+#define VM_UPDATE_OUT                                                          \
+  [h0] "+&v"(h[0]), [h1] "+&v"(h[1]), [h2] "+&v"(h[2]), [h3] "+&v"(h[3]),      \
+      [e0] "+&v"(e[0]), [e1] "+&v"(e[1]), [e2] "+&v"(e[2]), [e3] "+&v"(e[3])
+template <int S> __device__ __forceinline__ void update(f32x4 &e, float b, float x, f32x4 &h);
+template <int S> __device__ __forceinline__ float update_read(f32x4 &e, float b, float x, float c, f32x4 &h);
+#define VM_UPDATE(S, A, B, C, D)                                               \
+  template <>                                                                  \
+  __device__ __forceinline__ void update<S>(f32x4 &e, float b, float x, f32x4 &h) { \
+    asm(VM_UPDATE_TEXT(A, B, C, D) : VM_UPDATE_OUT : [b] "v"(b), [x] "v"(x));  \
+  }                                                                            \
+  template <>                                                                  \
+  __device__ __forceinline__ float update_read<S>(f32x4 &e, float b, float x, float c, f32x4 &h) { \
+    float y;                                                                   \
+    asm(VM_UPDATE_TEXT(A, B, C, D)                                             \
+        "v_mul_f32_dpp %[y], %[c], %[h0] row_newbcast:" #A " row_mask:0xf bank_mask:0xf\n"  \
+        "v_fmac_f32_dpp %[y], %[c], %[h1] row_newbcast:" #B " row_mask:0xf bank_mask:0xf\n" \
+        "v_fmac_f32_dpp %[y], %[c], %[h2] row_newbcast:" #C " row_mask:0xf bank_mask:0xf\n" \
+        "v_fmac_f32_dpp %[y], %[c], %[h3] row_newbcast:" #D " row_mask:0xf bank_mask:0xf\n" \
+        : VM_UPDATE_OUT, [y] "=&v"(y)                                          \
+        : [b] "v"(b), [x] "v"(x), [c] "v"(c));                                 \
+    return y;                                                                  \
+  }
+VM_UPDATE(0, 0, 1, 2, 3) VM_UPDATE(1, 4, 5, 6, 7) VM_UPDATE(2, 8, 9, 10, 11) VM_UPDATE(3, 12, 13, 14, 15)
+#undef VM_UPDATE
+#undef VM_UPDATE_TEXT
+#undef VM_UPDATE_OUT
 
 __device__ __forceinline__ void swap32(float &a, float &b) {
   auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
@@ -134,8 +183,7 @@ struct Lane {
   int cw;                             // channels of the block that exist
   bool live;
   uint32_t u, d, z;                   // token q of a tile
-  uint32_t b, c;                      // B by state, C by token
-  uint32_t bt, ct;                    // B by token, C by state (backward pass)
+  uint32_t b, c;                      // B and C of a group: token (l / 4) % 4, state 4 q + l % 4
   uint32_t state[4];                  // in a block's [16][n]
 };
 
@@ -153,11 +201,9 @@ __device__ __forceinline__ Lane lane_of(const PromptScanArgs &a, int c0, int lan
   l.u = at(l.live, a.us, q, ch);
   l.d = at(l.live, a.ds, q, ch);
   l.z = at(l.live, a.zs, q, ch);
-  const uint32_t n = a.n, sl = 4 * q + lo, sh = 4 * q + hi;
-  l.b = at(sl < n, a.bs, hi, sl);
-  l.c = at(sh < n, a.cs, lo, sh);
-  l.bt = at(sh < n, a.bs, lo, sh);
-  l.ct = at(sl < n, a.cs, hi, sl);
+  const uint32_t state = 4 * q + lo;
+  l.b = at(state < static_cast<uint32_t>(a.n), a.bs, hi, state);
+  l.c = at(state < static_cast<uint32_t>(a.n), a.cs, hi, state);
 #pragma unroll
   for (int i = 0; i < 4; ++i) l.state[i] = l.live && 4 * l.q + i < a.n ? (l.ch * a.n + 4 * l.q + i) * 4 : kOob;
   return l;
@@ -172,6 +218,23 @@ template <typename T>
 __device__ __forceinline__ Rsrc rows(const void *base, int64_t stride, int64_t token, int64_t col, int tokens, int width) {
   const int bytes = tokens > 0 ? static_cast<int>(((tokens - 1) * stride + width) * sizeof(T)) : 0;
   return make_rsrc(static_cast<const T *>(base) + token * stride + col, bytes);
+}
+
+// The step of a token, 0 past the chunk's end: such a step leaves the state as it is.
+__device__ __forceinline__ float step_of(const PromptScanArgs &a, float x, bool in) {
+  const float soft = softplus_f(x);
+  const float dt = a.softplus ? soft : x;
+  return in ? dt : 0.0f;
+}
+
+// One value rounded to nearest even (NaN stays NaN) and stored.
+template <typename T>
+__device__ __forceinline__ void put(Rsrc r, uint32_t off, float x) {
+  if constexpr (sizeof(T) == 2)
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, static_cast<__bf16>(x)), r, static_cast<int>(off),
+                                          0, 0);
+  else
+    bstore<T>(r, off, x);
 }
 
 // Decay rates, ready for 2^x.  A rate of -Inf (which decays to 0 in any step) is

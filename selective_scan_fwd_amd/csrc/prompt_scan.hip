@@ -3,10 +3,10 @@
 //   y_t = C_t h_t + D u_t;  out_t = y_t SiLU(z_t)
 // dense or packed, from given or zero states, the last states kept.
 //
-// A wave walks over the tokens of 16 channels, 4 states to a lane (the layout at
-// the top of prompt_device.h).  A state update is three vector instructions
-// (dt A, 2^x, times h): the rank-one term and the read-out run on the matrix
-// units.  A sequence is cut in chunks where there are too few channels to fill the
+// A wave walks over the tokens of 16 channels, 4 states to a lane (the layout in
+// prompt_device.h).  A state update is five vector instructions, one of them an
+// exponential, and these bound it: 28.6 a wave and token, the SIMD busy with them all
+// the while at 4.8 cycles each.  A sequence is cut in chunks where there are too few channels to fill the
 // card.  Then one launch walks every chunk but a sequence's last from a zero state
 // (its first, whose state is known, in full) and notes its end state and the sum of
 // its steps T; a second one forms each later chunk's first state from the chunks
@@ -54,52 +54,76 @@ __device__ __forceinline__ void load_tile(const PromptScanArgs &a, const Lane &l
 
 template <int S, bool FULL>
 __device__ __forceinline__ void token(const float (&A2)[4], float dt, float b, float du, float c, f32x4 &h, float &y) {
+  f32x4 e;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] *= hw_exp2(dt * A2[i]);
-  h = rank1<S>(b, du, h);
-  if (FULL) y = read_out<S>(c, h);
+  for (int i = 0; i < 4; ++i) e[i] = dt * A2[i];
+  if (FULL)
+    y = update_read<S>(e, b, du, c, h);
+  else
+    update<S>(e, b, du, h);
+}
+
+// One tile of m tokens (ALL: a whole one) from (token, c0) on.
+template <typename T, bool FULL, bool GATE, bool ALL>
+__device__ __forceinline__ void tile(const PromptScanArgs &a, const Lane &l, const Raw &r, int64_t at, int m, int c0,
+                                     const float (&A2)[4], float bias, float D, f32x4 &h, float &steps,
+                                     float (*meet)[16][8]) {
+  const Rsrc ro = rows<T>(a.out, a.dim, at, c0, FULL ? m : 0, l.cw);
+  const uint32_t so = 4 * a.dim * sizeof(T);
+  const uint32_t oo = l.live ? (l.q * static_cast<uint32_t>(a.dim) + l.ch) * sizeof(T) : kOob;
+  // every lane gets its channel's dt and dt u of all tokens by way of LDS
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const float dt = step_of(a, r.d[g] + bias, ALL || 4 * g + l.q < m);
+    steps += dt;
+    meet[g][l.ch][2 * l.q] = dt;
+    meet[g][l.ch][2 * l.q + 1] = dt * r.u[g];
+  }
+  wave_lds_fence();
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    if (!ALL && 4 * g >= m) break;
+    float dts[4], dus[4], y[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      dts[s] = meet[g][l.ch][2 * s];
+      dus[s] = meet[g][l.ch][2 * s + 1];
+    }
+    token<0, FULL>(A2, dts[0], r.b[g], dus[0], r.c[g], h, y[0]);
+    token<1, FULL>(A2, dts[1], r.b[g], dus[1], r.c[g], h, y[1]);
+    token<2, FULL>(A2, dts[2], r.b[g], dus[2], r.c[g], h, y[2]);
+    token<3, FULL>(A2, dts[3], r.b[g], dus[3], r.c[g], h, y[3]);
+    if (FULL) {
+      settle(y);
+      float o = __builtin_fmaf(D, r.u[g], gather(y));
+      if (GATE) o *= silu_f(r.z[g]);
+      put<T>(ro, oo + g * so, o);
+    }
+  }
+  wave_lds_fence();
 }
 
 // Walks a chunk from state h; returns the sum of this lane's steps.
 template <typename T, bool FULL, bool GATE>
 __device__ __forceinline__ float walk(const PromptScanArgs &a, const Lane &l, const Piece &p, int c0, const float (&A2)[4],
-                                      float bias, float D, f32x4 &h) {
+                                      float bias, float D, f32x4 &h, float (*meet)[16][8]) {
   float steps = 0.0f;
   Raw next;
   load_tile<T, FULL, GATE>(a, l, p.t0, p.len, c0, next);
-  for (int at = 0; at < p.len; at += kTile) {
+  int at = 0;
+  for (; at + kTile <= p.len; at += kTile) {
     const Raw r = next;
     load_tile<T, FULL, GATE>(a, l, p.t0 + at + kTile, p.len - at - kTile, c0, next);
-    const int m = p.len - at < kTile ? p.len - at : kTile;
-    const Rsrc ro = rows<T>(a.out, a.dim, p.t0 + at, c0, FULL ? m : 0, l.cw);
-    const uint32_t so = 4 * a.dim * sizeof(T);
-    const uint32_t oo = l.live ? (l.q * static_cast<uint32_t>(a.dim) + l.ch) * sizeof(T) : kOob;
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      if (4 * g >= m) break;
-      // steps past the end are 0: they leave the state as it is
-      const float x = r.d[g] + bias;
-      const float dt = 4 * g + l.q < m ? (a.softplus ? softplus_f(x) : x) : 0.0f;
-      const float du = dt * r.u[g];
-      steps += dt;
-      float dts[4], y[4];
-      hand_out(dt, dts);
-      token<0, FULL>(A2, dts[0], r.b[g], du, r.c[g], h, y[0]);
-      token<1, FULL>(A2, dts[1], r.b[g], du, r.c[g], h, y[1]);
-      token<2, FULL>(A2, dts[2], r.b[g], du, r.c[g], h, y[2]);
-      token<3, FULL>(A2, dts[3], r.b[g], du, r.c[g], h, y[3]);
-      if (FULL) {
-        float o = __builtin_fmaf(D, r.u[g], gather(y));
-        if (GATE) o *= silu_f(r.z[g]);
-        bstore<T>(ro, oo + g * so, o);
-      }
-    }
+    tile<T, FULL, GATE, true>(a, l, r, p.t0 + at, kTile, c0, A2, bias, D, h, steps, meet);
   }
+  if (at < p.len) tile<T, FULL, GATE, false>(a, l, next, p.t0 + at, p.len - at, c0, A2, bias, D, h, steps, meet);
   return steps;
 }
 
 template <typename T, bool GATE, bool SECOND>
 __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScanArgs a) {
+  __shared__ __align__(16) float meets[kScanWaves][kGroups][16][8];
+  float(*meet)[16][8] = meets[threadIdx.x / 64];
   const int lane = threadIdx.x % 64;
   const int blocks = (a.dim + 15) / 16, waves = blockDim.x / 64;
   const int wide = (blocks + waves - 1) / waves;
@@ -135,9 +159,9 @@ __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScan
   }
   float steps;
   if (SECOND || p.c == 0)
-    steps = walk<T, true, GATE>(a, l, p, c0, A2, bias, D, h);
+    steps = walk<T, true, GATE>(a, l, p, c0, A2, bias, D, h, meet);
   else
-    steps = walk<T, false, false>(a, l, p, c0, A2, bias, D, h);
+    steps = walk<T, false, false>(a, l, p, c0, A2, bias, D, h, meet);
   if (p.c == p.count - 1) {
     if (a.state != nullptr && kept >= 0) {
       const Rsrc rh = make_rsrc(a.state + (kept * a.dim + c0) * a.n, l.cw * a.n * 4);

@@ -32,24 +32,51 @@ __device__ __forceinline__ float silu_both(float z, float &slope) {
   return z * s;
 }
 
-__device__ __forceinline__ float step_of(const PromptScanArgs &a, float x, bool in) {
-  return in ? (a.softplus ? softplus_f(x) : x) : 0.0f;
-}
-
 // ------------------------------------------------- chunks by themselves
+// h[i] += b[4 S + i] x
+template <int S> __device__ __forceinline__ void add_rank1(float b, float x, f32x4 &h);
+#define VM_RANK1(S, A, B, C, D)                                                       \
+  template <>                                                                         \
+  __device__ __forceinline__ void add_rank1<S>(float b, float x, f32x4 &h) {          \
+    asm("s_nop 1\n"                                                                   \
+        "v_fmac_f32_dpp %0, %4, %5 row_newbcast:" #A " row_mask:0xf bank_mask:0xf\n"  \
+        "v_fmac_f32_dpp %1, %4, %5 row_newbcast:" #B " row_mask:0xf bank_mask:0xf\n"  \
+        "v_fmac_f32_dpp %2, %4, %5 row_newbcast:" #C " row_mask:0xf bank_mask:0xf\n"  \
+        "v_fmac_f32_dpp %3, %4, %5 row_newbcast:" #D " row_mask:0xf bank_mask:0xf\n"  \
+        : "+&v"(h[0]), "+&v"(h[1]), "+&v"(h[2]), "+&v"(h[3])                          \
+        : "v"(b), "v"(x));                                                            \
+  }
+VM_RANK1(0, 0, 1, 2, 3) VM_RANK1(1, 4, 5, 6, 7) VM_RANK1(2, 8, 9, 10, 11) VM_RANK1(3, 12, 13, 14, 15)
+#undef VM_RANK1
+// g[i] += c[4 S + i] x[i]
+template <int S> __device__ __forceinline__ void add_each(float c, const f32x4 &x, f32x4 &g);
+#define VM_ADD_EACH(S, A, B, C, D)                                                    \
+  template <>                                                                         \
+  __device__ __forceinline__ void add_each<S>(float c, const f32x4 &x, f32x4 &g) {    \
+    asm("s_nop 1\n"                                                                   \
+        "v_fmac_f32_dpp %0, %4, %5 row_newbcast:" #A " row_mask:0xf bank_mask:0xf\n"  \
+        "v_fmac_f32_dpp %1, %4, %6 row_newbcast:" #B " row_mask:0xf bank_mask:0xf\n"  \
+        "v_fmac_f32_dpp %2, %4, %7 row_newbcast:" #C " row_mask:0xf bank_mask:0xf\n"  \
+        "v_fmac_f32_dpp %3, %4, %8 row_newbcast:" #D " row_mask:0xf bank_mask:0xf\n"  \
+        : "+&v"(g[0]), "+&v"(g[1]), "+&v"(g[2]), "+&v"(g[3])                          \
+        : "v"(c), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]));                        \
+  }
+VM_ADD_EACH(0, 0, 1, 2, 3) VM_ADD_EACH(1, 4, 5, 6, 7) VM_ADD_EACH(2, 8, 9, 10, 11) VM_ADD_EACH(3, 12, 13, 14, 15)
+#undef VM_ADD_EACH
+
 template <int S>
 __device__ __forceinline__ void local_token(const float (&A2)[4], float dt, float b, float du, float c, float dy, f32x4 &h,
                                             f32x4 &decay, f32x4 &grad) {
+  f32x4 e;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float e = hw_exp2(dt * A2[i]);
-    h[i] *= e;
-    decay[i] *= e;
-  }
-  h = rank1<S>(b, du, h);
-  const f32x4 o = rank1<S>(c, dy, f32x4{0, 0, 0, 0});
+  for (int i = 0; i < 4; ++i) e[i] = dt * A2[i];
+  update<S>(e, b, du, h);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) grad[i] = __builtin_fmaf(decay[i], o[i], grad[i]);
+  for (int i = 0; i < 4; ++i) decay[i] *= e[i];
+  f32x4 o = decay;                      // decay C dy: summed over the chunk
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] *= dy;
+  add_each<S>(c, o, grad);
 }
 
 template <typename T>
@@ -83,7 +110,7 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_local_kernel(PromptScanA
       u[g] = bload<T>(ru, l.u + g * static_cast<uint32_t>(4 * a.us * sizeof(T)));
       d[g] = bload<T>(rd, l.d + g * static_cast<uint32_t>(4 * a.ds * sizeof(T)));
       b[g] = bload<T>(rb, l.b + g * static_cast<uint32_t>(4 * a.bs * sizeof(T)));
-      c[g] = bload<T>(rc, l.ct + g * static_cast<uint32_t>(4 * a.cs * sizeof(T)));
+      c[g] = bload<T>(rc, l.c + g * static_cast<uint32_t>(4 * a.cs * sizeof(T)));
       o[g] = bload<T>(ro, doff + g * static_cast<uint32_t>(4 * a.dim * sizeof(T)));
       z[g] = bload<T>(rz, l.z + g * static_cast<uint32_t>(4 * a.zs * sizeof(T)));
     }
@@ -93,12 +120,14 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_local_kernel(PromptScanA
       const float dt = step_of(a, d[g] + bias, 4 * g + l.q < m), du = dt * u[g];
       const float dy = a.z != nullptr ? o[g] * silu_f(z[g]) : o[g];
       steps += dt;
-      float dts[4];
+      float dts[4], dus[4], dys[4];
       hand_out(dt, dts);
-      local_token<0>(A2, dts[0], b[g], du, c[g], dy, h, decay, grad);
-      local_token<1>(A2, dts[1], b[g], du, c[g], dy, h, decay, grad);
-      local_token<2>(A2, dts[2], b[g], du, c[g], dy, h, decay, grad);
-      local_token<3>(A2, dts[3], b[g], du, c[g], dy, h, decay, grad);
+      hand_out(du, dus);
+      hand_out(dy, dys);
+      local_token<0>(A2, dts[0], b[g], dus[0], c[g], dys[0], h, decay, grad);
+      local_token<1>(A2, dts[1], b[g], dus[1], c[g], dys[1], h, decay, grad);
+      local_token<2>(A2, dts[2], b[g], dus[2], c[g], dys[2], h, decay, grad);
+      local_token<3>(A2, dts[3], b[g], dus[3], c[g], dys[3], h, decay, grad);
     }
   }
   const int64_t block = slot * blocks + blk;
@@ -153,7 +182,10 @@ __device__ __forceinline__ void fold(const float (&x)[4][4], const float (&y)[4]
 #pragma unroll
   for (int s = 0; s < 4; ++s) fold8(x[s], y[s], a[s]);
 #pragma unroll
-  for (int s = 0; s < 2; ++s) fold4(a[s], a[s + 2], b[s]);
+  for (int s = 0; s < 2; ++s) {
+    fold4(a[s], a[s + 2], b[s]);
+    settle(b[s]);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) c[i] = fold_quad<0x4e>(b[0][i], b[1][i], (lane & 2) != 0);   // lane ^ 2
 #pragma unroll
@@ -164,21 +196,19 @@ __device__ __forceinline__ void fold(const float (&x)[4][4], const float (&y)[4]
 template <int S>
 __device__ __forceinline__ void again(const float (&A2)[4], float dt, float b, float du, f32x4 &h, f32x4 &decay) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    decay[i] = hw_exp2(dt * A2[i]);
-    h[i] *= decay[i];
-  }
-  h = rank1<S>(b, du, h);
+  for (int i = 0; i < 4; ++i) decay[i] = dt * A2[i];
+  update<S>(decay, b, du, h);
 }
 
 template <int S, bool GATE>
-__device__ __forceinline__ void back_token(const float (&A)[4], float dts, float dus, float dys, float c, float dy, float bt,
-                                           float ct, const f32x4 &decay, const f32x4 &h, const f32x4 &before, f32x4 &p,
+__device__ __forceinline__ void back_token(const float (&A)[4], float dts, float dus, float dys, float b, float c,
+                                           const f32x4 &decay, const f32x4 &h, const f32x4 &before, f32x4 &p,
                                            float (&dA)[4], float (&x)[4], float (&yy)[4], float &w, float &through,
                                            float &y) {
-  const f32x4 g = rank1<S>(c, dy, p);
-  w = read_out<S>(bt, g);
-  if (GATE) y = read_out<S>(ct, h);
+  f32x4 g = p;
+  add_rank1<S>(c, dys, g);
+  w = read_out<S>(b, g);
+  if (GATE) y = read_out<S>(c, h);
   through = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -268,13 +298,14 @@ __global__ __launch_bounds__(64 * kScanWaves, 2) void scan_back_kernel(PromptSca
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const float dt = step_of(a, d[g] + bias, true), du = dt * u[g];
-      float dts[4];
+      float dts[4], dus[4];
       f32x4 e;
       hand_out(dt, dts);
-      again<0>(A2, dts[0], b[g], du, h, e);
-      again<1>(A2, dts[1], b[g], du, h, e);
-      again<2>(A2, dts[2], b[g], du, h, e);
-      again<3>(A2, dts[3], b[g], du, h, e);
+      hand_out(du, dus);
+      again<0>(A2, dts[0], b[g], dus[0], h, e);
+      again<1>(A2, dts[1], b[g], dus[1], h, e);
+      again<2>(A2, dts[2], b[g], dus[2], h, e);
+      again<3>(A2, dts[3], b[g], dus[3], h, e);
     }
   }
 
@@ -285,17 +316,15 @@ __global__ __launch_bounds__(64 * kScanWaves, 2) void scan_back_kernel(PromptSca
     const Rsrc ru = rows<T>(a.u, a.us, t, c0, m, l.cw), rd = rows<T>(a.delta, a.ds, t, c0, m, l.cw),
                rb = rows<T>(a.B, a.bs, t, 0, m, a.n), rc = rows<T>(a.C, a.cs, t, 0, m, a.n),
                ro = rows<T>(a.dout, a.dim, t, c0, m, l.cw), rz = rows<T>(a.z, a.zs, t, c0, GATE ? m : 0, l.cw);
-    float u[kGroups], d[kGroups], b[kGroups], bt[kGroups], c[kGroups], ct[kGroups], o[kGroups], z[kGroups];
+    float u[kGroups], d[kGroups], b[kGroups], c[kGroups], o[kGroups], z[kGroups];
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       u[g] = bload<T>(ru, l.u + g * static_cast<uint32_t>(4 * a.us * sizeof(T)));
       d[g] = bload<T>(rd, l.d + g * static_cast<uint32_t>(4 * a.ds * sizeof(T)));
       b[g] = bload<T>(rb, l.b + g * static_cast<uint32_t>(4 * a.bs * sizeof(T)));
-      bt[g] = bload<T>(rb, l.bt + g * static_cast<uint32_t>(4 * a.bs * sizeof(T)));
-      c[g] = bload<T>(rc, l.ct + g * static_cast<uint32_t>(4 * a.cs * sizeof(T)));
+      c[g] = bload<T>(rc, l.c + g * static_cast<uint32_t>(4 * a.cs * sizeof(T)));
       o[g] = bload<T>(ro, doff + g * dstep);
       if (GATE) {
-        ct[g] = bload<T>(rc, l.c + g * static_cast<uint32_t>(4 * a.cs * sizeof(T)));
         z[g] = bload<T>(rz, l.z + g * static_cast<uint32_t>(4 * a.zs * sizeof(T)));
       }
     }
@@ -307,15 +336,16 @@ __global__ __launch_bounds__(64 * kScanWaves, 2) void scan_back_kernel(PromptSca
     for (int g = 0; g < kGroups; ++g) {
       dt[g] = step_of(a, d[g] + bias, 4 * g + l.q < m);
       const float du = dt[g] * u[g];
-      float dts[4];
+      float dts[4], dus[4];
       hand_out(dt[g], dts);
-      again<0>(A2, dts[0], b[g], du, h, es[4 * g]);
+      hand_out(du, dus);
+      again<0>(A2, dts[0], b[g], dus[0], h, es[4 * g]);
       hs[4 * g] = h;
-      again<1>(A2, dts[1], b[g], du, h, es[4 * g + 1]);
+      again<1>(A2, dts[1], b[g], dus[1], h, es[4 * g + 1]);
       hs[4 * g + 1] = h;
-      again<2>(A2, dts[2], b[g], du, h, es[4 * g + 2]);
+      again<2>(A2, dts[2], b[g], dus[2], h, es[4 * g + 2]);
       hs[4 * g + 2] = h;
-      again<3>(A2, dts[3], b[g], du, h, es[4 * g + 3]);
+      again<3>(A2, dts[3], b[g], dus[3], h, es[4 * g + 3]);
       hs[4 * g + 3] = h;
     }
     float *mine = sums[tile & 1][wave];
@@ -332,23 +362,26 @@ __global__ __launch_bounds__(64 * kScanWaves, 2) void scan_back_kernel(PromptSca
       hand_out(dt[g], dts);
       hand_out(du, dus);
       hand_out(dy, dys);
-      back_token<3, GATE>(A, dts[3], dus[3], dys[3], c[g], dy, bt[g], ct[g], es[4 * g + 3], hs[4 * g + 3], hs[4 * g + 2],
+      back_token<3, GATE>(A, dts[3], dus[3], dys[3], b[g], c[g], es[4 * g + 3], hs[4 * g + 3], hs[4 * g + 2],
                           grad, dA, x[3], yy[3], w[3], th[3], y[3]);
-      back_token<2, GATE>(A, dts[2], dus[2], dys[2], c[g], dy, bt[g], ct[g], es[4 * g + 2], hs[4 * g + 2], hs[4 * g + 1],
+      back_token<2, GATE>(A, dts[2], dus[2], dys[2], b[g], c[g], es[4 * g + 2], hs[4 * g + 2], hs[4 * g + 1],
                           grad, dA, x[2], yy[2], w[2], th[2], y[2]);
-      back_token<1, GATE>(A, dts[1], dus[1], dys[1], c[g], dy, bt[g], ct[g], es[4 * g + 1], hs[4 * g + 1], hs[4 * g],
+      back_token<1, GATE>(A, dts[1], dus[1], dys[1], b[g], c[g], es[4 * g + 1], hs[4 * g + 1], hs[4 * g],
                           grad, dA, x[1], yy[1], w[1], th[1], y[1]);
-      back_token<0, GATE>(A, dts[0], dus[0], dys[0], c[g], dy, bt[g], ct[g], es[4 * g], hs[4 * g],
+      back_token<0, GATE>(A, dts[0], dus[0], dys[0], b[g], c[g], es[4 * g], hs[4 * g],
                           g > 0 ? hs[g > 0 ? 4 * g - 1 : 0] : begin, grad, dA, x[0], yy[0], w[0], th[0], y[0]);
+      settle(w);
+      if (GATE) settle(y);
       const float along = gather(w), through = gather(th);
       if (GATE) {
         const float yt = __builtin_fmaf(D, u[g], gather(y));
-        bstore<T>(rdz, doff + g * dstep, o[g] * yt * slope);
+        put<T>(rdz, doff + g * dstep, o[g] * yt * slope);
       }
-      bstore<T>(rdu, doff + g * dstep, __builtin_fmaf(along, dt[g], D * dy));
+      put<T>(rdu, doff + g * dstep, __builtin_fmaf(along, dt[g], D * dy));
       float dd = __builtin_fmaf(along, u[g], through);
-      if (a.softplus) dd *= hw_rcp(1.0f + hw_exp2((d[g] + bias) * -kLog2e));
-      bstore<T>(rdd, doff + g * dstep, dd);
+      const float slope2 = hw_rcp(1.0f + hw_exp2((d[g] + bias) * -kLog2e));
+      dd *= a.softplus ? slope2 : 1.0f;
+      put<T>(rdd, doff + g * dstep, dd);
       dD = __builtin_fmaf(dy, u[g], dD);
       dbias += in ? dd : 0.0f;
       float r[2];
