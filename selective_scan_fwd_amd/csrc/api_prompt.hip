@@ -137,14 +137,16 @@ bool scan_fits(const vmk::PromptScanArgs &a) { return a.q.slots <= kMaxBlocks / 
 // Temporary memory of the forward and of the backward pass.
 void scan_parts(vmk::PromptScanArgs &a, bool back, Parts &parts) {
   const int64_t blocks = a.q.slots * vmk::scan_blocks(a.dim), tokens = all_tokens(a.q);
-  if (a.q.slots > a.q.nseq + (a.q.off != nullptr ? 1 : 0) || a.q.chunk < a.q.L) {
+  if (a.q.chunk < a.q.L) {
     parts.add(&a.ends, blocks * 256 * 4);
     parts.add(&a.steps, blocks * 16 * 4);
     if (back) parts.add(&a.starts, blocks * 256 * 4);
   }
   if (back) {
     const int64_t wide = vmk::scan_wide(a.dim);
-    parts.add(&a.marks, (tokens / vmk::kBackTile + a.q.slots + 1) * wide * vmk::kScanWaves * 256 * 4);
+    const int64_t tiles = (tokens / vmk::kBackTile + a.q.slots + 1) * vmk::scan_blocks(a.dim);
+    parts.add(&a.marks, tiles * 256 * 4);
+    if (a.q.chunk < a.q.L) parts.add(&a.before, tiles * 16 * 4);
     parts.add(&a.partA, a.q.slots * a.dim * a.n * 4);
     parts.add(&a.partD, a.q.slots * 2 * a.dim * 4);
     parts.add(&a.partBC, wide * tokens * 2 * a.n * 4);
@@ -323,7 +325,7 @@ int vm_prompt_scan(const vm_scan_rows *p, const vm_sequences *q, const float *h0
   if (st != VM_OK) return st;
   if (out == nullptr) return VM_ERR_NULL;
   const int es = size_of(dtype);
-  divide(a.q, vmk::scan_chunk_tokens(all_tokens(a.q), a.q.nseq, seqlen, a.dim, a.q.off != nullptr, false));
+  divide(a.q, vmk::scan_chunk(all_tokens(a.q), a.q.nseq, seqlen, a.dim, a.q.off != nullptr));
   if (!scan_fits(a)) return VM_ERR_UNSUPPORTED;
   const SeqSpans sq(a.q);
   const Span ins[] = {span(p->u, e.u * es), span(p->delta, e.delta * es), span(p->B, e.B * es), span(p->C, e.C * es),
@@ -359,7 +361,8 @@ int64_t vm_prompt_scan_workspace(int64_t batch, int64_t seqlen, int64_t n, int64
   a.q.L = seqlen;
   a.dim = static_cast<int>(dim);
   a.n = static_cast<int>(dstate);
-  divide(a.q, vmk::scan_chunk_tokens(all_tokens(a.q), n, seqlen, a.dim, packed != 0, backward != 0));
+  divide(a.q, backward != 0 ? vmk::scan_back_chunk(all_tokens(a.q), n, seqlen, a.dim, packed != 0)
+                            : vmk::scan_chunk(all_tokens(a.q), n, seqlen, a.dim, packed != 0));
   if (!scan_fits(a)) return -VM_ERR_UNSUPPORTED;
   Parts parts;
   scan_parts(a, backward != 0, parts);
@@ -378,7 +381,7 @@ int vm_prompt_scan_bwd(const vm_scan_rows *p, const vm_sequences *q, const float
       g->dC == nullptr || (g->dz == nullptr) != (p->z == nullptr))
     return VM_ERR_NULL;
   const int es = size_of(dtype);
-  divide(a.q, vmk::scan_chunk_tokens(all_tokens(a.q), a.q.nseq, seqlen, a.dim, a.q.off != nullptr, true));
+  divide(a.q, vmk::scan_back_chunk(all_tokens(a.q), a.q.nseq, seqlen, a.dim, a.q.off != nullptr));
   if (!scan_fits(a)) return VM_ERR_UNSUPPORTED;
   const SeqSpans sq(a.q);
   const int64_t bc = batch * seqlen * N * es;

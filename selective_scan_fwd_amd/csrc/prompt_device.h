@@ -20,6 +20,7 @@ struct Piece {
   int64_t lo, hi;        // the sequence's tokens
   int64_t t0;            // the chunk's first token
   int len;               // its tokens; 0 for an empty sequence's only chunk, -1: no chunk
+  int64_t id;            // its slot in the tokens' order
 };
 
 __device__ __forceinline__ int64_t clamped(int32_t x, int64_t most) {
@@ -48,12 +49,43 @@ __device__ __forceinline__ Piece piece_of(const SeqArgs &q, int64_t slot) {
     p.hi = clamped(q.off[a + 1], q.L);
     p.c = static_cast<int>(slot - p.lo / q.chunk - a);
   }
+  p.id = slot;
   const int64_t all = p.hi - p.lo;
   p.count = all > q.chunk ? static_cast<int>((all + q.chunk - 1) / q.chunk) : 1;
   p.t0 = p.lo + p.c * q.chunk;
   const int64_t left = p.hi - p.t0;
   p.len = static_cast<int>(left < q.chunk ? left : q.chunk);
   if (p.c < 0 || p.c >= p.count || p.len < 0) p.len = p.c == 0 && all <= 0 ? 0 : -1;
+  return p;
+}
+
+// The same for a whole wave with up to 64 packed sequences, whose slots then go by
+// falling length, so that no long sequence starts last.
+__device__ __forceinline__ Piece piece_by_length(const SeqArgs &q, int64_t slot) {
+  if (q.off == nullptr || q.nseq > 64) return piece_of(q, slot);
+  const int lane = threadIdx.x % 64;
+  const bool has = lane < q.nseq;
+  const int lo = has ? static_cast<int>(clamped(q.off[lane], q.L)) : 0;
+  const int len = has ? static_cast<int>(clamped(q.off[lane + 1], q.L)) - lo : -1;
+  const int chunk = static_cast<int>(q.chunk);
+  const int count = !has ? 0 : len > chunk ? (len + chunk - 1) / chunk : 1;
+  int start = 0;
+  for (int i = 0; i < q.nseq; ++i) {
+    const int l = __builtin_amdgcn_readlane(len, i), c = __builtin_amdgcn_readlane(count, i);
+    start += l > len || (l == len && i < lane) ? c : 0;
+  }
+  Piece p;
+  const uint64_t mine = __ballot(has && slot >= start && slot < start + count);
+  p.seq = mine != 0 ? __builtin_ctzll(mine) : 0;
+  p.lo = __builtin_amdgcn_readlane(lo, p.seq);
+  const int all = __builtin_amdgcn_readlane(len, p.seq);
+  p.hi = p.lo + (all > 0 ? all : 0);
+  p.count = __builtin_amdgcn_readlane(count, p.seq);
+  p.c = static_cast<int>(slot) - __builtin_amdgcn_readlane(start, p.seq);
+  p.id = p.lo / chunk + p.seq + p.c;
+  p.t0 = p.lo + static_cast<int64_t>(p.c) * chunk;
+  const int64_t left = p.hi - p.t0;
+  p.len = mine == 0 ? -1 : static_cast<int>(left < chunk ? left : chunk);
   return p;
 }
 
@@ -124,7 +156,27 @@ __device__ __forceinline__ void settle(float (&y)[4]) {
       [e0] "+&v"(e[0]), [e1] "+&v"(e[1]), [e2] "+&v"(e[2]), [e3] "+&v"(e[3])
 template <int S> __device__ __forceinline__ void update(f32x4 &e, float b, float x, f32x4 &h);
 template <int S> __device__ __forceinline__ float update_read(f32x4 &e, float b, float x, float c, f32x4 &h);
+// The same from state h into another, r.
+template <int S> __device__ __forceinline__ void update_to(f32x4 &e, float b, float x, const f32x4 &h, f32x4 &r);
 #define VM_UPDATE(S, A, B, C, D)                                               \
+  template <>                                                                  \
+  __device__ __forceinline__ void update_to<S>(f32x4 &e, float b, float x, const f32x4 &h, f32x4 &r) { \
+    asm("v_exp_f32 %[e0], %[e0]\n"                                             \
+        "v_exp_f32 %[e1], %[e1]\n"                                             \
+        "v_exp_f32 %[e2], %[e2]\n"                                             \
+        "v_exp_f32 %[e3], %[e3]\n"                                             \
+        "v_mul_f32 %[r0], %[h0], %[e0]\n"                                      \
+        "v_mul_f32 %[r1], %[h1], %[e1]\n"                                      \
+        "v_mul_f32 %[r2], %[h2], %[e2]\n"                                      \
+        "v_mul_f32 %[r3], %[h3], %[e3]\n"                                      \
+        "v_fmac_f32_dpp %[r0], %[b], %[x] row_newbcast:" #A " row_mask:0xf bank_mask:0xf\n" \
+        "v_fmac_f32_dpp %[r1], %[b], %[x] row_newbcast:" #B " row_mask:0xf bank_mask:0xf\n" \
+        "v_fmac_f32_dpp %[r2], %[b], %[x] row_newbcast:" #C " row_mask:0xf bank_mask:0xf\n" \
+        "v_fmac_f32_dpp %[r3], %[b], %[x] row_newbcast:" #D " row_mask:0xf bank_mask:0xf\n" \
+        : [r0] "=&v"(r[0]), [r1] "=&v"(r[1]), [r2] "=&v"(r[2]), [r3] "=&v"(r[3]), \
+          [e0] "+&v"(e[0]), [e1] "+&v"(e[1]), [e2] "+&v"(e[2]), [e3] "+&v"(e[3]) \
+        : [h0] "v"(h[0]), [h1] "v"(h[1]), [h2] "v"(h[2]), [h3] "v"(h[3]), [b] "v"(b), [x] "v"(x)); \
+  }                                                                            \
   template <>                                                                  \
   __device__ __forceinline__ void update<S>(f32x4 &e, float b, float x, f32x4 &h) { \
     asm(VM_UPDATE_TEXT(A, B, C, D) : VM_UPDATE_OUT : [b] "v"(b), [x] "v"(x));  \
@@ -182,7 +234,7 @@ struct Lane {
   int ch, q;                          // channel of the block, row of 16 lanes
   int cw;                             // channels of the block that exist
   bool live;
-  uint32_t u, d, z;                   // token q of a tile
+  uint32_t u, d, z, dense;            // token q of a tile (dense: of outputs and their gradients)
   uint32_t b, c;                      // B and C of a group: token (l / 4) % 4, state 4 q + l % 4
   uint32_t state[4];                  // in a block's [16][n]
 };
@@ -201,6 +253,7 @@ __device__ __forceinline__ Lane lane_of(const PromptScanArgs &a, int c0, int lan
   l.u = at(l.live, a.us, q, ch);
   l.d = at(l.live, a.ds, q, ch);
   l.z = at(l.live, a.zs, q, ch);
+  l.dense = at(l.live, a.dim, q, ch);
   const uint32_t state = 4 * q + lo;
   l.b = at(state < static_cast<uint32_t>(a.n), a.bs, hi, state);
   l.c = at(state < static_cast<uint32_t>(a.n), a.cs, hi, state);
@@ -235,6 +288,34 @@ __device__ __forceinline__ void put(Rsrc r, uint32_t off, float x) {
                                           0, 0);
   else
     bstore<T>(r, off, x);
+}
+
+// Joins chunks to x: x <- 2^(A2 t_j) x + e_j for the blocks j = first, first + step, ...
+// of `many` (with loads of four under way).
+__device__ __forceinline__ void join_chunks(const float *ends, const float *steps, int64_t first, int64_t step, int many,
+                                            int lane, const float (&A2)[4], f32x4 &x) {
+  int j = 0;
+  for (; j + 4 <= many; j += 4) {
+    f32x4 e[4];
+    float t[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t at = first + (j + k) * step;
+      e[k] = *reinterpret_cast<const f32x4 *>(ends + at * 256 + lane * 4);
+      t[k] = steps[at * 16 + lane % 16];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = __builtin_fmaf(hw_exp2(A2[i] * t[k]), x[i], e[k][i]);
+  }
+  for (; j < many; ++j) {
+    const int64_t at = first + j * step;
+    const f32x4 e = *reinterpret_cast<const f32x4 *>(ends + at * 256 + lane * 4);
+    const float t = steps[at * 16 + lane % 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __builtin_fmaf(hw_exp2(A2[i] * t), x[i], e[i]);
+  }
 }
 
 // Decay rates, ready for 2^x.  A rate of -Inf (which decays to 0 in any step) is

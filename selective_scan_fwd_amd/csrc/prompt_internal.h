@@ -95,8 +95,11 @@ struct PromptScanArgs {
   void *du, *ddelta, *dB, *dC, *dz;   // dense
   float *dh0;
   float *starts;             // as ends: gradients of the states before a chunk
-  float *marks;              // [tile][block][64][4]: states at the tiles' starts; a chunk's tiles
-                             // have the numbers from (first token) / kBackTile + slot on
+  // [tile][block][64][4]: states at the tiles' starts (with several chunks from zero at
+  // the chunk's, and then [tile][block][16]: the sum of the chunk's steps before them).
+  // A chunk's tiles have the numbers from (first token) / kBackTile + (its slot in the
+  // tokens' order) on.
+  float *marks, *before;
   float *partA, *partD;      // [slot][dim][n], [slot][2][dim]
   float *partBC;             // [workgroup's blocks][token][2 n]
 };
@@ -105,7 +108,8 @@ inline int scan_blocks(int dim) { return (dim + 15) / 16; }
 inline int scan_wide(int dim) { return (scan_blocks(dim) + 3) / 4; }
 constexpr int kBackTile = 16;     // tokens of a tile of the backward pass
 constexpr int kScanWaves = 4;     // blocks of 16 channels to a workgroup
-int64_t scan_chunk_tokens(int64_t tokens, int64_t nseq, int64_t L, int dim, bool packed, bool back);
+int64_t scan_chunk(int64_t tokens, int64_t nseq, int64_t L, int dim, bool packed);
+int64_t scan_back_chunk(int64_t tokens, int64_t nseq, int64_t L, int dim, bool packed);
 hipError_t launch_prompt_scan(const PromptScanArgs &a, bool bf16, hipStream_t s);
 hipError_t launch_prompt_scan_back(const PromptScanArgs &a, bool bf16, hipStream_t s);
 

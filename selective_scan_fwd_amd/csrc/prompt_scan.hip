@@ -13,6 +13,8 @@
 // before it, h <- exp(A T) h + end, and walks it in full.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
+
 #include "prompt_device.h"
 
 namespace vmk {
@@ -127,11 +129,25 @@ __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScan
   const int lane = threadIdx.x % 64;
   const int blocks = (a.dim + 15) / 16, waves = blockDim.x / 64;
   const int wide = (blocks + waves - 1) / waves;
-  const int64_t slot = blockIdx.x / wide;
+  int64_t slot = blockIdx.x / wide;
+  if (a.q.off == nullptr && a.ends != nullptr) {   // all chunks of a sequence but its last or first
+    const int64_t per = (a.q.L + a.q.chunk - 1) / a.q.chunk, seq = slot / (per - 1);
+    slot += seq + (SECOND ? 1 : 0);
+  }
   const int blk = uniform(static_cast<int>(blockIdx.x % wide) * waves + threadIdx.x / 64);
   if (blk >= blocks) return;
-  const Piece p = piece_of(a.q, slot);
+  const Piece p = piece_by_length(a.q, slot);
   if (p.len < 0 || (SECOND ? p.c == 0 : p.c > 0 && p.c == p.count - 1)) return;
+  // a long chunk goes on at its own pace beside short ones
+  const int64_t part = p.len * int64_t{4} / (a.q.chunk < a.q.L ? a.q.chunk : a.q.L);
+  if (a.q.off != nullptr) {
+    if (part >= 3)
+      __builtin_amdgcn_s_setprio(3);
+    else if (part == 2)
+      __builtin_amdgcn_s_setprio(2);
+    else if (part == 1)
+      __builtin_amdgcn_s_setprio(1);
+  }
   const int c0 = blk * 16;
   const Lane l = lane_of<T>(a, c0, lane);
   float A2[4];
@@ -150,12 +166,7 @@ __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScan
       for (int i = 0; i < 4; ++i) h[i] = bload<float>(rh, l.state[i]);
     }
   } else {
-    for (int64_t j = block - static_cast<int64_t>(p.c) * blocks; j < block; j += blocks) {
-      const f32x4 e = *reinterpret_cast<const f32x4 *>(a.ends + j * 256 + lane * 4);
-      const float t = a.steps[j * 16 + l.ch];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = __builtin_fmaf(hw_exp2(A2[i] * t), h[i], e[i]);
-    }
+    join_chunks(a.ends, a.steps, block - static_cast<int64_t>(p.c) * blocks, blocks, p.c, lane, A2, h);
   }
   float steps;
   if (SECOND || p.c == 0)
@@ -179,7 +190,8 @@ __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScan
 template <typename T, bool GATE>
 hipError_t launch_scan(const PromptScanArgs &a, hipStream_t s) {
   const int blocks = (a.dim + 15) / 16, waves = blocks < kScanWaves ? blocks : kScanWaves;
-  const dim3 grid(static_cast<uint32_t>(a.q.slots * ((blocks + waves - 1) / waves)));
+  const int64_t slots = a.q.off == nullptr && a.ends != nullptr ? a.q.slots - a.q.nseq : a.q.slots;
+  const dim3 grid(static_cast<uint32_t>(slots * ((blocks + waves - 1) / waves)));
   prompt_scan_kernel<T, GATE, false><<<grid, 64 * waves, 0, s>>>(a);
   if (a.ends != nullptr) prompt_scan_kernel<T, GATE, true><<<grid, 64 * waves, 0, s>>>(a);
   return hipGetLastError();
@@ -191,15 +203,32 @@ int64_t seq_slots(int64_t nseq, int64_t L, int64_t chunk, bool packed) {
   return packed ? L / chunk + nseq : nseq * ((L + chunk - 1) / chunk);
 }
 
-int64_t scan_chunk_tokens(int64_t tokens, int64_t nseq, int64_t L, int dim, bool packed, bool back) {
-  (void)back;
-  // waves that fill the card
-  const int64_t want = 2048 / scan_blocks(dim) + 1;
-  if (!packed && nseq >= want) return L;
-  int64_t chunk = packed ? (tokens + want - 1) / want : (L + (want + nseq - 1) / nseq - 1) / ((want + nseq - 1) / nseq);
-  chunk = (chunk + 15) / 16 * 16;
-  if (chunk < 64) chunk = 64;
-  return chunk < L ? chunk : L;
+// Chunks of a forward pass.  In cycles a token: a wave takes some 205 alone on its SIMD,
+// k together 60 + 131 k; without read-out three quarters (but the first chunk is walked in
+// full in the first launch, which shows where waves are alone).  A second launch costs some
+// 25000, and a chunk 900 for the joining of all before it.
+int64_t scan_chunk(int64_t tokens, int64_t nseq, int64_t L, int dim, bool packed) {
+  const int64_t blocks = scan_blocks(dim);
+  if (packed) {                              // (the lengths are not known here)
+    const int64_t want = 1024 / blocks + 1, chunk = (tokens / want + kTile) / kTile * kTile;
+    return chunk < 64 ? (L < 64 ? L : 64) : chunk < L ? chunk : L;
+  }
+  const auto pace = [](double k) { return k <= 1 ? 205 : 60 + 131 * (k < 4 ? ceil(k) : k); };
+  const double all = static_cast<double>(nseq * blocks) / 1024.0;
+  int64_t best = L;
+  double least = L * pace(all);
+  for (int64_t parts = 2; parts <= 128; ++parts) {
+    const int64_t chunk = ((L + parts - 1) / parts + kTile - 1) / kTile * kTile;
+    if (chunk < 32) break;
+    if (chunk >= L) continue;
+    const double k = all * (parts - 1), full = pace(k);
+    const double cost = chunk * full * (parts == 2 || k <= 1 ? 2.0 : 1.75) + 25000 + parts * 900;
+    if (cost < least) {
+      least = cost;
+      best = chunk;
+    }
+  }
+  return best;
 }
 
 hipError_t launch_prompt_scan(const PromptScanArgs &a, bool bf16, hipStream_t s) {

@@ -5,14 +5,15 @@
 //   du = dt w + D dy;    ddt = u w + sum_n A p_t h_{t-1};  ddelta = ddt softplus'
 //   dA = sum_t dt p_t h_{t-1};  dD = sum_t u dy;  dz = dout y SiLU'(z)
 //
-// The lane layout is the forward pass's (prompt_device.h).  A workgroup walks one
-// chunk of four blocks of 16 channels: forward once, leaving the states at the
-// starts of its tiles of 16 tokens in memory, then back over the tiles, whose
-// states and decays are formed again and held in registers.  Where sequences have
-// several chunks, a launch before it walks every chunk from a zero state and a zero
-// gradient: with P_t the product of the decays from the chunk's start to t,
+// The lane layout is the forward pass's (prompt_device.h).  A first launch walks every
+// chunk forward and leaves the states at the starts of its tiles of 16 tokens in memory.
+// The second walks back over the tiles, a workgroup over one chunk of four blocks of 16
+// channels: a tile's states and decays are formed again and held in registers.  Where
+// sequences have several chunks, the first launch starts each of them from a zero state
+// and gathers the gradient of the state before it besides; with P_t the product of the
+// decays from the chunk's start to t,
 //   end state = sum over the chunk as forward,  gradient before it = sum P_t C_t dy_t,
-// and each chunk joins what it needs from the chunks on either side.
+// and the second launch joins what a chunk needs from those on either side of it.
 // Sums over channels: 32 products of a group of 4 tokens are folded over the 16
 // lanes of a row, halving the values at each step, then over the workgroup's waves
 // in LDS; sums over blocks and chunks in a fixed order by launches of their own.
@@ -33,21 +34,6 @@ __device__ __forceinline__ float silu_both(float z, float &slope) {
 }
 
 // ------------------------------------------------- chunks by themselves
-// h[i] += b[4 S + i] x
-template <int S> __device__ __forceinline__ void add_rank1(float b, float x, f32x4 &h);
-#define VM_RANK1(S, A, B, C, D)                                                       \
-  template <>                                                                         \
-  __device__ __forceinline__ void add_rank1<S>(float b, float x, f32x4 &h) {          \
-    asm("s_nop 1\n"                                                                   \
-        "v_fmac_f32_dpp %0, %4, %5 row_newbcast:" #A " row_mask:0xf bank_mask:0xf\n"  \
-        "v_fmac_f32_dpp %1, %4, %5 row_newbcast:" #B " row_mask:0xf bank_mask:0xf\n"  \
-        "v_fmac_f32_dpp %2, %4, %5 row_newbcast:" #C " row_mask:0xf bank_mask:0xf\n"  \
-        "v_fmac_f32_dpp %3, %4, %5 row_newbcast:" #D " row_mask:0xf bank_mask:0xf\n"  \
-        : "+&v"(h[0]), "+&v"(h[1]), "+&v"(h[2]), "+&v"(h[3])                          \
-        : "v"(b), "v"(x));                                                            \
-  }
-VM_RANK1(0, 0, 1, 2, 3) VM_RANK1(1, 4, 5, 6, 7) VM_RANK1(2, 8, 9, 10, 11) VM_RANK1(3, 12, 13, 14, 15)
-#undef VM_RANK1
 // g[i] += c[4 S + i] x[i]
 template <int S> __device__ __forceinline__ void add_each(float c, const f32x4 &x, f32x4 &g);
 #define VM_ADD_EACH(S, A, B, C, D)                                                    \
@@ -79,14 +65,117 @@ __device__ __forceinline__ void local_token(const float (&A2)[4], float dt, floa
   add_each<S>(c, o, grad);
 }
 
-template <typename T>
-__global__ __launch_bounds__(64 * kScanWaves) void scan_local_kernel(PromptScanArgs a, int wide) {
+// The state after a token, r, from the one before it, and its decays.
+template <int S>
+__device__ __forceinline__ void again(const float (&A2)[4], float dt, float b, float du, const f32x4 &h, f32x4 &r, f32x4 &decay) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) decay[i] = dt * A2[i];
+  f32x4 to;
+  update_to<S>(decay, b, du, h, to);
+  r = to;
+}
+
+// What a tile's tokens bring, as loaded.
+struct Raw {
+  float u[kGroups], d[kGroups], b[kGroups], c[kGroups], o[kGroups], z[kGroups];
+};
+template <typename T, bool ALL, bool GATE>
+__device__ __forceinline__ void load_tile(const PromptScanArgs &a, const Lane &l, int64_t t, int left, int c0, Raw &r) {
+  const int m = left < kBackTile ? left : kBackTile;
+  const Rsrc ru = rows<T>(a.u, a.us, t, c0, m, l.cw), rd = rows<T>(a.delta, a.ds, t, c0, m, l.cw),
+             rb = rows<T>(a.B, a.bs, t, 0, m, a.n);
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    r.u[g] = bload<T>(ru, l.u + g * static_cast<uint32_t>(4 * a.us * sizeof(T)));
+    r.d[g] = bload<T>(rd, l.d + g * static_cast<uint32_t>(4 * a.ds * sizeof(T)));
+    r.b[g] = bload<T>(rb, l.b + g * static_cast<uint32_t>(4 * a.bs * sizeof(T)));
+  }
+  if (!ALL) return;
+  const Rsrc rc = rows<T>(a.C, a.cs, t, 0, m, a.n), ro = rows<T>(a.dout, a.dim, t, c0, m, l.cw),
+             rz = rows<T>(a.z, a.zs, t, c0, GATE ? m : 0, l.cw);
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    r.c[g] = bload<T>(rc, l.c + g * static_cast<uint32_t>(4 * a.cs * sizeof(T)));
+    r.o[g] = bload<T>(ro, l.dense + g * static_cast<uint32_t>(4 * a.dim * sizeof(T)));
+    if (GATE) r.z[g] = bload<T>(rz, l.z + g * static_cast<uint32_t>(4 * a.zs * sizeof(T)));
+  }
+}
+
+// Walks a chunk forward from state h.  MANY: one of several of its sequence, from zero.
+template <typename T, bool GATE, bool MANY>
+__device__ __forceinline__ void mark_chunk(const PromptScanArgs &a, const Lane &l, const Piece &p, int64_t slot, int blk,
+                                           int lane, const float (&A2)[4], float bias, f32x4 h, float (*meet)[16][12]) {
+  const int blocks = (a.dim + 15) / 16, c0 = blk * 16;
+  const int64_t first = (p.t0 / kBackTile + p.id) * blocks + blk;
+  float *mark = a.marks + first * 256 + lane * 4, *before = a.before + first * 16 + l.ch;
+  const int64_t mstep = static_cast<int64_t>(blocks) * 256;
+  f32x4 decay = {1, 1, 1, 1}, grad = {0, 0, 0, 0};
+  float steps = 0.0f;
+  Raw next;
+  load_tile<T, MANY, GATE>(a, l, p.t0, p.len, c0, next);
+  for (int at = 0; at < p.len; at += kBackTile) {
+    const Raw r = next;
+    const int m = p.len - at;
+    load_tile<T, MANY, GATE>(a, l, p.t0 + at + kBackTile, m - kBackTile, c0, next);
+    *reinterpret_cast<f32x4 *>(mark) = h;
+    mark += mstep;
+    if (MANY) {
+      if (l.q == 0) *before = steps;
+      before += blocks * 16;
+    } else if (m <= kBackTile) {
+      break;                               // (nobody asks for the state after the last tile)
+    }
+    float mine = 0.0f;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const float dt = step_of(a, r.d[g] + bias, 4 * g + l.q < m);
+      meet[g][l.ch][2 * l.q] = dt;
+      meet[g][l.ch][2 * l.q + 1] = dt * r.u[g];
+      if (MANY) {
+        meet[g][l.ch][8 + l.q] = GATE ? r.o[g] * silu_f(r.z[g]) : r.o[g];
+        mine += dt;
+      }
+    }
+    wave_lds_fence();
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const auto &w = meet[g][l.ch];
+      if (MANY) {
+        local_token<0>(A2, w[0], r.b[g], w[1], r.c[g], w[8], h, decay, grad);
+        local_token<1>(A2, w[2], r.b[g], w[3], r.c[g], w[9], h, decay, grad);
+        local_token<2>(A2, w[4], r.b[g], w[5], r.c[g], w[10], h, decay, grad);
+        local_token<3>(A2, w[6], r.b[g], w[7], r.c[g], w[11], h, decay, grad);
+      } else {
+        f32x4 e;
+        again<0>(A2, w[0], r.b[g], w[1], h, h, e);
+        again<1>(A2, w[2], r.b[g], w[3], h, h, e);
+        again<2>(A2, w[4], r.b[g], w[5], h, h, e);
+        again<3>(A2, w[6], r.b[g], w[7], h, h, e);
+      }
+    }
+    wave_lds_fence();
+    if (MANY) {
+      const float s[4] = {mine, mine, mine, mine};
+      steps += gather(s);
+    }
+  }
+  if (MANY) {
+    const int64_t block = slot * blocks + blk;
+    *reinterpret_cast<f32x4 *>(a.ends + block * 256 + lane * 4) = h;
+    *reinterpret_cast<f32x4 *>(a.starts + block * 256 + lane * 4) = grad;
+    if (l.q == 0) a.steps[block * 16 + l.ch] = steps;
+  }
+}
+
+template <typename T, bool GATE>
+__global__ __launch_bounds__(64 * kScanWaves) void scan_marks_kernel(PromptScanArgs a, int wide) {
+  __shared__ __align__(16) float meets[kScanWaves][kGroups][16][12];
   const int lane = threadIdx.x % 64, blocks = (a.dim + 15) / 16;
   const int64_t slot = blockIdx.x / wide;
   const int blk = uniform(static_cast<int>(blockIdx.x % wide) * kScanWaves + threadIdx.x / 64);
   if (blk >= blocks) return;
-  const Piece p = piece_of(a.q, slot);
-  if (p.len <= 0 || p.count == 1) return;
+  const Piece p = piece_by_length(a.q, slot);
+  if (p.len <= 0) return;
   const int c0 = blk * 16;
   const Lane l = lane_of<T>(a, c0, lane);
   float A2[4];
@@ -94,48 +183,17 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_local_kernel(PromptScanA
 #pragma unroll
   for (int i = 0; i < 4; ++i) A2[i] = rate2(bload<float>(rA, l.state[i]));
   const float bias = channel_value(a.bias, c0, l);
-  const uint32_t doff = l.live ? (l.q * static_cast<uint32_t>(a.dim) + l.ch) * sizeof(T) : kOob;
-  f32x4 h = {0, 0, 0, 0}, decay = {1, 1, 1, 1}, grad = {0, 0, 0, 0};
-  float steps = 0.0f;
-  for (int at = 0; at < p.len; at += kBackTile) {
-    const int m = p.len - at < kBackTile ? p.len - at : kBackTile;
-    const int64_t t = p.t0 + at;
-    const Rsrc ru = rows<T>(a.u, a.us, t, c0, m, l.cw), rd = rows<T>(a.delta, a.ds, t, c0, m, l.cw),
-               rb = rows<T>(a.B, a.bs, t, 0, m, a.n), rc = rows<T>(a.C, a.cs, t, 0, m, a.n),
-               ro = rows<T>(a.dout, a.dim, t, c0, m, l.cw),
-               rz = rows<T>(a.z, a.zs, t, c0, a.z != nullptr ? m : 0, l.cw);
-    float u[kGroups], d[kGroups], b[kGroups], c[kGroups], o[kGroups], z[kGroups];
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      u[g] = bload<T>(ru, l.u + g * static_cast<uint32_t>(4 * a.us * sizeof(T)));
-      d[g] = bload<T>(rd, l.d + g * static_cast<uint32_t>(4 * a.ds * sizeof(T)));
-      b[g] = bload<T>(rb, l.b + g * static_cast<uint32_t>(4 * a.bs * sizeof(T)));
-      c[g] = bload<T>(rc, l.c + g * static_cast<uint32_t>(4 * a.cs * sizeof(T)));
-      o[g] = bload<T>(ro, doff + g * static_cast<uint32_t>(4 * a.dim * sizeof(T)));
-      z[g] = bload<T>(rz, l.z + g * static_cast<uint32_t>(4 * a.zs * sizeof(T)));
-    }
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      if (4 * g >= m) break;
-      const float dt = step_of(a, d[g] + bias, 4 * g + l.q < m), du = dt * u[g];
-      const float dy = a.z != nullptr ? o[g] * silu_f(z[g]) : o[g];
-      steps += dt;
-      float dts[4], dus[4], dys[4];
-      hand_out(dt, dts);
-      hand_out(du, dus);
-      hand_out(dy, dys);
-      local_token<0>(A2, dts[0], b[g], dus[0], c[g], dys[0], h, decay, grad);
-      local_token<1>(A2, dts[1], b[g], dus[1], c[g], dys[1], h, decay, grad);
-      local_token<2>(A2, dts[2], b[g], dus[2], c[g], dys[2], h, decay, grad);
-      local_token<3>(A2, dts[3], b[g], dus[3], c[g], dys[3], h, decay, grad);
-    }
+  f32x4 h = {0, 0, 0, 0};
+  if (p.count > 1) {
+    mark_chunk<T, GATE, true>(a, l, p, slot, blk, lane, A2, bias, h, meets[threadIdx.x / 64]);
+    return;
   }
-  const int64_t block = slot * blocks + blk;
-  const float s[4] = {steps, steps, steps, steps};
-  steps = gather(s);
-  *reinterpret_cast<f32x4 *>(a.ends + block * 256 + lane * 4) = h;
-  *reinterpret_cast<f32x4 *>(a.starts + block * 256 + lane * 4) = grad;
-  if (l.q == 0) a.steps[block * 16 + l.ch] = steps;
+  if (a.h0 != nullptr) {
+    const Rsrc r = make_rsrc(a.h0 + (static_cast<int64_t>(p.seq) * a.dim + c0) * a.n, l.cw * a.n * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = bload<float>(r, l.state[i]);
+  }
+  mark_chunk<T, GATE, false>(a, l, p, slot, blk, lane, A2, bias, h, meets[threadIdx.x / 64]);
 }
 
 // ------------------------------------------------------------ folding
@@ -193,44 +251,79 @@ __device__ __forceinline__ void fold(const float (&x)[4][4], const float (&y)[4]
 }
 
 // ------------------------------------------------------- a chunk's gradients
-template <int S>
-__device__ __forceinline__ void again(const float (&A2)[4], float dt, float b, float du, f32x4 &h, f32x4 &decay) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) decay[i] = dt * A2[i];
-  update<S>(decay, b, du, h);
-}
+// yy[i] = h[i] dy,  g[i] += c[4 S + i] dy,  w = sum_i b[4 S + i] g[i], and with READ
+// y = sum_i c[4 S + i] h[i]  (w and y to be settled; the four products before the first
+// DPP operand are its two states, for b and c).
+template <int S, bool READ>
+__device__ __forceinline__ void back_sums(float dy, float b, float c, const f32x4 &h, f32x4 &g, float (&yy)[4], float &w, float &y);
+#define VM_BACK_TEXT(A, B, C, D)                                                                   \
+  "v_mul_f32 %[m0], %[h0], %[dy]\n"                                                                \
+  "v_mul_f32 %[m1], %[h1], %[dy]\n"                                                                \
+  "v_mul_f32 %[m2], %[h2], %[dy]\n"                                                                \
+  "v_mul_f32 %[m3], %[h3], %[dy]\n"                                                                \
+  "v_fmac_f32_dpp %[g0], %[c], %[dy] row_newbcast:" #A " row_mask:0xf bank_mask:0xf\n"             \
+  "v_fmac_f32_dpp %[g1], %[c], %[dy] row_newbcast:" #B " row_mask:0xf bank_mask:0xf\n"             \
+  "v_fmac_f32_dpp %[g2], %[c], %[dy] row_newbcast:" #C " row_mask:0xf bank_mask:0xf\n"             \
+  "v_fmac_f32_dpp %[g3], %[c], %[dy] row_newbcast:" #D " row_mask:0xf bank_mask:0xf\n"
+#define VM_BACK_W(OP, I, L) "v_" OP "_f32_dpp %[w], %[b], %[g" #I "] row_newbcast:" #L " row_mask:0xf bank_mask:0xf\n"
+#define VM_BACK_Y(OP, I, L) "v_" OP "_f32_dpp %[y], %[c], %[h" #I "] row_newbcast:" #L " row_mask:0xf bank_mask:0xf\n"
+#define VM_BACK_OUT                                                                                \
+  [g0] "+&v"(g[0]), [g1] "+&v"(g[1]), [g2] "+&v"(g[2]), [g3] "+&v"(g[3]), [m0] "=&v"(yy[0]),       \
+      [m1] "=&v"(yy[1]), [m2] "=&v"(yy[2]), [m3] "=&v"(yy[3]), [w] "=&v"(w)
+#define VM_BACK_IN                                                                                 \
+  [h0] "v"(h[0]), [h1] "v"(h[1]), [h2] "v"(h[2]), [h3] "v"(h[3]), [b] "v"(b), [c] "v"(c), [dy] "v"(dy)
+#define VM_BACK(S, A, B, C, D)                                                                     \
+  template <>                                                                                      \
+  __device__ __forceinline__ void back_sums<S, false>(float dy, float b, float c, const f32x4 &h, f32x4 &g, \
+                                                      float (&yy)[4], float &w, float &) {         \
+    asm(VM_BACK_TEXT(A, B, C, D) VM_BACK_W("mul", 0, A) VM_BACK_W("fmac", 1, B)                    \
+        VM_BACK_W("fmac", 2, C) VM_BACK_W("fmac", 3, D) : VM_BACK_OUT : VM_BACK_IN);               \
+  }                                                                                                \
+  template <>                                                                                      \
+  __device__ __forceinline__ void back_sums<S, true>(float dy, float b, float c, const f32x4 &h, f32x4 &g, \
+                                                     float (&yy)[4], float &w, float &y) {         \
+    asm(VM_BACK_TEXT(A, B, C, D) VM_BACK_W("mul", 0, A) VM_BACK_Y("mul", 0, A) VM_BACK_W("fmac", 1, B) \
+        VM_BACK_Y("fmac", 1, B) VM_BACK_W("fmac", 2, C) VM_BACK_Y("fmac", 2, C) VM_BACK_W("fmac", 3, D) \
+        VM_BACK_Y("fmac", 3, D) : VM_BACK_OUT, [y] "=&v"(y) : VM_BACK_IN);                         \
+  }
+VM_BACK(0, 0, 1, 2, 3) VM_BACK(1, 4, 5, 6, 7) VM_BACK(2, 8, 9, 10, 11) VM_BACK(3, 12, 13, 14, 15)
+#undef VM_BACK
+#undef VM_BACK_TEXT
+#undef VM_BACK_W
+#undef VM_BACK_Y
+#undef VM_BACK_OUT
+#undef VM_BACK_IN
 
 template <int S, bool GATE>
 __device__ __forceinline__ void back_token(const float (&A)[4], float dts, float dus, float dys, float b, float c,
                                            const f32x4 &decay, const f32x4 &h, const f32x4 &before, f32x4 &p,
                                            float (&dA)[4], float (&x)[4], float (&yy)[4], float &w, float &through,
                                            float &y) {
-  f32x4 g = p;
-  add_rank1<S>(c, dys, g);
-  w = read_out<S>(b, g);
-  if (GATE) y = read_out<S>(c, h);
+  back_sums<S, GATE>(dys, b, c, h, p, yy, w, y);
   through = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[i] = g[i] * dus;
-    yy[i] = h[i] * dys;
-    p[i] = decay[i] * g[i];
+    x[i] = p[i] * dus;
+    p[i] *= decay[i];
     const float m = p[i] * before[i];
     dA[i] = __builtin_fmaf(m, dts, dA[i]);
-    through = __builtin_fmaf(m, A[i], through);
+    through = i == 0 ? m * A[0] : __builtin_fmaf(m, A[i], through);
   }
 }
 
 template <typename T, bool GATE>
 __global__ __launch_bounds__(64 * kScanWaves, 2) void scan_back_kernel(PromptScanArgs a, int wide) {
-  __shared__ float sums[2][kScanWaves][kBackTile * 32];
-  const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), blocks = (a.dim + 15) / 16, padded = wide * kScanWaves;
+  __shared__ __align__(16) float sums[2][kScanWaves][kBackTile * 32];
+  __shared__ __align__(16) float meets[kScanWaves][kGroups][16][12];
+  const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), blocks = (a.dim + 15) / 16;
   const int64_t slot = blockIdx.x / wide;
   const int group = blockIdx.x % wide, blk = group * kScanWaves + wave;
-  Piece p = piece_of(a.q, slot);
+  float(*meet)[16][12] = meets[wave];
+  Piece p = piece_by_length(a.q, slot);
   const bool none = p.len < 0;         // a slot without a chunk: its partial sums are 0
   if (none) {
     p.seq = p.c = p.len = 0;
+    p.id = 0;
     p.count = 1;
     p.t0 = 0;
   }
@@ -245,108 +338,68 @@ __global__ __launch_bounds__(64 * kScanWaves, 2) void scan_back_kernel(PromptSca
     A2[i] = rate2(A[i]);
   }
   const float bias = channel_value(a.bias, c0, l), D = channel_value(a.D, c0, l);
-  const uint32_t doff = l.live ? (l.q * static_cast<uint32_t>(a.dim) + l.ch) * sizeof(T) : kOob,
-                 dstep = 4 * static_cast<uint32_t>(a.dim) * sizeof(T);
+  const uint32_t dstep = 4 * static_cast<uint32_t>(a.dim) * sizeof(T);
 
-  // the state before the chunk and the gradient of the one after it
-  f32x4 h = {0, 0, 0, 0}, grad = {0, 0, 0, 0};
+  // the gradient of the state after the chunk, and of several chunks the state before it
+  f32x4 init = {0, 0, 0, 0}, grad = {0, 0, 0, 0};
   const int64_t sbase = (static_cast<int64_t>(p.seq) * a.dim + c0) * a.n;
-  if (a.h0 != nullptr) {
-    const Rsrc r = make_rsrc(a.h0 + sbase, l.cw * a.n * 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = bload<float>(r, l.state[i]);
-  }
   if (a.dstate != nullptr) {
     const Rsrc r = make_rsrc(a.dstate + sbase, l.cw * a.n * 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) grad[i] = bload<float>(r, l.state[i]);
   }
   if (p.count > 1 && blk < blocks) {
+    if (a.h0 != nullptr) {
+      const Rsrc r = make_rsrc(a.h0 + sbase, l.cw * a.n * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) init[i] = bload<float>(r, l.state[i]);
+    }
     const int64_t first = (slot - p.c) * blocks + blk;
-    for (int j = 0; j < p.c; ++j) {
-      const int64_t at = first + static_cast<int64_t>(j) * blocks;
-      const f32x4 e = *reinterpret_cast<const f32x4 *>(a.ends + at * 256 + lane * 4);
-      const float t = a.steps[at * 16 + l.ch];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = __builtin_fmaf(hw_exp2(A2[i] * t), h[i], e[i]);
-    }
-    for (int j = p.count - 1; j > p.c; --j) {
-      const int64_t at = first + static_cast<int64_t>(j) * blocks;
-      const f32x4 e = *reinterpret_cast<const f32x4 *>(a.starts + at * 256 + lane * 4);
-      const float t = a.steps[at * 16 + l.ch];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) grad[i] = __builtin_fmaf(hw_exp2(A2[i] * t), grad[i], e[i]);
-    }
+    join_chunks(a.ends, a.steps, first, blocks, p.c, lane, A2, init);
+    join_chunks(a.starts, a.steps, first + static_cast<int64_t>(p.count - 1) * blocks, -blocks, p.count - 1 - p.c, lane, A2,
+                grad);
   }
 
-  // forward: the states at the tiles' starts
   const int tiles = (p.len + kBackTile - 1) / kBackTile;
-  float *mark = a.marks + ((p.t0 / kBackTile + slot) * padded + blk) * 256 + lane * 4;
-  const int64_t mstep = static_cast<int64_t>(padded) * 256;
-  for (int tile = 0; tile + 1 < tiles; ++tile) {
-    *reinterpret_cast<f32x4 *>(mark + tile * mstep) = h;
-    const int64_t t = p.t0 + tile * kBackTile;
-    const Rsrc ru = rows<T>(a.u, a.us, t, c0, kBackTile, l.cw), rd = rows<T>(a.delta, a.ds, t, c0, kBackTile, l.cw),
-               rb = rows<T>(a.B, a.bs, t, 0, kBackTile, a.n);
-    float u[kGroups], d[kGroups], b[kGroups];
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      u[g] = bload<T>(ru, l.u + g * static_cast<uint32_t>(4 * a.us * sizeof(T)));
-      d[g] = bload<T>(rd, l.d + g * static_cast<uint32_t>(4 * a.ds * sizeof(T)));
-      b[g] = bload<T>(rb, l.b + g * static_cast<uint32_t>(4 * a.bs * sizeof(T)));
-    }
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const float dt = step_of(a, d[g] + bias, true), du = dt * u[g];
-      float dts[4], dus[4];
-      f32x4 e;
-      hand_out(dt, dts);
-      hand_out(du, dus);
-      again<0>(A2, dts[0], b[g], dus[0], h, e);
-      again<1>(A2, dts[1], b[g], dus[1], h, e);
-      again<2>(A2, dts[2], b[g], dus[2], h, e);
-      again<3>(A2, dts[3], b[g], dus[3], h, e);
-    }
-  }
-
+  const int64_t mark = (p.t0 / kBackTile + p.id) * blocks + blk;
+  const int64_t tokens = a.q.L * (a.q.off != nullptr ? 1 : a.q.nseq);
   float dD = 0.0f, dbias = 0.0f;
+  Raw r;
+  f32x4 begin = {0, 0, 0, 0};
+  const auto fetch = [&](int tile) {
+    load_tile<T, true, GATE>(a, l, p.t0 + tile * kBackTile, p.len - tile * kBackTile, c0, r);
+    const int64_t at = mark + static_cast<int64_t>(tile) * blocks;
+    if (blk >= blocks) return;
+    begin = *reinterpret_cast<const f32x4 *>(a.marks + at * 256 + lane * 4);
+    if (p.count > 1) {
+      const float t = a.before[at * 16 + l.ch];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) begin[i] = __builtin_fmaf(hw_exp2(A2[i] * t), init[i], begin[i]);
+    }
+  };
   for (int tile = tiles - 1; tile >= 0; --tile) {
     const int64_t t = p.t0 + tile * kBackTile;
     const int m = p.len - tile * kBackTile < kBackTile ? p.len - tile * kBackTile : kBackTile;
-    const Rsrc ru = rows<T>(a.u, a.us, t, c0, m, l.cw), rd = rows<T>(a.delta, a.ds, t, c0, m, l.cw),
-               rb = rows<T>(a.B, a.bs, t, 0, m, a.n), rc = rows<T>(a.C, a.cs, t, 0, m, a.n),
-               ro = rows<T>(a.dout, a.dim, t, c0, m, l.cw), rz = rows<T>(a.z, a.zs, t, c0, GATE ? m : 0, l.cw);
-    float u[kGroups], d[kGroups], b[kGroups], c[kGroups], o[kGroups], z[kGroups];
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      u[g] = bload<T>(ru, l.u + g * static_cast<uint32_t>(4 * a.us * sizeof(T)));
-      d[g] = bload<T>(rd, l.d + g * static_cast<uint32_t>(4 * a.ds * sizeof(T)));
-      b[g] = bload<T>(rb, l.b + g * static_cast<uint32_t>(4 * a.bs * sizeof(T)));
-      c[g] = bload<T>(rc, l.c + g * static_cast<uint32_t>(4 * a.cs * sizeof(T)));
-      o[g] = bload<T>(ro, doff + g * dstep);
-      if (GATE) {
-        z[g] = bload<T>(rz, l.z + g * static_cast<uint32_t>(4 * a.zs * sizeof(T)));
-      }
-    }
-    if (tile + 1 < tiles) h = *reinterpret_cast<const f32x4 *>(mark + tile * mstep);
-    const f32x4 begin = h;
+    fetch(tile);
     f32x4 hs[kBackTile], es[kBackTile];
-    float dt[kGroups];
+    float slope[kGroups];
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      dt[g] = step_of(a, d[g] + bias, 4 * g + l.q < m);
-      const float du = dt[g] * u[g];
-      float dts[4], dus[4];
-      hand_out(dt[g], dts);
-      hand_out(du, dus);
-      again<0>(A2, dts[0], b[g], dus[0], h, es[4 * g]);
-      hs[4 * g] = h;
-      again<1>(A2, dts[1], b[g], dus[1], h, es[4 * g + 1]);
-      hs[4 * g + 1] = h;
-      again<2>(A2, dts[2], b[g], dus[2], h, es[4 * g + 2]);
-      hs[4 * g + 2] = h;
-      again<3>(A2, dts[3], b[g], dus[3], h, es[4 * g + 3]);
-      hs[4 * g + 3] = h;
+      const float dt = step_of(a, r.d[g] + bias, 4 * g + l.q < m);
+      float dy = r.o[g];
+      if (GATE) dy *= silu_both(r.z[g], slope[g]);
+      meet[g][l.ch][2 * l.q] = dt;
+      meet[g][l.ch][2 * l.q + 1] = dt * r.u[g];
+      meet[g][l.ch][8 + l.q] = dy;
+    }
+    wave_lds_fence();
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const auto &w = meet[g][l.ch];
+      again<0>(A2, w[0], r.b[g], w[1], g > 0 ? hs[g > 0 ? 4 * g - 1 : 0] : begin, hs[4 * g], es[4 * g]);
+      again<1>(A2, w[2], r.b[g], w[3], hs[4 * g], hs[4 * g + 1], es[4 * g + 1]);
+      again<2>(A2, w[4], r.b[g], w[5], hs[4 * g + 1], hs[4 * g + 2], es[4 * g + 2]);
+      again<3>(A2, w[6], r.b[g], w[7], hs[4 * g + 2], hs[4 * g + 3], es[4 * g + 3]);
     }
     float *mine = sums[tile & 1][wave];
     const Rsrc rdu = rows<T>(a.du, a.dim, t, c0, m, l.cw), rdd = rows<T>(a.ddelta, a.dim, t, c0, m, l.cw),
@@ -355,40 +408,36 @@ __global__ __launch_bounds__(64 * kScanWaves, 2) void scan_back_kernel(PromptSca
     for (int g = kGroups - 1; g >= 0; --g) {
       if (4 * g >= m) continue;
       const bool in = 4 * g + l.q < m;
-      const float du = dt[g] * u[g];
-      float slope = 0.0f, dy = o[g];
-      if (GATE) dy *= silu_both(z[g], slope);
-      float dts[4], dus[4], dys[4], x[4][4], yy[4][4], w[4], th[4], y[4];
-      hand_out(dt[g], dts);
-      hand_out(du, dus);
-      hand_out(dy, dys);
-      back_token<3, GATE>(A, dts[3], dus[3], dys[3], b[g], c[g], es[4 * g + 3], hs[4 * g + 3], hs[4 * g + 2],
-                          grad, dA, x[3], yy[3], w[3], th[3], y[3]);
-      back_token<2, GATE>(A, dts[2], dus[2], dys[2], b[g], c[g], es[4 * g + 2], hs[4 * g + 2], hs[4 * g + 1],
-                          grad, dA, x[2], yy[2], w[2], th[2], y[2]);
-      back_token<1, GATE>(A, dts[1], dus[1], dys[1], b[g], c[g], es[4 * g + 1], hs[4 * g + 1], hs[4 * g],
-                          grad, dA, x[1], yy[1], w[1], th[1], y[1]);
-      back_token<0, GATE>(A, dts[0], dus[0], dys[0], b[g], c[g], es[4 * g], hs[4 * g],
-                          g > 0 ? hs[g > 0 ? 4 * g - 1 : 0] : begin, grad, dA, x[0], yy[0], w[0], th[0], y[0]);
-      settle(w);
+      const auto &w = meet[g][l.ch];
+      float x[4][4], yy[4][4], along4[4], th[4], y[4];
+      back_token<3, GATE>(A, w[6], w[7], w[11], r.b[g], r.c[g], es[4 * g + 3], hs[4 * g + 3], hs[4 * g + 2], grad, dA, x[3],
+                          yy[3], along4[3], th[3], y[3]);
+      back_token<2, GATE>(A, w[4], w[5], w[10], r.b[g], r.c[g], es[4 * g + 2], hs[4 * g + 2], hs[4 * g + 1], grad, dA, x[2],
+                          yy[2], along4[2], th[2], y[2]);
+      back_token<1, GATE>(A, w[2], w[3], w[9], r.b[g], r.c[g], es[4 * g + 1], hs[4 * g + 1], hs[4 * g], grad, dA, x[1], yy[1],
+                          along4[1], th[1], y[1]);
+      back_token<0, GATE>(A, w[0], w[1], w[8], r.b[g], r.c[g], es[4 * g], hs[4 * g], g > 0 ? hs[g > 0 ? 4 * g - 1 : 0] : begin,
+                          grad, dA, x[0], yy[0], along4[0], th[0], y[0]);
+      settle(along4);
       if (GATE) settle(y);
-      const float along = gather(w), through = gather(th);
+      const float along = gather(along4), through = gather(th);
+      const float dt = meet[g][l.ch][2 * l.q], dy = meet[g][l.ch][8 + l.q];
       if (GATE) {
-        const float yt = __builtin_fmaf(D, u[g], gather(y));
-        put<T>(rdz, doff + g * dstep, o[g] * yt * slope);
+        const float yt = __builtin_fmaf(D, r.u[g], gather(y));
+        put<T>(rdz, l.dense + g * dstep, r.o[g] * yt * slope[g]);
       }
-      put<T>(rdu, doff + g * dstep, __builtin_fmaf(along, dt[g], D * dy));
-      float dd = __builtin_fmaf(along, u[g], through);
-      const float slope2 = hw_rcp(1.0f + hw_exp2((d[g] + bias) * -kLog2e));
+      put<T>(rdu, l.dense + g * dstep, __builtin_fmaf(along, dt, D * dy));
+      float dd = __builtin_fmaf(along, r.u[g], through);
+      const float slope2 = hw_rcp(1.0f + hw_exp2((r.d[g] + bias) * -kLog2e));
       dd *= a.softplus ? slope2 : 1.0f;
-      put<T>(rdd, doff + g * dstep, dd);
-      dD = __builtin_fmaf(dy, u[g], dD);
+      put<T>(rdd, l.dense + g * dstep, dd);
+      dD = __builtin_fmaf(dy, r.u[g], dD);
       dbias += in ? dd : 0.0f;
-      float r[2];
-      fold(x, yy, lane, r);
+      float s[2];
+      fold(x, yy, lane, s);
       typedef float f32x2 __attribute__((ext_vector_type(2)));
       const int at = (4 * g + ((lane >> 1) & 3)) * 32 + (lane & 8) * 2 + 4 * l.q + 2 * (lane & 1);
-      *reinterpret_cast<f32x2 *>(mine + at) = f32x2{r[0], r[1]};
+      *reinterpret_cast<f32x2 *>(mine + at) = f32x2{s[0], s[1]};
     }
     // (the other tile's sums may still be read by waves behind this barrier)
     __syncthreads();
@@ -397,9 +446,8 @@ __global__ __launch_bounds__(64 * kScanWaves, 2) void scan_back_kernel(PromptSca
 #pragma unroll
       for (int w = 0; w < kScanWaves; ++w) s += sums[tile & 1][w][i];
       const int tok = i / 32, which = (i / 16) % 2, n = i % 16;
-      if (tok < m && n < a.n) a.partBC[((group * a.q.L * (a.q.off != nullptr ? 1 : a.q.nseq) + t + tok) * 2 + which) * a.n + n] = s;
+      if (tok < m && n < a.n) a.partBC[((group * tokens + t + tok) * 2 + which) * a.n + n] = s;
     }
-    h = begin;
   }
 
   if (p.c == 0 && !none && a.dh0 != nullptr) {
@@ -429,7 +477,15 @@ __global__ __launch_bounds__(256) void scan_back_sum_kernel(PromptScanArgs a, in
   const int col = static_cast<int>(i - tok * 2 * a.n);
   if (a.q.off != nullptr && tok >= clamped(a.q.off[a.q.nseq], a.q.L)) return;
   float s = 0.0f;
-  for (int g = 0; g < wide; ++g) s += a.partBC[g * per + i];
+  int g = 0;
+  for (; g + 8 <= wide; g += 8) {            // (eight loads under way)
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = a.partBC[(g + k) * per + i];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += v[k];
+  }
+  for (; g < wide; ++g) s += a.partBC[g * per + i];
   T *out = static_cast<T *>(col < a.n ? a.dB : a.dC);
   out[tok * a.n + (col < a.n ? col : col - a.n)] = from_f32<T>(s);
 }
@@ -439,16 +495,44 @@ hipError_t launch_back(const PromptScanArgs &a, hipStream_t s) {
   const int wide = scan_wide(a.dim);
   const dim3 grid(static_cast<uint32_t>(a.q.slots * wide));
   const int64_t tokens = a.q.L * (a.q.off != nullptr ? 1 : a.q.nseq);
-  if (a.ends != nullptr) scan_local_kernel<T><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
-  if (a.z != nullptr)
+  if (a.z != nullptr) {
+    scan_marks_kernel<T, true><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
     scan_back_kernel<T, true><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
-  else
+  } else {
+    scan_marks_kernel<T, false><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
     scan_back_kernel<T, false><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
+  }
   scan_back_sum_kernel<T><<<static_cast<uint32_t>((tokens * 2 * a.n + 255) / 256), 256, 0, s>>>(a, wide, tokens);
   return hipGetLastError();
 }
 
 }  // namespace
+
+// Chunks of a backward pass.  In cycles a token: a workgroup of the second launch takes
+// some 680 alone on its compute unit and two take 810 together; the first launch some 120
+// a wave and SIMD, 200 where it gathers gradients besides (230 and more alone).
+int64_t scan_back_chunk(int64_t tokens, int64_t nseq, int64_t L, int dim, bool packed) {
+  const int64_t wide = scan_wide(dim);
+  if (packed) {                              // (the lengths are not known here)
+    const int64_t want = 512 / wide + 1, chunk = (tokens / want + kBackTile) / kBackTile * kBackTile;
+    return chunk < 64 ? (L < 64 ? L : 64) : chunk < L ? chunk : L;
+  }
+  int64_t best = L;
+  double least = 0;
+  for (int64_t parts = 1; parts <= 128; ++parts) {
+    const int64_t chunk = parts == 1 ? L : ((L + parts - 1) / parts + kBackTile - 1) / kBackTile * kBackTile;
+    if (chunk < 32 && parts > 1) break;
+    if (chunk >= L && parts > 1) continue;
+    const int64_t groups = wide * nseq * ((L + chunk - 1) / chunk), k = (groups + 255) / 256;
+    const double waves = groups * 4 / 1024.0, first = waves * (parts > 1 ? 200 : 120);
+    const double cost = chunk * ((k / 2) * 810.0 + (k % 2) * 680.0 + (first > 230 ? first : 230)) + parts * 300.0;
+    if (parts == 1 || cost < least) {
+      least = cost;
+      best = chunk;
+    }
+  }
+  return best;
+}
 
 hipError_t launch_prompt_scan_back(const PromptScanArgs &a, bool bf16, hipStream_t s) {
   return bf16 ? launch_back<bf16_t>(a, s) : launch_back<float>(a, s);
