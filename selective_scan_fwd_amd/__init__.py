@@ -955,7 +955,7 @@ def _row_tensor(t, name, dtype, shape, index):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.is_contiguous():
         return t.data_ptr(), 0
-    strides = t.stride()
+    strides, shape = t.stride(), tuple(shape)
     step, rows = 0, 1                            # of one row, and rows so far, from the last axis to the first
     good = strides[-1] == 1 or shape[-1] == 1
     for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
@@ -1180,7 +1180,8 @@ def _lead(t, name):
     """Rows and channels of a tensor [..., dim]."""
     if not isinstance(t, torch.Tensor) or t.dim() < 1:
         raise ValueError(f"{name} must be a [..., dim] tensor")
-    return t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1]
+    dim = t.shape[-1]
+    return t.numel() // dim if dim else 0, dim
 
 
 def _residual_type(t, x_dtype):
@@ -1196,18 +1197,17 @@ def vm_norm_before(x, w=None, b=None, residual=None, scale=None, factor=1.0, cen
     off).  r (of residual's dtype; may be residual itself) is None unless
     want_residual or a buffer is given."""
     rows, dim = _lead(x, "x")
-    index, dtype = x.get_device(), x.dtype
-    px, xs = _row_tensor(x, "x", dtype, tuple(x.shape), index)
+    index, dtype, shape = x.get_device(), x.dtype, x.shape
+    px, xs = _row_tensor(x, "x", dtype, shape, index)
     rtype = _residual_type(residual, _residual_type(r, dtype))
     if y is None:
-        y = torch.empty(x.shape, dtype=dtype, device=x.device)
+        y = torch.empty(shape, dtype=dtype, device=x.device)
     if r is None and want_residual:
-        r = torch.empty(x.shape, dtype=rtype, device=x.device)
-    vec = lambda t, name: _float_arg(t, name, (dim,), index)
-    p = VmBlockNorm(px, vec(w, "w"), vec(b, "b"), vec(scale, "scale"), None, xs, 0, 0, 0, eps, factor,
-                    VM_NORM_CENTER if center else 0)
-    _launch("vm_norm_before", index, p, _arg(residual, "residual", rtype, x.shape, index), _arg(y, "y", dtype, x.shape, index),
-            _arg(r, "r", rtype, x.shape, index), rows, dim, _dtype_code(x), _GRAD_CODES.get(rtype, -1))
+        r = torch.empty(shape, dtype=rtype, device=x.device)
+    p = VmBlockNorm(px, _float_arg(w, "w", (dim,), index), _float_arg(b, "b", (dim,), index),
+                    _float_arg(scale, "scale", (dim,), index), None, xs, 0, 0, 0, eps, factor, VM_NORM_CENTER if center else 0)
+    _launch("vm_norm_before", index, p, _arg(residual, "residual", rtype, shape, index), _arg(y, "y", dtype, shape, index),
+            _arg(r, "r", rtype, shape, index), rows, dim, _dtype_code(x), _GRAD_CODES.get(rtype, -1))
     return y, r
 
 
@@ -1223,7 +1223,7 @@ def vm_norm_before_bwd(dy, r, w=None, b=None, dr=None, x=None, scale=None, facto
     if scale is not None and x is None:
         raise ValueError("the gradient of scale needs x")
     rtype = r.dtype
-    px, xs = _row_tensor(x, "x", dtype, tuple(shape), index) if scale is not None else (None, 0)
+    px, xs = _row_tensor(x, "x", dtype, shape, index) if scale is not None else (None, 0)
     make = lambda kind, size: torch.empty(size, dtype=kind, device=dy.device)
     d = dict(residual=make(rtype, shape))
     same = scale is None and factor == 1.0 and rtype is dtype
@@ -1249,8 +1249,8 @@ def _norm_after(x, w, z, group, scale, factor, gate_first, eps):
     group = dim if group is None else int(group)
     if group < 1 or dim % group:
         raise ValueError(f"group {group} does not divide {dim} channels")
-    px, xs = _row_tensor(x, "x", dtype, tuple(x.shape), index)
-    pz, zs = _row_tensor(z, "z", dtype, tuple(x.shape), index) if z is not None else (None, 0)
+    px, xs = _row_tensor(x, "x", dtype, x.shape, index)
+    pz, zs = _row_tensor(z, "z", dtype, x.shape, index) if z is not None else (None, 0)
     gains = dim
     if w is not None:
         if not isinstance(w, torch.Tensor) or w.dim() != 1 or w.shape[0] not in (dim, group):

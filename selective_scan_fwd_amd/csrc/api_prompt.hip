@@ -86,8 +86,8 @@ int check_conv(const vm_sequences *q, bool pool, const void *x, int64_t x_stride
   a->silu = silu;
   return VM_OK;
 }
-// (a thread to each channel and chunk, where rows are not whole pieces)
-bool conv_fits(const vmk::SeqArgs &q, int64_t dim) { return q.slots <= (kMaxBlocks * 256) / dim; }
+// (a lane to each channel and chunk, where rows are not whole pieces, in whole waves)
+bool conv_fits(const vmk::SeqArgs &q, int64_t dim) { return q.slots <= (kMaxBlocks * 256) / (((dim + 63) / 64 + 3) * 64); }
 
 int64_t conv_partial(const vmk::PromptConvArgs &a) {
   return Parts::whole(static_cast<int64_t>(a.workers) * (a.width + 1) * a.dim * 4);

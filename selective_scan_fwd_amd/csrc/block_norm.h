@@ -69,7 +69,11 @@ __device__ __forceinline__ void store(T *p, int size, int lane, const float (&x)
         for (int j = 0; j < 8 / k; ++j) {
           Eight<T> v;
 #pragma unroll
-          for (int e = 0; e < k; ++e) v.v[e] = from_f32<T>(x[i][j * k + e]);
+          for (int e = 0; e < k; ++e)
+            if constexpr (sizeof(T) == 2)
+              v.v[e] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(x[i][j * k + e]));   // (to nearest even)
+            else
+              v.v[e] = x[i][j * k + e];
           *reinterpret_cast<Eight<T> *>(p + at + j * k) = v;
         }
       }
@@ -83,15 +87,30 @@ __device__ __forceinline__ void store(T *p, int size, int lane, const float (&x)
   }
 }
 
+template <int CTRL>
+__device__ __forceinline__ float moved(float x) {
+  return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
 // Sums of N values over the lanes of a group (LANES > 64: the workgroup, whose
 // waves meet in `meet`; every thread comes through here equally often).
 constexpr int kMeet = 16;
 template <int LANES, int N>
 __device__ __forceinline__ void sum_lanes(float (&s)[N], float (*meet)[N]) {
 #pragma unroll
-  for (int m = 1; m < (LANES < 64 ? LANES : 64); m *= 2)
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] += __shfl_xor(s[i], m, 64);
+  for (int i = 0; i < N; ++i) {
+    s[i] += moved<0xb1>(s[i]);                          // lane ^ 1
+    s[i] += moved<0x4e>(s[i]);                          // lane ^ 2
+    if (LANES > 4) {
+      s[i] += moved<0x141>(s[i]);                       // the other four of each eight
+      s[i] += moved<0x140>(s[i]);                       // the other eight of each row
+    }
+    if (LANES > 16) {
+      auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(s[i]), __float_as_uint(s[i]), false, false);
+      s[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+      r = __builtin_amdgcn_permlane32_swap(__float_as_uint(s[i]), __float_as_uint(s[i]), false, false);
+      s[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+  }
   if (LANES > 64) {
     __syncthreads();
     if (threadIdx.x % 64 == 0)

@@ -1,4 +1,4 @@
-// Sums over the rows of fp32 matrices, in a fixed order: the last step of the
+// Sums over the rows of fp32 matrices, in fp64 and a fixed order: the last step of the
 // gradients that every token or row adds to.  64 columns to a workgroup, four
 // threads to a column; several matrices to a launch.
 #include <hip/hip_runtime.h>
@@ -11,16 +11,16 @@ namespace {
 constexpr int kCols = 64, kRowsAt = 16;
 
 __global__ __launch_bounds__(kCols * kRowsAt) void column_sums_kernel(ColumnSums all) {
-  __shared__ float part[kRowsAt][kCols];
+  __shared__ double part[kRowsAt][kCols];
   int k = 0;
   while (k + 1 < all.n && static_cast<int>(blockIdx.x) >= all.first[k + 1]) ++k;
   const ColumnSum &m = all.s[k];
   const int col = (blockIdx.x - all.first[k]) * kCols + threadIdx.x % kCols, row = threadIdx.x / kCols;
-  float s = 0.0f;
+  double s = 0.0;
   if (col < m.fold)
     for (int c = col; c < m.cols; c += m.fold) {
       const float *in = m.in + c;
-      float t[4] = {0, 0, 0, 0};
+      double t[4] = {0, 0, 0, 0};
       int64_t r = row;
       for (; r + 3 * kRowsAt < m.rows; r += 4 * kRowsAt)
 #pragma unroll
@@ -31,10 +31,10 @@ __global__ __launch_bounds__(kCols * kRowsAt) void column_sums_kernel(ColumnSums
   part[row][threadIdx.x % kCols] = s;
   __syncthreads();
   if (row == 0 && col < m.fold) {
-    s = 0.0f;
+    s = 0.0;
 #pragma unroll
     for (int i = 0; i < kRowsAt; ++i) s += part[i][threadIdx.x];
-    m.out[col] = s;
+    m.out[col] = static_cast<float>(s);
   }
 }
 

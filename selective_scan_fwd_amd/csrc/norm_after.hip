@@ -57,12 +57,22 @@ __global__ __launch_bounds__(threads_of(LANES)) void after_back_kernel(BlockNorm
     dw[i][e] = ds[i][e] = 0.0f;
   }
   const float over = 1.0f / static_cast<float>(a.group);
+  float nx[P][8], nz[P][8], nd[P][8];       // the next row, under way
+  const auto fetch = [&](int64_t row) {
+    load<LANES, P, VEC>(static_cast<const T *>(a.x) + row * a.xs + col, a.group, u.lane, nx);
+    load<LANES, P, VEC>(static_cast<const R *>(a.dy) + row * a.dim + col, a.group, u.lane, nd);
+    if (a.z != nullptr) load<LANES, P, VEC>(static_cast<const T *>(a.z) + row * a.zs + col, a.group, u.lane, nz);
+  };
+  if (u.live && u.row < a.rows) fetch(u.row);
   for (int64_t row = u.row; row < a.rows && u.live; row += a.workers) {
     // v: what is normed; d: the gradient of n w
     float x[P][8], z[P][8], v[P][8], d[P][8];
-    load<LANES, P, VEC>(static_cast<const T *>(a.x) + row * a.xs + col, a.group, u.lane, x);
-    load<LANES, P, VEC>(static_cast<const R *>(a.dy) + row * a.dim + col, a.group, u.lane, d);
-    if (a.z != nullptr) load<LANES, P, VEC>(static_cast<const T *>(a.z) + row * a.zs + col, a.group, u.lane, z);
+    VM_EACH {
+      x[i][e] = nx[i][e];
+      z[i][e] = nz[i][e];
+      d[i][e] = nd[i][e];
+    }
+    if (row + a.workers < a.rows) fetch(row + a.workers);
     float s[2] = {0.0f, 0.0f};
     VM_EACH {
       const float gate = a.z != nullptr ? silu_f(z[i][e]) : 1.0f;

@@ -43,7 +43,11 @@ template <typename T, int V>
 __device__ __forceinline__ void store(void *base, int64_t at, const float (&y)[V]) {
   Vec<T, V> x;
 #pragma unroll
-  for (int e = 0; e < V; ++e) x.v[e] = from_f32<T>(y[e]);
+  for (int e = 0; e < V; ++e)
+    if constexpr (sizeof(T) == 2)
+      x.v[e] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(y[e]));   // (to nearest even)
+    else
+      x.v[e] = y[e];
   store_raw<T, V>(base, at, x);
 }
 
@@ -54,11 +58,14 @@ struct Taps {
 template <int W, int V>
 __device__ __forceinline__ Taps<W, V> load_taps(const float *w, const float *bias, int c) {
   Taps<W, V> t;
+  float all[W * V];                        // (one run of memory: the compiler widens the loads)
+#pragma unroll
+  for (int i = 0; i < W * V; ++i) all[i] = w[static_cast<int64_t>(c) * W + i];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     t.bias[e] = bias != nullptr ? bias[c + e] : 0.0f;
 #pragma unroll
-    for (int k = 0; k < W; ++k) t.w[k][e] = w[static_cast<int64_t>(c + e) * W + k];
+    for (int k = 0; k < W; ++k) t.w[k][e] = all[e * W + k];
   }
   return t;
 }
@@ -100,13 +107,11 @@ __device__ __forceinline__ void window_before(const void *in, int64_t xs, int c,
 }
 
 template <typename T, int W, int V>
-__global__ __launch_bounds__(kThreads) void prompt_conv_kernel(PromptConvArgs a) {
-  const int nv = a.dim / V;
-  const int64_t id = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x, slot = id / nv;
-  if (slot >= a.q.slots) return;
-  const int c = static_cast<int>(id - slot * nv) * V;
+__global__ __launch_bounds__(kThreads) void prompt_conv_kernel(PromptConvArgs a, uint32_t wide) {
+  const int64_t slot = blockIdx.x / wide;
+  const int c = static_cast<int>((blockIdx.x % wide) * blockDim.x + threadIdx.x) * V;
   const Piece p = piece_of(a.q, slot);
-  if (p.len < 0) return;
+  if (p.len < 0 || c >= a.dim) return;
   const int64_t kept = kept_at(a.q, p.seq), window = static_cast<int64_t>(W - 1) * a.dim;
   const T *old = a.h0 != nullptr && kept >= 0 && starts_kept(a.q, p.seq) ? static_cast<const T *>(a.h0) + kept * window : nullptr;
   const Taps<W, V> taps = load_taps<W, V>(a.w, a.bias, c);
@@ -152,17 +157,17 @@ __global__ __launch_bounds__(kThreads) void prompt_conv_kernel(PromptConvArgs a)
 
 // A worker walks every workers-th chunk and keeps its sums of dw and dbias.
 template <typename T, int W, int V>
-__global__ __launch_bounds__(kThreads) void prompt_conv_back_kernel(PromptConvArgs a) {
-  const int nv = a.dim / V;
-  const int64_t id = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x, worker = id / nv;
-  if (worker >= a.workers) return;
-  const int c = static_cast<int>(id - worker * nv) * V;
+__global__ __launch_bounds__(kThreads) void prompt_conv_back_kernel(PromptConvArgs a, uint32_t wide) {
+  const int64_t worker = blockIdx.x / wide;
+  const int at0 = static_cast<int>((blockIdx.x % wide) * blockDim.x + threadIdx.x) * V;
+  const bool live = at0 < a.dim;
+  const int c = live ? at0 : 0;               // (lanes past the channels stay for the search, and do no work)
   const Taps<W, V> taps = load_taps<W, V>(a.w, a.bias, c);
   const int64_t window = static_cast<int64_t>(W - 1) * a.dim;
   float dw[W][V] = {}, db[V] = {};
   for (int64_t slot = worker; slot < a.q.slots; slot += a.workers) {
     const Piece p = piece_of(a.q, slot);
-    if (p.len < 0) continue;
+    if (p.len < 0 || !live) continue;
     const T *old = a.h0 != nullptr ? static_cast<const T *>(a.h0) + p.seq * window : nullptr;
     const T *dlast = a.dstate != nullptr ? static_cast<const T *>(a.dstate) + p.seq * window : nullptr;
     float x[W][V], dv[W][V] = {};
@@ -171,50 +176,66 @@ __global__ __launch_bounds__(kThreads) void prompt_conv_back_kernel(PromptConvAr
     // dv of the chunk's tokens and of the W - 1 after them; a token's dx is whole when
     // the last of the outputs that read it has passed, and so is the window's gradient
     // (places before the sequence's first token) in its first chunk
-    for (int64_t t = p.t0; t < end + W - 1; ++t) {
-      push<W, V>(x);
-      push<W, V>(dv);
+    constexpr int kAhead = 4;
+    Vec<T, V> nx[kAhead], nd[kAhead];       // the next tokens, under way
+    const int64_t last = end + W - 1 < p.hi ? end + W - 1 : p.hi;
+    const auto fetch = [&](int64_t t, int i) {
+      if (t >= last) return;
+      nx[i] = load_raw<T, V>(a.x, t * a.xs + c);
+      nd[i] = load_raw<T, V>(a.dout, t * a.dim + c);
+    };
 #pragma unroll
-      for (int e = 0; e < V; ++e) dv[W - 1][e] = 0.0f;
-      if (t < p.hi) {
-        load<T, V>(a.x, t * a.xs + c, x[W - 1]);
-        load<T, V>(a.dout, t * a.dim + c, dv[W - 1]);
-        if (a.silu) {
-          float v[V];
-          convolve<W, V>(taps, x, v);
+    for (int i = 0; i < kAhead; ++i) fetch(p.t0 + i, i);
+    for (int64_t t0 = p.t0; t0 < end + W - 1; t0 += kAhead)
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float s = hw_rcp(1.0f + hw_exp2(-v[e] * kLog2e));
-            dv[W - 1][e] *= s * __builtin_fmaf(v[e], 1.0f - s, 1.0f);
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t t = t0 + i;
+        if (t >= end + W - 1) break;
+        push<W, V>(x);
+        push<W, V>(dv);
+#pragma unroll
+        for (int e = 0; e < V; ++e) dv[W - 1][e] = 0.0f;
+        if (t < last) {
+          widen<T, V>(nx[i], x[W - 1]);
+          widen<T, V>(nd[i], dv[W - 1]);
+          fetch(t + kAhead, i);
+          if (a.silu) {
+            float v[V];
+            convolve<W, V>(taps, x, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              const float s = hw_rcp(1.0f + hw_exp2(-v[e] * kLog2e));
+              dv[W - 1][e] *= s * __builtin_fmaf(v[e], 1.0f - s, 1.0f);
+            }
           }
+          if (t < end)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              db[e] += dv[W - 1][e];
+#pragma unroll
+              for (int k = 0; k < W; ++k) dw[k][e] = __builtin_fmaf(dv[W - 1][e], x[k][e], dw[k][e]);
+            }
         }
-        if (t < end)
+        const int64_t at = t - (W - 1);
+        if (at >= p.t0 ? at >= end : p.c > 0 || a.dh0 == nullptr) continue;
+        float d[V] = {};
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            db[e] += dv[W - 1][e];
+        for (int k = 0; k < W; ++k)
 #pragma unroll
-            for (int k = 0; k < W; ++k) dw[k][e] = __builtin_fmaf(dv[W - 1][e], x[k][e], dw[k][e]);
-          }
+          for (int e = 0; e < V; ++e) d[e] = __builtin_fmaf(taps.w[W - 1 - k][e], dv[k][e], d[e]);
+        if (dlast != nullptr && at >= p.hi - (W - 1)) {
+          float more[V];
+          load<T, V>(dlast, (at - p.hi + W - 1) * a.dim + c, more);
+#pragma unroll
+          for (int e = 0; e < V; ++e) d[e] += more[e];
+        }
+        if (at >= p.t0)
+          store<T, V>(a.dx, at * a.dim + c, d);
+        else
+          store<T, V>(static_cast<T *>(a.dh0) + p.seq * window, (at - p.lo + W - 1) * a.dim + c, d);
       }
-      const int64_t at = t - (W - 1);
-      if (at >= p.t0 ? at >= end : p.c > 0 || a.dh0 == nullptr) continue;
-      float d[V] = {};
-#pragma unroll
-      for (int k = 0; k < W; ++k)
-#pragma unroll
-        for (int e = 0; e < V; ++e) d[e] = __builtin_fmaf(taps.w[W - 1 - k][e], dv[k][e], d[e]);
-      if (dlast != nullptr && at >= p.hi - (W - 1)) {
-        float more[V];
-        load<T, V>(dlast, (at - p.hi + W - 1) * a.dim + c, more);
-#pragma unroll
-        for (int e = 0; e < V; ++e) d[e] += more[e];
-      }
-      if (at >= p.t0)
-        store<T, V>(a.dx, at * a.dim + c, d);
-      else
-        store<T, V>(static_cast<T *>(a.dh0) + p.seq * window, (at - p.lo + W - 1) * a.dim + c, d);
-    }
   }
+  if (!live) return;
   float *part = a.partial + worker * (W + 1) * a.dim + c;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
@@ -264,17 +285,27 @@ hipError_t by_width(int width, F &&f) {
 
 uint32_t blocks_of(int64_t threads) { return static_cast<uint32_t>((threads + kThreads - 1) / kThreads); }
 
+// Workgroups to a row of `lanes` lanes, and threads of each (whole waves).
+struct Cut {
+  uint32_t wide, threads;
+};
+Cut cut(int lanes) {
+  const int waves = (lanes + 63) / 64, wide = (waves + kThreads / 64 - 1) / (kThreads / 64);
+  return {static_cast<uint32_t>(wide), static_cast<uint32_t>((waves + wide - 1) / wide * 64)};
+}
+
 template <typename T, int V>
 hipError_t launch_fwd(const PromptConvArgs &a, hipStream_t s) {
+  const Cut z = cut(a.dim / V);
   return by_width<T, V>(a.width, [&](auto w) {
-    prompt_conv_kernel<T, decltype(w)::value, V><<<blocks_of(a.q.slots * (a.dim / V)), kThreads, 0, s>>>(a);
+    prompt_conv_kernel<T, decltype(w)::value, V><<<static_cast<uint32_t>(a.q.slots * z.wide), z.threads, 0, s>>>(a, z.wide);
   });
 }
 template <typename T, int V>
 hipError_t launch_bwd(const PromptConvArgs &a, hipStream_t s) {
+  const Cut z = cut(a.dim / V);
   return by_width<T, V>(a.width, [&](auto w) {
-    prompt_conv_back_kernel<T, decltype(w)::value, V>
-        <<<blocks_of(static_cast<int64_t>(a.workers) * (a.dim / V)), kThreads, 0, s>>>(a);
+    prompt_conv_back_kernel<T, decltype(w)::value, V><<<static_cast<uint32_t>(a.workers) * z.wide, z.threads, 0, s>>>(a, z.wide);
   });
 }
 template <typename T, int V>

@@ -28,7 +28,10 @@ __device__ __forceinline__ int64_t clamped(int32_t x, int64_t most) {
   return y < 0 ? 0 : y > most ? most : y;
 }
 
-// Offsets that do not rise from 0 to L give wrong chunks, but none outside [0, L).
+// The piece of a slot, the same for all lanes of a wave.  Packed: the last sequence whose
+// slots start at or before this one is looked for by 64 lanes at once (one load for up to
+// 64 sequences).  Offsets that do not rise from 0 to L give wrong chunks, but none
+// outside [0, L).
 __device__ __forceinline__ Piece piece_of(const SeqArgs &q, int64_t slot) {
   Piece p;
   if (q.off == nullptr) {
@@ -39,10 +42,15 @@ __device__ __forceinline__ Piece piece_of(const SeqArgs &q, int64_t slot) {
     p.lo = seq * q.L;
     p.hi = p.lo + q.L;
   } else {
-    int a = 0, b = q.nseq;                 // the last sequence whose slots start at or before this one
-    while (b - a > 1) {
-      const int m = (a + b) / 2;
-      if (clamped(q.off[m], q.L) / q.chunk + m <= slot) a = m; else b = m;
+    const int lane = threadIdx.x % 64;
+    int a = 0, n = q.nseq;                 // among sequences a .. a + n - 1
+    while (n > 1) {
+      const int step = (n + 63) / 64, at = a + lane * step;
+      const bool before = lane * step < n && clamped(q.off[at < q.nseq ? at : 0], q.L) / q.chunk + at <= slot;
+      const uint64_t m = __ballot(before);
+      const int k = m != 0 ? 63 - __builtin_clzll(m) : 0;
+      n = n - k * step < step ? n - k * step : step;
+      a += k * step;
     }
     p.seq = a;
     p.lo = clamped(q.off[a], q.L);

@@ -12,7 +12,8 @@ namespace vmk {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChannels = kThreads / 4;
+constexpr int kEach = 2;                 // channels to each four lanes
+constexpr int kChannels = kThreads / 4 * kEach;
 
 // Sum over each four neighbouring lanes.
 __device__ __forceinline__ float sum4(float x) {
@@ -34,49 +35,62 @@ __device__ __forceinline__ f32x4 load_states(const float *p, int first, int n) {
   return x;
 }
 
+// Two channels to each four lanes, every load under way before the first use: an idle
+// row reads the first state and stores none.
 template <typename T, bool VEC>
 __global__ __launch_bounds__(kThreads) void token_scan_kernel(TokenScanArgs a, int wide) {
-  const int row = blockIdx.x / wide, ch = (blockIdx.x % wide) * kChannels + threadIdx.x / 4, q = threadIdx.x % 4;
-  const bool live = ch < a.dim;
-  const int c = live ? ch : 0;                 // (lanes past the channels go along with the first)
+  const int row = blockIdx.x / wide, q = threadIdx.x % 4;
   const int64_t slot = a.where != nullptr ? a.where[row] : row;
-  float y = 0.0f;
-  if (slot >= 0 && slot < a.kept) {
-    float *state = a.state + (slot * a.dim + c) * a.n;
-    f32x4 h = load_states<VEC>(state, 4 * q, a.n);
-    const f32x4 A = load_states<VEC>(a.A + static_cast<int64_t>(c) * a.n, 4 * q, a.n);
-    const float u = to_f32(static_cast<const T *>(a.u)[row * a.us + c]);
-    float dt = to_f32(static_cast<const T *>(a.delta)[row * a.ds + c]) + (a.bias != nullptr ? a.bias[c] : 0.0f);
-    const float z = a.z != nullptr ? to_f32(static_cast<const T *>(a.z)[row * a.zs + c]) : 0.0f;
-    const float D = a.D != nullptr ? a.D[c] : 0.0f;
-    f32x4 B = {0, 0, 0, 0}, C = B;
+  const bool idle = slot < 0 || slot >= a.kept;
+  f32x4 B = {0, 0, 0, 0}, C = B, h[kEach], A[kEach];
+  float u[kEach], d[kEach], z[kEach], D[kEach];
+  float *state[kEach];
+  int c[kEach];
+  bool live[kEach];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (4 * q + i < a.n) {
-        B[i] = to_f32(static_cast<const T *>(a.B)[row * a.bs + 4 * q + i]);
-        C[i] = to_f32(static_cast<const T *>(a.C)[row * a.cs + 4 * q + i]);
-      }
-    if (a.softplus) dt = softplus_f(dt);
-    const float du = dt * u;
+  for (int k = 0; k < kEach; ++k) {
+    const int ch = (blockIdx.x % wide) * kChannels + k * (kThreads / 4) + threadIdx.x / 4;
+    live[k] = ch < a.dim;
+    c[k] = live[k] ? ch : 0;                   // (lanes past the channels go along with the first)
+    A[k] = load_states<VEC>(a.A + static_cast<int64_t>(c[k]) * a.n, 4 * q, a.n);
+    u[k] = to_f32(static_cast<const T *>(a.u)[row * a.us + c[k]]);
+    d[k] = to_f32(static_cast<const T *>(a.delta)[row * a.ds + c[k]]) + (a.bias != nullptr ? a.bias[c[k]] : 0.0f);
+    z[k] = a.z != nullptr ? to_f32(static_cast<const T *>(a.z)[row * a.zs + c[k]]) : 0.0f;
+    D[k] = a.D != nullptr ? a.D[c[k]] : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (4 * q + i < a.n) {
+      B[i] = to_f32(static_cast<const T *>(a.B)[row * a.bs + 4 * q + i]);
+      C[i] = to_f32(static_cast<const T *>(a.C)[row * a.cs + 4 * q + i]);
+    }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    state[k] = a.state + ((idle ? 0 : slot) * a.dim + c[k]) * a.n;
+    h[k] = load_states<VEC>(state[k], 4 * q, a.n);
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const float dt = a.softplus ? softplus_f(d[k]) : d[k], du = dt * u[k];
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      h[i] = __builtin_fmaf(hw_exp2(dt * rate2(A[i])), h[i], du * B[i]);
-      sum = __builtin_fmaf(C[i], h[i], sum);
+      h[k][i] = __builtin_fmaf(hw_exp2(dt * rate2(A[k][i])), h[k][i], du * B[i]);
+      sum = __builtin_fmaf(C[i], h[k][i], sum);
     }
-    if (live) {
+    if (live[k] && !idle) {
       if (VEC) {
-        if (4 * q < a.n) *reinterpret_cast<f32x4 *>(state + 4 * q) = h;
+        if (4 * q < a.n) *reinterpret_cast<f32x4 *>(state[k] + 4 * q) = h[k];
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (4 * q + i < a.n) state[4 * q + i] = h[i];
+          if (4 * q + i < a.n) state[k][4 * q + i] = h[k][i];
       }
     }
-    y = __builtin_fmaf(D, u, sum4(sum));
-    if (a.z != nullptr) y *= silu_f(z);
+    float y = __builtin_fmaf(D[k], u[k], sum4(sum));
+    if (a.z != nullptr) y *= silu_f(z[k]);
+    if (live[k] && q == 0) static_cast<T *>(a.out)[static_cast<int64_t>(row) * a.dim + c[k]] = from_f32<T>(idle ? 0.0f : y);
   }
-  if (live && q == 0) static_cast<T *>(a.out)[static_cast<int64_t>(row) * a.dim + c] = from_f32<T>(y);
 }
 
 }  // namespace
