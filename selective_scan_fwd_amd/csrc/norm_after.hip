@@ -65,37 +65,36 @@ __global__ __launch_bounds__(threads_of(LANES)) void after_back_kernel(BlockNorm
   };
   if (u.live && u.row < a.rows) fetch(u.row);
   for (int64_t row = u.row; row < a.rows && u.live; row += a.workers) {
-    // v: what is normed; d: the gradient of n w
-    float x[P][8], z[P][8], v[P][8], d[P][8];
+    // d: the gradient of n w; what is normed is x, or (gate first) x times the gate
+    float x[P][8], gate[P][8], slope[P][8], d[P][8];
     VM_EACH {
       x[i][e] = nx[i][e];
-      z[i][e] = nz[i][e];
       d[i][e] = nd[i][e];
+      slope[i][e] = 0.0f;
+      gate[i][e] = a.z != nullptr ? silu_both(nz[i][e], slope[i][e]) : 1.0f;
     }
     if (row + a.workers < a.rows) fetch(row + a.workers);
     float s[2] = {0.0f, 0.0f};
     VM_EACH {
-      const float gate = a.z != nullptr ? silu_f(z[i][e]) : 1.0f;
-      v[i][e] = a.gate_first ? x[i][e] * gate : x[i][e];
-      const float g = rounded(d[i][e] * scale[i][e] * (a.gate_first ? 1.0f : gate) * w[i][e]);
-      s[0] = __builtin_fmaf(v[i][e], v[i][e], s[0]);
-      s[1] = __builtin_fmaf(g, v[i][e], s[1]);
+      const float v = a.gate_first ? rounded(x[i][e] * gate[i][e]) : x[i][e];
+      const float g = rounded(d[i][e] * scale[i][e] * (a.gate_first ? 1.0f : gate[i][e]) * w[i][e]);
+      s[0] = __builtin_fmaf(v, v, s[0]);
+      s[1] = __builtin_fmaf(g, v, s[1]);
     }
     sum_lanes<LANES, 2>(s, meet);
     const float size = inverse_root(s[0] * over + a.eps);
     VM_EACH {
-      float slope = 0.0f;
-      const float gate = a.z != nullptr ? silu_both(z[i][e], slope) : 1.0f;
-      const float n = v[i][e] * size, after = a.gate_first ? 1.0f : gate;
+      const float v = a.gate_first ? rounded(x[i][e] * gate[i][e]) : x[i][e];
+      const float n = v * size, after = a.gate_first ? 1.0f : gate[i][e];
       if (a.want_scale) ds[i][e] = __builtin_fmaf(d[i][e] * a.factor, n * w[i][e] * after, ds[i][e]);
       const float dout = d[i][e] * scale[i][e], dn = dout * after;
       dw[i][e] = __builtin_fmaf(dn, n, dw[i][e]);
-      const float dv = norm_back(rounded(dn * w[i][e]), v[i][e], size, s[0], s[1], over, a.eps);
-      d[i][e] = a.gate_first ? dv * gate : dv;
-      z[i][e] = (a.gate_first ? dv * x[i][e] : dout * n * w[i][e]) * slope;
+      const float dv = norm_back(rounded(dn * w[i][e]), v, size, s[0], s[1], over, a.eps);
+      d[i][e] = a.gate_first ? dv * gate[i][e] : dv;
+      slope[i][e] *= a.gate_first ? dv * x[i][e] : dout * n * w[i][e];
     }
     store<LANES, P, VEC>(static_cast<T *>(a.dx) + row * a.dim + col, a.group, u.lane, d);
-    if (a.dz != nullptr) store<LANES, P, VEC>(static_cast<T *>(a.dz) + row * a.dim + col, a.group, u.lane, z);
+    if (a.dz != nullptr) store<LANES, P, VEC>(static_cast<T *>(a.dz) + row * a.dim + col, a.group, u.lane, slope);
   }
   int which = 0;
   if (a.want_w) keep_sums<LANES, P, VEC>(a, u, which++, dw);

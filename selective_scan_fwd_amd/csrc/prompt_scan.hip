@@ -130,6 +130,15 @@ __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScan
   const int blocks = (a.dim + 15) / 16, waves = blockDim.x / 64;
   const int wide = (blocks + waves - 1) / waves;
   int64_t slot = blockIdx.x / wide;
+  if (a.q.off != nullptr) {
+    // by falling length: every other round of workgroups over the 256 compute units backwards, so
+    // that the longest sequence of one round shares its units with the shortest of the next
+    const int64_t each = 256 / wide, round = each > 1 ? slot / each : 0;
+    if ((round & 1) != 0) {
+      const int64_t end = (round + 1) * each < a.q.slots ? (round + 1) * each : a.q.slots;
+      slot = end - 1 - (slot - round * each);
+    }
+  }
   if (a.q.off == nullptr && a.ends != nullptr) {   // all chunks of a sequence but its last or first
     const int64_t per = (a.q.L + a.q.chunk - 1) / a.q.chunk, seq = slot / (per - 1);
     slot += seq + (SECOND ? 1 : 0);
