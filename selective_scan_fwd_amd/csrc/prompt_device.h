@@ -118,24 +118,6 @@ __device__ __forceinline__ bool starts_kept(const SeqArgs &q, int seq) {
 // 15, and no vector instruction goes on meanwhile; four multiplications take 11 to 17.)
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// y = sum_i c[4 S + i] h[i], to be settled (see there; s_nop: c may have been written
-// by the instruction before).
-template <int S> __device__ __forceinline__ float read_out(float c, const f32x4 &h);
-#define VM_READ_OUT(S, A, B, C, D)                                                    \
-  template <>                                                                         \
-  __device__ __forceinline__ float read_out<S>(float c, const f32x4 &h) {             \
-    float y;                                                                          \
-    asm("s_nop 1\n"                                                                   \
-        "v_mul_f32_dpp %0, %1, %2 row_newbcast:" #A " row_mask:0xf bank_mask:0xf\n"   \
-        "v_fmac_f32_dpp %0, %1, %3 row_newbcast:" #B " row_mask:0xf bank_mask:0xf\n"  \
-        "v_fmac_f32_dpp %0, %1, %4 row_newbcast:" #C " row_mask:0xf bank_mask:0xf\n"  \
-        "v_fmac_f32_dpp %0, %1, %5 row_newbcast:" #D " row_mask:0xf bank_mask:0xf\n"  \
-        : "=&v"(y)                                                                    \
-        : "v"(c), "v"(h[0]), "v"(h[1]), "v"(h[2]), "v"(h[3]));                        \
-    return y;                                                                         \
-  }
-VM_READ_OUT(0, 0, 1, 2, 3) VM_READ_OUT(1, 4, 5, 6, 7) VM_READ_OUT(2, 8, 9, 10, 11) VM_READ_OUT(3, 12, 13, 14, 15)
-#undef VM_READ_OUT
 // Two states after everything before: what assembly text wrote may be read through DPP
 // or a lane swap (whose waits the compiler counts for its own instructions only).
 __device__ __forceinline__ void settle(float (&y)[4]) {
@@ -216,16 +198,7 @@ __device__ __forceinline__ void swap16(float &a, float &b) {
   a = __uint_as_float(r[0]);
   b = __uint_as_float(r[1]);
 }
-// Every lane gets its channel's values of the group's four tokens.
-__device__ __forceinline__ void hand_out(float x, float (&y)[4]) {
-  float a = x, b = x;
-  swap32(a, b);                       // rows 0 1 0 1 and 2 3 2 3
-  y[0] = y[1] = a;
-  swap16(y[0], y[1]);
-  y[2] = y[3] = b;
-  swap16(y[2], y[3]);
-}
-// The other way: four values of each lane, summed over a channel's four lanes; lane
+// Four values of each lane, summed over a channel's four lanes; lane
 // (channel, q) gets that of token q.
 __device__ __forceinline__ float gather(const float (&y)[4]) {
   float a = y[0], c = y[2], b = y[1], d = y[3];

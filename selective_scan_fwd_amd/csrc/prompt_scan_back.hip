@@ -470,24 +470,24 @@ __global__ __launch_bounds__(64 * kScanWaves, 2) void scan_back_kernel(PromptSca
 // dB and dC: the sums over the workgroups' blocks.
 template <typename T>
 __global__ __launch_bounds__(256) void scan_back_sum_kernel(PromptScanArgs a, int wide, int64_t tokens) {
-  const int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x;
   const int64_t per = tokens * 2 * a.n;
-  if (i >= per) return;
-  const int64_t tok = i / (2 * a.n);
-  const int col = static_cast<int>(i - tok * 2 * a.n);
-  if (a.q.off != nullptr && tok >= clamped(a.q.off[a.q.nseq], a.q.L)) return;
-  float s = 0.0f;
-  int g = 0;
-  for (; g + 8 <= wide; g += 8) {            // (eight loads under way)
-    float v[8];
+  const int64_t end = a.q.off != nullptr ? clamped(a.q.off[a.q.nseq], a.q.L) * 2 * a.n : per;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x; i < end; i += gridDim.x * static_cast<int64_t>(256)) {
+    float s = 0.0f;
+    int g = 0;
+    for (; g + 8 <= wide; g += 8) {          // (eight loads under way)
+      float v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = a.partBC[(g + k) * per + i];
+      for (int k = 0; k < 8; ++k) v[k] = a.partBC[(g + k) * per + i];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += v[k];
+      for (int k = 0; k < 8; ++k) s += v[k];
+    }
+    for (; g < wide; ++g) s += a.partBC[g * per + i];
+    const int64_t tok = i / (2 * a.n);
+    const int col = static_cast<int>(i - tok * 2 * a.n);
+    T *out = static_cast<T *>(col < a.n ? a.dB : a.dC);
+    out[tok * a.n + (col < a.n ? col : col - a.n)] = from_f32<T>(s);
   }
-  for (; g < wide; ++g) s += a.partBC[g * per + i];
-  T *out = static_cast<T *>(col < a.n ? a.dB : a.dC);
-  out[tok * a.n + (col < a.n ? col : col - a.n)] = from_f32<T>(s);
 }
 
 template <typename T>
@@ -502,7 +502,8 @@ hipError_t launch_back(const PromptScanArgs &a, hipStream_t s) {
     scan_marks_kernel<T, false><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
     scan_back_kernel<T, false><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
   }
-  scan_back_sum_kernel<T><<<static_cast<uint32_t>((tokens * 2 * a.n + 255) / 256), 256, 0, s>>>(a, wide, tokens);
+  const int64_t sums = (tokens * 2 * a.n + 255) / 256, most = 1 << 16;
+  scan_back_sum_kernel<T><<<static_cast<uint32_t>(sums < most ? sums : most), 256, 0, s>>>(a, wide, tokens);
   return hipGetLastError();
 }
 
