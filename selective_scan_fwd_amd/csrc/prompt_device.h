@@ -28,6 +28,30 @@ __device__ __forceinline__ int64_t clamped(int32_t x, int64_t most) {
   return y < 0 ? 0 : y > most ? most : y;
 }
 
+// Of packed sequence i: its first token over the tokens of a chunk.
+__device__ __forceinline__ int slots_before(const SeqArgs &q, int i) {
+  return static_cast<int>(static_cast<uint32_t>(clamped(q.off[i], q.L)) / static_cast<uint32_t>(q.chunk));
+}
+
+// The same in scalar registers (all lanes hold the same): addresses that the compiler
+// takes for the lanes' own cost a loop over them at every load.
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x)),
+                 hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ Piece uniform(Piece p) {
+  p.seq = uniform(p.seq);
+  p.c = uniform(p.c);
+  p.count = uniform(p.count);
+  p.lo = uniform64(p.lo);
+  p.hi = uniform64(p.hi);
+  p.t0 = uniform64(p.t0);
+  p.len = uniform(p.len);
+  p.id = uniform64(p.id);
+  return p;
+}
+
 // The piece of a slot, the same for all lanes of a wave.  Packed: the last sequence whose
 // slots start at or before this one is looked for by 64 lanes at once (one load for up to
 // 64 sequences).  Offsets that do not rise from 0 to L give wrong chunks, but none
@@ -35,10 +59,11 @@ __device__ __forceinline__ int64_t clamped(int32_t x, int64_t most) {
 __device__ __forceinline__ Piece piece_of(const SeqArgs &q, int64_t slot) {
   Piece p;
   if (q.off == nullptr) {
-    const int64_t per = (q.L + q.chunk - 1) / q.chunk;
-    const int64_t seq = slot / per;
+    // (all below 2^31: a 64-bit division takes 150 instructions)
+    const uint32_t per = (static_cast<uint32_t>(q.L) + static_cast<uint32_t>(q.chunk) - 1) / static_cast<uint32_t>(q.chunk);
+    const uint32_t seq = static_cast<uint32_t>(slot) / per;
     p.seq = static_cast<int>(seq);
-    p.c = static_cast<int>(slot - seq * per);
+    p.c = static_cast<int>(static_cast<uint32_t>(slot) - seq * per);
     p.lo = seq * q.L;
     p.hi = p.lo + q.L;
   } else {
@@ -46,7 +71,7 @@ __device__ __forceinline__ Piece piece_of(const SeqArgs &q, int64_t slot) {
     int a = 0, n = q.nseq;                 // among sequences a .. a + n - 1
     while (n > 1) {
       const int step = (n + 63) / 64, at = a + lane * step;
-      const bool before = lane * step < n && clamped(q.off[at < q.nseq ? at : 0], q.L) / q.chunk + at <= slot;
+      const bool before = lane * step < n && slots_before(q, at < q.nseq ? at : 0) + at <= slot;
       const uint64_t m = __ballot(before);
       const int k = m != 0 ? 63 - __builtin_clzll(m) : 0;
       n = n - k * step < step ? n - k * step : step;
@@ -55,16 +80,17 @@ __device__ __forceinline__ Piece piece_of(const SeqArgs &q, int64_t slot) {
     p.seq = a;
     p.lo = clamped(q.off[a], q.L);
     p.hi = clamped(q.off[a + 1], q.L);
-    p.c = static_cast<int>(slot - p.lo / q.chunk - a);
+    p.c = static_cast<int>(slot - slots_before(q, a) - a);
   }
   p.id = slot;
   const int64_t all = p.hi - p.lo;
-  p.count = all > q.chunk ? static_cast<int>((all + q.chunk - 1) / q.chunk) : 1;
+  p.count = all > q.chunk ? static_cast<int>((static_cast<uint32_t>(all) + static_cast<uint32_t>(q.chunk) - 1) /
+                                             static_cast<uint32_t>(q.chunk)) : 1;
   p.t0 = p.lo + p.c * q.chunk;
   const int64_t left = p.hi - p.t0;
   p.len = static_cast<int>(left < q.chunk ? left : q.chunk);
   if (p.c < 0 || p.c >= p.count || p.len < 0) p.len = p.c == 0 && all <= 0 ? 0 : -1;
-  return p;
+  return uniform(p);
 }
 
 // The same for a whole wave with up to 64 packed sequences, whose slots then go by
@@ -90,11 +116,11 @@ __device__ __forceinline__ Piece piece_by_length(const SeqArgs &q, int64_t slot)
   p.hi = p.lo + (all > 0 ? all : 0);
   p.count = __builtin_amdgcn_readlane(count, p.seq);
   p.c = static_cast<int>(slot) - __builtin_amdgcn_readlane(start, p.seq);
-  p.id = p.lo / chunk + p.seq + p.c;
+  p.id = static_cast<uint32_t>(p.lo) / static_cast<uint32_t>(chunk) + p.seq + p.c;
   p.t0 = p.lo + static_cast<int64_t>(p.c) * chunk;
   const int64_t left = p.hi - p.t0;
   p.len = mine == 0 ? -1 : static_cast<int>(left < chunk ? left : chunk);
-  return p;
+  return uniform(p);
 }
 
 // Where a sequence's state is kept, -1: nowhere.

@@ -133,14 +133,15 @@ __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScan
   if (a.q.off != nullptr) {
     // by falling length: every other round of workgroups over the 256 compute units backwards, so
     // that the longest sequence of one round shares its units with the shortest of the next
-    const int64_t each = 256 / wide, round = each > 1 ? slot / each : 0;
+    const int each = 256 / wide, round = each > 1 ? static_cast<int>(slot) / each : 0;
     if ((round & 1) != 0) {
-      const int64_t end = (round + 1) * each < a.q.slots ? (round + 1) * each : a.q.slots;
-      slot = end - 1 - (slot - round * each);
+      const int64_t next = (round + int64_t{1}) * each, end = next < a.q.slots ? next : a.q.slots;
+      slot = end - 1 - (slot - static_cast<int64_t>(round) * each);
     }
   }
   if (a.q.off == nullptr && a.ends != nullptr) {   // all chunks of a sequence but its last or first
-    const int64_t per = (a.q.L + a.q.chunk - 1) / a.q.chunk, seq = slot / (per - 1);
+    const uint32_t per = (static_cast<uint32_t>(a.q.L) + static_cast<uint32_t>(a.q.chunk) - 1) / static_cast<uint32_t>(a.q.chunk),
+                   seq = static_cast<uint32_t>(slot) / (per - 1);
     slot += seq + (SECOND ? 1 : 0);
   }
   const int blk = uniform(static_cast<int>(blockIdx.x % wide) * waves + threadIdx.x / 64);
@@ -148,13 +149,13 @@ __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScan
   const Piece p = piece_by_length(a.q, slot);
   if (p.len < 0 || (SECOND ? p.c == 0 : p.c > 0 && p.c == p.count - 1)) return;
   // a long chunk goes on at its own pace beside short ones
-  const int64_t part = p.len * int64_t{4} / (a.q.chunk < a.q.L ? a.q.chunk : a.q.L);
   if (a.q.off != nullptr) {
-    if (part >= 3)
+    const int64_t whole = a.q.chunk < a.q.L ? a.q.chunk : a.q.L, four = int64_t{4} * p.len;
+    if (four >= 3 * whole)
       __builtin_amdgcn_s_setprio(3);
-    else if (part == 2)
+    else if (four >= 2 * whole)
       __builtin_amdgcn_s_setprio(2);
-    else if (part == 1)
+    else if (four >= whole)
       __builtin_amdgcn_s_setprio(1);
   }
   const int c0 = blk * 16;

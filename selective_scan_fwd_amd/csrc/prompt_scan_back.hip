@@ -113,7 +113,9 @@ __device__ __forceinline__ void mark_chunk(const PromptScanArgs &a, const Lane &
   float steps = 0.0f;
   Raw next;
   load_tile<T, MANY, GATE>(a, l, p.t0, p.len, c0, next);
-  for (int at = 0; at < p.len; at += kBackTile) {
+  // (nobody asks for the state after a sequence's last tile)
+  const int end = MANY ? p.len : p.len - kBackTile;
+  for (int at = 0; at < end; at += kBackTile) {
     const Raw r = next;
     const int m = p.len - at;
     load_tile<T, MANY, GATE>(a, l, p.t0 + at + kBackTile, m - kBackTile, c0, next);
@@ -122,8 +124,6 @@ __device__ __forceinline__ void mark_chunk(const PromptScanArgs &a, const Lane &
     if (MANY) {
       if (l.q == 0) *before = steps;
       before += blocks * 16;
-    } else if (m <= kBackTile) {
-      break;                               // (nobody asks for the state after the last tile)
     }
     float mine = 0.0f;
 #pragma unroll
@@ -159,6 +159,7 @@ __device__ __forceinline__ void mark_chunk(const PromptScanArgs &a, const Lane &
       steps += gather(s);
     }
   }
+  if (!MANY) *reinterpret_cast<f32x4 *>(mark) = h;
   if (MANY) {
     const int64_t block = slot * blocks + blk;
     *reinterpret_cast<f32x4 *>(a.ends + block * 256 + lane * 4) = h;
