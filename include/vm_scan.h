@@ -786,7 +786,7 @@ int vm_prompt_scan(const vm_scan_rows *p, const vm_sequences *q,
 
 /*
  * Workspace of vm_prompt_scan (backward = 0) or vm_prompt_scan_bwd (backward = 1),
- * with packed = 1 for sequences given by offsets.  The backward pass takes about 4
+ * with packed = 1 for sequences given by offsets.  The backward pass takes about 8
  * bytes per token and channel.  Pure host function.
  */
 int64_t vm_prompt_scan_workspace(int64_t batch, int64_t seqlen, int64_t n,

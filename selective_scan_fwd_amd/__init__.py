@@ -137,6 +137,8 @@ _lib = None
 def load_library():
     """Load libvmscan.so and declare the C signatures.  Raises if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -956,6 +958,10 @@ def _row_tensor(t, name, dtype, shape, index):
     if t.is_contiguous():
         return t.data_ptr(), 0
     strides, shape = t.stride(), tuple(shape)
+    if len(shape) == 2 and strides[1] == 1 and strides[0] >= shape[1]:
+        return t.data_ptr(), strides[0]
+    if len(shape) == 3 and strides[2] == 1 and strides[1] >= shape[2] and strides[0] == shape[1] * strides[1]:
+        return t.data_ptr(), strides[1]
     step, rows = 0, 1                            # of one row, and rows so far, from the last axis to the first
     good = strides[-1] == 1 or shape[-1] == 1
     for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):

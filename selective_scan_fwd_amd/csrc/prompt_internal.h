@@ -106,7 +106,7 @@ struct PromptScanArgs {
 // Blocks of 16 channels, and as many as whole workgroups hold.
 inline int scan_blocks(int dim) { return (dim + 15) / 16; }
 inline int scan_wide(int dim) { return (scan_blocks(dim) + 3) / 4; }
-constexpr int kBackTile = 16;     // tokens of a tile of the backward pass
+constexpr int kBackTile = 8;     // tokens of a tile of the backward pass
 constexpr int kScanWaves = 4;     // blocks of 16 channels to a workgroup
 int64_t scan_chunk(int64_t tokens, int64_t nseq, int64_t L, int dim, bool packed);
 int64_t scan_back_chunk(int64_t tokens, int64_t nseq, int64_t L, int dim, bool packed);

@@ -6,7 +6,7 @@
 //   dA = sum_t dt p_t h_{t-1};  dD = sum_t u dy;  dz = dout y SiLU'(z)
 //
 // The lane layout is the forward pass's (prompt_device.h).  A first launch walks every
-// chunk forward and leaves the states at the starts of its tiles of 16 tokens in memory.
+// chunk forward and leaves the states at the starts of its tiles of 8 tokens in memory.
 // The second walks back over the tiles, a workgroup over one chunk of four blocks of 16
 // channels: a tile's states and decays are formed again and held in registers.  Where
 // sequences have several chunks, the first launch starts each of them from a zero state
@@ -313,7 +313,7 @@ __device__ __forceinline__ void back_token(const float (&A)[4], float dts, float
 }
 
 template <typename T, bool GATE>
-__global__ __launch_bounds__(64 * kScanWaves, 2) void scan_back_kernel(PromptScanArgs a, int wide) {
+__global__ __launch_bounds__(64 * kScanWaves, 3) void scan_back_kernel(PromptScanArgs a, int wide) {
   __shared__ __align__(16) float sums[2][kScanWaves][kBackTile * 32];
   __shared__ __align__(16) float meets[kScanWaves][kGroups][16][12];
   const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), blocks = (a.dim + 15) / 16;
@@ -511,7 +511,7 @@ hipError_t launch_back(const PromptScanArgs &a, hipStream_t s) {
 }  // namespace
 
 // Chunks of a backward pass.  In cycles a token: a workgroup of the second launch takes
-// some 680 alone on its compute unit and two take 810 together; the first launch some 120
+// some 680 alone on its compute unit, two 900 and k more 415 k; the first launch some 120
 // a wave and SIMD, 200 where it gathers gradients besides (230 and more alone).
 int64_t scan_back_chunk(int64_t tokens, int64_t nseq, int64_t L, int dim, bool packed) {
   const int64_t wide = scan_wide(dim);
@@ -527,7 +527,7 @@ int64_t scan_back_chunk(int64_t tokens, int64_t nseq, int64_t L, int dim, bool p
     if (chunk >= L && parts > 1) continue;
     const int64_t groups = wide * nseq * ((L + chunk - 1) / chunk), k = (groups + 255) / 256;
     const double waves = groups * 4 / 1024.0, first = waves * (parts > 1 ? 200 : 120);
-    const double cost = chunk * ((k / 2) * 810.0 + (k % 2) * 680.0 + (first > 230 ? first : 230)) + parts * 300.0;
+    const double cost = chunk * ((k > 2 ? k * 415.0 : k > 1 ? 900.0 : 680.0) + (first > 230 ? first : 230)) + parts * 300.0;
     if (parts == 1 || cost < least) {
       least = cost;
       best = chunk;
