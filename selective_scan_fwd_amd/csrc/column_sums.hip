@@ -1,6 +1,7 @@
 // Sums over the rows of fp32 matrices, in fp64 and a fixed order: the last step of the
-// gradients that every token or row adds to.  64 columns to a workgroup, four
-// threads to a column; several matrices to a launch.
+// gradients that every token or row adds to.  16 columns to a workgroup and 64 threads
+// to a column, so that few columns of many rows fill the card too; several matrices to
+// a launch.
 #include <hip/hip_runtime.h>
 
 #include "prompt_internal.h"
@@ -8,7 +9,7 @@
 namespace vmk {
 namespace {
 
-constexpr int kCols = 64, kRowsAt = 16;
+constexpr int kCols = 16, kRowsAt = 64;
 
 __global__ __launch_bounds__(kCols * kRowsAt) void column_sums_kernel(ColumnSums all) {
   __shared__ double part[kRowsAt][kCols];
@@ -30,10 +31,18 @@ __global__ __launch_bounds__(kCols * kRowsAt) void column_sums_kernel(ColumnSums
     }
   part[row][threadIdx.x % kCols] = s;
   __syncthreads();
+  if (row < 8) {
+    s = 0.0;
+#pragma unroll
+    for (int i = 0; i < kRowsAt; i += 8) s += part[row + i][threadIdx.x % kCols];
+  }
+  __syncthreads();
+  if (row < 8) part[row][threadIdx.x % kCols] = s;
+  __syncthreads();
   if (row == 0 && col < m.fold) {
     s = 0.0;
 #pragma unroll
-    for (int i = 0; i < kRowsAt; ++i) s += part[i][threadIdx.x];
+    for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
     m.out[col] = static_cast<float>(s);
   }
 }
