@@ -210,7 +210,7 @@ int vm_prompt_conv(const vm_sequences *q, const void *x, int64_t x_stride, const
   if (out == nullptr) return VM_ERR_NULL;
   const bool bf16 = dtype == VM_BF16;
   const int es = size_of(dtype);
-  divide(a.q, vmk::conv_chunk(all_tokens(a.q), a.dim, bf16, false));
+  divide(a.q, vmk::kConvChunk);
   if (!conv_fits(a.q, dim)) return VM_ERR_UNSUPPORTED;
   const SeqSpans sq(a.q);
   const Span ins[] = {span(x, ext * es), span(w, dim * width * 4), span(bias, dim * 4),
@@ -239,7 +239,7 @@ int64_t vm_prompt_conv_workspace(int64_t batch, int64_t seqlen, int64_t n, int64
   a.width = static_cast<int>(width);
   a.xs = dim;
   const bool bf16 = dtype == VM_BF16;
-  divide(a.q, vmk::conv_chunk(all_tokens(a.q), a.dim, bf16, true));
+  divide(a.q, vmk::kConvBackChunk);
   if (!conv_fits(a.q, dim)) return -VM_ERR_UNSUPPORTED;
   a.workers = vmk::conv_workers(a, bf16);      // (rows of whole pieces have the most)
   return conv_partial(a);
@@ -255,7 +255,7 @@ int vm_prompt_conv_bwd(const vm_sequences *q, const void *x, int64_t x_stride, c
   if (dout == nullptr || g == nullptr || g->dx == nullptr || g->dw == nullptr) return VM_ERR_NULL;
   const bool bf16 = dtype == VM_BF16;
   const int es = size_of(dtype);
-  divide(a.q, vmk::conv_chunk(all_tokens(a.q), a.dim, bf16, true));
+  divide(a.q, vmk::kConvBackChunk);
   if (!conv_fits(a.q, dim)) return VM_ERR_UNSUPPORTED;
   const SeqSpans sq(a.q);
   const int64_t out = batch * seqlen * dim * es;

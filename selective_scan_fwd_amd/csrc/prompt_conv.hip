@@ -329,13 +329,10 @@ bool whole(const PromptConvArgs &a, int es) {
 
 }  // namespace
 
-int64_t conv_chunk(int64_t tokens, int dim, bool bf16, bool back) {
-  (void)tokens, (void)dim, (void)bf16, (void)back;
-  return 32;
-}
 int conv_workers(const PromptConvArgs &a, bool bf16) {
+  // (a worker is at least a wave)
   const int es = bf16 ? 2 : 4, nv = whole(a, es) ? a.dim * es / 16 : a.dim;
-  const int64_t most = (int64_t{1} << 18) / nv + 1;
+  const int64_t most = (int64_t{1} << 18) / (nv > 64 ? nv : 64) + 1;
   return static_cast<int>(a.q.slots < most ? a.q.slots : most);
 }
 

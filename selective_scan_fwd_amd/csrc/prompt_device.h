@@ -114,8 +114,11 @@ __device__ __forceinline__ Piece piece_by_length(const SeqArgs &q, int64_t slot)
   p.lo = __builtin_amdgcn_readlane(lo, p.seq);
   const int all = __builtin_amdgcn_readlane(len, p.seq);
   p.hi = p.lo + (all > 0 ? all : 0);
+  // (of offsets that overlap, sequences may have more chunks than there are slots)
+  const int begin = __builtin_amdgcn_readlane(start, p.seq), room = static_cast<int>(q.slots) - begin;
   p.count = __builtin_amdgcn_readlane(count, p.seq);
-  p.c = static_cast<int>(slot) - __builtin_amdgcn_readlane(start, p.seq);
+  p.count = p.count < room ? p.count : room;
+  p.c = static_cast<int>(slot) - begin;
   p.id = static_cast<uint32_t>(p.lo) / static_cast<uint32_t>(chunk) + p.seq + p.c;
   p.t0 = p.lo + static_cast<int64_t>(p.c) * chunk;
   const int64_t left = p.hi - p.t0;
