@@ -189,7 +189,7 @@ __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScan
 #pragma unroll
       for (int i = 0; i < 4; ++i) bstore<float>(rh, l.state[i], h[i]);
     }
-  } else {
+  } else if (!SECOND) {                    // (the second launch's other workgroups read these)
     float s[4] = {steps, steps, steps, steps};
     steps = gather(s);
     *reinterpret_cast<f32x4 *>(a.ends + block * 256 + lane * 4) = h;

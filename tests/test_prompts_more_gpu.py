@@ -68,6 +68,23 @@ def test_chunks_are_the_whole_walk(dtype):
     close(h2[:1], host(h1), 2 * F32, "state")
 
 
+@pytest.mark.parametrize("dim,n", [(2000, 1), (1984, 16)])
+def test_more_chunks_than_run_at_once(dim, n):
+    """Chunks whose workgroups start when others have ended: every one joins the ends that the first launch left."""
+    l = 4097
+    s = Scan(dim, 1, l, dim, n, "f32", gate=False)
+    a = {k: v.double() if v is not None else None for k, v in s.a.items()}
+    h, want = s.h0[0].double(), []
+    dt = torch.nn.functional.softplus(a["delta"] + a["delta_bias"])[0]
+    for t in range(l):
+        h = torch.exp(dt[t][:, None] * a["A"]) * h + (dt[t] * a["u"][0, t])[:, None] * a["B"][0, t]
+        want.append((h * a["C"][0, t]).sum(-1) + a["D"] * a["u"][0, t])
+    for _ in range(3):
+        out, state = vm.vm_prompt_scan(**s.a, h0=s.h0, want_state=True)
+        close(out[0], host(torch.stack(want)), F32, "out")
+        close(state[0], host(h), F32, "state")
+
+
 def test_results_repeat_bit_for_bit():
     s = Scan(5, 2, 700, 48, 16, "bf16", strided=True)
     run = lambda: vm.vm_prompt_scan_bwd(**s.a, dout=s.dout, h0=s.h0, dstate=s.dstate)
@@ -75,6 +92,10 @@ def test_results_repeat_bit_for_bit():
     for _ in range(3):
         again = run()
         assert all(torch.equal(bits(first[k]), bits(again[k])) for k in first)
+    s = Scan(6, 1, 4000, 1000, 16, "f32")
+    first = [t.clone() for t in vm.vm_prompt_scan(**s.a, want_state=True)]
+    for _ in range(3):
+        assert all(torch.equal(x, y) for x, y in zip(first, vm.vm_prompt_scan(**s.a, want_state=True)))
     g = gen(2)
     x, w, dout = dev(randn(g, 2, 500, 40)), dev(randn(g, 40, 4)), dev(randn(g, 2, 500, 40))
     a, b = (vm.vm_prompt_conv_bwd(x, w, dout) for _ in range(2))
