@@ -153,69 +153,54 @@ __device__ __forceinline__ void settle(float (&y)[4]) {
   asm("s_nop 1" : "+v"(y[0]), "+v"(y[1]), "+v"(y[2]), "+v"(y[3]));
 }
 
-// One token's update and read-out:  e[i] = 2^e[i],  h[i] = e[i] h[i] + b[4 S + i] x,
-// y = sum_i c[4 S + i] h[i]  (y to be settled).  In one piece, for the waits that the
-// compiler does not count inside: an exponential's result may be read one state later,
-// and what the last instruction before wrote (b or c) through DPP two states later.
-#define VM_UPDATE_TEXT(A, B, C, D)                                             \
-  "v_exp_f32 %[e0], %[e0]\n"                                                   \
-  "v_exp_f32 %[e1], %[e1]\n"                                                   \
-  "v_exp_f32 %[e2], %[e2]\n"                                                   \
-  "v_exp_f32 %[e3], %[e3]\n"                                                   \
-  "v_mul_f32 %[h0], %[h0], %[e0]\n"                                            \
-  "v_mul_f32 %[h1], %[h1], %[e1]\n"                                            \
-  "v_mul_f32 %[h2], %[h2], %[e2]\n"                                            \
-  "v_mul_f32 %[h3], %[h3], %[e3]\n"                                            \
-  "v_fmac_f32_dpp %[h0], %[b], %[x] row_newbcast:" #A " row_mask:0xf bank_mask:0xf\n" \
-  "v_fmac_f32_dpp %[h1], %[b], %[x] row_newbcast:" #B " row_mask:0xf bank_mask:0xf\n" \
-  "v_fmac_f32_dpp %[h2], %[b], %[x] row_newbcast:" #C " row_mask:0xf bank_mask:0xf\n" \
-  "v_fmac_f32_dpp %[h3], %[b], %[x] row_newbcast:" #D " row_mask:0xf bank_mask:0xf\n"
-#define VM_UPDATE_OUT                                                          \
-  [h0] "+&v"(h[0]), [h1] "+&v"(h[1]), [h2] "+&v"(h[2]), [h3] "+&v"(h[3]),      \
-      [e0] "+&v"(e[0]), [e1] "+&v"(e[1]), [e2] "+&v"(e[2]), [e3] "+&v"(e[3])
-template <int S> __device__ __forceinline__ void update(f32x4 &e, float b, float x, f32x4 &h);
-template <int S> __device__ __forceinline__ float update_read(f32x4 &e, float b, float x, float c, f32x4 &h);
-// The same from state h into another, r.
-template <int S> __device__ __forceinline__ void update_to(f32x4 &e, float b, float x, const f32x4 &h, f32x4 &r);
-#define VM_UPDATE(S, A, B, C, D)                                               \
-  template <>                                                                  \
-  __device__ __forceinline__ void update_to<S>(f32x4 &e, float b, float x, const f32x4 &h, f32x4 &r) { \
-    asm("v_exp_f32 %[e0], %[e0]\n"                                             \
-        "v_exp_f32 %[e1], %[e1]\n"                                             \
-        "v_exp_f32 %[e2], %[e2]\n"                                             \
-        "v_exp_f32 %[e3], %[e3]\n"                                             \
-        "v_mul_f32 %[r0], %[h0], %[e0]\n"                                      \
-        "v_mul_f32 %[r1], %[h1], %[e1]\n"                                      \
-        "v_mul_f32 %[r2], %[h2], %[e2]\n"                                      \
-        "v_mul_f32 %[r3], %[h3], %[e3]\n"                                      \
-        "v_fmac_f32_dpp %[r0], %[b], %[x] row_newbcast:" #A " row_mask:0xf bank_mask:0xf\n" \
-        "v_fmac_f32_dpp %[r1], %[b], %[x] row_newbcast:" #B " row_mask:0xf bank_mask:0xf\n" \
-        "v_fmac_f32_dpp %[r2], %[b], %[x] row_newbcast:" #C " row_mask:0xf bank_mask:0xf\n" \
-        "v_fmac_f32_dpp %[r3], %[b], %[x] row_newbcast:" #D " row_mask:0xf bank_mask:0xf\n" \
-        : [r0] "=&v"(r[0]), [r1] "=&v"(r[1]), [r2] "=&v"(r[2]), [r3] "=&v"(r[3]), \
-          [e0] "+&v"(e[0]), [e1] "+&v"(e[1]), [e2] "+&v"(e[2]), [e3] "+&v"(e[3]) \
-        : [h0] "v"(h[0]), [h1] "v"(h[1]), [h2] "v"(h[2]), [h3] "v"(h[3]), [b] "v"(b), [x] "v"(x)); \
-  }                                                                            \
-  template <>                                                                  \
-  __device__ __forceinline__ void update<S>(f32x4 &e, float b, float x, f32x4 &h) { \
-    asm(VM_UPDATE_TEXT(A, B, C, D) : VM_UPDATE_OUT : [b] "v"(b), [x] "v"(x));  \
-  }                                                                            \
-  template <>                                                                  \
-  __device__ __forceinline__ float update_read<S>(f32x4 &e, float b, float x, float c, f32x4 &h) { \
-    float y;                                                                   \
-    asm(VM_UPDATE_TEXT(A, B, C, D)                                             \
-        "v_mul_f32_dpp %[y], %[c], %[h0] row_newbcast:" #A " row_mask:0xf bank_mask:0xf\n"  \
-        "v_fmac_f32_dpp %[y], %[c], %[h1] row_newbcast:" #B " row_mask:0xf bank_mask:0xf\n" \
-        "v_fmac_f32_dpp %[y], %[c], %[h2] row_newbcast:" #C " row_mask:0xf bank_mask:0xf\n" \
-        "v_fmac_f32_dpp %[y], %[c], %[h3] row_newbcast:" #D " row_mask:0xf bank_mask:0xf\n" \
-        : VM_UPDATE_OUT, [y] "=&v"(y)                                          \
-        : [b] "v"(b), [x] "v"(x), [c] "v"(c));                                 \
-    return y;                                                                  \
+// One token's update and read-out:  e[i] = 2^e[i],  r[i] = e[i] h[i] + b[4 S + i] x,
+// y = sum_i c[4 S + i] r[i]  (y to be settled).  The state is rounded once a token.  In one
+// piece, for the waits that the compiler does not count inside: an exponential's result may
+// be read one state later, and what the last instruction before wrote (b or c) through DPP
+// two states later.
+#define VM_UPDATE_TEXT(A, B, C, D)                                                          \
+  "v_exp_f32 %[e0], %[e0]\n"                                                                \
+  "v_exp_f32 %[e1], %[e1]\n"                                                                \
+  "v_exp_f32 %[e2], %[e2]\n"                                                                \
+  "v_exp_f32 %[e3], %[e3]\n"                                                                \
+  "v_mul_f32_dpp %[r0], %[b], %[x] row_newbcast:" #A " row_mask:0xf bank_mask:0xf\n"        \
+  "v_mul_f32_dpp %[r1], %[b], %[x] row_newbcast:" #B " row_mask:0xf bank_mask:0xf\n"        \
+  "v_mul_f32_dpp %[r2], %[b], %[x] row_newbcast:" #C " row_mask:0xf bank_mask:0xf\n"        \
+  "v_mul_f32_dpp %[r3], %[b], %[x] row_newbcast:" #D " row_mask:0xf bank_mask:0xf\n"        \
+  "v_fmac_f32 %[r0], %[h0], %[e0]\n"                                                        \
+  "v_fmac_f32 %[r1], %[h1], %[e1]\n"                                                        \
+  "v_fmac_f32 %[r2], %[h2], %[e2]\n"                                                        \
+  "v_fmac_f32 %[r3], %[h3], %[e3]\n"
+#define VM_UPDATE_OUT                                                                       \
+  [r0] "=&v"(r[0]), [r1] "=&v"(r[1]), [r2] "=&v"(r[2]), [r3] "=&v"(r[3]), [e0] "+&v"(e[0]), \
+      [e1] "+&v"(e[1]), [e2] "+&v"(e[2]), [e3] "+&v"(e[3])
+#define VM_UPDATE_IN                                                                        \
+  [h0] "v"(h[0]), [h1] "v"(h[1]), [h2] "v"(h[2]), [h3] "v"(h[3]), [b] "v"(b), [x] "v"(x)
+template <int S> __device__ __forceinline__ void update(f32x4 &e, float b, float x, const f32x4 &h, f32x4 &r);
+template <int S>
+__device__ __forceinline__ float update_read(f32x4 &e, float b, float x, float c, const f32x4 &h, f32x4 &r);
+#define VM_UPDATE(S, A, B, C, D)                                                            \
+  template <>                                                                               \
+  __device__ __forceinline__ void update<S>(f32x4 &e, float b, float x, const f32x4 &h, f32x4 &r) { \
+    asm(VM_UPDATE_TEXT(A, B, C, D) : VM_UPDATE_OUT : VM_UPDATE_IN);                         \
+  }                                                                                         \
+  template <>                                                                               \
+  __device__ __forceinline__ float update_read<S>(f32x4 &e, float b, float x, float c, const f32x4 &h, f32x4 &r) { \
+    float y;                                                                                \
+    asm(VM_UPDATE_TEXT(A, B, C, D)                                                          \
+        "v_mul_f32_dpp %[y], %[c], %[r0] row_newbcast:" #A " row_mask:0xf bank_mask:0xf\n"  \
+        "v_fmac_f32_dpp %[y], %[c], %[r1] row_newbcast:" #B " row_mask:0xf bank_mask:0xf\n" \
+        "v_fmac_f32_dpp %[y], %[c], %[r2] row_newbcast:" #C " row_mask:0xf bank_mask:0xf\n" \
+        "v_fmac_f32_dpp %[y], %[c], %[r3] row_newbcast:" #D " row_mask:0xf bank_mask:0xf\n" \
+        : VM_UPDATE_OUT, [y] "=&v"(y)                                                       \
+        : VM_UPDATE_IN, [c] "v"(c));                                                        \
+    return y;                                                                               \
   }
 VM_UPDATE(0, 0, 1, 2, 3) VM_UPDATE(1, 4, 5, 6, 7) VM_UPDATE(2, 8, 9, 10, 11) VM_UPDATE(3, 12, 13, 14, 15)
 #undef VM_UPDATE
 #undef VM_UPDATE_TEXT
 #undef VM_UPDATE_OUT
+#undef VM_UPDATE_IN
 
 __device__ __forceinline__ void swap32(float &a, float &b) {
   auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);

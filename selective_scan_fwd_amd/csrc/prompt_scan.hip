@@ -59,10 +59,12 @@ __device__ __forceinline__ void token(const float (&A2)[4], float dt, float b, f
   f32x4 e;
 #pragma unroll
   for (int i = 0; i < 4; ++i) e[i] = dt * A2[i];
+  f32x4 r;
   if (FULL)
-    y = update_read<S>(e, b, du, c, h);
+    y = update_read<S>(e, b, du, c, h, r);
   else
-    update<S>(e, b, du, h);
+    update<S>(e, b, du, h, r);
+  h = r;
 }
 
 // One tile of m tokens (ALL: a whole one) from (token, c0) on.

@@ -56,7 +56,9 @@ __device__ __forceinline__ void local_token(const float (&A2)[4], float dt, floa
   f32x4 e;
 #pragma unroll
   for (int i = 0; i < 4; ++i) e[i] = dt * A2[i];
-  update<S>(e, b, du, h);
+  f32x4 r;
+  update<S>(e, b, du, h, r);
+  h = r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) decay[i] *= e[i];
   f32x4 o = decay;                      // decay C dy: summed over the chunk
@@ -71,7 +73,7 @@ __device__ __forceinline__ void again(const float (&A2)[4], float dt, float b, f
 #pragma unroll
   for (int i = 0; i < 4; ++i) decay[i] = dt * A2[i];
   f32x4 to;
-  update_to<S>(decay, b, du, h, to);
+  update<S>(decay, b, du, h, to);
   r = to;
 }
 
