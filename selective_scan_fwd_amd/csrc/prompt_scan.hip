@@ -11,6 +11,8 @@
 // (its first, whose state is known, in full) and notes its end state and the sum of
 // its steps T; a second one forms each later chunk's first state from the chunks
 // before it, h <- exp(A T) h + end, and walks it in full.
+// 40 packed prompts of 1 to 1500 tokens, 4096 channels, bf16 (1.7 TB/s): 168 us; one prompt of
+// 4097 tokens: 118 us in two launches over 20 chunks.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

@@ -17,6 +17,9 @@
 // Sums over channels: 32 products of a group of 4 tokens are folded over the 16
 // lanes of a row, halving the values at each step, then over the workgroup's waves
 // in LDS; sums over blocks and chunks in a fixed order by launches of their own.
+// Bound by vector instructions: 87 a wave and token in the second launch, 37 in the first
+// with the gathered gradients and 20 without.  128 x 197 tokens of 384 channels, fp32:
+// 35 and 130 us; 2 x 4097 of 2048, bf16, in chunks: 104 and 210 us.
 #include <hip/hip_runtime.h>
 
 #include "prompt_device.h"
