@@ -977,6 +977,15 @@ def _row_tensor(t, name, dtype, shape, index):
     raise ValueError(f"{name} must have contiguous rows, evenly spaced (shape {tuple(shape)}, strides {strides})")
 
 
+def _out(t, name, like, dtype, shape, index):
+    """An output of a call: the caller's tensor, or a new one beside `like` (which was
+    checked).  Returns it and its address."""
+    if t is None:
+        t = like.new_empty(shape) if like.dtype is dtype else torch.empty(shape, dtype=dtype, device=like.device)
+        return t, t.data_ptr()
+    return t, _arg(t, name, dtype, shape, index)
+
+
 def _float_arg(t, name, shape, index):
     return None if t is None else _arg(t, name, torch.float32, shape, index)
 
@@ -1032,16 +1041,14 @@ def vm_prompt_conv(x, w, bias=None, silu=True, h0=None, state=None, want_state=F
     px, xs = _row_tensor(x, "x", dtype, (batch, L, dim), index)
     seq, n, kept = _sequences(batch, offsets, slots, fresh, h0, state, index)
     shape = (kept, width - 1, dim)
-    if out is None:
-        out = torch.empty((batch, L, dim), dtype=dtype, device=x.device)
+    out, po = _out(out, "out", x, dtype, (batch, L, dim), index)
     if state is None and want_state:
         if slots is not None:
             raise ValueError("with slots, state is a pool of the caller's")
         state = torch.empty(shape, dtype=dtype, device=x.device)
     _launch("vm_prompt_conv", index, seq, px, xs, _float_arg(w, "w", (dim, width), index),
             _float_arg(bias, "bias", (dim,), index), _arg(h0, "h0", dtype, shape, index),
-            _arg(state, "state", dtype, shape, index), _arg(out, "out", dtype, (batch, L, dim), index), batch, L, dim, width,
-            int(bool(silu)), _dtype_code(x))
+            _arg(state, "state", dtype, shape, index), po, batch, L, dim, width, int(bool(silu)), _dtype_code(x))
     return out, state
 
 
@@ -1086,11 +1093,10 @@ def vm_token_conv(x, w, state, bias=None, silu=True, slots=None, out=None):
     if not isinstance(state, torch.Tensor) or state.dim() != 3:
         raise ValueError("state must be a [n_slots, width - 1, dim] tensor")
     n = state.shape[0]
-    if out is None:
-        out = torch.empty((batch, dim), dtype=dtype, device=x.device)
+    out, po = _out(out, "out", x, dtype, (batch, dim), index)
     _launch("vm_token_conv", index, px, xs, _float_arg(w, "w", (dim, width), index), _float_arg(bias, "bias", (dim,), index),
-            _arg(state, "state", dtype, (n, width - 1, dim), index), _arg(slots, "slots", torch.int32, (batch,), index),
-            _arg(out, "out", dtype, (batch, dim), index), batch, n, dim, width, int(bool(silu)), _dtype_code(x))
+            _arg(state, "state", dtype, (n, width - 1, dim), index), _arg(slots, "slots", torch.int32, (batch,), index), po,
+            batch, n, dim, width, int(bool(silu)), _dtype_code(x))
     return out
 
 
@@ -1121,16 +1127,15 @@ def vm_prompt_scan(u, delta, A, B, C, D=None, delta_bias=None, z=None, delta_sof
     batch, L, dim = _three(u, "u").shape
     p, index, dim, N = _scan_rows(u, delta, A, B, C, D, delta_bias, z)
     seq, n, kept = _sequences(batch, offsets, slots, fresh, h0, state, index)
-    if out is None:
-        out = torch.empty((batch, L, dim), dtype=u.dtype, device=u.device)
+    out, po = _out(out, "out", u, u.dtype, (batch, L, dim), index)
     if state is None and want_state:
         if slots is not None:
             raise ValueError("with slots, state is a pool of the caller's")
         state = torch.empty((n, dim, N), dtype=torch.float32, device=u.device)
     ws, wp, wn = _workspace(load_library().vm_prompt_scan_workspace(batch, L, n, dim, N, offsets is not None, 0), u.device)
     _launch("vm_prompt_scan", index, p, seq, _float_arg(h0, "h0", (kept, dim, N), index),
-            _float_arg(state, "state", (kept, dim, N), index), _arg(out, "out", u.dtype, (batch, L, dim), index), batch, L,
-            dim, N, _dtype_code(u), _options(delta_softplus, False), wp, wn)
+            _float_arg(state, "state", (kept, dim, N), index), po, batch, L, dim, N, _dtype_code(u),
+            _options(delta_softplus, False), wp, wn)
     return out, state
 
 
@@ -1174,11 +1179,10 @@ def vm_token_scan(u, delta, A, B, C, state, D=None, delta_bias=None, z=None, del
     if not isinstance(state, torch.Tensor) or state.dim() != 3:
         raise ValueError("state must be a [n_slots, dim, N] tensor")
     n = state.shape[0]
-    if out is None:
-        out = torch.empty((batch, dim), dtype=u.dtype, device=u.device)
+    out, po = _out(out, "out", u, u.dtype, (batch, dim), index)
     _launch("vm_token_scan", index, p, _float_arg(state, "state", (n, dim, N), index),
-            _arg(slots, "slots", torch.int32, (batch,), index), _arg(out, "out", u.dtype, (batch, dim), index), batch, n, dim,
-            N, _dtype_code(u), _options(delta_softplus, False))
+            _arg(slots, "slots", torch.int32, (batch,), index), po, batch, n, dim, N, _dtype_code(u),
+            _options(delta_softplus, False))
     return out
 
 
@@ -1206,14 +1210,14 @@ def vm_norm_before(x, w=None, b=None, residual=None, scale=None, factor=1.0, cen
     index, dtype, shape = x.get_device(), x.dtype, x.shape
     px, xs = _row_tensor(x, "x", dtype, shape, index)
     rtype = _residual_type(residual, _residual_type(r, dtype))
-    if y is None:
-        y = torch.empty(shape, dtype=dtype, device=x.device)
-    if r is None and want_residual:
-        r = torch.empty(shape, dtype=rtype, device=x.device)
+    pres = _arg(residual, "residual", rtype, shape, index)
+    y, py = _out(y, "y", x, dtype, shape, index)
+    pr = None
+    if want_residual or r is not None:
+        r, pr = _out(r, "r", x if residual is None else residual, rtype, shape, index)
     p = VmBlockNorm(px, _float_arg(w, "w", (dim,), index), _float_arg(b, "b", (dim,), index),
                     _float_arg(scale, "scale", (dim,), index), None, xs, 0, 0, 0, eps, factor, VM_NORM_CENTER if center else 0)
-    _launch("vm_norm_before", index, p, _arg(residual, "residual", rtype, shape, index), _arg(y, "y", dtype, shape, index),
-            _arg(r, "r", rtype, shape, index), rows, dim, _dtype_code(x), _GRAD_CODES.get(rtype, -1))
+    _launch("vm_norm_before", index, p, pres, py, pr, rows, dim, _dtype_code(x), _GRAD_CODES.get(rtype, -1))
     return y, r
 
 
@@ -1278,10 +1282,9 @@ def vm_norm_after(x, w=None, z=None, group=None, residual=None, scale=None, fact
     residual's dtype and may be residual itself."""
     p, index, rows, dim, _, _ = _norm_after(x, w, z, group, scale, factor, gate_first, eps)
     rtype = _residual_type(residual, _residual_type(out, x.dtype))
-    if out is None:
-        out = torch.empty(x.shape, dtype=rtype, device=x.device)
-    _launch("vm_norm_after", index, p, _arg(residual, "residual", rtype, x.shape, index), _arg(out, "out", rtype, x.shape, index),
-            rows, dim, _dtype_code(x), _GRAD_CODES.get(rtype, -1))
+    pres = _arg(residual, "residual", rtype, x.shape, index)
+    out, po = _out(out, "out", x if residual is None else residual, rtype, x.shape, index)
+    _launch("vm_norm_after", index, p, pres, po, rows, dim, _dtype_code(x), _GRAD_CODES.get(rtype, -1))
     return out
 
 
