@@ -94,7 +94,10 @@ __device__ __forceinline__ Piece piece_of(const SeqArgs &q, int64_t slot) {
 }
 
 // The same for a whole wave with up to 64 packed sequences, whose slots then go by
-// falling length, so that no long sequence starts last.
+// falling length, so that no long sequence starts last.  PART: slots of all chunks (0),
+// all but the last of several (1), or all but the first (2, of which there are at most L
+// over the tokens of a chunk).
+template <int PART = 0>
 __device__ __forceinline__ Piece piece_by_length(const SeqArgs &q, int64_t slot) {
   if (q.off == nullptr || q.nseq > 64) return piece_of(q, slot);
   const int lane = threadIdx.x % 64;
@@ -103,22 +106,27 @@ __device__ __forceinline__ Piece piece_by_length(const SeqArgs &q, int64_t slot)
   const int len = has ? static_cast<int>(clamped(q.off[lane + 1], q.L)) - lo : -1;
   const int chunk = static_cast<int>(q.chunk);
   const int count = !has ? 0 : len > chunk ? (len + chunk - 1) / chunk : 1;
+  const int here = PART == 0 ? count : PART == 1 ? (count > 1 ? count - 1 : count) : (count > 1 ? count - 1 : 0);
+  // (lengths past 2^24 in the sequences' order; no two keys alike)
+  constexpr int kMost = 1 << 24;
+  const int key = has ? (len < 0 ? 0 : len < kMost ? len : kMost) * 64 + 63 - lane : -1;
   int start = 0;
-  for (int i = 0; i < q.nseq; ++i) {
-    const int l = __builtin_amdgcn_readlane(len, i), c = __builtin_amdgcn_readlane(count, i);
-    start += l > len || (l == len && i < lane) ? c : 0;
-  }
+  for (int i = 0; i < q.nseq; ++i)
+    start += __builtin_amdgcn_readlane(key, i) > key ? __builtin_amdgcn_readlane(here, i) : 0;
   Piece p;
-  const uint64_t mine = __ballot(has && slot >= start && slot < start + count);
+  const uint64_t mine = __ballot(has && slot >= start && slot < start + here);
   p.seq = mine != 0 ? __builtin_ctzll(mine) : 0;
   p.lo = __builtin_amdgcn_readlane(lo, p.seq);
   const int all = __builtin_amdgcn_readlane(len, p.seq);
   p.hi = p.lo + (all > 0 ? all : 0);
-  // (of offsets that overlap, sequences may have more chunks than there are slots)
-  const int begin = __builtin_amdgcn_readlane(start, p.seq), room = static_cast<int>(q.slots) - begin;
+  const int begin = __builtin_amdgcn_readlane(start, p.seq);
   p.count = __builtin_amdgcn_readlane(count, p.seq);
-  p.count = p.count < room ? p.count : room;
-  p.c = static_cast<int>(slot) - begin;
+  if (PART == 0) {
+    // (of offsets that overlap, sequences may have more chunks than there are slots)
+    const int room = static_cast<int>(q.slots) - begin;
+    p.count = p.count < room ? p.count : room;
+  }
+  p.c = static_cast<int>(slot) - begin + (PART == 2 ? 1 : 0);
   p.id = static_cast<uint32_t>(p.lo) / static_cast<uint32_t>(chunk) + p.seq + p.c;
   p.t0 = p.lo + static_cast<int64_t>(p.c) * chunk;
   const int64_t left = p.hi - p.t0;

@@ -11,7 +11,7 @@
 // (its first, whose state is known, in full) and notes its end state and the sum of
 // its steps T; a second one forms each later chunk's first state from the chunks
 // before it, h <- exp(A T) h + end, and walks it in full.
-// 40 packed prompts of 1 to 1500 tokens, 4096 channels, bf16 (1.7 TB/s): 168 us; one prompt of
+// 40 packed prompts of 1 to 1500 tokens, 4096 channels, bf16 (1.9 TB/s): 156 us; one prompt of
 // 4097 tokens: 118 us in two launches over 20 chunks.
 #include <hip/hip_runtime.h>
 
@@ -127,7 +127,7 @@ __device__ __forceinline__ float walk(const PromptScanArgs &a, const Lane &l, co
 }
 
 template <typename T, bool GATE, bool SECOND>
-__global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScanArgs a) {
+__global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScanArgs a, int64_t slots) {
   __shared__ __align__(16) float meets[kScanWaves][kGroups][16][8];
   float(*meet)[16][8] = meets[threadIdx.x / 64];
   const int lane = threadIdx.x % 64;
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScan
     // that the longest sequence of one round shares its units with the shortest of the next
     const int each = 256 / wide, round = each > 1 ? static_cast<int>(slot) / each : 0;
     if ((round & 1) != 0) {
-      const int64_t next = (round + int64_t{1}) * each, end = next < a.q.slots ? next : a.q.slots;
+      const int64_t next = (round + int64_t{1}) * each, end = next < slots ? next : slots;
       slot = end - 1 - (slot - static_cast<int64_t>(round) * each);
     }
   }
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScan
   }
   const int blk = uniform(static_cast<int>(blockIdx.x % wide) * waves + threadIdx.x / 64);
   if (blk >= blocks) return;
-  const Piece p = piece_by_length(a.q, slot);
+  const Piece p = piece_by_length<SECOND ? 2 : 1>(a.q, slot);
   if (p.len < 0 || (SECOND ? p.c == 0 : p.c > 0 && p.c == p.count - 1)) return;
   // a long chunk goes on at its own pace beside short ones
   if (a.q.off != nullptr) {
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScan
   const float D = channel_value(a.D, c0, l), bias = channel_value(a.bias, c0, l);
 
   const int64_t kept = kept_at(a.q, p.seq);
-  const int64_t block = slot * blocks + blk;
+  const int64_t block = p.id * blocks + blk;
   f32x4 h = {0, 0, 0, 0};
   if (!SECOND) {
     if (p.c == 0 && a.h0 != nullptr && kept >= 0 && starts_kept(a.q, p.seq)) {
@@ -204,10 +204,15 @@ __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScan
 template <typename T, bool GATE>
 hipError_t launch_scan(const PromptScanArgs &a, hipStream_t s) {
   const int blocks = (a.dim + 15) / 16, waves = blocks < kScanWaves ? blocks : kScanWaves;
-  const int64_t slots = a.q.off == nullptr && a.ends != nullptr ? a.q.slots - a.q.nseq : a.q.slots;
-  const dim3 grid(static_cast<uint32_t>(slots * ((blocks + waves - 1) / waves)));
-  prompt_scan_kernel<T, GATE, false><<<grid, 64 * waves, 0, s>>>(a);
-  if (a.ends != nullptr) prompt_scan_kernel<T, GATE, true><<<grid, 64 * waves, 0, s>>>(a);
+  const int64_t wide = (blocks + waves - 1) / waves;
+  const bool packed = a.q.off != nullptr, many = a.ends != nullptr;
+  const int64_t first = !packed && many ? a.q.slots - a.q.nseq : a.q.slots;
+  prompt_scan_kernel<T, GATE, false><<<static_cast<uint32_t>(first * wide), 64 * waves, 0, s>>>(a, first);
+  if (many) {
+    // (40 packed prompts of one chunk each: 16 us to find nothing to do in all slots, 5 in these)
+    const int64_t second = packed && a.q.nseq <= 64 ? a.q.L / a.q.chunk : first;
+    prompt_scan_kernel<T, GATE, true><<<static_cast<uint32_t>(second * wide), 64 * waves, 0, s>>>(a, second);
+  }
   return hipGetLastError();
 }
 
@@ -223,8 +228,16 @@ int64_t seq_slots(int64_t nseq, int64_t L, int64_t chunk, bool packed) {
 // 25000, and a chunk 900 for the joining of all before it.
 int64_t scan_chunk(int64_t tokens, int64_t nseq, int64_t L, int dim, bool packed) {
   const int64_t blocks = scan_blocks(dim);
-  if (packed) {                              // (the lengths are not known here)
-    const int64_t want = 1024 / blocks + 1, chunk = (tokens / want + kTile) / kTile * kTile;
+  if (packed) {
+    // The lengths are not known here.  Many waves to a SIMD share it whatever the lengths,
+    // and a second walk costs them most: only what is longer than most of a SIMD's tokens is
+    // cut.  With fewer the longest sequence sets the time: chunks of a quarter of a SIMD's
+    // tokens, but not so many to a sequence that joining them costs more.  (Lengths of 1 to
+    // 1369, 8145 in all, us: 4096 channels, 10 waves, 1632 tokens 160, 528 175; 2048, 5 waves,
+    // 912 136, 272 112; 768, 384 77, 144 65.)
+    const double all = static_cast<double>(tokens * blocks) / 1024.0, few = all / 4, join = 1.5 * sqrt(static_cast<double>(tokens));
+    const bool full = nseq * blocks >= 8 * 1024;
+    const int64_t chunk = static_cast<int64_t>(full ? 0.8 * all : few > join ? few : join) / kTile * kTile + kTile;
     return chunk < 64 ? (L < 64 ? L : 64) : chunk < L ? chunk : L;
   }
   const auto pace = [](double k) { return k <= 1 ? 205 : 60 + 131 * (k < 4 ? ceil(k) : k); };

@@ -520,8 +520,13 @@ hipError_t launch_back(const PromptScanArgs &a, hipStream_t s) {
 // a wave and SIMD, 200 where it gathers gradients besides (230 and more alone).
 int64_t scan_back_chunk(int64_t tokens, int64_t nseq, int64_t L, int dim, bool packed) {
   const int64_t wide = scan_wide(dim);
-  if (packed) {                              // (the lengths are not known here)
-    const int64_t want = 512 / wide + 1, chunk = (tokens / want + kBackTile) / kBackTile * kBackTile;
+  if (packed) {
+    // The lengths are not known here.  A cut sequence costs the first launch's gathered
+    // gradients, one that is too long its chain: a third of a SIMD's tokens where it has many
+    // waves, else a fifth.  (Lengths of 1 to 1369, 8145 in all, us: 4096 channels, 10 waves,
+    // 1040 tokens 684, 528 621; 2048, 5 waves, 528 393, 208 350; 768, 208 164, 96 152.)
+    const int64_t all = tokens * scan_blocks(dim) / 1024, cut = all / (nseq * scan_blocks(dim) >= 8 * 1024 ? 3 : 5);
+    const int64_t chunk = cut / kBackTile * kBackTile + kBackTile;
     return chunk < 64 ? (L < 64 ? L : 64) : chunk < L ? chunk : L;
   }
   int64_t best = L;

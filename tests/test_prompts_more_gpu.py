@@ -51,6 +51,24 @@ def test_many_sequences(count):
         close(v, want[k], SUMS, "conv d" + k)
 
 
+@pytest.mark.parametrize("count", [31, 32])
+def test_one_long_sequence_among_many_short_ones(count):
+    """Packed sequences of many channels: with 32 of 4096 only the longest is cut, with 31 chunks are shorter; the other
+    launches' slots are those of the chunks that they have."""
+    lens = [2] * 10 + [430] + [0, 7] + [1] * (count - 13)
+    s = Scan(count, 1, sum(lens) + 3, 4096, 2, "f32", lens=lens)
+    pool = s.h0.clone()
+    out, _ = vm.vm_prompt_scan(**s.a, h0=pool, state=pool, offsets=s.offsets)
+    want, last, _ = s.ref(list(host(s.h0)))
+    close(s.inside(out), s.inside(want), F32, "out")
+    close(pool, last, F32, "state")
+    d = vm.vm_prompt_scan_bwd(**s.a, dout=s.dout, h0=s.h0, dstate=s.dstate, offsets=s.offsets)
+    want = s.ref_grad(list(host(s.h0)), list(host(s.dstate)))
+    for k, v in d.items():
+        inside = s.inside if k in ("u", "delta", "B", "C", "z") else (lambda x: x)
+        close(inside(v), inside(want[k]), SUMS, k)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_chunks_are_the_whole_walk(dtype):
     """A row of few channels is cut in chunks; beside enough others of its kind it is walked whole."""
