@@ -105,7 +105,7 @@ __device__ __forceinline__ Piece piece_by_length(const SeqArgs &q, int64_t slot)
   const int lo = has ? static_cast<int>(clamped(q.off[lane], q.L)) : 0;
   const int len = has ? static_cast<int>(clamped(q.off[lane + 1], q.L)) - lo : -1;
   const int chunk = static_cast<int>(q.chunk);
-  const int count = !has ? 0 : len > chunk ? (len + chunk - 1) / chunk : 1;
+  const int count = !has ? 0 : len > chunk ? (len - 1) / chunk + 1 : 1;
   const int here = PART == 0 ? count : PART == 1 ? (count > 1 ? count - 1 : count) : (count > 1 ? count - 1 : 0);
   // (lengths past 2^24 in the sequences' order; no two keys alike)
   constexpr int kMost = 1 << 24;

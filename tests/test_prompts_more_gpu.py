@@ -176,6 +176,46 @@ def test_graph_of_a_block():
         assert torch.equal(bits(tok), bits(twant)) and torch.equal(states, kept[0]) and torch.equal(bits(windows), bits(kept[1]))
 
 
+def test_row_of_empty_sequences():
+    s = Scan(1, 1, 5, 20, 4, "f32", lens=[0, 0])
+    out = torch.full((1, 5, 20), 7.0, device=DEV)
+    _, state = vm.vm_prompt_scan(**s.a, h0=s.h0, want_state=True, offsets=s.offsets, out=out)
+    assert (out == 7.0).all() and torch.equal(state, s.h0)
+    d = vm.vm_prompt_scan_bwd(**s.a, dout=s.dout, h0=s.h0, dstate=s.dstate, offsets=s.offsets)
+    assert torch.equal(d["h0"], s.dstate) and not any(d[k].any() for k in ("A", "D", "delta_bias"))
+    x, w, h0 = s.a["u"], dev(torch.ones(20, 4)), dev(randn(gen(1), 2, 3, 20))
+    out.fill_(7.0)
+    _, state = vm.vm_prompt_conv(x, w, h0=h0, want_state=True, offsets=s.offsets, out=out)
+    assert (out == 7.0).all() and torch.equal(state, h0)
+    d = vm.vm_prompt_conv_bwd(x, w, s.dout, h0=h0, dstate=h0, offsets=s.offsets)
+    assert torch.equal(d["h0"], h0) and not d["w"].any()
+
+
+def test_calls_from_threads_on_their_own_streams():
+    import threading
+
+    s = Scan(6, 1, 900, 200, 16, "f32")
+    want = vm.vm_prompt_scan(**s.a, want_state=True)
+    want_d = vm.vm_prompt_scan_bwd(**s.a, dout=s.dout)
+    torch.cuda.synchronize()
+    good = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got, d = vm.vm_prompt_scan(**s.a, want_state=True), vm.vm_prompt_scan_bwd(**s.a, dout=s.dout)
+                stream.synchronize()
+                good.append(all(torch.equal(x, y) for x, y in zip(got, want)) and all(torch.equal(d[k], want_d[k]) for k in d))
+
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(good) == 60 and all(good)
+
+
 def test_other_streams():
     s = Scan(4, 1, 2000, 64, 16, "f32")
     want = vm.vm_prompt_scan(**s.a)[0].clone()
