@@ -6,7 +6,7 @@ import torch
 
 import oracle.prompts as ref
 import selective_scan_fwd_amd as vm
-from _prompts import BF16, DEV, F32, SUMS, Scan, close, dev, gen, host, randn, tol_of
+from _prompts import BF16, DEV, F32, SUMS, Scan, close, dev, gen, host, offsets_of, randn, tol_of
 
 pytestmark = pytest.mark.gpu
 
@@ -174,6 +174,46 @@ def test_graph_of_a_block():
         assert torch.isfinite(junk)
         assert all(torch.equal(bits(a), bits(c)) for a, c in zip(got, want)), i
         assert torch.equal(bits(tok), bits(twant)) and torch.equal(states, kept[0]) and torch.equal(bits(windows), bits(kept[1]))
+
+
+def test_graph_of_packed_prompts():
+    """One graph for every packed batch of a size: lengths, slots and fresh flags are read when it runs."""
+    dim, n, pool, most = 64, 16, 9, 700
+    g = gen(17)
+    s = Scan(17, 1, most, dim, n, "bf16")
+    x, cw = dev(randn(g, 1, most, dim), torch.bfloat16), dev(0.5 * randn(g, dim, 4))
+    rest = {k: v for k, v in s.a.items() if k != "u"}
+    states, windows = dev(randn(g, pool, dim, n)), dev(randn(g, pool, 3, dim), torch.bfloat16)
+    first = states.clone(), windows.clone()
+    offsets, slots, fresh = (torch.zeros(k, dtype=torch.int32, device=DEV) for k in (6, 5, 5))
+    out = torch.empty(1, most, dim, device=DEV, dtype=torch.bfloat16)
+
+    def prompts():
+        u, _ = vm.vm_prompt_conv(x, cw, h0=windows, state=windows, offsets=offsets, slots=slots, fresh=fresh)
+        vm.vm_prompt_scan(u, **rest, h0=states, state=states, offsets=offsets, slots=slots, fresh=fresh, out=out)
+        return u
+
+    def reset():
+        states.copy_(first[0]), windows.copy_(first[1]), out.fill_(7.0)
+
+    slots.copy_(torch.arange(5))
+    prompts()                                          # (warm-up outside)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        prompts()
+    for i, lens in enumerate([[700, 0, 0, 0, 0], [1, 650, 3, 0, 46], [100] * 5, [0, 1, 2, 3, 4], [300, 1, 64, 65, 200]]):
+        offsets.copy_(offsets_of(lens)), slots.copy_(torch.randperm(pool, generator=g)[:5]), fresh.copy_(torch.arange(5) % 2 == i % 2)
+        reset()
+        prompts()
+        want = out.clone(), states.clone(), windows.clone()
+        reset()
+        torch.cuda.synchronize()
+        graph.replay()
+        junk = torch.randn(1 << 20, device=DEV).sum()  # (the program's own work between)
+        torch.cuda.synchronize()
+        assert torch.isfinite(junk) and (out[0, sum(lens):] == 7.0).all()
+        assert all(torch.equal(bits(a), bits(b)) for a, b in zip((out, states, windows), want)), lens
 
 
 def test_row_of_empty_sequences():
