@@ -12,7 +12,7 @@
 // its steps T; a second one forms each later chunk's first state from the chunks
 // before it, h <- exp(A T) h + end, and walks it in full.
 // 40 packed prompts of 1 to 1500 tokens, 4096 channels, bf16 (1.9 TB/s): 156 us; one prompt of
-// 4097 tokens: 118 us in two launches over 20 chunks.
+// 4097 tokens: 118 us in two launches over 13 chunks.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
