@@ -293,6 +293,12 @@ __device__ __forceinline__ void put(Rsrc r, uint32_t off, float x) {
     bstore<T>(r, off, x);
 }
 
+// decay x + e for a decay over many tokens: it may round to 0 though none of its factors
+// does, and an infinite x stays what it is.
+__device__ __forceinline__ float carry(float decay, float x, float e) {
+  return __builtin_fabsf(x) == __builtin_inff() ? x + e : __builtin_fmaf(decay, x, e);
+}
+
 // Joins chunks to x: x <- 2^(A2 t_j) x + e_j for the blocks j = first, first + step, ...
 // of `many` (with loads of four under way).
 __device__ __forceinline__ void join_chunks(const float *ends, const float *steps, int64_t first, int64_t step, int many,
@@ -310,14 +316,14 @@ __device__ __forceinline__ void join_chunks(const float *ends, const float *step
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = __builtin_fmaf(hw_exp2(A2[i] * t[k]), x[i], e[k][i]);
+      for (int i = 0; i < 4; ++i) x[i] = carry(hw_exp2(A2[i] * t[k]), x[i], e[k][i]);
   }
   for (; j < many; ++j) {
     const int64_t at = first + j * step;
     const f32x4 e = *reinterpret_cast<const f32x4 *>(ends + at * 256 + lane * 4);
     const float t = steps[at * 16 + lane % 16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __builtin_fmaf(hw_exp2(A2[i] * t), x[i], e[i]);
+    for (int i = 0; i < 4; ++i) x[i] = carry(hw_exp2(A2[i] * t), x[i], e[i]);
   }
 }
 

@@ -380,7 +380,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 3) void scan_back_kernel(PromptSca
     if (p.count > 1) {
       const float t = a.before[at * 16 + l.ch];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) begin[i] = __builtin_fmaf(hw_exp2(A2[i] * t), init[i], begin[i]);
+      for (int i = 0; i < 4; ++i) begin[i] = carry(hw_exp2(A2[i] * t), init[i], begin[i]);
     }
   };
   for (int tile = tiles - 1; tile >= 0; --tile) {
