@@ -240,7 +240,16 @@ struct Lane {
   uint32_t u, d, z, dense;            // token q of a tile (dense: of outputs and their gradients)
   uint32_t b, c;                      // B and C of a group: token (l / 4) % 4, state 4 q + l % 4
   uint32_t state[4];                  // in a block's [16][n]
+  __device__ __forceinline__ bool has(int i) const { return state[i] != kOob; }   // a state in place i
 };
+
+// Places without a state hold 0 and read 0 for B and C, which leaves them 0 as long as every
+// factor is finite.  What was formed with others is cleared by this.
+__device__ __forceinline__ void clear_places(const Lane &l, f32x4 &x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = l.has(i) ? x[i] : 0.0f;
+}
+__device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) < __builtin_inff(); }
 
 template <typename T>
 __device__ __forceinline__ Lane lane_of(const PromptScanArgs &a, int c0, int lane) {
@@ -274,6 +283,15 @@ template <typename T>
 __device__ __forceinline__ Rsrc rows(const void *base, int64_t stride, int64_t token, int64_t col, int tokens, int width) {
   const int bytes = tokens > 0 ? static_cast<int>(((tokens - 1) * stride + width) * sizeof(T)) : 0;
   return make_rsrc(static_cast<const T *>(base) + token * stride + col, bytes);
+}
+
+// y = sum_i c[4 S + i] r[i], as in update_read.
+template <int S>
+__device__ __forceinline__ float read_out(float c, const f32x4 &r) {
+  float y = row_bcast<4 * S>(c) * r[0];
+  y = __builtin_fmaf(row_bcast<4 * S + 1>(c), r[1], y);
+  y = __builtin_fmaf(row_bcast<4 * S + 2>(c), r[2], y);
+  return __builtin_fmaf(row_bcast<4 * S + 3>(c), r[3], y);
 }
 
 // The step of a token, 0 past the chunk's end: such a step leaves the state as it is.

@@ -56,36 +56,30 @@ __device__ __forceinline__ void load_tile(const PromptScanArgs &a, const Lane &l
   }
 }
 
-template <int S, bool FULL>
-__device__ __forceinline__ void token(const float (&A2)[4], float dt, float b, float du, float c, f32x4 &h, float &y) {
+// CLEAR: places without a state are cleared before they are read.
+template <int S, bool FULL, bool CLEAR>
+__device__ __forceinline__ void token(const Lane &l, const float (&A2)[4], float dt, float b, float du, float c, f32x4 &h,
+                                      float &y) {
   f32x4 e;
 #pragma unroll
   for (int i = 0; i < 4; ++i) e[i] = dt * A2[i];
   f32x4 r;
-  if (FULL)
+  if (FULL && !CLEAR)
     y = update_read<S>(e, b, du, c, h, r);
   else
     update<S>(e, b, du, h, r);
+  if (CLEAR) {
+    clear_places(l, r);
+    y = read_out<S>(c, r);
+  }
   h = r;
 }
 
-// One tile of m tokens (ALL: a whole one) from (token, c0) on.
-template <typename T, bool FULL, bool GATE, bool ALL>
-__device__ __forceinline__ void tile(const PromptScanArgs &a, const Lane &l, const Raw &r, int64_t at, int m, int c0,
-                                     const float (&A2)[4], float bias, float D, f32x4 &h, float &steps,
-                                     float (*meet)[16][8]) {
-  const Rsrc ro = rows<T>(a.out, a.dim, at, c0, FULL ? m : 0, l.cw);
+// The tokens of a tile, whose dt and dt u are in `meet`.
+template <typename T, bool FULL, bool GATE, bool ALL, bool CLEAR>
+__device__ __forceinline__ void tokens(const PromptScanArgs &a, const Lane &l, const Raw &r, Rsrc ro, uint32_t oo, int m,
+                                       const float (&A2)[4], float D, f32x4 &h, float (*meet)[16][8]) {
   const uint32_t so = 4 * a.dim * sizeof(T);
-  const uint32_t oo = l.live ? (l.q * static_cast<uint32_t>(a.dim) + l.ch) * sizeof(T) : kOob;
-  // every lane gets its channel's dt and dt u of all tokens by way of LDS
-#pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    const float dt = step_of(a, r.d[g] + bias, ALL || 4 * g + l.q < m);
-    steps += dt;
-    meet[g][l.ch][2 * l.q] = dt;
-    meet[g][l.ch][2 * l.q + 1] = dt * r.u[g];
-  }
-  wave_lds_fence();
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
     if (!ALL && 4 * g >= m) break;
@@ -95,10 +89,10 @@ __device__ __forceinline__ void tile(const PromptScanArgs &a, const Lane &l, con
       dts[s] = meet[g][l.ch][2 * s];
       dus[s] = meet[g][l.ch][2 * s + 1];
     }
-    token<0, FULL>(A2, dts[0], r.b[g], dus[0], r.c[g], h, y[0]);
-    token<1, FULL>(A2, dts[1], r.b[g], dus[1], r.c[g], h, y[1]);
-    token<2, FULL>(A2, dts[2], r.b[g], dus[2], r.c[g], h, y[2]);
-    token<3, FULL>(A2, dts[3], r.b[g], dus[3], r.c[g], h, y[3]);
+    token<0, FULL, CLEAR>(l, A2, dts[0], r.b[g], dus[0], r.c[g], h, y[0]);
+    token<1, FULL, CLEAR>(l, A2, dts[1], r.b[g], dus[1], r.c[g], h, y[1]);
+    token<2, FULL, CLEAR>(l, A2, dts[2], r.b[g], dus[2], r.c[g], h, y[2]);
+    token<3, FULL, CLEAR>(l, A2, dts[3], r.b[g], dus[3], r.c[g], h, y[3]);
     if (FULL) {
       settle(y);
       float o = __builtin_fmaf(D, r.u[g], gather(y));
@@ -106,11 +100,35 @@ __device__ __forceinline__ void tile(const PromptScanArgs &a, const Lane &l, con
       put<T>(ro, oo + g * so, o);
     }
   }
+}
+
+// One tile of m tokens (ALL: a whole one) from (token, c0) on.
+template <typename T, bool FULL, bool GATE, bool PLACES, bool ALL>
+__device__ __forceinline__ void tile(const PromptScanArgs &a, const Lane &l, const Raw &r, int64_t at, int m, int c0,
+                                     const float (&A2)[4], float bias, float D, f32x4 &h, float &steps,
+                                     float (*meet)[16][8]) {
+  const Rsrc ro = rows<T>(a.out, a.dim, at, c0, FULL ? m : 0, l.cw);
+  const uint32_t oo = l.live ? (l.q * static_cast<uint32_t>(a.dim) + l.ch) * sizeof(T) : kOob;
+  // every lane gets its channel's dt and dt u of all tokens by way of LDS
+  bool odd = false;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const float dt = step_of(a, r.d[g] + bias, ALL || 4 * g + l.q < m), du = dt * r.u[g];
+    steps += dt;
+    meet[g][l.ch][2 * l.q] = dt;
+    meet[g][l.ch][2 * l.q + 1] = du;
+    if (FULL && PLACES) odd |= !finite(du);  // (so is it where dt is not)
+  }
+  wave_lds_fence();
+  if (FULL && PLACES && __any(odd))
+    tokens<T, FULL, GATE, ALL, true>(a, l, r, ro, oo, m, A2, D, h, meet);
+  else
+    tokens<T, FULL, GATE, ALL, false>(a, l, r, ro, oo, m, A2, D, h, meet);
   wave_lds_fence();
 }
 
 // Walks a chunk from state h; returns the sum of this lane's steps.
-template <typename T, bool FULL, bool GATE>
+template <typename T, bool FULL, bool GATE, bool PLACES>
 __device__ __forceinline__ float walk(const PromptScanArgs &a, const Lane &l, const Piece &p, int c0, const float (&A2)[4],
                                       float bias, float D, f32x4 &h, float (*meet)[16][8]) {
   float steps = 0.0f;
@@ -120,14 +138,17 @@ __device__ __forceinline__ float walk(const PromptScanArgs &a, const Lane &l, co
   for (; at + kTile <= p.len; at += kTile) {
     const Raw r = next;
     load_tile<T, FULL, GATE>(a, l, p.t0 + at + kTile, p.len - at - kTile, c0, next);
-    tile<T, FULL, GATE, true>(a, l, r, p.t0 + at, kTile, c0, A2, bias, D, h, steps, meet);
+    tile<T, FULL, GATE, PLACES, true>(a, l, r, p.t0 + at, kTile, c0, A2, bias, D, h, steps, meet);
   }
-  if (at < p.len) tile<T, FULL, GATE, false>(a, l, next, p.t0 + at, p.len - at, c0, A2, bias, D, h, steps, meet);
+  if (at < p.len) tile<T, FULL, GATE, PLACES, false>(a, l, next, p.t0 + at, p.len - at, c0, A2, bias, D, h, steps, meet);
   return steps;
 }
 
-template <typename T, bool GATE, bool SECOND>
-__global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScanArgs a, int64_t slots) {
+// PLACES: there are fewer than 16 states.  (A kernel of its own, since the test of each tile
+// costs the scan of 16 states 2.7%: 163 -> 168 us for 40 packed prompts.  Four waves a SIMD: with
+// three, which the compiler would take, 8 states need 154 us, with four 150.)
+template <typename T, bool GATE, bool PLACES, bool SECOND>
+__global__ __launch_bounds__(64 * kScanWaves, PLACES ? 4 : 1) void prompt_scan_kernel(PromptScanArgs a, int64_t slots) {
   __shared__ __align__(16) float meets[kScanWaves][kGroups][16][8];
   float(*meet)[16][8] = meets[threadIdx.x / 64];
   const int lane = threadIdx.x % 64;
@@ -181,12 +202,13 @@ __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScan
     }
   } else {
     join_chunks(a.ends, a.steps, block - static_cast<int64_t>(p.c) * blocks, blocks, p.c, lane, A2, h);
+    if (PLACES) clear_places(l, h);
   }
   float steps;
   if (SECOND || p.c == 0)
-    steps = walk<T, true, GATE>(a, l, p, c0, A2, bias, D, h, meet);
+    steps = walk<T, true, GATE, PLACES>(a, l, p, c0, A2, bias, D, h, meet);
   else
-    steps = walk<T, false, false>(a, l, p, c0, A2, bias, D, h, meet);
+    steps = walk<T, false, false, PLACES>(a, l, p, c0, A2, bias, D, h, meet);
   if (p.c == p.count - 1) {
     if (a.state != nullptr && kept >= 0) {
       const Rsrc rh = make_rsrc(a.state + (kept * a.dim + c0) * a.n, l.cw * a.n * 4);
@@ -201,19 +223,25 @@ __global__ __launch_bounds__(64 * kScanWaves) void prompt_scan_kernel(PromptScan
   }
 }
 
-template <typename T, bool GATE>
+template <typename T, bool GATE, bool PLACES>
 hipError_t launch_scan(const PromptScanArgs &a, hipStream_t s) {
   const int blocks = (a.dim + 15) / 16, waves = blocks < kScanWaves ? blocks : kScanWaves;
   const int64_t wide = (blocks + waves - 1) / waves;
   const bool packed = a.q.off != nullptr, many = a.ends != nullptr;
   const int64_t first = !packed && many ? a.q.slots - a.q.nseq : a.q.slots;
-  prompt_scan_kernel<T, GATE, false><<<static_cast<uint32_t>(first * wide), 64 * waves, 0, s>>>(a, first);
+  prompt_scan_kernel<T, GATE, PLACES, false><<<static_cast<uint32_t>(first * wide), 64 * waves, 0, s>>>(a, first);
   if (many) {
     // (40 packed prompts of one chunk each: 16 us to find nothing to do in all slots, 5 in these)
     const int64_t second = packed && a.q.nseq <= 64 ? a.q.L / a.q.chunk : first;
-    prompt_scan_kernel<T, GATE, true><<<static_cast<uint32_t>(second * wide), 64 * waves, 0, s>>>(a, second);
+    prompt_scan_kernel<T, GATE, PLACES, true><<<static_cast<uint32_t>(second * wide), 64 * waves, 0, s>>>(a, second);
   }
   return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_type(const PromptScanArgs &a, hipStream_t s) {
+  if (a.n < 16) return a.z != nullptr ? launch_scan<T, true, true>(a, s) : launch_scan<T, false, true>(a, s);
+  return a.z != nullptr ? launch_scan<T, true, false>(a, s) : launch_scan<T, false, false>(a, s);
 }
 
 }  // namespace
@@ -259,8 +287,7 @@ int64_t scan_chunk(int64_t tokens, int64_t nseq, int64_t L, int dim, bool packed
 }
 
 hipError_t launch_prompt_scan(const PromptScanArgs &a, bool bf16, hipStream_t s) {
-  if (bf16) return a.z != nullptr ? launch_scan<bf16_t, true>(a, s) : launch_scan<bf16_t, false>(a, s);
-  return a.z != nullptr ? launch_scan<float, true>(a, s) : launch_scan<float, false>(a, s);
+  return bf16 ? launch_type<bf16_t>(a, s) : launch_type<float>(a, s);
 }
 
 }  // namespace vmk

@@ -77,7 +77,8 @@ __global__ __launch_bounds__(kThreads) void token_scan_kernel(TokenScanArgs a, i
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       h[k][i] = __builtin_fmaf(hw_exp2(dt * rate2(A[k][i])), h[k][i], du * B[i]);
-      sum = __builtin_fmaf(C[i], h[k][i], sum);
+      // (a place without a state has 0 times an infinite dt or dt u, which is no number)
+      sum = 4 * q + i < a.n ? __builtin_fmaf(C[i], h[k][i], sum) : sum;
     }
     if (live[k] && !idle) {
       if (VEC) {

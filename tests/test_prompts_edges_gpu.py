@@ -79,3 +79,53 @@ def test_an_infinite_state_stays_infinite_over_chunks():
     s.a["A"] = torch.full((16, 16), -8.0, device=DEV)
     s.dstate[0, 4] = INF
     check_backward(s)
+
+
+# ------------------------------------------- fewer than 16 states or channels
+SHAPES = [(1, 1, 1), (2, 37, 20), (1, 130, 33), (3, 18, 64)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 5, 8, 16])
+@pytest.mark.parametrize("batch,seqlen,dim", SHAPES)
+def test_infinite_tokens(batch, seqlen, dim, n, dtype):
+    """A lane's places past the last state hold 0, whatever a token brings."""
+    for name in ("u", "delta"):
+        s = mild(Scan(seqlen + n, batch, seqlen, dim, n, dtype, gate=dim != 33))
+        put(s, name, (batch - 1, seqlen // 2, dim // 2), INF)
+        check_forward(s)
+        put(s, "D", slice(None), s.a["D"].abs())
+        put(s, "u", (0, 0, 0), -INF)
+        check_forward(s)
+
+
+@pytest.mark.parametrize("n", [1, 5, 8])
+def test_infinite_tokens_of_packed_sequences(n):
+    lens = [3, 0, 70, 1, 16, 129]
+    s = mild(Scan(n, 1, sum(lens), 40, n, "f32", lens=lens))
+    put(s, "u", (0, 20, 7), INF)
+    put(s, "u", (0, sum(lens) - 129, 39), -INF)
+    check_forward(s)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 3, 5, 8, 16])
+def test_infinite_single_tokens(n, dtype):
+    s = mild(Scan(n, 4, 1, 70, n, dtype))
+    put(s, "u", (1, 0, 2), INF)
+    put(s, "u", (2, 0, 69), -INF)
+    put(s, "delta", (3, 0, 5), INF)
+    state = s.h0.clone()
+    a = {k: v if v is None or k in ("A", "D", "delta_bias") else v[:, 0].contiguous() for k, v in s.a.items()}
+    out = vm.vm_token_scan(**a, state=state)
+    with np.errstate(all="ignore"):
+        want, last, _ = s.ref(list(host(s.h0)))
+    same(out, want[:, 0], tol(out), "out")
+    same(state, last, F32, "state")
+
+
+def test_an_infinite_state_stays_infinite_over_chunks_with_one_state():
+    s = mild(Scan(23, 1, 700, 16, 1, "f32", bias=False))
+    s.a["A"] = torch.full((16, 1), -8.0, device=DEV)
+    put(s, "u", (0, 3, 5), INF)
+    check_forward(s)
