@@ -347,9 +347,15 @@ __device__ __forceinline__ void join_chunks(const float *ends, const float *step
 
 // Decay rates, ready for 2^x.  A rate of -Inf (which decays to 0 in any step) is
 // held finite, so that the steps of 0 that fill up a group leave a state alone.
+constexpr float kLeastRate2 = -3.0e38f;
 __device__ __forceinline__ float rate2(float a) {
   const float r = a * kLog2e;
-  return r < -3.0e38f ? -3.0e38f : r;      // (NaN stays)
+  return r < kLeastRate2 ? kLeastRate2 : r;      // (NaN stays)
+}
+// The same rate as a factor: times a decay of 0 it is 0.
+__device__ __forceinline__ float rate(float a) {
+  constexpr float least = kLeastRate2 / kLog2e;
+  return a < least ? least : a;
 }
 
 }  // namespace

@@ -340,8 +340,9 @@ __global__ __launch_bounds__(64 * kScanWaves, 3) void scan_back_kernel(PromptSca
   const Rsrc rA = make_rsrc(a.A + static_cast<int64_t>(c0) * a.n, l.cw * a.n * 4);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    A[i] = bload<float>(rA, l.state[i]);
-    A2[i] = rate2(A[i]);
+    const float x = bload<float>(rA, l.state[i]);
+    A[i] = rate(x);
+    A2[i] = rate2(x);
   }
   const float bias = channel_value(a.bias, c0, l), D = channel_value(a.D, c0, l);
   const uint32_t dstep = 4 * static_cast<uint32_t>(a.dim) * sizeof(T);

@@ -129,3 +129,17 @@ def test_an_infinite_state_stays_infinite_over_chunks_with_one_state():
     s.a["A"] = torch.full((16, 1), -8.0, device=DEV)
     put(s, "u", (0, 3, 5), INF)
     check_forward(s)
+
+
+# ------------------------------------------------------ rates and partial tiles
+@pytest.mark.parametrize("seqlen", [1, 37, 700])
+def test_gradients_at_a_rate_of_minus_infinity(seqlen):
+    """Such a rate clears a state at every step; its gradients are those of a rate that does the same and is finite."""
+    s = Scan(seqlen, 1, seqlen, 24, 16, "f32")
+    put(s, "A", (3, slice(None)), -INF)
+    put(s, "A", (20, 5), -INF)
+    d = vm.vm_prompt_scan_bwd(**s.a, dout=s.dout, h0=s.h0, dstate=s.dstate)
+    s.a["A"] = s.a["A"].clamp(min=-1e30)
+    want = s.ref_grad(list(host(s.h0)), list(host(s.dstate)))
+    for k, v in d.items():
+        same(v, want[k], SUMS, "d" + k)
