@@ -317,6 +317,31 @@ __device__ __forceinline__ void back_token(const float (&A)[4], float dts, float
   }
 }
 
+// The same in a tile that the chunk's tokens do not fill.  in: this is one of them.  The steps of
+// 0 behind them add nothing to dA: 0 times the last token's state, which they would add, is no
+// number where that state is infinite.
+template <int S>
+__device__ __forceinline__ void back_token_of(bool in, const float (&A)[4], float dts, float dus, float dys, float b, float c,
+                                               const f32x4 &decay, const f32x4 &h, const f32x4 &before, f32x4 &p,
+                                               float (&dA)[4], float (&x)[4], float (&yy)[4], float &w, float &through,
+                                               float &y) {
+  const float bs[4] = {row_bcast<4 * S>(b), row_bcast<4 * S + 1>(b), row_bcast<4 * S + 2>(b), row_bcast<4 * S + 3>(b)};
+  const float cs[4] = {row_bcast<4 * S>(c), row_bcast<4 * S + 1>(c), row_bcast<4 * S + 2>(c), row_bcast<4 * S + 3>(c)};
+  w = y = through = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float g = __builtin_fmaf(cs[i], dys, p[i]);
+    w = __builtin_fmaf(bs[i], g, w);
+    y = __builtin_fmaf(cs[i], h[i], y);
+    yy[i] = h[i] * dys;
+    x[i] = g * dus;
+    p[i] = g * decay[i];
+    const float m = p[i] * before[i];
+    dA[i] = in ? __builtin_fmaf(m, dts, dA[i]) : dA[i];
+    through = __builtin_fmaf(m, A[i], through);
+  }
+}
+
 template <typename T, bool GATE>
 __global__ __launch_bounds__(64 * kScanWaves, 3) void scan_back_kernel(PromptScanArgs a, int wide) {
   __shared__ __align__(16) float sums[2][kScanWaves][kBackTile * 32];
@@ -367,32 +392,29 @@ __global__ __launch_bounds__(64 * kScanWaves, 3) void scan_back_kernel(PromptSca
                 grad);
   }
 
-  const int tiles = (p.len + kBackTile - 1) / kBackTile;
   const int64_t mark = (p.t0 / kBackTile + p.id) * blocks + blk;
   const int64_t tokens = a.q.L * (a.q.off != nullptr ? 1 : a.q.nseq);
   float dD = 0.0f, dbias = 0.0f;
-  Raw r;
-  f32x4 begin = {0, 0, 0, 0};
-  const auto fetch = [&](int tile) {
-    load_tile<T, true, GATE>(a, l, p.t0 + tile * kBackTile, p.len - tile * kBackTile, c0, r);
-    const int64_t at = mark + static_cast<int64_t>(tile) * blocks;
-    if (blk >= blocks) return;
-    begin = *reinterpret_cast<const f32x4 *>(a.marks + at * 256 + lane * 4);
-    if (p.count > 1) {
-      const float t = a.before[at * 16 + l.ch];
+  // One tile.  WHOLE: of kBackTile tokens; else it is the chunk's last.
+  const auto walk_tile = [&](int tile, auto whole) __attribute__((always_inline)) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    const int64_t t = p.t0 + tile * kBackTile, at = mark + static_cast<int64_t>(tile) * blocks;
+    const int m = WHOLE ? kBackTile : p.len - tile * kBackTile;
+    Raw r;
+    load_tile<T, true, GATE>(a, l, t, m, c0, r);
+    f32x4 begin = {0, 0, 0, 0};
+    if (blk < blocks) {
+      begin = *reinterpret_cast<const f32x4 *>(a.marks + at * 256 + lane * 4);
+      if (p.count > 1) {
+        const float before = a.before[at * 16 + l.ch];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) begin[i] = carry(hw_exp2(A2[i] * t), init[i], begin[i]);
+        for (int i = 0; i < 4; ++i) begin[i] = carry(hw_exp2(A2[i] * before), init[i], begin[i]);
+      }
     }
-  };
-  for (int tile = tiles - 1; tile >= 0; --tile) {
-    const int64_t t = p.t0 + tile * kBackTile;
-    const int m = p.len - tile * kBackTile < kBackTile ? p.len - tile * kBackTile : kBackTile;
-    fetch(tile);
-    f32x4 hs[kBackTile], es[kBackTile];
-    float slope[kGroups];
+    float slope[kGroups] = {};
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      const float dt = step_of(a, r.d[g] + bias, 4 * g + l.q < m);
+      const float dt = step_of(a, r.d[g] + bias, WHOLE || 4 * g + l.q < m);
       float dy = r.o[g];
       if (GATE) dy *= silu_both(r.z[g], slope[g]);
       meet[g][l.ch][2 * l.q] = dt;
@@ -400,31 +422,12 @@ __global__ __launch_bounds__(64 * kScanWaves, 3) void scan_back_kernel(PromptSca
       meet[g][l.ch][8 + l.q] = dy;
     }
     wave_lds_fence();
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const auto &w = meet[g][l.ch];
-      again<0>(A2, w[0], r.b[g], w[1], g > 0 ? hs[g > 0 ? 4 * g - 1 : 0] : begin, hs[4 * g], es[4 * g]);
-      again<1>(A2, w[2], r.b[g], w[3], hs[4 * g], hs[4 * g + 1], es[4 * g + 1]);
-      again<2>(A2, w[4], r.b[g], w[5], hs[4 * g + 1], hs[4 * g + 2], es[4 * g + 2]);
-      again<3>(A2, w[6], r.b[g], w[7], hs[4 * g + 2], hs[4 * g + 3], es[4 * g + 3]);
-    }
     float *mine = sums[tile & 1][wave];
     const Rsrc rdu = rows<T>(a.du, a.dim, t, c0, m, l.cw), rdd = rows<T>(a.ddelta, a.dim, t, c0, m, l.cw),
                rdz = rows<T>(a.dz, a.dim, t, c0, GATE ? m : 0, l.cw);
-#pragma unroll
-    for (int g = kGroups - 1; g >= 0; --g) {
-      if (4 * g >= m) continue;
-      const bool in = 4 * g + l.q < m;
-      const auto &w = meet[g][l.ch];
-      float x[4][4], yy[4][4], along4[4], th[4], y[4];
-      back_token<3, GATE>(A, w[6], w[7], w[11], r.b[g], r.c[g], es[4 * g + 3], hs[4 * g + 3], hs[4 * g + 2], grad, dA, x[3],
-                          yy[3], along4[3], th[3], y[3]);
-      back_token<2, GATE>(A, w[4], w[5], w[10], r.b[g], r.c[g], es[4 * g + 2], hs[4 * g + 2], hs[4 * g + 1], grad, dA, x[2],
-                          yy[2], along4[2], th[2], y[2]);
-      back_token<1, GATE>(A, w[2], w[3], w[9], r.b[g], r.c[g], es[4 * g + 1], hs[4 * g + 1], hs[4 * g], grad, dA, x[1], yy[1],
-                          along4[1], th[1], y[1]);
-      back_token<0, GATE>(A, w[0], w[1], w[8], r.b[g], r.c[g], es[4 * g], hs[4 * g], g > 0 ? hs[g > 0 ? 4 * g - 1 : 0] : begin,
-                          grad, dA, x[0], yy[0], along4[0], th[0], y[0]);
+    // what a group's tokens give, from their products and sums over a lane's states
+    const auto finish = [&](int g, float(&along4)[4], const float(&th)[4], float(&y)[4], const float(&x)[4][4],
+                            const float(&yy)[4][4]) __attribute__((always_inline)) {
       settle(along4);
       if (GATE) settle(y);
       const float along = gather(along4), through = gather(th);
@@ -439,12 +442,64 @@ __global__ __launch_bounds__(64 * kScanWaves, 3) void scan_back_kernel(PromptSca
       dd *= a.softplus ? slope2 : 1.0f;
       put<T>(rdd, l.dense + g * dstep, dd);
       dD = __builtin_fmaf(dy, r.u[g], dD);
-      dbias += in ? dd : 0.0f;
+      dbias += WHOLE || 4 * g + l.q < m ? dd : 0.0f;
       float s[2];
       fold(x, yy, lane, s);
       typedef float f32x2 __attribute__((ext_vector_type(2)));
-      const int at = (4 * g + ((lane >> 1) & 3)) * 32 + (lane & 8) * 2 + 4 * l.q + 2 * (lane & 1);
-      *reinterpret_cast<f32x2 *>(mine + at) = f32x2{s[0], s[1]};
+      const int to = (4 * g + ((lane >> 1) & 3)) * 32 + (lane & 8) * 2 + 4 * l.q + 2 * (lane & 1);
+      *reinterpret_cast<f32x2 *>(mine + to) = f32x2{s[0], s[1]};
+    };
+    if constexpr (WHOLE) {
+      f32x4 hs[kBackTile], es[kBackTile];
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const auto &w = meet[g][l.ch];
+        again<0>(A2, w[0], r.b[g], w[1], g > 0 ? hs[g > 0 ? 4 * g - 1 : 0] : begin, hs[4 * g], es[4 * g]);
+        again<1>(A2, w[2], r.b[g], w[3], hs[4 * g], hs[4 * g + 1], es[4 * g + 1]);
+        again<2>(A2, w[4], r.b[g], w[5], hs[4 * g + 1], hs[4 * g + 2], es[4 * g + 2]);
+        again<3>(A2, w[6], r.b[g], w[7], hs[4 * g + 2], hs[4 * g + 3], es[4 * g + 3]);
+      }
+#pragma unroll
+      for (int g = kGroups - 1; g >= 0; --g) {
+        const auto &w = meet[g][l.ch];
+        float x[4][4], yy[4][4], along4[4], th[4], y[4];
+        back_token<3, GATE>(A, w[6], w[7], w[11], r.b[g], r.c[g], es[4 * g + 3], hs[4 * g + 3], hs[4 * g + 2], grad, dA, x[3],
+                            yy[3], along4[3], th[3], y[3]);
+        back_token<2, GATE>(A, w[4], w[5], w[10], r.b[g], r.c[g], es[4 * g + 2], hs[4 * g + 2], hs[4 * g + 1], grad, dA, x[2],
+                            yy[2], along4[2], th[2], y[2]);
+        back_token<1, GATE>(A, w[2], w[3], w[9], r.b[g], r.c[g], es[4 * g + 1], hs[4 * g + 1], hs[4 * g], grad, dA, x[1], yy[1],
+                            along4[1], th[1], y[1]);
+        back_token<0, GATE>(A, w[0], w[1], w[8], r.b[g], r.c[g], es[4 * g], hs[4 * g], g > 0 ? hs[g > 0 ? 4 * g - 1 : 0] : begin,
+                            grad, dA, x[0], yy[0], along4[0], th[0], y[0]);
+        finish(g, along4, th, y, x, yy);
+      }
+    } else {
+      // one group at a time, its states walked to from the tile's start
+#pragma unroll
+      for (int g = kGroups - 1; g >= 0; --g) {
+        if (4 * g >= m) continue;
+        f32x4 hs[4], es[4], first = begin;
+#pragma unroll
+        for (int k = 0; k <= g; ++k) {
+          if (k > 0) first = hs[3];
+          const auto &w = meet[k][l.ch];
+          again<0>(A2, w[0], r.b[k], w[1], first, hs[0], es[0]);
+          again<1>(A2, w[2], r.b[k], w[3], hs[0], hs[1], es[1]);
+          again<2>(A2, w[4], r.b[k], w[5], hs[1], hs[2], es[2]);
+          again<3>(A2, w[6], r.b[k], w[7], hs[2], hs[3], es[3]);
+        }
+        const auto &w = meet[g][l.ch];
+        float x[4][4], yy[4][4], along4[4], th[4], y[4];
+        back_token_of<3>(4 * g + 3 < m, A, w[6], w[7], w[11], r.b[g], r.c[g], es[3], hs[3], hs[2], grad, dA, x[3], yy[3],
+                         along4[3], th[3], y[3]);
+        back_token_of<2>(4 * g + 2 < m, A, w[4], w[5], w[10], r.b[g], r.c[g], es[2], hs[2], hs[1], grad, dA, x[2], yy[2],
+                         along4[2], th[2], y[2]);
+        back_token_of<1>(4 * g + 1 < m, A, w[2], w[3], w[9], r.b[g], r.c[g], es[1], hs[1], hs[0], grad, dA, x[1], yy[1],
+                         along4[1], th[1], y[1]);
+        back_token_of<0>(true, A, w[0], w[1], w[8], r.b[g], r.c[g], es[0], hs[0], first, grad, dA, x[0], yy[0], along4[0], th[0],
+                         y[0]);
+        finish(g, along4, th, y, x, yy);
+      }
     }
     // (the other tile's sums may still be read by waves behind this barrier)
     __syncthreads();
@@ -455,7 +510,10 @@ __global__ __launch_bounds__(64 * kScanWaves, 3) void scan_back_kernel(PromptSca
       const int tok = i / 32, which = (i / 16) % 2, n = i % 16;
       if (tok < m && n < a.n) a.partBC[((group * tokens + t + tok) * 2 + which) * a.n + n] = s;
     }
-  }
+  };
+  int tile = p.len / kBackTile;
+  if (p.len % kBackTile != 0) walk_tile(tile, std::false_type());
+  while (--tile >= 0) walk_tile(tile, std::true_type());
 
   if (p.c == 0 && !none && a.dh0 != nullptr) {
     const Rsrc r = make_rsrc(a.dh0 + sbase, l.cw * a.n * 4);

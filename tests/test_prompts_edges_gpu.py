@@ -143,3 +143,24 @@ def test_gradients_at_a_rate_of_minus_infinity(seqlen):
     want = s.ref_grad(list(host(s.h0)), list(host(s.dstate)))
     for k, v in d.items():
         same(v, want[k], SUMS, "d" + k)
+
+
+@pytest.mark.parametrize("value", [NAN, INF])
+@pytest.mark.parametrize("seqlen", [1, 2, 3, 5, 8, 13, 130])
+def test_gradients_at_a_bad_last_token(seqlen, value):
+    """What the last token brings to the state reaches no gradient that does not read that state, wherever in a tile
+    the sequence ends."""
+    s = mild(Scan(seqlen, 2, seqlen, 20, 16, "f32"))
+    put(s, "u", (1, seqlen - 1, 2), value)
+    check_backward(s)
+    s = mild(Scan(seqlen, 2, seqlen, 20, 16, "f32"))
+    s.dstate[0, 4] = value
+    check_backward(s)
+
+
+def test_gradients_at_bad_last_tokens_of_packed_sequences():
+    lens = [6, 9, 4, 0, 2]
+    s = mild(Scan(3, 1, sum(lens), 20, 16, "f32", lens=lens))
+    for end, ch in ((6, 1), (15, 2), (19, 3)):
+        put(s, "u", (0, end - 1, ch), NAN)
+    check_backward(s)
