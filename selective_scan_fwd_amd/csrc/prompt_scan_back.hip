@@ -317,32 +317,37 @@ __device__ __forceinline__ void back_token(const float (&A)[4], float dts, float
   }
 }
 
-// The same in a tile that the chunk's tokens do not fill.  in: this is one of them.  The steps of
-// 0 behind them add nothing to dA: 0 times the last token's state, which they would add, is no
-// number where that state is infinite.
-template <int S>
-__device__ __forceinline__ void back_token_of(bool in, const float (&A)[4], float dts, float dus, float dys, float b, float c,
-                                               const f32x4 &decay, const f32x4 &h, const f32x4 &before, f32x4 &p,
-                                               float (&dA)[4], float (&x)[4], float (&yy)[4], float &w, float &through,
-                                               float &y) {
+// The same where a product that the formulas do not have may not be finite.  in: the token is one
+// of the chunk.  The steps of 0 behind them add nothing to dA: 0 times the last token's state,
+// which they would add, is no number where that state is infinite.  PLACES: nor do places without
+// a state or channel add to any sum.
+template <int S, bool PLACES>
+__device__ __forceinline__ void back_token_of(const Lane &l, bool in, const float (&A)[4], float dts, float dus, float dys, float b,
+                                              float c, const f32x4 &decay, const f32x4 &h, const f32x4 &before, f32x4 &p,
+                                              float (&dA)[4], float (&x)[4], float (&yy)[4], float &w, float &through,
+                                              float &y) {
   const float bs[4] = {row_bcast<4 * S>(b), row_bcast<4 * S + 1>(b), row_bcast<4 * S + 2>(b), row_bcast<4 * S + 3>(b)};
   const float cs[4] = {row_bcast<4 * S>(c), row_bcast<4 * S + 1>(c), row_bcast<4 * S + 2>(c), row_bcast<4 * S + 3>(c)};
   w = y = through = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float g = __builtin_fmaf(cs[i], dys, p[i]);
-    w = __builtin_fmaf(bs[i], g, w);
-    y = __builtin_fmaf(cs[i], h[i], y);
-    yy[i] = h[i] * dys;
-    x[i] = g * dus;
-    p[i] = g * decay[i];
+    const bool has = !PLACES || l.has(i);
+    const auto only = [&](float v, float other) { return has ? v : other; };
+    const float g = only(__builtin_fmaf(cs[i], dys, p[i]), 0.0f);
+    w = only(__builtin_fmaf(bs[i], g, w), w);
+    y = only(__builtin_fmaf(cs[i], h[i], y), y);
+    yy[i] = only(h[i] * dys, 0.0f);
+    x[i] = only(g * dus, 0.0f);
+    p[i] = only(g * decay[i], 0.0f);
     const float m = p[i] * before[i];
     dA[i] = in ? __builtin_fmaf(m, dts, dA[i]) : dA[i];
-    through = __builtin_fmaf(m, A[i], through);
+    through = only(__builtin_fmaf(m, A[i], through), through);
   }
 }
 
-template <typename T, bool GATE>
+// PLACES: there are fewer than 16 states, or waves with lanes of no channel.  (A kernel of its
+// own: the test of each tile costs 3%, 128 x 197 tokens of 8 states 175 -> 180 us.)
+template <typename T, bool GATE, bool PLACES>
 __global__ __launch_bounds__(64 * kScanWaves, 3) void scan_back_kernel(PromptScanArgs a, int wide) {
   __shared__ __align__(16) float sums[2][kScanWaves][kBackTile * 32];
   __shared__ __align__(16) float meets[kScanWaves][kGroups][16][12];
@@ -390,6 +395,10 @@ __global__ __launch_bounds__(64 * kScanWaves, 3) void scan_back_kernel(PromptSca
     join_chunks(a.ends, a.steps, first, blocks, p.c, lane, A2, init);
     join_chunks(a.starts, a.steps, first + static_cast<int64_t>(p.count - 1) * blocks, -blocks, p.count - 1 - p.c, lane, A2,
                 grad);
+    if (PLACES) {
+      clear_places(l, init);
+      clear_places(l, grad);
+    }
   }
 
   const int64_t mark = (p.t0 / kBackTile + p.id) * blocks + blk;
@@ -410,16 +419,20 @@ __global__ __launch_bounds__(64 * kScanWaves, 3) void scan_back_kernel(PromptSca
 #pragma unroll
         for (int i = 0; i < 4; ++i) begin[i] = carry(hw_exp2(A2[i] * before), init[i], begin[i]);
       }
+      if (PLACES) clear_places(l, begin);
     }
     float slope[kGroups] = {};
+    float size = 0.0f;                       // of what places without a state or channel multiply by 0
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      const float dt = step_of(a, r.d[g] + bias, WHOLE || 4 * g + l.q < m);
+      const float dt = step_of(a, r.d[g] + bias, WHOLE || 4 * g + l.q < m), du = dt * r.u[g];
       float dy = r.o[g];
       if (GATE) dy *= silu_both(r.z[g], slope[g]);
       meet[g][l.ch][2 * l.q] = dt;
-      meet[g][l.ch][2 * l.q + 1] = dt * r.u[g];
+      meet[g][l.ch][2 * l.q + 1] = du;
       meet[g][l.ch][8 + l.q] = dy;
+      if (PLACES && WHOLE)
+        size += __builtin_fabsf(du) + __builtin_fabsf(dy) + __builtin_fabsf(r.b[g]) + __builtin_fabsf(r.c[g]);
     }
     wave_lds_fence();
     float *mine = sums[tile & 1][wave];
@@ -449,7 +462,34 @@ __global__ __launch_bounds__(64 * kScanWaves, 3) void scan_back_kernel(PromptSca
       const int to = (4 * g + ((lane >> 1) & 3)) * 32 + (lane & 8) * 2 + 4 * l.q + 2 * (lane & 1);
       *reinterpret_cast<f32x2 *>(mine + to) = f32x2{s[0], s[1]};
     };
-    if constexpr (WHOLE) {
+    if (!WHOLE || (PLACES && uniform(__ballot(!finite(size)) != 0) != 0)) {
+      // one group at a time, its states walked to from the tile's start
+#pragma unroll
+      for (int g = kGroups - 1; g >= 0; --g) {
+        if (4 * g >= m) continue;
+        f32x4 hs[4], es[4], first = begin;
+#pragma unroll
+        for (int k = 0; k <= g; ++k) {
+          if (k > 0) first = hs[3];
+          const auto &w = meet[k][l.ch];
+          again<0>(A2, w[0], r.b[k], w[1], first, hs[0], es[0]);
+          again<1>(A2, w[2], r.b[k], w[3], hs[0], hs[1], es[1]);
+          again<2>(A2, w[4], r.b[k], w[5], hs[1], hs[2], es[2]);
+          again<3>(A2, w[6], r.b[k], w[7], hs[2], hs[3], es[3]);
+        }
+        const auto &w = meet[g][l.ch];
+        float x[4][4], yy[4][4], along4[4], th[4], y[4];
+        back_token_of<3, PLACES>(l, 4 * g + 3 < m, A, w[6], w[7], w[11], r.b[g], r.c[g], es[3], hs[3], hs[2], grad, dA,
+                                 x[3], yy[3], along4[3], th[3], y[3]);
+        back_token_of<2, PLACES>(l, 4 * g + 2 < m, A, w[4], w[5], w[10], r.b[g], r.c[g], es[2], hs[2], hs[1], grad, dA,
+                                 x[2], yy[2], along4[2], th[2], y[2]);
+        back_token_of<1, PLACES>(l, 4 * g + 1 < m, A, w[2], w[3], w[9], r.b[g], r.c[g], es[1], hs[1], hs[0], grad, dA,
+                                 x[1], yy[1], along4[1], th[1], y[1]);
+        back_token_of<0, PLACES>(l, true, A, w[0], w[1], w[8], r.b[g], r.c[g], es[0], hs[0], first, grad, dA, x[0], yy[0],
+                                 along4[0], th[0], y[0]);
+        finish(g, along4, th, y, x, yy);
+      }
+    } else if constexpr (WHOLE) {
       f32x4 hs[kBackTile], es[kBackTile];
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
@@ -471,33 +511,6 @@ __global__ __launch_bounds__(64 * kScanWaves, 3) void scan_back_kernel(PromptSca
                             along4[1], th[1], y[1]);
         back_token<0, GATE>(A, w[0], w[1], w[8], r.b[g], r.c[g], es[4 * g], hs[4 * g], g > 0 ? hs[g > 0 ? 4 * g - 1 : 0] : begin,
                             grad, dA, x[0], yy[0], along4[0], th[0], y[0]);
-        finish(g, along4, th, y, x, yy);
-      }
-    } else {
-      // one group at a time, its states walked to from the tile's start
-#pragma unroll
-      for (int g = kGroups - 1; g >= 0; --g) {
-        if (4 * g >= m) continue;
-        f32x4 hs[4], es[4], first = begin;
-#pragma unroll
-        for (int k = 0; k <= g; ++k) {
-          if (k > 0) first = hs[3];
-          const auto &w = meet[k][l.ch];
-          again<0>(A2, w[0], r.b[k], w[1], first, hs[0], es[0]);
-          again<1>(A2, w[2], r.b[k], w[3], hs[0], hs[1], es[1]);
-          again<2>(A2, w[4], r.b[k], w[5], hs[1], hs[2], es[2]);
-          again<3>(A2, w[6], r.b[k], w[7], hs[2], hs[3], es[3]);
-        }
-        const auto &w = meet[g][l.ch];
-        float x[4][4], yy[4][4], along4[4], th[4], y[4];
-        back_token_of<3>(4 * g + 3 < m, A, w[6], w[7], w[11], r.b[g], r.c[g], es[3], hs[3], hs[2], grad, dA, x[3], yy[3],
-                         along4[3], th[3], y[3]);
-        back_token_of<2>(4 * g + 2 < m, A, w[4], w[5], w[10], r.b[g], r.c[g], es[2], hs[2], hs[1], grad, dA, x[2], yy[2],
-                         along4[2], th[2], y[2]);
-        back_token_of<1>(4 * g + 1 < m, A, w[2], w[3], w[9], r.b[g], r.c[g], es[1], hs[1], hs[0], grad, dA, x[1], yy[1],
-                         along4[1], th[1], y[1]);
-        back_token_of<0>(true, A, w[0], w[1], w[8], r.b[g], r.c[g], es[0], hs[0], first, grad, dA, x[0], yy[0], along4[0], th[0],
-                         y[0]);
         finish(g, along4, th, y, x, yy);
       }
     }
@@ -560,13 +573,19 @@ hipError_t launch_back(const PromptScanArgs &a, hipStream_t s) {
   const int wide = scan_wide(a.dim);
   const dim3 grid(static_cast<uint32_t>(a.q.slots * wide));
   const int64_t tokens = a.q.L * (a.q.off != nullptr ? 1 : a.q.nseq);
-  if (a.z != nullptr) {
-    scan_marks_kernel<T, true><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
-    scan_back_kernel<T, true><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
-  } else {
-    scan_marks_kernel<T, false><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
-    scan_back_kernel<T, false><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
-  }
+  const bool places = a.n < 16 || a.dim % (16 * kScanWaves) != 0;
+  const auto both = [&](auto gate) {
+    constexpr bool GATE = decltype(gate)::value;
+    scan_marks_kernel<T, GATE><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
+    if (places)
+      scan_back_kernel<T, GATE, true><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
+    else
+      scan_back_kernel<T, GATE, false><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
+  };
+  if (a.z != nullptr)
+    both(std::true_type());
+  else
+    both(std::false_type());
   const int64_t sums = (tokens * 2 * a.n + 255) / 256, most = 1 << 16;
   scan_back_sum_kernel<T><<<static_cast<uint32_t>(sums < most ? sums : most), 256, 0, s>>>(a, wide, tokens);
   return hipGetLastError();

@@ -164,3 +164,45 @@ def test_gradients_at_bad_last_tokens_of_packed_sequences():
     for end, ch in ((6, 1), (15, 2), (19, 3)):
         put(s, "u", (0, end - 1, ch), NAN)
     check_backward(s)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 5, 8, 16])
+@pytest.mark.parametrize("batch,seqlen,dim", [*SHAPES, (1, 7, 1)])
+def test_gradients_at_infinite_tokens(batch, seqlen, dim, n, dtype):
+    """Places past the last state and lanes past the last channel take no part in any sum."""
+    def case():
+        return mild(Scan(seqlen + n, batch, seqlen, dim, n, dtype, gate=dim != 33))
+
+    where = (batch - 1, seqlen // 2)
+    for name in ("u", "delta"):
+        s = case()
+        put(s, name, (*where, dim // 2), INF)
+        check_backward(s)
+    s = case()
+    s.dout[(*where, dim // 2)] = -INF
+    check_backward(s)
+    for name in ("B", "C"):
+        s = case()
+        put(s, name, (*where, n - 1), INF)
+        check_backward(s)
+
+
+@pytest.mark.parametrize("value", [NAN, INF])
+@pytest.mark.parametrize("n", [1, 5, 8])
+@pytest.mark.parametrize("seqlen", [1, 5, 8, 130])
+def test_gradients_at_a_bad_last_token_of_few_states(seqlen, n, value):
+    s = mild(Scan(seqlen, 2, seqlen, 20, n, "f32"))
+    put(s, "u", (1, seqlen - 1, 2), value)
+    check_backward(s)
+    s = mild(Scan(seqlen, 2, seqlen, 20, n, "f32"))
+    s.dstate[0, 4] = value
+    check_backward(s)
+
+
+@pytest.mark.parametrize("n", [1, 16])
+def test_gradients_at_infinite_tokens_over_chunks(n):
+    s = mild(Scan(23, 1, 700, 20, n, "f32", bias=False))
+    put(s, "u", (0, 3, 5), INF)
+    put(s, "B", (0, 350, 0), INF)
+    check_backward(s)
