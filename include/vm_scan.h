@@ -664,7 +664,8 @@ int64_t vm_clip_grad_workspace(int64_t count);
  *                           they read to [0, seqlen], and with other offsets the
  *                           results are undefined but no access leaves the tensors).
  *                           A sequence may be empty; its state stays its first.
- *                           Tokens behind the last sequence are not written.
+ *                           Tokens behind the last sequence are not written (with
+ *                           VM_CLEAR_REST: zeros are).
  *   slots    [n] int32      where in h0 and state (both of n_slots states) each
  *                           sequence's state lies; NULL: sequence i has state i, of n.
  *                           A sequence whose slot is outside [0, n_slots) starts from
@@ -673,7 +674,14 @@ int64_t vm_clip_grad_workspace(int64_t count);
  *   fresh    [n] int32      nonzero: the sequence starts from zero though h0 is given;
  *                           NULL: none does
  * The backward calls take offsets only (slots or fresh: VM_ERR_FLAG).
+ *
+ * VM_CLEAR_REST, beside the other options of a scan over prompts or added to a
+ * convolution's silu: the rows behind the last sequence are set to zero in every
+ * output of a call that holds rows of tokens.  In buffers that are new to each call
+ * they would hold whatever was there, which a sum over all rows takes up.  (The calls
+ * on single tokens have no such rows: VM_ERR_FLAG.)
  */
+enum { VM_CLEAR_REST = 16 };
 typedef struct vm_sequences {
   const int32_t *offsets;
   const int32_t *slots;
@@ -684,7 +692,7 @@ typedef struct vm_sequences {
 
 /*
  * Depthwise causal convolution over rows of tokens, with SiLU (silu = 1) or
- * without: with x before a sequence's first token from its kept window,
+ * without (0): with x before a sequence's first token from its kept window,
  *   v_t = bias + sum_k w_k x_{t-width+1+k},   out_t = SiLU(v_t) or v_t
  *   x [batch, seqlen, dim] (dtype), token stride x_stride; w [dim, width], bias
  *   [dim] (NULL = 0) fp32; out dense.
@@ -712,8 +720,8 @@ typedef struct vm_conv_grad {
  * Backward pass of vm_prompt_conv: the gradients of
  * L = sum(dout * out) + sum(dstate * state) for the same arguments.
  *   dout [batch, seqlen, dim] (dtype), dense; dstate [n, width - 1, dim] (dtype) or
- *   NULL (= 0).  Gradients of tokens of no sequence are not written.  Sums are
- *   formed in a fixed order (deterministic).
+ *   NULL (= 0).  Gradients of tokens of no sequence are not written (with
+ *   VM_CLEAR_REST: they are 0).  Sums are formed in a fixed order (deterministic).
  */
 int vm_prompt_conv_bwd(const vm_sequences *q, const void *x, int64_t x_stride,
                        const float *w, const float *bias, const void *h0,
@@ -771,8 +779,8 @@ typedef struct vm_scan_rows {
  *   out_t = y_t SiLU(z_t)  (z != NULL),  y_t otherwise
  *   h0, state [n or n_slots, dim, dstate] fp32: first and last states; NULL = 0 /
  *   not kept.  state may be h0 itself, but must not overlap it otherwise.
- *   out [batch, seqlen, dim] (dtype), dense.  options: VM_DELTA_SOFTPLUS or 0 (the
- *   write is dt; VM_ZOH is VM_ERR_FLAG).
+ *   out [batch, seqlen, dim] (dtype), dense.  options: VM_DELTA_SOFTPLUS or 0,
+ *   VM_CLEAR_REST (the write is dt; VM_ZOH is VM_ERR_FLAG).
  * dstate in [1, 16], dim up to 2^22, token strides below 2^23 elements
  * (VM_ERR_UNSUPPORTED).  Long sequences of few channels are walked in chunks at
  * once, whose states need a workspace (vm_prompt_scan_workspace; 0 bytes where
@@ -812,9 +820,9 @@ typedef struct vm_rows_grad {
  * Backward pass of vm_prompt_scan: the gradients of
  * L = sum(dout * out) + sum(dstate * state) for the same arguments.
  *   dout [batch, seqlen, dim] (dtype), dense; dstate [n, dim, N] or NULL (= 0).
- * Gradients of tokens of no sequence are not written.  Outputs must not overlap any
- * input or each other.  Sums over channels, rows and chunks are formed in a fixed
- * order (deterministic).
+ * Gradients of tokens of no sequence are not written (with VM_CLEAR_REST: they are
+ * 0).  Outputs must not overlap any input or each other.  Sums over channels, rows
+ * and chunks are formed in a fixed order (deterministic).
  */
 int vm_prompt_scan_bwd(const vm_scan_rows *p, const vm_sequences *q,
                        const float *h0, const void *dout, const float *dstate,

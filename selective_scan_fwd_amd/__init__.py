@@ -35,6 +35,7 @@ VM_F32, VM_BF16 = 0, 1
 VM_DELTA_SOFTPLUS, VM_ZOH = 1, 2
 VM_NORM_L2, VM_ROPE_INTERLEAVED = 1, 2
 VM_NORM_CENTER, VM_NORM_GATE_FIRST = 4, 8
+VM_CLEAR_REST = 16
 VM_OK = 0
 STATUS_NAMES = {0: "VM_OK", 1: "VM_ERR_NULL", 2: "VM_ERR_SHAPE", 3: "VM_ERR_DTYPE", 4: "VM_ERR_FLAG",
                 5: "VM_ERR_ALIAS", 6: "VM_ERR_UNSUPPORTED", 7: "VM_ERR_HIP", 8: "VM_ERR_ALLOC"}
@@ -1012,6 +1013,11 @@ def _sequences(batch, offsets, slots, fresh, h0, state, index):
                        kept), n, kept
 
 
+def _clear(offsets, new=True):
+    """Packed rows in new outputs: what lies behind the last sequence is set to 0."""
+    return VM_CLEAR_REST if new and offsets is not None else 0
+
+
 def _three(t, name):
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{name} must be a [batch, seqlen, channels] tensor")
@@ -1034,13 +1040,15 @@ def vm_prompt_conv(x, w, bias=None, silu=True, h0=None, state=None, want_state=F
     want_state or a buffer is given.  offsets (int32 [n + 1], batch 1): sequence i is
     tokens offsets[i] .. offsets[i + 1] - 1.  slots (int32 [n]): h0 and state are
     pools [n_slots, ...] and each sequence's lies there (outside: starts from 0, not
-    kept; no two alike).  fresh (int32 [n]): nonzero = starts from 0."""
+    kept; no two alike).  fresh (int32 [n]): nonzero = starts from 0.  Rows behind the
+    last sequence are 0 in a new out and stay as they are in the caller's."""
     batch, L, dim = _three(x, "x").shape
     width = _conv_weights(w, dim)
     index, dtype = x.get_device(), x.dtype
     px, xs = _row_tensor(x, "x", dtype, (batch, L, dim), index)
     seq, n, kept = _sequences(batch, offsets, slots, fresh, h0, state, index)
     shape = (kept, width - 1, dim)
+    clear = _clear(offsets, out is None)
     out, po = _out(out, "out", x, dtype, (batch, L, dim), index)
     if state is None and want_state:
         if slots is not None:
@@ -1048,14 +1056,15 @@ def vm_prompt_conv(x, w, bias=None, silu=True, h0=None, state=None, want_state=F
         state = torch.empty(shape, dtype=dtype, device=x.device)
     _launch("vm_prompt_conv", index, seq, px, xs, _float_arg(w, "w", (dim, width), index),
             _float_arg(bias, "bias", (dim,), index), _arg(h0, "h0", dtype, shape, index),
-            _arg(state, "state", dtype, shape, index), po, batch, L, dim, width, int(bool(silu)), _dtype_code(x))
+            _arg(state, "state", dtype, shape, index), po, batch, L, dim, width, int(bool(silu)) | clear,
+            _dtype_code(x))
     return out, state
 
 
 def vm_prompt_conv_bwd(x, w, dout, bias=None, silu=True, h0=None, dstate=None, offsets=None):
     """Gradients of sum(dout * out) + sum(dstate * state) of vm_prompt_conv.
-    Returns a dict: x (dense, in its dtype), w, bias (fp32, with bias) and, when h0
-    is given, h0."""
+    Returns a dict: x (dense, in its dtype; 0 behind the last sequence), w, bias (fp32,
+    with bias) and, when h0 is given, h0."""
     batch, L, dim = _three(x, "x").shape
     width = _conv_weights(w, dim)
     index, dtype = x.get_device(), x.dtype
@@ -1074,7 +1083,7 @@ def vm_prompt_conv_bwd(x, w, dout, bias=None, silu=True, h0=None, dstate=None, o
     _launch("vm_prompt_conv_bwd", index, seq, px, xs, _float_arg(w, "w", (dim, width), index),
             _float_arg(bias, "bias", (dim,), index), _arg(h0, "h0", dtype, shape, index),
             _arg(dout, "dout", dtype, (batch, L, dim), index), _arg(dstate, "dstate", dtype, shape, index), grads, batch, L,
-            dim, width, int(bool(silu)), _dtype_code(x), wp, wn)
+            dim, width, int(bool(silu)) | _clear(offsets), _dtype_code(x), wp, wn)
     return d
 
 
@@ -1123,10 +1132,12 @@ def vm_prompt_scan(u, delta, A, B, C, D=None, delta_bias=None, z=None, delta_sof
     [batch, L, dim]; B, C: [batch, L, N] (fp32 or bf16; slices of a projection's row
     are read in place); A: [dim, N], D, delta_bias: [dim] fp32.  h0, state: [n, dim,
     N] fp32; state (the last states, may be h0 itself) is None unless want_state or a
-    buffer is given.  offsets, slots and fresh as in vm_prompt_conv.  out is dense."""
+    buffer is given.  offsets, slots, fresh and what lies behind the last sequence as in
+    vm_prompt_conv.  out is dense."""
     batch, L, dim = _three(u, "u").shape
     p, index, dim, N = _scan_rows(u, delta, A, B, C, D, delta_bias, z)
     seq, n, kept = _sequences(batch, offsets, slots, fresh, h0, state, index)
+    clear = _clear(offsets, out is None)
     out, po = _out(out, "out", u, u.dtype, (batch, L, dim), index)
     if state is None and want_state:
         if slots is not None:
@@ -1135,15 +1146,15 @@ def vm_prompt_scan(u, delta, A, B, C, D=None, delta_bias=None, z=None, delta_sof
     ws, wp, wn = _workspace(load_library().vm_prompt_scan_workspace(batch, L, n, dim, N, offsets is not None, 0), u.device)
     _launch("vm_prompt_scan", index, p, seq, _float_arg(h0, "h0", (kept, dim, N), index),
             _float_arg(state, "state", (kept, dim, N), index), po, batch, L, dim, N, _dtype_code(u),
-            _options(delta_softplus, False), wp, wn)
+            _options(delta_softplus, False) | clear, wp, wn)
     return out, state
 
 
 def vm_prompt_scan_bwd(u, delta, A, B, C, dout, D=None, delta_bias=None, z=None, delta_softplus=True, h0=None, dstate=None,
                        offsets=None):
     """Gradients of sum(dout * out) + sum(dstate * state) of vm_prompt_scan.
-    Returns a dict: u, delta, B, C and (with z) z, dense in their dtype; A and, where
-    given, D, delta_bias, h0 in fp32."""
+    Returns a dict: u, delta, B, C and (with z) z, dense in their dtype (0 behind the
+    last sequence); A and, where given, D, delta_bias, h0 in fp32."""
     batch, L, dim = _three(u, "u").shape
     p, index, dim, N = _scan_rows(u, delta, A, B, C, D, delta_bias, z)
     seq, n, _ = _sequences(batch, offsets, None, None, h0, None, index)
@@ -1164,7 +1175,7 @@ def vm_prompt_scan_bwd(u, delta, A, B, C, dout, D=None, delta_bias=None, z=None,
     ws, wp, wn = _workspace(load_library().vm_prompt_scan_workspace(batch, L, n, dim, N, offsets is not None, 1), u.device)
     _launch("vm_prompt_scan_bwd", index, p, seq, _float_arg(h0, "h0", (n, dim, N), index),
             _arg(dout, "dout", dt, (batch, L, dim), index), _float_arg(dstate, "dstate", (n, dim, N), index), grads, batch, L,
-            dim, N, _dtype_code(u), _options(delta_softplus, False), wp, wn)
+            dim, N, _dtype_code(u), _options(delta_softplus, False) | _clear(offsets), wp, wn)
     return d
 
 

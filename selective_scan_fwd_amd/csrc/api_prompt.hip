@@ -32,9 +32,10 @@ constexpr int64_t kMaxDim = int64_t{1} << 22;
 bool type_ok(int dtype) { return dtype == VM_F32 || dtype == VM_BF16; }
 int size_of(int dtype) { return dtype == VM_BF16 ? 2 : 4; }
 
-// A call's sequences; `kept` elements of all kept states of `each` elements.
-int check_sequences(const vm_sequences *q, int64_t batch, int64_t seqlen, bool pool, int64_t each, vmk::SeqArgs *s,
-                    int64_t *kept) {
+// A call's sequences over rows of `dim` values; `kept` elements of all kept states of `each`
+// elements.
+int check_sequences(const vm_sequences *q, int64_t batch, int64_t seqlen, int64_t dim, bool pool, int64_t each, int clear,
+                    vmk::SeqArgs *s, int64_t *kept) {
   int64_t tokens = 0;
   if (!dims_ok({batch, seqlen}, &tokens)) return VM_ERR_SHAPE;
   const int64_t n = q != nullptr ? q->n : batch;
@@ -48,6 +49,7 @@ int check_sequences(const vm_sequences *q, int64_t batch, int64_t seqlen, bool p
   if (!dims_ok({n}, &unused) || !dims_ok({s->kept, each}, kept)) return VM_ERR_SHAPE;
   s->nseq = static_cast<int>(n);
   s->L = seqlen;
+  s->clear = clear != 0 && s->off != nullptr ? vmk::clear_blocks(seqlen, dim) : 0;
   return VM_OK;
 }
 int64_t all_tokens(const vmk::SeqArgs &s) { return s.off != nullptr ? s.L : s.L * s.nseq; }
@@ -69,25 +71,27 @@ struct SeqSpans {
 int check_conv(const vm_sequences *q, bool pool, const void *x, int64_t x_stride, const float *w, int64_t batch, int64_t seqlen,
                int64_t dim, int64_t width, int silu, int dtype, vmk::PromptConvArgs *a, int64_t *ext, int64_t *kept) {
   if (!type_ok(dtype)) return VM_ERR_DTYPE;
-  if (silu != 0 && silu != 1) return VM_ERR_FLAG;
+  if ((silu & ~(1 | VM_CLEAR_REST)) != 0) return VM_ERR_FLAG;
   if (x == nullptr || w == nullptr) return VM_ERR_NULL;
   a->xs = x_stride;
   int64_t each = 0;
   if (!token_extent(batch, seqlen, 1, dim, &a->xs, ext)) return VM_ERR_SHAPE;
   if (width < 2 || width > vmk::kMaxTaps) return VM_ERR_UNSUPPORTED;
   if (!dims_ok({width - 1, dim}, &each)) return VM_ERR_SHAPE;
-  const int st = check_sequences(q, batch, seqlen, pool, each, &a->q, kept);
+  const int st = check_sequences(q, batch, seqlen, dim, pool, each, silu & VM_CLEAR_REST, &a->q, kept);
   if (st != VM_OK) return st;
   if (dim > kMaxDim) return VM_ERR_UNSUPPORTED;
   a->x = x;
   a->w = w;
   a->dim = static_cast<int>(dim);
   a->width = static_cast<int>(width);
-  a->silu = silu;
+  a->silu = silu & 1;
   return VM_OK;
 }
 // (a lane to each channel and chunk, where rows are not whole pieces, in whole waves)
-bool conv_fits(const vmk::SeqArgs &q, int64_t dim) { return q.slots <= (kMaxBlocks * 256) / (((dim + 63) / 64 + 3) * 64); }
+bool conv_fits(const vmk::SeqArgs &q, int64_t dim) {
+  return q.slots <= ((kMaxBlocks - q.clear) * 256) / (((dim + 63) / 64 + 3) * 64);
+}
 
 int64_t conv_partial(const vmk::PromptConvArgs &a) {
   return Parts::whole(static_cast<int64_t>(a.workers) * (a.width + 1) * a.dim * 4);
@@ -99,9 +103,9 @@ struct ScanExtents {
 };
 
 int check_rows(const vm_scan_rows *p, int64_t batch, int64_t seqlen, int64_t dim, int64_t dstate, int dtype, int options,
-               vmk::PromptScanArgs *a, ScanExtents *e) {
+               int allowed, vmk::PromptScanArgs *a, ScanExtents *e) {
   if (!type_ok(dtype)) return VM_ERR_DTYPE;
-  if ((options & ~VM_DELTA_SOFTPLUS) != 0) return VM_ERR_FLAG;
+  if ((options & ~allowed) != 0) return VM_ERR_FLAG;
   if (p == nullptr || p->u == nullptr || p->delta == nullptr || p->A == nullptr || p->B == nullptr || p->C == nullptr)
     return VM_ERR_NULL;
   a->us = p->u_stride;
@@ -132,7 +136,7 @@ int check_rows(const vm_scan_rows *p, int64_t batch, int64_t seqlen, int64_t dim
   return VM_OK;
 }
 
-bool scan_fits(const vmk::PromptScanArgs &a) { return a.q.slots <= kMaxBlocks / vmk::scan_wide(a.dim); }
+bool scan_fits(const vmk::PromptScanArgs &a) { return a.q.slots <= (kMaxBlocks - a.q.clear) / vmk::scan_wide(a.dim); }
 
 // Temporary memory of the forward and of the backward pass.
 void scan_parts(vmk::PromptScanArgs &a, bool back, Parts &parts) {
@@ -320,8 +324,9 @@ int vm_prompt_scan(const vm_scan_rows *p, const vm_sequences *q, const float *h0
                    int64_t workspace_bytes, void *stream) {
   vmk::PromptScanArgs a = {};
   ScanExtents e = {};
-  int st = check_rows(p, batch, seqlen, dim, dstate, dtype, options, &a, &e);
-  if (st == VM_OK) st = check_sequences(q, batch, seqlen, true, dim * dstate, &a.q, &e.kept);
+  int st = check_rows(p, batch, seqlen, dim, dstate, dtype, options, VM_DELTA_SOFTPLUS | VM_CLEAR_REST, &a, &e);
+  if (st == VM_OK)
+    st = check_sequences(q, batch, seqlen, dim, true, dim * dstate, options & VM_CLEAR_REST, &a.q, &e.kept);
   if (st != VM_OK) return st;
   if (out == nullptr) return VM_ERR_NULL;
   const int es = size_of(dtype);
@@ -374,8 +379,8 @@ int vm_prompt_scan_bwd(const vm_scan_rows *p, const vm_sequences *q, const float
                        void *workspace, int64_t workspace_bytes, void *stream) {
   vmk::PromptScanArgs a = {};
   ScanExtents e = {};
-  int st = check_rows(p, batch, seqlen, dim, N, dtype, options, &a, &e);
-  if (st == VM_OK) st = check_sequences(q, batch, seqlen, false, dim * N, &a.q, &e.kept);
+  int st = check_rows(p, batch, seqlen, dim, N, dtype, options, VM_DELTA_SOFTPLUS | VM_CLEAR_REST, &a, &e);
+  if (st == VM_OK) st = check_sequences(q, batch, seqlen, dim, false, dim * N, options & VM_CLEAR_REST, &a.q, &e.kept);
   if (st != VM_OK) return st;
   if (dout == nullptr || g == nullptr || g->du == nullptr || g->ddelta == nullptr || g->dA == nullptr || g->dB == nullptr ||
       g->dC == nullptr || (g->dz == nullptr) != (p->z == nullptr))
@@ -420,7 +425,7 @@ int vm_token_scan(const vm_scan_rows *p, float *state, const int32_t *slots, voi
                   int64_t dim, int64_t dstate, int dtype, int options, void *stream) {
   vmk::PromptScanArgs r = {};
   ScanExtents e = {};
-  const int st = check_rows(p, batch, 1, dim, dstate, dtype, options, &r, &e);
+  const int st = check_rows(p, batch, 1, dim, dstate, dtype, options, VM_DELTA_SOFTPLUS, &r, &e);
   if (st != VM_OK) return st;
   if (state == nullptr || out == nullptr) return VM_ERR_NULL;
   if (!dims_ok({n_slots, dim, dstate}, &e.kept) || (slots == nullptr && batch > n_slots)) return VM_ERR_SHAPE;

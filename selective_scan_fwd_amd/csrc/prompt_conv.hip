@@ -111,6 +111,10 @@ __device__ __forceinline__ void window_before(const void *in, int64_t xs, int c,
 template <typename T, int W, int V>
 __global__ __launch_bounds__(kThreads) void prompt_conv_kernel(PromptConvArgs a, uint32_t wide) {
   const int64_t slot = blockIdx.x / wide;
+  if (slot >= a.q.slots) {
+    clear_rest<T>(a.q, a.out, a.dim, blockIdx.x - a.q.slots * wide);
+    return;
+  }
   const int c = static_cast<int>((blockIdx.x % wide) * blockDim.x + threadIdx.x) * V;
   const Piece p = piece_of(a.q, slot);
   if (p.len < 0 || c >= a.dim) return;
@@ -161,6 +165,10 @@ __global__ __launch_bounds__(kThreads) void prompt_conv_kernel(PromptConvArgs a,
 template <typename T, int W, int V>
 __global__ __launch_bounds__(kThreads) void prompt_conv_back_kernel(PromptConvArgs a, uint32_t wide) {
   const int64_t worker = blockIdx.x / wide;
+  if (worker >= a.workers) {
+    clear_rest<T>(a.q, a.dx, a.dim, blockIdx.x - static_cast<int64_t>(a.workers) * wide);
+    return;
+  }
   const int at0 = static_cast<int>((blockIdx.x % wide) * blockDim.x + threadIdx.x) * V;
   const bool live = at0 < a.dim;
   const int c = live ? at0 : 0;               // (lanes past the channels stay for the search, and do no work)
@@ -300,14 +308,14 @@ template <typename T, int V>
 hipError_t launch_fwd(const PromptConvArgs &a, hipStream_t s) {
   const Cut z = cut(a.dim / V);
   return by_width<T, V>(a.width, [&](auto w) {
-    prompt_conv_kernel<T, decltype(w)::value, V><<<static_cast<uint32_t>(a.q.slots * z.wide), z.threads, 0, s>>>(a, z.wide);
+    prompt_conv_kernel<T, decltype(w)::value, V><<<static_cast<uint32_t>(a.q.slots * z.wide + a.q.clear), z.threads, 0, s>>>(a, z.wide);
   });
 }
 template <typename T, int V>
 hipError_t launch_bwd(const PromptConvArgs &a, hipStream_t s) {
   const Cut z = cut(a.dim / V);
   return by_width<T, V>(a.width, [&](auto w) {
-    prompt_conv_back_kernel<T, decltype(w)::value, V><<<static_cast<uint32_t>(a.workers) * z.wide, z.threads, 0, s>>>(a, z.wide);
+    prompt_conv_back_kernel<T, decltype(w)::value, V><<<static_cast<uint32_t>(a.workers) * z.wide + a.q.clear, z.threads, 0, s>>>(a, z.wide);
   });
 }
 template <typename T, int V>

@@ -134,6 +134,26 @@ __device__ __forceinline__ Piece piece_by_length(const SeqArgs &q, int64_t slot)
   return uniform(p);
 }
 
+// Sets the rows of `dim` values behind the last sequence to 0, by workgroup `block` of a launch's
+// q.clear last ones.
+template <typename T>
+__device__ __forceinline__ void clear_rest(const SeqArgs &q, void *out, int64_t dim, int64_t block) {
+  if (out == nullptr) return;
+  T *p = static_cast<T *>(out);
+  const int64_t first = clamped(q.off[q.nseq], q.L) * dim, end = q.L * dim, step = static_cast<int64_t>(q.clear) * blockDim.x;
+  const int64_t me = block * blockDim.x + threadIdx.x;
+  // whole pieces of 16 bytes, and what is left on either side of them
+  constexpr int64_t kEach = 16 / sizeof(T);
+  const int64_t skew = static_cast<int64_t>((reinterpret_cast<uintptr_t>(p + first) & 15) / sizeof(T));
+  int64_t from = first + (skew != 0 ? kEach - skew : 0);
+  from = from < end ? from : end;
+  const int64_t pieces = (end - from) / kEach, to = from + pieces * kEach;
+  typedef uint32_t Piece16 __attribute__((ext_vector_type(4)));
+  for (int64_t i = me; i < pieces; i += step) reinterpret_cast<Piece16 *>(p + from)[i] = Piece16{0, 0, 0, 0};
+  if (me < from - first) p[first + me] = T(0);
+  if (me < end - to) p[to + me] = T(0);
+}
+
 // Where a sequence's state is kept, -1: nowhere.
 __device__ __forceinline__ int64_t kept_at(const SeqArgs &q, int seq) {
   const int64_t s = q.where != nullptr ? q.where[seq] : seq;

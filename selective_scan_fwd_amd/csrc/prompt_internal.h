@@ -23,7 +23,16 @@ struct SeqArgs {
   int64_t slots;             // chunks of the launch
   int64_t kept;              // number of kept states
   int nseq;
+  int clear;                 // workgroups behind a launch's others that clear rows of no sequence
 };
+// Those workgroups for rows of `dim` values: one to 8192 of them, as no launch of its own is
+// wanted for what is mostly little or nothing.  40 packed prompts of 4096 channels, 8187 tokens in
+// all: 1 us with nothing to clear; as many rows again cost the convolution 7 us, the scan 27.
+constexpr int kMostClear = 256;
+inline int clear_blocks(int64_t L, int64_t dim) {
+  const int64_t n = L * dim / 8192 + 1;
+  return static_cast<int>(n < kMostClear ? n : kMostClear);
+}
 int64_t seq_slots(int64_t nseq, int64_t L, int64_t chunk, bool packed);
 
 // ---------------------------------------------------- column sums

@@ -155,6 +155,10 @@ __global__ __launch_bounds__(64 * kScanWaves, PLACES ? 4 : 1) void prompt_scan_k
   const int blocks = (a.dim + 15) / 16, waves = blockDim.x / 64;
   const int wide = (blocks + waves - 1) / waves;
   int64_t slot = blockIdx.x / wide;
+  if (!SECOND && slot >= slots) {
+    clear_rest<T>(a.q, a.out, a.dim, blockIdx.x - slots * wide);
+    return;
+  }
   if (a.q.off != nullptr) {
     // by falling length: every other round of workgroups over the 256 compute units backwards, so
     // that the longest sequence of one round shares its units with the shortest of the next
@@ -229,7 +233,7 @@ hipError_t launch_scan(const PromptScanArgs &a, hipStream_t s) {
   const int64_t wide = (blocks + waves - 1) / waves;
   const bool packed = a.q.off != nullptr, many = a.ends != nullptr;
   const int64_t first = !packed && many ? a.q.slots - a.q.nseq : a.q.slots;
-  prompt_scan_kernel<T, GATE, PLACES, false><<<static_cast<uint32_t>(first * wide), 64 * waves, 0, s>>>(a, first);
+  prompt_scan_kernel<T, GATE, PLACES, false><<<static_cast<uint32_t>(first * wide + a.q.clear), 64 * waves, 0, s>>>(a, first);
   if (many) {
     // (40 packed prompts of one chunk each: 16 us to find nothing to do in all slots, 5 in these)
     const int64_t second = packed && a.q.nseq <= 64 ? a.q.L / a.q.chunk : first;

@@ -178,6 +178,10 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_marks_kernel(PromptScanA
   __shared__ __align__(16) float meets[kScanWaves][kGroups][16][12];
   const int lane = threadIdx.x % 64, blocks = (a.dim + 15) / 16;
   const int64_t slot = blockIdx.x / wide;
+  if (slot >= a.q.slots) {
+    for (void *rows : {a.du, a.ddelta, a.dz}) clear_rest<T>(a.q, rows, a.dim, blockIdx.x - a.q.slots * wide);
+    return;
+  }
   const int blk = uniform(static_cast<int>(blockIdx.x % wide) * kScanWaves + threadIdx.x / 64);
   if (blk >= blocks) return;
   const Piece p = piece_by_length(a.q, slot);
@@ -549,10 +553,10 @@ __global__ __launch_bounds__(64 * kScanWaves, 3) void scan_back_kernel(PromptSca
 template <typename T>
 __global__ __launch_bounds__(256) void scan_back_sum_kernel(PromptScanArgs a, int wide, int64_t tokens) {
   const int64_t per = tokens * 2 * a.n;
-  const int64_t end = a.q.off != nullptr ? clamped(a.q.off[a.q.nseq], a.q.L) * 2 * a.n : per;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x; i < end; i += gridDim.x * static_cast<int64_t>(256)) {
+  const int64_t end = a.q.off != nullptr ? clamped(a.q.off[a.q.nseq], a.q.L) * 2 * a.n : per, last = a.q.clear > 0 ? per : end;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x; i < last; i += gridDim.x * static_cast<int64_t>(256)) {
     float s = 0.0f;
-    int g = 0;
+    int g = i < end ? 0 : wide;              // (rows of no sequence: 0)
     for (; g + 8 <= wide; g += 8) {          // (eight loads under way)
       float v[8];
 #pragma unroll
@@ -576,7 +580,7 @@ hipError_t launch_back(const PromptScanArgs &a, hipStream_t s) {
   const bool places = a.n < 16 || a.dim % (16 * kScanWaves) != 0;
   const auto both = [&](auto gate) {
     constexpr bool GATE = decltype(gate)::value;
-    scan_marks_kernel<T, GATE><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
+    scan_marks_kernel<T, GATE><<<grid.x + a.q.clear, 64 * kScanWaves, 0, s>>>(a, wide);
     if (places)
       scan_back_kernel<T, GATE, true><<<grid, 64 * kScanWaves, 0, s>>>(a, wide);
     else

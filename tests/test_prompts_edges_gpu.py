@@ -206,3 +206,78 @@ def test_gradients_at_infinite_tokens_over_chunks(n):
     put(s, "u", (0, 3, 5), INF)
     put(s, "B", (0, 350, 0), INF)
     check_backward(s)
+
+
+# ------------------------------------------------ rows behind the last sequence
+class Filled:
+    """New tensors hold NaN (torch fills uninitialised memory in its deterministic mode)."""
+
+    def __enter__(self):
+        torch.use_deterministic_algorithms(True)
+        assert torch.isnan(torch.empty(8, device=DEV)).all()
+
+    def __exit__(self, *_):
+        torch.use_deterministic_algorithms(False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim,lens,rest", [(24, [3, 0, 20], 1), (24, [5], 300), (33, [0, 0], 7), (520, [70, 1, 130], 900),
+                                           (64, [1] * 70, 25), (64, [40, 41], 0)])
+def test_new_outputs_are_zero_behind_the_last_sequence(dtype, dim, lens, rest):
+    total, n = sum(lens), 8
+    s = Scan(total, 1, total + rest, dim, n, dtype, lens=lens)
+    x, w, bias = s.a["u"], dev(torch.ones(dim, 4)), dev(torch.ones(dim))
+    with Filled():
+        conv, _ = vm.vm_prompt_conv(x, w, bias, offsets=s.offsets)
+        dc = vm.vm_prompt_conv_bwd(x, w, s.dout, bias, offsets=s.offsets)
+        out, _ = vm.vm_prompt_scan(**s.a, offsets=s.offsets)
+        d = vm.vm_prompt_scan_bwd(**s.a, dout=s.dout, offsets=s.offsets)
+    for name, t in dict(conv=conv, conv_dx=dc["x"], out=out, **{k: d[k] for k in ("u", "delta", "B", "C", "z")}).items():
+        assert (t[:, total:] == 0).all(), name
+        assert torch.isfinite(t).all(), name
+
+
+def test_a_packed_row_with_room_left_through_a_block_backward():
+    """Sums over all rows of a packed buffer: what lies behind the last sequence adds nothing."""
+    import oracle.prompts as ref
+
+    lens, room, dim = [7, 0, 30], 11, 40
+    s = Scan(5, 1, sum(lens) + room, dim, 16, "f32", lens=lens)
+    x, w = s.a["u"], dev(0.3 * torch.ones(dim, 4))
+    gain, r = dev(1 + 0.1 * torch.arange(dim) / dim), s.a["z"].clone()
+    with Filled():
+        dc = vm.vm_prompt_conv_bwd(x, w, s.dout, offsets=s.offsets)
+        d = vm.vm_norm_before_bwd(dc["x"], r, gain)
+    want = ref.conv_grad(host(x), host(w), host(s.dout), offsets=s.offsets)["x"][0]
+    same(d["w"], ref.norm_before_grad(want, host(r)[0], host(gain))["w"], SUMS, "dw")
+
+
+def test_graph_of_packed_prompts_with_room_left():
+    """Where the sequences end is read when a graph runs: the rest of its own outputs is cleared then."""
+    dim, most = 64, 500
+    s = Scan(17, 1, most, dim, 16, "bf16", lens=[1] * 4)
+    x, w = s.a["u"], dev(torch.ones(dim, 4))
+    off = s.offsets.clone()
+
+    def run():
+        u, _ = vm.vm_prompt_conv(x, w, offsets=off)
+        d = vm.vm_prompt_scan_bwd(**dict(s.a, u=u), dout=s.dout, offsets=off)
+        dc = vm.vm_prompt_conv_bwd(x, w, d["u"], offsets=off)
+        return [u, vm.vm_prompt_scan(**dict(s.a, u=u), offsets=off)[0], d["u"], d["delta"], d["B"], d["C"], d["z"], dc["x"], dc["w"]]
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for ends in ([500, 500, 500, 500], [1, 2, 3, 4], [100, 100, 350, 499], [0, 0, 0, 0]):
+        off.copy_(torch.tensor([0] + ends))
+        want = [t.clone() for t in run()]
+        torch.cuda.synchronize()
+        graph.replay()
+        junk = torch.randn(1 << 20, device=DEV).sum()      # (the program's own work between)
+        torch.cuda.synchronize()
+        assert torch.isfinite(junk)
+        for i, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b) and torch.isfinite(a).all(), (ends, i)
+            assert i == 8 or (a[:, ends[-1]:] == 0).all(), (ends, i)
