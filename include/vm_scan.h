@@ -833,8 +833,8 @@ int vm_prompt_scan_bwd(const vm_scan_rows *p, const vm_sequences *q,
 /*
  * One token of the selective scan for every row of a batch, on states that are
  * kept: the rows of p with seqlen 1; state [n_slots, dim, dstate] fp32 is updated
- * in place; out [batch, dim] (dtype), dense; slots as for vm_token_conv.  One
- * launch, no temporary memory.
+ * in place; out [batch, dim] (dtype), dense; slots as for vm_token_conv.  (Rows may
+ * lie as far apart as 2^31 - 1 elements.)  One launch, no temporary memory.
  */
 int vm_token_scan(const vm_scan_rows *p, float *state, const int32_t *slots,
                   void *out, int64_t batch, int64_t n_slots, int64_t dim,

@@ -23,7 +23,7 @@ using vmk::span;
 using vmk::token_extent;
 
 constexpr int64_t kMaxState = 16, kMaxNorm = 16384;
-// Token strides: a tile's rows are reached with 31-bit byte offsets.
+// Token strides of prompts: a tile's rows are reached with 31-bit byte offsets.
 constexpr int64_t kMaxStride = (int64_t{1} << 23) - 1;
 // Workgroups of 256 work-items, of which a launch holds less than 2^32.
 constexpr int64_t kMaxBlocks = (int64_t{1} << 24) - 1;
@@ -103,7 +103,7 @@ struct ScanExtents {
 };
 
 int check_rows(const vm_scan_rows *p, int64_t batch, int64_t seqlen, int64_t dim, int64_t dstate, int dtype, int options,
-               int allowed, vmk::PromptScanArgs *a, ScanExtents *e) {
+               int allowed, int64_t most_stride, vmk::PromptScanArgs *a, ScanExtents *e) {
   if (!type_ok(dtype)) return VM_ERR_DTYPE;
   if ((options & ~allowed) != 0) return VM_ERR_FLAG;
   if (p == nullptr || p->u == nullptr || p->delta == nullptr || p->A == nullptr || p->B == nullptr || p->C == nullptr)
@@ -121,7 +121,7 @@ int check_rows(const vm_scan_rows *p, int64_t batch, int64_t seqlen, int64_t dim
     return VM_ERR_SHAPE;
   if (dstate > kMaxState || dim > kMaxDim) return VM_ERR_UNSUPPORTED;
   for (int64_t s : {a->us, a->ds, a->bs, a->cs, a->zs})
-    if (s > kMaxStride) return VM_ERR_UNSUPPORTED;
+    if (s > most_stride) return VM_ERR_UNSUPPORTED;
   a->u = p->u;
   a->delta = p->delta;
   a->A = p->A;
@@ -324,7 +324,7 @@ int vm_prompt_scan(const vm_scan_rows *p, const vm_sequences *q, const float *h0
                    int64_t workspace_bytes, void *stream) {
   vmk::PromptScanArgs a = {};
   ScanExtents e = {};
-  int st = check_rows(p, batch, seqlen, dim, dstate, dtype, options, VM_DELTA_SOFTPLUS | VM_CLEAR_REST, &a, &e);
+  int st = check_rows(p, batch, seqlen, dim, dstate, dtype, options, VM_DELTA_SOFTPLUS | VM_CLEAR_REST, kMaxStride, &a, &e);
   if (st == VM_OK)
     st = check_sequences(q, batch, seqlen, dim, true, dim * dstate, options & VM_CLEAR_REST, &a.q, &e.kept);
   if (st != VM_OK) return st;
@@ -379,7 +379,7 @@ int vm_prompt_scan_bwd(const vm_scan_rows *p, const vm_sequences *q, const float
                        void *workspace, int64_t workspace_bytes, void *stream) {
   vmk::PromptScanArgs a = {};
   ScanExtents e = {};
-  int st = check_rows(p, batch, seqlen, dim, N, dtype, options, VM_DELTA_SOFTPLUS | VM_CLEAR_REST, &a, &e);
+  int st = check_rows(p, batch, seqlen, dim, N, dtype, options, VM_DELTA_SOFTPLUS | VM_CLEAR_REST, kMaxStride, &a, &e);
   if (st == VM_OK) st = check_sequences(q, batch, seqlen, dim, false, dim * N, options & VM_CLEAR_REST, &a.q, &e.kept);
   if (st != VM_OK) return st;
   if (dout == nullptr || g == nullptr || g->du == nullptr || g->ddelta == nullptr || g->dA == nullptr || g->dB == nullptr ||
@@ -425,7 +425,7 @@ int vm_token_scan(const vm_scan_rows *p, float *state, const int32_t *slots, voi
                   int64_t dim, int64_t dstate, int dtype, int options, void *stream) {
   vmk::PromptScanArgs r = {};
   ScanExtents e = {};
-  const int st = check_rows(p, batch, 1, dim, dstate, dtype, options, VM_DELTA_SOFTPLUS, &r, &e);
+  const int st = check_rows(p, batch, 1, dim, dstate, dtype, options, VM_DELTA_SOFTPLUS, vmk::kMaxElems, &r, &e);
   if (st != VM_OK) return st;
   if (state == nullptr || out == nullptr) return VM_ERR_NULL;
   if (!dims_ok({n_slots, dim, dstate}, &e.kept) || (slots == nullptr && batch > n_slots)) return VM_ERR_SHAPE;

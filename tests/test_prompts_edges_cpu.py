@@ -41,3 +41,13 @@ def test_the_rest_of_a_packed_row_is_cleared_only_where_there_is_one(lib):
     assert conv(clear, None) == NULL and conv(1 | clear, None) == NULL and conv(2 | clear, None) == FLAG
     assert token_scan(lib, rows(), options=clear) == FLAG and token_scan(lib, rows(), options=1 | clear) == FLAG
     assert lib.vm_token_conv(at(0), 0, at(4), at(5), at(1), at(2), at(3), 2, 3, 32, 4, 1 | clear, 0, None) == FLAG
+
+
+def test_rows_of_single_tokens_may_lie_far_apart(lib):
+    """Only prompts have a limit on token strides (the call then fails at its next check, that of overlaps)."""
+    for name in ("u_stride", "delta_stride", "B_stride", "C_stride", "z_stride"):
+        far = rows(**{name: 1 << 27})
+        assert token_scan(lib, far, out=at(10)) == ALIAS
+        assert lib.vm_prompt_scan(far, None, None, None, at(12), 2, 8, 32, 16, 0, 1, None, 0, None) == UNSUPPORTED
+    # the rows' whole extent is what must not meet an output
+    assert token_scan(lib, rows(u_stride=1 << 30), out=at(0) + 2 * 3 * (1 << 30)) == ALIAS

@@ -281,3 +281,26 @@ def test_graph_of_packed_prompts_with_room_left():
         for i, (a, b) in enumerate(zip(got, want)):
             assert torch.equal(a, b) and torch.isfinite(a).all(), (ends, i)
             assert i == 8 or (a[:, ends[-1]:] == 0).all(), (ends, i)
+
+
+# ------------------------------------------------------------ far apart rows
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_single_tokens_far_apart(dtype):
+    """The last token of every row of a long buffer, read in place (rows 2^23 values and more apart)."""
+    batch, seqlen, dim, n = 3, 4096, 64, 16
+    wide = 2 * dim + 2 * n + (1 << 23) // seqlen
+    s = Scan(4, batch, 1, dim, n, dtype)
+    row = torch.zeros(batch, seqlen, wide, device=DEV, dtype=s.dtype)
+    names, at = ("u", "z", "B", "C"), 0
+    a = {k: v if v is None or k in ("A", "D", "delta_bias") else v[:, 0] for k, v in s.a.items()}
+    for k in names:
+        size = a[k].shape[-1]
+        row[:, -1, at: at + size] = a[k]
+        a[k] = row[:, -1, at: at + size]
+        at += size
+    assert a["u"].stride(0) >= 1 << 23
+    state = s.h0.clone()
+    out = vm.vm_token_scan(**a, state=state)
+    want, last, _ = s.ref(list(host(s.h0)))
+    same(out, want[:, 0], tol(out), "out")
+    same(state, last, F32, "state")
