@@ -130,18 +130,30 @@ __device__ __forceinline__ void mark_chunk(const PromptScanArgs &a, const Lane &
       if (l.q == 0) *before = steps;
       before += blocks * 16;
     }
-    float mine = 0.0f;
+    float mine = 0.0f, size = 0.0f;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const float dt = step_of(a, r.d[g] + bias, 4 * g + l.q < m);
       meet[g][l.ch][2 * l.q] = dt;
       meet[g][l.ch][2 * l.q + 1] = dt * r.u[g];
       if (MANY) {
-        meet[g][l.ch][8 + l.q] = GATE ? r.o[g] * silu_f(r.z[g]) : r.o[g];
+        const float dy = GATE ? r.o[g] * silu_f(r.z[g]) : r.o[g];
+        meet[g][l.ch][8 + l.q] = dy;
+        size += __builtin_fabsf(dy);
         mine += dt;
       }
     }
     wave_lds_fence();
+    if (MANY && uniform(__ballot(!finite(size)) != 0) != 0) {
+      // an infinite gradient stays one, though the decays before it may have rounded to 0
+      float worst = 0.0f;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) worst += __builtin_fabsf(meet[g][l.ch][8 + s]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) decay[i] = finite(worst) ? decay[i] : 1.0f;
+    }
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const auto &w = meet[g][l.ch];

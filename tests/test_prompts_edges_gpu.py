@@ -304,3 +304,14 @@ def test_single_tokens_far_apart(dtype):
     want, last, _ = s.ref(list(host(s.h0)))
     same(out, want[:, 0], tol(out), "out")
     same(state, last, F32, "state")
+
+
+@pytest.mark.parametrize("n", [1, 16])
+def test_an_infinite_gradient_stays_infinite_over_chunks(n):
+    """As an infinite state does, walking back: a chunk gathers the gradient of the state before it with decays that may
+    round to 0 together."""
+    s = mild(Scan(24, 1, 700, 16, n, "f32", bias=False))
+    s.a["A"] = torch.full((16, n), -8.0, device=DEV)
+    for ch in range(8):                      # (at all kinds of places in a chunk)
+        s.dout[0, 300 + 9 * ch, ch] = INF if ch % 2 else -INF
+    check_backward(s)
