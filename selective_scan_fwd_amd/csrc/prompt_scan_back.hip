@@ -146,13 +146,13 @@ __device__ __forceinline__ void mark_chunk(const PromptScanArgs &a, const Lane &
     wave_lds_fence();
     if (MANY && uniform(__ballot(!finite(size)) != 0) != 0) {
       // an infinite gradient stays one, though the decays before it may have rounded to 0
-      float worst = 0.0f;
+      bool all = true;
 #pragma unroll
       for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) worst += __builtin_fabsf(meet[g][l.ch][8 + s]);
+        for (int s = 0; s < 4; ++s) all = all && finite(meet[g][l.ch][8 + s]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) decay[i] = finite(worst) ? decay[i] : 1.0f;
+      for (int i = 0; i < 4; ++i) decay[i] = all ? decay[i] : 1.0f;
     }
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {

@@ -315,3 +315,16 @@ def test_an_infinite_gradient_stays_infinite_over_chunks(n):
     for ch in range(8):                      # (at all kinds of places in a chunk)
         s.dout[0, 300 + 9 * ch, ch] = INF if ch % 2 else -INF
     check_backward(s)
+
+
+def test_a_huge_gradient_decays_over_chunks():
+    """Values whose sum overflows, though none is infinite, decay like others."""
+    s = Scan(25, 1, 700, 16, 16, "f32", bias=False)
+    s.a["A"] = torch.full((16, 16), -8.0, device=DEV)
+    s.a.update({k: scale * s.a[k] for k, scale in (("u", 1e-2), ("B", 1e-3), ("C", 1e-3))})
+    s.a["z"] = s.a["z"].clamp(-1, 1)
+    for ch in range(8):
+        at = slice(304 + 8 * ch, 312 + 8 * ch, 4)
+        s.dout[0, at, ch] = 3e38
+        put(s, "z", (0, at, ch), 1.0)
+    check_backward(s)
