@@ -756,7 +756,8 @@ def vm_gated_delta_fwd(q, k, v, g, beta, scale=None, h0=None, want_state=False, 
     is tokens offsets[i] .. offsets[i + 1] - 1.  reverse=True visits each
     sequence from its last token.  out is [batch, L, hv, dv]; state (the last
     states, [n, hv, dk, dv] fp32) is None unless want_state or a state buffer
-    (which may be h0) is given."""
+    (which may be h0) is given.  Rows behind the last packed sequence are not
+    written: those of a new out hold what memory held."""
     p, index, (batch, L, n, hk, hv, dk, dv) = _delta(q, k, v, g, beta, h0, offsets)
     if out is None:
         out = torch.empty((batch, L, hv, dv), dtype=q.dtype, device=q.device)
@@ -773,7 +774,8 @@ def vm_gated_delta_fwd(q, k, v, g, beta, scale=None, h0=None, want_state=False, 
 def vm_gated_delta_bwd(q, k, v, g, beta, dout, scale=None, h0=None, dstate=None, reverse=False, offsets=None):
     """Gradients of sum(dout * out) + sum(dstate * state) of vm_gated_delta_fwd.
     Returns a dict: q, k, v (dense, in their dtype), g, beta (fp32) and, when h0
-    is given, h0 (fp32)."""
+    is given, h0 (fp32).  Rows behind the last packed sequence are not written: clear
+    them before a sum over all rows."""
     p, index, (batch, L, n, hk, hv, dk, dv) = _delta(q, k, v, g, beta, h0, offsets)
     po = _arg(dout, "dout", q.dtype, (batch, L, hv, dv), index)
     ps = _arg(dstate, "dstate", torch.float32, (n, hv, dk, dv), index)

@@ -5,7 +5,11 @@
 //   back: d the gradient of n w:  dv = s (w d - n mean(w d n)),  dw = sum d n
 // Bound by memory: every input is read once and every output written once.  4 x 4097 rows of
 // 16 heads of 128, bf16 (201 MB): 39 us, 5.1 TB/s; backward of 128 x 197 rows of 384, fp32 (194
-// MB): 45 us, the next row's loads under way (55 without), and 4 for the sums.
+// MB): 48 us, of which 39 this kernel with the next row's loads under way and 6 the sums.
+// The backward pass holds four arrays of columns and two rows in registers, which groups above
+// 2048 channels (two pieces a lane) are too wide for: one wave a SIMD to 4096 channels, spills
+// through memory above.  Whole rows, gated, bf16: 16384 rows of 2048 128 us (2.6 TB/s), 8192 of
+// 4096 209 (1.6), 8192 of 8192 789 (0.9), 4096 of 16384 1896 (0.4); forward 41, 42, 82 and 91.
 #include <hip/hip_runtime.h>
 
 #include "block_norm.h"

@@ -11,8 +11,9 @@
 // (its first, whose state is known, in full) and notes its end state and the sum of
 // its steps T; a second one forms each later chunk's first state from the chunks
 // before it, h <- exp(A T) h + end, and walks it in full.
-// 40 packed prompts of 1 to 1500 tokens, 4096 channels, bf16 (1.9 TB/s): 156 us; one prompt of
-// 4097 tokens: 118 us in two launches over 13 chunks.
+// 40 packed prompts of 1 to 1500 tokens, 4096 channels, bf16 (1.8 TB/s): 158 us; one prompt of
+// 4097 tokens: 119 us in two launches over 13 chunks.  Fewer states leave places empty and take
+// the time of 16.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

@@ -17,9 +17,12 @@
 // Sums over channels: 32 products of a group of 4 tokens are folded over the 16
 // lanes of a row, halving the values at each step, then over the workgroup's waves
 // in LDS; sums over blocks and chunks in a fixed order by launches of their own.
-// Bound by vector instructions: 87 a wave and token in the second launch, 37 in the first
-// with the gathered gradients and 20 without.  128 x 197 tokens of 384 channels, fp32:
-// 35 and 130 us; 2 x 4097 of 2048, bf16, in chunks: 104 and 210 us.
+// Bound by vector instructions: 88 a wave and token in the second launch (92 with chunks to
+// join), 38 in the first with the gathered gradients and 20 without.  128 x 197 tokens of 384
+// channels, fp32: 40 and 135 us; 2 x 4097 of 2048, bf16, in chunks: 103 and 237 us.
+// A tile of 8 tokens has places for 16 states of 16 channels.  What fills them up is 0, which
+// adds nothing as long as what it meets is finite: tiles with other values, and those that a
+// chunk's tokens do not fill, are walked with every sum restricted to what there is.
 #include <hip/hip_runtime.h>
 
 #include "prompt_device.h"
