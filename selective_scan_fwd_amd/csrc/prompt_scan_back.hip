@@ -19,7 +19,7 @@
 // in LDS; sums over blocks and chunks in a fixed order by launches of their own.
 // Bound by vector instructions: 88 a wave and token in the second launch (92 with chunks to
 // join), 38 in the first with the gathered gradients and 20 without.  128 x 197 tokens of 384
-// channels, fp32: 40 and 135 us; 2 x 4097 of 2048, bf16, in chunks: 103 and 237 us.
+// channels, fp32: 40 and 135 us; 2 x 4097 of 2048, bf16, in chunks: 106 and 236 us.
 // A tile of 8 tokens has places for 16 states of 16 channels.  What fills them up is 0, which
 // adds nothing as long as what it meets is finite: tiles with other values, and those that a
 // chunk's tokens do not fill, are walked with every sum restricted to what there is.
